@@ -66,7 +66,7 @@ typedef enum {
 typedef enum {
     MHC_OK = 0,
     MHC_ERR_NULL = -1,            /* a required pointer is NULL */
-    MHC_ERR_SHAPE = -2,           /* T < 0, H <= 0, H % 8 != 0, or H % 32 != 0 for mxfp8 */
+    MHC_ERR_SHAPE = -2,           /* T < 0, H <= 0, H % 8 != 0, H % 32 != 0 for mxfp8, or another size out of range */
     MHC_ERR_ALIGN = -3,           /* a pointer breaks its alignment rule */
     MHC_ERR_INCOMPLETE_POST = -4, /* exactly one of Y, post_prev is NULL, or Y without comb_prev */
     MHC_ERR_WORKSPACE = -5,       /* workspace NULL or smaller than mhc_workspace_bytes() */
@@ -259,6 +259,133 @@ int mhc_seam_noalloc(const void* R, const void* Y, const float* post_prev, const
  * the entry point it serves, it has no counterpart in the method's pages and
  * allocates nothing. */
 int mhc_noalloc_check_status(void* stream);
+
+/* ------------------------------------------------------------------------
+ * The operators around the seam, forward and backward: rows of an embedding
+ * table into the residual streams (what the identity form reads), the norms,
+ * gate and residual scale around a block of one residual stream, and the
+ * routing of tokens to experts from logits of the seam's norm.  The
+ * conventions above hold for them too, and:
+ *  - `mhc_dtype` is the type of the matrices and of the weights of H columns;
+ *    sums, norms and scores are fp32 and each output is rounded once, to nearest
+ *    even.
+ *  - `ld_*` is the elements from one row to the next (a multiple of 8, at least
+ *    H), so a matrix may be one stream of a [T,4,H] tensor; matrices without an
+ *    ld are dense.  Matrices and weights of H columns are 16-byte aligned and H is
+ *    a multiple of 8; other arrays are aligned to their elements.
+ *  - The results do not depend on timing: no float atomics.
+ *  - No call needs set-up: the first call may be captured into a graph.
+ * ------------------------------------------------------------------------ */
+typedef enum { MHC_DT_BF16 = 0, MHC_DT_F16 = 1, MHC_DT_F32 = 2 } mhc_dtype;
+typedef enum { MHC_GATE_NONE = 0, MHC_GATE_CHANNEL = 1, MHC_GATE_TOKEN = 2 } mhc_gate_mode;
+typedef enum { MHC_SCORE_SOFTMAX = 0, MHC_SCORE_SIGMOID = 1 } mhc_score;
+
+/* out[t,s,:] = scale * table[ids[t] - first_id, :] for s < streams.
+ *   ids     [T] int32 or int64 (id_bytes 4 or 8)
+ *   table   [V,H] of `dtype`, rows table_ld apart: the whole vocabulary, or its
+ *           shard that starts at first_id
+ *   out     [T,streams,H] of `dtype`, dense; 1 <= streams <= 64
+ * An id outside [first_id, first_id + V) reads nothing and gives a zero row
+ * (another shard's token, or a negative "ignore" id).  Errors: MHC_ERR_CONFIG,
+ * MHC_ERR_SHAPE, MHC_ERR_NULL, MHC_ERR_ALIGN, MHC_ERR_ALIAS, MHC_ERR_CUDA. */
+int mhc_embed(const void* ids, int id_bytes, const void* table, int64_t table_ld, int64_t V, int64_t first_id,
+              float scale, int64_t T, int H, int streams, mhc_dtype dtype, void* out, void* stream);
+
+/* Bytes of the workspace of mhc_embed_grad().  It needs no initialisation and
+ * holds nothing between calls. */
+size_t mhc_embed_grad_workspace_bytes(int64_t T, int64_t V, int H);
+
+/* The gradient of mhc_embed() by its table, from tokens sorted by row:
+ *   dtable[v,:] = scale * sum over t of row v, ascending, of sum_s dout[t,s,:]
+ *   dout       [T,streams,H] of `dtype`, dense
+ *   dtable     [V,H], rows ld apart, of fp32 or of `dtype` (grad_dtype).  Every row
+ *              is written (zero where no token has it); with `accumulate` not 0 the
+ *              sum is added to dtable and rows without tokens are left alone
+ *   padding_id NULL, or (host) the id that has no gradient
+ * Ids outside the table have no gradient.  T and V at most 2^30.  Errors as
+ * mhc_embed(), and MHC_ERR_WORKSPACE. */
+int mhc_embed_grad(const void* ids, int id_bytes, const void* dout, mhc_dtype dtype, float scale, int64_t T, int H,
+                   int streams, int64_t V, int64_t first_id, const int64_t* padding_id, int accumulate, void* dtable,
+                   mhc_dtype grad_dtype, int64_t ld, void* workspace, size_t ws_bytes, void* stream);
+
+/* The norm after a block, its gate, the residual add and the norm before the
+ * next block, in one launch, for one residual stream:
+ *   p     = y / rms(y) * gamma_post      (gamma_post NULL: p = y)
+ *   r_out = res_scale * r + gate * p     (gate [H] or [T]; none: 1)
+ *   norm  = r_out / rms(r_out) * gamma_pre,  rms(x) = sqrt(mean x^2 + eps)
+ * The norm is formed from r_out before its rounding.
+ *   y, r, r_out, norm  [T,H] of `dtype`; r_out may be r (same stride, in place)
+ *   gamma_post, gamma_pre  [H] of `dtype`; gamma_pre NULL: no norm (the last
+ *             block; norm and rstd_pre are ignored)
+ *   gate      MHC_GATE_CHANNEL: [H] of `dtype`; MHC_GATE_TOKEN: [T] fp32 (as
+ *             the seam's gates); MHC_GATE_NONE: NULL
+ *   rstd_post, rstd_pre  [T] fp32: 1/rms of y and of r_out, for the gradient;
+ *             required where their gamma is given
+ * y NULL is the norm before the first block: norm = r / rms(r) * gamma_pre, and
+ * r_out is not written (gamma_post and the gate must be absent, else
+ * MHC_ERR_INCOMPLETE_POST).  H <= 16384, T < 2^31.  Errors: MHC_ERR_CONFIG,
+ * MHC_ERR_SHAPE, MHC_ERR_NULL, MHC_ERR_INCOMPLETE_POST, MHC_ERR_ALIGN,
+ * MHC_ERR_ALIAS, MHC_ERR_CUDA. */
+int mhc_block_norm(const void* y, int64_t ld_y, const void* r, int64_t ld_r, const void* gamma_post, const void* gate,
+                   int gate_mode, const void* gamma_pre, float res_scale, float eps, int64_t T, int H, mhc_dtype dtype,
+                   void* r_out, int64_t ld_r_out, void* norm, int64_t ld_norm, float* rstd_post, float* rstd_pre,
+                   void* stream);
+
+/* Bytes of the workspace of mhc_block_norm_grad().  It needs no initialisation
+ * and holds nothing between calls. */
+size_t mhc_block_norm_grad_workspace_bytes(int64_t T, int H);
+
+/* The gradient of mhc_block_norm(): from dr_out and dnorm, those of r_out and
+ * norm, to dy, dr and the weights' gradients.  y, r_out, the weights, the gate
+ * and the rstd arrays are those of the forward call; all matrices are dense.
+ *   dr_out     NULL: zero (then gamma_pre must be given)
+ *   dnorm, r_out, rstd_pre, dgamma_pre  used where gamma_pre is given; without y,
+ *              r_out is the forward call's r
+ *   dy         required where y is given;  dr always
+ *   dgamma_post, dgamma_pre [H] fp32, dgate [H] (channel) or [T] (token) fp32:
+ *              required where their weight is given; written, not added to (zero
+ *              for T = 0)
+ * Errors as mhc_block_norm(), and MHC_ERR_WORKSPACE. */
+int mhc_block_norm_grad(const void* dr_out, const void* dnorm, const void* y, const void* r_out, const void* gamma_post,
+                        const void* gate, int gate_mode, const void* gamma_pre, const float* rstd_post,
+                        const float* rstd_pre, float res_scale, int64_t T, int H, mhc_dtype dtype, void* dy, void* dr,
+                        float* dgamma_post, float* dgate, float* dgamma_pre, void* workspace, size_t ws_bytes,
+                        void* stream);
+
+/* Bytes of the workspace of mhc_route() with counts: it needs
+ * mhc_workspace_init() once; its counters reset themselves. */
+size_t mhc_route_workspace_bytes(int E);
+
+/* Routing of tokens to experts.  Per token, with l its logits:
+ *   score_e = 1 / (1 + exp(-l_e)), or softmax(l)_e over the row
+ *   choice  = score + bias (bias [E] fp32, used for the choice only; NULL: none)
+ *   With groups > 1 the experts fall into `groups` runs of E / groups; a group
+ *   counts as the sum of its two best choices (its one, if it has one), and only
+ *   experts of the best top_groups groups are taken
+ *   indices = the k experts of the best choice, best first, ties to the lowest
+ *   weights = scale * score, with `renorm` not 0 divided by the sum over the k
+ * An expert whose logit is -inf or NaN is never chosen; slots that find no expert
+ * have index -1 and weight 0.  Scores are fp32 (expf and IEEE division), so the
+ * choice follows the formulas in fp32 exactly; without a bias, softmax scores are
+ * compared as exp(l - max).
+ *   logits  [T,E] of `dtype`, rows ld >= E apart (any alignment of the type)
+ *   indices [T,k] int32, weights [T,k] fp32
+ *   counts  [E] int32: tokens sent to each expert by this call, or NULL (then
+ *           workspace may be NULL)
+ * 1 <= E <= 1024, k <= 32, groups <= 32, k <= top_groups * E / groups.  Errors:
+ * MHC_ERR_CONFIG, MHC_ERR_SHAPE, MHC_ERR_NULL, MHC_ERR_ALIGN, MHC_ERR_WORKSPACE,
+ * MHC_ERR_ALIAS, MHC_ERR_CUDA. */
+int mhc_route(const void* logits, int64_t ld, mhc_dtype dtype, const float* bias, mhc_score score, int E, int groups,
+              int top_groups, int k, int renorm, float scale, int64_t T, int32_t* indices, float* weights,
+              int32_t* counts, void* workspace, size_t ws_bytes, void* stream);
+
+/* The gradient of mhc_route()'s weights by the logits (the choice itself has
+ * none): dlogits [T,E] of `dtype`, rows ld_d apart, every element written, from
+ * dweights [T,k] fp32 and the forward call's logits and indices.  Slots whose index is
+ * not in [0, E) are skipped.  Errors as mhc_route(). */
+int mhc_route_grad(const float* dweights, const void* logits, int64_t ld, mhc_dtype dtype, const int32_t* indices,
+                   mhc_score score, int E, int k, int renorm, float scale, int64_t T, void* dlogits, int64_t ld_d,
+                   void* stream);
 
 /* Number of kernel launches the last successful mhc_seam() on this host
  * thread issued (1 for every non-empty call). */

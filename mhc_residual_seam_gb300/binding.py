@@ -17,6 +17,9 @@ from . import build as _build
 MHC_OUT_BF16 = 0
 MHC_OUT_MXFP8 = 1
 MHC_OUT_FP8_GRID = 2
+MHC_DT_BF16, MHC_DT_F16, MHC_DT_F32 = 0, 1, 2
+MHC_GATE_NONE, MHC_GATE_CHANNEL, MHC_GATE_TOKEN = 0, 1, 2
+MHC_SCORE_SOFTMAX, MHC_SCORE_SIGMOID = 0, 1
 STATUS_NAMES = {
     0: "MHC_OK", -1: "MHC_ERR_NULL", -2: "MHC_ERR_SHAPE", -3: "MHC_ERR_ALIGN", -4: "MHC_ERR_INCOMPLETE_POST",
     -5: "MHC_ERR_WORKSPACE", -6: "MHC_ERR_CAPTURE", -7: "MHC_ERR_TIMEOUT", -8: "MHC_ERR_CUDA", -9: "MHC_ERR_ALIAS",
@@ -73,6 +76,25 @@ def lib():
         L.mhc_quant_ue8m0.argtypes = [P, I64, I, C.c_float, P, P, P]
         L.mhc_copy.restype = I
         L.mhc_copy.argtypes = [P, P, C.c_size_t, P]
+        F, SZ = C.c_float, C.c_size_t
+        L.mhc_embed.restype = I
+        L.mhc_embed.argtypes = [P, I, P, I64, I64, I64, F, I64, I, I, I, P, P]
+        L.mhc_embed_grad_workspace_bytes.restype = SZ
+        L.mhc_embed_grad_workspace_bytes.argtypes = [I64, I64, I]
+        L.mhc_embed_grad.restype = I
+        L.mhc_embed_grad.argtypes = [P, I, P, I, F, I64, I, I, I64, I64, P, I, P, I, I64, P, SZ, P]
+        L.mhc_block_norm.restype = I
+        L.mhc_block_norm.argtypes = [P, I64, P, I64, P, P, I, P, F, F, I64, I, I, P, I64, P, I64, P, P, P]
+        L.mhc_block_norm_grad_workspace_bytes.restype = SZ
+        L.mhc_block_norm_grad_workspace_bytes.argtypes = [I64, I]
+        L.mhc_block_norm_grad.restype = I
+        L.mhc_block_norm_grad.argtypes = [P] * 6 + [I, P, P, P, F, I64, I, I] + [P] * 6 + [SZ, P]
+        L.mhc_route_workspace_bytes.restype = SZ
+        L.mhc_route_workspace_bytes.argtypes = [I]
+        L.mhc_route.restype = I
+        L.mhc_route.argtypes = [P, I64, I, P, I, I, I, I, I, I, F, I64, P, P, P, P, SZ, P]
+        L.mhc_route_grad.restype = I
+        L.mhc_route_grad.argtypes = [P, P, I64, I, P, I, I, I, I, F, I64, P, I64, P]
         L.mhc_last_launch_count.restype = I
         L.mhc_last_launch_count.argtypes = []
         L.mhc_last_wave_parts.restype = I
@@ -218,6 +240,180 @@ def mhc_last_wave_parts() -> int:
 
 def mhc_last_error_string() -> str:
     return lib().mhc_last_error_string().decode()
+
+
+# ------------------------------------------- the operators around the seam --
+# Pointers carry no type or shape, so these functions check the tensors'
+# before they pass the pointers on (MHC_ERR_CONFIG for a type, MHC_ERR_SHAPE
+# for a shape or a stride).
+_DTYPES: dict = {}
+
+
+def _dtype(t) -> int:
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.bfloat16: MHC_DT_BF16, torch.float16: MHC_DT_F16, torch.float32: MHC_DT_F32})
+    d = _DTYPES.get(t.dtype)
+    if d is None:
+        raise MhcError(-10, f"{t.dtype} is not bf16, fp16 or fp32")
+    return d
+
+
+def _need(ok: bool, msg: str, code: int = -2) -> None:
+    if not ok:
+        raise MhcError(code, msg)
+
+
+def _dense(t, shape, dtype, name: str) -> None:
+    """``t`` is None or a dense tensor of this shape and type."""
+    if t is not None:
+        _need(t.is_cuda, f"{name} is not on the GPU", -10)
+        _need(t.dtype == dtype, f"{name} must be {dtype}", -10)
+        _need(tuple(t.shape) == shape and t.is_contiguous(), f"{name} must be dense, of shape {shape}")
+
+
+def _rows(t, T: int, H: int, dtype, name: str) -> int:
+    """The row stride of a [T, H] matrix with dense rows (H for None)."""
+    if t is None:
+        return H
+    _need(t.is_cuda, f"{name} is not on the GPU", -10)
+    _need(t.dtype == dtype, f"{name} must be {dtype}", -10)
+    _need(t.dim() == 2 and t.shape[0] == T and t.shape[1] == H and (t.stride(1) == 1 or H == 1),
+          f"{name} must be [{T}, {H}] with dense rows")
+    return t.stride(0) if T > 1 else max(H, t.stride(0) // 8 * 8)
+
+
+def _id_bytes(ids) -> int:
+    import torch
+    _need(ids.is_cuda, "ids is not on the GPU", -10)
+    _need(ids.dtype in (torch.int32, torch.int64), "ids must be int32 or int64", -10)
+    _need(ids.dim() == 1 and ids.is_contiguous(), "ids must be a dense vector")
+    return ids.element_size()
+
+
+def mhc_embed(ids, table, out, scale: float = 1.0, first_id: int = 0, stream=None) -> None:
+    """Rows of ``table`` [V, H] into ``out`` [T, H] or [T, streams, H]."""
+    T, (V, H) = ids.shape[0], table.shape
+    S = out.shape[1] if out.dim() == 3 else 1
+    _dense(out, (T, S, H) if out.dim() == 3 else (T, H), table.dtype, "out")
+    _check(lib().mhc_embed(_ptr(ids), _id_bytes(ids), _ptr(table), _rows(table, V, H, table.dtype, "table"), V,
+                           int(first_id), float(scale), T, H, S, _dtype(table), _ptr(out), _stream(stream)))
+
+
+def mhc_embed_grad_workspace_bytes(T: int, V: int, H: int) -> int:
+    return int(lib().mhc_embed_grad_workspace_bytes(int(T), int(V), int(H)))
+
+
+def mhc_embed_grad(ids, dout, dtable, workspace, scale: float = 1.0, first_id: int = 0, padding_id: int | None = None,
+                   accumulate: bool = False, stream=None) -> None:
+    """The gradient of mhc_embed by its table: ``dout`` [T, H] or [T, streams, H]
+    into ``dtable`` [V, H] (fp32 or dout's type)."""
+    T, (V, H) = ids.shape[0], dtable.shape
+    S = dout.shape[1] if dout.dim() == 3 else 1
+    _dense(dout, (T, S, H) if dout.dim() == 3 else (T, H), dout.dtype, "dout")
+    pad = None if padding_id is None else C.byref(C.c_int64(padding_id))
+    _check(lib().mhc_embed_grad(_ptr(ids), _id_bytes(ids), _ptr(dout), _dtype(dout), float(scale), T, H, S, V,
+                                int(first_id), pad, int(accumulate), _ptr(dtable), _dtype(dtable),
+                                _rows(dtable, V, H, dtable.dtype, "dtable"), _ptr(workspace), _bytes(workspace),
+                                _stream(stream)))
+
+
+def _bytes(t) -> int:
+    if t is None:
+        return 0
+    _need(t.is_cuda and t.is_contiguous(), "workspace must be dense and on the GPU", -10)
+    return t.numel() * t.element_size()
+
+
+def _gate(gate, gate_mode: int, T: int, H: int, dtype) -> None:
+    import torch
+    if gate is not None:
+        token = gate_mode == MHC_GATE_TOKEN
+        _dense(gate, (T,) if token else (H,), torch.float32 if token else dtype, "gate")
+
+
+def mhc_block_norm(y, r, gamma_post, gate, gamma_pre, r_out, norm, rstd_post, rstd_pre, gate_mode: int = MHC_GATE_NONE,
+                   res_scale: float = 1.0, eps: float = 1e-6, stream=None) -> None:
+    """Norm after a block, gate, residual add and norm before the next block;
+    y, r, r_out and norm are [T, H] (rows may be strided)."""
+    import torch
+    (T, H), dt = r.shape, r.dtype
+    _gate(gate, gate_mode, T, H, dt)
+    for t, n in ((gamma_post, "gamma_post"), (gamma_pre, "gamma_pre")):
+        _dense(t, (H,), dt, n)
+    for t, n in ((rstd_post, "rstd_post"), (rstd_pre, "rstd_pre")):
+        _dense(t, (T,), torch.float32, n)
+    _check(lib().mhc_block_norm(_ptr(y), _rows(y, T, H, dt, "y"), _ptr(r), _rows(r, T, H, dt, "r"), _ptr(gamma_post),
+                                _ptr(gate), gate_mode, _ptr(gamma_pre), float(res_scale), float(eps), T, H, _dtype(r),
+                                _ptr(r_out), _rows(r_out, T, H, dt, "r_out"), _ptr(norm), _rows(norm, T, H, dt, "norm"),
+                                _ptr(rstd_post), _ptr(rstd_pre), _stream(stream)))
+
+
+def mhc_block_norm_grad_workspace_bytes(T: int, H: int) -> int:
+    return int(lib().mhc_block_norm_grad_workspace_bytes(int(T), int(H)))
+
+
+def mhc_block_norm_grad(dr_out, dnorm, y, r_out, gamma_post, gate, gamma_pre, rstd_post, rstd_pre, dy, dr, dgamma_post,
+                        dgate, dgamma_pre, workspace, gate_mode: int = MHC_GATE_NONE, res_scale: float = 1.0,
+                        stream=None) -> None:
+    """The gradient of mhc_block_norm; all matrices are dense [T, H], the
+    weights' gradients fp32."""
+    import torch
+    (T, H), dt, f32 = dr.shape, dr.dtype, torch.float32
+    _gate(gate, gate_mode, T, H, dt)
+    for t, n in ((dr_out, "dr_out"), (dnorm, "dnorm"), (y, "y"), (r_out, "r_out"), (dy, "dy"), (dr, "dr")):
+        _dense(t, (T, H), dt, n)
+    for t, n in ((gamma_post, "gamma_post"), (gamma_pre, "gamma_pre")):
+        _dense(t, (H,), dt, n)
+    for t, n in ((rstd_post, "rstd_post"), (rstd_pre, "rstd_pre")):
+        _dense(t, (T,), f32, n)
+    for t, n in ((dgamma_post, "dgamma_post"), (dgamma_pre, "dgamma_pre")):
+        _dense(t, (H,), f32, n)
+    _dense(dgate, (T,) if gate_mode == MHC_GATE_TOKEN else (H,), f32, "dgate")
+    _check(lib().mhc_block_norm_grad(_ptr(dr_out), _ptr(dnorm), _ptr(y), _ptr(r_out), _ptr(gamma_post), _ptr(gate),
+                                     gate_mode, _ptr(gamma_pre), _ptr(rstd_post), _ptr(rstd_pre), float(res_scale), T,
+                                     H, _dtype(dr), _ptr(dy), _ptr(dr), _ptr(dgamma_post), _ptr(dgate),
+                                     _ptr(dgamma_pre), _ptr(workspace), _bytes(workspace), _stream(stream)))
+
+
+def mhc_route_workspace_bytes(E: int) -> int:
+    return int(lib().mhc_route_workspace_bytes(int(E)))
+
+
+def mhc_route(logits, bias, indices, weights, counts=None, workspace=None, score: int = MHC_SCORE_SIGMOID,
+              groups: int = 1, top_groups: int = 1, renorm: bool = True, scale: float = 1.0, stream=None) -> None:
+    """The k best experts of each row of ``logits`` [T, E]: ``indices`` [T, k]
+    int32, ``weights`` [T, k] fp32 and, where given, the experts' ``counts``."""
+    import torch
+    (T, E), k = logits.shape, indices.shape[-1]
+    _dense(bias, (E,), torch.float32, "bias")
+    _dense(indices, (T, k), torch.int32, "indices")
+    _dense(weights, (T, k), torch.float32, "weights")
+    _dense(counts, (E,), torch.int32, "counts")
+    _check(lib().mhc_route(_ptr(logits), _pitch(logits, T, E, "logits"), _dtype(logits), _ptr(bias), score, E, groups,
+                           top_groups, k, int(renorm), float(scale), T, _ptr(indices), _ptr(weights), _ptr(counts),
+                           _ptr(workspace), _bytes(workspace), _stream(stream)))
+
+
+def _pitch(t, T: int, E: int, name: str) -> int:
+    """The row stride of a [T, E] matrix with dense rows, of any alignment."""
+    _need(t.is_cuda, f"{name} is not on the GPU", -10)
+    _need(t.dim() == 2 and t.shape[0] == T and t.shape[1] == E and (t.stride(1) == 1 or E == 1),
+          f"{name} must be [{T}, {E}] with dense rows")
+    return t.stride(0) if T > 1 else E
+
+
+def mhc_route_grad(dweights, logits, indices, dlogits, score: int = MHC_SCORE_SIGMOID, renorm: bool = True,
+                   scale: float = 1.0, stream=None) -> None:
+    """The gradient of mhc_route's weights by the logits."""
+    import torch
+    (T, E), k = logits.shape, indices.shape[-1]
+    _dense(dweights, (T, k), torch.float32, "dweights")
+    _dense(indices, (T, k), torch.int32, "indices")
+    _need(dlogits.dtype == logits.dtype, "dlogits must have logits' type", -10)
+    _check(lib().mhc_route_grad(_ptr(dweights), _ptr(logits), _pitch(logits, T, E, "logits"), _dtype(logits),
+                                _ptr(indices), score, E, k, int(renorm), float(scale), T, _ptr(dlogits),
+                                _pitch(dlogits, T, E, "dlogits"), _stream(stream)))
 
 
 # ----------------------------------------------------------- allocation ----

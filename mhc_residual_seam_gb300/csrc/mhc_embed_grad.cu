@@ -1,0 +1,418 @@
+// mhc_embed_grad: the gradient of an embedding table from tokens sorted by row.
+//
+// dtable[v] = scale * sum over the tokens t of row v, in token order, of
+// sum_s dout[t, s].  Three steps:
+//   1. a stable radix sort of the tokens by row (tokens of no row get the key V,
+//      which sorts behind all rows);
+//   2. the rows' ends and the sorted tokens are one merged list (a row's end
+//      comes behind its tokens); the list is cut into chunks of equal bytes,
+//      and each CTA walks one chunk: a token is added to the sum in registers, a
+//      row's end writes it (zero where the row has no token);
+//   3. a row whose tokens lie in more than one chunk is joined: the chunks'
+//      partial sums in chunk order, then the last chunk's tokens.
+// No float atomics, so the result does not depend on timing.
+
+#include "mhc_ops.cuh"
+
+namespace mhc {
+
+constexpr int kSortThreads = 512;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kSortRounds = 4;                               // keys per lane
+constexpr int kSortTile = kSortThreads * kSortRounds;        // keys per CTA
+constexpr int kDigits = 512;                                 // 9-bit digits at most
+constexpr int kColumns = 1024;                               // columns per CTA of the sum
+constexpr int kSumThreads = kColumns / 8;
+
+struct Bounds {  // a chunk's first token and row, and the ones behind its last
+  int a0, a1, b0, b1;
+};
+
+struct EmbedGradWs {  // byte offsets into the workspace
+  size_t key[2], tok[2], hist, valid, bounds, carry, total;
+  int tiles, chunks, passes, digit_bits;
+};
+
+struct SortArgs {
+  const void* ids;
+  int64_t first, V, pad;
+  bool has_pad;
+  int T, bits, shift, tiles;
+  uint32_t *key_in, *key_out;
+  int *tok_in, *tok_out;
+  int *hist_in, *hist_out;  // [tiles][kDigits] of this pass and of the next one
+  int passes;
+  int* valid;               // [tiles] tokens that have a row
+};
+
+template <typename Id>
+__device__ __forceinline__ uint32_t row_of(const SortArgs& a, int t) {
+  const int64_t id = (int64_t) static_cast<const Id*>(a.ids)[t];
+  const uint64_t row = (uint64_t)id - (uint64_t)a.first;
+  return row < (uint64_t)a.V && !(a.has_pad && id == a.pad) ? (uint32_t)row : (uint32_t)a.V;
+}
+
+// Digit counts of each tile for the first pass, the rows of the tokens, and
+// zeroed counts for the later passes (which follow the first one's).
+template <typename Id>
+__global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const SortArgs a) {
+  __shared__ int count[kDigits];
+  __shared__ int valid;
+  for (int d = threadIdx.x; d < kDigits; d += kSortThreads) count[d] = 0;
+  if (threadIdx.x == 0) valid = 0;
+  __syncthreads();
+  const int base = blockIdx.x * kSortTile;
+  int mine = 0;
+  for (int i = threadIdx.x; i < kSortTile && base + i < a.T; i += kSortThreads) {
+    const uint32_t k = row_of<Id>(a, base + i);
+    a.key_in[base + i] = k;
+    mine += k < (uint32_t)a.V;
+    atomicAdd(&count[k & ((1u << a.bits) - 1)], 1);
+  }
+  atomicAdd(&valid, mine);
+  __syncthreads();
+  for (int d = threadIdx.x; d < kDigits; d += kSortThreads) {
+    a.hist_in[blockIdx.x * kDigits + d] = count[d];
+    for (int p = 1; p < a.passes; ++p) a.hist_in[((int64_t)p * a.tiles + blockIdx.x) * kDigits + d] = 0;
+  }
+  if (threadIdx.x == 0) a.valid[blockIdx.x] = valid;
+}
+
+// One pass of the stable sort: a key's place is the keys of smaller digits,
+// the same digit in earlier tiles, in earlier warps of the tile, and before it
+// in its warp (whose keys are taken in order, 32 at a time).
+__global__ void __launch_bounds__(kSortThreads) sort_pass_kernel(const SortArgs a, bool identity, bool last) {
+  __shared__ int start[kDigits];
+  __shared__ int scan[kSortWarps];
+  __shared__ unsigned short rank[kSortWarps][kDigits];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t mask = (1u << a.bits) - 1;
+  for (int i = threadIdx.x; i < kSortWarps * kDigits; i += kSortThreads) (&rank[0][0])[i] = 0;
+  // the digit's keys in all tiles and in the tiles before this one
+  int before = 0, all = 0;
+  for (int b = 0; b < a.tiles; ++b) {
+    const int n = a.hist_in[b * kDigits + threadIdx.x];
+    before += b < (int)blockIdx.x ? n : 0;
+    all += n;
+  }
+  int x = all;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, d);
+    if (lane >= d) x += y;
+  }
+  if (lane == 31) scan[warp] = x;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) x += scan[w];
+  start[threadIdx.x] = x - all + before;
+  uint32_t key[kSortRounds];
+  int place[kSortRounds];
+  const int base = blockIdx.x * kSortTile + warp * 32 * kSortRounds;
+#pragma unroll
+  for (int r = 0; r < kSortRounds; ++r) {
+    const int i = base + r * 32 + lane;
+    key[r] = i < a.T ? a.key_in[i] : 0xffffffffu;
+    const uint32_t d = i < a.T ? (key[r] >> a.shift) & mask : kDigits;  // kDigits: no key
+    const unsigned peers = __match_any_sync(0xffffffffu, d);
+    const unsigned below = peers & ((1u << lane) - 1);
+    place[r] = d < kDigits ? rank[warp][d] + __popc(below) : 0;
+    __syncwarp();
+    if (d < kDigits && below == 0) rank[warp][d] += (unsigned short)__popc(peers);
+    __syncwarp();
+  }
+  __syncthreads();
+  {  // the digit's keys in the warps before
+    int sum = 0;
+    for (int w = 0; w < kSortWarps; ++w) {
+      const int n = rank[w][threadIdx.x];
+      rank[w][threadIdx.x] = (unsigned short)sum;
+      sum += n;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < kSortRounds; ++r) {
+    const int i = base + r * 32 + lane;
+    if (i >= a.T) continue;
+    const uint32_t d = (key[r] >> a.shift) & mask;
+    const int at = start[d] + rank[warp][d] + place[r];
+    a.key_out[at] = key[r];
+    a.tok_out[at] = identity ? i : a.tok_in[i];
+    if (!last) atomicAdd(a.hist_out + at / kSortTile * kDigits + ((key[r] >> (a.shift + a.bits)) & mask), 1);
+  }
+}
+
+struct SumArgs {
+  const void* dout;
+  void* dtable;
+  int64_t ld, V;
+  int H, streams, tiles, chunks, wt, wr;
+  bool accumulate;
+  float scale;
+  const uint32_t* key;
+  const int* tok;
+  const int* valid;
+  Bounds* bounds;
+  float* carry;  // [chunks][H]
+};
+
+// Tokens that have a row: the sum over the sort's tiles.
+__device__ __forceinline__ int valid_tokens(const SumArgs& a, int* sh) {
+  int n = 0;
+  for (int i = threadIdx.x; i < a.tiles; i += blockDim.x) n += a.valid[i];
+#pragma unroll
+  for (int d = 16; d; d >>= 1) n += __shfl_xor_sync(0xffffffffu, n, d);
+  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = n;
+  __syncthreads();
+  n = 0;
+  for (int i = 0; i < (int)blockDim.x / 32; ++i) n += sh[i];
+  return n;
+}
+
+// Where the merged list is cut so that `target` weight lies before: (token,
+// row).  Before token i lie i tokens and key[i] rows' ends.
+__device__ __forceinline__ void cut(const SumArgs& a, int n, int64_t target, int* tok, int* row) {
+  int lo = 0, hi = n;  // the first token that has at least `target` before it
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if ((int64_t)a.wt * mid + (int64_t)a.wr * a.key[mid] >= target) hi = mid;
+    else lo = mid + 1;
+  }
+  const int64_t from = lo ? (int64_t)a.key[lo - 1] : 0, to = lo < n ? (int64_t)a.key[lo] : a.V;
+  int64_t r = (target - (int64_t)a.wt * lo + a.wr - 1) / a.wr;
+  if (target < (int64_t)a.wt * lo) r = 0;
+  *tok = lo;
+  *row = (int)(r < from ? from : r > to ? to : r);
+}
+
+template <typename T>
+__device__ __forceinline__ void add_token(const SumArgs& a, int i, int64_t c, Vec8& acc) {
+  const T* p = static_cast<const T*>(a.dout) + (int64_t)a.tok[i] * a.streams * a.H + c;
+  for (int s = 0; s < a.streams; ++s, p += a.H) {
+    const Vec8 x = unpack(ld8_stream(p));
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc.v[e] += x.v[e];
+  }
+}
+
+template <typename O>
+__device__ __forceinline__ void end_row(const SumArgs& a, int64_t row, int64_t c, Vec8 acc) {
+  O* o = static_cast<O*>(a.dtable) + row * a.ld + c;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) acc.v[e] *= a.scale;
+  if (a.accumulate) {
+    const Vec8 old = unpack(ld8(o));
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc.v[e] += old.v[e];
+  }
+  st8_stream(o, pack<O>(acc));
+}
+
+template <typename T, typename O>
+__global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const SumArgs a) {
+  __shared__ int sh[kSumThreads / 32];
+  __shared__ Bounds sb;
+  const int n = valid_tokens(a, sh);
+  const int64_t weight = (int64_t)a.wt * n + (int64_t)a.wr * a.V;
+  const int chunk = blockIdx.x;
+  if (threadIdx.x == 0) {
+    cut(a, n, weight * chunk / a.chunks, &sb.a0, &sb.b0);
+    if (chunk + 1 < a.chunks) cut(a, n, weight * (chunk + 1) / a.chunks, &sb.a1, &sb.b1);
+    else sb.a1 = n, sb.b1 = (int)a.V;
+    if (blockIdx.y == 0) a.bounds[chunk] = sb;
+  }
+  __syncthreads();
+  const Bounds b = sb;
+  const int64_t c = (int64_t)blockIdx.y * kColumns + threadIdx.x * 8;
+  if (c >= a.H) return;
+  int i = b.a0, row = b.b0;
+  if (i > 0 && row < b.b1 && (int)a.key[i - 1] == row) {  // the join ends this row
+    while (i < b.a1 && (int)a.key[i] == row) ++i;
+    ++row;
+  }
+  for (; row < b.b1; ++row) {
+    Vec8 acc = {};
+    const int i0 = i;
+    for (; i < b.a1 && (int)a.key[i] == row; ++i) add_token<T>(a, i, c, acc);
+    if (i > i0 || !a.accumulate) end_row<O>(a, row, c, acc);
+  }
+  if (i < b.a1) {  // tokens of a row that ends in a later chunk
+    Vec8 acc = {};
+    for (; i < b.a1; ++i) add_token<T>(a, i, c, acc);
+    st8(a.carry + (int64_t)chunk * a.H + c, pack<float>(acc));
+  }
+}
+
+// Rows whose tokens lie in several chunks, by the chunk that holds their end.
+template <typename T, typename O>
+__global__ void __launch_bounds__(kSumThreads) embed_join_kernel(const SumArgs a) {
+  pdl_wait();
+  const int chunk = blockIdx.x;
+  const Bounds b = a.bounds[chunk];
+  const int row = b.b0;
+  if (b.a0 == 0 || row >= b.b1 || (int)a.key[b.a0 - 1] != row) return;
+  const int64_t c = (int64_t)blockIdx.y * kColumns + threadIdx.x * 8;
+  if (c >= a.H) return;
+  int from = chunk - 1;  // the first chunk that holds tokens of the row
+  while (from > 0) {
+    const Bounds p = a.bounds[from];
+    if (p.b0 < row || p.a0 == 0 || (int)a.key[p.a0 - 1] != row) break;
+    --from;
+  }
+  Vec8 acc = {};
+  for (int k = from; k < chunk; ++k) {
+    const Bounds p = a.bounds[k];
+    if (p.a1 == p.a0) continue;  // no token in it
+    const Vec8 x = unpack(ld8(a.carry + (int64_t)k * a.H + c));
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc.v[e] += x.v[e];
+  }
+  for (int i = b.a0; i < b.a1 && (int)a.key[i] == row; ++i) add_token<T>(a, i, c, acc);
+  end_row<O>(a, row, c, acc);
+}
+
+static int bits_of(int64_t v) {
+  int b = 0;
+  while (v >> b) ++b;
+  return b < 1 ? 1 : b;
+}
+
+// Workspace and launch plan; a pure function of the sizes.
+static EmbedGradWs embed_grad_plan(int64_t T, int64_t V, int H) {
+  EmbedGradWs w = {};
+  const int bits = bits_of(V);  // keys 0 .. V
+  w.passes = (bits + 8) / 9;
+  w.digit_bits = (bits + w.passes - 1) / w.passes;
+  w.tiles = (int)((T + kSortTile - 1) / kSortTile);
+  const int cols = (H + kColumns - 1) / kColumns;
+  const int64_t most = (152 * 16 + cols - 1) / cols;  // about one round of resident CTAs
+  int64_t chunks = (T + V + 15) / 16;
+  w.chunks = (int)(chunks < 1 ? 1 : chunks > most ? most : chunks);
+  size_t at = 256;
+  auto take = [&](size_t bytes) {
+    const size_t o = at;
+    at += (bytes + 255) / 256 * 256;
+    return o;
+  };
+  for (int i = 0; i < 2; ++i) w.key[i] = take((size_t)T * 4), w.tok[i] = take((size_t)T * 4);
+  w.hist = take((size_t)w.passes * w.tiles * kDigits * 4);
+  w.valid = take((size_t)w.tiles * 4);
+  w.bounds = take((size_t)w.chunks * sizeof(Bounds));
+  w.carry = take((size_t)w.chunks * H * 4);
+  w.total = at;
+  return w;
+}
+
+template <typename T>
+static cudaError_t sum_launch(const SumArgs& a, int grad_dtype, dim3 grid, cudaStream_t s) {
+  cudaError_t e = cudaSuccess;
+  auto go = [&](auto o) {
+    using O = decltype(o);
+    embed_sum_kernel<T, O><<<grid, kSumThreads, 0, s>>>(a);
+    e = cudaGetLastError();
+    if (e == cudaSuccess) e = launch_pdl(embed_join_kernel<T, O>, grid, dim3(kSumThreads), 0, s, a);
+  };
+  if (grad_dtype == MHC_DT_F32) go(float());
+  else go(T());
+  return e;
+}
+
+}  // namespace mhc
+
+extern "C" {
+
+size_t mhc_embed_grad_workspace_bytes(int64_t T, int64_t V, int H) {
+  if (T <= 0 || V <= 0 || H <= 0) return 256;
+  return mhc::embed_grad_plan(T, V, H).total;
+}
+
+int mhc_embed_grad(const void* ids, int id_bytes, const void* dout, mhc_dtype dtype, float scale, int64_t T, int H,
+                   int streams, int64_t V, int64_t first_id, const int64_t* padding_id, int accumulate, void* dtable,
+                   mhc_dtype grad_dtype, int64_t ld, void* workspace, size_t ws_bytes, void* stream) {
+  using namespace mhc;
+  if (!dtype_ok(dtype) || !dtype_ok(grad_dtype)) return ops_fail(MHC_ERR_CONFIG, "unknown dtype");
+  if (grad_dtype != MHC_DT_F32 && grad_dtype != dtype)
+    return ops_fail(MHC_ERR_CONFIG, "the gradient table is fp32 or of the same type as dout");
+  if (id_bytes != 4 && id_bytes != 8) return ops_fail(MHC_ERR_CONFIG, "id_bytes must be 4 or 8");
+  if (T < 0 || T > 0x40000000 || V < 0 || V > 0x40000000 || H <= 0 || H % 8 != 0 || H > 1 << 20 || streams < 1 ||
+      streams > 64)
+    return ops_fail(MHC_ERR_SHAPE, "need 0 <= T, V <= 2^30, H a positive multiple of 8 and 1 <= streams <= 64");
+  if (ld < H || ld % 8 != 0) return ops_fail(MHC_ERR_SHAPE, "the table's row stride must be a multiple of 8, at least H");
+  if (V == 0 || (T == 0 && accumulate)) return MHC_OK;
+  if (!dtable || (T && (!ids || !dout))) return ops_fail(MHC_ERR_NULL, "ids, dout and dtable are required");
+  if (!ops_aligned(ids, id_bytes) || !ops_aligned(dout, 16) || !ops_aligned(dtable, 16) || !ops_aligned(workspace, 16))
+    return ops_fail(MHC_ERR_ALIGN, "dout, dtable and workspace must be 16-byte aligned, ids to their size");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const size_t gb = dtype_bytes(grad_dtype);
+  if (T == 0)
+    return ops_cuda(cudaMemset2DAsync(dtable, (size_t)ld * gb, 0, (size_t)H * gb, (size_t)V, s), "cudaMemset2DAsync");
+  const EmbedGradWs w = embed_grad_plan(T, V, H);
+  if (!workspace || ws_bytes < w.total)
+    return ops_fail(MHC_ERR_WORKSPACE, "workspace NULL or smaller than mhc_embed_grad_workspace_bytes(T, V, H)");
+  const size_t b = dtype_bytes(dtype);
+  const Rows in[] = {{ids, 1, T, T, (size_t)id_bytes}, {dout, T, (int64_t)streams * H, (int64_t)streams * H, b}};
+  const Rows out[] = {{dtable, V, H, ld, gb}, {workspace, 1, (int64_t)w.total, 1, 1}};
+  for (const Rows& o : out)
+    for (const Rows& i : in)
+      if (rows_overlap(o, i)) return ops_fail(MHC_ERR_ALIAS, "an output overlaps an input");
+  if (rows_overlap(out[0], out[1])) return ops_fail(MHC_ERR_ALIAS, "two outputs overlap");
+
+  char* ws = static_cast<char*>(workspace);
+  SortArgs a = {};
+  a.ids = ids;
+  a.first = first_id;
+  a.V = V;
+  a.has_pad = padding_id != nullptr;
+  a.pad = padding_id ? *padding_id : 0;
+  a.T = (int)T;
+  a.bits = w.digit_bits;
+  a.tiles = w.tiles;
+  a.passes = w.passes;
+  a.valid = reinterpret_cast<int*>(ws + w.valid);
+  int* hist = reinterpret_cast<int*>(ws + w.hist);
+  const size_t per_pass = (size_t)w.tiles * kDigits;
+  cudaError_t e = cudaSuccess;
+  int from = 0;
+  for (int p = 0; p < w.passes && e == cudaSuccess; ++p, from ^= 1) {
+    const bool last = p + 1 == w.passes;
+    a.shift = p * w.digit_bits;
+    a.key_in = reinterpret_cast<uint32_t*>(ws + w.key[from]);
+    a.key_out = reinterpret_cast<uint32_t*>(ws + w.key[from ^ 1]);
+    a.tok_in = reinterpret_cast<int*>(ws + w.tok[from]);
+    a.tok_out = reinterpret_cast<int*>(ws + w.tok[from ^ 1]);
+    a.hist_in = hist + p * per_pass;
+    a.hist_out = last ? nullptr : hist + (p + 1) * per_pass;
+    if (p == 0) {
+      if (id_bytes == 4) sort_count_kernel<int32_t><<<w.tiles, kSortThreads, 0, s>>>(a);
+      else sort_count_kernel<int64_t><<<w.tiles, kSortThreads, 0, s>>>(a);
+      e = cudaGetLastError();
+      if (e != cudaSuccess) break;
+    }
+    sort_pass_kernel<<<w.tiles, kSortThreads, 0, s>>>(a, p == 0, last);
+    e = cudaGetLastError();
+  }
+  if (e != cudaSuccess) return ops_cuda(e, "embed_grad sort launch");
+  SumArgs m = {};
+  m.dout = dout;
+  m.dtable = dtable;
+  m.ld = ld;
+  m.V = V;
+  m.H = H;
+  m.streams = streams;
+  m.tiles = w.tiles;
+  m.chunks = w.chunks;
+  m.wt = (int)(streams * b);
+  m.wr = (int)gb;
+  m.accumulate = accumulate != 0;
+  m.scale = scale;
+  m.key = reinterpret_cast<const uint32_t*>(ws + w.key[from]);
+  m.tok = reinterpret_cast<const int*>(ws + w.tok[from]);
+  m.valid = a.valid;
+  m.bounds = reinterpret_cast<Bounds*>(ws + w.bounds);
+  m.carry = reinterpret_cast<float*>(ws + w.carry);
+  const dim3 grid(w.chunks, (H + kColumns - 1) / kColumns);
+  MHC_BY_DTYPE(dtype, E, { e = sum_launch<E>(m, grad_dtype, grid, s); });
+  return ops_cuda(e, "embed_grad sum launch");
+}
+
+}  // extern "C"

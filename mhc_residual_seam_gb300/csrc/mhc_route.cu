@@ -1,0 +1,334 @@
+// mhc_route and its gradient: scores of a token's experts, the choice of the
+// best k (in the best groups), their weights and the experts' loads.
+
+#include "mhc_ops.cuh"
+
+namespace mhc {
+
+constexpr int kRouteWarps = 4;
+constexpr int kMaxExperts = 1024;
+
+template <typename T>
+__device__ __forceinline__ float logit_of(const T* p) {
+  float l;
+  if constexpr (sizeof(T) == 4) l = *p;
+  else l = pair_of((uint32_t)*reinterpret_cast<const uint16_t*>(p), T()).x;
+  return l == l ? l : -INFINITY;  // a NaN logit is never chosen, as -inf
+}
+
+// exp(l - max) with equal infinities at distance zero.
+__device__ __forceinline__ float soft_exp(float l, float m) { return l == -INFINITY ? 0.f : expf(l == m ? 0.f : l - m); }
+__device__ __forceinline__ float logistic(float l) { return 1.0f / (1.0f + expf(-l)); }
+
+// A key whose unsigned order is the values' order; 0 for what cannot be chosen.
+__device__ __forceinline__ uint32_t order_key(float x) {
+  if (!(x > -INFINITY)) return 0u;
+  const uint32_t u = __float_as_uint(x + 0.0f);  // -0 and +0 are equal
+  return u ^ (u >> 31 ? 0xffffffffu : 0x80000000u);
+}
+__device__ __forceinline__ float order_value(uint32_t k) {
+  return k ? __uint_as_float(k ^ (k >> 31 ? 0x80000000u : 0xffffffffu)) : -INFINITY;
+}
+
+struct RouteArgs {
+  const void* logits;
+  int64_t ld, T;
+  const float* bias;
+  int E, groups, top_groups, k;
+  bool sigmoid, renorm;
+  float scale;
+  int* indices;
+  float* weights;
+  int* counts;
+  unsigned* ticket;  // workspace: CTAs done, then the E loads (all zero between calls)
+  unsigned* loads;
+};
+
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+  return x;
+}
+
+// One warp per token; lane l holds the scores of experts l*EPL .. l*EPL+EPL-1
+// as order keys, so the lowest lane that has the maximum also has the lowest
+// index.  A round takes the warp's maximum (one redux), finds its lane (one
+// ballot), and that lane drops the expert and looks for its next best.
+template <typename T, int EPL>
+__global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs a) {
+  __shared__ uint32_t keys[kRouteWarps][EPL * 32];
+  __shared__ int load[EPL * 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int e = threadIdx.x; e < EPL * 32; e += blockDim.x) load[e] = 0;
+  __syncthreads();
+  const int per = a.E / a.groups;
+  for (int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp; t < a.T; t += (int64_t)gridDim.x * kRouteWarps) {
+    const T* row = static_cast<const T*>(a.logits) + t * a.ld;
+    float s[EPL];
+    uint32_t key[EPL];
+    float m = -INFINITY, total = 0.f;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const int e = lane * EPL + i;
+      s[i] = e < a.E ? logit_of(row + e) : -INFINITY;
+      m = fmaxf(m, s[i]);
+    }
+    if (!a.sigmoid) {
+      m = warp_max(m);
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) total += soft_exp(s[i], m);
+      total = warp_sum(total);
+    }
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const int e = lane * EPL + i;
+      float v = a.sigmoid ? logistic(s[i]) : soft_exp(s[i], m);
+      if (a.bias && e < a.E) v = (a.sigmoid ? v : v / total) + a.bias[e];
+      key[i] = s[i] == -INFINITY ? 0u : order_key(v);
+    }
+    if (a.groups > 1) {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) keys[warp][lane * EPL + i] = key[i];
+      __syncwarp();
+      uint32_t b1 = 0, b2 = 0;
+      if (lane < a.groups)
+        for (int j = 0; j < per; ++j) {
+          const uint32_t q = keys[warp][lane * per + j];
+          b2 = max(b2, min(b1, q));
+          b1 = max(b1, q);
+        }
+      __syncwarp();
+      const uint32_t mine = b1 == 0 ? 0u : order_key(order_value(b1) + (b2 ? order_value(b2) : 0.f));
+      int rank = 0;
+      for (int g = 0; g < a.groups; ++g) {
+        const uint32_t other = __shfl_sync(0xffffffffu, mine, g);
+        rank += other > mine || (other == mine && g < lane);
+      }
+      const unsigned keep = __ballot_sync(0xffffffffu, lane < a.groups && rank < a.top_groups);
+#pragma unroll
+      for (int i = 0; i < EPL; ++i)
+        if (!((keep >> ((lane * EPL + i) / per & 31)) & 1)) key[i] = 0;
+    }
+    uint32_t best = 0;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) best = max(best, key[i]);
+    int chosen = -1;  // lane j ends with the expert of slot j
+    for (int j = 0; j < a.k; ++j) {
+      const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+      if (top == 0) break;
+      const int who = __ffs(__ballot_sync(0xffffffffu, best == top)) - 1;
+      int at = 0;
+      if (lane == who) {
+        best = 0;
+        bool found = false;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+          if (!found && key[i] == top) {
+            found = true;
+            at = lane * EPL + i;
+            key[i] = 0;
+          }
+          best = max(best, key[i]);
+        }
+      }
+      at = __shfl_sync(0xffffffffu, at, who);
+      if (lane == j) chosen = at;
+    }
+    float w = 0.f;
+    if (chosen >= 0) {
+      const float l = logit_of(row + chosen);
+      w = a.sigmoid ? logistic(l) : soft_exp(l, m);
+      if (!a.renorm && !a.sigmoid) w = w / total;
+      atomicAdd(&load[chosen], 1);
+    }
+    if (a.renorm) {
+      const float sum = warp_sum(w);
+      w = sum > 0.f ? a.scale * w / sum : 0.f;
+    } else {
+      w *= a.scale;
+    }
+    if (lane < a.k) {
+      a.indices[t * a.k + lane] = chosen;
+      a.weights[t * a.k + lane] = w;
+    }
+  }
+  if (!a.counts) return;
+  // Loads of all CTAs: whole-number atomics, so their order does not matter.
+  // The last CTA to come copies them out and leaves the workspace zero.
+  __shared__ bool last;
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.E; e += blockDim.x)
+    if (load[e]) atomicAdd(a.loads + e, (unsigned)load[e]);
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) last = atom_add_acq_rel_gpu(a.ticket, 1u) == gridDim.x - 1;
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  for (int e = threadIdx.x; e < a.E; e += blockDim.x) a.counts[e] = (int)atomicExch(a.loads + e, 0u);
+  if (threadIdx.x == 0) *a.ticket = 0;
+}
+
+struct RouteGradArgs {
+  const float* dweights;
+  const void* logits;
+  int64_t ld, T;
+  const int* indices;
+  int E, k;
+  bool sigmoid, renorm;
+  float scale;
+  void* dlogits;
+  int64_t ld_d;
+};
+
+template <typename T>
+__device__ __forceinline__ void store_one(T* p, float x) {
+  if constexpr (sizeof(T) == 4) *p = x;
+  else *reinterpret_cast<uint16_t*>(p) = (uint16_t)word_of(x, 0.f, T());
+}
+
+// One warp per token; lane j < k holds slot j.  The row of gradients is put
+// together in shared memory.
+template <typename T, int EPL>
+__global__ void __launch_bounds__(kRouteWarps * 32) route_grad_kernel(const RouteGradArgs a) {
+  __shared__ float rows[kRouteWarps][EPL * 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float* out = rows[warp];
+  for (int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp; t < a.T; t += (int64_t)gridDim.x * kRouteWarps) {
+    const T* row = static_cast<const T*>(a.logits) + t * a.ld;
+    int e = lane < a.k ? a.indices[t * a.k + lane] : -1;
+    if (e >= a.E) e = -1;
+    const float dw = e >= 0 ? a.dweights[t * a.k + lane] : 0.f;
+    const float l = e >= 0 ? logit_of(row + e) : -INFINITY;
+    for (int i = lane; i < a.E; i += 32) out[i] = 0.f;
+    __syncwarp();
+    if (a.sigmoid || a.renorm) {
+      float v, d;
+      if (a.sigmoid) v = e >= 0 ? logistic(l) : 0.f;
+      else v = soft_exp(l, warp_max(l));
+      if (a.renorm) {
+        const float total = warp_sum(v);
+        const float q = total > 0.f ? v / total : 0.f;
+        const float mean = warp_sum(q * dw);
+        d = a.scale * q * (dw - mean);
+        if (a.sigmoid) d *= 1.f - v;
+      } else {
+        d = a.scale * dw * v * (1.f - v);
+      }
+      if (e >= 0) atomicAdd(&out[e], d);
+      __syncwarp();
+    } else {
+      float m = -INFINITY, total = 0.f;
+      for (int i = lane; i < a.E; i += 32) m = fmaxf(m, logit_of(row + i));
+      m = warp_max(m);
+      for (int i = lane; i < a.E; i += 32) total += soft_exp(logit_of(row + i), m);
+      total = warp_sum(total);
+      const float mean = warp_sum(total > 0.f ? soft_exp(l, m) / total * dw : 0.f);
+      if (e >= 0) atomicAdd(&out[e], dw);
+      __syncwarp();
+      for (int i = lane; i < a.E; i += 32) {
+        const float p = total > 0.f ? soft_exp(logit_of(row + i), m) / total : 0.f;
+        out[i] = a.scale * p * (out[i] - mean);
+      }
+      __syncwarp();
+    }
+    T* d = static_cast<T*>(a.dlogits) + t * a.ld_d;
+    for (int i = lane; i < a.E; i += 32) store_one(d + i, out[i]);
+    __syncwarp();
+  }
+}
+
+static int route_checks(int64_t T, int E, int k, int dtype, int score, int64_t ld, float scale) {
+  if (!dtype_ok(dtype)) return ops_fail(MHC_ERR_CONFIG, "unknown dtype");
+  if (score != MHC_SCORE_SOFTMAX && score != MHC_SCORE_SIGMOID) return ops_fail(MHC_ERR_CONFIG, "unknown score");
+  if (T < 0 || E < 1 || E > kMaxExperts) return ops_fail(MHC_ERR_SHAPE, "need T >= 0 and 1 <= E <= 1024");
+  if (k < 1 || k > 32 || k > E) return ops_fail(MHC_ERR_SHAPE, "need 1 <= k <= min(E, 32)");
+  if (ld < E) return ops_fail(MHC_ERR_SHAPE, "the row stride must be at least E");
+  if (!(scale == scale)) return ops_fail(MHC_ERR_CONFIG, "scale is not a number");
+  return MHC_OK;
+}
+
+#define MHC_BY_EXPERTS(E, ...)                                   \
+  if (E <= 32) { constexpr int N = 1; __VA_ARGS__; }             \
+  else if (E <= 64) { constexpr int N = 2; __VA_ARGS__; }        \
+  else if (E <= 128) { constexpr int N = 4; __VA_ARGS__; }       \
+  else if (E <= 256) { constexpr int N = 8; __VA_ARGS__; }       \
+  else if (E <= 512) { constexpr int N = 16; __VA_ARGS__; }      \
+  else { constexpr int N = 32; __VA_ARGS__; }
+
+}  // namespace mhc
+
+extern "C" {
+
+size_t mhc_route_workspace_bytes(int E) { return E > 0 ? 256 + ((size_t)E * 4 + 255) / 256 * 256 : 0; }
+
+int mhc_route(const void* logits, int64_t ld, mhc_dtype dtype, const float* bias, mhc_score score, int E, int groups,
+              int top_groups, int k, int renorm, float scale, int64_t T, int32_t* indices, float* weights,
+              int32_t* counts, void* workspace, size_t ws_bytes, void* stream) {
+  using namespace mhc;
+  int rc = route_checks(T, E, k, dtype, score, ld, scale);
+  if (rc != MHC_OK) return rc;
+  if (groups < 1 || groups > 32 || E % groups != 0 || top_groups < 1 || top_groups > groups)
+    return ops_fail(MHC_ERR_SHAPE, "need 1 <= groups <= 32, E a multiple of groups and 1 <= top_groups <= groups");
+  if (k > E / groups * top_groups) return ops_fail(MHC_ERR_SHAPE, "k is more than the experts of top_groups groups");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (!ops_aligned(counts, 4)) return ops_fail(MHC_ERR_ALIGN, "counts is not aligned");
+  if (T == 0) return counts ? ops_cuda(cudaMemsetAsync(counts, 0, (size_t)E * 4, s), "cudaMemsetAsync") : MHC_OK;
+  if (!logits || !indices || !weights) return ops_fail(MHC_ERR_NULL, "logits, indices and weights are required");
+  const size_t b = dtype_bytes(dtype), need = counts ? mhc_route_workspace_bytes(E) : 0;
+  if (!ops_aligned(logits, b) || !ops_aligned(bias, 4) || !ops_aligned(indices, 4) || !ops_aligned(weights, 4) ||
+      (counts && !ops_aligned(workspace, 16)))
+    return ops_fail(MHC_ERR_ALIGN, "a pointer is not aligned to its type");
+  if (counts && (!workspace || ws_bytes < need))
+    return ops_fail(MHC_ERR_WORKSPACE, "counts needs a workspace of mhc_route_workspace_bytes(E)");
+  const Rows in[] = {{logits, T, E, ld, b}, {bias, 1, E, E, 4}};
+  const Rows out[] = {{indices, 1, T * k, 1, 4}, {weights, 1, T * k, 1, 4}, {counts, 1, E, E, 4},
+                      {counts ? workspace : nullptr, 1, (int64_t)need, 1, 1}};
+  for (int o = 0; o < 4; ++o) {
+    for (const Rows& i : in)
+      if (rows_overlap(out[o], i)) return ops_fail(MHC_ERR_ALIAS, "an output overlaps an input");
+    for (int q = o + 1; q < 4; ++q)
+      if (rows_overlap(out[o], out[q])) return ops_fail(MHC_ERR_ALIAS, "two outputs overlap");
+  }
+  int sms = 0;
+  cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return ops_cuda(e, "device query");
+  unsigned* ws = static_cast<unsigned*>(workspace);
+  const RouteArgs a = {logits, ld, T, bias, E, groups, top_groups, k, score == MHC_SCORE_SIGMOID, renorm != 0, scale,
+                       indices, weights, counts, counts ? ws + 16 : nullptr, counts ? ws + 64 : nullptr};
+  int64_t grid = (T + kRouteWarps - 1) / kRouteWarps;
+  if (grid > (int64_t)sms * 12) grid = (int64_t)sms * 12;
+  MHC_BY_DTYPE(dtype, D, { MHC_BY_EXPERTS(E, { route_kernel<D, N><<<(unsigned)grid, kRouteWarps * 32, 0, s>>>(a); }) });
+  return ops_cuda(cudaGetLastError(), "route launch");
+}
+
+int mhc_route_grad(const float* dweights, const void* logits, int64_t ld, mhc_dtype dtype, const int32_t* indices,
+                   mhc_score score, int E, int k, int renorm, float scale, int64_t T, void* dlogits, int64_t ld_d,
+                   void* stream) {
+  using namespace mhc;
+  int rc = route_checks(T, E, k, dtype, score, ld, scale);
+  if (rc != MHC_OK) return rc;
+  if (ld_d < E) return ops_fail(MHC_ERR_SHAPE, "the row stride must be at least E");
+  if (T == 0) return MHC_OK;
+  if (!dweights || !logits || !indices || !dlogits)
+    return ops_fail(MHC_ERR_NULL, "dweights, logits, indices and dlogits are required");
+  const size_t b = dtype_bytes(dtype);
+  if (!ops_aligned(logits, b) || !ops_aligned(dlogits, b) || !ops_aligned(dweights, 4) || !ops_aligned(indices, 4))
+    return ops_fail(MHC_ERR_ALIGN, "a pointer is not aligned to its type");
+  const Rows out = {dlogits, T, E, ld_d, b};
+  if (rows_overlap(out, {logits, T, E, ld, b}) || rows_overlap(out, {dweights, 1, T * k, 1, 4}) ||
+      rows_overlap(out, {indices, 1, T * k, 1, 4}))
+    return ops_fail(MHC_ERR_ALIAS, "dlogits overlaps an input");
+  int sms = 0;
+  cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return ops_cuda(e, "device query");
+  const RouteGradArgs a = {dweights, logits, ld, T, indices, E, k, score == MHC_SCORE_SIGMOID, renorm != 0, scale,
+                           dlogits, ld_d};
+  int64_t grid = (T + kRouteWarps - 1) / kRouteWarps;
+  if (grid > (int64_t)sms * 12) grid = (int64_t)sms * 12;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  MHC_BY_DTYPE(dtype, D, { MHC_BY_EXPERTS(E, { route_grad_kernel<D, N><<<(unsigned)grid, kRouteWarps * 32, 0, s>>>(a); }) });
+  return ops_cuda(cudaGetLastError(), "route_grad launch");
+}
+
+}  // extern "C"
