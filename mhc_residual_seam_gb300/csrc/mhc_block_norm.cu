@@ -29,228 +29,364 @@ struct BlockNormGradArgs {
   float* parts;  // [gridDim.x][3][H] column sums of each CTA: gamma_post, gate, gamma_pre
 };
 
-// A team of threads works on one row: a warp (several rows per CTA) or the
-// whole CTA.  team_sum adds over the team; `buf` is the caller's own slot of
-// shared memory for this sum, so one barrier per sum is enough.
+// A team of threads works on one row: a warp (rows of at most 256 columns,
+// several teams per CTA) or the whole CTA.  A thread keeps the same VPT groups of
+// eight columns for all of its team's rows.
 template <bool WARP>
-__device__ __forceinline__ float team_sum(float x, float* buf) {
-  x = warp_sum(x);
+struct Team {
+  int lanes, lane, teams, team;
+  __device__ Team() {
+    lanes = WARP ? 32 : blockDim.x;
+    lane = WARP ? (threadIdx.x & 31) : threadIdx.x;
+    teams = WARP ? (blockDim.x >> 5) : 1;
+    team = WARP ? (threadIdx.x >> 5) : 0;
+  }
+};
+
+// The sum over a team; `buf` is the caller's own slot of shared memory for this
+// sum (the slots of warps that the CTA lacks hold zero), so one barrier per sum is
+// enough.  The warps' sums are added in the same order everywhere.
+template <bool WARP>
+__device__ __forceinline__ float team_sum(float2 v, float4* buf) {
+  float x = warp_sum(v.x + v.y);
   if constexpr (!WARP) {
-    const int w = threadIdx.x >> 5, nw = blockDim.x >> 5;
-    if ((threadIdx.x & 31) == 0) buf[w] = x;
+    const int w = threadIdx.x >> 5, quads = (blockDim.x + 127) >> 7;
+    if ((threadIdx.x & 31) == 0) reinterpret_cast<float*>(buf)[w] = x;
     __syncthreads();
     x = 0.f;
-    for (int i = 0; i < nw; ++i) x += buf[i];
+    for (int i = 0; i < quads; ++i) {
+      const float4 s = buf[i];
+      x += (s.x + s.y) + (s.z + s.w);
+    }
   }
   return x;
 }
 
+// A row's weights of one thread: gamma_post * gate (channel) and gamma_pre.
+template <typename T>
+__device__ __forceinline__ Vec8 weight8(const void* w, int g) {
+  if (w) return unpack(ld8(static_cast<const T*>(w) + g * 8));
+  Vec8 o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o.p[i] = make_float2(1.f, 1.f);
+  return o;
+}
+__device__ __forceinline__ Vec8 mul8(const Vec8& a, const Vec8& b) {
+  Vec8 o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o.p[i] = __fmul2_rn(a.p[i], b.p[i]);
+  return o;
+}
+
+// Threads of a CTA at most: 640 leaves a thread the registers for the weights and
+// column sums of its columns (and the forward pass a second CTA per SM), 1024 is
+// for rows of more than 5120 columns.
+constexpr int kTeamThreads = 640, kBigThreads = 1024;
+
 // p = y rho1 gamma_post;  r' = scale r + gate p;  norm = r' rho2 gamma_pre.
 // Bound by HBM: y and r are read once, r' and the norm written once; the row
 // stays in registers between the two sums of squares.  The norm is formed from
-// the fp32 r', so it carries one rounding only.
-template <typename T, int VPT, bool WARP>
-__global__ void __launch_bounds__(WARP ? 128 : 512) block_norm_kernel(const BlockNormArgs a) {
-  __shared__ float buf[2][16];
-  const int lanes = WARP ? 32 : blockDim.x;
-  const int lane = WARP ? (threadIdx.x & 31) : threadIdx.x;
-  const int64_t t = WARP ? (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
-  if (WARP && t >= a.T) return;
+// the fp32 r', so it carries one rounding only.  Each thread fetches its columns
+// STAGES rows ahead (0: no shared memory for that, plain loads), so loads stay in
+// flight across the two barriers of a row.  Arithmetic is two columns per
+// instruction; gamma_post and a channel gate are one fp32 factor.
+template <typename T, int VPT, bool WARP, bool BIG, int STAGES>
+__global__ void __launch_bounds__(BIG ? kBigThreads : kTeamThreads, BIG ? 1 : 2) block_norm_kernel(const BlockNormArgs a) {
+  __shared__ float4 buf[2][2][8];
+  extern __shared__ uint4 ring[];
+  const Team<WARP> q;
   const int segs = a.H >> 3;
   const float inv = 1.0f / (float)a.H;
   const T* y = static_cast<const T*>(a.y);
   const T* r = static_cast<const T*>(a.r);
-
-  Vec8 p[VPT], x[VPT];
-  float ss = 0.f;
-#pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int g = lane + i * lanes;
-    p[i] = {};
-    x[i] = {};
-    if (g < segs) {
-      x[i] = unpack(ld8_stream(r + t * a.ld_r + g * 8));
-      if (y) p[i] = unpack(ld8_stream(y + t * a.ld_y + g * 8));
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fmaf(p[i].v[e], p[i].v[e], ss);
-  }
-  if (y) {
-    float rho = 1.f;
-    if (a.gamma_post) {
-      ss = team_sum<WARP>(ss, buf[0]);
-      rho = 1.0f / sqrtf(fmaf(ss, inv, a.eps));
-      if (lane == 0) a.rstd_post[t] = rho;
-    }
-    const float gt = a.gate_mode == MHC_GATE_TOKEN ? static_cast<const float*>(a.gate)[t] : 1.f;
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int g = lane + i * lanes;
-      if (g < segs) {
-        Vec8 w, c;
-        if (a.gamma_post) w = unpack(ld8(static_cast<const T*>(a.gamma_post) + g * 8));
-        if (a.gate_mode == MHC_GATE_CHANNEL) c = unpack(ld8(static_cast<const T*>(a.gate) + g * 8));
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          float q = p[i].v[e];
-          if (a.gamma_post) q = q * rho * w.v[e];
-          q *= a.gate_mode == MHC_GATE_CHANNEL ? c.v[e] : gt;
-          x[i].v[e] = fmaf(a.scale, x[i].v[e], q);
-        }
-        st8_stream(static_cast<T*>(a.r_out) + t * a.ld_ro + g * 8, pack<T>(x[i]));
-      }
-    }
-  }
-  if (a.gamma_pre) {
-    ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < VPT; ++i)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(x[i].v[e], x[i].v[e], ss);
-    ss = team_sum<WARP>(ss, buf[1]);
-    const float rho = 1.0f / sqrtf(fmaf(ss, inv, a.eps));
-    if (lane == 0) a.rstd_pre[t] = rho;
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int g = lane + i * lanes;
-      if (g < segs) {
-        const Vec8 w = unpack(ld8(static_cast<const T*>(a.gamma_pre) + g * 8));
-        Vec8 n;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) n.v[e] = x[i].v[e] * rho * w.v[e];
-        st8_stream(static_cast<T*>(a.norm) + t * a.ld_n + g * 8, pack<T>(n));
-      }
-    }
-  }
-}
-
-// With u = r' rho2 and c = gamma_pre dnorm:
-//   G = dr_out + rho2 (c - u mean(c u)),  dgamma_pre += dnorm u,  dr = scale G
-// and with u = y rho1, dp = gate G, c = gamma_post dp:
-//   dy = rho1 (c - u mean(c u)),  dgamma_post += dp u,  dgate += u gamma_post G
-// Bound by HBM: four rows read, two written.  A thread keeps the same columns
-// over all of its CTA's rows, so the column sums stay in registers until the
-// CTA's end; a second kernel adds the CTAs' sums in a fixed order.
-template <typename T, int VPT, bool WARP>
-__global__ void __launch_bounds__(WARP ? 128 : 512) block_norm_grad_kernel(const BlockNormGradArgs a) {
-  __shared__ float buf[2][3][16];
-  const int lanes = WARP ? 32 : blockDim.x;
-  const int lane = WARP ? (threadIdx.x & 31) : threadIdx.x;
-  const int teams = WARP ? (blockDim.x >> 5) : 1, team = WARP ? (threadIdx.x >> 5) : 0;
-  const int segs = a.H >> 3;
-  const float inv = 1.0f / (float)a.H;
-  float s_post[VPT][8] = {}, s_gate[VPT][8] = {}, s_pre[VPT][8] = {};
-  int flip = 0;
-  for (int64_t t = (int64_t)blockIdx.x * teams + team; t < a.T; t += (int64_t)gridDim.x * teams, flip ^= 1) {
-    Vec8 G[VPT], u[VPT];
-    const int64_t row = t * a.H;
-    float m = 0.f;
-    if (a.gamma_pre) {
-      const float rho = a.rstd_pre[t];
+  const int64_t step = (int64_t)gridDim.x * q.teams;
+  const int unit = segs * (int)(sizeof(T) / 2);  // 16-byte pieces of a row
+  uint4* mine = ring + q.team * STAGES * 2 * unit;
+  auto fetch = [&](int64_t t, int stage) {
+    if (t < a.T) {
+      uint4* s = mine + stage * 2 * unit;
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
-        const int g = lane + i * lanes;
-        G[i] = {};
-        u[i] = {};
+        const int g = q.lane + i * q.lanes;
         if (g < segs) {
-          u[i] = unpack(ld8_stream(static_cast<const T*>(a.r_out) + row + g * 8));
-          const Vec8 dn = unpack(ld8_stream(static_cast<const T*>(a.dnorm) + row + g * 8));
-          const Vec8 w = unpack(ld8(static_cast<const T*>(a.gamma_pre) + g * 8));
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            u[i].v[e] *= rho;
-            s_pre[i][e] = fmaf(dn.v[e], u[i].v[e], s_pre[i][e]);
-            G[i].v[e] = w.v[e] * dn.v[e];
-            m = fmaf(G[i].v[e], u[i].v[e], m);
-          }
+          fetch8<T>(s, segs, g, r + t * a.ld_r + g * 8);
+          if (y) fetch8<T>(s + unit, segs, g, y + t * a.ld_y + g * 8);
         }
       }
-      m = team_sum<WARP>(m, buf[flip][0]) * inv;
+    }
+    cp_async_commit();
+  };
+  int64_t t = (int64_t)blockIdx.x * q.teams + q.team;
+#pragma unroll
+  for (int s = 0; s < STAGES; ++s) fetch(t + s * step, s);
+  Vec8 wc[VPT];
+  Raw8<T> wn[VPT];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int g = q.lane + i * q.lanes;
+    if (g < segs) {
+      wc[i] = mul8(weight8<T>(a.gamma_post, g), weight8<T>(a.gate_mode == MHC_GATE_CHANNEL ? a.gate : nullptr, g));
+      if (a.gamma_pre) wn[i] = ld8(static_cast<const T*>(a.gamma_pre) + g * 8);
+    }
+  }
+  const float* gates = a.gate_mode == MHC_GATE_TOKEN ? static_cast<const float*>(a.gate) : nullptr;
+  float gate = gates && t < a.T ? gates[t] : 1.f;
+  if constexpr (!WARP) {
+    if (threadIdx.x < 32) buf[threadIdx.x >> 4][(threadIdx.x >> 3) & 1][threadIdx.x & 7] = make_float4(0.f, 0.f, 0.f, 0.f);
+    __syncthreads();
+  }
+  int stage = 0, flip = 0;
+  for (; t < a.T; t += step, flip ^= 1) {
+    Vec8 p[VPT], x[VPT];
+    if constexpr (STAGES > 0) cp_async_wait<(STAGES > 0 ? STAGES - 1 : 0)>();
+    const uint4* s = mine + stage * 2 * unit;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int g = q.lane + i * q.lanes;
+      p[i] = x[i] = zero8();
+      if (g < segs) {
+        x[i] = unpack(STAGES ? fetched8<T>(s, segs, g) : ld8_stream(r + t * a.ld_r + g * 8));
+        if (y) p[i] = unpack(STAGES ? fetched8<T>(s + unit, segs, g) : ld8_stream(y + t * a.ld_y + g * 8));
+      }
+    }
+    if constexpr (STAGES > 0) {
+      fetch(t + STAGES * step, stage);
+      stage = stage + 1 == STAGES ? 0 : stage + 1;
+    }
+    const float gt = gate;
+    if (gates && t + step < a.T) gate = gates[t + step];
+    if (y) {
+      float k = gt;
+      if (a.gamma_post) {
+        float2 ss = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) ss = __ffma2_rn(p[i].p[e], p[i].p[e], ss);
+        const float rho = 1.0f / sqrtf(fmaf(team_sum<WARP>(ss, buf[flip][0]), inv, a.eps));
+        if (q.lane == 0) a.rstd_post[t] = rho;
+        k *= rho;
+      }
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int g = q.lane + i * q.lanes;
+        if (g < segs) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            x[i].p[e] = __ffma2_rn(__fmul2_rn(p[i].p[e], splat(k)), wc[i].p[e], __fmul2_rn(x[i].p[e], splat(a.scale)));
+          st8_stream(static_cast<T*>(a.r_out) + t * a.ld_ro + g * 8, pack<T>(x[i]));
+        }
+      }
+    }
+    if (a.gamma_pre) {
+      float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < VPT; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) G[i].v[e] = rho * (G[i].v[e] - u[i].v[e] * m);
-    } else {
+        for (int e = 0; e < 4; ++e) ss = __ffma2_rn(x[i].p[e], x[i].p[e], ss);
+      const float rho = 1.0f / sqrtf(fmaf(team_sum<WARP>(ss, buf[flip][1]), inv, a.eps));
+      if (q.lane == 0) a.rstd_pre[t] = rho;
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) G[i] = {};
-    }
+      for (int i = 0; i < VPT; ++i) {
+        const int g = q.lane + i * q.lanes;
+        if (g < segs) {
+          const Vec8 w = unpack(wn[i]);
+          Vec8 n;
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int g = lane + i * lanes;
-      if (g < segs) {
-        if (a.dr_out) {
-          const Vec8 d = unpack(ld8_stream(static_cast<const T*>(a.dr_out) + row + g * 8));
-#pragma unroll
-          for (int e = 0; e < 8; ++e) G[i].v[e] += d.v[e];
+          for (int e = 0; e < 4; ++e) n.p[e] = __fmul2_rn(__fmul2_rn(x[i].p[e], splat(rho)), w.p[e]);
+          st8_stream(static_cast<T*>(a.norm) + t * a.ld_n + g * 8, pack<T>(n));
         }
-        Vec8 o;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o.v[e] = a.scale * G[i].v[e];
-        st8_stream(static_cast<T*>(a.dr) + row + g * 8, pack<T>(o));
-      }
-    }
-    if (!a.y) continue;
-    const float rho = a.gamma_post ? a.rstd_post[t] : 1.f;
-    const float gt = a.gate_mode == MHC_GATE_TOKEN ? static_cast<const float*>(a.gate)[t] : 1.f;
-    float dg = 0.f;
-    m = 0.f;
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int g = lane + i * lanes;
-      u[i] = {};
-      if (g < segs) {
-        u[i] = unpack(ld8_stream(static_cast<const T*>(a.y) + row + g * 8));
-        Vec8 w, c;
-        if (a.gamma_post) w = unpack(ld8(static_cast<const T*>(a.gamma_post) + g * 8));
-        if (a.gate_mode == MHC_GATE_CHANNEL) c = unpack(ld8(static_cast<const T*>(a.gate) + g * 8));
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          u[i].v[e] *= rho;
-          const float we = a.gamma_post ? w.v[e] : 1.f;
-          const float pg = u[i].v[e] * we * G[i].v[e];
-          dg += pg;
-          s_gate[i][e] += pg;
-          const float dp = (a.gate_mode == MHC_GATE_CHANNEL ? c.v[e] : gt) * G[i].v[e];
-          s_post[i][e] = fmaf(dp, u[i].v[e], s_post[i][e]);
-          G[i].v[e] = dp * we;
-          m = fmaf(G[i].v[e], u[i].v[e], m);
-        }
-      }
-    }
-    if (a.gate_mode == MHC_GATE_TOKEN) {
-      dg = team_sum<WARP>(dg, buf[flip][1]);
-      if (lane == 0) a.dgate[t] = dg;
-    }
-    if (a.gamma_post) m = team_sum<WARP>(m, buf[flip][2]) * inv;
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int g = lane + i * lanes;
-      if (g < segs) {
-        Vec8 o;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o.v[e] = a.gamma_post ? rho * (G[i].v[e] - u[i].v[e] * m) : G[i].v[e];
-        st8_stream(static_cast<T*>(a.dy) + row + g * 8, pack<T>(o));
       }
     }
   }
-  float* out = a.parts + ((int64_t)blockIdx.x * teams + team) * 3 * a.H;
+  if constexpr (STAGES > 0) cp_async_wait<0>();
+}
+
+// With x = r', c = gamma_pre dnorm and M = sum c x over the row:
+//   G = dr_out + rho2 c - x (rho2^3 M / H),  dr = scale G,
+//   dgamma_pre += rho2 dnorm x
+// and with g = rho1 G, w = gamma_post * gate (channel), b = w g, N = sum b y:
+//   dy = gate(token) (b - y (rho1^2 N / H)),  dgate(token) = N
+//   S += gate(token) g y: dgamma_post = S gate(channel), dgate(channel) = S gamma_post
+// (S is one column sum for both; without gamma_post, rho1 = 1 and dy has no second
+// term.)  Bound by HBM: four rows read, two written.  A thread keeps the same
+// columns over all of its team's rows, so the column sums stay in registers until
+// the end; a second kernel adds the CTAs' sums in a fixed order.  Rows are
+// fetched ahead as in the forward kernel.
+template <typename T, int VPT, bool WARP, bool BIG, int STAGES>
+__global__ void __launch_bounds__(BIG ? kBigThreads : kTeamThreads) block_norm_grad_kernel(const BlockNormGradArgs a) {
+  __shared__ float4 buf[2][2][8];
+  extern __shared__ uint4 ring[];
+  const Team<WARP> q;
+  const int segs = a.H >> 3;
+  const float inv = 1.0f / (float)a.H;
+  const int unit = segs * (int)(sizeof(T) / 2);
+  uint4* mine = ring + q.team * STAGES * 4 * unit;
+  const T* src[4] = {static_cast<const T*>(a.r_out), static_cast<const T*>(a.dnorm), static_cast<const T*>(a.dr_out),
+                     static_cast<const T*>(a.y)};
+  auto fetch = [&](int64_t t, int stage) {
+    if (t < a.T) {
+      uint4* s = mine + stage * 4 * unit;
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int g = q.lane + i * q.lanes;
+        const int64_t at = t * a.H + g * 8;
+        if (g < segs) {
+#pragma unroll
+          for (int m = 0; m < 4; ++m)
+            if (src[m]) fetch8<T>(s + m * unit, segs, g, src[m] + at);
+        }
+      }
+    }
+    cp_async_commit();
+  };
+  Vec8 s_post[VPT], s_pre[VPT], wc[VPT];
+  Raw8<T> wn[VPT];
+  int flip = 0, stage = 0;
+  const int64_t step = (int64_t)gridDim.x * q.teams;
+  int64_t t = (int64_t)blockIdx.x * q.teams + q.team;
+#pragma unroll
+  for (int s = 0; s < STAGES; ++s) fetch(t + s * step, s);
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int g = lane + i * lanes;
+    const int g = q.lane + i * q.lanes;
+    s_post[i] = s_pre[i] = zero8();
+    if (g < segs) {
+      wc[i] = mul8(weight8<T>(a.gamma_post, g), weight8<T>(a.gate_mode == MHC_GATE_CHANNEL ? a.gate : nullptr, g));
+      if (a.gamma_pre) wn[i] = ld8(static_cast<const T*>(a.gamma_pre) + g * 8);
+    }
+  }
+  const float* gates = a.gate_mode == MHC_GATE_TOKEN ? static_cast<const float*>(a.gate) : nullptr;
+  float n_pre = 1.f, n_post = 1.f, n_gate = 1.f;  // the next row's factors
+  auto factors = [&](int64_t r) {
+    if (r < a.T) {
+      if (a.gamma_pre) n_pre = a.rstd_pre[r];
+      if (a.gamma_post) n_post = a.rstd_post[r];
+      if (gates) n_gate = gates[r];
+    }
+  };
+  factors(t);
+  if constexpr (!WARP) {
+    if (threadIdx.x < 32) buf[threadIdx.x >> 4][(threadIdx.x >> 3) & 1][threadIdx.x & 7] = make_float4(0.f, 0.f, 0.f, 0.f);
+    __syncthreads();
+  }
+  for (; t < a.T; t += step, flip ^= 1) {
+    Vec8 G[VPT], x[VPT];
+    const int64_t row = t * a.H;
+    const float rho2 = n_pre, rho1 = n_post, gt = n_gate;
+    factors(t + step);
+    if constexpr (STAGES > 0) cp_async_wait<(STAGES > 0 ? STAGES - 1 : 0)>();
+    const uint4* s = mine + stage * 4 * unit;
+    auto take = [&](int m, int g) {
+      return unpack(STAGES ? fetched8<T>(s + m * unit, segs, g) : ld8_stream(src[m] + row + g * 8));
+    };
+    if (a.gamma_pre) {
+      float2 m2 = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int g = q.lane + i * q.lanes;
+        G[i] = x[i] = zero8();
+        if (g < segs) {
+          x[i] = take(0, g);
+          const Vec8 dn = take(1, g), w = unpack(wn[i]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 dx = __fmul2_rn(dn.p[e], x[i].p[e]);
+            s_pre[i].p[e] = __ffma2_rn(dx, splat(rho2), s_pre[i].p[e]);
+            G[i].p[e] = __fmul2_rn(w.p[e], dn.p[e]);
+            m2 = __ffma2_rn(G[i].p[e], x[i].p[e], m2);
+          }
+        }
+      }
+      const float k = -rho2 * rho2 * (team_sum<WARP>(m2, buf[flip][0]) * inv) * rho2;
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int g = q.lane + i * q.lanes;
+        const Vec8 d = a.dr_out && g < segs ? take(2, g) : zero8();
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          G[i].p[e] = __ffma2_rn(x[i].p[e], splat(k), __ffma2_rn(G[i].p[e], splat(rho2), d.p[e]));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int g = q.lane + i * q.lanes;
+        G[i] = g < segs ? take(2, g) : zero8();
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int g = q.lane + i * q.lanes;
+      if (g < segs) {
+        Vec8 o;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o.p[e] = __fmul2_rn(G[i].p[e], splat(a.scale));
+        st8_stream(static_cast<T*>(a.dr) + row + g * 8, pack<T>(o));
+      }
+    }
+    if (a.y) {
+      float2 n2 = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int g = q.lane + i * q.lanes;
+        x[i] = zero8();
+        if (g < segs) {
+          x[i] = take(3, g);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 gr = __fmul2_rn(G[i].p[e], splat(rho1));
+            s_post[i].p[e] = __ffma2_rn(__fmul2_rn(gr, splat(gt)), x[i].p[e], s_post[i].p[e]);
+            G[i].p[e] = __fmul2_rn(wc[i].p[e], gr);
+            n2 = __ffma2_rn(G[i].p[e], x[i].p[e], n2);
+          }
+        }
+      }
+      // the row's columns are in registers: its stage takes the row STAGES further on
+      if constexpr (STAGES > 0) fetch(t + STAGES * step, stage);
+      float k = 0.f;
+      if (a.gamma_post || gates) {
+        const float N = team_sum<WARP>(n2, buf[flip][1]);
+        if (gates && q.lane == 0) a.dgate[t] = N;
+        if (a.gamma_post) k = -rho1 * (N * inv) * rho1 * gt;
+      }
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int g = q.lane + i * q.lanes;
+        if (g < segs) {
+          Vec8 o;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            o.p[e] = __fmul2_rn(G[i].p[e], splat(gt));
+            if (a.gamma_post) o.p[e] = __ffma2_rn(x[i].p[e], splat(k), o.p[e]);
+          }
+          st8_stream(static_cast<T*>(a.dy) + row + g * 8, pack<T>(o));
+        }
+      }
+    } else {
+      if constexpr (STAGES > 0) fetch(t + STAGES * step, stage);
+    }
+    if constexpr (STAGES > 0) stage = stage + 1 == STAGES ? 0 : stage + 1;
+  }
+  if constexpr (STAGES > 0) cp_async_wait<0>();
+  float* out = a.parts + ((int64_t)blockIdx.x * q.teams + q.team) * 3 * a.H;
+  const void* channel = a.gate_mode == MHC_GATE_CHANNEL ? a.gate : nullptr;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int g = q.lane + i * q.lanes;
     if (g < segs) {
       float* o = out + g * 8;
-      if (a.dgamma_post) st8(o, pack<float>(*reinterpret_cast<Vec8*>(s_post[i])));
-      if (a.gate_mode == MHC_GATE_CHANNEL) st8(o + a.H, pack<float>(*reinterpret_cast<Vec8*>(s_gate[i])));
-      if (a.dgamma_pre) st8(o + 2 * a.H, pack<float>(*reinterpret_cast<Vec8*>(s_pre[i])));
+      if (a.dgamma_post) st8(o, pack<float>(mul8(s_post[i], weight8<T>(channel, g))));
+      if (channel) st8(o + a.H, pack<float>(mul8(s_post[i], weight8<T>(a.gamma_post, g))));
+      if (a.dgamma_pre) st8(o + 2 * a.H, pack<float>(s_pre[i]));
     }
   }
 }
 
-// Adds the parts' column sums in part order: 32 columns x 8 slices of parts per
-// CTA, the slices joined in slice order.
-__global__ void __launch_bounds__(256) block_norm_fold_kernel(const float* __restrict__ parts, int n, int H, float* post,
-                                                              float* gate, float* pre) {
-  __shared__ float sh[8][33];
+// Adds the parts' column sums in a fixed order: 32 columns x 32 slices of parts
+// per CTA, the slices joined in slice order.
+__global__ void __launch_bounds__(1024) block_norm_fold_kernel(const float* __restrict__ parts, int n, int H, float* post,
+                                                               float* gate, float* pre) {
+  __shared__ float sh[32][33];
   pdl_wait();
   float* out = blockIdx.y == 0 ? post : blockIdx.y == 1 ? gate : pre;
   if (!out) return;
@@ -258,54 +394,88 @@ __global__ void __launch_bounds__(256) block_norm_fold_kernel(const float* __res
   float x = 0.f;
   if (c < H) {
     const float* p = parts + (int64_t)blockIdx.y * H + c;
-    const int lo = (int)((int64_t)n * w / 8), hi = (int)((int64_t)n * (w + 1) / 8);
-#pragma unroll 4
+    const int lo = (int)((int64_t)n * w / 32), hi = (int)((int64_t)n * (w + 1) / 32);
+#pragma unroll 8
     for (int i = lo; i < hi; ++i) x += p[(int64_t)i * 3 * H];
   }
   sh[w][threadIdx.x & 31] = x;
   __syncthreads();
   if (w == 0 && c < H) {
 #pragma unroll
-    for (int i = 1; i < 8; ++i) x += sh[i][threadIdx.x];
+    for (int i = 1; i < 32; ++i) x += sh[i][threadIdx.x];
     out[c] = x;
   }
 }
 
-// Teams: a warp per row up to 1024 columns, else a CTA per row.
+// The teams of a row of H columns and how many rows they fetch ahead.
 struct TeamPlan {
-  bool warp;
-  int vpt, threads;
+  bool warp, big;
+  int vpt, threads, teams, stages;
+  size_t smem;
+  int ctas;  // per SM
 };
-static TeamPlan team_plan(int H) {
+
+constexpr int kSMs = 152;
+constexpr size_t kRingBytes = 216 * 1024;  // shared memory of an SM for rows in flight
+
+static TeamPlan team_plan(int H, size_t type_bytes, int matrices, int sm_threads) {
   const int segs = H / 8;
   TeamPlan p;
-  p.warp = segs <= 128;
-  if (p.warp) {
-    p.threads = 128;
-    p.vpt = segs <= 32 ? 1 : segs <= 64 ? 2 : 4;
-  } else {
-    p.vpt = segs <= 512 ? 1 : segs <= 1024 ? 2 : 4;
-    p.threads = ((segs + p.vpt - 1) / p.vpt + 31) / 32 * 32;
-  }
+  p.warp = segs <= 32;
+  p.vpt = segs <= kBigThreads ? 1 : 2;
+  p.big = segs > kTeamThreads;
+  p.threads = p.warp ? 128 : ((segs + p.vpt - 1) / p.vpt + 31) / 32 * 32;
+  p.teams = p.warp ? 4 : 1;
+  const size_t row = (size_t)H * type_bytes * matrices * p.teams;
+  p.ctas = sm_threads / p.threads;
+  if (p.ctas < 1) p.ctas = 1;
+  if (p.ctas > 16) p.ctas = 16;
+  while (p.ctas > 1 && row * p.ctas * 2 > kRingBytes) --p.ctas;
+  const size_t fit = kRingBytes / (row * p.ctas);
+  p.stages = fit >= 4 ? 4 : fit >= 2 ? 2 : (int)fit;
+  p.smem = row * p.stages;
   return p;
 }
 
-constexpr int kMaxParts = 304;  // column sums kept by the gradient: at most this many teams, two CTAs per SM of 152
+static TeamPlan norm_plan(int H, size_t b) { return team_plan(H, b, 2, 2 * kTeamThreads); }
+static TeamPlan grad_plan(int H, size_t b) { return team_plan(H, b, 4, kTeamThreads); }
 
-static int grad_parts(int64_t T) { return (int)(T < kMaxParts ? T : kMaxParts); }
+// CTAs of the gradient: all resident at once.
+static int64_t grad_ctas(int64_t T, const TeamPlan& p) {
+  const int64_t need = (T + p.teams - 1) / p.teams, most = (int64_t)kSMs * p.ctas;
+  return need < most ? need : most;
+}
 
-#define MHC_BY_TEAM(plan, ...)                                                            \
-  if (plan.warp) {                                                                        \
-    constexpr bool W = true;                                                              \
-    if (plan.vpt == 1) { constexpr int N = 1; __VA_ARGS__; }                              \
-    else if (plan.vpt == 2) { constexpr int N = 2; __VA_ARGS__; }                         \
-    else { constexpr int N = 4; __VA_ARGS__; }                                            \
-  } else {                                                                                \
-    constexpr bool W = false;                                                             \
-    if (plan.vpt == 1) { constexpr int N = 1; __VA_ARGS__; }                              \
-    else if (plan.vpt == 2) { constexpr int N = 2; __VA_ARGS__; }                         \
-    else { constexpr int N = 4; __VA_ARGS__; }                                            \
-  }
+#define MHC_BY_TEAM(plan, ...)                                                                        \
+  if (plan.stages == 4) { constexpr int K = 4; MHC_BY_TEAM_(plan, __VA_ARGS__) }                      \
+  else if (plan.stages == 2) { constexpr int K = 2; MHC_BY_TEAM_(plan, __VA_ARGS__) }                 \
+  else if (plan.stages == 1) { constexpr int K = 1; MHC_BY_TEAM_(plan, __VA_ARGS__) }                 \
+  else { constexpr int K = 0; MHC_BY_TEAM_(plan, __VA_ARGS__) }
+#define MHC_BY_TEAM_(plan, ...)                                                                       \
+  if (plan.warp) { constexpr bool W = true, L = false; constexpr int N = 1; __VA_ARGS__; }            \
+  else if (!plan.big) { constexpr bool W = false, L = false; constexpr int N = 1; __VA_ARGS__; }      \
+  else if (plan.vpt == 1) { constexpr bool W = false, L = true; constexpr int N = 1; __VA_ARGS__; }   \
+  else { constexpr bool W = false, L = true; constexpr int N = 2; __VA_ARGS__; }
+
+template <typename T, int N, bool W, bool L, int K>
+static cudaError_t norm_launch(const BlockNormArgs& a, const TeamPlan& p, cudaStream_t s) {
+  static SmemGrant grant;
+  cudaError_t e = allow_smem(grant, (const void*)block_norm_kernel<T, N, W, L, K>, p.smem);
+  if (e != cudaSuccess) return e;
+  int64_t grid = (a.T + p.teams - 1) / p.teams;
+  if (K && grid > (int64_t)kSMs * p.ctas) grid = (int64_t)kSMs * p.ctas;
+  block_norm_kernel<T, N, W, L, K><<<(unsigned)grid, p.threads, p.smem, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename T, int N, bool W, bool L, int K>
+static cudaError_t grad_launch(const BlockNormGradArgs& a, const TeamPlan& p, int64_t grid, cudaStream_t s) {
+  static SmemGrant grant;
+  cudaError_t e = allow_smem(grant, (const void*)block_norm_grad_kernel<T, N, W, L, K>, p.smem);
+  if (e != cudaSuccess) return e;
+  block_norm_grad_kernel<T, N, W, L, K><<<(unsigned)grid, p.threads, p.smem, s>>>(a);
+  return cudaGetLastError();
+}
 
 constexpr int kMaxWidth = 16384;
 
@@ -361,16 +531,22 @@ int mhc_block_norm(const void* y, int64_t ld_y, const void* r, int64_t ld_r, con
   }
   const BlockNormArgs a = {y, r, gamma_post, gate, gamma_pre, ld_y, ld_r, ld_r_out, ld_norm, gate_mode, res_scale, eps,
                            T, H, r_out, norm, rstd_post, rstd_pre};
-  const TeamPlan plan = team_plan(H);
-  const unsigned grid = (unsigned)(plan.warp ? (T + 3) / 4 : T);
+  const TeamPlan plan = norm_plan(H, b);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  MHC_BY_DTYPE(dtype, E, { MHC_BY_TEAM(plan, { block_norm_kernel<E, N, W><<<grid, plan.threads, 0, s>>>(a); }) });
-  return ops_cuda(cudaGetLastError(), "block_norm launch");
+  cudaError_t e = cudaSuccess;
+  MHC_BY_DTYPE(dtype, E, { MHC_BY_TEAM(plan, { e = norm_launch<E, N, W, L, K>(a, plan, s); }) });
+  return ops_cuda(e, "block_norm launch");
 }
 
 size_t mhc_block_norm_grad_workspace_bytes(int64_t T, int H) {
   if (T <= 0 || H <= 0) return 0;
-  return (size_t)mhc::grad_parts(T) * 3 * H * sizeof(float) + 3 * (size_t)H * 4 * sizeof(float);
+  size_t most = 0;  // the plan differs by the type's size
+  for (size_t b = 2; b <= 4; b += 2) {
+    const mhc::TeamPlan p = mhc::grad_plan(H, b);
+    const size_t n = (size_t)mhc::grad_ctas(T, p) * p.teams * 3 * H * sizeof(float);
+    if (n > most) most = n;
+  }
+  return most;
 }
 
 int mhc_block_norm_grad(const void* dr_out, const void* dnorm, const void* y, const void* r_out, const void* gamma_post,
@@ -429,17 +605,13 @@ int mhc_block_norm_grad(const void* dr_out, const void* dnorm, const void* y, co
   }
   const BlockNormGradArgs a = {dr_out, dnorm, y, r_out, gamma_post, gate, gamma_pre, rstd_post, rstd_pre, gate_mode,
                                res_scale, T, H, dy, dr, dgamma_post, dgate, dgamma_pre, static_cast<float*>(workspace)};
-  const TeamPlan plan = team_plan(H);
-  int parts = grad_parts(T);
-  unsigned grid = (unsigned)parts;
-  if (plan.warp) {
-    grid = (unsigned)((parts + 3) / 4);
-    parts = (int)grid * 4;
-  }
-  MHC_BY_DTYPE(dtype, E, { MHC_BY_TEAM(plan, { block_norm_grad_kernel<E, N, W><<<grid, plan.threads, 0, s>>>(a); }) });
-  cudaError_t e = cudaGetLastError();
+  const TeamPlan plan = grad_plan(H, b);
+  const int64_t grid = grad_ctas(T, plan);
+  const int parts = (int)grid * plan.teams;
+  cudaError_t e = cudaSuccess;
+  MHC_BY_DTYPE(dtype, E, { MHC_BY_TEAM(plan, { e = grad_launch<E, N, W, L, K>(a, plan, grid, s); }) });
   if (e == cudaSuccess && (dgamma_post || dgamma_pre || channel))
-    e = launch_pdl(block_norm_fold_kernel, dim3((H + 31) / 32, 3), dim3(256), 0, s, a.parts, parts, H, dgamma_post,
+    e = launch_pdl(block_norm_fold_kernel, dim3((H + 31) / 32, 3), dim3(1024), 0, s, a.parts, parts, H, dgamma_post,
                    channel ? dgate : nullptr, dgamma_pre);
   return ops_cuda(e, "block_norm_grad launch");
 }

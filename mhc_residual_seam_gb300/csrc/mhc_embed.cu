@@ -17,11 +17,11 @@ __global__ void __launch_bounds__(256) embed_kernel(const Id* __restrict__ ids, 
     const int64_t t = i / segs;
     const int64_t c = (i - t * segs) * 8;
     const uint64_t row = (uint64_t)(int64_t)ids[t] - (uint64_t)first;  // ids below `first` wrap to above V
-    Vec8 x = {};
+    Vec8 x = zero8();
     if (row < (uint64_t)V) {
       x = unpack(ld8(table + (int64_t)row * ld + c));
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x.v[e] *= scale;
+      for (int e = 0; e < 4; ++e) x.p[e] = __fmul2_rn(x.p[e], splat(scale));
     }
     const Raw8<T> r = pack<T>(x);
     T* o = out + t * streams * (int64_t)segs * 8 + c;

@@ -191,7 +191,7 @@ __device__ __forceinline__ void add_token(const SumArgs& a, int i, int64_t c, Ve
   for (int s = 0; s < a.streams; ++s, p += a.H) {
     const Vec8 x = unpack(ld8_stream(p));
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc.v[e] += x.v[e];
+    for (int e = 0; e < 4; ++e) acc.p[e] = __fadd2_rn(acc.p[e], x.p[e]);
   }
 }
 
@@ -199,11 +199,11 @@ template <typename O>
 __device__ __forceinline__ void end_row(const SumArgs& a, int64_t row, int64_t c, Vec8 acc) {
   O* o = static_cast<O*>(a.dtable) + row * a.ld + c;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) acc.v[e] *= a.scale;
+  for (int e = 0; e < 4; ++e) acc.p[e] = __fmul2_rn(acc.p[e], splat(a.scale));
   if (a.accumulate) {
     const Vec8 old = unpack(ld8(o));
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc.v[e] += old.v[e];
+    for (int e = 0; e < 4; ++e) acc.p[e] = __fadd2_rn(acc.p[e], old.p[e]);
   }
   st8_stream(o, pack<O>(acc));
 }
@@ -231,13 +231,13 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const SumArgs a)
     ++row;
   }
   for (; row < b.b1; ++row) {
-    Vec8 acc = {};
+    Vec8 acc = zero8();
     const int i0 = i;
     for (; i < b.a1 && (int)a.key[i] == row; ++i) add_token<T>(a, i, c, acc);
     if (i > i0 || !a.accumulate) end_row<O>(a, row, c, acc);
   }
   if (i < b.a1) {  // tokens of a row that ends in a later chunk
-    Vec8 acc = {};
+    Vec8 acc = zero8();
     for (; i < b.a1; ++i) add_token<T>(a, i, c, acc);
     st8(a.carry + (int64_t)chunk * a.H + c, pack<float>(acc));
   }
@@ -259,13 +259,13 @@ __global__ void __launch_bounds__(kSumThreads) embed_join_kernel(const SumArgs a
     if (p.b0 < row || p.a0 == 0 || (int)a.key[p.a0 - 1] != row) break;
     --from;
   }
-  Vec8 acc = {};
+  Vec8 acc = zero8();
   for (int k = from; k < chunk; ++k) {
     const Bounds p = a.bounds[k];
     if (p.a1 == p.a0) continue;  // no token in it
     const Vec8 x = unpack(ld8(a.carry + (int64_t)k * a.H + c));
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc.v[e] += x.v[e];
+    for (int e = 0; e < 4; ++e) acc.p[e] = __fadd2_rn(acc.p[e], x.p[e]);
   }
   for (int i = b.a0; i < b.a1 && (int)a.key[i] == row; ++i) add_token<T>(a, i, c, acc);
   end_row<O>(a, row, c, acc);

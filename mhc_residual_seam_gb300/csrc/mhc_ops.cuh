@@ -19,8 +19,16 @@ void set_last_error(const std::string& msg);  // mhc_api.cu: the text mhc_last_e
 // access for the 16-bit types, two for fp32.  Sums and products are fp32;
 // store8 rounds once, to nearest even.
 struct Vec8 {
-  float v[8];
+  float2 p[4];
 };
+
+__device__ __forceinline__ float2 splat(float x) { return make_float2(x, x); }
+__device__ __forceinline__ Vec8 zero8() {
+  Vec8 o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o.p[i] = make_float2(0.f, 0.f);
+  return o;
+}
 
 template <typename T>
 struct Raw8 {  // eight columns as they lie in memory
@@ -39,18 +47,16 @@ template <typename T>
 __device__ __forceinline__ Vec8 unpack(const Raw8<T>& r) {
   Vec8 o;
   if constexpr (sizeof(T) == 4) {
-    o.v[0] = __uint_as_float(r.q[0].x); o.v[1] = __uint_as_float(r.q[0].y);
-    o.v[2] = __uint_as_float(r.q[0].z); o.v[3] = __uint_as_float(r.q[0].w);
-    o.v[4] = __uint_as_float(r.q[1].x); o.v[5] = __uint_as_float(r.q[1].y);
-    o.v[6] = __uint_as_float(r.q[1].z); o.v[7] = __uint_as_float(r.q[1].w);
-  } else {
-    const uint32_t w[4] = {r.q[0].x, r.q[0].y, r.q[0].z, r.q[0].w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 p = pair_of(w[i], T());
-      o.v[2 * i] = p.x;
-      o.v[2 * i + 1] = p.y;
+    for (int i = 0; i < 2; ++i) {
+      o.p[2 * i] = make_float2(__uint_as_float(r.q[i].x), __uint_as_float(r.q[i].y));
+      o.p[2 * i + 1] = make_float2(__uint_as_float(r.q[i].z), __uint_as_float(r.q[i].w));
     }
+  } else {
+    o.p[0] = pair_of(r.q[0].x, T());
+    o.p[1] = pair_of(r.q[0].y, T());
+    o.p[2] = pair_of(r.q[0].z, T());
+    o.p[3] = pair_of(r.q[0].w, T());
   }
   return o;
 }
@@ -59,11 +65,13 @@ template <typename T>
 __device__ __forceinline__ Raw8<T> pack(const Vec8& x) {
   Raw8<T> r;
   if constexpr (sizeof(T) == 4) {
-    r.q[0] = make_uint4(__float_as_uint(x.v[0]), __float_as_uint(x.v[1]), __float_as_uint(x.v[2]), __float_as_uint(x.v[3]));
-    r.q[1] = make_uint4(__float_as_uint(x.v[4]), __float_as_uint(x.v[5]), __float_as_uint(x.v[6]), __float_as_uint(x.v[7]));
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      r.q[i] = make_uint4(__float_as_uint(x.p[2 * i].x), __float_as_uint(x.p[2 * i].y), __float_as_uint(x.p[2 * i + 1].x),
+                          __float_as_uint(x.p[2 * i + 1].y));
   } else {
-    r.q[0] = make_uint4(word_of(x.v[0], x.v[1], T()), word_of(x.v[2], x.v[3], T()), word_of(x.v[4], x.v[5], T()),
-                        word_of(x.v[6], x.v[7], T()));
+    r.q[0] = make_uint4(word_of(x.p[0].x, x.p[0].y, T()), word_of(x.p[1].x, x.p[1].y, T()),
+                        word_of(x.p[2].x, x.p[2].y, T()), word_of(x.p[3].x, x.p[3].y, T()));
   }
   return r;
 }
@@ -91,6 +99,34 @@ template <typename T>
 __device__ __forceinline__ void st8_stream(T* p, const Raw8<T>& r) {
 #pragma unroll
   for (int i = 0; i < (int)sizeof(T) / 2; ++i) __stcs(reinterpret_cast<uint4*>(p) + i, r.q[i]);
+}
+
+// ------------------------------------------------ rows fetched ahead of use --
+// A thread copies the eight columns it will work on into shared memory of its
+// own (cp.async), some rows ahead: nobody else reads them, so its own
+// wait_group is the only synchronisation.  A row of one matrix takes
+// `segs` * 8 elements; the 16-byte halves of fp32 columns lie in two planes, so a
+// warp's accesses are free of bank conflicts.
+__device__ __forceinline__ void cp_async16(void* smem, const void* gmem) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(gmem)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+template <typename T>
+__device__ __forceinline__ void fetch8(uint4* row, int segs, int g, const T* src) {
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) cp_async16(row + i * segs + g, reinterpret_cast<const uint4*>(src) + i);
+}
+template <typename T>
+__device__ __forceinline__ Raw8<T> fetched8(const uint4* row, int segs, int g) {
+  Raw8<T> r;
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.q[i] = row[i * segs + g];
+  return r;
 }
 
 // ------------------------------------------------------------------ sums --
@@ -156,6 +192,25 @@ inline cudaError_t sm_count(int* out) {
   }
   *out = known[dev];
   return cudaSuccess;
+}
+
+// Allows a kernel `bytes` of dynamic shared memory, once per kernel and device.
+// (An attribute of the function, no stream work: also legal during capture.)
+struct SmemGrant {
+  std::mutex mu;
+  size_t have[64] = {};
+};
+inline cudaError_t allow_smem(SmemGrant& grant, const void* kernel, size_t bytes) {
+  if (bytes <= 40 * 1024) return cudaSuccess;  // with the static part, within the default of 48 KB
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lk(grant.mu);
+  if (grant.have[dev] >= bytes) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) grant.have[dev] = bytes;
+  return e;
 }
 
 // Launch that may begin while the kernel before it on the stream ends; the
