@@ -29,9 +29,10 @@ struct BlockNormGradArgs {
   float* parts;  // [gridDim.x][3][H] column sums of each CTA: gamma_post, gate, gamma_pre
 };
 
-// A team of threads works on one row: a warp (rows of at most 256 columns,
+// A team of threads works on one row: a warp (rows of at most 512 columns,
 // several teams per CTA) or the whole CTA.  A thread keeps the same VPT groups of
-// eight columns for all of its team's rows.
+// eight columns for all of its team's rows: two groups, so that what a row costs
+// beside its columns (the sums over the team, addresses) is shared by 16 columns.
 template <bool WARP>
 struct Team {
   int lanes, lane, teams, team;
@@ -44,25 +45,27 @@ struct Team {
 };
 
 // The sum over a team; `buf` is the caller's own slot of shared memory for this
-// sum (the slots of warps that the CTA lacks hold zero), so one barrier per sum is
-// enough.  The warps' sums are added in the same order everywhere.
-template <bool WARP>
+// sum (QUADS * 4 warps at most; the places of warps that the CTA lacks hold zero),
+// so one barrier per sum is enough.  The warps' sums are added in the same order
+// everywhere.
+template <bool WARP, int QUADS>
 __device__ __forceinline__ float team_sum(float2 v, float4* buf) {
   float x = warp_sum(v.x + v.y);
   if constexpr (!WARP) {
-    const int w = threadIdx.x >> 5, quads = (blockDim.x + 127) >> 7;
-    if ((threadIdx.x & 31) == 0) reinterpret_cast<float*>(buf)[w] = x;
+    if ((threadIdx.x & 31) == 0) reinterpret_cast<float*>(buf)[threadIdx.x >> 5] = x;
     __syncthreads();
-    x = 0.f;
-    for (int i = 0; i < quads; ++i) {
-      const float4 s = buf[i];
-      x += (s.x + s.y) + (s.z + s.w);
+    float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < QUADS; ++i) {
+      const float4 q = buf[i];
+      s = __fadd2_rn(s, __fadd2_rn(make_float2(q.x, q.y), make_float2(q.z, q.w)));
     }
+    x = s.x + s.y;
   }
   return x;
 }
 
-// A row's weights of one thread: gamma_post * gate (channel) and gamma_pre.
+// Eight weights of a row; ones where there is no weight.
 template <typename T>
 __device__ __forceinline__ Vec8 weight8(const void* w, int g) {
   if (w) return unpack(ld8(static_cast<const T*>(w) + g * 8));
@@ -78,10 +81,25 @@ __device__ __forceinline__ Vec8 mul8(const Vec8& a, const Vec8& b) {
   return o;
 }
 
-// Threads of a CTA at most: 640 leaves a thread the registers for the weights and
-// column sums of its columns (and the forward pass a second CTA per SM), 1024 is
-// for rows of more than 5120 columns.
+// A CTA of at most kTeamThreads has 96 registers a thread, one of kBigThreads 64.
 constexpr int kTeamThreads = 640, kBigThreads = 1024;
+
+// Dynamic shared memory of a CTA: per team, the product of gamma_post and a
+// channel gate as fp32 (each thread its own columns), then the fetched rows, then
+// per warp and stage four words for the row's scalars.
+struct TeamSmem {
+  uint4 *weight, *ring;
+  float* scalars;
+};
+template <typename T, int STAGES>
+__device__ __forceinline__ TeamSmem team_smem(uint4* base, int segs, int teams, int team, int matrices) {
+  const int unit = segs * (int)(sizeof(T) / 2);  // 16-byte pieces of a row
+  TeamSmem m;
+  m.weight = base + team * segs * 2;
+  m.ring = base + teams * segs * 2 + team * STAGES * matrices * unit;
+  m.scalars = reinterpret_cast<float*>(base + teams * (segs * 2 + STAGES * matrices * unit)) + (threadIdx.x >> 5) * STAGES * 4;
+  return m;
+}
 
 // p = y rho1 gamma_post;  r' = scale r + gate p;  norm = r' rho2 gamma_pre.
 // Bound by HBM: y and r are read once, r' and the norm written once; the row
@@ -89,48 +107,53 @@ constexpr int kTeamThreads = 640, kBigThreads = 1024;
 // the fp32 r', so it carries one rounding only.  Each thread fetches its columns
 // STAGES rows ahead (0: no shared memory for that, plain loads), so loads stay in
 // flight across the two barriers of a row.  Arithmetic is two columns per
-// instruction; gamma_post and a channel gate are one fp32 factor.
-template <typename T, int VPT, bool WARP, bool BIG, int STAGES>
-__global__ void __launch_bounds__(BIG ? kBigThreads : kTeamThreads, BIG ? 1 : 2) block_norm_kernel(const BlockNormArgs a) {
+// instruction.  rsqrtf (2 ulp) replaces a square root and a division that every
+// thread would repeat.
+template <typename T, int VPT, bool WARP, int STAGES>
+__global__ void __launch_bounds__(kBigThreads) block_norm_kernel(const BlockNormArgs a) {
   __shared__ float4 buf[2][2][8];
-  extern __shared__ uint4 ring[];
+  extern __shared__ uint4 dyn[];
   const Team<WARP> q;
   const int segs = a.H >> 3;
   const float inv = 1.0f / (float)a.H;
   const T* y = static_cast<const T*>(a.y);
   const T* r = static_cast<const T*>(a.r);
+  const float* gates = a.gate_mode == MHC_GATE_TOKEN ? static_cast<const float*>(a.gate) : nullptr;
   const int64_t step = (int64_t)gridDim.x * q.teams;
-  const int unit = segs * (int)(sizeof(T) / 2);  // 16-byte pieces of a row
-  uint4* mine = ring + q.team * STAGES * 2 * unit;
+  const int unit = segs * (int)(sizeof(T) / 2);
+  const TeamSmem m = team_smem<T, STAGES>(dyn, segs, q.teams, q.team, 2);
   auto fetch = [&](int64_t t, int stage) {
     if (t < a.T) {
-      uint4* s = mine + stage * 2 * unit;
+      uint4* s = m.ring + stage * 2 * unit;
+      const T* pr = r + t * a.ld_r;
+      const T* py = y + t * a.ld_y;
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
         const int g = q.lane + i * q.lanes;
         if (g < segs) {
-          fetch8<T>(s, segs, g, r + t * a.ld_r + g * 8);
-          if (y) fetch8<T>(s + unit, segs, g, y + t * a.ld_y + g * 8);
+          fetch8<T>(s, segs, g, pr + g * 8);
+          if (y) fetch8<T>(s + unit, segs, g, py + g * 8);
         }
       }
+      if (gates && (threadIdx.x & 31) == 0) cp_async4(m.scalars + stage * 4, gates + t);
     }
     cp_async_commit();
   };
   int64_t t = (int64_t)blockIdx.x * q.teams + q.team;
 #pragma unroll
   for (int s = 0; s < STAGES; ++s) fetch(t + s * step, s);
-  Vec8 wc[VPT];
   Raw8<T> wn[VPT];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int g = q.lane + i * q.lanes;
     if (g < segs) {
-      wc[i] = mul8(weight8<T>(a.gamma_post, g), weight8<T>(a.gate_mode == MHC_GATE_CHANNEL ? a.gate : nullptr, g));
+      const Raw8<float> w = pack<float>(
+          mul8(weight8<T>(a.gamma_post, g), weight8<T>(a.gate_mode == MHC_GATE_CHANNEL ? a.gate : nullptr, g)));
+      m.weight[g] = w.q[0];
+      m.weight[segs + g] = w.q[1];
       if (a.gamma_pre) wn[i] = ld8(static_cast<const T*>(a.gamma_pre) + g * 8);
     }
   }
-  const float* gates = a.gate_mode == MHC_GATE_TOKEN ? static_cast<const float*>(a.gate) : nullptr;
-  float gate = gates && t < a.T ? gates[t] : 1.f;
   if constexpr (!WARP) {
     if (threadIdx.x < 32) buf[threadIdx.x >> 4][(threadIdx.x >> 3) & 1][threadIdx.x & 7] = make_float4(0.f, 0.f, 0.f, 0.f);
     __syncthreads();
@@ -139,7 +162,13 @@ __global__ void __launch_bounds__(BIG ? kBigThreads : kTeamThreads, BIG ? 1 : 2)
   for (; t < a.T; t += step, flip ^= 1) {
     Vec8 p[VPT], x[VPT];
     if constexpr (STAGES > 0) cp_async_wait<(STAGES > 0 ? STAGES - 1 : 0)>();
-    const uint4* s = mine + stage * 2 * unit;
+    const uint4* s = m.ring + stage * 2 * unit;
+    float gt = 1.f;
+    if (gates) {
+      __syncwarp();
+      gt = STAGES ? m.scalars[stage * 4] : gates[t];
+      __syncwarp();
+    }
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int g = q.lane + i * q.lanes;
@@ -153,8 +182,6 @@ __global__ void __launch_bounds__(BIG ? kBigThreads : kTeamThreads, BIG ? 1 : 2)
       fetch(t + STAGES * step, stage);
       stage = stage + 1 == STAGES ? 0 : stage + 1;
     }
-    const float gt = gate;
-    if (gates && t + step < a.T) gate = gates[t + step];
     if (y) {
       float k = gt;
       if (a.gamma_post) {
@@ -163,18 +190,20 @@ __global__ void __launch_bounds__(BIG ? kBigThreads : kTeamThreads, BIG ? 1 : 2)
         for (int i = 0; i < VPT; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e) ss = __ffma2_rn(p[i].p[e], p[i].p[e], ss);
-        const float rho = 1.0f / sqrtf(fmaf(team_sum<WARP>(ss, buf[flip][0]), inv, a.eps));
+        const float rho = rsqrtf(fmaf(team_sum<WARP, 8>(ss, buf[flip][0]), inv, a.eps));
         if (q.lane == 0) a.rstd_post[t] = rho;
         k *= rho;
       }
+      T* o = static_cast<T*>(a.r_out) + t * a.ld_ro;
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
         const int g = q.lane + i * q.lanes;
         if (g < segs) {
+          const Vec8 wc = unpack(fetched8<float>(m.weight, segs, g));
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            x[i].p[e] = __ffma2_rn(__fmul2_rn(p[i].p[e], splat(k)), wc[i].p[e], __fmul2_rn(x[i].p[e], splat(a.scale)));
-          st8_stream(static_cast<T*>(a.r_out) + t * a.ld_ro + g * 8, pack<T>(x[i]));
+            x[i].p[e] = __ffma2_rn(__fmul2_rn(p[i].p[e], splat(k)), wc.p[e], __fmul2_rn(x[i].p[e], splat(a.scale)));
+          st8_stream(o + g * 8, pack<T>(x[i]));
         }
       }
     }
@@ -184,8 +213,9 @@ __global__ void __launch_bounds__(BIG ? kBigThreads : kTeamThreads, BIG ? 1 : 2)
       for (int i = 0; i < VPT; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) ss = __ffma2_rn(x[i].p[e], x[i].p[e], ss);
-      const float rho = 1.0f / sqrtf(fmaf(team_sum<WARP>(ss, buf[flip][1]), inv, a.eps));
+      const float rho = rsqrtf(fmaf(team_sum<WARP, 8>(ss, buf[flip][1]), inv, a.eps));
       if (q.lane == 0) a.rstd_pre[t] = rho;
+      T* o = static_cast<T*>(a.norm) + t * a.ld_n;
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
         const int g = q.lane + i * q.lanes;
@@ -194,7 +224,7 @@ __global__ void __launch_bounds__(BIG ? kBigThreads : kTeamThreads, BIG ? 1 : 2)
           Vec8 n;
 #pragma unroll
           for (int e = 0; e < 4; ++e) n.p[e] = __fmul2_rn(__fmul2_rn(x[i].p[e], splat(rho)), w.p[e]);
-          st8_stream(static_cast<T*>(a.norm) + t * a.ld_n + g * 8, pack<T>(n));
+          st8_stream(o + g * 8, pack<T>(n));
         }
       }
     }
@@ -211,74 +241,85 @@ __global__ void __launch_bounds__(BIG ? kBigThreads : kTeamThreads, BIG ? 1 : 2)
 // (S is one column sum for both; without gamma_post, rho1 = 1 and dy has no second
 // term.)  Bound by HBM: four rows read, two written.  A thread keeps the same
 // columns over all of its team's rows, so the column sums stay in registers until
-// the end; a second kernel adds the CTAs' sums in a fixed order.  Rows are
-// fetched ahead as in the forward kernel.
+// the end; a second kernel adds the CTAs' sums in a fixed order.  Rows and
+// their scalars are fetched ahead as in the forward kernel.
 template <typename T, int VPT, bool WARP, bool BIG, int STAGES>
 __global__ void __launch_bounds__(BIG ? kBigThreads : kTeamThreads) block_norm_grad_kernel(const BlockNormGradArgs a) {
+  constexpr int QUADS = BIG ? 8 : kTeamThreads / 128;
   __shared__ float4 buf[2][2][8];
-  extern __shared__ uint4 ring[];
+  extern __shared__ uint4 dyn[];
   const Team<WARP> q;
   const int segs = a.H >> 3;
   const float inv = 1.0f / (float)a.H;
   const int unit = segs * (int)(sizeof(T) / 2);
-  uint4* mine = ring + q.team * STAGES * 4 * unit;
-  const T* src[4] = {static_cast<const T*>(a.r_out), static_cast<const T*>(a.dnorm), static_cast<const T*>(a.dr_out),
-                     static_cast<const T*>(a.y)};
+  const TeamSmem sm = team_smem<T, STAGES>(dyn, segs, q.teams, q.team, 4);
+  const T* const r_out = static_cast<const T*>(a.r_out);
+  const T* const dnorm = static_cast<const T*>(a.dnorm);
+  const T* const dr_out = static_cast<const T*>(a.dr_out);
+  const T* const y = static_cast<const T*>(a.y);
+  const float* gates = a.gate_mode == MHC_GATE_TOKEN ? static_cast<const float*>(a.gate) : nullptr;
   auto fetch = [&](int64_t t, int stage) {
     if (t < a.T) {
-      uint4* s = mine + stage * 4 * unit;
+      uint4* s = sm.ring + stage * 4 * unit;
+      const int64_t row = t * a.H;
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
         const int g = q.lane + i * q.lanes;
-        const int64_t at = t * a.H + g * 8;
+        const int64_t at = row + g * 8;
         if (g < segs) {
-#pragma unroll
-          for (int m = 0; m < 4; ++m)
-            if (src[m]) fetch8<T>(s + m * unit, segs, g, src[m] + at);
+          if (a.gamma_pre) {
+            fetch8<T>(s, segs, g, r_out + at);
+            fetch8<T>(s + unit, segs, g, dnorm + at);
+          }
+          if (dr_out) fetch8<T>(s + 2 * unit, segs, g, dr_out + at);
+          if (y) fetch8<T>(s + 3 * unit, segs, g, y + at);
         }
+      }
+      if ((threadIdx.x & 31) == 0) {
+        if (a.gamma_pre) cp_async4(sm.scalars + stage * 4, a.rstd_pre + t);
+        if (a.gamma_post) cp_async4(sm.scalars + stage * 4 + 1, a.rstd_post + t);
+        if (gates) cp_async4(sm.scalars + stage * 4 + 2, gates + t);
       }
     }
     cp_async_commit();
   };
-  Vec8 s_post[VPT], s_pre[VPT], wc[VPT];
-  Raw8<T> wn[VPT];
-  int flip = 0, stage = 0;
   const int64_t step = (int64_t)gridDim.x * q.teams;
   int64_t t = (int64_t)blockIdx.x * q.teams + q.team;
 #pragma unroll
   for (int s = 0; s < STAGES; ++s) fetch(t + s * step, s);
+  Vec8 s_post[VPT], s_pre[VPT];
+  Raw8<T> wn[VPT];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int g = q.lane + i * q.lanes;
     s_post[i] = s_pre[i] = zero8();
     if (g < segs) {
-      wc[i] = mul8(weight8<T>(a.gamma_post, g), weight8<T>(a.gate_mode == MHC_GATE_CHANNEL ? a.gate : nullptr, g));
+      const Raw8<float> w = pack<float>(
+          mul8(weight8<T>(a.gamma_post, g), weight8<T>(a.gate_mode == MHC_GATE_CHANNEL ? a.gate : nullptr, g)));
+      sm.weight[g] = w.q[0];
+      sm.weight[segs + g] = w.q[1];
       if (a.gamma_pre) wn[i] = ld8(static_cast<const T*>(a.gamma_pre) + g * 8);
     }
   }
-  const float* gates = a.gate_mode == MHC_GATE_TOKEN ? static_cast<const float*>(a.gate) : nullptr;
-  float n_pre = 1.f, n_post = 1.f, n_gate = 1.f;  // the next row's factors
-  auto factors = [&](int64_t r) {
-    if (r < a.T) {
-      if (a.gamma_pre) n_pre = a.rstd_pre[r];
-      if (a.gamma_post) n_post = a.rstd_post[r];
-      if (gates) n_gate = gates[r];
-    }
-  };
-  factors(t);
   if constexpr (!WARP) {
     if (threadIdx.x < 32) buf[threadIdx.x >> 4][(threadIdx.x >> 3) & 1][threadIdx.x & 7] = make_float4(0.f, 0.f, 0.f, 0.f);
     __syncthreads();
   }
+  int flip = 0, stage = 0;
   for (; t < a.T; t += step, flip ^= 1) {
     Vec8 G[VPT], x[VPT];
     const int64_t row = t * a.H;
-    const float rho2 = n_pre, rho1 = n_post, gt = n_gate;
-    factors(t + step);
-    if constexpr (STAGES > 0) cp_async_wait<(STAGES > 0 ? STAGES - 1 : 0)>();
-    const uint4* s = mine + stage * 4 * unit;
-    auto take = [&](int m, int g) {
-      return unpack(STAGES ? fetched8<T>(s + m * unit, segs, g) : ld8_stream(src[m] + row + g * 8));
+    if constexpr (STAGES > 0) {
+      cp_async_wait<(STAGES > 0 ? STAGES - 1 : 0)>();
+      __syncwarp();
+    }
+    float rho2 = 1.f, rho1 = 1.f, gt = 1.f;
+    if (a.gamma_pre) rho2 = STAGES ? sm.scalars[stage * 4] : a.rstd_pre[t];
+    if (a.gamma_post) rho1 = STAGES ? sm.scalars[stage * 4 + 1] : a.rstd_post[t];
+    if (gates) gt = STAGES ? sm.scalars[stage * 4 + 2] : gates[t];
+    const uint4* s = sm.ring + stage * 4 * unit;
+    auto take = [&](int m, const T* src, int g) {
+      return unpack(STAGES ? fetched8<T>(s + m * unit, segs, g) : ld8_stream(src + row + g * 8));
     };
     if (a.gamma_pre) {
       float2 m2 = make_float2(0.f, 0.f);
@@ -287,8 +328,8 @@ __global__ void __launch_bounds__(BIG ? kBigThreads : kTeamThreads) block_norm_g
         const int g = q.lane + i * q.lanes;
         G[i] = x[i] = zero8();
         if (g < segs) {
-          x[i] = take(0, g);
-          const Vec8 dn = take(1, g), w = unpack(wn[i]);
+          x[i] = take(0, r_out, g);
+          const Vec8 dn = take(1, dnorm, g), w = unpack(wn[i]);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float2 dx = __fmul2_rn(dn.p[e], x[i].p[e]);
@@ -298,11 +339,11 @@ __global__ void __launch_bounds__(BIG ? kBigThreads : kTeamThreads) block_norm_g
           }
         }
       }
-      const float k = -rho2 * rho2 * (team_sum<WARP>(m2, buf[flip][0]) * inv) * rho2;
+      const float k = -rho2 * rho2 * (team_sum<WARP, QUADS>(m2, buf[flip][0]) * inv) * rho2;
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
         const int g = q.lane + i * q.lanes;
-        const Vec8 d = a.dr_out && g < segs ? take(2, g) : zero8();
+        const Vec8 d = dr_out && g < segs ? take(2, dr_out, g) : zero8();
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           G[i].p[e] = __ffma2_rn(x[i].p[e], splat(k), __ffma2_rn(G[i].p[e], splat(rho2), d.p[e]));
@@ -311,9 +352,10 @@ __global__ void __launch_bounds__(BIG ? kBigThreads : kTeamThreads) block_norm_g
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
         const int g = q.lane + i * q.lanes;
-        G[i] = g < segs ? take(2, g) : zero8();
+        G[i] = g < segs ? take(2, dr_out, g) : zero8();
       }
     }
+    T* dr = static_cast<T*>(a.dr) + row;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int g = q.lane + i * q.lanes;
@@ -321,34 +363,42 @@ __global__ void __launch_bounds__(BIG ? kBigThreads : kTeamThreads) block_norm_g
         Vec8 o;
 #pragma unroll
         for (int e = 0; e < 4; ++e) o.p[e] = __fmul2_rn(G[i].p[e], splat(a.scale));
-        st8_stream(static_cast<T*>(a.dr) + row + g * 8, pack<T>(o));
+        st8_stream(dr + g * 8, pack<T>(o));
       }
     }
-    if (a.y) {
-      float2 n2 = make_float2(0.f, 0.f);
+    float2 n2 = make_float2(0.f, 0.f);
+    if (y) {
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
         const int g = q.lane + i * q.lanes;
         x[i] = zero8();
         if (g < segs) {
-          x[i] = take(3, g);
+          x[i] = take(3, y, g);
+          const Vec8 wc = unpack(fetched8<float>(sm.weight, segs, g));
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float2 gr = __fmul2_rn(G[i].p[e], splat(rho1));
             s_post[i].p[e] = __ffma2_rn(__fmul2_rn(gr, splat(gt)), x[i].p[e], s_post[i].p[e]);
-            G[i].p[e] = __fmul2_rn(wc[i].p[e], gr);
+            G[i].p[e] = __fmul2_rn(wc.p[e], gr);
             n2 = __ffma2_rn(G[i].p[e], x[i].p[e], n2);
           }
         }
       }
-      // the row's columns are in registers: its stage takes the row STAGES further on
-      if constexpr (STAGES > 0) fetch(t + STAGES * step, stage);
+    }
+    // the row is in registers: its stage takes the row STAGES further on
+    if constexpr (STAGES > 0) {
+      __syncwarp();
+      fetch(t + STAGES * step, stage);
+      stage = stage + 1 == STAGES ? 0 : stage + 1;
+    }
+    if (y) {
       float k = 0.f;
       if (a.gamma_post || gates) {
-        const float N = team_sum<WARP>(n2, buf[flip][1]);
+        const float N = team_sum<WARP, QUADS>(n2, buf[flip][1]);
         if (gates && q.lane == 0) a.dgate[t] = N;
         if (a.gamma_post) k = -rho1 * (N * inv) * rho1 * gt;
       }
+      T* dy = static_cast<T*>(a.dy) + row;
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
         const int g = q.lane + i * q.lanes;
@@ -359,13 +409,10 @@ __global__ void __launch_bounds__(BIG ? kBigThreads : kTeamThreads) block_norm_g
             o.p[e] = __fmul2_rn(G[i].p[e], splat(gt));
             if (a.gamma_post) o.p[e] = __ffma2_rn(x[i].p[e], splat(k), o.p[e]);
           }
-          st8_stream(static_cast<T*>(a.dy) + row + g * 8, pack<T>(o));
+          st8_stream(dy + g * 8, pack<T>(o));
         }
       }
-    } else {
-      if constexpr (STAGES > 0) fetch(t + STAGES * step, stage);
     }
-    if constexpr (STAGES > 0) stage = stage + 1 == STAGES ? 0 : stage + 1;
   }
   if constexpr (STAGES > 0) cp_async_wait<0>();
   float* out = a.parts + ((int64_t)blockIdx.x * q.teams + q.team) * 3 * a.H;
@@ -416,29 +463,33 @@ struct TeamPlan {
 };
 
 constexpr int kSMs = 152;
-constexpr size_t kRingBytes = 216 * 1024;  // shared memory of an SM for rows in flight
+constexpr size_t kSmem = 227 * 1024;         // shared memory of an SM
+constexpr size_t kCtaSmem = 1024 + 512 + 128;  // what a CTA takes of it beside the dynamic part
 
+// `sm_threads`: threads of an SM that the kernel's registers allow for.
 static TeamPlan team_plan(int H, size_t type_bytes, int matrices, int sm_threads) {
   const int segs = H / 8;
   TeamPlan p;
-  p.warp = segs <= 32;
-  p.vpt = segs <= kBigThreads ? 1 : 2;
-  p.big = segs > kTeamThreads;
-  p.threads = p.warp ? 128 : ((segs + p.vpt - 1) / p.vpt + 31) / 32 * 32;
+  p.warp = segs <= 64;
+  p.vpt = segs <= 32 ? 1 : 2;
+  p.threads = p.warp ? 128 : ((segs + 1) / 2 + 31) / 32 * 32;
+  p.big = p.threads > kTeamThreads;
   p.teams = p.warp ? 4 : 1;
-  const size_t row = (size_t)H * type_bytes * matrices * p.teams;
+  const size_t row = (size_t)H * type_bytes * matrices * p.teams, weights = (size_t)H * 4 * p.teams;
   p.ctas = sm_threads / p.threads;
   if (p.ctas < 1) p.ctas = 1;
   if (p.ctas > 16) p.ctas = 16;
-  while (p.ctas > 1 && row * p.ctas * 2 > kRingBytes) --p.ctas;
-  const size_t fit = kRingBytes / (row * p.ctas);
+  const size_t stage = row + (size_t)(p.threads / 32) * 16;  // with the rows' scalars
+  while (p.ctas > 1 && (stage * 2 + weights + kCtaSmem) * p.ctas > kSmem) --p.ctas;
+  const size_t have = kSmem / p.ctas, fixed = weights + kCtaSmem;
+  const size_t fit = have > fixed ? (have - fixed) / stage : 0;
   p.stages = fit >= 4 ? 4 : fit >= 2 ? 2 : (int)fit;
-  p.smem = row * p.stages;
+  p.smem = weights + stage * p.stages;
   return p;
 }
 
-static TeamPlan norm_plan(int H, size_t b) { return team_plan(H, b, 2, 2 * kTeamThreads); }
-static TeamPlan grad_plan(int H, size_t b) { return team_plan(H, b, 4, kTeamThreads); }
+static TeamPlan norm_plan(int H, size_t b) { return team_plan(H, b, 2, 1024); }
+static TeamPlan grad_plan(int H, size_t b) { return team_plan(H, b, 4, 640); }
 
 // CTAs of the gradient: all resident at once.
 static int64_t grad_ctas(int64_t T, const TeamPlan& p) {
@@ -452,19 +503,19 @@ static int64_t grad_ctas(int64_t T, const TeamPlan& p) {
   else if (plan.stages == 1) { constexpr int K = 1; MHC_BY_TEAM_(plan, __VA_ARGS__) }                 \
   else { constexpr int K = 0; MHC_BY_TEAM_(plan, __VA_ARGS__) }
 #define MHC_BY_TEAM_(plan, ...)                                                                       \
-  if (plan.warp) { constexpr bool W = true, L = false; constexpr int N = 1; __VA_ARGS__; }            \
-  else if (!plan.big) { constexpr bool W = false, L = false; constexpr int N = 1; __VA_ARGS__; }      \
-  else if (plan.vpt == 1) { constexpr bool W = false, L = true; constexpr int N = 1; __VA_ARGS__; }   \
+  if (plan.vpt == 1) { constexpr bool W = true, L = false; constexpr int N = 1; __VA_ARGS__; }        \
+  else if (plan.warp) { constexpr bool W = true, L = false; constexpr int N = 2; __VA_ARGS__; }       \
+  else if (!plan.big) { constexpr bool W = false, L = false; constexpr int N = 2; __VA_ARGS__; }      \
   else { constexpr bool W = false, L = true; constexpr int N = 2; __VA_ARGS__; }
 
-template <typename T, int N, bool W, bool L, int K>
+template <typename T, int N, bool W, int K>
 static cudaError_t norm_launch(const BlockNormArgs& a, const TeamPlan& p, cudaStream_t s) {
   static SmemGrant grant;
-  cudaError_t e = allow_smem(grant, (const void*)block_norm_kernel<T, N, W, L, K>, p.smem);
+  cudaError_t e = allow_smem(grant, (const void*)block_norm_kernel<T, N, W, K>, p.smem);
   if (e != cudaSuccess) return e;
   int64_t grid = (a.T + p.teams - 1) / p.teams;
-  if (K && grid > (int64_t)kSMs * p.ctas) grid = (int64_t)kSMs * p.ctas;
-  block_norm_kernel<T, N, W, L, K><<<(unsigned)grid, p.threads, p.smem, s>>>(a);
+  if (grid > (int64_t)kSMs * p.ctas) grid = (int64_t)kSMs * p.ctas;
+  block_norm_kernel<T, N, W, K><<<(unsigned)grid, p.threads, p.smem, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -534,7 +585,7 @@ int mhc_block_norm(const void* y, int64_t ld_y, const void* r, int64_t ld_r, con
   const TeamPlan plan = norm_plan(H, b);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
-  MHC_BY_DTYPE(dtype, E, { MHC_BY_TEAM(plan, { e = norm_launch<E, N, W, L, K>(a, plan, s); }) });
+  MHC_BY_DTYPE(dtype, E, { MHC_BY_TEAM(plan, { (void)L; e = norm_launch<E, N, W, K>(a, plan, s); }) });
   return ops_cuda(e, "block_norm launch");
 }
 
