@@ -86,20 +86,32 @@ constexpr int kTeamThreads = 640, kBigThreads = 1024;
 
 // Dynamic shared memory of a CTA: per team, the product of gamma_post and a
 // channel gate as fp32 (each thread its own columns), then the fetched rows, then
-// per warp and stage four words for the row's scalars.
-struct TeamSmem {
-  uint4 *weight, *ring;
-  float* scalars;
+// per warp and stage four words for the row's scalars.  All addresses are of
+// this thread's columns.
+template <typename T, int VPT, bool WARP, int STAGES, int MATRICES>
+struct TeamMemory {
+  uint32_t plane;    // bytes of eight 16-bit columns per group: one plane of a row
+  uint32_t matrix;   // bytes of a row of one matrix
+  uint32_t weight, ring, scalars;
+  uint32_t stage_bytes;
+  uint32_t col[VPT], smem[VPT];  // byte offsets of the thread's columns in a row, and in a plane
+  bool on[VPT];                  // whether the row has these columns
+  __device__ TeamMemory(const Team<WARP>& q, int segs, uint4* dyn) {
+    plane = segs * 16;
+    matrix = plane * (sizeof(T) / 2);
+    stage_bytes = MATRICES * matrix;
+    weight = smem_of(dyn) + q.team * plane * 2;
+    ring = smem_of(dyn) + q.teams * plane * 2 + q.team * STAGES * stage_bytes;
+    scalars = smem_of(dyn) + q.teams * (plane * 2 + STAGES * stage_bytes) + (threadIdx.x >> 5) * STAGES * 16;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int g = q.lane + i * q.lanes;
+      on[i] = g < segs;
+      col[i] = g * 8 * sizeof(T);
+      smem[i] = g * 16;
+    }
+  }
 };
-template <typename T, int STAGES>
-__device__ __forceinline__ TeamSmem team_smem(uint4* base, int segs, int teams, int team, int matrices) {
-  const int unit = segs * (int)(sizeof(T) / 2);  // 16-byte pieces of a row
-  TeamSmem m;
-  m.weight = base + team * segs * 2;
-  m.ring = base + teams * segs * 2 + team * STAGES * matrices * unit;
-  m.scalars = reinterpret_cast<float*>(base + teams * (segs * 2 + STAGES * matrices * unit)) + (threadIdx.x >> 5) * STAGES * 4;
-  return m;
-}
 
 // p = y rho1 gamma_post;  r' = scale r + gate p;  norm = r' rho2 gamma_pre.
 // Bound by HBM: y and r are read once, r' and the norm written once; the row
@@ -108,83 +120,86 @@ __device__ __forceinline__ TeamSmem team_smem(uint4* base, int segs, int teams, 
 // STAGES rows ahead (0: no shared memory for that, plain loads), so loads stay in
 // flight across the two barriers of a row.  Arithmetic is two columns per
 // instruction.  rsqrtf (2 ulp) replaces a square root and a division that every
-// thread would repeat.
-template <typename T, int VPT, bool WARP, int STAGES>
+// thread would repeat.  FULL: every part but a token gate is given and each thread
+// has all of its columns, known when compiling (no tests per row).
+template <typename T, int VPT, bool WARP, int STAGES, bool FULL>
 __global__ void __launch_bounds__(kBigThreads) block_norm_kernel(const BlockNormArgs a) {
   __shared__ float4 buf[2][2][8];
   extern __shared__ uint4 dyn[];
   const Team<WARP> q;
   const int segs = a.H >> 3;
   const float inv = 1.0f / (float)a.H;
-  const T* y = static_cast<const T*>(a.y);
-  const T* r = static_cast<const T*>(a.r);
+  const bool has_y = FULL || a.y, has_post = FULL || a.gamma_post, has_pre = FULL || a.gamma_pre;
+  const char* y = static_cast<const char*>(a.y);
+  const char* r = static_cast<const char*>(a.r);
   const float* gates = a.gate_mode == MHC_GATE_TOKEN ? static_cast<const float*>(a.gate) : nullptr;
   const int64_t step = (int64_t)gridDim.x * q.teams;
-  const int unit = segs * (int)(sizeof(T) / 2);
-  const TeamSmem m = team_smem<T, STAGES>(dyn, segs, q.teams, q.team, 2);
-  auto fetch = [&](int64_t t, int stage) {
+  const TeamMemory<T, VPT, WARP, STAGES, 2> m(q, segs, dyn);
+  auto on = [&](int i) { return FULL || m.on[i]; };
+  auto fetch = [&](int64_t t, uint32_t slot, uint32_t scalar) {
     if (t < a.T) {
-      uint4* s = m.ring + stage * 2 * unit;
-      const T* pr = r + t * a.ld_r;
-      const T* py = y + t * a.ld_y;
+      const char* pr = r + t * (a.ld_r * (int)sizeof(T));
+      const char* py = y + t * (a.ld_y * (int)sizeof(T));
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int g = q.lane + i * q.lanes;
-        if (g < segs) {
-          fetch8<T>(s, segs, g, pr + g * 8);
-          if (y) fetch8<T>(s + unit, segs, g, py + g * 8);
+      for (int i = 0; i < VPT; ++i)
+        if (on(i)) {
+          fetch8<T>(slot + m.smem[i], m.plane, pr + m.col[i]);
+          if (has_y) fetch8<T>(slot + m.matrix + m.smem[i], m.plane, py + m.col[i]);
         }
-      }
-      if (gates && (threadIdx.x & 31) == 0) cp_async4(m.scalars + stage * 4, gates + t);
+      if (gates && (threadIdx.x & 31) == 0) cp_async4(scalar, gates + t);
     }
     cp_async_commit();
   };
   int64_t t = (int64_t)blockIdx.x * q.teams + q.team;
 #pragma unroll
-  for (int s = 0; s < STAGES; ++s) fetch(t + s * step, s);
+  for (int s = 0; s < STAGES; ++s) fetch(t + s * step, m.ring + s * m.stage_bytes, m.scalars + s * 16);
   Raw8<T> wn[VPT];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int g = q.lane + i * q.lanes;
-    if (g < segs) {
+    if (on(i)) {
       const Raw8<float> w = pack<float>(
           mul8(weight8<T>(a.gamma_post, g), weight8<T>(a.gate_mode == MHC_GATE_CHANNEL ? a.gate : nullptr, g)));
-      m.weight[g] = w.q[0];
-      m.weight[segs + g] = w.q[1];
-      if (a.gamma_pre) wn[i] = ld8(static_cast<const T*>(a.gamma_pre) + g * 8);
+      sts16(m.weight + m.smem[i], w.q[0]);
+      sts16(m.weight + m.plane + m.smem[i], w.q[1]);
+      if (has_pre) wn[i] = ld8(static_cast<const T*>(a.gamma_pre) + g * 8);
     }
   }
   if constexpr (!WARP) {
     if (threadIdx.x < 32) buf[threadIdx.x >> 4][(threadIdx.x >> 3) & 1][threadIdx.x & 7] = make_float4(0.f, 0.f, 0.f, 0.f);
     __syncthreads();
   }
-  int stage = 0, flip = 0;
+  int flip = 0;
+  uint32_t slot = m.ring, scalar = m.scalars;
   for (; t < a.T; t += step, flip ^= 1) {
     Vec8 p[VPT], x[VPT];
     if constexpr (STAGES > 0) cp_async_wait<(STAGES > 0 ? STAGES - 1 : 0)>();
-    const uint4* s = m.ring + stage * 2 * unit;
     float gt = 1.f;
     if (gates) {
       __syncwarp();
-      gt = STAGES ? m.scalars[stage * 4] : gates[t];
+      gt = STAGES ? lds4(scalar) : gates[t];
       __syncwarp();
     }
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int g = q.lane + i * q.lanes;
-      p[i] = x[i] = zero8();
-      if (g < segs) {
-        x[i] = unpack(STAGES ? fetched8<T>(s, segs, g) : ld8_stream(r + t * a.ld_r + g * 8));
-        if (y) p[i] = unpack(STAGES ? fetched8<T>(s + unit, segs, g) : ld8_stream(y + t * a.ld_y + g * 8));
+      if (!FULL) p[i] = x[i] = zero8();
+      if (on(i)) {
+        const char* pr = r + t * (a.ld_r * (int)sizeof(T)) + m.col[i];
+        const char* py = y + t * (a.ld_y * (int)sizeof(T)) + m.col[i];
+        x[i] = unpack(STAGES ? fetched8<T>(slot + m.smem[i], m.plane) : ld8_stream(reinterpret_cast<const T*>(pr)));
+        if (has_y)
+          p[i] = unpack(STAGES ? fetched8<T>(slot + m.matrix + m.smem[i], m.plane) : ld8_stream(reinterpret_cast<const T*>(py)));
       }
     }
     if constexpr (STAGES > 0) {
-      fetch(t + STAGES * step, stage);
-      stage = stage + 1 == STAGES ? 0 : stage + 1;
+      fetch(t + STAGES * step, slot, scalar);
+      slot += m.stage_bytes;
+      scalar += 16;
+      if (slot == m.ring + STAGES * m.stage_bytes) slot = m.ring, scalar = m.scalars;
     }
-    if (y) {
+    if (has_y) {
       float k = gt;
-      if (a.gamma_post) {
+      if (has_post) {
         float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
@@ -194,20 +209,18 @@ __global__ void __launch_bounds__(kBigThreads) block_norm_kernel(const BlockNorm
         if (q.lane == 0) a.rstd_post[t] = rho;
         k *= rho;
       }
-      T* o = static_cast<T*>(a.r_out) + t * a.ld_ro;
+      char* o = static_cast<char*>(a.r_out) + t * (a.ld_ro * (int)sizeof(T));
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int g = q.lane + i * q.lanes;
-        if (g < segs) {
-          const Vec8 wc = unpack(fetched8<float>(m.weight, segs, g));
+      for (int i = 0; i < VPT; ++i)
+        if (on(i)) {
+          const Vec8 wc = unpack(fetched8<float>(m.weight + m.smem[i], m.plane));
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             x[i].p[e] = __ffma2_rn(__fmul2_rn(p[i].p[e], splat(k)), wc.p[e], __fmul2_rn(x[i].p[e], splat(a.scale)));
-          st8_stream(o + g * 8, pack<T>(x[i]));
+          st8_stream(reinterpret_cast<T*>(o + m.col[i]), pack<T>(x[i]));
         }
-      }
     }
-    if (a.gamma_pre) {
+    if (has_pre) {
       float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < VPT; ++i)
@@ -215,18 +228,16 @@ __global__ void __launch_bounds__(kBigThreads) block_norm_kernel(const BlockNorm
         for (int e = 0; e < 4; ++e) ss = __ffma2_rn(x[i].p[e], x[i].p[e], ss);
       const float rho = rsqrtf(fmaf(team_sum<WARP, 8>(ss, buf[flip][1]), inv, a.eps));
       if (q.lane == 0) a.rstd_pre[t] = rho;
-      T* o = static_cast<T*>(a.norm) + t * a.ld_n;
+      char* o = static_cast<char*>(a.norm) + t * (a.ld_n * (int)sizeof(T));
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int g = q.lane + i * q.lanes;
-        if (g < segs) {
+      for (int i = 0; i < VPT; ++i)
+        if (on(i)) {
           const Vec8 w = unpack(wn[i]);
           Vec8 n;
 #pragma unroll
           for (int e = 0; e < 4; ++e) n.p[e] = __fmul2_rn(__fmul2_rn(x[i].p[e], splat(rho)), w.p[e]);
-          st8_stream(o + g * 8, pack<T>(n));
+          st8_stream(reinterpret_cast<T*>(o + m.col[i]), pack<T>(n));
         }
-      }
     }
   }
   if constexpr (STAGES > 0) cp_async_wait<0>();
@@ -242,8 +253,8 @@ __global__ void __launch_bounds__(kBigThreads) block_norm_kernel(const BlockNorm
 // term.)  Bound by HBM: four rows read, two written.  A thread keeps the same
 // columns over all of its team's rows, so the column sums stay in registers until
 // the end; a second kernel adds the CTAs' sums in a fixed order.  Rows and
-// their scalars are fetched ahead as in the forward kernel.
-template <typename T, int VPT, bool WARP, bool BIG, int STAGES>
+// their scalars are fetched ahead as in the forward kernel; FULL as there.
+template <typename T, int VPT, bool WARP, bool BIG, int STAGES, bool FULL>
 __global__ void __launch_bounds__(BIG ? kBigThreads : kTeamThreads) block_norm_grad_kernel(const BlockNormGradArgs a) {
   constexpr int QUADS = BIG ? 8 : kTeamThreads / 128;
   __shared__ float4 buf[2][2][8];
@@ -251,34 +262,29 @@ __global__ void __launch_bounds__(BIG ? kBigThreads : kTeamThreads) block_norm_g
   const Team<WARP> q;
   const int segs = a.H >> 3;
   const float inv = 1.0f / (float)a.H;
-  const int unit = segs * (int)(sizeof(T) / 2);
-  const TeamSmem sm = team_smem<T, STAGES>(dyn, segs, q.teams, q.team, 4);
-  const T* const r_out = static_cast<const T*>(a.r_out);
-  const T* const dnorm = static_cast<const T*>(a.dnorm);
-  const T* const dr_out = static_cast<const T*>(a.dr_out);
-  const T* const y = static_cast<const T*>(a.y);
+  const TeamMemory<T, VPT, WARP, STAGES, 4> m(q, segs, dyn);
+  const bool has_y = FULL || a.y, has_post = FULL || a.gamma_post, has_pre = FULL || a.gamma_pre, has_dr = FULL || a.dr_out;
+  const char* const src[4] = {static_cast<const char*>(a.r_out), static_cast<const char*>(a.dnorm),
+                              static_cast<const char*>(a.dr_out), static_cast<const char*>(a.y)};
+  const bool has[4] = {has_pre, has_pre, has_dr, has_y};
   const float* gates = a.gate_mode == MHC_GATE_TOKEN ? static_cast<const float*>(a.gate) : nullptr;
-  auto fetch = [&](int64_t t, int stage) {
+  const int row_bytes = a.H * (int)sizeof(T);
+  auto on = [&](int i) { return FULL || m.on[i]; };
+  auto fetch = [&](int64_t t, uint32_t slot, uint32_t scalar) {
     if (t < a.T) {
-      uint4* s = sm.ring + stage * 4 * unit;
-      const int64_t row = t * a.H;
+      const int64_t row = t * row_bytes;
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int g = q.lane + i * q.lanes;
-        const int64_t at = row + g * 8;
-        if (g < segs) {
-          if (a.gamma_pre) {
-            fetch8<T>(s, segs, g, r_out + at);
-            fetch8<T>(s + unit, segs, g, dnorm + at);
-          }
-          if (dr_out) fetch8<T>(s + 2 * unit, segs, g, dr_out + at);
-          if (y) fetch8<T>(s + 3 * unit, segs, g, y + at);
+      for (int k = 0; k < 4; ++k)
+        if (has[k]) {
+          const char* p = src[k] + row;
+#pragma unroll
+          for (int i = 0; i < VPT; ++i)
+            if (on(i)) fetch8<T>(slot + k * m.matrix + m.smem[i], m.plane, p + m.col[i]);
         }
-      }
       if ((threadIdx.x & 31) == 0) {
-        if (a.gamma_pre) cp_async4(sm.scalars + stage * 4, a.rstd_pre + t);
-        if (a.gamma_post) cp_async4(sm.scalars + stage * 4 + 1, a.rstd_post + t);
-        if (gates) cp_async4(sm.scalars + stage * 4 + 2, gates + t);
+        if (has_pre) cp_async4(scalar, a.rstd_pre + t);
+        if (has_post) cp_async4(scalar + 4, a.rstd_post + t);
+        if (gates) cp_async4(scalar + 8, gates + t);
       }
     }
     cp_async_commit();
@@ -286,95 +292,88 @@ __global__ void __launch_bounds__(BIG ? kBigThreads : kTeamThreads) block_norm_g
   const int64_t step = (int64_t)gridDim.x * q.teams;
   int64_t t = (int64_t)blockIdx.x * q.teams + q.team;
 #pragma unroll
-  for (int s = 0; s < STAGES; ++s) fetch(t + s * step, s);
+  for (int s = 0; s < STAGES; ++s) fetch(t + s * step, m.ring + s * m.stage_bytes, m.scalars + s * 16);
   Vec8 s_post[VPT], s_pre[VPT];
   Raw8<T> wn[VPT];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int g = q.lane + i * q.lanes;
     s_post[i] = s_pre[i] = zero8();
-    if (g < segs) {
+    if (on(i)) {
       const Raw8<float> w = pack<float>(
           mul8(weight8<T>(a.gamma_post, g), weight8<T>(a.gate_mode == MHC_GATE_CHANNEL ? a.gate : nullptr, g)));
-      sm.weight[g] = w.q[0];
-      sm.weight[segs + g] = w.q[1];
-      if (a.gamma_pre) wn[i] = ld8(static_cast<const T*>(a.gamma_pre) + g * 8);
+      sts16(m.weight + m.smem[i], w.q[0]);
+      sts16(m.weight + m.plane + m.smem[i], w.q[1]);
+      if (has_pre) wn[i] = ld8(static_cast<const T*>(a.gamma_pre) + g * 8);
     }
   }
   if constexpr (!WARP) {
     if (threadIdx.x < 32) buf[threadIdx.x >> 4][(threadIdx.x >> 3) & 1][threadIdx.x & 7] = make_float4(0.f, 0.f, 0.f, 0.f);
     __syncthreads();
   }
-  int flip = 0, stage = 0;
+  int flip = 0;
+  uint32_t slot = m.ring, scalar = m.scalars;
   for (; t < a.T; t += step, flip ^= 1) {
     Vec8 G[VPT], x[VPT];
-    const int64_t row = t * a.H;
+    const int64_t row = t * row_bytes;
     if constexpr (STAGES > 0) {
       cp_async_wait<(STAGES > 0 ? STAGES - 1 : 0)>();
       __syncwarp();
     }
     float rho2 = 1.f, rho1 = 1.f, gt = 1.f;
-    if (a.gamma_pre) rho2 = STAGES ? sm.scalars[stage * 4] : a.rstd_pre[t];
-    if (a.gamma_post) rho1 = STAGES ? sm.scalars[stage * 4 + 1] : a.rstd_post[t];
-    if (gates) gt = STAGES ? sm.scalars[stage * 4 + 2] : gates[t];
-    const uint4* s = sm.ring + stage * 4 * unit;
-    auto take = [&](int m, const T* src, int g) {
-      return unpack(STAGES ? fetched8<T>(s + m * unit, segs, g) : ld8_stream(src + row + g * 8));
+    if (has_pre) rho2 = STAGES ? lds4(scalar) : a.rstd_pre[t];
+    if (has_post) rho1 = STAGES ? lds4(scalar + 4) : a.rstd_post[t];
+    if (gates) gt = STAGES ? lds4(scalar + 8) : gates[t];
+    auto take = [&](int k, int i) {
+      return unpack(STAGES ? fetched8<T>(slot + k * m.matrix + m.smem[i], m.plane)
+                           : ld8_stream(reinterpret_cast<const T*>(src[k] + row + m.col[i])));
     };
-    if (a.gamma_pre) {
+    if (has_pre) {
       float2 m2 = make_float2(0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
-        const int g = q.lane + i * q.lanes;
-        G[i] = x[i] = zero8();
-        if (g < segs) {
-          x[i] = take(0, r_out, g);
-          const Vec8 dn = take(1, dnorm, g), w = unpack(wn[i]);
+        if (!FULL) G[i] = x[i] = zero8();
+        if (on(i)) {
+          x[i] = take(0, i);
+          const Vec8 dn = take(1, i), w = unpack(wn[i]);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float2 dx = __fmul2_rn(dn.p[e], x[i].p[e]);
             s_pre[i].p[e] = __ffma2_rn(dx, splat(rho2), s_pre[i].p[e]);
             G[i].p[e] = __fmul2_rn(w.p[e], dn.p[e]);
-            m2 = __ffma2_rn(G[i].p[e], x[i].p[e], m2);
+            m2 = __ffma2_rn(w.p[e], dx, m2);
           }
         }
       }
       const float k = -rho2 * rho2 * (team_sum<WARP, QUADS>(m2, buf[flip][0]) * inv) * rho2;
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
-        const int g = q.lane + i * q.lanes;
-        const Vec8 d = dr_out && g < segs ? take(2, dr_out, g) : zero8();
+        const Vec8 d = has_dr && on(i) ? take(2, i) : zero8();
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           G[i].p[e] = __ffma2_rn(x[i].p[e], splat(k), __ffma2_rn(G[i].p[e], splat(rho2), d.p[e]));
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int g = q.lane + i * q.lanes;
-        G[i] = g < segs ? take(2, dr_out, g) : zero8();
-      }
+      for (int i = 0; i < VPT; ++i) G[i] = on(i) ? take(2, i) : zero8();
     }
-    T* dr = static_cast<T*>(a.dr) + row;
+    char* dr = static_cast<char*>(a.dr) + row;
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int g = q.lane + i * q.lanes;
-      if (g < segs) {
+    for (int i = 0; i < VPT; ++i)
+      if (on(i)) {
         Vec8 o;
 #pragma unroll
         for (int e = 0; e < 4; ++e) o.p[e] = __fmul2_rn(G[i].p[e], splat(a.scale));
-        st8_stream(dr + g * 8, pack<T>(o));
+        st8_stream(reinterpret_cast<T*>(dr + m.col[i]), pack<T>(o));
       }
-    }
     float2 n2 = make_float2(0.f, 0.f);
-    if (y) {
+    if (has_y) {
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
-        const int g = q.lane + i * q.lanes;
-        x[i] = zero8();
-        if (g < segs) {
-          x[i] = take(3, y, g);
-          const Vec8 wc = unpack(fetched8<float>(sm.weight, segs, g));
+        if (!FULL) x[i] = zero8();
+        if (on(i)) {
+          x[i] = take(3, i);
+          const Vec8 wc = unpack(fetched8<float>(m.weight + m.smem[i], m.plane));
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float2 gr = __fmul2_rn(G[i].p[e], splat(rho1));
@@ -388,30 +387,30 @@ __global__ void __launch_bounds__(BIG ? kBigThreads : kTeamThreads) block_norm_g
     // the row is in registers: its stage takes the row STAGES further on
     if constexpr (STAGES > 0) {
       __syncwarp();
-      fetch(t + STAGES * step, stage);
-      stage = stage + 1 == STAGES ? 0 : stage + 1;
+      fetch(t + STAGES * step, slot, scalar);
+      slot += m.stage_bytes;
+      scalar += 16;
+      if (slot == m.ring + STAGES * m.stage_bytes) slot = m.ring, scalar = m.scalars;
     }
-    if (y) {
+    if (has_y) {
       float k = 0.f;
-      if (a.gamma_post || gates) {
+      if (has_post || gates) {
         const float N = team_sum<WARP, QUADS>(n2, buf[flip][1]);
         if (gates && q.lane == 0) a.dgate[t] = N;
-        if (a.gamma_post) k = -rho1 * (N * inv) * rho1 * gt;
+        if (has_post) k = -rho1 * (N * inv) * rho1 * gt;
       }
-      T* dy = static_cast<T*>(a.dy) + row;
+      char* dy = static_cast<char*>(a.dy) + row;
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int g = q.lane + i * q.lanes;
-        if (g < segs) {
+      for (int i = 0; i < VPT; ++i)
+        if (on(i)) {
           Vec8 o;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             o.p[e] = __fmul2_rn(G[i].p[e], splat(gt));
-            if (a.gamma_post) o.p[e] = __ffma2_rn(x[i].p[e], splat(k), o.p[e]);
+            if (has_post) o.p[e] = __ffma2_rn(x[i].p[e], splat(k), o.p[e]);
           }
-          st8_stream(dy + g * 8, pack<T>(o));
+          st8_stream(reinterpret_cast<T*>(dy + m.col[i]), pack<T>(o));
         }
-      }
     }
   }
   if constexpr (STAGES > 0) cp_async_wait<0>();
@@ -420,7 +419,7 @@ __global__ void __launch_bounds__(BIG ? kBigThreads : kTeamThreads) block_norm_g
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int g = q.lane + i * q.lanes;
-    if (g < segs) {
+    if (on(i)) {
       float* o = out + g * 8;
       if (a.dgamma_post) st8(o, pack<float>(mul8(s_post[i], weight8<T>(channel, g))));
       if (channel) st8(o + a.H, pack<float>(mul8(s_post[i], weight8<T>(a.gamma_post, g))));
@@ -497,34 +496,40 @@ static int64_t grad_ctas(int64_t T, const TeamPlan& p) {
   return need < most ? need : most;
 }
 
-#define MHC_BY_TEAM(plan, ...)                                                                        \
+#define MHC_BY_TEAM(plan, full, ...)                                                                  \
+  if (plan.stages == 0) { constexpr int K = 0; constexpr bool F = false; MHC_BY_TEAM_(plan, __VA_ARGS__) } \
+  else if (full) { constexpr bool F = true; MHC_BY_STAGES(plan, __VA_ARGS__) }                        \
+  else { constexpr bool F = false; MHC_BY_STAGES(plan, __VA_ARGS__) }
+#define MHC_BY_STAGES(plan, ...)                                                                      \
   if (plan.stages == 4) { constexpr int K = 4; MHC_BY_TEAM_(plan, __VA_ARGS__) }                      \
   else if (plan.stages == 2) { constexpr int K = 2; MHC_BY_TEAM_(plan, __VA_ARGS__) }                 \
-  else if (plan.stages == 1) { constexpr int K = 1; MHC_BY_TEAM_(plan, __VA_ARGS__) }                 \
-  else { constexpr int K = 0; MHC_BY_TEAM_(plan, __VA_ARGS__) }
+  else { constexpr int K = 1; MHC_BY_TEAM_(plan, __VA_ARGS__) }
 #define MHC_BY_TEAM_(plan, ...)                                                                       \
   if (plan.vpt == 1) { constexpr bool W = true, L = false; constexpr int N = 1; __VA_ARGS__; }        \
   else if (plan.warp) { constexpr bool W = true, L = false; constexpr int N = 2; __VA_ARGS__; }       \
   else if (!plan.big) { constexpr bool W = false, L = false; constexpr int N = 2; __VA_ARGS__; }      \
   else { constexpr bool W = false, L = true; constexpr int N = 2; __VA_ARGS__; }
 
-template <typename T, int N, bool W, int K>
+// Whether every thread has all of its columns.
+static bool even_columns(int H, const TeamPlan& p) { return H / 8 == p.vpt * (p.warp ? 32 : p.threads); }
+
+template <typename T, int N, bool W, int K, bool F>
 static cudaError_t norm_launch(const BlockNormArgs& a, const TeamPlan& p, cudaStream_t s) {
   static SmemGrant grant;
-  cudaError_t e = allow_smem(grant, (const void*)block_norm_kernel<T, N, W, K>, p.smem);
+  cudaError_t e = allow_smem(grant, (const void*)block_norm_kernel<T, N, W, K, F>, p.smem);
   if (e != cudaSuccess) return e;
   int64_t grid = (a.T + p.teams - 1) / p.teams;
   if (grid > (int64_t)kSMs * p.ctas) grid = (int64_t)kSMs * p.ctas;
-  block_norm_kernel<T, N, W, K><<<(unsigned)grid, p.threads, p.smem, s>>>(a);
+  block_norm_kernel<T, N, W, K, F><<<(unsigned)grid, p.threads, p.smem, s>>>(a);
   return cudaGetLastError();
 }
 
-template <typename T, int N, bool W, bool L, int K>
+template <typename T, int N, bool W, bool L, int K, bool F>
 static cudaError_t grad_launch(const BlockNormGradArgs& a, const TeamPlan& p, int64_t grid, cudaStream_t s) {
   static SmemGrant grant;
-  cudaError_t e = allow_smem(grant, (const void*)block_norm_grad_kernel<T, N, W, L, K>, p.smem);
+  cudaError_t e = allow_smem(grant, (const void*)block_norm_grad_kernel<T, N, W, L, K, F>, p.smem);
   if (e != cudaSuccess) return e;
-  block_norm_grad_kernel<T, N, W, L, K><<<(unsigned)grid, p.threads, p.smem, s>>>(a);
+  block_norm_grad_kernel<T, N, W, L, K, F><<<(unsigned)grid, p.threads, p.smem, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -583,9 +588,10 @@ int mhc_block_norm(const void* y, int64_t ld_y, const void* r, int64_t ld_r, con
   const BlockNormArgs a = {y, r, gamma_post, gate, gamma_pre, ld_y, ld_r, ld_r_out, ld_norm, gate_mode, res_scale, eps,
                            T, H, r_out, norm, rstd_post, rstd_pre};
   const TeamPlan plan = norm_plan(H, b);
+  const bool full = y && gamma_post && gamma_pre && even_columns(H, plan);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
-  MHC_BY_DTYPE(dtype, E, { MHC_BY_TEAM(plan, { (void)L; e = norm_launch<E, N, W, K>(a, plan, s); }) });
+  MHC_BY_DTYPE(dtype, E, { MHC_BY_TEAM(plan, full, { (void)L; e = norm_launch<E, N, W, K, F>(a, plan, s); }) });
   return ops_cuda(e, "block_norm launch");
 }
 
@@ -657,10 +663,11 @@ int mhc_block_norm_grad(const void* dr_out, const void* dnorm, const void* y, co
   const BlockNormGradArgs a = {dr_out, dnorm, y, r_out, gamma_post, gate, gamma_pre, rstd_post, rstd_pre, gate_mode,
                                res_scale, T, H, dy, dr, dgamma_post, dgate, dgamma_pre, static_cast<float*>(workspace)};
   const TeamPlan plan = grad_plan(H, b);
+  const bool full = y && dr_out && gamma_post && gamma_pre && even_columns(H, plan);
   const int64_t grid = grad_ctas(T, plan);
   const int parts = (int)grid * plan.teams;
   cudaError_t e = cudaSuccess;
-  MHC_BY_DTYPE(dtype, E, { MHC_BY_TEAM(plan, { e = grad_launch<E, N, W, L, K>(a, plan, grid, s); }) });
+  MHC_BY_DTYPE(dtype, E, { MHC_BY_TEAM(plan, full, { e = grad_launch<E, N, W, L, K, F>(a, plan, grid, s); }) });
   if (e == cudaSuccess && (dgamma_post || dgamma_pre || channel))
     e = launch_pdl(block_norm_fold_kernel, dim3((H + 31) / 32, 3), dim3(1024), 0, s, a.parts, parts, H, dgamma_post,
                    channel ? dgate : nullptr, dgamma_pre);

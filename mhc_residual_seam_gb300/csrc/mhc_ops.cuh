@@ -104,32 +104,45 @@ __device__ __forceinline__ void st8_stream(T* p, const Raw8<T>& r) {
 // ------------------------------------------------ rows fetched ahead of use --
 // A thread copies the eight columns it will work on into shared memory of its
 // own (cp.async), some rows ahead: nobody else reads them, so its own
-// wait_group is the only synchronisation.  A row of one matrix takes
-// `segs` * 8 elements; the 16-byte halves of fp32 columns lie in two planes, so a
-// warp's accesses are free of bank conflicts.
-__device__ __forceinline__ void cp_async16(void* smem, const void* gmem) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(gmem)
-               : "memory");
+// wait_group is the only synchronisation.  Shared addresses are 32-bit, global
+// ones a row's address plus a 32-bit offset.  The 16-byte halves of fp32 columns
+// lie in two planes of `plane` bytes, so a warp's accesses are free of bank
+// conflicts.
+__device__ __forceinline__ uint32_t smem_of(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void cp_async16(uint32_t smem, const void* gmem) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(gmem) : "memory");
 }
-__device__ __forceinline__ void cp_async4(void* smem, const void* gmem) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(gmem)
-               : "memory");
+__device__ __forceinline__ void cp_async4(uint32_t smem, const void* gmem) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem), "l"(gmem) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-template <typename T>
-__device__ __forceinline__ void fetch8(uint4* row, int segs, int g, const T* src) {
-#pragma unroll
-  for (int i = 0; i < (int)sizeof(T) / 2; ++i) cp_async16(row + i * segs + g, reinterpret_cast<const uint4*>(src) + i);
+__device__ __forceinline__ uint4 lds16(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ float lds4(uint32_t at) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts16(uint32_t at, const uint4& v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 template <typename T>
-__device__ __forceinline__ Raw8<T> fetched8(const uint4* row, int segs, int g) {
+__device__ __forceinline__ void fetch8(uint32_t smem, uint32_t plane, const char* src) {
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) cp_async16(smem + i * plane, src + i * 16);
+}
+template <typename T>
+__device__ __forceinline__ Raw8<T> fetched8(uint32_t smem, uint32_t plane) {
   Raw8<T> r;
 #pragma unroll
-  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.q[i] = row[i * segs + g];
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.q[i] = lds16(smem + i * plane);
   return r;
 }
 
