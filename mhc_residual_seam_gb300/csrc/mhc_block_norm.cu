@@ -15,6 +15,7 @@ struct BlockNormArgs {
   int H;
   void *r_out, *norm;
   float *rstd_post, *rstd_pre;
+  int run;  // rows of a CTA
 };
 
 struct BlockNormGradArgs {
@@ -26,7 +27,8 @@ struct BlockNormGradArgs {
   int H;
   void *dy, *dr;
   float *dgamma_post, *dgate, *dgamma_pre;
-  float* parts;  // [gridDim.x][3][H] column sums of each CTA: gamma_post, gate, gamma_pre
+  float* parts;  // [teams][2][H] column sums of each team: S and dgamma_pre
+  int run;       // rows of a CTA
 };
 
 // A team of threads works on one row: a warp (rows of at most 512 columns,
@@ -73,6 +75,11 @@ __device__ __forceinline__ Vec8 weight8(const void* w, int g) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) o.p[i] = make_float2(1.f, 1.f);
   return o;
+}
+template <typename T>
+__device__ __forceinline__ float weight1(const void* w, int c) {
+  if constexpr (sizeof(T) == 4) return static_cast<const float*>(w)[c];
+  else return pair_of((uint32_t)static_cast<const uint16_t*>(w)[c], T()).x;
 }
 __device__ __forceinline__ Vec8 mul8(const Vec8& a, const Vec8& b) {
   Vec8 o;
@@ -133,11 +140,12 @@ __global__ void __launch_bounds__(kBigThreads) block_norm_kernel(const BlockNorm
   const char* y = static_cast<const char*>(a.y);
   const char* r = static_cast<const char*>(a.r);
   const float* gates = a.gate_mode == MHC_GATE_TOKEN ? static_cast<const float*>(a.gate) : nullptr;
-  const int64_t step = (int64_t)gridDim.x * q.teams;
+  const int step = q.teams;
+  const int64_t first = (int64_t)blockIdx.x * a.run, end = first + a.run < a.T ? first + a.run : a.T;
   const TeamMemory<T, VPT, WARP, STAGES, 2> m(q, segs, dyn);
   auto on = [&](int i) { return FULL || m.on[i]; };
   auto fetch = [&](int64_t t, uint32_t slot, uint32_t scalar) {
-    if (t < a.T) {
+    if (t < end) {
       const char* pr = r + t * (a.ld_r * (int)sizeof(T));
       const char* py = y + t * (a.ld_y * (int)sizeof(T));
 #pragma unroll
@@ -150,7 +158,7 @@ __global__ void __launch_bounds__(kBigThreads) block_norm_kernel(const BlockNorm
     }
     cp_async_commit();
   };
-  int64_t t = (int64_t)blockIdx.x * q.teams + q.team;
+  int64_t t = first + q.team;
 #pragma unroll
   for (int s = 0; s < STAGES; ++s) fetch(t + s * step, m.ring + s * m.stage_bytes, m.scalars + s * 16);
   Raw8<T> wn[VPT];
@@ -171,7 +179,7 @@ __global__ void __launch_bounds__(kBigThreads) block_norm_kernel(const BlockNorm
   }
   int flip = 0;
   uint32_t slot = m.ring, scalar = m.scalars;
-  for (; t < a.T; t += step, flip ^= 1) {
+  for (; t < end; t += step, flip ^= 1) {
     Vec8 p[VPT], x[VPT];
     if constexpr (STAGES > 0) cp_async_wait<(STAGES > 0 ? STAGES - 1 : 0)>();
     float gt = 1.f;
@@ -270,8 +278,9 @@ __global__ void __launch_bounds__(BIG ? kBigThreads : kTeamThreads) block_norm_g
   const float* gates = a.gate_mode == MHC_GATE_TOKEN ? static_cast<const float*>(a.gate) : nullptr;
   const int row_bytes = a.H * (int)sizeof(T);
   auto on = [&](int i) { return FULL || m.on[i]; };
+  const int64_t first = (int64_t)blockIdx.x * a.run, end = first + a.run < a.T ? first + a.run : a.T;
   auto fetch = [&](int64_t t, uint32_t slot, uint32_t scalar) {
-    if (t < a.T) {
+    if (t < end) {
       const int64_t row = t * row_bytes;
 #pragma unroll
       for (int k = 0; k < 4; ++k)
@@ -289,8 +298,8 @@ __global__ void __launch_bounds__(BIG ? kBigThreads : kTeamThreads) block_norm_g
     }
     cp_async_commit();
   };
-  const int64_t step = (int64_t)gridDim.x * q.teams;
-  int64_t t = (int64_t)blockIdx.x * q.teams + q.team;
+  const int step = q.teams;
+  int64_t t = first + q.team;
 #pragma unroll
   for (int s = 0; s < STAGES; ++s) fetch(t + s * step, m.ring + s * m.stage_bytes, m.scalars + s * 16);
   Vec8 s_post[VPT], s_pre[VPT];
@@ -313,7 +322,7 @@ __global__ void __launch_bounds__(BIG ? kBigThreads : kTeamThreads) block_norm_g
   }
   int flip = 0;
   uint32_t slot = m.ring, scalar = m.scalars;
-  for (; t < a.T; t += step, flip ^= 1) {
+  for (; t < end; t += step, flip ^= 1) {
     Vec8 G[VPT], x[VPT];
     const int64_t row = t * row_bytes;
     if constexpr (STAGES > 0) {
@@ -414,42 +423,52 @@ __global__ void __launch_bounds__(BIG ? kBigThreads : kTeamThreads) block_norm_g
     }
   }
   if constexpr (STAGES > 0) cp_async_wait<0>();
-  float* out = a.parts + ((int64_t)blockIdx.x * q.teams + q.team) * 3 * a.H;
-  const void* channel = a.gate_mode == MHC_GATE_CHANNEL ? a.gate : nullptr;
+  pdl_launch();
+  float* out = a.parts + ((int64_t)blockIdx.x * q.teams + q.team) * 2 * a.H;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int g = q.lane + i * q.lanes;
     if (on(i)) {
-      float* o = out + g * 8;
-      if (a.dgamma_post) st8(o, pack<float>(mul8(s_post[i], weight8<T>(channel, g))));
-      if (channel) st8(o + a.H, pack<float>(mul8(s_post[i], weight8<T>(a.gamma_post, g))));
-      if (a.dgamma_pre) st8(o + 2 * a.H, pack<float>(s_pre[i]));
+      if (has_y) st8(out + g * 8, pack<float>(s_post[i]));
+      if (has_pre) st8(out + a.H + g * 8, pack<float>(s_pre[i]));
     }
   }
 }
 
-// Adds the parts' column sums in a fixed order: 32 columns x 32 slices of parts
-// per CTA, the slices joined in slice order.
-__global__ void __launch_bounds__(1024) block_norm_fold_kernel(const float* __restrict__ parts, int n, int H, float* post,
-                                                               float* gate, float* pre) {
-  __shared__ float sh[32][33];
+// Adds the teams' column sums in a fixed order and finishes the weights'
+// gradients: 128 columns x 32 slices of teams per CTA, four columns a thread, the
+// slices joined in slice order.
+template <typename T>
+__global__ void __launch_bounds__(1024) block_norm_fold_kernel(const BlockNormGradArgs a, int n) {
+  __shared__ float4 sh[32][32];
   pdl_wait();
-  float* out = blockIdx.y == 0 ? post : blockIdx.y == 1 ? gate : pre;
-  if (!out) return;
-  const int c = blockIdx.x * 32 + (threadIdx.x & 31), w = threadIdx.x >> 5;
-  float x = 0.f;
-  if (c < H) {
-    const float* p = parts + (int64_t)blockIdx.y * H + c;
+  const bool post = blockIdx.y == 0;
+  const bool channel = a.gate_mode == MHC_GATE_CHANNEL;
+  if (post ? !a.dgamma_post && !channel : !a.dgamma_pre) return;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int c = (blockIdx.x * 32 + lane) * 4;
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](const float4& v) { x.x += v.x, x.y += v.y, x.z += v.z, x.w += v.w; };
+  if (c < a.H) {
+    const float* p = a.parts + (post ? 0 : a.H) + c;
     const int lo = (int)((int64_t)n * w / 32), hi = (int)((int64_t)n * (w + 1) / 32);
 #pragma unroll 8
-    for (int i = lo; i < hi; ++i) x += p[(int64_t)i * 3 * H];
+    for (int i = lo; i < hi; ++i) add(*reinterpret_cast<const float4*>(p + (int64_t)i * 2 * a.H));
   }
-  sh[w][threadIdx.x & 31] = x;
+  sh[w][lane] = x;
   __syncthreads();
-  if (w == 0 && c < H) {
+  if (w || c >= a.H) return;
+#pragma unroll 8
+  for (int i = 1; i < 32; ++i) add(sh[i][lane]);
+  const float v[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-    for (int i = 1; i < 32; ++i) x += sh[i][threadIdx.x];
-    out[c] = x;
+  for (int e = 0; e < 4; ++e) {
+    if (!post) {
+      a.dgamma_pre[c + e] = v[e];
+      continue;
+    }
+    if (a.dgamma_post) a.dgamma_post[c + e] = v[e] * (channel ? weight1<T>(a.gate, c + e) : 1.f);
+    if (channel) a.dgate[c + e] = v[e] * (a.gamma_post ? weight1<T>(a.gamma_post, c + e) : 1.f);
   }
 }
 
@@ -490,11 +509,22 @@ static TeamPlan team_plan(int H, size_t type_bytes, int matrices, int sm_threads
 static TeamPlan norm_plan(int H, size_t b) { return team_plan(H, b, 2, 1024); }
 static TeamPlan grad_plan(int H, size_t b) { return team_plan(H, b, 4, 640); }
 
-// CTAs of the gradient: all resident at once.
-static int64_t grad_ctas(int64_t T, const TeamPlan& p) {
-  const int64_t need = (T + p.teams - 1) / p.teams, most = (int64_t)kSMs * p.ctas;
-  return need < most ? need : most;
+// Rows of a CTA.  Forward: runs of four, so that CTAs start as others end and an
+// SM that gets through faster takes more of them (T = 16384, H = 5120 bf16: 102 us;
+// one run of 36 rows per resident CTA, with the same number of bytes in flight,
+// 120; runs of 1, 2 and 9 rows 123, 103 and 105).  Fewer when that leaves SMs idle.
+// Gradient: one run per resident CTA, since every run adds a row of column sums
+// that has to be written and folded (runs of 54 rows 166 us, 27 rows 172, 16 rows 192).
+static int resident_run(int64_t T, const TeamPlan& p) {
+  const int64_t slots = (int64_t)kSMs * p.ctas, even = (T + slots - 1) / slots;
+  return (int)((even + p.teams - 1) / p.teams * p.teams);
 }
+static int norm_run(int64_t T, const TeamPlan& p) {
+  const int even = resident_run(T, p);
+  return even > 4 * p.teams ? 4 * p.teams : even;
+}
+static int grad_run(int64_t T, const TeamPlan& p) { return resident_run(T, p); }
+static int64_t grad_ctas(int64_t T, const TeamPlan& p) { return (T + grad_run(T, p) - 1) / grad_run(T, p); }
 
 #define MHC_BY_TEAM(plan, full, ...)                                                                  \
   if (plan.stages == 0) { constexpr int K = 0; constexpr bool F = false; MHC_BY_TEAM_(plan, __VA_ARGS__) } \
@@ -518,8 +548,7 @@ static cudaError_t norm_launch(const BlockNormArgs& a, const TeamPlan& p, cudaSt
   static SmemGrant grant;
   cudaError_t e = allow_smem(grant, (const void*)block_norm_kernel<T, N, W, K, F>, p.smem);
   if (e != cudaSuccess) return e;
-  int64_t grid = (a.T + p.teams - 1) / p.teams;
-  if (grid > (int64_t)kSMs * p.ctas) grid = (int64_t)kSMs * p.ctas;
+  const int64_t grid = (a.T + a.run - 1) / a.run;
   block_norm_kernel<T, N, W, K, F><<<(unsigned)grid, p.threads, p.smem, s>>>(a);
   return cudaGetLastError();
 }
@@ -585,10 +614,11 @@ int mhc_block_norm(const void* y, int64_t ld_y, const void* r, int64_t ld_r, con
     for (int q = o + 1; q < 4; ++q)
       if (rows_overlap(out[o], out[q])) return ops_fail(MHC_ERR_ALIAS, "two outputs overlap");
   }
-  const BlockNormArgs a = {y, r, gamma_post, gate, gamma_pre, ld_y, ld_r, ld_r_out, ld_norm, gate_mode, res_scale, eps,
-                           T, H, r_out, norm, rstd_post, rstd_pre};
+  BlockNormArgs a = {y, r, gamma_post, gate, gamma_pre, ld_y, ld_r, ld_r_out, ld_norm, gate_mode, res_scale, eps,
+                           T, H, r_out, norm, rstd_post, rstd_pre, 1};
   const TeamPlan plan = norm_plan(H, b);
   const bool full = y && gamma_post && gamma_pre && even_columns(H, plan);
+  a.run = norm_run(T, plan);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
   MHC_BY_DTYPE(dtype, E, { MHC_BY_TEAM(plan, full, { (void)L; e = norm_launch<E, N, W, K, F>(a, plan, s); }) });
@@ -600,7 +630,7 @@ size_t mhc_block_norm_grad_workspace_bytes(int64_t T, int H) {
   size_t most = 0;  // the plan differs by the type's size
   for (size_t b = 2; b <= 4; b += 2) {
     const mhc::TeamPlan p = mhc::grad_plan(H, b);
-    const size_t n = (size_t)mhc::grad_ctas(T, p) * p.teams * 3 * H * sizeof(float);
+    const size_t n = (size_t)mhc::grad_ctas(T, p) * p.teams * 2 * H * sizeof(float);
     if (n > most) most = n;
   }
   return most;
@@ -660,17 +690,17 @@ int mhc_block_norm_grad(const void* dr_out, const void* dnorm, const void* y, co
     for (int q = o + 1; q < 6; ++q)
       if (rows_overlap(out[o], out[q])) return ops_fail(MHC_ERR_ALIAS, "two outputs overlap");
   }
-  const BlockNormGradArgs a = {dr_out, dnorm, y, r_out, gamma_post, gate, gamma_pre, rstd_post, rstd_pre, gate_mode,
-                               res_scale, T, H, dy, dr, dgamma_post, dgate, dgamma_pre, static_cast<float*>(workspace)};
+  BlockNormGradArgs a = {dr_out, dnorm, y, r_out, gamma_post, gate, gamma_pre, rstd_post, rstd_pre, gate_mode,
+                               res_scale, T, H, dy, dr, dgamma_post, dgate, dgamma_pre, static_cast<float*>(workspace), 1};
   const TeamPlan plan = grad_plan(H, b);
   const bool full = y && dr_out && gamma_post && gamma_pre && even_columns(H, plan);
+  a.run = grad_run(T, plan);
   const int64_t grid = grad_ctas(T, plan);
   const int parts = (int)grid * plan.teams;
   cudaError_t e = cudaSuccess;
   MHC_BY_DTYPE(dtype, E, { MHC_BY_TEAM(plan, full, { e = grad_launch<E, N, W, L, K, F>(a, plan, grid, s); }) });
   if (e == cudaSuccess && (dgamma_post || dgamma_pre || channel))
-    e = launch_pdl(block_norm_fold_kernel, dim3((H + 31) / 32, 3), dim3(1024), 0, s, a.parts, parts, H, dgamma_post,
-                   channel ? dgate : nullptr, dgamma_pre);
+    MHC_BY_DTYPE(dtype, E, { e = launch_pdl(block_norm_fold_kernel<E>, dim3((H + 127) / 128, 2), dim3(1024), 0, s, a, parts); });
   return ops_cuda(e, "block_norm_grad launch");
 }
 
