@@ -7,6 +7,10 @@ namespace mhc {
 
 constexpr int kRouteWarps = 4;
 constexpr int kMaxExperts = 1024;
+#ifndef RC
+#define RC 7
+#endif
+constexpr int kRouteCtas = RC;  // per SM
 
 template <typename T>
 __device__ __forceinline__ float logit_of(const T* p) {
@@ -16,14 +20,37 @@ __device__ __forceinline__ float logit_of(const T* p) {
   return l == l ? l : -INFINITY;  // a NaN logit is never chosen, as -inf
 }
 
+// A lane's EPL logits in 16-byte loads (fewer bytes in one load).
+template <typename T, int EPL>
+__device__ __forceinline__ void load_logits(const T* p, float* l) {
+  constexpr int BYTES = EPL * (int)sizeof(T);
+  if constexpr (BYTES >= 16 && sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < EPL / 4; ++i) {
+      const float4 q = __ldcs(reinterpret_cast<const float4*>(p) + i);
+      l[4 * i] = q.x, l[4 * i + 1] = q.y, l[4 * i + 2] = q.z, l[4 * i + 3] = q.w;
+    }
+  } else if constexpr (BYTES >= 16) {
+#pragma unroll
+    for (int i = 0; i < EPL / 8; ++i) {
+      const Vec8 q = unpack(ld8_stream(p + 8 * i));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) l[8 * i + 2 * e] = q.p[e].x, l[8 * i + 2 * e + 1] = q.p[e].y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) l[i] = logit_of(p + i);
+  }
+}
+
 // exp(l - max) with equal infinities at distance zero.
 __device__ __forceinline__ float soft_exp(float l, float m) { return l == -INFINITY ? 0.f : expf(l == m ? 0.f : l - m); }
-__device__ __forceinline__ float logistic(float l) { return 1.0f / (1.0f + expf(-l)); }
+__device__ __forceinline__ float logistic(float l) { return __frcp_rn(1.0f + expf(-l)); }  // rounded as 1 / (1 + e)
 
 // A key whose unsigned order is the values' order; 0 for what cannot be chosen.
 __device__ __forceinline__ uint32_t order_key(float x) {
   if (!(x > -INFINITY)) return 0u;
-  const uint32_t u = __float_as_uint(x + 0.0f);  // -0 and +0 are equal
+  const uint32_t u = __float_as_uint(x + 0.0f);  // a -0 (from a bias) counts as +0
   return u ^ (u >> 31 ? 0xffffffffu : 0x80000000u);
 }
 __device__ __forceinline__ float order_value(uint32_t k) {
@@ -36,6 +63,8 @@ struct RouteArgs {
   const float* bias;
   int E, groups, top_groups, k;
   bool sigmoid, renorm;
+  bool vector;       // rows are 16-byte aligned and no lane has part of its experts
+  bool whole_lanes;  // a group is a power of two of whole lanes
   float scale;
   int* indices;
   float* weights;
@@ -50,104 +79,251 @@ __device__ __forceinline__ float warp_max(float x) {
   return x;
 }
 
-// One warp per token; lane l holds the scores of experts l*EPL .. l*EPL+EPL-1
-// as order keys, so the lowest lane that has the maximum also has the lowest
-// index.  A round takes the warp's maximum (one redux), finds its lane (one
-// ballot), and that lane drops the expert and looks for its next best.
-template <typename T, int EPL>
+// Reductions over a segment of LANES adjacent lanes (one token).
+template <int LANES>
+__device__ __forceinline__ float seg_max(float x) {
+#pragma unroll
+  for (int d = LANES / 2; d; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+  return x;
+}
+template <int LANES>
+__device__ __forceinline__ float seg_sum(float x) {
+#pragma unroll
+  for (int d = LANES / 2; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+  return x;
+}
+template <int LANES>
+__device__ __forceinline__ uint32_t seg_max(uint32_t x) {
+  if constexpr (LANES == 32) {
+    return __reduce_max_sync(0xffffffffu, x);
+  } else {
+#pragma unroll
+    for (int d = LANES / 2; d; d >>= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, d));
+    return x;
+  }
+}
+// The lanes of this thread's segment for which `p` holds, from bit 0.
+template <int LANES>
+__device__ __forceinline__ unsigned seg_ballot(bool p) {
+  const unsigned all = __ballot_sync(0xffffffffu, p);
+  if constexpr (LANES == 32) return all;
+  else return (all >> (threadIdx.x & 31 & ~(LANES - 1))) & ((1u << LANES) - 1);
+}
+
+template <int EPL>
+struct BitsOf {
+  static constexpr int value = EPL == 1 ? 0 : 1 + BitsOf<EPL / 2>::value;
+};
+template <>
+struct BitsOf<1> {
+  static constexpr int value = 0;
+};
+
+// LANES lanes work on one token (32 / LANES tokens per warp); lane l of them
+// holds experts l*EPL .. l*EPL+EPL-1 as order keys.
+//
+// The k rounds of the choice work on each lane's two best keys, with the expert's
+// place in its lane written into the key's lowest log2(EPL) bits (lower places
+// first): a round is one maximum over the lanes and one ballot for the lowest
+// lane that has it, and the winner moves its second key up.  A lane whose two keys
+// are spent looks for the next two.  Keys that differ in those low bits only
+// could come in the wrong order; they are next to each other in it, so the slots
+// are compared with their neighbours by the exact choice afterwards, and a token
+// where they disagree (or where the k-th and the next key agree above the low bits)
+// is done again with whole keys, one scan of all keys per round.
+// Bound by instruction issue: about 20 instructions per expert for the score, 12
+// per round.
+template <typename T, int EPL, int LANES>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs a) {
-  __shared__ uint32_t keys[kRouteWarps][EPL * 32];
-  __shared__ int load[EPL * 32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int e = threadIdx.x; e < EPL * 32; e += blockDim.x) load[e] = 0;
+  constexpr uint32_t LOW = EPL - 1;
+  constexpr int TOKENS = 32 / LANES;
+  constexpr bool SMEM_GROUPS = LANES == 32;  // groups that do not fall on whole lanes
+  __shared__ uint32_t keys[SMEM_GROUPS ? kRouteWarps : 1][SMEM_GROUPS ? EPL * 32 : 1];
+  __shared__ int load[EPL * LANES];
+  const int lane = threadIdx.x & (LANES - 1), warp = threadIdx.x >> 5;
+  const int sub = (threadIdx.x & 31) / LANES;
+  for (int e = threadIdx.x; e < EPL * LANES; e += blockDim.x) load[e] = 0;
   __syncthreads();
   const int per = a.E / a.groups;
-  for (int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp; t < a.T; t += (int64_t)gridDim.x * kRouteWarps) {
+  const int group_lanes = per / EPL;  // where groups fall on whole lanes
+  float bias[EPL];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const int e = lane * EPL + i;
+    bias[i] = a.bias && e < a.E ? a.bias[e] : 0.f;
+  }
+  for (int64_t base = ((int64_t)blockIdx.x * kRouteWarps + warp) * TOKENS; base < a.T;
+       base += (int64_t)gridDim.x * kRouteWarps * TOKENS) {
+    const bool real = base + sub < a.T;
+    const int64_t t = real ? base + sub : a.T - 1;  // a segment without a token repeats the last one's work
     const T* row = static_cast<const T*>(a.logits) + t * a.ld;
-    float s[EPL];
     uint32_t key[EPL];
     float m = -INFINITY, total = 0.f;
+    {
+      float l[EPL];
+      if (a.vector) {
+        load_logits<T, EPL>(row + lane * EPL, l);
+      } else {
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const int e = lane * EPL + i;
-      s[i] = e < a.E ? logit_of(row + e) : -INFINITY;
-      m = fmaxf(m, s[i]);
-    }
-    if (!a.sigmoid) {
-      m = warp_max(m);
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) total += soft_exp(s[i], m);
-      total = warp_sum(total);
-    }
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const int e = lane * EPL + i;
-      float v = a.sigmoid ? logistic(s[i]) : soft_exp(s[i], m);
-      if (a.bias && e < a.E) v = (a.sigmoid ? v : v / total) + a.bias[e];
-      key[i] = s[i] == -INFINITY ? 0u : order_key(v);
-    }
-    if (a.groups > 1) {
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) keys[warp][lane * EPL + i] = key[i];
-      __syncwarp();
-      uint32_t b1 = 0, b2 = 0;
-      if (lane < a.groups)
-        for (int j = 0; j < per; ++j) {
-          const uint32_t q = keys[warp][lane * per + j];
-          b2 = max(b2, min(b1, q));
-          b1 = max(b1, q);
-        }
-      __syncwarp();
-      const uint32_t mine = b1 == 0 ? 0u : order_key(order_value(b1) + (b2 ? order_value(b2) : 0.f));
-      int rank = 0;
-      for (int g = 0; g < a.groups; ++g) {
-        const uint32_t other = __shfl_sync(0xffffffffu, mine, g);
-        rank += other > mine || (other == mine && g < lane);
+        for (int i = 0; i < EPL; ++i) l[i] = lane * EPL + i < a.E ? logit_of(row + lane * EPL + i) : -INFINITY;
       }
-      const unsigned keep = __ballot_sync(0xffffffffu, lane < a.groups && rank < a.top_groups);
-#pragma unroll
-      for (int i = 0; i < EPL; ++i)
-        if (!((keep >> ((lane * EPL + i) / per & 31)) & 1)) key[i] = 0;
-    }
-    uint32_t best = 0;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) best = max(best, key[i]);
-    int chosen = -1;  // lane j ends with the expert of slot j
-    for (int j = 0; j < a.k; ++j) {
-      const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-      if (top == 0) break;
-      const int who = __ffs(__ballot_sync(0xffffffffu, best == top)) - 1;
-      int at = 0;
-      if (lane == who) {
-        best = 0;
-        bool found = false;
+      if (a.sigmoid) {
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
-          if (!found && key[i] == top) {
-            found = true;
-            at = lane * EPL + i;
-            key[i] = 0;
-          }
-          best = max(best, key[i]);
+          const float v = logistic(l[i]) + bias[i];
+          key[i] = l[i] > -INFINITY ? order_key(v) : 0u;
         }
+      } else {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) m = fmaxf(m, l[i]);  // fmaxf passes NaN over
+        m = seg_max<LANES>(m);
+        float e[EPL];
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) e[i] = l[i] > -INFINITY ? soft_exp(l[i], m) : 0.f;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) total += e[i];
+        total = seg_sum<LANES>(total);
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+          key[i] = l[i] > -INFINITY ? order_key(a.bias ? e[i] / total + bias[i] : e[i]) : 0u;
       }
-      at = __shfl_sync(0xffffffffu, at, who);
-      if (lane == j) chosen = at;
     }
-    float w = 0.f;
-    if (chosen >= 0) {
+    if (a.groups > 1) {
+      if (!SMEM_GROUPS || a.whole_lanes) {
+        uint32_t b1 = 0, b2 = 0;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+          b2 = max(b2, min(b1, key[i]));
+          b1 = max(b1, key[i]);
+        }
+        for (int d = 1; d < group_lanes; d <<= 1) {
+          const uint32_t c1 = __shfl_xor_sync(0xffffffffu, b1, d), c2 = __shfl_xor_sync(0xffffffffu, b2, d);
+          b2 = max(max(b2, c2), min(b1, c1));
+          b1 = max(b1, c1);
+        }
+        const uint32_t mine = b1 == 0 ? 0u : order_key(order_value(b1) + (b2 ? order_value(b2) : 0.f));
+        int rank = 0;  // groups before this one
+        for (int d = group_lanes; d < LANES; d += group_lanes) {
+          const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, d);
+          rank += other > mine || (other == mine && (lane ^ d) < lane);
+        }
+        if (rank >= a.top_groups) {
+#pragma unroll
+          for (int i = 0; i < EPL; ++i) key[i] = 0;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) keys[warp][lane * EPL + i] = key[i];
+        __syncwarp();
+        uint32_t b1 = 0, b2 = 0;
+        if (lane < a.groups)
+          for (int j = 0; j < per; ++j) {
+            const uint32_t q = keys[warp][lane * per + j];
+            b2 = max(b2, min(b1, q));
+            b1 = max(b1, q);
+          }
+        __syncwarp();
+        const uint32_t mine = b1 == 0 ? 0u : order_key(order_value(b1) + (b2 ? order_value(b2) : 0.f));
+        int rank = 0;
+        for (int g = 0; g < a.groups; ++g) {
+          const uint32_t other = __shfl_sync(0xffffffffu, mine, g);
+          rank += other > mine || (other == mine && g < lane);
+        }
+        const unsigned keep = __ballot_sync(0xffffffffu, lane < a.groups && rank < a.top_groups);
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+          if (!((keep >> ((lane * EPL + i) / per & 31)) & 1)) key[i] = 0;
+      }
+    }
+
+    // the lane's two best keys below `under`
+    uint32_t b1, b2;
+    auto refill = [&](uint32_t under) {
+      b1 = b2 = 0;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        uint32_t p = key[i] ? (key[i] & ~LOW) | (LOW - i) : 0u;
+        p = p < under ? p : 0u;
+        b2 = max(b2, min(b1, p));
+        b1 = max(b1, p);
+      }
+    };
+    refill(0xffffffffu);
+    uint32_t slot = 0, next = 0;  // lane j: the key of slot j; the best key left
+    int chosen = -1;              // lane j: the expert of slot j
+    for (int j = 0; j < a.k; ++j) {
+      const uint32_t top = seg_max<LANES>(b1);
+      const unsigned have = seg_ballot<LANES>((b1 | LOW) == (top | LOW));
+      const int who = __ffs(have) - 1;
+      const uint32_t won = LANES == 32 && EPL == 1 ? top : __shfl_sync(0xffffffffu, b1, who, LANES);
+      if (lane == j && won) {
+        slot = won;
+        chosen = who * EPL + (int)(LOW - (won & LOW));
+      }
+      bool spent = false;
+      if (lane == who && won) {
+        b1 = b2;
+        b2 = 0;
+        spent = EPL > 2 && b1 == 0;
+      }
+      if (EPL > 2 && __any_sync(0xffffffffu, spent)) {
+        const uint32_t o1 = b1, o2 = b2;
+        refill(won);
+        if (!spent) b1 = o1, b2 = o2;
+      }
+    }
+    next = seg_max<LANES>(b1);
+
+    float w = 0.f, pick = -INFINITY;
+    auto weigh = [&]() {  // the chosen expert's score (w) and exact choice (pick)
+      w = 0.f;
+      pick = -INFINITY;
+      if (chosen < 0) return;
       const float l = logit_of(row + chosen);
-      w = a.sigmoid ? logistic(l) : soft_exp(l, m);
-      if (!a.renorm && !a.sigmoid) w = w / total;
-      atomicAdd(&load[chosen], 1);
+      const float raw = a.sigmoid ? logistic(l) : soft_exp(l, m);
+      const float score = a.sigmoid || (a.renorm && !a.bias) ? raw : raw / total;
+      pick = a.bias ? score + a.bias[chosen] : raw;
+      w = a.renorm ? raw : score;
+    };
+    weigh();
+    if (EPL > 1) {
+      const uint32_t after = __shfl_down_sync(0xffffffffu, slot, 1, LANES);
+      const float later = __shfl_down_sync(0xffffffffu, pick, 1, LANES);
+      bool redo = false;
+      if (slot) {
+        if (lane + 1 == a.k) redo = (slot | LOW) == (next | LOW);
+        else if (lane + 1 < a.k) redo = after && (slot | LOW) == (after | LOW) && pick != later;
+      }
+      if (__any_sync(0xffffffffu, redo)) {
+        unsigned alive = 0xffffffffu;
+        chosen = -1;
+        for (int j = 0; j < a.k; ++j) {
+          uint32_t best = 0;
+#pragma unroll
+          for (int i = 0; i < EPL; ++i) best = max(best, (alive >> i) & 1 ? key[i] : 0u);
+          const uint32_t top = seg_max<LANES>(best);
+          const int who = __ffs(seg_ballot<LANES>(best == top)) - 1;
+          int at = 0;
+          if (lane == who) {
+#pragma unroll
+            for (int i = EPL - 1; i >= 0; --i)
+              if (((alive >> i) & 1) && key[i] == top) at = i;
+            alive &= ~(1u << at);
+          }
+          at = __shfl_sync(0xffffffffu, at, who, LANES);
+          if (lane == j && top) chosen = who * EPL + at;
+        }
+        weigh();
+      }
     }
     if (a.renorm) {
-      const float sum = warp_sum(w);
+      const float sum = seg_sum<LANES>(w);
       w = sum > 0.f ? a.scale * w / sum : 0.f;
     } else {
       w *= a.scale;
     }
-    if (lane < a.k) {
+    if (real && lane < a.k) {
+      if (chosen >= 0) atomicAdd(&load[chosen], 1);
       a.indices[t * a.k + lane] = chosen;
       a.weights[t * a.k + lane] = w;
     }
@@ -248,6 +424,24 @@ static int route_checks(int64_t T, int E, int k, int dtype, int score, int64_t l
   return MHC_OK;
 }
 
+#define MHC_BY_LANES(epl, lanes, ...)                                                              \
+  if (lanes == 8) {                                                                                \
+    constexpr int L = 8;                                                                           \
+    if (epl == 1) { constexpr int N = 1; __VA_ARGS__; }                                            \
+    else if (epl == 2) { constexpr int N = 2; __VA_ARGS__; }                                       \
+    else if (epl == 4) { constexpr int N = 4; __VA_ARGS__; }                                       \
+    else { constexpr int N = 8; __VA_ARGS__; }                                                     \
+  } else if (lanes == 16) { constexpr int L = 16, N = 8; __VA_ARGS__; }                            \
+  else {                                                                                           \
+    constexpr int L = 32;                                                                          \
+    if (epl == 1) { constexpr int N = 1; __VA_ARGS__; }                                            \
+    else if (epl == 2) { constexpr int N = 2; __VA_ARGS__; }                                       \
+    else if (epl == 4) { constexpr int N = 4; __VA_ARGS__; }                                       \
+    else if (epl == 8) { constexpr int N = 8; __VA_ARGS__; }                                       \
+    else if (epl == 16) { constexpr int N = 16; __VA_ARGS__; }                                     \
+    else { constexpr int N = 32; __VA_ARGS__; }                                                    \
+  }
+
 #define MHC_BY_EXPERTS(E, ...)                                   \
   if (E <= 32) { constexpr int N = 1; __VA_ARGS__; }             \
   else if (E <= 64) { constexpr int N = 2; __VA_ARGS__; }        \
@@ -294,11 +488,26 @@ int mhc_route(const void* logits, int64_t ld, mhc_dtype dtype, const float* bias
   cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return ops_cuda(e, "device query");
   unsigned* ws = static_cast<unsigned*>(workspace);
-  const RouteArgs a = {logits, ld, T, bias, E, groups, top_groups, k, score == MHC_SCORE_SIGMOID, renorm != 0, scale,
-                       indices, weights, counts, counts ? ws + 16 : nullptr, counts ? ws + 64 : nullptr};
-  int64_t grid = (T + kRouteWarps - 1) / kRouteWarps;
-  if (grid > (int64_t)sms * 12) grid = (int64_t)sms * 12;
-  MHC_BY_DTYPE(dtype, D, { MHC_BY_EXPERTS(E, { route_kernel<D, N><<<(unsigned)grid, kRouteWarps * 32, 0, s>>>(a); }) });
+  // Eight experts a lane where they allow it, so that a warp takes several tokens of a
+  // small router; 32 lanes for more slots than lanes and for groups that do not
+  // fall on whole lanes.
+  int lanes = E <= 64 ? 8 : E <= 128 ? 16 : 32, epl = 1;
+  while (epl * lanes < E) epl <<= 1;
+  auto whole = [&]() {
+    const int per = E / groups, n = per / epl;
+    return E == epl * lanes && per % epl == 0 && (n & (n - 1)) == 0;
+  };
+  if (lanes < 32 && (k > lanes || (groups > 1 && !whole()))) {
+    lanes = 32;
+    for (epl = 1; epl * lanes < E;) epl <<= 1;
+  }
+  const bool vector = E == epl * lanes && (epl * b) % 16 == 0 && (ld * b) % 16 == 0 && ops_aligned(logits, 16);
+  const RouteArgs a = {logits, ld, T, bias, E, groups, top_groups, k, score == MHC_SCORE_SIGMOID, renorm != 0, vector,
+                       whole(), scale, indices, weights, counts, counts ? ws + 16 : nullptr, counts ? ws + 64 : nullptr};
+  const int64_t tokens = kRouteWarps * (32 / lanes);
+  int64_t grid = (T + tokens - 1) / tokens;
+  if (grid > (int64_t)sms * kRouteCtas) grid = (int64_t)sms * kRouteCtas;
+  MHC_BY_DTYPE(dtype, D, { MHC_BY_LANES(epl, lanes, { route_kernel<D, N, L><<<(unsigned)grid, kRouteWarps * 32, 0, s>>>(a); }) });
   return ops_cuda(cudaGetLastError(), "route launch");
 }
 
