@@ -65,6 +65,7 @@ struct RouteArgs {
   bool sigmoid, renorm;
   bool vector;       // rows are 16-byte aligned and no lane has part of its experts
   bool whole_lanes;  // a group is a power of two of whole lanes
+  bool estimate;     // choose from estimated scores first
   float scale;
   int* indices;
   float* weights;
@@ -119,20 +120,73 @@ struct BitsOf<1> {
   static constexpr int value = 0;
 };
 
-// LANES lanes work on one token (32 / LANES tokens per warp); lane l of them
-// holds experts l*EPL .. l*EPL+EPL-1 as order keys.
+// --------------------------------------------------- the choice, estimated --
+__device__ __forceinline__ float ex2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+template <int LANES>
+__device__ __forceinline__ float seg_fmax(float x) {
+  if constexpr (LANES == 32) {
+    float y;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    return y;
+  } else {
+    return seg_max<LANES>(x);
+  }
+}
+
+__device__ __forceinline__ void order(float& a, float& b) {  // a >= b
+  const float hi = fmaxf(a, b);
+  b = fminf(a, b);
+  a = hi;
+}
+__device__ __forceinline__ void sort4(float* v) {
+  order(v[0], v[1]), order(v[2], v[3]), order(v[0], v[2]), order(v[1], v[3]), order(v[1], v[2]);
+}
+// The best of two descending lists of four, descending, into `a`: the larger of
+// opposite ends is a bitonic list (Batcher's merge).
+__device__ __forceinline__ void merge4(float* a, const float* b) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) a[i] = fmaxf(a[i], b[3 - i]);
+  order(a[0], a[2]), order(a[1], a[3]), order(a[0], a[1]), order(a[2], a[3]);
+}
+// Batcher's odd-even merge sort of eight, descending.
+__device__ __forceinline__ void sort8(float* v) {
+  sort4(v), sort4(v + 4);
+  order(v[0], v[4]), order(v[1], v[5]), order(v[2], v[6]), order(v[3], v[7]);
+  order(v[2], v[4]), order(v[3], v[5]);
+  order(v[1], v[2]), order(v[3], v[4]), order(v[5], v[6]);
+}
+
+// LANES lanes work on one token (32 / LANES tokens per warp); lane l of them has
+// experts l*EPL .. l*EPL+EPL-1.
 //
-// The k rounds of the choice work on each lane's two best keys, with the expert's
-// place in its lane written into the key's lowest log2(EPL) bits (lower places
-// first): a round is one maximum over the lanes and one ballot for the lowest
-// lane that has it, and the winner moves its second key up.  A lane whose two keys
-// are spent looks for the next two.  Keys that differ in those low bits only
-// could come in the wrong order; they are next to each other in it, so the slots
-// are compared with their neighbours by the exact choice afterwards, and a token
-// where they disagree (or where the k-th and the next key agree above the low bits)
-// is done again with whole keys, one scan of all keys per round.
-// Bound by instruction issue: about 20 instructions per expert for the score, 12
-// per round.
+// The choice is made twice, the second time for few tokens.  First from
+// estimated scores (the hardware's exp2 and reciprocal, 4 instructions for a
+// sigmoid instead of about 20), with the expert's place in its lane written over the
+// lowest log2(EPL) bits: each lane sorts its best few, and a round is one maximum
+// over the lanes and one ballot for the lane that has it, which moves its list up.
+// An estimate is off by less than 2e-5 of the score (exp2's argument, at most 126,
+// is rounded to 2^-24 of itself, the two approximations to 2^-22, the place to
+// 2^-18), with a bias by less than 1e-6 and 5e-6 of the sum (a score is at most 1 and
+// its error largest in its middle), so slots that differ by more than twice that
+// from their neighbours, the last of them from the best expert left, are in the
+// order of the exact scores.  Where they do not (near ties, about one
+// token in a hundred of N(0, 1.5) logits), where two groups' sums are too near, or
+// where a lane's list runs out, the token is chosen again from the exact scores.
+//
+// The exact choice has whole order keys; its rounds work on each lane's two best
+// with the place in the low bits, and a lane whose two are spent looks for the
+// next two.  Keys that differ in those bits only could come in the wrong order;
+// they are next to each other in it, so the slots are compared with their
+// neighbours by the exact choice, and a token where they disagree (or where the
+// k-th and the next agree above the low bits) is done with whole keys, one scan of
+// all of them per round.
+//
+// Bound by instruction issue (the floor of T = 131072, E = 256 in fp32 is 21 us of
+// HBM).
 template <typename T, int EPL, int LANES>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs a) {
   constexpr uint32_t LOW = EPL - 1;
@@ -147,174 +201,276 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs
   const int per = a.E / a.groups;
   const int group_lanes = per / EPL;  // where groups fall on whole lanes
   float bias[EPL];
+  bool finite = true;
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
     const int e = lane * EPL + i;
     bias[i] = a.bias && e < a.E ? a.bias[e] : 0.f;
+    finite &= fabsf(bias[i]) < 3e38f;
   }
+  const bool estimate = a.estimate && __all_sync(0xffffffffu, finite);
   for (int64_t base = ((int64_t)blockIdx.x * kRouteWarps + warp) * TOKENS; base < a.T;
        base += (int64_t)gridDim.x * kRouteWarps * TOKENS) {
     const bool real = base + sub < a.T;
     const int64_t t = real ? base + sub : a.T - 1;  // a segment without a token repeats the last one's work
     const T* row = static_cast<const T*>(a.logits) + t * a.ld;
-    uint32_t key[EPL];
     float m = -INFINITY, total = 0.f;
-    {
-      float l[EPL];
+    int chosen = -1;  // lane j: the expert of slot j
+    auto logits = [&](float* l) {
       if (a.vector) {
         load_logits<T, EPL>(row + lane * EPL, l);
       } else {
 #pragma unroll
         for (int i = 0; i < EPL; ++i) l[i] = lane * EPL + i < a.E ? logit_of(row + lane * EPL + i) : -INFINITY;
       }
+    };
+    auto softmax = [&](const float* l) {  // the row's maximum, and its sum where a score needs it
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) m = fmaxf(m, l[i]);  // fmaxf passes NaN over
+      m = seg_max<LANES>(m);
+      total = 0.f;
+      if (a.bias || !a.renorm) {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) total += l[i] > -INFINITY ? soft_exp(l[i], m) : 0.f;
+        total = seg_sum<LANES>(total);
+      }
+    };
+
+    bool redo = !estimate;
+    if (estimate) {
+      constexpr int KEPT = EPL <= 4 ? EPL : LANES == 8 ? 8 : 4;  // how many of its best a lane keeps sorted
+      float v[EPL];
+      logits(v);
       if (a.sigmoid) {
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
-          const float v = logistic(l[i]) + bias[i];
-          key[i] = l[i] > -INFINITY ? order_key(v) : 0u;
+          const float s = rcp_approx(1.0f + ex2_approx(v[i] * -1.44269504f)) + bias[i];
+          const float p = __uint_as_float((__float_as_uint(s) & ~LOW) | i);
+          v[i] = v[i] > -INFINITY ? p : -INFINITY;
         }
       } else {
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) m = fmaxf(m, l[i]);  // fmaxf passes NaN over
-        m = seg_max<LANES>(m);
-        float e[EPL];
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) e[i] = l[i] > -INFINITY ? soft_exp(l[i], m) : 0.f;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) total += e[i];
-        total = seg_sum<LANES>(total);
-#pragma unroll
-        for (int i = 0; i < EPL; ++i)
-          key[i] = l[i] > -INFINITY ? order_key(a.bias ? e[i] / total + bias[i] : e[i]) : 0u;
-      }
-    }
-    if (a.groups > 1) {
-      if (!SMEM_GROUPS || a.whole_lanes) {
-        uint32_t b1 = 0, b2 = 0;
+        softmax(v);
+        redo = !(fabsf(m) < 3e38f);
+        const float c = m * 1.44269504f, share = a.bias ? rcp_approx(total) : 1.f;
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
-          b2 = max(b2, min(b1, key[i]));
-          b1 = max(b1, key[i]);
+          const float s = fmaf(ex2_approx(fmaf(v[i], 1.44269504f, -c)), share, bias[i]);
+          const float p = __uint_as_float((__float_as_uint(s) & ~LOW) | i);
+          v[i] = v[i] > -INFINITY ? p : -INFINITY;
         }
-        for (int d = 1; d < group_lanes; d <<= 1) {
-          const uint32_t c1 = __shfl_xor_sync(0xffffffffu, b1, d), c2 = __shfl_xor_sync(0xffffffffu, b2, d);
-          b2 = max(max(b2, c2), min(b1, c1));
-          b1 = max(b1, c1);
-        }
-        const uint32_t mine = b1 == 0 ? 0u : order_key(order_value(b1) + (b2 ? order_value(b2) : 0.f));
-        int rank = 0;  // groups before this one
-        for (int d = group_lanes; d < LANES; d += group_lanes) {
-          const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, d);
-          rank += other > mine || (other == mine && (lane ^ d) < lane);
-        }
-        if (rank >= a.top_groups) {
+      }
+      // estimates nearer than this may be in the wrong order (1e-36: scores that exp2 flushes to zero)
+      const float near0 = a.bias ? 2e-5f : 1e-36f, near1 = a.bias ? 1e-5f : 4e-5f;
+      float b[KEPT];
+      if constexpr (KEPT == 8) {
+        sort8(v);
 #pragma unroll
-          for (int i = 0; i < EPL; ++i) key[i] = 0;
+        for (int i = 0; i < 8; ++i) b[i] = v[i];
+      } else if constexpr (EPL >= 4) {
+#pragma unroll
+        for (int i = 0; i < EPL; i += 4) {
+          sort4(v + i);
+          if (i) merge4(v, v + i);
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) b[i] = v[i];
       } else {
+        if constexpr (EPL == 2) order(v[0], v[1]);
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) keys[warp][lane * EPL + i] = key[i];
-        __syncwarp();
-        uint32_t b1 = 0, b2 = 0;
-        if (lane < a.groups)
-          for (int j = 0; j < per; ++j) {
-            const uint32_t q = keys[warp][lane * per + j];
-            b2 = max(b2, min(b1, q));
-            b1 = max(b1, q);
+        for (int i = 0; i < EPL; ++i) b[i] = v[i];
+      }
+      if (a.groups > 1) {
+        if (!SMEM_GROUPS || a.whole_lanes) {
+          float b1 = b[0], b2 = EPL > 1 ? b[KEPT > 1 ? 1 : 0] : -INFINITY;
+          for (int d = 1; d < group_lanes; d <<= 1) {
+            const float c1 = __shfl_xor_sync(0xffffffffu, b1, d), c2 = __shfl_xor_sync(0xffffffffu, b2, d);
+            b2 = fmaxf(fmaxf(b2, c2), fminf(b1, c1));
+            b1 = fmaxf(b1, c1);
           }
-        __syncwarp();
-        const uint32_t mine = b1 == 0 ? 0u : order_key(order_value(b1) + (b2 ? order_value(b2) : 0.f));
-        int rank = 0;
-        for (int g = 0; g < a.groups; ++g) {
-          const uint32_t other = __shfl_sync(0xffffffffu, mine, g);
-          rank += other > mine || (other == mine && g < lane);
+          const float mine = b1 + (b2 > -INFINITY ? b2 : 0.f);
+          const float near = b1 > -INFINITY ? 2.f * near0 + near1 * (fabsf(b1) + (b2 > -INFINITY ? fabsf(b2) : 0.f)) : 0.f;
+          int rank = 0;  // groups before this one
+          for (int d = group_lanes; d < LANES; d += group_lanes) {
+            const float other = __shfl_xor_sync(0xffffffffu, mine, d);
+            rank += other > mine || (other == mine && (lane ^ d) < lane);
+            redo |= fabsf(other - mine) <= near;
+          }
+          if (rank >= a.top_groups) {
+#pragma unroll
+            for (int i = 0; i < KEPT; ++i) b[i] = -INFINITY;
+          }
+        } else {
+          redo = true;
         }
-        const unsigned keep = __ballot_sync(0xffffffffu, lane < a.groups && rank < a.top_groups);
+      }
+      float slot = -INFINITY;  // lane j: the estimate of slot j
+      const unsigned own = LANES == 32 ? 0u : threadIdx.x & 31 & ~(LANES - 1);
+      for (int j = 0; j < a.k; ++j) {
+        const float top = seg_fmax<LANES>(b[0]);
+        const unsigned all = __ballot_sync(0xffffffffu, b[0] == top);
+        const int who = __ffs(LANES == 32 ? all : all >> own) - 1;
+        if (lane == j) {
+          slot = top;
+          chosen = who * EPL + (int)(__float_as_uint(top) & LOW);
+        }
+        if (lane == who) {
 #pragma unroll
-        for (int i = 0; i < EPL; ++i)
-          if (!((keep >> ((lane * EPL + i) / per & 31)) & 1)) key[i] = 0;
+          for (int i = 0; i + 1 < KEPT; ++i) b[i] = b[i + 1];
+          b[KEPT - 1] = -INFINITY;
+          redo |= KEPT < EPL && b[0] == -INFINITY && top > -INFINITY;  // the list has run out
+        }
+      }
+      if (slot == -INFINITY) chosen = -1;
+      const float best = seg_fmax<LANES>(b[0]);
+      float after = __shfl_down_sync(0xffffffffu, slot, 1, LANES);
+      if (lane + 1 >= a.k) after = best;
+      if (lane < a.k) redo |= slot - after <= near0 + near1 * fabsf(slot);  // no slot: NaN, false
+    }
+
+    if (__any_sync(0xffffffffu, redo)) {
+      uint32_t key[EPL];
+      {
+        float l[EPL];
+        logits(l);
+        if (a.sigmoid) {
+#pragma unroll
+          for (int i = 0; i < EPL; ++i) key[i] = l[i] > -INFINITY ? order_key(logistic(l[i]) + bias[i]) : 0u;
+        } else {
+          if (!estimate) softmax(l);
+#pragma unroll
+          for (int i = 0; i < EPL; ++i) {
+            const float e = l[i] > -INFINITY ? soft_exp(l[i], m) : 0.f;
+            key[i] = l[i] > -INFINITY ? order_key(a.bias ? e / total + bias[i] : e) : 0u;
+          }
+        }
+      }
+      if (a.groups > 1) {
+        if (!SMEM_GROUPS || a.whole_lanes) {
+          uint32_t b1 = 0, b2 = 0;
+#pragma unroll
+          for (int i = 0; i < EPL; ++i) {
+            b2 = max(b2, min(b1, key[i]));
+            b1 = max(b1, key[i]);
+          }
+          for (int d = 1; d < group_lanes; d <<= 1) {
+            const uint32_t c1 = __shfl_xor_sync(0xffffffffu, b1, d), c2 = __shfl_xor_sync(0xffffffffu, b2, d);
+            b2 = max(max(b2, c2), min(b1, c1));
+            b1 = max(b1, c1);
+          }
+          const uint32_t mine = b1 == 0 ? 0u : order_key(order_value(b1) + (b2 ? order_value(b2) : 0.f));
+          int rank = 0;
+          for (int d = group_lanes; d < LANES; d += group_lanes) {
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, d);
+            rank += other > mine || (other == mine && (lane ^ d) < lane);
+          }
+          if (rank >= a.top_groups) {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) key[i] = 0;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < EPL; ++i) keys[warp][lane * EPL + i] = key[i];
+          __syncwarp();
+          uint32_t b1 = 0, b2 = 0;
+          if (lane < a.groups)
+            for (int j = 0; j < per; ++j) {
+              const uint32_t q = keys[warp][lane * per + j];
+              b2 = max(b2, min(b1, q));
+              b1 = max(b1, q);
+            }
+          __syncwarp();
+          const uint32_t mine = b1 == 0 ? 0u : order_key(order_value(b1) + (b2 ? order_value(b2) : 0.f));
+          int rank = 0;
+          for (int g = 0; g < a.groups; ++g) {
+            const uint32_t other = __shfl_sync(0xffffffffu, mine, g);
+            rank += other > mine || (other == mine && g < lane);
+          }
+          const unsigned keep = __ballot_sync(0xffffffffu, lane < a.groups && rank < a.top_groups);
+#pragma unroll
+          for (int i = 0; i < EPL; ++i)
+            if (!((keep >> ((lane * EPL + i) / per & 31)) & 1)) key[i] = 0;
+        }
+      }
+
+      // the lane's two best keys below `under`
+      uint32_t b1, b2;
+      auto refill = [&](uint32_t under) {
+        b1 = b2 = 0;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+          uint32_t p = key[i] ? (key[i] & ~LOW) | (LOW - i) : 0u;
+          p = p < under ? p : 0u;
+          b2 = max(b2, min(b1, p));
+          b1 = max(b1, p);
+        }
+      };
+      refill(0xffffffffu);
+      uint32_t slot = 0;  // lane j: the key of slot j
+      chosen = -1;
+      for (int j = 0; j < a.k; ++j) {
+        const uint32_t top = seg_max<LANES>(b1);
+        const unsigned have = seg_ballot<LANES>((b1 | LOW) == (top | LOW));
+        const int who = __ffs(have) - 1;
+        const uint32_t won = __shfl_sync(0xffffffffu, b1, who, LANES);
+        if (lane == j && won) {
+          slot = won;
+          chosen = who * EPL + (int)(LOW - (won & LOW));
+        }
+        bool spent = false;
+        if (lane == who && won) {
+          b1 = b2;
+          b2 = 0;
+          spent = EPL > 2 && b1 == 0;
+        }
+        if (EPL > 2 && __any_sync(0xffffffffu, spent)) {
+          const uint32_t o1 = b1, o2 = b2;
+          refill(won);
+          if (!spent) b1 = o1, b2 = o2;
+        }
+      }
+      if constexpr (EPL > 1) {
+        const uint32_t next = seg_max<LANES>(b1);  // the best key left
+        float pick = -INFINITY;                    // the exact choice of the slot's expert
+        if (chosen >= 0) {
+          const float l = logit_of(row + chosen);
+          pick = a.sigmoid ? logistic(l) : soft_exp(l, m);
+          if (a.bias) pick = (a.sigmoid ? pick : pick / total) + a.bias[chosen];
+        }
+        const uint32_t after = __shfl_down_sync(0xffffffffu, slot, 1, LANES);
+        const float later = __shfl_down_sync(0xffffffffu, pick, 1, LANES);
+        bool again = false;
+        if (slot) {
+          if (lane + 1 == a.k) again = (slot | LOW) == (next | LOW);
+          else if (lane + 1 < a.k) again = after && (slot | LOW) == (after | LOW) && pick != later;
+        }
+        if (__any_sync(0xffffffffu, again)) {
+          unsigned alive = 0xffffffffu;
+          chosen = -1;
+          for (int j = 0; j < a.k; ++j) {
+            uint32_t best = 0;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) best = max(best, (alive >> i) & 1 ? key[i] : 0u);
+            const uint32_t top = seg_max<LANES>(best);
+            const int who = __ffs(seg_ballot<LANES>(best == top)) - 1;
+            int at = 0;
+            if (lane == who) {
+#pragma unroll
+              for (int i = EPL - 1; i >= 0; --i)
+                if (((alive >> i) & 1) && key[i] == top) at = i;
+              alive &= ~(1u << at);
+            }
+            at = __shfl_sync(0xffffffffu, at, who, LANES);
+            if (lane == j && top) chosen = who * EPL + at;
+          }
+        }
       }
     }
 
-    // the lane's two best keys below `under`
-    uint32_t b1, b2;
-    auto refill = [&](uint32_t under) {
-      b1 = b2 = 0;
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) {
-        uint32_t p = key[i] ? (key[i] & ~LOW) | (LOW - i) : 0u;
-        p = p < under ? p : 0u;
-        b2 = max(b2, min(b1, p));
-        b1 = max(b1, p);
-      }
-    };
-    refill(0xffffffffu);
-    uint32_t slot = 0, next = 0;  // lane j: the key of slot j; the best key left
-    int chosen = -1;              // lane j: the expert of slot j
-    for (int j = 0; j < a.k; ++j) {
-      const uint32_t top = seg_max<LANES>(b1);
-      const unsigned have = seg_ballot<LANES>((b1 | LOW) == (top | LOW));
-      const int who = __ffs(have) - 1;
-      const uint32_t won = LANES == 32 && EPL == 1 ? top : __shfl_sync(0xffffffffu, b1, who, LANES);
-      if (lane == j && won) {
-        slot = won;
-        chosen = who * EPL + (int)(LOW - (won & LOW));
-      }
-      bool spent = false;
-      if (lane == who && won) {
-        b1 = b2;
-        b2 = 0;
-        spent = EPL > 2 && b1 == 0;
-      }
-      if (EPL > 2 && __any_sync(0xffffffffu, spent)) {
-        const uint32_t o1 = b1, o2 = b2;
-        refill(won);
-        if (!spent) b1 = o1, b2 = o2;
-      }
-    }
-    next = seg_max<LANES>(b1);
-
-    float w = 0.f, pick = -INFINITY;
-    auto weigh = [&]() {  // the chosen expert's score (w) and exact choice (pick)
-      w = 0.f;
-      pick = -INFINITY;
-      if (chosen < 0) return;
+    float w = 0.f;
+    if (chosen >= 0) {
       const float l = logit_of(row + chosen);
-      const float raw = a.sigmoid ? logistic(l) : soft_exp(l, m);
-      const float score = a.sigmoid || (a.renorm && !a.bias) ? raw : raw / total;
-      pick = a.bias ? score + a.bias[chosen] : raw;
-      w = a.renorm ? raw : score;
-    };
-    weigh();
-    if (EPL > 1) {
-      const uint32_t after = __shfl_down_sync(0xffffffffu, slot, 1, LANES);
-      const float later = __shfl_down_sync(0xffffffffu, pick, 1, LANES);
-      bool redo = false;
-      if (slot) {
-        if (lane + 1 == a.k) redo = (slot | LOW) == (next | LOW);
-        else if (lane + 1 < a.k) redo = after && (slot | LOW) == (after | LOW) && pick != later;
-      }
-      if (__any_sync(0xffffffffu, redo)) {
-        unsigned alive = 0xffffffffu;
-        chosen = -1;
-        for (int j = 0; j < a.k; ++j) {
-          uint32_t best = 0;
-#pragma unroll
-          for (int i = 0; i < EPL; ++i) best = max(best, (alive >> i) & 1 ? key[i] : 0u);
-          const uint32_t top = seg_max<LANES>(best);
-          const int who = __ffs(seg_ballot<LANES>(best == top)) - 1;
-          int at = 0;
-          if (lane == who) {
-#pragma unroll
-            for (int i = EPL - 1; i >= 0; --i)
-              if (((alive >> i) & 1) && key[i] == top) at = i;
-            alive &= ~(1u << at);
-          }
-          at = __shfl_sync(0xffffffffu, at, who, LANES);
-          if (lane == j && top) chosen = who * EPL + at;
-        }
-        weigh();
-      }
+      w = a.sigmoid ? logistic(l) : soft_exp(l, m);
+      if (!a.sigmoid && !a.renorm) w = w / total;
     }
     if (a.renorm) {
       const float sum = seg_sum<LANES>(w);
@@ -502,8 +658,14 @@ int mhc_route(const void* logits, int64_t ld, mhc_dtype dtype, const float* bias
     for (epl = 1; epl * lanes < E;) epl <<= 1;
   }
   const bool vector = E == epl * lanes && (epl * b) % 16 == 0 && (ld * b) % 16 == 0 && ops_aligned(logits, 16);
+  // Estimates do not help where equal choices are common (16-bit logits without a
+  // bias), where groups need the exact path, and where a lane's list of four would
+  // run out too often: with n lanes in play, about k^4 / (24 n^3) of the tokens.
+  const int64_t n = lanes * top_groups / groups;
+  const bool lists = epl <= 4 || lanes == 8 || (int64_t)k * k * k * k <= 2 * n * n * n;
+  const bool estimate = (b == 4 || bias) && (groups == 1 || whole()) && lists;
   const RouteArgs a = {logits, ld, T, bias, E, groups, top_groups, k, score == MHC_SCORE_SIGMOID, renorm != 0, vector,
-                       whole(), scale, indices, weights, counts, counts ? ws + 16 : nullptr, counts ? ws + 64 : nullptr};
+                       whole(), estimate, scale, indices, weights, counts, counts ? ws + 16 : nullptr, counts ? ws + 64 : nullptr};
   const int64_t tokens = kRouteWarps * (32 / lanes);
   int64_t grid = (T + tokens - 1) / tokens;
   if (grid > (int64_t)sms * kRouteCtas) grid = (int64_t)sms * kRouteCtas;

@@ -409,6 +409,54 @@ def test_route_infinities_and_rows_without_experts():
         assert not bool(w[[0, 3]].any())
 
 
+@pytest.mark.parametrize("E,groups,top,k", [(8, 1, 1, 2), (16, 1, 1, 5), (32, 8, 4, 6), (64, 1, 1, 6), (64, 8, 3, 8), (128, 4, 2, 8),
+                                            (256, 8, 4, 8), (256, 1, 1, 8), (160, 8, 3, 6), (512, 1, 1, 10), (1024, 1, 1, 4)])
+@pytest.mark.parametrize("kind", ["normal", "near", "far", "half"])
+def test_route_choice_is_the_fp32_formula_of_every_token(E, groups, top, k, kind):
+    # 20000 tokens against the formula in fp32 torch operations (the same roundings): logits of N(0, 1.5); many
+    # that differ by a few units in the last place; far ones (tiny scores); bf16 with many equal
+    g = torch.Generator(device="cuda").manual_seed(E + k)
+    T = 20000
+    l = 1.5 * torch.randn(T, E, device="cuda", generator=g)
+    if kind == "near":
+        l = torch.randint(-2, 3, (T, E), device="cuda", generator=g) * 0.5 + 1.25  # not 0: its neighbours below are NaN
+        l = (l.view(torch.int32) + torch.randint(-3, 4, (T, E), device="cuda", generator=g).int()).view(torch.float32)
+    elif kind == "far":
+        l = 25 * l - 40
+    elif kind == "half":
+        l = l.to(BF16)
+    for sigmoid in (True, False):
+        for bias in (None, 0.1 * torch.randn(E, device="cuda", generator=g)):
+            if bias is not None and not sigmoid:
+                continue  # the sum's order is the kernel's own
+            x = l.float()
+            v = 1 / (1 + torch.exp(-x)) if sigmoid else torch.exp(x - x.max(1, keepdim=True).values)
+            sel = v if bias is None else v + bias
+            if groups > 1:
+                best = sel.view(T, groups, -1).sort(dim=2, descending=True).values
+                first = (best[:, :, 0] + best[:, :, 1]).sort(dim=1, descending=True, stable=True).indices[:, :top]
+                keep = torch.zeros(T, groups, dtype=torch.bool, device="cuda").scatter_(1, first, True)
+                sel = torch.where(keep.repeat_interleave(E // groups, 1), sel, -math.inf)
+            want = sel.sort(dim=1, descending=True, stable=True).indices[:, :k]
+            idx, w, c = run_route(l, bias, sigmoid, groups, top, k, False)
+            assert torch.equal(idx.long(), want), (sigmoid, bias is not None, int((idx != want).any(1).sum()))
+            assert torch.equal(c.long(), torch.bincount(want.reshape(-1), minlength=E))
+            if sigmoid:
+                assert torch.equal(w, 2.5 * v.gather(1, want))
+
+
+def test_route_bias_that_is_not_finite():
+    g = gen(4)
+    l, b = normal(g, 300, 64), normal(g, 64)
+    b[[3, 9]], b[20] = -math.inf, math.inf
+    idx, _, _ = run_route(l, b, True, 1, 1, 6, True)
+    want = (1 / (1 + torch.exp(-l.cuda())) + b.cuda()).sort(dim=1, descending=True, stable=True).indices[:, :6]
+    assert torch.equal(idx.long(), want)
+    b[:] = -math.inf
+    idx, w, c = run_route(l, b, True, 1, 1, 6, True)
+    assert bool((idx == -1).all()) and not bool(w.any()) and not bool(c.any())
+
+
 def test_route_strided_unaligned_rows_many_tokens_and_reused_workspace():
     g = gen(11)
     big = normal(g, 5000, 301).cuda()
