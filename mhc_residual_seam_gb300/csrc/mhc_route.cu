@@ -8,7 +8,10 @@ namespace mhc {
 constexpr int kRouteWarps = 4;
 constexpr int kMaxExperts = 1024;
 #ifndef RC
-#define RC 7
+#define RC 30
+#endif
+#ifndef LB
+#define LB 10
 #endif
 constexpr int kRouteCtas = RC;  // per SM
 
@@ -62,6 +65,7 @@ struct RouteArgs {
   int64_t ld, T;
   const float* bias;
   int E, groups, top_groups, k;
+  int log_slots;  // log2 of the slots kept for a token: k, rounded up to a power of two
   bool sigmoid, renorm;
   bool vector;       // rows are 16-byte aligned and no lane has part of its experts
   bool whole_lanes;  // a group is a power of two of whole lanes
@@ -100,6 +104,16 @@ __device__ __forceinline__ uint32_t seg_max(uint32_t x) {
   } else {
 #pragma unroll
     for (int d = LANES / 2; d; d >>= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, d));
+    return x;
+  }
+}
+template <int LANES>
+__device__ __forceinline__ int seg_add(int x) {
+  if constexpr (LANES == 32) {
+    return __reduce_add_sync(0xffffffffu, x);
+  } else {
+#pragma unroll
+    for (int d = LANES / 2; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
     return x;
   }
 }
@@ -167,7 +181,7 @@ __device__ __forceinline__ void sort8(float* v) {
 // estimated scores (the hardware's exp2 and reciprocal, 4 instructions for a
 // sigmoid instead of about 20), with the expert's place in its lane written over the
 // lowest log2(EPL) bits: each lane sorts its best few, and a round is one maximum
-// over the lanes and one ballot for the lane that has it, which moves its list up.
+// over the lanes; the lane that has it writes the slot and moves its list up.
 // An estimate is off by less than 2e-5 of the score (exp2's argument, at most 126,
 // is rounded to 2^-24 of itself, the two approximations to 2^-22, the place to
 // 2^-18), with a bias by less than 1e-6 and 5e-6 of the sum (a score is at most 1 and
@@ -185,21 +199,37 @@ __device__ __forceinline__ void sort8(float* v) {
 // k-th and the next agree above the low bits) is done with whole keys, one scan of
 // all of them per round.
 //
+// A warp takes as many tokens in turn as it has lanes for their k slots; checks,
+// weights and stores are then one slot per lane.
+//
 // Bound by instruction issue (the floor of T = 131072, E = 256 in fp32 is 21 us of
 // HBM).
 template <typename T, int EPL, int LANES>
-__global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs a) {
+__global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? LB : 1) route_kernel(const RouteArgs a) {
   constexpr uint32_t LOW = EPL - 1;
   constexpr int TOKENS = 32 / LANES;
   constexpr bool SMEM_GROUPS = LANES == 32;  // groups that do not fall on whole lanes
   __shared__ uint32_t keys[SMEM_GROUPS ? kRouteWarps : 1][SMEM_GROUPS ? EPL * 32 : 1];
   __shared__ int load[EPL * LANES];
+  // A warp's batch: 32 slots of 32 >> log_slots tokens.  chosen: the expert; value: its
+  // estimate; left: the best estimate left over; won: how
+  // many lanes' experts the slots took; soft: the row's maximum and sum.
+  __shared__ int chosen_[kRouteWarps][32];
+  __shared__ float value_[kRouteWarps][32], left_[kRouteWarps][32];
+  __shared__ int won_[kRouteWarps][32];
+  __shared__ float2 soft_[kRouteWarps][32];
   const int lane = threadIdx.x & (LANES - 1), warp = threadIdx.x >> 5;
   const int sub = (threadIdx.x & 31) / LANES;
+  int* const chosen = chosen_[warp];
+  float* const value = value_[warp];
+  float* const left = left_[warp];
+  int* const won = won_[warp];
+  float2* const soft = soft_[warp];
   for (int e = threadIdx.x; e < EPL * LANES; e += blockDim.x) load[e] = 0;
   __syncthreads();
   const int per = a.E / a.groups;
   const int group_lanes = per / EPL;  // where groups fall on whole lanes
+  const int slots = 1 << a.log_slots, batch = 32 >> a.log_slots;
   float bias[EPL];
   bool finite = true;
 #pragma unroll
@@ -209,14 +239,39 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs
     finite &= fabsf(bias[i]) < 3e38f;
   }
   const bool estimate = a.estimate && __all_sync(0xffffffffu, finite);
-  for (int64_t base = ((int64_t)blockIdx.x * kRouteWarps + warp) * TOKENS; base < a.T;
-       base += (int64_t)gridDim.x * kRouteWarps * TOKENS) {
-    const bool real = base + sub < a.T;
-    const int64_t t = real ? base + sub : a.T - 1;  // a segment without a token repeats the last one's work
-    const T* row = static_cast<const T*>(a.logits) + t * a.ld;
-    float m = -INFINITY, total = 0.f;
-    int chosen = -1;  // lane j: the expert of slot j
-    auto logits = [&](float* l) {
+  const bool need_sum = !a.sigmoid && (a.bias || !a.renorm);
+  // estimates nearer than this may be in the wrong order (1e-36: scores that exp2 flushes to zero)
+  const float near0 = a.bias ? 2e-5f : 1e-36f, near1 = a.bias ? 1e-5f : 4e-5f;
+
+  // The lane's logits of the next two passes come through shared memory of its own.
+  constexpr int PIECES = EPL * (int)sizeof(T) / 16;  // 16-byte pieces of a lane's logits
+  constexpr bool RING = PIECES >= 1 && EPL <= 16;
+  __shared__ uint4 ring_[RING ? kRouteWarps : 1][RING ? 2 : 1][RING ? PIECES * 32 : 1];
+  const bool ring = RING && a.vector && estimate;
+  const uint32_t ring_at = smem_of(&ring_[RING ? warp : 0][0][0]) + (threadIdx.x & 31) * 16;
+  const int64_t stride = (int64_t)gridDim.x * kRouteWarps * batch;
+  auto fetch = [&](int64_t first, int stage) {  // the pass whose first token is `first`
+    if constexpr (RING) {
+      if (ring && first < a.T) {
+        const int64_t t = first + sub < a.T ? first + sub : a.T - 1;
+        const char* p = reinterpret_cast<const char*>(static_cast<const T*>(a.logits) + t * a.ld + lane * EPL);
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) cp_async16(ring_at + (stage * PIECES + i) * 512, p + i * 16);
+      }
+      cp_async_commit();
+    }
+  };
+  const int64_t start = ((int64_t)blockIdx.x * kRouteWarps + warp) * batch;
+  fetch(start, 0);
+  fetch(TOKENS < batch ? start + TOKENS : start + stride, 1);
+  int stage = 0;
+  for (int64_t base = start; base < a.T; base += stride) {
+    // the tokens of pass `it`: a segment without one repeats the last token's work
+    auto token = [&](int it) {
+      const int64_t t = base + it * TOKENS + sub;
+      return t < a.T ? t : a.T - 1;
+    };
+    auto logits = [&](const T* row, float* l) {
       if (a.vector) {
         load_logits<T, EPL>(row + lane * EPL, l);
       } else {
@@ -225,22 +280,55 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs
       }
     };
     auto softmax = [&](const float* l) {  // the row's maximum, and its sum where a score needs it
+      float2 ms = make_float2(-INFINITY, 0.f);
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) m = fmaxf(m, l[i]);  // fmaxf passes NaN over
-      m = seg_max<LANES>(m);
-      total = 0.f;
-      if (a.bias || !a.renorm) {
+      for (int i = 0; i < EPL; ++i) ms.x = fmaxf(ms.x, l[i]);  // fmaxf passes NaN over
+      ms.x = seg_fmax<LANES>(ms.x);
+      if (need_sum) {
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) total += l[i] > -INFINITY ? soft_exp(l[i], m) : 0.f;
-        total = seg_sum<LANES>(total);
+        for (int i = 0; i < EPL; ++i) ms.y += l[i] > -INFINITY ? soft_exp(l[i], ms.x) : 0.f;
+        ms.y = seg_sum<LANES>(ms.y);
       }
+      return ms;
     };
+    const int64_t rest = a.T - base;
+    const int passes = (int)((rest < batch ? rest : batch) + TOKENS - 1) / TOKENS;
+    unsigned again = estimate ? 0u : 0xffffffffu;  // passes to choose exactly
+    __syncwarp();
+    chosen[threadIdx.x & 31] = -1;
+    value[threadIdx.x & 31] = -INFINITY;
+    __syncwarp();
 
-    bool redo = !estimate;
-    if (estimate) {
+    for (int it = 0; estimate && it < passes; ++it) {
       constexpr int KEPT = EPL <= 4 ? EPL : LANES == 8 ? 8 : 4;  // how many of its best a lane keeps sorted
+      const int first = (it * TOKENS + sub) << a.log_slots;
       float v[EPL];
-      logits(v);
+      bool redo = false;
+      if (ring) {
+        if constexpr (RING) {
+          cp_async_wait<1>();
+#pragma unroll
+          for (int i = 0; i < PIECES; ++i) {
+            const uint4 q = lds16(ring_at + (stage * PIECES + i) * 512);
+            if constexpr (sizeof(T) == 4) {
+              v[4 * i] = __uint_as_float(q.x), v[4 * i + 1] = __uint_as_float(q.y);
+              v[4 * i + 2] = __uint_as_float(q.z), v[4 * i + 3] = __uint_as_float(q.w);
+            } else {
+              Raw8<T> r;
+              r.q[0] = q;
+              const Vec8 x = unpack(r);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) v[8 * i + 2 * e] = x.p[e].x, v[8 * i + 2 * e + 1] = x.p[e].y;
+            }
+          }
+          // two passes on: in this batch, or in the warp's next
+          const int on = (it + 2) * TOKENS;
+          fetch(on < batch ? base + on : base + stride + (on - batch), stage);
+          stage ^= 1;
+        }
+      } else {
+        logits(static_cast<const T*>(a.logits) + token(it) * a.ld, v);
+      }
       if (a.sigmoid) {
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
@@ -249,9 +337,10 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs
           v[i] = v[i] > -INFINITY ? p : -INFINITY;
         }
       } else {
-        softmax(v);
-        redo = !(fabsf(m) < 3e38f);
-        const float c = m * 1.44269504f, share = a.bias ? rcp_approx(total) : 1.f;
+        const float2 ms = softmax(v);
+        if (lane == 0) soft[it * TOKENS + sub] = ms;
+        redo = !(fabsf(ms.x) < 3e38f);
+        const float c = ms.x * 1.44269504f, share = a.bias ? rcp_approx(ms.y) : 1.f;
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
           const float s = fmaf(ex2_approx(fmaf(v[i], 1.44269504f, -c)), share, bias[i]);
@@ -259,8 +348,6 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs
           v[i] = v[i] > -INFINITY ? p : -INFINITY;
         }
       }
-      // estimates nearer than this may be in the wrong order (1e-36: scores that exp2 flushes to zero)
-      const float near0 = a.bias ? 2e-5f : 1e-36f, near1 = a.bias ? 1e-5f : 4e-5f;
       float b[KEPT];
       if constexpr (KEPT == 8) {
         sort8(v);
@@ -279,64 +366,91 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs
 #pragma unroll
         for (int i = 0; i < EPL; ++i) b[i] = v[i];
       }
-      if (a.groups > 1) {
-        if (!SMEM_GROUPS || a.whole_lanes) {
-          float b1 = b[0], b2 = EPL > 1 ? b[KEPT > 1 ? 1 : 0] : -INFINITY;
-          for (int d = 1; d < group_lanes; d <<= 1) {
-            const float c1 = __shfl_xor_sync(0xffffffffu, b1, d), c2 = __shfl_xor_sync(0xffffffffu, b2, d);
-            b2 = fmaxf(fmaxf(b2, c2), fminf(b1, c1));
-            b1 = fmaxf(b1, c1);
-          }
-          const float mine = b1 + (b2 > -INFINITY ? b2 : 0.f);
-          const float near = b1 > -INFINITY ? 2.f * near0 + near1 * (fabsf(b1) + (b2 > -INFINITY ? fabsf(b2) : 0.f)) : 0.f;
-          int rank = 0;  // groups before this one
-          for (int d = group_lanes; d < LANES; d += group_lanes) {
-            const float other = __shfl_xor_sync(0xffffffffu, mine, d);
-            rank += other > mine || (other == mine && (lane ^ d) < lane);
-            redo |= fabsf(other - mine) <= near;
-          }
-          if (rank >= a.top_groups) {
+      if (a.groups > 1) {  // on whole lanes
+        float b1 = b[0], b2 = EPL > 1 ? b[KEPT > 1 ? 1 : 0] : -INFINITY;
+        for (int d = 1; d < group_lanes; d <<= 1) {
+          const float c1 = __shfl_xor_sync(0xffffffffu, b1, d), c2 = __shfl_xor_sync(0xffffffffu, b2, d);
+          b2 = fmaxf(fmaxf(b2, c2), fminf(b1, c1));
+          b1 = fmaxf(b1, c1);
+        }
+        const bool two = b2 > -INFINITY;
+        const float mine = two ? b1 + b2 : b1;
+        const float near = b1 > -INFINITY ? 2.f * near0 + near1 * (fabsf(b1) + (two ? fabsf(b2) : 0.f)) : 0.f;
+        // the best groups one by one; then the best one left has to be clearly behind
+        float open = mine, last = -INFINITY;
+        for (int n = 0; n < a.top_groups; ++n) {
+          last = seg_fmax<LANES>(open);
+          open = open == last ? -INFINITY : open;
+        }
+        const float behind = seg_fmax<LANES>(open);
+        const bool keep = open == -INFINITY;
+        redo |= keep && mine == last && mine - behind <= near;
+        if constexpr (LANES == 32) redo |= __popc(__ballot_sync(0xffffffffu, keep)) > a.top_groups * group_lanes && last > -INFINITY;
+        else redo |= seg_add<LANES>(keep) > a.top_groups * group_lanes && last > -INFINITY;
+        if (!keep) {
 #pragma unroll
-            for (int i = 0; i < KEPT; ++i) b[i] = -INFINITY;
-          }
-        } else {
-          redo = true;
+          for (int i = 0; i < KEPT; ++i) b[i] = -INFINITY;
         }
       }
-      float slot = -INFINITY;  // lane j: the estimate of slot j
-      const unsigned own = LANES == 32 ? 0u : threadIdx.x & 31 & ~(LANES - 1);
+      const bool full = KEPT < EPL && b[KEPT - 1] > -INFINITY;
+      int wins = 0;
       for (int j = 0; j < a.k; ++j) {
         const float top = seg_fmax<LANES>(b[0]);
-        const unsigned all = __ballot_sync(0xffffffffu, b[0] == top);
-        const int who = __ffs(LANES == 32 ? all : all >> own) - 1;
-        if (lane == j) {
-          slot = top;
-          chosen = who * EPL + (int)(__float_as_uint(top) & LOW);
+        const bool win = b[0] == top && top > -INFINITY;  // one lane, or a tie: then there are more wins than slots
+        if (win) {
+          chosen[first + j] = lane * EPL | (int)(__float_as_uint(top) & LOW);
+          value[first + j] = top;
         }
-        if (lane == who) {
+        wins += win;
 #pragma unroll
-          for (int i = 0; i + 1 < KEPT; ++i) b[i] = b[i + 1];
-          b[KEPT - 1] = -INFINITY;
-          redo |= KEPT < EPL && b[0] == -INFINITY && top > -INFINITY;  // the list has run out
-        }
+        for (int i = 0; i + 1 < KEPT; ++i) b[i] = win ? b[i + 1] : b[i];
+        b[KEPT - 1] = win ? -INFINITY : b[KEPT - 1];
       }
-      if (slot == -INFINITY) chosen = -1;
       const float best = seg_fmax<LANES>(b[0]);
-      float after = __shfl_down_sync(0xffffffffu, slot, 1, LANES);
-      if (lane + 1 >= a.k) after = best;
-      if (lane < a.k) redo |= slot - after <= near0 + near1 * fabsf(slot);  // no slot: NaN, false
+      wins = seg_add<LANES>(wins);
+      if (lane == 0) left[it * TOKENS + sub] = best, won[it * TOKENS + sub] = wins;
+      redo |= full && b[0] == -INFINITY;  // a list has run out
+      if (__any_sync(0xffffffffu, redo)) again |= 1u << it;
+    }
+    __syncwarp();
+
+    // One slot per lane from here: slot `at` of token base + tok.
+    const int tok = (threadIdx.x & 31) >> a.log_slots, at = threadIdx.x & (slots - 1);
+    const bool mine = at < a.k && base + tok < a.T;
+    if (estimate) {
+      bool redo = false, filled = false;
+      if (mine) {
+        const float v = value[threadIdx.x & 31];
+        const float after = at + 1 < a.k ? value[(threadIdx.x & 31) + 1] : left[tok];
+        redo = v - after <= near0 + near1 * fabsf(v);  // no slot: NaN, false
+        filled = v > -INFINITY;
+      }
+      const unsigned f = __ballot_sync(0xffffffffu, filled) >> (threadIdx.x & 31 & ~(slots - 1));
+      redo |= mine && __popc(slots == 32 ? f : f & ((1u << slots) - 1)) != won[tok];
+      const unsigned r = __ballot_sync(0xffffffffu, redo);
+      for (int it = 0; r && it < passes; ++it) {
+        const int bits = TOKENS << a.log_slots;  // slots of a pass
+        if ((r >> (it * bits)) & (bits == 32 ? 0xffffffffu : (1u << bits) - 1)) again |= 1u << it;
+      }
+      __syncwarp();
     }
 
-    if (__any_sync(0xffffffffu, redo)) {
+    for (int it = 0; it < passes; ++it) {
+      if (!((again >> it) & 1)) continue;
+      const T* row = static_cast<const T*>(a.logits) + token(it) * a.ld;
+      const int first = (it * TOKENS + sub) << a.log_slots;
       uint32_t key[EPL];
+      float m = 0.f, total = 1.f;
       {
         float l[EPL];
-        logits(l);
+        logits(row, l);
         if (a.sigmoid) {
 #pragma unroll
           for (int i = 0; i < EPL; ++i) key[i] = l[i] > -INFINITY ? order_key(logistic(l[i]) + bias[i]) : 0u;
         } else {
-          if (!estimate) softmax(l);
+          const float2 ms = softmax(l);
+          m = ms.x, total = ms.y;
+          if (lane == 0) soft[it * TOKENS + sub] = ms;
 #pragma unroll
           for (int i = 0; i < EPL; ++i) {
             const float e = l[i] > -INFINITY ? soft_exp(l[i], m) : 0.f;
@@ -357,11 +471,11 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs
             b2 = max(max(b2, c2), min(b1, c1));
             b1 = max(b1, c1);
           }
-          const uint32_t mine = b1 == 0 ? 0u : order_key(order_value(b1) + (b2 ? order_value(b2) : 0.f));
+          const uint32_t sum = b1 == 0 ? 0u : order_key(order_value(b1) + (b2 ? order_value(b2) : 0.f));
           int rank = 0;
           for (int d = group_lanes; d < LANES; d += group_lanes) {
-            const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, d);
-            rank += other > mine || (other == mine && (lane ^ d) < lane);
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, sum, d);
+            rank += other > sum || (other == sum && (lane ^ d) < lane);
           }
           if (rank >= a.top_groups) {
 #pragma unroll
@@ -379,11 +493,11 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs
               b1 = max(b1, q);
             }
           __syncwarp();
-          const uint32_t mine = b1 == 0 ? 0u : order_key(order_value(b1) + (b2 ? order_value(b2) : 0.f));
+          const uint32_t sum = b1 == 0 ? 0u : order_key(order_value(b1) + (b2 ? order_value(b2) : 0.f));
           int rank = 0;
           for (int g = 0; g < a.groups; ++g) {
-            const uint32_t other = __shfl_sync(0xffffffffu, mine, g);
-            rank += other > mine || (other == mine && g < lane);
+            const uint32_t other = __shfl_sync(0xffffffffu, sum, g);
+            rank += other > sum || (other == sum && g < lane);
           }
           const unsigned keep = __ballot_sync(0xffffffffu, lane < a.groups && rank < a.top_groups);
 #pragma unroll
@@ -406,7 +520,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs
       };
       refill(0xffffffffu);
       uint32_t slot = 0;  // lane j: the key of slot j
-      chosen = -1;
+      int expert = -1;    // and its expert
       for (int j = 0; j < a.k; ++j) {
         const uint32_t top = seg_max<LANES>(b1);
         const unsigned have = seg_ballot<LANES>((b1 | LOW) == (top | LOW));
@@ -414,7 +528,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs
         const uint32_t won = __shfl_sync(0xffffffffu, b1, who, LANES);
         if (lane == j && won) {
           slot = won;
-          chosen = who * EPL + (int)(LOW - (won & LOW));
+          expert = who * EPL + (int)(LOW - (won & LOW));
         }
         bool spent = false;
         if (lane == who && won) {
@@ -431,57 +545,66 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs
       if constexpr (EPL > 1) {
         const uint32_t next = seg_max<LANES>(b1);  // the best key left
         float pick = -INFINITY;                    // the exact choice of the slot's expert
-        if (chosen >= 0) {
-          const float l = logit_of(row + chosen);
+        if (expert >= 0) {
+          const float l = logit_of(row + expert);
           pick = a.sigmoid ? logistic(l) : soft_exp(l, m);
-          if (a.bias) pick = (a.sigmoid ? pick : pick / total) + a.bias[chosen];
+          if (a.bias) pick = (a.sigmoid ? pick : pick / total) + a.bias[expert];
         }
         const uint32_t after = __shfl_down_sync(0xffffffffu, slot, 1, LANES);
         const float later = __shfl_down_sync(0xffffffffu, pick, 1, LANES);
-        bool again = false;
+        bool unsure = false;
         if (slot) {
-          if (lane + 1 == a.k) again = (slot | LOW) == (next | LOW);
-          else if (lane + 1 < a.k) again = after && (slot | LOW) == (after | LOW) && pick != later;
+          if (lane + 1 == a.k) unsure = (slot | LOW) == (next | LOW);
+          else if (lane + 1 < a.k) unsure = after && (slot | LOW) == (after | LOW) && pick != later;
         }
-        if (__any_sync(0xffffffffu, again)) {
+        if (__any_sync(0xffffffffu, unsure)) {
           unsigned alive = 0xffffffffu;
-          chosen = -1;
+          expert = -1;
           for (int j = 0; j < a.k; ++j) {
             uint32_t best = 0;
 #pragma unroll
             for (int i = 0; i < EPL; ++i) best = max(best, (alive >> i) & 1 ? key[i] : 0u);
             const uint32_t top = seg_max<LANES>(best);
             const int who = __ffs(seg_ballot<LANES>(best == top)) - 1;
-            int at = 0;
+            int place = 0;
             if (lane == who) {
 #pragma unroll
               for (int i = EPL - 1; i >= 0; --i)
-                if (((alive >> i) & 1) && key[i] == top) at = i;
-              alive &= ~(1u << at);
+                if (((alive >> i) & 1) && key[i] == top) place = i;
+              alive &= ~(1u << place);
             }
-            at = __shfl_sync(0xffffffffu, at, who, LANES);
-            if (lane == j && top) chosen = who * EPL + at;
+            place = __shfl_sync(0xffffffffu, place, who, LANES);
+            if (lane == j && top) expert = who * EPL + place;
           }
         }
       }
+      if (lane < a.k) chosen[first + lane] = expert;
     }
+    __syncwarp();
 
+    const int e = mine ? chosen[threadIdx.x & 31] : -1;
     float w = 0.f;
-    if (chosen >= 0) {
-      const float l = logit_of(row + chosen);
-      w = a.sigmoid ? logistic(l) : soft_exp(l, m);
-      if (!a.sigmoid && !a.renorm) w = w / total;
+    if (e >= 0) {
+      const float l = logit_of(static_cast<const T*>(a.logits) + (base + tok) * a.ld + e);
+      if (a.sigmoid) {
+        w = logistic(l);
+      } else {
+        const float2 ms = soft[tok];
+        w = soft_exp(l, ms.x);
+        if (!a.renorm) w = w / ms.y;
+      }
+      atomicAdd(&load[e], 1);
     }
     if (a.renorm) {
-      const float sum = seg_sum<LANES>(w);
+      float sum = w;
+      for (int d = slots >> 1; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
       w = sum > 0.f ? a.scale * w / sum : 0.f;
     } else {
       w *= a.scale;
     }
-    if (real && lane < a.k) {
-      if (chosen >= 0) atomicAdd(&load[chosen], 1);
-      a.indices[t * a.k + lane] = chosen;
-      a.weights[t * a.k + lane] = w;
+    if (mine) {
+      a.indices[(base + tok) * a.k + at] = e;
+      a.weights[(base + tok) * a.k + at] = w;
     }
   }
   if (!a.counts) return;
@@ -621,6 +744,7 @@ int mhc_route(const void* logits, int64_t ld, mhc_dtype dtype, const float* bias
   if (groups < 1 || groups > 32 || E % groups != 0 || top_groups < 1 || top_groups > groups)
     return ops_fail(MHC_ERR_SHAPE, "need 1 <= groups <= 32, E a multiple of groups and 1 <= top_groups <= groups");
   if (k > E / groups * top_groups) return ops_fail(MHC_ERR_SHAPE, "k is more than the experts of top_groups groups");
+  if (top_groups == groups) groups = top_groups = 1;  // no group is left out
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (!ops_aligned(counts, 4)) return ops_fail(MHC_ERR_ALIGN, "counts is not aligned");
   if (T == 0) return counts ? ops_cuda(cudaMemsetAsync(counts, 0, (size_t)E * 4, s), "cudaMemsetAsync") : MHC_OK;
@@ -664,9 +788,13 @@ int mhc_route(const void* logits, int64_t ld, mhc_dtype dtype, const float* bias
   const int64_t n = lanes * top_groups / groups;
   const bool lists = epl <= 4 || lanes == 8 || (int64_t)k * k * k * k <= 2 * n * n * n;
   const bool estimate = (b == 4 || bias) && (groups == 1 || whole()) && lists;
-  const RouteArgs a = {logits, ld, T, bias, E, groups, top_groups, k, score == MHC_SCORE_SIGMOID, renorm != 0, vector,
+  int log_slots = 0;
+  while ((1 << log_slots) < k) ++log_slots;
+  // tokens that a warp takes in turn cost latency: only as many as leave two warps per scheduler
+  while ((32 >> log_slots) > 32 / lanes && T < (int64_t)sms * 8 * (32 >> log_slots)) ++log_slots;
+  const RouteArgs a = {logits, ld, T, bias, E, groups, top_groups, k, log_slots, score == MHC_SCORE_SIGMOID, renorm != 0, vector,
                        whole(), estimate, scale, indices, weights, counts, counts ? ws + 16 : nullptr, counts ? ws + 64 : nullptr};
-  const int64_t tokens = kRouteWarps * (32 / lanes);
+  const int64_t tokens = kRouteWarps * (32 >> log_slots);
   int64_t grid = (T + tokens - 1) / tokens;
   if (grid > (int64_t)sms * kRouteCtas) grid = (int64_t)sms * kRouteCtas;
   MHC_BY_DTYPE(dtype, D, { MHC_BY_LANES(epl, lanes, { route_kernel<D, N, L><<<(unsigned)grid, kRouteWarps * 32, 0, s>>>(a); }) });
