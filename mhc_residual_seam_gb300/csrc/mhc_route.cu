@@ -7,13 +7,10 @@ namespace mhc {
 
 constexpr int kRouteWarps = 4;
 constexpr int kMaxExperts = 1024;
-#ifndef RC
-#define RC 30
-#endif
-#ifndef LB
-#define LB 10
-#endif
-constexpr int kRouteCtas = RC;  // per SM
+// CTAs per SM of the choice: eight are resident (64 registers a thread), and twice as
+// many let an SM that gets through faster take more of them (T = 131072: 81 us; ten
+// resident and ten in all 87).
+constexpr int kRouteResident = 8, kRouteCtas = 16;
 
 template <typename T>
 __device__ __forceinline__ float logit_of(const T* p) {
@@ -62,7 +59,7 @@ __device__ __forceinline__ float order_value(uint32_t k) {
 
 struct RouteArgs {
   const void* logits;
-  int64_t ld, T;
+  uint32_t ld_bytes, T;  // a row's bytes and the tokens: both below 2^31
   const float* bias;
   int E, groups, top_groups, k;
   int log_slots;  // log2 of the slots kept for a token: k, rounded up to a power of two
@@ -205,26 +202,24 @@ __device__ __forceinline__ void sort8(float* v) {
 // Bound by instruction issue (the floor of T = 131072, E = 256 in fp32 is 21 us of
 // HBM).
 template <typename T, int EPL, int LANES>
-__global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? LB : 1) route_kernel(const RouteArgs a) {
+__global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? kRouteResident : 1) route_kernel(const RouteArgs a) {
   constexpr uint32_t LOW = EPL - 1;
   constexpr int TOKENS = 32 / LANES;
   constexpr bool SMEM_GROUPS = LANES == 32;  // groups that do not fall on whole lanes
   __shared__ uint32_t keys[SMEM_GROUPS ? kRouteWarps : 1][SMEM_GROUPS ? EPL * 32 : 1];
   __shared__ int load[EPL * LANES];
-  // A warp's batch: 32 slots of 32 >> log_slots tokens.  chosen: the expert; value: its
-  // estimate; left: the best estimate left over; won: how
-  // many lanes' experts the slots took; soft: the row's maximum and sum.
-  __shared__ int chosen_[kRouteWarps][32];
-  __shared__ float value_[kRouteWarps][32], left_[kRouteWarps][32];
-  __shared__ int won_[kRouteWarps][32];
+  // A warp's batch: 32 slots of 32 >> log_slots tokens.  slot: the expert and its
+  // estimate; rest: a token's best estimate left over and how many lanes' experts its
+  // slots took; soft: its row's maximum and sum.
+  __shared__ int2 slot_[kRouteWarps][32], rest_[kRouteWarps][32];
   __shared__ float2 soft_[kRouteWarps][32];
   const int lane = threadIdx.x & (LANES - 1), warp = threadIdx.x >> 5;
   const int sub = (threadIdx.x & 31) / LANES;
-  int* const chosen = chosen_[warp];
-  float* const value = value_[warp];
-  float* const left = left_[warp];
-  int* const won = won_[warp];
+  int2* const slot = slot_[warp];
+  int2* const rest = rest_[warp];
   float2* const soft = soft_[warp];
+  const int id = threadIdx.x & 31;
+  const char* const rows = static_cast<const char*>(a.logits);
   for (int e = threadIdx.x; e < EPL * LANES; e += blockDim.x) load[e] = 0;
   __syncthreads();
   const int per = a.E / a.groups;
@@ -249,28 +244,25 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? LB : 1) route_ker
   __shared__ uint4 ring_[RING ? kRouteWarps : 1][RING ? 2 : 1][RING ? PIECES * 32 : 1];
   const bool ring = RING && a.vector && estimate;
   const uint32_t ring_at = smem_of(&ring_[RING ? warp : 0][0][0]) + (threadIdx.x & 31) * 16;
-  const int64_t stride = (int64_t)gridDim.x * kRouteWarps * batch;
-  auto fetch = [&](int64_t first, int stage) {  // the pass whose first token is `first`
+  const uint32_t stride = gridDim.x * kRouteWarps * batch;
+  auto row_of = [&](uint32_t first) {  // a segment without a token repeats the last token's work
+    return rows + (uint64_t)(TOKENS == 1 ? first : min(first + sub, a.T - 1)) * a.ld_bytes;
+  };
+  auto fetch = [&](uint32_t first, int stage) {  // the pass whose first token is `first`
     if constexpr (RING) {
       if (ring && first < a.T) {
-        const int64_t t = first + sub < a.T ? first + sub : a.T - 1;
-        const char* p = reinterpret_cast<const char*>(static_cast<const T*>(a.logits) + t * a.ld + lane * EPL);
+        const char* p = row_of(first) + lane * EPL * sizeof(T);
 #pragma unroll
         for (int i = 0; i < PIECES; ++i) cp_async16(ring_at + (stage * PIECES + i) * 512, p + i * 16);
       }
       cp_async_commit();
     }
   };
-  const int64_t start = ((int64_t)blockIdx.x * kRouteWarps + warp) * batch;
+  const uint32_t start = (blockIdx.x * kRouteWarps + warp) * batch;
   fetch(start, 0);
   fetch(TOKENS < batch ? start + TOKENS : start + stride, 1);
   int stage = 0;
-  for (int64_t base = start; base < a.T; base += stride) {
-    // the tokens of pass `it`: a segment without one repeats the last token's work
-    auto token = [&](int it) {
-      const int64_t t = base + it * TOKENS + sub;
-      return t < a.T ? t : a.T - 1;
-    };
+  for (uint32_t base = start; base < a.T; base += stride) {
     auto logits = [&](const T* row, float* l) {
       if (a.vector) {
         load_logits<T, EPL>(row + lane * EPL, l);
@@ -291,12 +283,10 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? LB : 1) route_ker
       }
       return ms;
     };
-    const int64_t rest = a.T - base;
-    const int passes = (int)((rest < batch ? rest : batch) + TOKENS - 1) / TOKENS;
-    unsigned again = estimate ? 0u : 0xffffffffu;  // passes to choose exactly
+    const int passes = ((int)min(a.T - base, (uint32_t)batch) + TOKENS - 1) / TOKENS;
+    unsigned again = 0;  // passes to choose exactly
     __syncwarp();
-    chosen[threadIdx.x & 31] = -1;
-    value[threadIdx.x & 31] = -INFINITY;
+    slot[id] = make_int2(-1, __float_as_int(-INFINITY));
     __syncwarp();
 
     for (int it = 0; estimate && it < passes; ++it) {
@@ -327,14 +317,23 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? LB : 1) route_ker
           stage ^= 1;
         }
       } else {
-        logits(static_cast<const T*>(a.logits) + token(it) * a.ld, v);
+        logits(reinterpret_cast<const T*>(row_of(base + it * TOKENS)), v);
+      }
+      // logits that are not finite are rare: found by 0 * l on the FMA pipe, masked in a branch
+      float odd = 0.f;
+      unsigned dead = 0;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) odd = fmaf(v[i], 0.f, odd);
+      const bool masks = __any_sync(0xffffffffu, !(odd == 0.f));
+      if (masks) {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) dead |= (v[i] > -INFINITY ? 0u : 1u) << i;
       }
       if (a.sigmoid) {
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
           const float s = rcp_approx(1.0f + ex2_approx(v[i] * -1.44269504f)) + bias[i];
-          const float p = __uint_as_float((__float_as_uint(s) & ~LOW) | i);
-          v[i] = v[i] > -INFINITY ? p : -INFINITY;
+          v[i] = __uint_as_float((__float_as_uint(s) & ~LOW) | i);
         }
       } else {
         const float2 ms = softmax(v);
@@ -344,9 +343,12 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? LB : 1) route_ker
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
           const float s = fmaf(ex2_approx(fmaf(v[i], 1.44269504f, -c)), share, bias[i]);
-          const float p = __uint_as_float((__float_as_uint(s) & ~LOW) | i);
-          v[i] = v[i] > -INFINITY ? p : -INFINITY;
+          v[i] = __uint_as_float((__float_as_uint(s) & ~LOW) | i);
         }
+      }
+      if (masks) {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) v[i] = (dead >> i) & 1 ? -INFINITY : v[i];
       }
       float b[KEPT];
       if constexpr (KEPT == 8) {
@@ -396,11 +398,8 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? LB : 1) route_ker
       int wins = 0;
       for (int j = 0; j < a.k; ++j) {
         const float top = seg_fmax<LANES>(b[0]);
-        const bool win = b[0] == top && top > -INFINITY;  // one lane, or a tie: then there are more wins than slots
-        if (win) {
-          chosen[first + j] = lane * EPL | (int)(__float_as_uint(top) & LOW);
-          value[first + j] = top;
-        }
+        const bool win = b[0] == top;  // one lane, or a tie (or no expert left): then wins and slots differ
+        if (win) slot[first + j] = make_int2(lane * EPL | (int)(__float_as_uint(top) & LOW), __float_as_int(top));
         wins += win;
 #pragma unroll
         for (int i = 0; i + 1 < KEPT; ++i) b[i] = win ? b[i + 1] : b[i];
@@ -408,36 +407,31 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? LB : 1) route_ker
       }
       const float best = seg_fmax<LANES>(b[0]);
       wins = seg_add<LANES>(wins);
-      if (lane == 0) left[it * TOKENS + sub] = best, won[it * TOKENS + sub] = wins;
+      if (lane == 0) rest[it * TOKENS + sub] = make_int2(__float_as_int(best), wins);
       redo |= full && b[0] == -INFINITY;  // a list has run out
-      if (__any_sync(0xffffffffu, redo)) again |= 1u << it;
+      again |= (unsigned)redo << it;
     }
     __syncwarp();
 
     // One slot per lane from here: slot `at` of token base + tok.
-    const int tok = (threadIdx.x & 31) >> a.log_slots, at = threadIdx.x & (slots - 1);
+    const int tok = id >> a.log_slots, at = id & (slots - 1);
     const bool mine = at < a.k && base + tok < a.T;
     if (estimate) {
-      bool redo = false, filled = false;
-      if (mine) {
-        const float v = value[threadIdx.x & 31];
-        const float after = at + 1 < a.k ? value[(threadIdx.x & 31) + 1] : left[tok];
-        redo = v - after <= near0 + near1 * fabsf(v);  // no slot: NaN, false
-        filled = v > -INFINITY;
-      }
-      const unsigned f = __ballot_sync(0xffffffffu, filled) >> (threadIdx.x & 31 & ~(slots - 1));
-      redo |= mine && __popc(slots == 32 ? f : f & ((1u << slots) - 1)) != won[tok];
-      const unsigned r = __ballot_sync(0xffffffffu, redo);
-      for (int it = 0; r && it < passes; ++it) {
-        const int bits = TOKENS << a.log_slots;  // slots of a pass
-        if ((r >> (it * bits)) & (bits == 32 ? 0xffffffffu : (1u << bits) - 1)) again |= 1u << it;
-      }
-      __syncwarp();
+      const int2 r = rest[tok];
+      const float v = __int_as_float(slot[id].y);
+      const float after = at + 1 < a.k ? __int_as_float(slot[id + 1 & 31].y) : __int_as_float(r.x);
+      const unsigned filled = __ballot_sync(0xffffffffu, mine && v > -INFINITY) >> (id & ~(slots - 1));
+      const bool redo = mine && (v - after <= near0 + near1 * fabsf(v) ||  // no slot: NaN, false
+                                 __popc(slots == 32 ? filled : filled & ((1u << slots) - 1)) != r.y);
+      again |= (unsigned)redo << tok / TOKENS;
+      again = __reduce_or_sync(0xffffffffu, again);
+    } else {
+      again = (2u << (passes - 1)) - 1;
     }
 
-    for (int it = 0; it < passes; ++it) {
-      if (!((again >> it) & 1)) continue;
-      const T* row = static_cast<const T*>(a.logits) + token(it) * a.ld;
+    for (; again; again &= again - 1) {
+      const int it = __ffs(again) - 1;
+      const T* row = reinterpret_cast<const T*>(row_of(base + it * TOKENS));
       const int first = (it * TOKENS + sub) << a.log_slots;
       uint32_t key[EPL];
       float m = 0.f, total = 1.f;
@@ -519,7 +513,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? LB : 1) route_ker
         }
       };
       refill(0xffffffffu);
-      uint32_t slot = 0;  // lane j: the key of slot j
+      uint32_t held = 0;  // lane j: the key of slot j
       int expert = -1;    // and its expert
       for (int j = 0; j < a.k; ++j) {
         const uint32_t top = seg_max<LANES>(b1);
@@ -527,7 +521,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? LB : 1) route_ker
         const int who = __ffs(have) - 1;
         const uint32_t won = __shfl_sync(0xffffffffu, b1, who, LANES);
         if (lane == j && won) {
-          slot = won;
+          held = won;
           expert = who * EPL + (int)(LOW - (won & LOW));
         }
         bool spent = false;
@@ -550,12 +544,12 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? LB : 1) route_ker
           pick = a.sigmoid ? logistic(l) : soft_exp(l, m);
           if (a.bias) pick = (a.sigmoid ? pick : pick / total) + a.bias[expert];
         }
-        const uint32_t after = __shfl_down_sync(0xffffffffu, slot, 1, LANES);
+        const uint32_t after = __shfl_down_sync(0xffffffffu, held, 1, LANES);
         const float later = __shfl_down_sync(0xffffffffu, pick, 1, LANES);
         bool unsure = false;
-        if (slot) {
-          if (lane + 1 == a.k) unsure = (slot | LOW) == (next | LOW);
-          else if (lane + 1 < a.k) unsure = after && (slot | LOW) == (after | LOW) && pick != later;
+        if (held) {
+          if (lane + 1 == a.k) unsure = (held | LOW) == (next | LOW);
+          else if (lane + 1 < a.k) unsure = after && (held | LOW) == (after | LOW) && pick != later;
         }
         if (__any_sync(0xffffffffu, unsure)) {
           unsigned alive = 0xffffffffu;
@@ -578,14 +572,14 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? LB : 1) route_ker
           }
         }
       }
-      if (lane < a.k) chosen[first + lane] = expert;
+      if (lane < a.k) slot[first + lane].x = expert;
     }
     __syncwarp();
 
-    const int e = mine ? chosen[threadIdx.x & 31] : -1;
+    const int e = mine ? slot[id].x : -1;
     float w = 0.f;
     if (e >= 0) {
-      const float l = logit_of(static_cast<const T*>(a.logits) + (base + tok) * a.ld + e);
+      const float l = logit_of(reinterpret_cast<const T*>(rows + (uint64_t)(base + tok) * a.ld_bytes) + e);
       if (a.sigmoid) {
         w = logistic(l);
       } else {
@@ -603,8 +597,9 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? LB : 1) route_ker
       w *= a.scale;
     }
     if (mine) {
-      a.indices[(base + tok) * a.k + at] = e;
-      a.weights[(base + tok) * a.k + at] = w;
+      const uint64_t o = (uint64_t)(base + tok) * a.k + at;
+      a.indices[o] = e;
+      a.weights[o] = w;
     }
   }
   if (!a.counts) return;
@@ -699,6 +694,8 @@ static int route_checks(int64_t T, int E, int k, int dtype, int score, int64_t l
   if (T < 0 || E < 1 || E > kMaxExperts) return ops_fail(MHC_ERR_SHAPE, "need T >= 0 and 1 <= E <= 1024");
   if (k < 1 || k > 32 || k > E) return ops_fail(MHC_ERR_SHAPE, "need 1 <= k <= min(E, 32)");
   if (ld < E) return ops_fail(MHC_ERR_SHAPE, "the row stride must be at least E");
+  if (T >= ((int64_t)1 << 31) || ld * (int64_t)dtype_bytes(dtype) >= ((int64_t)1 << 31))
+    return ops_fail(MHC_ERR_SHAPE, "T and a row's bytes must be below 2^31");
   if (!(scale == scale)) return ops_fail(MHC_ERR_CONFIG, "scale is not a number");
   return MHC_OK;
 }
@@ -792,7 +789,7 @@ int mhc_route(const void* logits, int64_t ld, mhc_dtype dtype, const float* bias
   while ((1 << log_slots) < k) ++log_slots;
   // tokens that a warp takes in turn cost latency: only as many as leave two warps per scheduler
   while ((32 >> log_slots) > 32 / lanes && T < (int64_t)sms * 8 * (32 >> log_slots)) ++log_slots;
-  const RouteArgs a = {logits, ld, T, bias, E, groups, top_groups, k, log_slots, score == MHC_SCORE_SIGMOID, renorm != 0, vector,
+  const RouteArgs a = {logits, (uint32_t)(ld * b), (uint32_t)T, bias, E, groups, top_groups, k, log_slots, score == MHC_SCORE_SIGMOID, renorm != 0, vector,
                        whole(), estimate, scale, indices, weights, counts, counts ? ws + 16 : nullptr, counts ? ws + 64 : nullptr};
   const int64_t tokens = kRouteWarps * (32 >> log_slots);
   int64_t grid = (T + tokens - 1) / tokens;
