@@ -18,7 +18,13 @@ namespace mhc {
 
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortRounds = 4;                               // keys per lane
+#ifndef SR
+#define SR 4
+#endif
+#ifndef SU
+#define SU 4
+#endif
+constexpr int kSortRounds = SR;                              // keys per lane
 constexpr int kSortTile = kSortThreads * kSortRounds;        // keys per CTA
 constexpr int kDigits = 512;                                 // 9-bit digits at most
 constexpr int kColumns = 1024;                               // columns per CTA of the sum
@@ -31,7 +37,9 @@ struct Bounds {  // a chunk's first token and row, and the ones behind its last
 struct EmbedGradWs {  // byte offsets into the workspace
   size_t key[2], tok[2], hist, valid, bounds, carry, total;
   int tiles, chunks, passes, digit_bits;
+  bool one;  // one CTA sorts
 };
+constexpr int kSumRounds = SU;
 
 struct SortArgs {
   const void* ids;
@@ -78,6 +86,103 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const SortArgs
   if (threadIdx.x == 0) a.valid[blockIdx.x] = valid;
 }
 
+// The whole sort in one CTA, for up to 1024 * R tokens: keys and tokens stay in
+// registers between the passes and change places through shared memory.  One launch
+// instead of one per pass and a count.
+constexpr int kOneThreads = 1024, kOneWarps = kOneThreads / 32;
+constexpr int kOneMost = 4;  // keys per thread at most
+static size_t one_smem(int R) { return (size_t)kOneThreads * R * 6 + (size_t)kOneWarps * kDigits * 2; }
+
+template <typename Id, int R>
+__global__ void __launch_bounds__(kOneThreads) sort_one_kernel(const SortArgs a) {
+  extern __shared__ uint32_t dyn[];
+  uint32_t* const keys = dyn;                                                    // [1024 R]
+  unsigned short* const toks = reinterpret_cast<unsigned short*>(dyn + kOneThreads * R);  // [1024 R]
+  unsigned short* const rank = toks + kOneThreads * R;                           // [kOneWarps][kDigits]
+  __shared__ int start[kDigits];
+  __shared__ int scan[kDigits / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t mask = (1u << a.bits) - 1;
+  const int base = warp * 32 * R + lane;  // a warp's keys are in order, 32 at a time
+  uint32_t key[R];
+  int tok[R];
+  int valid = 0;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int i = base + r * 32;
+    tok[r] = i;
+    key[r] = i < a.T ? row_of<Id>(a, i) : 0xffffffffu;
+    valid += key[r] < (uint32_t)a.V;
+  }
+  for (int p = 0; p < a.passes; ++p) {
+    const int shift = p * a.bits;
+    for (int i = threadIdx.x; i < kOneWarps * kDigits / 2; i += kOneThreads) reinterpret_cast<uint32_t*>(rank)[i] = 0;
+    __syncthreads();
+    int place[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {  // places past T get the digit kDigits: no key
+      const uint32_t d = key[r] == 0xffffffffu ? kDigits : (key[r] >> shift) & mask;
+      const unsigned peers = __match_any_sync(0xffffffffu, d);
+      const unsigned below = peers & ((1u << lane) - 1);
+      place[r] = d < kDigits ? rank[warp * kDigits + d] + __popc(below) : 0;
+      __syncwarp();
+      if (d < kDigits && below == 0) rank[warp * kDigits + d] += (unsigned short)__popc(peers);
+      __syncwarp();
+    }
+    __syncthreads();
+    int sum = 0, x = 0;
+    if (threadIdx.x < kDigits) {  // the digit's keys in the warps before, and in all
+      for (int w = 0; w < kOneWarps; ++w) {
+        const int n = rank[w * kDigits + threadIdx.x];
+        rank[w * kDigits + threadIdx.x] = (unsigned short)sum;
+        sum += n;
+      }
+      x = sum;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += y;
+      }
+      if (lane == 31) scan[warp] = x;
+    }
+    __syncthreads();
+    if (threadIdx.x < kDigits) {
+      for (int w = 0; w < warp; ++w) x += scan[w];
+      start[threadIdx.x] = x - sum;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (key[r] == 0xffffffffu) continue;
+      const uint32_t d = (key[r] >> shift) & mask;
+      const int at = start[d] + rank[warp * kDigits + d] + place[r];
+      keys[at] = key[r];
+      toks[at] = (unsigned short)tok[r];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int i = base + r * 32;
+      if (i < a.T) key[r] = keys[i], tok[r] = toks[i];
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int i = base + r * 32;
+    if (i < a.T) a.key_out[i] = key[r], a.tok_out[i] = tok[r];
+  }
+#pragma unroll
+  for (int d = 16; d; d >>= 1) valid += __shfl_xor_sync(0xffffffffu, valid, d);
+  __syncthreads();
+  if (lane == 0) start[warp] = valid;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int n = 0;
+    for (int w = 0; w < kOneWarps; ++w) n += start[w];
+    a.valid[0] = n;
+  }
+}
+
 // One pass of the stable sort: a key's place is the keys of smaller digits,
 // the same digit in earlier tiles, in earlier warps of the tile, and before it
 // in its warp (whose keys are taken in order, 32 at a time).
@@ -88,6 +193,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_pass_kernel(const SortArgs 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t mask = (1u << a.bits) - 1;
   for (int i = threadIdx.x; i < kSortWarps * kDigits; i += kSortThreads) (&rank[0][0])[i] = 0;
+  pdl_wait();
   // the digit's keys in all tiles and in the tiles before this one
   int before = 0, all = 0;
   for (int b = 0; b < a.tiles; ++b) {
@@ -153,7 +259,8 @@ struct SumArgs {
   const int* tok;
   const int* valid;
   Bounds* bounds;
-  float* carry;  // [chunks][H]
+  float* carry;  // [chunks][2][H]: the sum of the last row's tokens, where it ends later; of the first row's, where
+                 // it began earlier
 };
 
 // Tokens that have a row: the sum over the sort's tiles.
@@ -170,33 +277,43 @@ __device__ __forceinline__ int valid_tokens(const SumArgs& a, int* sh) {
 }
 
 // Where the merged list is cut so that `target` weight lies before: (token,
-// row).  Before token i lie i tokens and key[i] rows' ends.
+// row).  Before token i lie i tokens and key[i] rows' ends.  A warp looks for
+// the place, 32 probes at a time.
 __device__ __forceinline__ void cut(const SumArgs& a, int n, int64_t target, int* tok, int* row) {
+  const int lane = threadIdx.x & 31;
   int lo = 0, hi = n;  // the first token that has at least `target` before it
   while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if ((int64_t)a.wt * mid + (int64_t)a.wr * a.key[mid] >= target) hi = mid;
-    else lo = mid + 1;
+    const int step = (hi - lo + 31) / 32;
+    const int at = lo + lane * step;
+    const bool less = at < hi && (int64_t)a.wt * at + (int64_t)a.wr * a.key[at] < target;
+    const int k = __popc(__ballot_sync(0xffffffffu, less));  // probes 0 .. k-1 lie before
+    if (k == 0) {
+      hi = lo;
+    } else {
+      const int last = lo + (k - 1) * step;
+      hi = k < 32 && lo + k * step < hi ? lo + k * step : hi;
+      lo = last + 1;
+    }
   }
-  const int64_t from = lo ? (int64_t)a.key[lo - 1] : 0, to = lo < n ? (int64_t)a.key[lo] : a.V;
-  int64_t r = (target - (int64_t)a.wt * lo + a.wr - 1) / a.wr;
-  if (target < (int64_t)a.wt * lo) r = 0;
-  *tok = lo;
-  *row = (int)(r < from ? from : r > to ? to : r);
-}
-
-template <typename T>
-__device__ __forceinline__ void add_token(const SumArgs& a, int i, int64_t c, Vec8& acc) {
-  const T* p = static_cast<const T*>(a.dout) + (int64_t)a.tok[i] * a.streams * a.H + c;
-  for (int s = 0; s < a.streams; ++s, p += a.H) {
-    const Vec8 x = unpack(ld8_stream(p));
-#pragma unroll
-    for (int e = 0; e < 4; ++e) acc.p[e] = __fadd2_rn(acc.p[e], x.p[e]);
+  if (lane == 0) {
+    const int64_t from = lo ? (int64_t)a.key[lo - 1] : 0, to = lo < n ? (int64_t)a.key[lo] : a.V;
+    int64_t r = (target - (int64_t)a.wt * lo + a.wr - 1) / a.wr;
+    if (target < (int64_t)a.wt * lo) r = 0;
+    *tok = lo;
+    *row = (int)(r < from ? from : r > to ? to : r);
   }
 }
 
 template <typename O>
-__device__ __forceinline__ void end_row(const SumArgs& a, int64_t row, int64_t c, Vec8 acc) {
+__device__ __forceinline__ void store_row(O* o, const Raw8<O>& r, bool wide) {
+  if constexpr (sizeof(O) == 4) {
+    if (wide) return st32(o, r);
+  }
+  st8_stream(o, r);
+}
+
+template <typename O>
+__device__ __forceinline__ void end_row(const SumArgs& a, int64_t row, int64_t c, Vec8 acc, bool wide) {
   O* o = static_cast<O*>(a.dtable) + row * a.ld + c;
 #pragma unroll
   for (int e = 0; e < 4; ++e) acc.p[e] = __fmul2_rn(acc.p[e], splat(a.scale));
@@ -205,70 +322,162 @@ __device__ __forceinline__ void end_row(const SumArgs& a, int64_t row, int64_t c
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc.p[e] = __fadd2_rn(acc.p[e], old.p[e]);
   }
-  st8_stream(o, pack<O>(acc));
+  store_row(o, pack<O>(acc), wide);
+}
+__device__ __forceinline__ void add8(Vec8& acc, const Vec8& x) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) acc.p[e] = __fadd2_rn(acc.p[e], x.p[e]);
 }
 
-template <typename T, typename O>
+// Walks one chunk.  The rows of the next GROUP tokens are loaded before the
+// present ones are added (GROUP * S loads of 16 or 32 bytes in flight per thread and
+// as many being used), whatever rows they belong to.  S: streams, 0 for any number.
+constexpr int kWindow = 256;  // tokens of a chunk whose keys are in shared memory at a time
+template <typename T, typename O, int S>
 __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const SumArgs a) {
+  constexpr int GROUP = S == 1 ? 4 : S == 2 ? 2 : 1;
+  constexpr int LOADS = S ? S : 4;
   __shared__ int sh[kSumThreads / 32];
   __shared__ Bounds sb;
+  __shared__ int before;  // the row of the token before the chunk
+  __shared__ int wkey[kWindow + 1], wtok[kWindow + 1];
+  pdl_wait();
   const int n = valid_tokens(a, sh);
   const int64_t weight = (int64_t)a.wt * n + (int64_t)a.wr * a.V;
   const int chunk = blockIdx.x;
-  if (threadIdx.x == 0) {
+  if (threadIdx.x < 32) {
     cut(a, n, weight * chunk / a.chunks, &sb.a0, &sb.b0);
+    __syncwarp();
+    if (threadIdx.x == 0) before = sb.a0 ? (int)a.key[sb.a0 - 1] : -1;
+  } else if (threadIdx.x < 64) {
     if (chunk + 1 < a.chunks) cut(a, n, weight * (chunk + 1) / a.chunks, &sb.a1, &sb.b1);
-    else sb.a1 = n, sb.b1 = (int)a.V;
-    if (blockIdx.y == 0) a.bounds[chunk] = sb;
+    else if (threadIdx.x == 32) sb.a1 = n, sb.b1 = (int)a.V;
   }
   __syncthreads();
+  pdl_launch();
   const Bounds b = sb;
+  if (blockIdx.y == 0 && threadIdx.x == 0) a.bounds[chunk] = b;
   const int64_t c = (int64_t)blockIdx.y * kColumns + threadIdx.x * 8;
-  if (c >= a.H) return;
-  int i = b.a0, row = b.b0;
-  if (i > 0 && row < b.b1 && (int)a.key[i - 1] == row) {  // the join ends this row
-    while (i < b.a1 && (int)a.key[i] == row) ++i;
-    ++row;
+  const bool on = c < a.H;
+  const bool wide = ((reinterpret_cast<uintptr_t>(a.dtable) | (uintptr_t)(a.ld * sizeof(O))) & 31) == 0;
+  float* const carry = a.carry + (int64_t)chunk * 2 * a.H + c;
+  const T* const src = static_cast<const T*>(a.dout) + c;
+  const int64_t row_elems = (int64_t)a.streams * a.H;
+  const Raw8<O> zero = pack<O>(zero8());
+  int row = b.b0;
+  auto zeros = [&](int to) {  // rows without tokens
+    if (!a.accumulate && on)
+      for (int r = row; r < to; ++r) store_row(static_cast<O*>(a.dtable) + r * a.ld + c, zero, wide);
+    row = to;
+  };
+  Vec8 acc = zero8();
+  auto finish = [&](int k) {  // the tokens of row k end here or in a later chunk
+    if (on) {
+      if (k >= b.b1) st8(carry, pack<float>(acc));
+      else if (k == b.b0 && before == k) st8(carry + a.H, pack<float>(acc));
+      else end_row<O>(a, k, c, acc, wide);
+    }
+    acc = zero8();
+    if (k < b.b1) row = k + 1;
+  };
+  if (before == b.b0 && b.b0 < b.b1 && (b.a0 == b.a1 || (int)a.key[b.a0] != b.b0)) finish(b.b0);  // it has no token here
+
+  for (int w = b.a0; w < b.a1; w += kWindow) {
+    const int m = min(kWindow, b.a1 - w);
+    __syncthreads();
+    for (int i = threadIdx.x; i < m; i += kSumThreads) {
+      wkey[i] = (int)a.key[w + i];
+      wtok[i] = a.tok[w + i];
+    }
+    if (threadIdx.x == 0) wkey[m] = w + m < b.a1 ? (int)a.key[w + m] : -1;
+    __syncthreads();
+    if constexpr (S == 0) {
+      for (int i = 0; i < m; ++i) {
+        zeros(min(wkey[i], b.b1));
+        if (on) {
+          const T* p = src + (int64_t)wtok[i] * row_elems;
+          for (int s = 0; s < a.streams; s += LOADS) {
+            Raw8<T> x[LOADS];
+#pragma unroll
+            for (int u = 0; u < LOADS; ++u)
+              if (s + u < a.streams) x[u] = ld8_stream(p + (int64_t)(s + u) * a.H);
+#pragma unroll
+            for (int u = 0; u < LOADS; ++u)
+              if (s + u < a.streams) add8(acc, unpack(x[u]));
+          }
+        }
+        if (wkey[i + 1] != wkey[i]) finish(wkey[i]);
+      }
+    } else {
+      Raw8<T> cur[GROUP][S], next[GROUP][S];
+      auto load = [&](Raw8<T>(&x)[GROUP][S], int i) {
+#pragma unroll
+        for (int g = 0; g < GROUP; ++g)
+          if (i + g < m && on) {
+            const T* p = src + (int64_t)wtok[i + g] * row_elems;
+#pragma unroll
+            for (int s = 0; s < S; ++s) x[g][s] = ld8_stream(p + (int64_t)s * a.H);
+          }
+      };
+      load(cur, 0);
+      for (int i = 0; i < m; i += GROUP) {
+        load(next, i + GROUP);
+#pragma unroll
+        for (int g = 0; g < GROUP; ++g) {
+          if (i + g < m) {
+            const int k = wkey[i + g];
+            zeros(min(k, b.b1));
+            if (on) {
+#pragma unroll
+              for (int s = 0; s < S; ++s) add8(acc, unpack(cur[g][s]));
+            }
+            if (wkey[i + g + 1] != k) finish(k);
+          }
+        }
+#pragma unroll
+        for (int g = 0; g < GROUP; ++g)
+#pragma unroll
+          for (int s = 0; s < S; ++s) cur[g][s] = next[g][s];
+      }
+    }
   }
-  for (; row < b.b1; ++row) {
-    Vec8 acc = zero8();
-    const int i0 = i;
-    for (; i < b.a1 && (int)a.key[i] == row; ++i) add_token<T>(a, i, c, acc);
-    if (i > i0 || !a.accumulate) end_row<O>(a, row, c, acc);
-  }
-  if (i < b.a1) {  // tokens of a row that ends in a later chunk
-    Vec8 acc = zero8();
-    for (; i < b.a1; ++i) add_token<T>(a, i, c, acc);
-    st8(a.carry + (int64_t)chunk * a.H + c, pack<float>(acc));
-  }
+  zeros(b.b1);
 }
 
-// Rows whose tokens lie in several chunks, by the chunk that holds their end.
-template <typename T, typename O>
+// Rows whose tokens lie in several chunks, by the chunk that holds their end:
+// the earlier chunks' sums in chunk order, then its own.
+template <typename O>
 __global__ void __launch_bounds__(kSumThreads) embed_join_kernel(const SumArgs a) {
+  __shared__ int first;
   pdl_wait();
   const int chunk = blockIdx.x;
   const Bounds b = a.bounds[chunk];
   const int row = b.b0;
   if (b.a0 == 0 || row >= b.b1 || (int)a.key[b.a0 - 1] != row) return;
+  // the chunk that holds the row's first token: the last one before this that did not begin inside the row
+  for (int hi = chunk - 1;; hi -= kSumThreads) {
+    if (threadIdx.x == 0) first = -1;
+    __syncthreads();
+    const int k = hi - (int)threadIdx.x;
+    if (k >= 0) {
+      const Bounds p = a.bounds[k];
+      if (!(p.b0 == row && p.a0 > 0 && (int)a.key[p.a0 - 1] == row)) atomicMax(&first, k);
+    }
+    __syncthreads();
+    if (first >= 0 || hi < kSumThreads) break;
+    __syncthreads();
+  }
   const int64_t c = (int64_t)blockIdx.y * kColumns + threadIdx.x * 8;
   if (c >= a.H) return;
-  int from = chunk - 1;  // the first chunk that holds tokens of the row
-  while (from > 0) {
-    const Bounds p = a.bounds[from];
-    if (p.b0 < row || p.a0 == 0 || (int)a.key[p.a0 - 1] != row) break;
-    --from;
-  }
+  const bool wide = ((reinterpret_cast<uintptr_t>(a.dtable) | (uintptr_t)(a.ld * sizeof(O))) & 31) == 0;
   Vec8 acc = zero8();
-  for (int k = from; k < chunk; ++k) {
+#pragma unroll 4
+  for (int k = max(first, 0); k < chunk; ++k) {
     const Bounds p = a.bounds[k];
-    if (p.a1 == p.a0) continue;  // no token in it
-    const Vec8 x = unpack(ld8(a.carry + (int64_t)k * a.H + c));
-#pragma unroll
-    for (int e = 0; e < 4; ++e) acc.p[e] = __fadd2_rn(acc.p[e], x.p[e]);
+    if (p.a1 > p.a0) add8(acc, unpack(ld8(a.carry + (int64_t)k * 2 * a.H + c)));  // it has a token, the last of the row
   }
-  for (int i = b.a0; i < b.a1 && (int)a.key[i] == row; ++i) add_token<T>(a, i, c, acc);
-  end_row<O>(a, row, c, acc);
+  add8(acc, unpack(ld8(a.carry + ((int64_t)chunk * 2 + 1) * a.H + c)));
+  end_row<O>(a, row, c, acc, wide);
 }
 
 static int bits_of(int64_t v) {
@@ -285,9 +494,15 @@ static EmbedGradWs embed_grad_plan(int64_t T, int64_t V, int H) {
   w.digit_bits = (bits + w.passes - 1) / w.passes;
   w.tiles = (int)((T + kSortTile - 1) / kSortTile);
   const int cols = (H + kColumns - 1) / kColumns;
-  const int64_t most = (152 * 16 + cols - 1) / cols;  // about one round of resident CTAs
+  // Chunks: some rounds of CTAs, so that an SM that gets through faster takes more; at
+  // least 16 rows or tokens each; and 5 Mi columns of partial sums at most.
+  int64_t most = (kSumRounds * 152 * 8 + cols - 1) / cols;
+  if (most * H > (int64_t)5 << 20) most = ((int64_t)5 << 20) / H;
+  if (most < 152) most = 152;
   int64_t chunks = (T + V + 15) / 16;
   w.chunks = (int)(chunks < 1 ? 1 : chunks > most ? most : chunks);
+  w.one = T <= kOneThreads * kOneMost;
+  if (w.one) w.tiles = 1;
   size_t at = 256;
   auto take = [&](size_t bytes) {
     const size_t o = at;
@@ -298,7 +513,7 @@ static EmbedGradWs embed_grad_plan(int64_t T, int64_t V, int H) {
   w.hist = take((size_t)w.passes * w.tiles * kDigits * 4);
   w.valid = take((size_t)w.tiles * 4);
   w.bounds = take((size_t)w.chunks * sizeof(Bounds));
-  w.carry = take((size_t)w.chunks * H * 4);
+  w.carry = take((size_t)w.chunks * 2 * H * 4);
   w.total = at;
   return w;
 }
@@ -308,13 +523,28 @@ static cudaError_t sum_launch(const SumArgs& a, int grad_dtype, dim3 grid, cudaS
   cudaError_t e = cudaSuccess;
   auto go = [&](auto o) {
     using O = decltype(o);
-    embed_sum_kernel<T, O><<<grid, kSumThreads, 0, s>>>(a);
-    e = cudaGetLastError();
-    if (e == cudaSuccess) e = launch_pdl(embed_join_kernel<T, O>, grid, dim3(kSumThreads), 0, s, a);
+    if (a.streams == 1) e = launch_pdl(embed_sum_kernel<T, O, 1>, grid, dim3(kSumThreads), 0, s, a);
+    else if (a.streams == 2) e = launch_pdl(embed_sum_kernel<T, O, 2>, grid, dim3(kSumThreads), 0, s, a);
+    else if (a.streams == 4) e = launch_pdl(embed_sum_kernel<T, O, 4>, grid, dim3(kSumThreads), 0, s, a);
+    else e = launch_pdl(embed_sum_kernel<T, O, 0>, grid, dim3(kSumThreads), 0, s, a);
+    if (e == cudaSuccess && a.chunks > 1) e = launch_pdl(embed_join_kernel<O>, grid, dim3(kSumThreads), 0, s, a);
   };
   if (grad_dtype == MHC_DT_F32) go(float());
   else go(T());
   return e;
+}
+
+template <typename Id, int R>
+static cudaError_t sort_one_launch(const SortArgs& a, cudaStream_t s) {
+  static SmemGrant grant;
+  cudaError_t e = allow_smem(grant, (const void*)sort_one_kernel<Id, R>, one_smem(R));
+  if (e != cudaSuccess) return e;
+  sort_one_kernel<Id, R><<<1, kOneThreads, one_smem(R), s>>>(a);
+  return cudaGetLastError();
+}
+template <typename Id>
+static cudaError_t sort_one(const SortArgs& a, cudaStream_t s) {
+  return a.T <= kOneThreads ? sort_one_launch<Id, 1>(a, s) : sort_one_launch<Id, kOneMost>(a, s);
 }
 
 }  // namespace mhc
@@ -373,7 +603,12 @@ int mhc_embed_grad(const void* ids, int id_bytes, const void* dout, mhc_dtype dt
   const size_t per_pass = (size_t)w.tiles * kDigits;
   cudaError_t e = cudaSuccess;
   int from = 0;
-  for (int p = 0; p < w.passes && e == cudaSuccess; ++p, from ^= 1) {
+  if (w.one) {
+    a.key_out = reinterpret_cast<uint32_t*>(ws + w.key[0]);
+    a.tok_out = reinterpret_cast<int*>(ws + w.tok[0]);
+    e = id_bytes == 4 ? sort_one<int32_t>(a, s) : sort_one<int64_t>(a, s);
+  }
+  for (int p = 0; !w.one && p < w.passes && e == cudaSuccess; ++p, from ^= 1) {
     const bool last = p + 1 == w.passes;
     a.shift = p * w.digit_bits;
     a.key_in = reinterpret_cast<uint32_t*>(ws + w.key[from]);
@@ -388,8 +623,7 @@ int mhc_embed_grad(const void* ids, int id_bytes, const void* dout, mhc_dtype dt
       e = cudaGetLastError();
       if (e != cudaSuccess) break;
     }
-    sort_pass_kernel<<<w.tiles, kSortThreads, 0, s>>>(a, p == 0, last);
-    e = cudaGetLastError();
+    e = launch_pdl(sort_pass_kernel, dim3(w.tiles), dim3(kSortThreads), 0, s, a, p == 0, last);
   }
   if (e != cudaSuccess) return ops_cuda(e, "embed_grad sort launch");
   SumArgs m = {};

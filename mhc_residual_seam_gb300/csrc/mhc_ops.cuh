@@ -90,6 +90,13 @@ __device__ __forceinline__ Raw8<T> ld8_stream(const T* p) {  // read once
   for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.q[i] = __ldcs(reinterpret_cast<const uint4*>(p) + i);
   return r;
 }
+// (a 32-byte store of fp32 columns writes whole sectors; the pointer is 32-byte
+// aligned where the row is)
+__device__ __forceinline__ void st32(float* p, const Raw8<float>& r) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r.q[0].x), "r"(r.q[0].y), "r"(r.q[0].z),
+               "r"(r.q[0].w), "r"(r.q[1].x), "r"(r.q[1].y), "r"(r.q[1].z), "r"(r.q[1].w)
+               : "memory");
+}
 template <typename T>
 __device__ __forceinline__ void st8(T* p, const Raw8<T>& r) {
 #pragma unroll
