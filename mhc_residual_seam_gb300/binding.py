@@ -244,60 +244,97 @@ def mhc_last_error_string() -> str:
 
 # ------------------------------------------- the operators around the seam --
 # Pointers carry no type or shape, so these functions check the tensors'
-# before they pass the pointers on (MHC_ERR_CONFIG for a type, MHC_ERR_SHAPE
-# for a shape or a stride).
+# before they pass the pointers on (MHC_ERR_CONFIG for a type or a tensor that is
+# not on the GPU, MHC_ERR_SHAPE for a shape or a stride).  They are written to cost
+# a few microseconds of Python per call: messages are put together only for a
+# refusal.
 _DTYPES: dict = {}
+_F32 = _I32 = _raw_stream = _device = None
 
 
-def _dtype(t) -> int:
-    if not _DTYPES:
+def _ops():
+    """The library, with this section's constants and the stream lookup set up."""
+    global _F32, _I32, _raw_stream, _device
+    if _F32 is None:
         import torch
         _DTYPES.update({torch.bfloat16: MHC_DT_BF16, torch.float16: MHC_DT_F16, torch.float32: MHC_DT_F32})
+        # the current stream's handle without a Stream object around it
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _device = getattr(torch._C, "_cuda_getDevice", None)
+        _F32, _I32 = torch.float32, torch.int32
+    return lib()
+
+
+def _where(stream):
+    if stream is None and _raw_stream is not None and _device is not None:
+        return _raw_stream(_device())
+    return _stream(stream)
+
+
+def _refuse(t, name: str, want: str, dtype=None):
+    if not t.is_cuda:
+        raise MhcError(-10, f"{name} is not on the GPU")
+    if dtype is not None and t.dtype != dtype:
+        raise MhcError(-10, f"{name} must be {dtype}, not {t.dtype}")
+    raise MhcError(-2, f"{name} must be {want}, not {tuple(t.shape)} with strides {t.stride()}")
+
+
+def _dtype(t, name: str) -> int:
     d = _DTYPES.get(t.dtype)
     if d is None:
-        raise MhcError(-10, f"{t.dtype} is not bf16, fp16 or fp32")
+        raise MhcError(-10, f"{name} is {t.dtype}, not bf16, fp16 or fp32")
     return d
 
 
-def _need(ok: bool, msg: str, code: int = -2) -> None:
-    if not ok:
-        raise MhcError(code, msg)
+def _dense(t, shape, dtype, name: str):
+    """The address of ``t``, a dense tensor of this shape and type, or None."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        _refuse(t, name, f"dense, of shape {shape}", dtype)
+    return t.data_ptr()
 
 
-def _dense(t, shape, dtype, name: str) -> None:
-    """``t`` is None or a dense tensor of this shape and type."""
-    if t is not None:
-        _need(t.is_cuda, f"{name} is not on the GPU", -10)
-        _need(t.dtype == dtype, f"{name} must be {dtype}", -10)
-        _need(tuple(t.shape) == shape and t.is_contiguous(), f"{name} must be dense, of shape {shape}")
-
-
-def _rows(t, T: int, H: int, dtype, name: str) -> int:
+def _pitch(t, T: int, H: int, dtype, name: str) -> int:
     """The row stride of a [T, H] matrix with dense rows (H for None)."""
     if t is None:
         return H
-    _need(t.is_cuda, f"{name} is not on the GPU", -10)
-    _need(t.dtype == dtype, f"{name} must be {dtype}", -10)
-    _need(t.dim() == 2 and t.shape[0] == T and t.shape[1] == H and (t.stride(1) == 1 or H == 1),
-          f"{name} must be [{T}, {H}] with dense rows")
-    return t.stride(0) if T > 1 else max(H, t.stride(0) // 8 * 8)
+    if t.dtype != dtype or t.shape != (T, H) or not t.is_cuda:
+        _refuse(t, name, f"[{T}, {H}]", dtype)
+    rows, cols = t.stride()
+    if cols != 1 and H > 1:
+        _refuse(t, name, f"[{T}, {H}] with dense rows")
+    return rows if T > 1 else H
 
 
-def _id_bytes(ids) -> int:
+def _ids(ids):
     import torch
-    _need(ids.is_cuda, "ids is not on the GPU", -10)
-    _need(ids.dtype in (torch.int32, torch.int64), "ids must be int32 or int64", -10)
-    _need(ids.dim() == 1 and ids.is_contiguous(), "ids must be a dense vector")
-    return ids.element_size()
+    size = 8 if ids.dtype == torch.int64 else 4
+    if (size == 4 and ids.dtype != _I32) or ids.dim() != 1 or not ids.is_cuda or not ids.is_contiguous():
+        _refuse(ids, "ids", "a dense vector", ids.dtype if ids.dtype in (torch.int64, _I32) else torch.int64)
+    return ids.data_ptr(), size
+
+
+def _space(ws):
+    if ws is None:
+        return None, 0
+    if not ws.is_cuda or not ws.is_contiguous():
+        _refuse(ws, "workspace", "dense")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def mhc_embed(ids, table, out, scale: float = 1.0, first_id: int = 0, stream=None) -> None:
     """Rows of ``table`` [V, H] into ``out`` [T, H] or [T, streams, H]."""
-    T, (V, H) = ids.shape[0], table.shape
-    S = out.shape[1] if out.dim() == 3 else 1
-    _dense(out, (T, S, H) if out.dim() == 3 else (T, H), table.dtype, "out")
-    _check(lib().mhc_embed(_ptr(ids), _id_bytes(ids), _ptr(table), _rows(table, V, H, table.dtype, "table"), V,
-                           int(first_id), float(scale), T, H, S, _dtype(table), _ptr(out), _stream(stream)))
+    L = _ops()
+    (V, H), dt, shape = table.shape, table.dtype, out.shape
+    p, size = _ids(ids)
+    T = ids.shape[0]
+    S = shape[1] if len(shape) == 3 else 1
+    o = _dense(out, (T, S, H) if len(shape) == 3 else (T, H), dt, "out")
+    rc = L.mhc_embed(p, size, table.data_ptr(), _pitch(table, V, H, dt, "table"), V, first_id, scale, T, H, S,
+                     _dtype(table, "table"), o, _where(stream))
+    if rc:
+        _check(rc)
 
 
 def mhc_embed_grad_workspace_bytes(T: int, V: int, H: int) -> int:
@@ -308,45 +345,42 @@ def mhc_embed_grad(ids, dout, dtable, workspace, scale: float = 1.0, first_id: i
                    accumulate: bool = False, stream=None) -> None:
     """The gradient of mhc_embed by its table: ``dout`` [T, H] or [T, streams, H]
     into ``dtable`` [V, H] (fp32 or dout's type)."""
-    T, (V, H) = ids.shape[0], dtable.shape
-    S = dout.shape[1] if dout.dim() == 3 else 1
-    _dense(dout, (T, S, H) if dout.dim() == 3 else (T, H), dout.dtype, "dout")
+    L = _ops()
+    (V, H), dt, shape = dtable.shape, dout.dtype, dout.shape
+    p, size = _ids(ids)
+    T = ids.shape[0]
+    S = shape[1] if len(shape) == 3 else 1
+    d = _dense(dout, (T, S, H) if len(shape) == 3 else (T, H), dt, "dout")
     pad = None if padding_id is None else C.byref(C.c_int64(padding_id))
-    _check(lib().mhc_embed_grad(_ptr(ids), _id_bytes(ids), _ptr(dout), _dtype(dout), float(scale), T, H, S, V,
-                                int(first_id), pad, int(accumulate), _ptr(dtable), _dtype(dtable),
-                                _rows(dtable, V, H, dtable.dtype, "dtable"), _ptr(workspace), _bytes(workspace),
-                                _stream(stream)))
+    ws, n = _space(workspace)
+    rc = L.mhc_embed_grad(p, size, d, _dtype(dout, "dout"), scale, T, H, S, V, first_id, pad, int(accumulate),
+                          dtable.data_ptr(), _dtype(dtable, "dtable"), _pitch(dtable, V, H, dtable.dtype, "dtable"), ws, n,
+                          _where(stream))
+    if rc:
+        _check(rc)
 
 
-def _bytes(t) -> int:
-    if t is None:
-        return 0
-    _need(t.is_cuda and t.is_contiguous(), "workspace must be dense and on the GPU", -10)
-    return t.numel() * t.element_size()
-
-
-def _gate(gate, gate_mode: int, T: int, H: int, dtype) -> None:
-    import torch
-    if gate is not None:
-        token = gate_mode == MHC_GATE_TOKEN
-        _dense(gate, (T,) if token else (H,), torch.float32 if token else dtype, "gate")
+def _gate(gate, gate_mode: int, T: int, H: int, dtype):
+    if gate is None:
+        return None
+    return _dense(gate, (T,), _F32, "gate") if gate_mode == MHC_GATE_TOKEN else _dense(gate, (H,), dtype, "gate")
 
 
 def mhc_block_norm(y, r, gamma_post, gate, gamma_pre, r_out, norm, rstd_post, rstd_pre, gate_mode: int = MHC_GATE_NONE,
                    res_scale: float = 1.0, eps: float = 1e-6, stream=None) -> None:
     """Norm after a block, gate, residual add and norm before the next block;
     y, r, r_out and norm are [T, H] (rows may be strided)."""
-    import torch
+    L = _ops()
     (T, H), dt = r.shape, r.dtype
-    _gate(gate, gate_mode, T, H, dt)
-    for t, n in ((gamma_post, "gamma_post"), (gamma_pre, "gamma_pre")):
-        _dense(t, (H,), dt, n)
-    for t, n in ((rstd_post, "rstd_post"), (rstd_pre, "rstd_pre")):
-        _dense(t, (T,), torch.float32, n)
-    _check(lib().mhc_block_norm(_ptr(y), _rows(y, T, H, dt, "y"), _ptr(r), _rows(r, T, H, dt, "r"), _ptr(gamma_post),
-                                _ptr(gate), gate_mode, _ptr(gamma_pre), float(res_scale), float(eps), T, H, _dtype(r),
-                                _ptr(r_out), _rows(r_out, T, H, dt, "r_out"), _ptr(norm), _rows(norm, T, H, dt, "norm"),
-                                _ptr(rstd_post), _ptr(rstd_pre), _stream(stream)))
+    rc = L.mhc_block_norm(
+        None if y is None else y.data_ptr(), _pitch(y, T, H, dt, "y"), r.data_ptr(), _pitch(r, T, H, dt, "r"),
+        _dense(gamma_post, (H,), dt, "gamma_post"), _gate(gate, gate_mode, T, H, dt), gate_mode,
+        _dense(gamma_pre, (H,), dt, "gamma_pre"), res_scale, eps, T, H, _dtype(r, "r"),
+        None if r_out is None else r_out.data_ptr(), _pitch(r_out, T, H, dt, "r_out"),
+        None if norm is None else norm.data_ptr(), _pitch(norm, T, H, dt, "norm"),
+        _dense(rstd_post, (T,), _F32, "rstd_post"), _dense(rstd_pre, (T,), _F32, "rstd_pre"), _where(stream))
+    if rc:
+        _check(rc)
 
 
 def mhc_block_norm_grad_workspace_bytes(T: int, H: int) -> int:
@@ -358,22 +392,20 @@ def mhc_block_norm_grad(dr_out, dnorm, y, r_out, gamma_post, gate, gamma_pre, rs
                         stream=None) -> None:
     """The gradient of mhc_block_norm; all matrices are dense [T, H], the
     weights' gradients fp32."""
-    import torch
-    (T, H), dt, f32 = dr.shape, dr.dtype, torch.float32
-    _gate(gate, gate_mode, T, H, dt)
-    for t, n in ((dr_out, "dr_out"), (dnorm, "dnorm"), (y, "y"), (r_out, "r_out"), (dy, "dy"), (dr, "dr")):
-        _dense(t, (T, H), dt, n)
-    for t, n in ((gamma_post, "gamma_post"), (gamma_pre, "gamma_pre")):
-        _dense(t, (H,), dt, n)
-    for t, n in ((rstd_post, "rstd_post"), (rstd_pre, "rstd_pre")):
-        _dense(t, (T,), f32, n)
-    for t, n in ((dgamma_post, "dgamma_post"), (dgamma_pre, "dgamma_pre")):
-        _dense(t, (H,), f32, n)
-    _dense(dgate, (T,) if gate_mode == MHC_GATE_TOKEN else (H,), f32, "dgate")
-    _check(lib().mhc_block_norm_grad(_ptr(dr_out), _ptr(dnorm), _ptr(y), _ptr(r_out), _ptr(gamma_post), _ptr(gate),
-                                     gate_mode, _ptr(gamma_pre), _ptr(rstd_post), _ptr(rstd_pre), float(res_scale), T,
-                                     H, _dtype(dr), _ptr(dy), _ptr(dr), _ptr(dgamma_post), _ptr(dgate),
-                                     _ptr(dgamma_pre), _ptr(workspace), _bytes(workspace), _stream(stream)))
+    L = _ops()
+    shape, dt = dr.shape, dr.dtype
+    T, H = shape
+    ws, n = _space(workspace)
+    rc = L.mhc_block_norm_grad(
+        _dense(dr_out, shape, dt, "dr_out"), _dense(dnorm, shape, dt, "dnorm"), _dense(y, shape, dt, "y"),
+        _dense(r_out, shape, dt, "r_out"), _dense(gamma_post, (H,), dt, "gamma_post"), _gate(gate, gate_mode, T, H, dt),
+        gate_mode, _dense(gamma_pre, (H,), dt, "gamma_pre"), _dense(rstd_post, (T,), _F32, "rstd_post"),
+        _dense(rstd_pre, (T,), _F32, "rstd_pre"), res_scale, T, H, _dtype(dr, "dr"), _dense(dy, shape, dt, "dy"),
+        _dense(dr, shape, dt, "dr"), _dense(dgamma_post, (H,), _F32, "dgamma_post"),
+        _dense(dgate, (T,) if gate_mode == MHC_GATE_TOKEN else (H,), _F32, "dgate"),
+        _dense(dgamma_pre, (H,), _F32, "dgamma_pre"), ws, n, _where(stream))
+    if rc:
+        _check(rc)
 
 
 def mhc_route_workspace_bytes(E: int) -> int:
@@ -384,36 +416,29 @@ def mhc_route(logits, bias, indices, weights, counts=None, workspace=None, score
               groups: int = 1, top_groups: int = 1, renorm: bool = True, scale: float = 1.0, stream=None) -> None:
     """The k best experts of each row of ``logits`` [T, E]: ``indices`` [T, k]
     int32, ``weights`` [T, k] fp32 and, where given, the experts' ``counts``."""
-    import torch
-    (T, E), k = logits.shape, indices.shape[-1]
-    _dense(bias, (E,), torch.float32, "bias")
-    _dense(indices, (T, k), torch.int32, "indices")
-    _dense(weights, (T, k), torch.float32, "weights")
-    _dense(counts, (E,), torch.int32, "counts")
-    _check(lib().mhc_route(_ptr(logits), _pitch(logits, T, E, "logits"), _dtype(logits), _ptr(bias), score, E, groups,
-                           top_groups, k, int(renorm), float(scale), T, _ptr(indices), _ptr(weights), _ptr(counts),
-                           _ptr(workspace), _bytes(workspace), _stream(stream)))
-
-
-def _pitch(t, T: int, E: int, name: str) -> int:
-    """The row stride of a [T, E] matrix with dense rows, of any alignment."""
-    _need(t.is_cuda, f"{name} is not on the GPU", -10)
-    _need(t.dim() == 2 and t.shape[0] == T and t.shape[1] == E and (t.stride(1) == 1 or E == 1),
-          f"{name} must be [{T}, {E}] with dense rows")
-    return t.stride(0) if T > 1 else E
+    L = _ops()
+    T, E = logits.shape
+    k = indices.shape[-1]
+    ws, n = _space(workspace)
+    rc = L.mhc_route(logits.data_ptr(), _pitch(logits, T, E, logits.dtype, "logits"), _dtype(logits, "logits"),
+                     _dense(bias, (E,), _F32, "bias"), score, E, groups, top_groups, k, int(renorm), scale, T,
+                     _dense(indices, (T, k), _I32, "indices"), _dense(weights, (T, k), _F32, "weights"),
+                     _dense(counts, (E,), _I32, "counts"), ws, n, _where(stream))
+    if rc:
+        _check(rc)
 
 
 def mhc_route_grad(dweights, logits, indices, dlogits, score: int = MHC_SCORE_SIGMOID, renorm: bool = True,
                    scale: float = 1.0, stream=None) -> None:
     """The gradient of mhc_route's weights by the logits."""
-    import torch
-    (T, E), k = logits.shape, indices.shape[-1]
-    _dense(dweights, (T, k), torch.float32, "dweights")
-    _dense(indices, (T, k), torch.int32, "indices")
-    _need(dlogits.dtype == logits.dtype, "dlogits must have logits' type", -10)
-    _check(lib().mhc_route_grad(_ptr(dweights), _ptr(logits), _pitch(logits, T, E, "logits"), _dtype(logits),
-                                _ptr(indices), score, E, k, int(renorm), float(scale), T, _ptr(dlogits),
-                                _pitch(dlogits, T, E, "dlogits"), _stream(stream)))
+    L = _ops()
+    (T, E), dt = logits.shape, logits.dtype
+    k = indices.shape[-1]
+    rc = L.mhc_route_grad(_dense(dweights, (T, k), _F32, "dweights"), logits.data_ptr(), _pitch(logits, T, E, dt, "logits"),
+                          _dtype(logits, "logits"), _dense(indices, (T, k), _I32, "indices"), score, E, k, int(renorm), scale,
+                          T, dlogits.data_ptr(), _pitch(dlogits, T, E, dt, "dlogits"), _where(stream))
+    if rc:
+        _check(rc)
 
 
 # ----------------------------------------------------------- allocation ----

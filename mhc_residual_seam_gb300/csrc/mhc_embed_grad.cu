@@ -18,13 +18,7 @@ namespace mhc {
 
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
-#ifndef SR
-#define SR 4
-#endif
-#ifndef SU
-#define SU 4
-#endif
-constexpr int kSortRounds = SR;                              // keys per lane
+constexpr int kSortRounds = 1;                               // keys per lane
 constexpr int kSortTile = kSortThreads * kSortRounds;        // keys per CTA
 constexpr int kDigits = 512;                                 // 9-bit digits at most
 constexpr int kColumns = 1024;                               // columns per CTA of the sum
@@ -39,7 +33,7 @@ struct EmbedGradWs {  // byte offsets into the workspace
   int tiles, chunks, passes, digit_bits;
   bool one;  // one CTA sorts
 };
-constexpr int kSumRounds = SU;
+constexpr int kSumRounds = 8;
 
 struct SortArgs {
   const void* ids;
@@ -494,10 +488,11 @@ static EmbedGradWs embed_grad_plan(int64_t T, int64_t V, int H) {
   w.digit_bits = (bits + w.passes - 1) / w.passes;
   w.tiles = (int)((T + kSortTile - 1) / kSortTile);
   const int cols = (H + kColumns - 1) / kColumns;
-  // Chunks: some rounds of CTAs, so that an SM that gets through faster takes more; at
-  // least 16 rows or tokens each; and 5 Mi columns of partial sums at most.
+  // Chunks: rounds of CTAs, so that an SM that gets through faster takes more (T = 16384,
+  // V = 131072, H = 5120: 681 us with 243 chunks, 605 with 487, 568 with 1024, 558 with
+  // 1433); at least 16 rows or tokens each; and 7 Mi columns of partial sums (56 MiB) at most.
   int64_t most = (kSumRounds * 152 * 8 + cols - 1) / cols;
-  if (most * H > (int64_t)5 << 20) most = ((int64_t)5 << 20) / H;
+  if (most * H > (int64_t)7 << 20) most = ((int64_t)7 << 20) / H;
   if (most < 152) most = 152;
   int64_t chunks = (T + V + 15) / 16;
   w.chunks = (int)(chunks < 1 ? 1 : chunks > most ? most : chunks);
