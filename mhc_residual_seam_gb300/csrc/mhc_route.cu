@@ -629,6 +629,8 @@ struct RouteGradArgs {
   float scale;
   void* dlogits;
   int64_t ld_d;
+  int log_slots, rows, pad;  // slots per token (log2), tokens per warp, floats of a row in shared memory
+  bool vector;               // rows of dlogits are 16-byte pieces
 };
 
 template <typename T>
@@ -637,53 +639,125 @@ __device__ __forceinline__ void store_one(T* p, float x) {
   else *reinterpret_cast<uint16_t*>(p) = (uint16_t)word_of(x, 0.f, T());
 }
 
-// One warp per token; lane j < k holds slot j.  The row of gradients is put
-// together in shared memory.
-template <typename T, int EPL>
+// A row of gradients from the sums of its slots, through shared memory: `rows` rows
+// of `pad` floats per warp, zero but where a slot has added to them.
+template <typename T>
+__device__ __forceinline__ void store_row(T* d, const float* src, int E, bool vector) {
+  const int id = threadIdx.x & 31;
+  if (vector) {
+    constexpr int N = 16 / (int)sizeof(T);
+    for (int i = id * N; i < E; i += 32 * N) {
+      if constexpr (sizeof(T) == 4) {
+        __stcs(reinterpret_cast<float4*>(d + i), *reinterpret_cast<const float4*>(src + i));
+      } else {
+        const float4 x = *reinterpret_cast<const float4*>(src + i), y = *reinterpret_cast<const float4*>(src + i + 4);
+        __stcs(reinterpret_cast<uint4*>(d + i),
+               make_uint4(word_of(x.x, x.y, T()), word_of(x.z, x.w, T()), word_of(y.x, y.y, T()), word_of(y.z, y.w, T())));
+      }
+    }
+  } else {
+    for (int i = id; i < E; i += 32) store_one(d + i, src[i]);
+  }
+}
+
+// Gradients that only the chosen experts have (sigmoid scores, or softmax
+// renormalised over the k): with q = v / sum v and v the score,
+//   renorm:  dl = scale q (dw - sum q dw) (1 - v for a sigmoid),   else dl = scale dw v (1 - v).
+// One slot per lane, as many tokens per warp as have room; their rows are put
+// together in shared memory, written in 16-byte stores, and the slots' places set
+// back to zero.  Bound by the rows written (T = 131072, E = 256, fp32: 134 MB) and
+// the chosen logits read (a 64-byte burst of DRAM each: 67 MB): 37 us of the 31 that
+// these take at the copy's rate.  Loading the next batch's slots ahead did not change it.
+template <typename T>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_grad_kernel(const RouteGradArgs a) {
-  __shared__ float rows[kRouteWarps][EPL * 32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float* out = rows[warp];
+  extern __shared__ float4 dyn[];
+  const int id = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float* const rows = reinterpret_cast<float*>(dyn) + warp * a.rows * a.pad;
+  for (int i = id; i < a.rows * a.pad; i += 32) rows[i] = 0.f;
+  const int slots = 1 << a.log_slots, tok = id >> a.log_slots, at = id & (slots - 1);
+  const int64_t step = (int64_t)gridDim.x * kRouteWarps * a.rows;
+  __syncwarp();
+  for (int64_t base = ((int64_t)blockIdx.x * kRouteWarps + warp) * a.rows; base < a.T; base += step) {
+    const int64_t t = base + tok;
+    int e = -1;
+    float dw = 0.f, v = 0.f, l = -INFINITY;
+    if (tok < a.rows && t < a.T && at < a.k) {
+      e = a.indices[t * a.k + at];
+      if (e >= a.E) e = -1;
+      if (e >= 0) {
+        dw = a.dweights[t * a.k + at];
+        l = logit_of(static_cast<const T*>(a.logits) + t * a.ld + e);
+      }
+    }
+    if (a.sigmoid) {
+      if (e >= 0) v = logistic(l);
+    } else {
+      float m = l;
+      for (int d = slots >> 1; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+      v = soft_exp(l, m);
+    }
+    float d;
+    if (a.renorm) {
+      float total = v;
+      for (int s = slots >> 1; s; s >>= 1) total += __shfl_xor_sync(0xffffffffu, total, s);
+      const float q = total > 0.f ? v / total : 0.f;
+      float mean = q * dw;
+      for (int s = slots >> 1; s; s >>= 1) mean += __shfl_xor_sync(0xffffffffu, mean, s);
+      d = a.scale * q * (dw - mean);
+      if (a.sigmoid) d *= 1.f - v;
+    } else {
+      d = a.scale * dw * v * (1.f - v);
+    }
+    if (e >= 0) atomicAdd(&rows[tok * a.pad + e], d);  // (a token names an expert once; twice adds up)
+    __syncwarp();
+    const int n = (int)(a.T - base < a.rows ? a.T - base : a.rows);
+    T* out = static_cast<T*>(a.dlogits) + base * a.ld_d;
+    for (int i = 0; i < n; ++i, out += a.ld_d) store_row(out, rows + i * a.pad, a.E, a.vector);
+    __syncwarp();
+    if (e >= 0) rows[tok * a.pad + e] = 0.f;
+    __syncwarp();
+  }
+}
+
+// Softmax without renormalisation, where every logit has a gradient:
+//   dl_m = scale p_m (dw_m [m chosen] - sum over the chosen of p dw).
+// One warp per token, the row in registers (EPL per lane, a lane's 32 apart).
+template <typename T, int EPL>
+__global__ void __launch_bounds__(kRouteWarps * 32) route_grad_dense_kernel(const RouteGradArgs a) {
+  __shared__ float up_[kRouteWarps][EPL * 32];
+  const int id = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float* const up = up_[warp];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) up[i * 32 + id] = 0.f;
+  __syncwarp();
   for (int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp; t < a.T; t += (int64_t)gridDim.x * kRouteWarps) {
     const T* row = static_cast<const T*>(a.logits) + t * a.ld;
-    int e = lane < a.k ? a.indices[t * a.k + lane] : -1;
+    int e = id < a.k ? a.indices[t * a.k + id] : -1;
     if (e >= a.E) e = -1;
-    const float dw = e >= 0 ? a.dweights[t * a.k + lane] : 0.f;
-    const float l = e >= 0 ? logit_of(row + e) : -INFINITY;
-    for (int i = lane; i < a.E; i += 32) out[i] = 0.f;
-    __syncwarp();
-    if (a.sigmoid || a.renorm) {
-      float v, d;
-      if (a.sigmoid) v = e >= 0 ? logistic(l) : 0.f;
-      else v = soft_exp(l, warp_max(l));
-      if (a.renorm) {
-        const float total = warp_sum(v);
-        const float q = total > 0.f ? v / total : 0.f;
-        const float mean = warp_sum(q * dw);
-        d = a.scale * q * (dw - mean);
-        if (a.sigmoid) d *= 1.f - v;
-      } else {
-        d = a.scale * dw * v * (1.f - v);
-      }
-      if (e >= 0) atomicAdd(&out[e], d);
-      __syncwarp();
-    } else {
-      float m = -INFINITY, total = 0.f;
-      for (int i = lane; i < a.E; i += 32) m = fmaxf(m, logit_of(row + i));
-      m = warp_max(m);
-      for (int i = lane; i < a.E; i += 32) total += soft_exp(logit_of(row + i), m);
-      total = warp_sum(total);
-      const float mean = warp_sum(total > 0.f ? soft_exp(l, m) / total * dw : 0.f);
-      if (e >= 0) atomicAdd(&out[e], dw);
-      __syncwarp();
-      for (int i = lane; i < a.E; i += 32) {
-        const float p = total > 0.f ? soft_exp(logit_of(row + i), m) / total : 0.f;
-        out[i] = a.scale * p * (out[i] - mean);
-      }
-      __syncwarp();
+    const float dw = e >= 0 ? a.dweights[t * a.k + id] : 0.f;
+    float p[EPL], m = -INFINITY, total = 0.f;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      p[i] = i * 32 + id < a.E ? logit_of(row + i * 32 + id) : -INFINITY;
+      m = fmaxf(m, p[i]);
     }
+    m = warp_max(m);
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      p[i] = soft_exp(p[i], m);
+      total += p[i];
+    }
+    total = warp_sum(total);
+    const float share = total > 0.f ? 1.f / total : 0.f;
+    const float mean = warp_sum(e >= 0 ? soft_exp(logit_of(row + e), m) * share * dw : 0.f);
+    if (e >= 0) atomicAdd(&up[e], dw);
+    __syncwarp();
     T* d = static_cast<T*>(a.dlogits) + t * a.ld_d;
-    for (int i = lane; i < a.E; i += 32) store_one(d + i, out[i]);
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      if (i * 32 + id < a.E) store_one(d + i * 32 + id, a.scale * (p[i] * share) * (up[i * 32 + id] - mean));
+    __syncwarp();
+    if (e >= 0) up[e] = 0.f;
     __syncwarp();
   }
 }
@@ -818,12 +892,25 @@ int mhc_route_grad(const float* dweights, const void* logits, int64_t ld, mhc_dt
   int sms = 0;
   cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return ops_cuda(e, "device query");
-  const RouteGradArgs a = {dweights, logits, ld, T, indices, E, k, score == MHC_SCORE_SIGMOID, renorm != 0, scale,
-                           dlogits, ld_d};
-  int64_t grid = (T + kRouteWarps - 1) / kRouteWarps;
-  if (grid > (int64_t)sms * 12) grid = (int64_t)sms * 12;
+  RouteGradArgs a = {dweights, logits, ld, T, indices, E, k, score == MHC_SCORE_SIGMOID, renorm != 0, scale,
+                     dlogits, ld_d, 0, 1, (E + 3) / 4 * 4, false};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  MHC_BY_DTYPE(dtype, D, { MHC_BY_EXPERTS(E, { route_grad_kernel<D, N><<<(unsigned)grid, kRouteWarps * 32, 0, s>>>(a); }) });
+  const int64_t most = (int64_t)sms * 2 * kRouteCtas;
+  if (!a.sigmoid && !a.renorm) {
+    const int64_t grid = (T + kRouteWarps - 1) / kRouteWarps;
+    MHC_BY_DTYPE(dtype, D, {
+      MHC_BY_EXPERTS(E, { route_grad_dense_kernel<D, N><<<(unsigned)(grid < most ? grid : most), kRouteWarps * 32, 0, s>>>(a); })
+    });
+  } else {
+    while ((1 << a.log_slots) < k) ++a.log_slots;
+    // tokens of a warp: one slot per lane, 8 KB of rows, and enough warps for every scheduler
+    a.rows = 32 >> a.log_slots;
+    while (a.rows > 1 && (a.rows * a.pad * 4 > 8192 || T < (int64_t)sms * 16 * a.rows)) a.rows >>= 1;
+    a.vector = E * b % 16 == 0 && ld_d * b % 16 == 0 && ops_aligned(dlogits, 16);
+    const int64_t grid = (T + kRouteWarps * a.rows - 1) / (kRouteWarps * a.rows);
+    const size_t smem = (size_t)kRouteWarps * a.rows * a.pad * 4;
+    MHC_BY_DTYPE(dtype, D, { route_grad_kernel<D><<<(unsigned)(grid < most ? grid : most), kRouteWarps * 32, smem, s>>>(a); });
+  }
   return ops_cuda(cudaGetLastError(), "route_grad launch");
 }
 
