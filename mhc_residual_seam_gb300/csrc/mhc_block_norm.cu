@@ -429,46 +429,52 @@ __global__ void __launch_bounds__(BIG ? kBigThreads : kTeamThreads) block_norm_g
   for (int i = 0; i < VPT; ++i) {
     const int g = q.lane + i * q.lanes;
     if (on(i)) {
-      if (has_y) st8(out + g * 8, pack<float>(s_post[i]));
+      if (a.dgamma_post || a.gate_mode == MHC_GATE_CHANNEL) st8(out + g * 8, pack<float>(s_post[i]));
       if (has_pre) st8(out + a.H + g * 8, pack<float>(s_pre[i]));
     }
   }
 }
 
 // Adds the teams' column sums in a fixed order and finishes the weights'
-// gradients: 128 columns x 32 slices of teams per CTA, four columns a thread, the
-// slices joined in slice order.
-template <typename T>
+// gradients: 32 * N columns x 32 slices of teams per CTA, N columns a thread (four
+// for wide rows, one where that leaves most SMs idle), the slices joined in slice
+// order.
+template <typename T, int N>
 __global__ void __launch_bounds__(1024) block_norm_fold_kernel(const BlockNormGradArgs a, int n) {
-  __shared__ float4 sh[32][32];
+  struct alignas(N * 4) Cols {
+    float v[N];
+  };
+  __shared__ Cols sh[32][32];
   pdl_wait();
   const bool post = blockIdx.y == 0;
   const bool channel = a.gate_mode == MHC_GATE_CHANNEL;
   if (post ? !a.dgamma_post && !channel : !a.dgamma_pre) return;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int c = (blockIdx.x * 32 + lane) * 4;
-  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto add = [&](const float4& v) { x.x += v.x, x.y += v.y, x.z += v.z, x.w += v.w; };
+  const int c = (blockIdx.x * 32 + lane) * N;
+  Cols x = {};
+  auto add = [&](const Cols& o) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) x.v[e] += o.v[e];
+  };
   if (c < a.H) {
     const float* p = a.parts + (post ? 0 : a.H) + c;
     const int lo = (int)((int64_t)n * w / 32), hi = (int)((int64_t)n * (w + 1) / 32);
 #pragma unroll 8
-    for (int i = lo; i < hi; ++i) add(*reinterpret_cast<const float4*>(p + (int64_t)i * 2 * a.H));
+    for (int i = lo; i < hi; ++i) add(*reinterpret_cast<const Cols*>(p + (int64_t)i * 2 * a.H));
   }
   sh[w][lane] = x;
   __syncthreads();
   if (w || c >= a.H) return;
 #pragma unroll 8
   for (int i = 1; i < 32; ++i) add(sh[i][lane]);
-  const float v[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
+  for (int e = 0; e < N; ++e) {
     if (!post) {
-      a.dgamma_pre[c + e] = v[e];
+      a.dgamma_pre[c + e] = x.v[e];
       continue;
     }
-    if (a.dgamma_post) a.dgamma_post[c + e] = v[e] * (channel ? weight1<T>(a.gate, c + e) : 1.f);
-    if (channel) a.dgate[c + e] = v[e] * (a.gamma_post ? weight1<T>(a.gamma_post, c + e) : 1.f);
+    if (a.dgamma_post) a.dgamma_post[c + e] = x.v[e] * (channel ? weight1<T>(a.gate, c + e) : 1.f);
+    if (channel) a.dgate[c + e] = x.v[e] * (a.gamma_post ? weight1<T>(a.gamma_post, c + e) : 1.f);
   }
 }
 
@@ -700,7 +706,10 @@ int mhc_block_norm_grad(const void* dr_out, const void* dnorm, const void* y, co
   cudaError_t e = cudaSuccess;
   MHC_BY_DTYPE(dtype, E, { MHC_BY_TEAM(plan, full, { e = grad_launch<E, N, W, L, K, F>(a, plan, grid, s); }) });
   if (e == cudaSuccess && (dgamma_post || dgamma_pre || channel))
-    MHC_BY_DTYPE(dtype, E, { e = launch_pdl(block_norm_fold_kernel<E>, dim3((H + 127) / 128, 2), dim3(1024), 0, s, a, parts); });
+    MHC_BY_DTYPE(dtype, E, {
+      e = H >= 4096 ? launch_pdl(block_norm_fold_kernel<E, 4>, dim3((H + 127) / 128, 2), dim3(1024), 0, s, a, parts)
+                    : launch_pdl(block_norm_fold_kernel<E, 1>, dim3((H + 31) / 32, 2), dim3(1024), 0, s, a, parts);
+    });
   return ops_cuda(e, "block_norm_grad launch");
 }
 

@@ -343,9 +343,10 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const SumArgs a)
     cut(a, n, weight * chunk / a.chunks, &sb.a0, &sb.b0);
     __syncwarp();
     if (threadIdx.x == 0) before = sb.a0 ? (int)a.key[sb.a0 - 1] : -1;
-  } else if (threadIdx.x < 64) {
+  }
+  if (threadIdx.x >= 32 ? threadIdx.x < 64 : blockDim.x == 32) {
     if (chunk + 1 < a.chunks) cut(a, n, weight * (chunk + 1) / a.chunks, &sb.a1, &sb.b1);
-    else if (threadIdx.x == 32) sb.a1 = n, sb.b1 = (int)a.V;
+    else if ((threadIdx.x & 31) == 0) sb.a1 = n, sb.b1 = (int)a.V;
   }
   __syncthreads();
   pdl_launch();
@@ -379,7 +380,7 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const SumArgs a)
   for (int w = b.a0; w < b.a1; w += kWindow) {
     const int m = min(kWindow, b.a1 - w);
     __syncthreads();
-    for (int i = threadIdx.x; i < m; i += kSumThreads) {
+    for (int i = threadIdx.x; i < m; i += blockDim.x) {
       wkey[i] = (int)a.key[w + i];
       wtok[i] = a.tok[w + i];
     }
@@ -449,7 +450,7 @@ __global__ void __launch_bounds__(kSumThreads) embed_join_kernel(const SumArgs a
   const int row = b.b0;
   if (b.a0 == 0 || row >= b.b1 || (int)a.key[b.a0 - 1] != row) return;
   // the chunk that holds the row's first token: the last one before this that did not begin inside the row
-  for (int hi = chunk - 1;; hi -= kSumThreads) {
+  for (int hi = chunk - 1;; hi -= (int)blockDim.x) {
     if (threadIdx.x == 0) first = -1;
     __syncthreads();
     const int k = hi - (int)threadIdx.x;
@@ -458,7 +459,7 @@ __global__ void __launch_bounds__(kSumThreads) embed_join_kernel(const SumArgs a
       if (!(p.b0 == row && p.a0 > 0 && (int)a.key[p.a0 - 1] == row)) atomicMax(&first, k);
     }
     __syncthreads();
-    if (first >= 0 || hi < kSumThreads) break;
+    if (first >= 0 || hi < (int)blockDim.x) break;
     __syncthreads();
   }
   const int64_t c = (int64_t)blockIdx.y * kColumns + threadIdx.x * 8;
@@ -516,13 +517,14 @@ static EmbedGradWs embed_grad_plan(int64_t T, int64_t V, int H) {
 template <typename T>
 static cudaError_t sum_launch(const SumArgs& a, int grad_dtype, dim3 grid, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
+  const int threads = a.H >= kColumns ? kSumThreads : (a.H / 8 + 31) / 32 * 32;
   auto go = [&](auto o) {
     using O = decltype(o);
-    if (a.streams == 1) e = launch_pdl(embed_sum_kernel<T, O, 1>, grid, dim3(kSumThreads), 0, s, a);
-    else if (a.streams == 2) e = launch_pdl(embed_sum_kernel<T, O, 2>, grid, dim3(kSumThreads), 0, s, a);
-    else if (a.streams == 4) e = launch_pdl(embed_sum_kernel<T, O, 4>, grid, dim3(kSumThreads), 0, s, a);
-    else e = launch_pdl(embed_sum_kernel<T, O, 0>, grid, dim3(kSumThreads), 0, s, a);
-    if (e == cudaSuccess && a.chunks > 1) e = launch_pdl(embed_join_kernel<O>, grid, dim3(kSumThreads), 0, s, a);
+    if (a.streams == 1) e = launch_pdl(embed_sum_kernel<T, O, 1>, grid, dim3(threads), 0, s, a);
+    else if (a.streams == 2) e = launch_pdl(embed_sum_kernel<T, O, 2>, grid, dim3(threads), 0, s, a);
+    else if (a.streams == 4) e = launch_pdl(embed_sum_kernel<T, O, 4>, grid, dim3(threads), 0, s, a);
+    else e = launch_pdl(embed_sum_kernel<T, O, 0>, grid, dim3(threads), 0, s, a);
+    if (e == cudaSuccess && a.chunks > 1) e = launch_pdl(embed_join_kernel<O>, grid, dim3(threads), 0, s, a);
   };
   if (grad_dtype == MHC_DT_F32) go(float());
   else go(T());
