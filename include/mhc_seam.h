@@ -321,6 +321,7 @@ int mhc_embed_grad(const void* ids, int id_bytes, const void* dout, mhc_dtype dt
  *             the seam's gates); MHC_GATE_NONE: NULL
  *   rstd_post, rstd_pre  [T] fp32: 1/rms of y and of r_out, for the gradient;
  *             required where their gamma is given
+ * r NULL: no residual, r_out = gate * p (what the seam takes as its Y).
  * y NULL is the norm before the first block: norm = r / rms(r) * gamma_pre, and
  * r_out is not written (gamma_post and the gate must be absent, else
  * MHC_ERR_INCOMPLETE_POST).  H <= 16384, T < 2^31.  Errors: MHC_ERR_CONFIG,
@@ -341,7 +342,8 @@ size_t mhc_block_norm_grad_workspace_bytes(int64_t T, int H);
  *   dr_out     NULL: zero (then gamma_pre must be given)
  *   dnorm, r_out, rstd_pre, dgamma_pre  used where gamma_pre is given; without y,
  *              r_out is the forward call's r
- *   dy         required where y is given;  dr always
+ *   dy         required where y is given;  dr NULL: not wanted (the forward call had
+ *              no r; then y must be given)
  *   dgamma_post, dgamma_pre [H] fp32, dgate [H] (channel) or [T] (token) fp32:
  *              required where their weight is given; written, not added to (zero
  *              for T = 0)

@@ -371,11 +371,13 @@ def mhc_block_norm(y, r, gamma_post, gate, gamma_pre, r_out, norm, rstd_post, rs
     """Norm after a block, gate, residual add and norm before the next block;
     y, r, r_out and norm are [T, H] (rows may be strided)."""
     L = _ops()
-    (T, H), dt = r.shape, r.dtype
+    x = y if r is None else r
+    (T, H), dt = x.shape, x.dtype
     rc = L.mhc_block_norm(
-        None if y is None else y.data_ptr(), _pitch(y, T, H, dt, "y"), r.data_ptr(), _pitch(r, T, H, dt, "r"),
+        None if y is None else y.data_ptr(), _pitch(y, T, H, dt, "y"),
+        None if r is None else r.data_ptr(), _pitch(r, T, H, dt, "r"),
         _dense(gamma_post, (H,), dt, "gamma_post"), _gate(gate, gate_mode, T, H, dt), gate_mode,
-        _dense(gamma_pre, (H,), dt, "gamma_pre"), res_scale, eps, T, H, _dtype(r, "r"),
+        _dense(gamma_pre, (H,), dt, "gamma_pre"), res_scale, eps, T, H, _dtype(x, "r"),
         None if r_out is None else r_out.data_ptr(), _pitch(r_out, T, H, dt, "r_out"),
         None if norm is None else norm.data_ptr(), _pitch(norm, T, H, dt, "norm"),
         _dense(rstd_post, (T,), _F32, "rstd_post"), _dense(rstd_pre, (T,), _F32, "rstd_pre"), _where(stream))
@@ -393,14 +395,15 @@ def mhc_block_norm_grad(dr_out, dnorm, y, r_out, gamma_post, gate, gamma_pre, rs
     """The gradient of mhc_block_norm; all matrices are dense [T, H], the
     weights' gradients fp32."""
     L = _ops()
-    shape, dt = dr.shape, dr.dtype
+    x = dy if dr is None else dr
+    shape, dt = x.shape, x.dtype
     T, H = shape
     ws, n = _space(workspace)
     rc = L.mhc_block_norm_grad(
         _dense(dr_out, shape, dt, "dr_out"), _dense(dnorm, shape, dt, "dnorm"), _dense(y, shape, dt, "y"),
         _dense(r_out, shape, dt, "r_out"), _dense(gamma_post, (H,), dt, "gamma_post"), _gate(gate, gate_mode, T, H, dt),
         gate_mode, _dense(gamma_pre, (H,), dt, "gamma_pre"), _dense(rstd_post, (T,), _F32, "rstd_post"),
-        _dense(rstd_pre, (T,), _F32, "rstd_pre"), res_scale, T, H, _dtype(dr, "dr"), _dense(dy, shape, dt, "dy"),
+        _dense(rstd_pre, (T,), _F32, "rstd_pre"), res_scale, T, H, _dtype(x, "dr"), _dense(dy, shape, dt, "dy"),
         _dense(dr, shape, dt, "dr"), _dense(dgamma_post, (H,), _F32, "dgamma_post"),
         _dense(dgate, (T,) if gate_mode == MHC_GATE_TOKEN else (H,), _F32, "dgate"),
         _dense(dgamma_pre, (H,), _F32, "dgamma_pre"), ws, n, _where(stream))

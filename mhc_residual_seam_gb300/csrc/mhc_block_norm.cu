@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kBigThreads) block_norm_kernel(const BlockNorm
   const Team<WARP> q;
   const int segs = a.H >> 3;
   const float inv = 1.0f / (float)a.H;
-  const bool has_y = FULL || a.y, has_post = FULL || a.gamma_post, has_pre = FULL || a.gamma_pre;
+  const bool has_y = FULL || a.y, has_r = FULL || a.r, has_post = FULL || a.gamma_post, has_pre = FULL || a.gamma_pre;
   const char* y = static_cast<const char*>(a.y);
   const char* r = static_cast<const char*>(a.r);
   const float* gates = a.gate_mode == MHC_GATE_TOKEN ? static_cast<const float*>(a.gate) : nullptr;
@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kBigThreads) block_norm_kernel(const BlockNorm
 #pragma unroll
       for (int i = 0; i < VPT; ++i)
         if (on(i)) {
-          fetch8<T>(slot + m.smem[i], m.plane, pr + m.col[i]);
+          if (has_r) fetch8<T>(slot + m.smem[i], m.plane, pr + m.col[i]);
           if (has_y) fetch8<T>(slot + m.matrix + m.smem[i], m.plane, py + m.col[i]);
         }
       if (gates && (threadIdx.x & 31) == 0) cp_async4(scalar, gates + t);
@@ -194,7 +194,8 @@ __global__ void __launch_bounds__(kBigThreads) block_norm_kernel(const BlockNorm
       if (on(i)) {
         const char* pr = r + t * (a.ld_r * (int)sizeof(T)) + m.col[i];
         const char* py = y + t * (a.ld_y * (int)sizeof(T)) + m.col[i];
-        x[i] = unpack(STAGES ? fetched8<T>(slot + m.smem[i], m.plane) : ld8_stream(reinterpret_cast<const T*>(pr)));
+        if (has_r)
+          x[i] = unpack(STAGES ? fetched8<T>(slot + m.smem[i], m.plane) : ld8_stream(reinterpret_cast<const T*>(pr)));
         if (has_y)
           p[i] = unpack(STAGES ? fetched8<T>(slot + m.matrix + m.smem[i], m.plane) : ld8_stream(reinterpret_cast<const T*>(py)));
       }
@@ -369,7 +370,7 @@ __global__ void __launch_bounds__(BIG ? kBigThreads : kTeamThreads) block_norm_g
     char* dr = static_cast<char*>(a.dr) + row;
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
-      if (on(i)) {
+      if ((FULL || a.dr) && on(i)) {
         Vec8 o;
 #pragma unroll
         for (int e = 0; e < 4; ++e) o.p[e] = __fmul2_rn(G[i].p[e], splat(a.scale));
@@ -593,13 +594,13 @@ int mhc_block_norm(const void* y, int64_t ld_y, const void* r, int64_t ld_r, con
   if (T == 0) return MHC_OK;
   if (!y) r_out = nullptr;
   if (!gamma_pre) norm = nullptr;
-  if (!r || (y && !r_out) || (gamma_pre && (!norm || !rstd_pre)) || (gamma_post && !rstd_post))
+  if ((!r && !y) || (y && !r_out) || (gamma_pre && (!norm || !rstd_pre)) || (gamma_post && !rstd_post))
     return ops_fail(MHC_ERR_NULL, "a required pointer is NULL");
   if ((gate_mode != MHC_GATE_NONE) != (gate != nullptr))
     return ops_fail(MHC_ERR_NULL, "gate must be given exactly when gate_mode is not none");
   if (!y && (gamma_post || gate || !gamma_pre))
     return ops_fail(MHC_ERR_INCOMPLETE_POST, "without y the call is the norm before the first block: gamma_pre only");
-  const int64_t lds[] = {y ? ld_y : H, ld_r, y ? ld_r_out : H, gamma_pre ? ld_norm : H};
+  const int64_t lds[] = {y ? ld_y : H, r ? ld_r : H, y ? ld_r_out : H, gamma_pre ? ld_norm : H};
   for (int64_t ld : lds)
     if (ld < H || ld % 8 != 0) return ops_fail(MHC_ERR_SHAPE, "row strides must be multiples of 8, at least H");
   const void* a16[] = {y, r, gamma_post, gate_mode == MHC_GATE_CHANNEL ? gate : nullptr, gamma_pre, r_out, norm};
@@ -615,7 +616,7 @@ int mhc_block_norm(const void* y, int64_t ld_y, const void* r, int64_t ld_r, con
                       {gamma_pre ? rstd_pre : nullptr, 1, T, T, 4}};
   for (int o = 0; o < 4; ++o) {
     for (int i = 0; i < 5; ++i)
-      if (!(o == 0 && i == 1 && r_out == r && ld_r_out == ld_r) && rows_overlap(out[o], in[i]))
+      if (!(o == 0 && i == 1 && r_out && r_out == r && ld_r_out == ld_r) && rows_overlap(out[o], in[i]))
         return ops_fail(MHC_ERR_ALIAS, "an output overlaps an input");
     for (int q = o + 1; q < 4; ++q)
       if (rows_overlap(out[o], out[q])) return ops_fail(MHC_ERR_ALIAS, "two outputs overlap");
@@ -623,7 +624,7 @@ int mhc_block_norm(const void* y, int64_t ld_y, const void* r, int64_t ld_r, con
   BlockNormArgs a = {y, r, gamma_post, gate, gamma_pre, ld_y, ld_r, ld_r_out, ld_norm, gate_mode, res_scale, eps,
                            T, H, r_out, norm, rstd_post, rstd_pre, 1};
   const TeamPlan plan = norm_plan(H, b);
-  const bool full = y && gamma_post && gamma_pre && even_columns(H, plan);
+  const bool full = y && r && gamma_post && gamma_pre && even_columns(H, plan);
   a.run = norm_run(T, plan);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
@@ -670,7 +671,7 @@ int mhc_block_norm_grad(const void* dr_out, const void* dnorm, const void* y, co
       }
     return MHC_OK;
   }
-  if ((!dr_out && !gamma_pre) || !dr || (y && !dy) || (gamma_pre && (!dnorm || !r_out || !rstd_pre)) ||
+  if ((!dr_out && !gamma_pre) || (!dr && !y) || (y && !dy) || (gamma_pre && (!dnorm || !r_out || !rstd_pre)) ||
       (gamma_post && !rstd_post))
     return ops_fail(MHC_ERR_NULL, "a required pointer is NULL");
   if (!y && (gamma_post || gate || !gamma_pre))
@@ -699,7 +700,7 @@ int mhc_block_norm_grad(const void* dr_out, const void* dnorm, const void* y, co
   BlockNormGradArgs a = {dr_out, dnorm, y, r_out, gamma_post, gate, gamma_pre, rstd_post, rstd_pre, gate_mode,
                                res_scale, T, H, dy, dr, dgamma_post, dgate, dgamma_pre, static_cast<float*>(workspace), 1};
   const TeamPlan plan = grad_plan(H, b);
-  const bool full = y && dr_out && gamma_post && gamma_pre && even_columns(H, plan);
+  const bool full = y && dr && dr_out && gamma_post && gamma_pre && even_columns(H, plan);
   a.run = grad_run(T, plan);
   const int64_t grid = grad_ctas(T, plan);
   const int parts = (int)grid * plan.teams;

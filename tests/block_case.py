@@ -62,7 +62,7 @@ def _gate(gate, mode):
 def block_norm(y, r, gamma_post, gate, mode, gamma_pre, scale, eps):
     """{name: value} with the sums of absolute terms under name + "_terms"."""
     out = {}
-    r = r.double()
+    r = torch.zeros_like(y, dtype=torch.float64) if r is None else r.double()
     if y is None:
         x, terms = r, r.abs()
     else:

@@ -221,6 +221,32 @@ def test_block_norm_without_y_and_in_place():
     check_block(d, "token", b)
 
 
+@pytest.mark.parametrize("T,H,dtype", [(5, 5120, BF16), (33, 264, F32), (9, 64, F16)])
+def test_block_norm_without_residual(T, H, dtype):
+    # r None: r_out = gate * p, which is what the seam takes as its Y; the gradient then has no dr
+    for mode, post, pre in FORMS:
+        d = block_inputs(T, H, dtype, mode, post, pre, 41)
+        d["r"] = None
+        e = lambda *s, t=F32: torch.full(s, 11.0, dtype=t, device="cuda")  # noqa: E731
+        o = {"r_out": e(T, H, t=dtype), "norm": e(T, H, t=dtype) if pre else None, "rstd_post": e(T) if post else None,
+             "rstd_pre": e(T) if pre else None}
+        B.mhc_block_norm(dev(d["y"]), None, dev(d["gamma_post"]), dev(d["gate"]), dev(d["gamma_pre"]), o["r_out"], o["norm"],
+                         o["rstd_post"], o["rstd_pre"], gate_mode=MODES[mode])
+        check_block(d, mode, o, scale=1.0)
+        d["r"] = d["y"]  # (the gradient's helpers take the shape from it)
+        q = run_grad(d, mode, o)
+        full = {k: v.clone() for k, v in q.items() if v is not None}
+        dy, again = torch.empty_like(q["dy"]), {k: None if v is None else torch.empty_like(v) for k, v in q.items()}
+        B.mhc_block_norm_grad(dev(d["dr_out"]), dev(d["dnorm"]), dev(d["y"]), o["r_out"], dev(d["gamma_post"]), dev(d["gate"]),
+                              dev(d["gamma_pre"]), o["rstd_post"], o["rstd_pre"], dy, None, again["dgamma_post"],
+                              again["dgate"], again["dgamma_pre"],
+                              workspace(B.mhc_block_norm_grad_workspace_bytes(T, H)), gate_mode=MODES[mode], res_scale=0.75)
+        R.check(dy, full["dy"].cpu().double(), full["dy"].cpu().double().abs(), n=8, what="dy")
+        for k in ("dgamma_post", "dgate", "dgamma_pre"):
+            if again[k] is not None:
+                R.check(again[k], full[k].cpu().double(), full[k].cpu().double().abs(), n=8, what=k)
+
+
 def test_block_norm_strided_streams():
     # r, r_out, y and norm as streams of [T,4,H] tensors: interleaved rows
     T, H = 21, 328

@@ -61,7 +61,7 @@ NORM = dict(y=A, ld_y=64, r=A + STEP, ld_r=64, gpost=A + 2 * STEP, gate=A + 3 * 
 @pytest.mark.parametrize("over,code", [
     (dict(dtype=9), -10), (dict(mode=3), -10), (dict(mode=-1), -10), (dict(eps=-1.0), -10), (dict(eps=math.nan), -10),
     (dict(T=-1), -2), (dict(H=12), -2), (dict(H=16392), -2), (dict(ld_y=60), -2), (dict(ld_r=56), -2), (dict(ld_n=0), -2),
-    (dict(r=None), -1), (dict(ro=None), -1), (dict(norm=None), -1), (dict(rp=None), -1), (dict(rq=None), -1),
+    (dict(r=None, y=None, gpost=None, gate=None, mode=0), -1), (dict(ro=None), -1), (dict(norm=None), -1), (dict(rp=None), -1), (dict(rq=None), -1),
     (dict(gate=None), -1), (dict(mode=0), -1), (dict(y=None), -4), (dict(y=None, gpost=None, gate=None, mode=0, gpre=None), -4),
     (dict(y=A + 8), -3), (dict(gpre=A + 4 * STEP + 2), -3), (dict(rp=A + 7 * STEP + 2), -3), (dict(ro=A), -9),
     (dict(ro=A + STEP, ld_ro=72), -9), (dict(ro=A + STEP + 16), -9), (dict(norm=A + 5 * STEP), -9), (dict(norm=A + STEP), -9),
@@ -78,7 +78,7 @@ BGRAD = dict(dro=A, dn=A + STEP, y=A + 2 * STEP, ro=A + 3 * STEP, gpost=A + 4 * 
 
 @pytest.mark.parametrize("over,code", [
     (dict(dtype=3), -10), (dict(mode=7), -10), (dict(T=-2), -2), (dict(H=20), -2), (dict(dn=None), -1), (dict(ro=None), -1),
-    (dict(rq=None), -1), (dict(rp=None), -1), (dict(dr=None), -1), (dict(dy=None), -1), (dict(dgp=None), -1),
+    (dict(rq=None), -1), (dict(rp=None), -1), (dict(dr=None, y=None), -1), (dict(dy=None), -1), (dict(dgp=None), -1),
     (dict(dgt=None), -1), (dict(dgq=None), -1), (dict(gate=None), -1), (dict(mode=0), -1), (dict(dro=None, gpre=None), -1),
     (dict(y=None), -4), (dict(dy=A + 9 * STEP + 2), -3), (dict(dgp=A + 2), -3), (dict(ws=A + 8), -3), (dict(ws=None), -5),
     (dict(ws_bytes=100), -5), (dict(dy=A), -9), (dict(dr=A + 9 * STEP), -9), (dict(ws=A + 2 * STEP), -9), (dict(dgp=A + 13 * STEP), -9)])
