@@ -18,8 +18,7 @@ namespace mhc {
 
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortRounds = 1;                               // keys per lane
-constexpr int kSortTile = kSortThreads * kSortRounds;        // keys per CTA
+constexpr int kFewTokens = 65536;                            // up to here a tile is kSortThreads tokens, above four times that
 constexpr int kDigits = 512;                                 // 9-bit digits at most
 constexpr int kColumns = 1024;                               // columns per CTA of the sum
 constexpr int kSumThreads = kColumns / 8;
@@ -29,7 +28,7 @@ struct Bounds {  // a chunk's first token and row, and the ones behind its last
 };
 
 struct EmbedGradWs {  // byte offsets into the workspace
-  size_t key[2], tok[2], hist, valid, bounds, carry, total;
+  size_t key[2], tok[2], hist, places, valid, bounds, carry, total;
   int tiles, chunks, passes, digit_bits;
   bool one;  // one CTA sorts
 };
@@ -44,6 +43,7 @@ struct SortArgs {
   int *tok_in, *tok_out;
   int *hist_in, *hist_out;  // [tiles][kDigits] of this pass and of the next one
   int passes;
+  int* places;              // [tiles][kDigits] of this pass: where a tile's keys of a digit go; null: from the counts
   int* valid;               // [tiles] tokens that have a row
 };
 
@@ -56,14 +56,15 @@ __device__ __forceinline__ uint32_t row_of(const SortArgs& a, int t) {
 
 // Digit counts of each tile for the first pass, the rows of the tokens, and
 // zeroed counts for the later passes (which follow the first one's).
-template <typename Id>
+template <typename Id, int R>
 __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const SortArgs a) {
+  constexpr int kSortTile = kSortThreads * R;
   __shared__ int count[kDigits];
   __shared__ int valid;
   for (int d = threadIdx.x; d < kDigits; d += kSortThreads) count[d] = 0;
   if (threadIdx.x == 0) valid = 0;
   __syncthreads();
-  const int base = blockIdx.x * kSortTile;
+  const int base = (int)blockIdx.x * kSortTile;
   int mine = 0;
   for (int i = threadIdx.x; i < kSortTile && base + i < a.T; i += kSortThreads) {
     const uint32_t k = row_of<Id>(a, base + i);
@@ -74,7 +75,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const SortArgs
   atomicAdd(&valid, mine);
   __syncthreads();
   for (int d = threadIdx.x; d < kDigits; d += kSortThreads) {
-    a.hist_in[blockIdx.x * kDigits + d] = count[d];
+    a.hist_in[(int64_t)blockIdx.x * kDigits + d] = count[d];
     for (int p = 1; p < a.passes; ++p) a.hist_in[((int64_t)p * a.tiles + blockIdx.x) * kDigits + d] = 0;
   }
   if (threadIdx.x == 0) a.valid[blockIdx.x] = valid;
@@ -177,10 +178,39 @@ __global__ void __launch_bounds__(kOneThreads) sort_one_kernel(const SortArgs a)
   }
 }
 
+// Turns the counts of many tiles into places, so that a pass need not read all of
+// them: for each digit the keys of smaller digits and of earlier tiles.  First the
+// digits' totals and the tiles' sums before (32 digits and 32 slices of tiles per
+// CTA); the smaller digits are added by the pass, from `totals`.
+__global__ void __launch_bounds__(1024) sort_places_kernel(const int* __restrict__ hist, int tiles, int* __restrict__ places,
+                                                           int* __restrict__ totals) {
+  __shared__ int sums[32][32];
+  pdl_wait();
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int64_t d = blockIdx.x * 32 + lane;
+  const int lo = (int)((int64_t)tiles * w / 32), hi = (int)((int64_t)tiles * (w + 1) / 32);
+  int sum = 0;
+#pragma unroll 8
+  for (int b = lo; b < hi; ++b) sum += hist[b * (int64_t)kDigits + d];
+  sums[w][lane] = sum;
+  __syncthreads();
+  int before = 0;
+  for (int i = 0; i < w; ++i) before += sums[i][lane];
+  if (w == 31) totals[d] = before + sum;
+#pragma unroll 8
+  for (int b = lo; b < hi; ++b) {
+    const int n = hist[b * (int64_t)kDigits + d];
+    places[b * (int64_t)kDigits + d] = before;
+    before += n;
+  }
+}
+
 // One pass of the stable sort: a key's place is the keys of smaller digits,
 // the same digit in earlier tiles, in earlier warps of the tile, and before it
 // in its warp (whose keys are taken in order, 32 at a time).
+template <int R>
 __global__ void __launch_bounds__(kSortThreads) sort_pass_kernel(const SortArgs a, bool identity, bool last) {
+  constexpr int kSortTile = kSortThreads * R, kSortRounds = R;
   __shared__ int start[kDigits];
   __shared__ int scan[kSortWarps];
   __shared__ unsigned short rank[kSortWarps][kDigits];
@@ -190,10 +220,15 @@ __global__ void __launch_bounds__(kSortThreads) sort_pass_kernel(const SortArgs 
   pdl_wait();
   // the digit's keys in all tiles and in the tiles before this one
   int before = 0, all = 0;
-  for (int b = 0; b < a.tiles; ++b) {
-    const int n = a.hist_in[b * kDigits + threadIdx.x];
-    before += b < (int)blockIdx.x ? n : 0;
-    all += n;
+  if (a.places) {
+    before = a.places[(int64_t)blockIdx.x * kDigits + threadIdx.x];
+    all = a.places[(int64_t)a.tiles * kDigits + threadIdx.x];
+  } else {
+    for (int b = 0; b < a.tiles; ++b) {
+      const int n = a.hist_in[b * kDigits + threadIdx.x];
+      before += b < (int)blockIdx.x ? n : 0;
+      all += n;
+    }
   }
   int x = all;
 #pragma unroll
@@ -207,7 +242,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_pass_kernel(const SortArgs 
   start[threadIdx.x] = x - all + before;
   uint32_t key[kSortRounds];
   int place[kSortRounds];
-  const int base = blockIdx.x * kSortTile + warp * 32 * kSortRounds;
+  const int base = (int)blockIdx.x * kSortTile + warp * 32 * kSortRounds;
 #pragma unroll
   for (int r = 0; r < kSortRounds; ++r) {
     const int i = base + r * 32 + lane;
@@ -238,7 +273,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_pass_kernel(const SortArgs 
     const int at = start[d] + rank[warp][d] + place[r];
     a.key_out[at] = key[r];
     a.tok_out[at] = identity ? i : a.tok_in[i];
-    if (!last) atomicAdd(a.hist_out + at / kSortTile * kDigits + ((key[r] >> (a.shift + a.bits)) & mask), 1);
+    if (!last) atomicAdd(a.hist_out + (int64_t)(at / kSortTile) * kDigits + ((key[r] >> (a.shift + a.bits)) & mask), 1);
   }
 }
 
@@ -487,7 +522,8 @@ static EmbedGradWs embed_grad_plan(int64_t T, int64_t V, int H) {
   const int bits = bits_of(V);  // keys 0 .. V
   w.passes = (bits + 8) / 9;
   w.digit_bits = (bits + w.passes - 1) / w.passes;
-  w.tiles = (int)((T + kSortTile - 1) / kSortTile);
+  const int tile = T <= kFewTokens ? kSortThreads : kSortThreads * 4;
+  w.tiles = (int)((T + tile - 1) / tile);
   const int cols = (H + kColumns - 1) / kColumns;
   // Chunks: rounds of CTAs, so that an SM that gets through faster takes more (T = 16384,
   // V = 131072, H = 5120: 681 us with 243 chunks, 605 with 487, 568 with 1024, 558 with
@@ -507,6 +543,7 @@ static EmbedGradWs embed_grad_plan(int64_t T, int64_t V, int H) {
   };
   for (int i = 0; i < 2; ++i) w.key[i] = take((size_t)T * 4), w.tok[i] = take((size_t)T * 4);
   w.hist = take((size_t)w.passes * w.tiles * kDigits * 4);
+  w.places = take(T <= kFewTokens ? 0 : (size_t)(w.tiles + 1) * kDigits * 4);
   w.valid = take((size_t)w.tiles * 4);
   w.bounds = take((size_t)w.chunks * sizeof(Bounds));
   w.carry = take((size_t)w.chunks * 2 * H * 4);
@@ -614,13 +651,25 @@ int mhc_embed_grad(const void* ids, int id_bytes, const void* dout, mhc_dtype dt
     a.tok_out = reinterpret_cast<int*>(ws + w.tok[from ^ 1]);
     a.hist_in = hist + p * per_pass;
     a.hist_out = last ? nullptr : hist + (p + 1) * per_pass;
+    const bool few = T <= kFewTokens;
     if (p == 0) {
-      if (id_bytes == 4) sort_count_kernel<int32_t><<<w.tiles, kSortThreads, 0, s>>>(a);
-      else sort_count_kernel<int64_t><<<w.tiles, kSortThreads, 0, s>>>(a);
+      if (id_bytes == 4)
+        few ? sort_count_kernel<int32_t, 1><<<w.tiles, kSortThreads, 0, s>>>(a)
+            : sort_count_kernel<int32_t, 4><<<w.tiles, kSortThreads, 0, s>>>(a);
+      else
+        few ? sort_count_kernel<int64_t, 1><<<w.tiles, kSortThreads, 0, s>>>(a)
+            : sort_count_kernel<int64_t, 4><<<w.tiles, kSortThreads, 0, s>>>(a);
       e = cudaGetLastError();
       if (e != cudaSuccess) break;
     }
-    e = launch_pdl(sort_pass_kernel, dim3(w.tiles), dim3(kSortThreads), 0, s, a, p == 0, last);
+    if (few) {
+      e = launch_pdl(sort_pass_kernel<1>, dim3(w.tiles), dim3(kSortThreads), 0, s, a, p == 0, last);
+    } else {
+      a.places = reinterpret_cast<int*>(ws + w.places);
+      e = launch_pdl(sort_places_kernel, dim3(kDigits / 32), dim3(1024), 0, s, a.hist_in, w.tiles, a.places,
+                     a.places + (size_t)w.tiles * kDigits);
+      if (e == cudaSuccess) e = launch_pdl(sort_pass_kernel<4>, dim3(w.tiles), dim3(kSortThreads), 0, s, a, p == 0, last);
+    }
   }
   if (e != cudaSuccess) return ops_cuda(e, "embed_grad sort launch");
   SumArgs m = {};

@@ -2,6 +2,9 @@
 their gradients) against plain 64-bit implementations, with the bounds that
 block_case.py derives."""
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -103,6 +106,17 @@ def test_embed_grad(T, V, H, S, dtype, grad, kind):
     again = torch.full((V, H), 5.0, dtype=grad, device="cuda")
     B.mhc_embed_grad(dev(i.int()), dev(dout), again, ws, scale=0.75)
     assert torch.equal(out, again)  # the same bits whatever the timing and the ids' type
+
+
+@pytest.mark.parametrize("T,V,kind", [(65536, 700, "skewed"), (65537, 100000, "skewed"), (300001, 3, "any"), (400000, 600000, "any")])
+def test_embed_grad_of_many_tokens(T, V, kind):
+    # small whole numbers: every order of the sum gives the same bits
+    g = torch.Generator(device="cuda").manual_seed(T)
+    i = _ids(gen(T), T, V, kind).cuda()
+    dout = torch.randint(-2, 3, (T, 8), generator=g, device="cuda").float()
+    out = torch.full((V, 8), 3.0, device="cuda")
+    B.mhc_embed_grad(i, dout, out, workspace(B.mhc_embed_grad_workspace_bytes(T, V, 8)))
+    assert torch.equal(out, torch.zeros(V, 8, device="cuda").index_add_(0, i, dout))
 
 
 def test_embed_grad_shard_padding_accumulate():
@@ -610,6 +624,37 @@ def test_operators_on_a_side_stream_and_in_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+def test_first_calls_of_a_process_may_be_captured():
+    code = """
+import torch
+from mhc_residual_seam_gb300 import binding as B
+T, V, H, E, k = 3000, 50, 8192, 64, 4
+e = lambda *s, t=torch.bfloat16: torch.zeros(*s, dtype=t, device="cuda")
+f = torch.float32
+ids, table, x, y, w = torch.arange(T, device="cuda") % V, e(V, H) + 1, e(T, H), e(T, H) + 1, e(H) + 1
+ro, nm, dy, dr, rp, rq, a, b = e(T, H), e(T, H), e(T, H), e(T, H), e(T, t=f), e(T, t=f), e(H, t=f), e(H, t=f)
+l, idx, wt, c = e(T, E, t=f), e(T, k, t=torch.int32), e(T, k, t=f), e(E, t=torch.int32)
+dl, dt, wr = e(T, E, t=f), e(V, H, t=f), e(B.mhc_route_workspace_bytes(E), t=torch.uint8)
+wb = e(B.mhc_block_norm_grad_workspace_bytes(T, H), t=torch.uint8)
+we = e(B.mhc_embed_grad_workspace_bytes(T, V, H), t=torch.uint8)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    B.mhc_embed(ids, table, x)
+    B.mhc_block_norm(y, x, w, None, w, ro, nm, rp, rq)
+    B.mhc_route(l, None, idx, wt, c, wr)
+    B.mhc_route_grad(wt, l, idx, dl)
+    B.mhc_block_norm_grad(ro, nm, y, ro, w, None, w, rp, rq, dy, dr, a, None, b, wb)
+    B.mhc_embed_grad(ids, x, dt, we)
+g.replay()
+torch.cuda.synchronize()
+assert bool((dt == T // V).all()) and int(c.sum()) == T * k and bool((ro == 2).all())
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0, r.stderr[-2000:]
 
 
 def test_offsets_beyond_32_bits():
