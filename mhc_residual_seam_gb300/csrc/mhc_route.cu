@@ -179,14 +179,11 @@ __device__ __forceinline__ void sort8(float* v) {
 // sigmoid instead of about 20), with the expert's place in its lane written over the
 // lowest log2(EPL) bits: each lane sorts its best few, and a round is one maximum
 // over the lanes; the lane that has it writes the slot and moves its list up.
-// An estimate is off by less than 2e-5 of the score (exp2's argument, at most 126,
-// is rounded to 2^-24 of itself, the two approximations to 2^-22, the place to
-// 2^-18), with a bias by less than 1e-6 and 5e-6 of the sum (a score is at most 1 and
-// its error largest in its middle), so slots that differ by more than twice that
-// from their neighbours, the last of them from the best expert left, are in the
-// order of the exact scores.  Where they do not (near ties, about one
-// token in a hundred of N(0, 1.5) logits), where two groups' sums are too near, or
-// where a lane's list runs out, the token is chosen again from the exact scores.
+// Slots whose estimates differ by more than the errors of two (`near0`, `near1`) from
+// their neighbours, the last of them from the best expert left, are in the order of
+// the exact scores.  Where they do not (one token in five hundred of N(0, 1.5) logits
+// with a bias), where two groups' sums are too near, or where a lane's list runs out,
+// the token is chosen again from the exact scores.
 //
 // The exact choice has whole order keys; its rounds work on each lane's two best
 // with the place in the low bits, and a lane whose two are spent looks for the
@@ -235,8 +232,14 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? kRouteResident : 
   }
   const bool estimate = a.estimate && __all_sync(0xffffffffu, finite);
   const bool need_sum = !a.sigmoid && (a.bias || !a.renorm);
-  // estimates nearer than this may be in the wrong order (1e-36: scores that exp2 flushes to zero)
-  const float near0 = a.bias ? 2e-5f : 1e-36f, near1 = a.bias ? 1e-5f : 4e-5f;
+  // Estimates nearer than near0 + near1 * estimate may be in the wrong order: twice the
+  // error of one.  With a bias (scores at most 1): the score's 5e-7, the sum's rounding and
+  // the place.  Without: relative, from exp2's argument (at most 88 away from 0 or from
+  // the maximum, where the exact score's argument is rounded as well) and the place;
+  // 1e-36: scores that exp2 flushes to zero.
+  const float place = (LOW + 2) * 2.4e-7f;
+  const float near0 = a.bias ? 2e-6f : 1e-36f;
+  const float near1 = place + (a.bias ? 0.f : a.sigmoid ? 1.5e-5f : 2.5e-5f);
 
   // The lane's logits of the next two passes come through shared memory of its own.
   constexpr int PIECES = EPL * (int)sizeof(T) / 16;  // 16-byte pieces of a lane's logits
@@ -259,6 +262,9 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? kRouteResident : 
     }
   };
   const uint32_t start = (blockIdx.x * kRouteWarps + warp) * batch;
+  // from a token past this batch to the same place of the warp's next batch (batches of
+  // one pass: of the one after)
+  const uint32_t later = batch > TOKENS ? stride - batch : 2 * (stride - batch);
   fetch(start, 0);
   fetch(TOKENS < batch ? start + TOKENS : start + stride, 1);
   int stage = 0;
@@ -311,9 +317,8 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? kRouteResident : 
               for (int e = 0; e < 4; ++e) v[8 * i + 2 * e] = x.p[e].x, v[8 * i + 2 * e + 1] = x.p[e].y;
             }
           }
-          // two passes on: in this batch, or in the warp's next
-          const int on = (it + 2) * TOKENS;
-          fetch(on < batch ? base + on : base + stride + (on - batch), stage);
+          const int on = (it + 2) * TOKENS;  // two passes on: in this batch or in a later one
+          fetch(base + on + (on < batch ? 0u : later), stage);
           stage ^= 1;
         }
       } else {
@@ -377,7 +382,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? kRouteResident : 
         }
         const bool two = b2 > -INFINITY;
         const float mine = two ? b1 + b2 : b1;
-        const float near = b1 > -INFINITY ? 2.f * near0 + near1 * (fabsf(b1) + (two ? fabsf(b2) : 0.f)) : 0.f;
+        const float near = seg_fmax<LANES>(b1 > -INFINITY ? 2.f * near0 + near1 * (fabsf(b1) + (two ? fabsf(b2) : 0.f)) : 0.f);
         // the best groups one by one; then the best one left has to be clearly behind
         float open = mine, last = -INFINITY;
         for (int n = 0; n < a.top_groups; ++n) {

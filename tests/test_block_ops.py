@@ -453,10 +453,10 @@ def test_route_infinities_and_rows_without_experts():
                                             (256, 8, 4, 8), (256, 1, 1, 8), (160, 8, 3, 6), (512, 1, 1, 10), (1024, 1, 1, 4)])
 @pytest.mark.parametrize("kind", ["normal", "near", "far", "half"])
 def test_route_choice_is_the_fp32_formula_of_every_token(E, groups, top, k, kind):
-    # 20000 tokens against the formula in fp32 torch operations (the same roundings): logits of N(0, 1.5); many
+    # every token against the formula in fp32 torch operations (the same roundings): logits of N(0, 1.5); many
     # that differ by a few units in the last place; far ones (tiny scores); bf16 with many equal
     g = torch.Generator(device="cuda").manual_seed(E + k)
-    T = 20000
+    T = 20000 if kind != "normal" else 300000 if E <= 64 else 150000  # more: every warp takes several batches
     l = 1.5 * torch.randn(T, E, device="cuda", generator=g)
     if kind == "near":
         l = torch.randint(-2, 3, (T, E), device="cuda", generator=g) * 0.5 + 1.25  # not 0: its neighbours below are NaN
