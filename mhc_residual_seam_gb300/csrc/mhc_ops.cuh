@@ -234,6 +234,7 @@ inline cudaError_t allow_smem(SmemGrant& grant, const void* kernel, size_t bytes
   if (grant.have[dev] >= bytes) return cudaSuccess;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
   if (e == cudaSuccess) grant.have[dev] = bytes;
+  else cudaGetLastError();  // it is this call's, not the next one's
   return e;
 }
 
@@ -251,7 +252,9 @@ inline cudaError_t launch_pdl(void (*kernel)(Params...), dim3 grid, dim3 block, 
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+  if (e != cudaSuccess) cudaGetLastError();  // it is this call's, not the next one's
+  return e;
 }
 
 }  // namespace mhc

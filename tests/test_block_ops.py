@@ -340,6 +340,16 @@ def test_block_norm_grad_widths(H, dtype):
     assert all(torch.equal(q[k], again[k]) for k in q)
 
 
+@pytest.mark.parametrize("T,H,dtype,mode", [(30011, 40, BF16, "token"), (20011, 264, F32, "channel"), (9001, 520, BF16, "channel"),
+                                            (9001, 1024, BF16, "token"), (5003, 2056, F16, "channel")])
+def test_block_norm_of_many_rows(T, H, dtype, mode):
+    # more rows than the GPU has teams at a time
+    d = block_inputs(T, H, dtype, mode, True, True, 51)
+    o = run_block(d, mode)
+    check_block(d, mode, o)
+    check_grad(d, mode, o, run_grad(d, mode, o))
+
+
 def test_block_norm_grad_without_y_dr_or_tokens():
     d = block_inputs(40, 640, BF16, "none", False, True, 21, y=False)
     o = run_block(d, "none")
@@ -530,6 +540,27 @@ def test_route_grad(E, k, dtype, sigmoid, renorm):
                      renorm=renorm, scale=2.5)
     ref, terms = R.route_grad(dw, l, idx.cpu(), sigmoid, renorm, 2.5)
     R.check(out, ref, terms, n=128, what="dlogits")
+
+
+@pytest.mark.parametrize("E,k,dtype", [(8, 2, F32), (60, 7, BF16), (256, 8, F32), (300, 32, F32)])
+@pytest.mark.parametrize("sigmoid,renorm", [(True, True), (False, False)])
+def test_route_grad_of_many_tokens(E, k, dtype, sigmoid, renorm):
+    # every token against autograd in 64 bits on the GPU: more tokens than the GPU has warps at a time
+    T = 100_003
+    g = torch.Generator(device="cuda").manual_seed(E)
+    l = (1.5 * torch.randn(T, E, device="cuda", generator=g)).to(dtype)
+    idx, _, _ = run_route(l, None, sigmoid, 1, 1, k, renorm)
+    dw = torch.randn(T, k, device="cuda", generator=g)
+    out = torch.full((T, E), 5.0, dtype=dtype, device="cuda")
+    B.mhc_route_grad(dw, l, idx, out, score=int(sigmoid), renorm=renorm, scale=2.5)
+    x = l.double().requires_grad_()
+    p = (torch.sigmoid(x) if sigmoid else torch.softmax(x, 1)).gather(1, idx.long())
+    w = 2.5 * (p / p.sum(1, keepdim=True) if renorm else p)
+    (w * dw.double()).sum().backward()
+    # the terms of an element are its own and the mean over the k: at most 2.5 * (|dw| + sum |dw|) of its score
+    terms = 2.5 * (dw.abs().max(1, keepdim=True).values * (k + 1)).double().expand(T, E)
+    terms = terms * (torch.ones_like(x) if renorm else torch.softmax(x, 1)).detach()
+    R.check(out, x.grad.cpu(), terms.cpu(), n=32, what="dlogits")
 
 
 def test_route_grad_skips_foreign_indices_and_takes_strides():
