@@ -198,9 +198,10 @@ __device__ __forceinline__ void sort8(float* v) {
 //
 // Bound by instruction issue (the floor of T = 131072, E = 256 in fp32 is 21 us of
 // HBM).
-template <typename T, int EPL, int LANES>
+template <typename T, int EPL, int LANES, bool K8>
 __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? kRouteResident : 1) route_kernel(const RouteArgs a) {
   constexpr uint32_t LOW = EPL - 1;
+  const int k = K8 ? 8 : a.k, log_slots = K8 ? 3 : a.log_slots;
   constexpr int TOKENS = 32 / LANES;
   constexpr bool SMEM_GROUPS = LANES == 32;  // groups that do not fall on whole lanes
   __shared__ uint32_t keys[SMEM_GROUPS ? kRouteWarps : 1][SMEM_GROUPS ? EPL * 32 : 1];
@@ -221,7 +222,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? kRouteResident : 
   __syncthreads();
   const int per = a.E / a.groups;
   const int group_lanes = per / EPL;  // where groups fall on whole lanes
-  const int slots = 1 << a.log_slots, batch = 32 >> a.log_slots;
+  const int slots = 1 << log_slots, batch = 32 >> log_slots;
   float bias[EPL];
   bool finite = true;
 #pragma unroll
@@ -240,6 +241,10 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? kRouteResident : 
   const float place = (LOW + 2) * 2.4e-7f;
   const float near0 = a.bias ? 2e-6f : 1e-36f;
   const float near1 = place + (a.bias ? 0.f : a.sigmoid ? 1.5e-5f : 2.5e-5f);
+  float most = 0.f;  // |bias|
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) most = fmaxf(most, fabsf(bias[i]));
+  const float near_group = 2.f * (near0 + near1 * (1.f + warp_max(most)));
 
   // The lane's logits of the next two passes come through shared memory of its own.
   constexpr int PIECES = EPL * (int)sizeof(T) / 16;  // 16-byte pieces of a lane's logits
@@ -297,7 +302,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? kRouteResident : 
 
     for (int it = 0; estimate && it < passes; ++it) {
       constexpr int KEPT = EPL <= 4 ? EPL : LANES == 8 ? 8 : 4;  // how many of its best a lane keeps sorted
-      const int first = (it * TOKENS + sub) << a.log_slots;
+      const int first = (it * TOKENS + sub) << log_slots;
       float v[EPL];
       bool redo = false;
       if (ring) {
@@ -324,21 +329,34 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? kRouteResident : 
       } else {
         logits(reinterpret_cast<const T*>(row_of(base + it * TOKENS)), v);
       }
-      // logits that are not finite are rare: found by 0 * l on the FMA pipe, masked in a branch
-      float odd = 0.f;
+      // logits that are not finite are rare: their sum is not either; masked in a branch
       unsigned dead = 0;
+      float odd;
+      if constexpr (EPL == 1) {
+        odd = v[0];
+      } else {
+        float2 sum = make_float2(v[0], v[1]);
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) odd = fmaf(v[i], 0.f, odd);
-      const bool masks = __any_sync(0xffffffffu, !(odd == 0.f));
+        for (int i = 2; i < EPL; i += 2) sum = __fadd2_rn(sum, make_float2(v[i], v[i + 1]));
+        odd = sum.x + sum.y;
+      }
+      const bool masks = __any_sync(0xffffffffu, !(fabsf(odd) < 3e38f));
       if (masks) {
 #pragma unroll
         for (int i = 0; i < EPL; ++i) dead |= (v[i] > -INFINITY ? 0u : 1u) << i;
       }
       if (a.sigmoid) {
+        if constexpr (EPL == 1) {
+          v[0] = rcp_approx(1.0f + ex2_approx(v[0] * -1.44269504f)) + bias[0];
+        } else {
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-          const float s = rcp_approx(1.0f + ex2_approx(v[i] * -1.44269504f)) + bias[i];
-          v[i] = __uint_as_float((__float_as_uint(s) & ~LOW) | i);
+          for (int i = 0; i < EPL; i += 2) {  // two experts per instruction where the pipe has it
+            float2 s = __fmul2_rn(make_float2(v[i], v[i + 1]), splat(-1.44269504f));
+            s = __fadd2_rn(make_float2(ex2_approx(s.x), ex2_approx(s.y)), splat(1.f));
+            s = __fadd2_rn(make_float2(rcp_approx(s.x), rcp_approx(s.y)), make_float2(bias[i], bias[i + 1]));
+            v[i] = __uint_as_float((__float_as_uint(s.x) & ~LOW) | i);
+            v[i + 1] = __uint_as_float((__float_as_uint(s.y) & ~LOW) | (i + 1));
+          }
         }
       } else {
         const float2 ms = softmax(v);
@@ -382,7 +400,8 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? kRouteResident : 
         }
         const bool two = b2 > -INFINITY;
         const float mine = two ? b1 + b2 : b1;
-        const float near = seg_fmax<LANES>(b1 > -INFINITY ? 2.f * near0 + near1 * (fabsf(b1) + (two ? fabsf(b2) : 0.f)) : 0.f);
+        float near = near_group;  // (with a bias; else relative to the largest of the sums compared)
+        if (!a.bias) near = seg_fmax<LANES>(b1 > -INFINITY ? 2.f * near0 + near1 * (b1 + (two ? b2 : 0.f)) : 0.f);
         // the best groups one by one; then the best one left has to be clearly behind
         float open = mine, last = -INFINITY;
         for (int n = 0; n < a.top_groups; ++n) {
@@ -401,7 +420,8 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? kRouteResident : 
       }
       const bool full = KEPT < EPL && b[KEPT - 1] > -INFINITY;
       int wins = 0;
-      for (int j = 0; j < a.k; ++j) {
+#pragma unroll(K8 ? 8 : 1)
+      for (int j = 0; j < k; ++j) {
         const float top = seg_fmax<LANES>(b[0]);
         const bool win = b[0] == top;  // one lane, or a tie (or no expert left): then wins and slots differ
         if (win) slot[first + j] = make_int2(lane * EPL | (int)(__float_as_uint(top) & LOW), __float_as_int(top));
@@ -419,12 +439,12 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? kRouteResident : 
     __syncwarp();
 
     // One slot per lane from here: slot `at` of token base + tok.
-    const int tok = id >> a.log_slots, at = id & (slots - 1);
-    const bool mine = at < a.k && base + tok < a.T;
+    const int tok = id >> log_slots, at = id & (slots - 1);
+    const bool mine = at < k && base + tok < a.T;
     if (estimate) {
       const int2 r = rest[tok];
       const float v = __int_as_float(slot[id].y);
-      const float after = at + 1 < a.k ? __int_as_float(slot[id + 1 & 31].y) : __int_as_float(r.x);
+      const float after = at + 1 < k ? __int_as_float(slot[id + 1 & 31].y) : __int_as_float(r.x);
       const unsigned filled = __ballot_sync(0xffffffffu, mine && v > -INFINITY) >> (id & ~(slots - 1));
       const bool redo = mine && (v - after <= near0 + near1 * fabsf(v) ||  // no slot: NaN, false
                                  __popc(slots == 32 ? filled : filled & ((1u << slots) - 1)) != r.y);
@@ -437,7 +457,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? kRouteResident : 
     for (; again; again &= again - 1) {
       const int it = __ffs(again) - 1;
       const T* row = reinterpret_cast<const T*>(row_of(base + it * TOKENS));
-      const int first = (it * TOKENS + sub) << a.log_slots;
+      const int first = (it * TOKENS + sub) << log_slots;
       uint32_t key[EPL];
       float m = 0.f, total = 1.f;
       {
@@ -520,7 +540,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? kRouteResident : 
       refill(0xffffffffu);
       uint32_t held = 0;  // lane j: the key of slot j
       int expert = -1;    // and its expert
-      for (int j = 0; j < a.k; ++j) {
+      for (int j = 0; j < k; ++j) {
         const uint32_t top = seg_max<LANES>(b1);
         const unsigned have = seg_ballot<LANES>((b1 | LOW) == (top | LOW));
         const int who = __ffs(have) - 1;
@@ -553,13 +573,13 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? kRouteResident : 
         const float later = __shfl_down_sync(0xffffffffu, pick, 1, LANES);
         bool unsure = false;
         if (held) {
-          if (lane + 1 == a.k) unsure = (held | LOW) == (next | LOW);
-          else if (lane + 1 < a.k) unsure = after && (held | LOW) == (after | LOW) && pick != later;
+          if (lane + 1 == k) unsure = (held | LOW) == (next | LOW);
+          else if (lane + 1 < k) unsure = after && (held | LOW) == (after | LOW) && pick != later;
         }
         if (__any_sync(0xffffffffu, unsure)) {
           unsigned alive = 0xffffffffu;
           expert = -1;
-          for (int j = 0; j < a.k; ++j) {
+          for (int j = 0; j < k; ++j) {
             uint32_t best = 0;
 #pragma unroll
             for (int i = 0; i < EPL; ++i) best = max(best, (alive >> i) & 1 ? key[i] : 0u);
@@ -577,7 +597,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? kRouteResident : 
           }
         }
       }
-      if (lane < a.k) slot[first + lane].x = expert;
+      if (lane < k) slot[first + lane].x = expert;
     }
     __syncwarp();
 
@@ -602,7 +622,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? kRouteResident : 
       w *= a.scale;
     }
     if (mine) {
-      const uint64_t o = (uint64_t)(base + tok) * a.k + at;
+      const uint64_t o = (uint64_t)(base + tok) * k + at;
       a.indices[o] = e;
       a.weights[o] = w;
     }
@@ -767,6 +787,16 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_grad_dense_kernel(cons
   }
 }
 
+// Eight slots of a token (the usual k, and enough tokens for a warp to take four in turn)
+// are known when compiling where a lane has eight experts.
+template <typename T, int EPL, int LANES>
+static void route_go(const RouteArgs& a, unsigned grid, cudaStream_t s) {
+  if constexpr (EPL == 8) {
+    if (a.k == 8 && a.log_slots == 3) return route_kernel<T, EPL, LANES, true><<<grid, kRouteWarps * 32, 0, s>>>(a);
+  }
+  route_kernel<T, EPL, LANES, false><<<grid, kRouteWarps * 32, 0, s>>>(a);
+}
+
 static int route_checks(int64_t T, int E, int k, int dtype, int score, int64_t ld, float scale) {
   if (!dtype_ok(dtype)) return ops_fail(MHC_ERR_CONFIG, "unknown dtype");
   if (score != MHC_SCORE_SOFTMAX && score != MHC_SCORE_SIGMOID) return ops_fail(MHC_ERR_CONFIG, "unknown score");
@@ -873,7 +903,7 @@ int mhc_route(const void* logits, int64_t ld, mhc_dtype dtype, const float* bias
   const int64_t tokens = kRouteWarps * (32 >> log_slots);
   int64_t grid = (T + tokens - 1) / tokens;
   if (grid > (int64_t)sms * kRouteCtas) grid = (int64_t)sms * kRouteCtas;
-  MHC_BY_DTYPE(dtype, D, { MHC_BY_LANES(epl, lanes, { route_kernel<D, N, L><<<(unsigned)grid, kRouteWarps * 32, 0, s>>>(a); }) });
+  MHC_BY_DTYPE(dtype, D, { MHC_BY_LANES(epl, lanes, { route_go<D, N, L>(a, (unsigned)grid, s); }) });
   return ops_cuda(cudaGetLastError(), "route launch");
 }
 
