@@ -27,7 +27,7 @@ struct BlockNormGradArgs {
   int H;
   void *dy, *dr;
   float *dgamma_post, *dgate, *dgamma_pre;
-  float* parts;  // [teams][2][H] column sums of each team: S and dgamma_pre
+  float* parts;  // [CTAs][2][H] column sums of each CTA: S and dgamma_pre
   int run;       // rows of a CTA
 };
 
@@ -425,19 +425,61 @@ __global__ void __launch_bounds__(BIG ? kBigThreads : kTeamThreads) block_norm_g
   }
   if constexpr (STAGES > 0) cp_async_wait<0>();
   pdl_launch();
-  float* out = a.parts + ((int64_t)blockIdx.x * q.teams + q.team) * 2 * a.H;
+  const void* channel = a.gate_mode == MHC_GATE_CHANNEL ? a.gate : nullptr;
+  const bool want_post = a.dgamma_post || channel, want_pre = a.dgamma_pre;
+  // the CTA's column sums: to its row of `parts`, or, where it is the only CTA, to the weights' gradients
+  auto finish = [&](int g, const Vec8& post, const Vec8& pre) {
+    float* const out = a.parts + (int64_t)blockIdx.x * 2 * a.H + g * 8;
+    if (gridDim.x > 1) {
+      if (want_post) st8(out, pack<float>(post));
+      if (want_pre) st8(out + a.H, pack<float>(pre));
+    } else {
+      const Vec8 p = mul8(post, weight8<T>(channel, g)), q = mul8(post, weight8<T>(a.gamma_post, g));
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int g = q.lane + i * q.lanes;
-    if (on(i)) {
-      if (a.dgamma_post || a.gate_mode == MHC_GATE_CHANNEL) st8(out + g * 8, pack<float>(s_post[i]));
-      if (has_pre) st8(out + a.H + g * 8, pack<float>(s_pre[i]));
+      for (int e = 0; e < 4; ++e) {
+        const int c = g * 8 + 2 * e;
+        if (a.dgamma_post) a.dgamma_post[c] = p.p[e].x, a.dgamma_post[c + 1] = p.p[e].y;
+        if (channel) a.dgate[c] = q.p[e].x, a.dgate[c + 1] = q.p[e].y;
+        if (want_pre) a.dgamma_pre[c] = pre.p[e].x, a.dgamma_pre[c + 1] = pre.p[e].y;
+      }
+    }
+  };
+  if constexpr (!WARP) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+      if (on(i)) finish(q.lane + i * q.lanes, s_post[i], s_pre[i]);
+  } else {  // the teams' sums in team order, through the shared memory that held their rows
+    __syncthreads();
+    const uint32_t sums = smem_of(dyn), team_bytes = 4 * m.plane;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+      if (on(i)) {
+        const uint32_t at = sums + q.team * team_bytes + m.smem[i];
+        const Raw8<float> p = pack<float>(s_post[i]), r = pack<float>(s_pre[i]);
+        sts16(at, p.q[0]);
+        sts16(at + m.plane, p.q[1]);
+        sts16(at + 2 * m.plane, r.q[0]);
+        sts16(at + 3 * m.plane, r.q[1]);
+      }
+    __syncthreads();
+    for (int g = threadIdx.x; g < segs; g += blockDim.x) {
+      Vec8 post = zero8(), pre = zero8();
+      for (int t2 = 0; t2 < q.teams; ++t2) {
+        const Vec8 p = unpack(fetched8<float>(sums + t2 * team_bytes + g * 16, m.plane));
+        const Vec8 r = unpack(fetched8<float>(sums + t2 * team_bytes + 2 * m.plane + g * 16, m.plane));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          post.p[e] = __fadd2_rn(post.p[e], p.p[e]);
+          pre.p[e] = __fadd2_rn(pre.p[e], r.p[e]);
+        }
+      }
+      finish(g, post, pre);
     }
   }
 }
 
-// Adds the teams' column sums in a fixed order and finishes the weights'
-// gradients: 32 * N columns x 32 slices of teams per CTA, N columns a thread (four
+// Adds the CTAs' column sums in a fixed order and finishes the weights'
+// gradients: 32 * N columns x 32 slices of parts per CTA, N columns a thread (four
 // for wide rows, one where that leaves most SMs idle), the slices joined in slice
 // order.
 template <typename T, int N>
@@ -487,7 +529,7 @@ struct TeamPlan {
   int ctas;  // per SM
 };
 
-constexpr int kSMs = 152;
+constexpr int kSMs = 152, kFewRows = 4;
 constexpr size_t kSmem = 227 * 1024;         // shared memory of an SM
 constexpr size_t kCtaSmem = 1024 + 512 + 128;  // what a CTA takes of it beside the dynamic part
 
@@ -495,7 +537,9 @@ constexpr size_t kCtaSmem = 1024 + 512 + 128;  // what a CTA takes of it beside 
 static TeamPlan team_plan(int H, size_t type_bytes, int matrices, int sm_threads) {
   const int segs = H / 8;
   TeamPlan p;
-  p.warp = segs <= 64;
+  // (the gradient keeps 64 registers of sums a thread: one warp per CTA instead of four
+  // teams with two groups a thread, T = 65536, H = 512 bf16: 77 us against 114)
+  p.warp = segs <= (matrices == 4 ? 32 : 64);
   p.vpt = segs <= 32 ? 1 : 2;
   p.threads = p.warp ? 128 : ((segs + 1) / 2 + 31) / 32 * 32;
   p.big = p.threads > kTeamThreads;
@@ -506,6 +550,9 @@ static TeamPlan team_plan(int H, size_t type_bytes, int matrices, int sm_threads
   if (p.ctas > 16) p.ctas = 16;
   const size_t stage = row + (size_t)(p.threads / 32) * 16;  // with the rows' scalars
   while (p.ctas > 1 && (stage * 2 + weights + kCtaSmem) * p.ctas > kSmem) --p.ctas;
+  // two CTAs with one row each in flight rather than one with two: CTAs of a short run
+  // have to overlap
+  if (p.ctas == 1 && 2 * p.threads <= sm_threads && (stage + weights + kCtaSmem) * 2 <= kSmem) p.ctas = 2;
   const size_t have = kSmem / p.ctas, fixed = weights + kCtaSmem;
   const size_t fit = have > fixed ? (have - fixed) / stage : 0;
   p.stages = fit >= 4 ? 4 : fit >= 2 ? 2 : (int)fit;
@@ -530,7 +577,11 @@ static int norm_run(int64_t T, const TeamPlan& p) {
   const int even = resident_run(T, p);
   return even > 4 * p.teams ? 4 * p.teams : even;
 }
-static int grad_run(int64_t T, const TeamPlan& p) { return resident_run(T, p); }
+// A few rows go to one CTA, which needs no fold (T = 4, H = 5120: one launch less).
+static int grad_run(int64_t T, const TeamPlan& p) {
+  const int few = kFewRows * p.teams;
+  return T <= few ? few : resident_run(T, p);
+}
 static int64_t grad_ctas(int64_t T, const TeamPlan& p) { return (T + grad_run(T, p) - 1) / grad_run(T, p); }
 
 #define MHC_BY_TEAM(plan, full, ...)                                                                  \
@@ -637,7 +688,7 @@ size_t mhc_block_norm_grad_workspace_bytes(int64_t T, int H) {
   size_t most = 0;  // the plan differs by the type's size
   for (size_t b = 2; b <= 4; b += 2) {
     const mhc::TeamPlan p = mhc::grad_plan(H, b);
-    const size_t n = (size_t)mhc::grad_ctas(T, p) * p.teams * 2 * H * sizeof(float);
+    const size_t n = (size_t)mhc::grad_ctas(T, p) * 2 * H * sizeof(float);
     if (n > most) most = n;
   }
   return most;
@@ -703,13 +754,12 @@ int mhc_block_norm_grad(const void* dr_out, const void* dnorm, const void* y, co
   const bool full = y && dr && dr_out && gamma_post && gamma_pre && even_columns(H, plan);
   a.run = grad_run(T, plan);
   const int64_t grid = grad_ctas(T, plan);
-  const int parts = (int)grid * plan.teams;
   cudaError_t e = cudaSuccess;
   MHC_BY_DTYPE(dtype, E, { MHC_BY_TEAM(plan, full, { e = grad_launch<E, N, W, L, K, F>(a, plan, grid, s); }) });
-  if (e == cudaSuccess && (dgamma_post || dgamma_pre || channel))
+  if (e == cudaSuccess && grid > 1 && (dgamma_post || dgamma_pre || channel))
     MHC_BY_DTYPE(dtype, E, {
-      e = H >= 4096 ? launch_pdl(block_norm_fold_kernel<E, 4>, dim3((H + 127) / 128, 2), dim3(1024), 0, s, a, parts)
-                    : launch_pdl(block_norm_fold_kernel<E, 1>, dim3((H + 31) / 32, 2), dim3(1024), 0, s, a, parts);
+      e = H >= 4096 ? launch_pdl(block_norm_fold_kernel<E, 4>, dim3((H + 127) / 128, 2), dim3(1024), 0, s, a, (int)grid)
+                    : launch_pdl(block_norm_fold_kernel<E, 1>, dim3((H + 31) / 32, 2), dim3(1024), 0, s, a, (int)grid);
     });
   return ops_cuda(e, "block_norm_grad launch");
 }

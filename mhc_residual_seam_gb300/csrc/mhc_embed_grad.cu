@@ -23,12 +23,14 @@ constexpr int kDigits = 512;                                 // 9-bit digits at 
 constexpr int kColumns = 1024;                               // columns per CTA of the sum
 constexpr int kSumThreads = kColumns / 8;
 
-struct Bounds {  // a chunk's first token and row, and the ones behind its last
+constexpr int kJoinCtas = 1024;  // of the join, over all columns: it takes the rows to join from a list
+
+struct alignas(16) Bounds {  // a chunk's first token and row, and the ones behind its last
   int a0, a1, b0, b1;
 };
 
 struct EmbedGradWs {  // byte offsets into the workspace
-  size_t key[2], tok[2], hist, places, valid, bounds, carry, total;
+  size_t key[2], tok[2], hist, places, valid, joins, bounds, carry, total;
   int tiles, chunks, passes, digit_bits;
   bool one;  // one CTA sorts
 };
@@ -45,6 +47,7 @@ struct SortArgs {
   int passes;
   int* places;              // [tiles][kDigits] of this pass: where a tile's keys of a digit go; null: from the counts
   int* valid;               // [tiles] tokens that have a row
+  int* joins;               // how many rows the join has to finish, set to 0 here
 };
 
 template <typename Id>
@@ -63,6 +66,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const SortArgs
   __shared__ int valid;
   for (int d = threadIdx.x; d < kDigits; d += kSortThreads) count[d] = 0;
   if (threadIdx.x == 0) valid = 0;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.joins = 0;
   __syncthreads();
   const int base = (int)blockIdx.x * kSortTile;
   int mine = 0;
@@ -175,6 +179,7 @@ __global__ void __launch_bounds__(kOneThreads) sort_one_kernel(const SortArgs a)
     int n = 0;
     for (int w = 0; w < kOneWarps; ++w) n += start[w];
     a.valid[0] = n;
+    *a.joins = 0;
   }
 }
 
@@ -287,6 +292,7 @@ struct SumArgs {
   const uint32_t* key;
   const int* tok;
   const int* valid;
+  int* joins;  // how many, then the chunks that end a row begun earlier, in any order
   Bounds* bounds;
   float* carry;  // [chunks][2][H]: the sum of the last row's tokens, where it ends later; of the first row's, where
                  // it began earlier
@@ -386,7 +392,10 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const SumArgs a)
   __syncthreads();
   pdl_launch();
   const Bounds b = sb;
-  if (blockIdx.y == 0 && threadIdx.x == 0) a.bounds[chunk] = b;
+  if (blockIdx.y == 0 && threadIdx.x == 0) {
+    a.bounds[chunk] = b;
+    if (before == b.b0 && b.b0 < b.b1) a.joins[1 + atomicAdd(a.joins, 1)] = chunk;
+  }
   const int64_t c = (int64_t)blockIdx.y * kColumns + threadIdx.x * 8;
   const bool on = c < a.H;
   const bool wide = ((reinterpret_cast<uintptr_t>(a.dtable) | (uintptr_t)(a.ld * sizeof(O))) & 31) == 0;
@@ -475,39 +484,72 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const SumArgs a)
 }
 
 // Rows whose tokens lie in several chunks, by the chunk that holds their end:
-// the earlier chunks' sums in chunk order, then its own.
+// the earlier chunks' sums in chunk order, then its own.  A frequent token has
+// hundreds of chunks, so they are taken in kSlices runs, whose sums are added in
+// order, and each run's loads eight at a time, whether a chunk has a sum or not
+// (empty chunks count as zero).
+constexpr int kSlices = 4;
 template <typename O>
-__global__ void __launch_bounds__(kSumThreads) embed_join_kernel(const SumArgs a) {
+__global__ void __launch_bounds__(kSumThreads* kSlices) embed_join_kernel(const SumArgs a) {
   __shared__ int first;
+  __shared__ float4 part[kSlices - 1][2][kSumThreads];
   pdl_wait();
-  const int chunk = blockIdx.x;
-  const Bounds b = a.bounds[chunk];
-  const int row = b.b0;
-  if (b.a0 == 0 || row >= b.b1 || (int)a.key[b.a0 - 1] != row) return;
-  // the chunk that holds the row's first token: the last one before this that did not begin inside the row
-  for (int hi = chunk - 1;; hi -= (int)blockDim.x) {
-    if (threadIdx.x == 0) first = -1;
-    __syncthreads();
-    const int k = hi - (int)threadIdx.x;
-    if (k >= 0) {
-      const Bounds p = a.bounds[k];
-      if (!(p.b0 == row && p.a0 > 0 && (int)a.key[p.a0 - 1] == row)) atomicMax(&first, k);
+  const int jobs = a.joins[0];
+  const int width = blockDim.x / kSlices, at = threadIdx.x % width, slice = threadIdx.x / width;
+  const int64_t c = (int64_t)blockIdx.y * kColumns + at * 8;
+  const bool on = c < a.H;
+  const bool wide = ((reinterpret_cast<uintptr_t>(a.dtable) | (uintptr_t)(a.ld * sizeof(O))) & 31) == 0;
+  for (int job = blockIdx.x; job < jobs; job += gridDim.x) {
+    const int chunk = a.joins[1 + job];
+    const int row = a.bounds[chunk].b0;
+    // the chunk that holds the row's first token: the last one before this that did not begin inside the row
+    for (int hi = chunk - 1;; hi -= (int)blockDim.x) {
+      __syncthreads();
+      if (threadIdx.x == 0) first = -1;
+      __syncthreads();
+      const int k = hi - (int)threadIdx.x;
+      if (k >= 0) {
+        const Bounds p = a.bounds[k];
+        if (!(p.b0 == row && p.a0 > 0 && (int)a.key[p.a0 - 1] == row)) atomicMax(&first, k);
+      }
+      __syncthreads();
+      if (first >= 0 || hi < (int)blockDim.x) break;
+    }
+    const int from = max(first, 0), n = chunk - from;
+    Vec8 acc = zero8();
+    if (on) {
+      const int lo = from + (int)((int64_t)n * slice / kSlices), hi = from + (int)((int64_t)n * (slice + 1) / kSlices);
+      for (int k = lo; k < hi; k += 8) {
+        Raw8<float> x[8];
+        bool has[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int q = min(k + u, chunk);  // (the chunk itself has memory too)
+          const int2 tokens = *reinterpret_cast<const int2*>(&a.bounds[q].a0);
+          has[u] = k + u < hi && tokens.y > tokens.x;  // a chunk with a token: its last is of the row
+          x[u] = ld8(a.carry + (int64_t)q * 2 * a.H + c);
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          if (has[u]) add8(acc, unpack(x[u]));
+      }
+    }
+    if (slice) {
+      const Raw8<float> mine = pack<float>(acc);
+      part[slice - 1][0][at] = *reinterpret_cast<const float4*>(&mine.q[0]);
+      part[slice - 1][1][at] = *reinterpret_cast<const float4*>(&mine.q[1]);
     }
     __syncthreads();
-    if (first >= 0 || hi < (int)blockDim.x) break;
-    __syncthreads();
+    if (slice || !on) continue;
+    for (int s = 0; s < kSlices - 1; ++s) {
+      Raw8<float> r;
+      r.q[0] = *reinterpret_cast<const uint4*>(&part[s][0][at]);
+      r.q[1] = *reinterpret_cast<const uint4*>(&part[s][1][at]);
+      add8(acc, unpack(r));
+    }
+    add8(acc, unpack(ld8(a.carry + ((int64_t)chunk * 2 + 1) * a.H + c)));
+    end_row<O>(a, row, c, acc, wide);
   }
-  const int64_t c = (int64_t)blockIdx.y * kColumns + threadIdx.x * 8;
-  if (c >= a.H) return;
-  const bool wide = ((reinterpret_cast<uintptr_t>(a.dtable) | (uintptr_t)(a.ld * sizeof(O))) & 31) == 0;
-  Vec8 acc = zero8();
-#pragma unroll 4
-  for (int k = max(first, 0); k < chunk; ++k) {
-    const Bounds p = a.bounds[k];
-    if (p.a1 > p.a0) add8(acc, unpack(ld8(a.carry + (int64_t)k * 2 * a.H + c)));  // it has a token, the last of the row
-  }
-  add8(acc, unpack(ld8(a.carry + ((int64_t)chunk * 2 + 1) * a.H + c)));
-  end_row<O>(a, row, c, acc, wide);
 }
 
 static int bits_of(int64_t v) {
@@ -545,6 +587,7 @@ static EmbedGradWs embed_grad_plan(int64_t T, int64_t V, int H) {
   w.hist = take((size_t)w.passes * w.tiles * kDigits * 4);
   w.places = take(T <= kFewTokens ? 0 : (size_t)(w.tiles + 1) * kDigits * 4);
   w.valid = take((size_t)w.tiles * 4);
+  w.joins = take((size_t)(w.chunks + 1) * 4);
   w.bounds = take((size_t)w.chunks * sizeof(Bounds));
   w.carry = take((size_t)w.chunks * 2 * H * 4);
   w.total = at;
@@ -561,7 +604,7 @@ static cudaError_t sum_launch(const SumArgs& a, int grad_dtype, dim3 grid, cudaS
     else if (a.streams == 2) e = launch_pdl(embed_sum_kernel<T, O, 2>, grid, dim3(threads), 0, s, a);
     else if (a.streams == 4) e = launch_pdl(embed_sum_kernel<T, O, 4>, grid, dim3(threads), 0, s, a);
     else e = launch_pdl(embed_sum_kernel<T, O, 0>, grid, dim3(threads), 0, s, a);
-    if (e == cudaSuccess && a.chunks > 1) e = launch_pdl(embed_join_kernel<O>, grid, dim3(threads), 0, s, a);
+    if (e == cudaSuccess && a.chunks > 1) e = launch_pdl(embed_join_kernel<O>, dim3(a.chunks < kJoinCtas / (int)grid.y ? a.chunks : (kJoinCtas + grid.y - 1) / grid.y, grid.y), dim3(threads * kSlices), 0, s, a);
   };
   if (grad_dtype == MHC_DT_F32) go(float());
   else go(T());
@@ -633,6 +676,7 @@ int mhc_embed_grad(const void* ids, int id_bytes, const void* dout, mhc_dtype dt
   a.tiles = w.tiles;
   a.passes = w.passes;
   a.valid = reinterpret_cast<int*>(ws + w.valid);
+  a.joins = reinterpret_cast<int*>(ws + w.joins);
   int* hist = reinterpret_cast<int*>(ws + w.hist);
   const size_t per_pass = (size_t)w.tiles * kDigits;
   cudaError_t e = cudaSuccess;
@@ -688,6 +732,7 @@ int mhc_embed_grad(const void* ids, int id_bytes, const void* dout, mhc_dtype dt
   m.key = reinterpret_cast<const uint32_t*>(ws + w.key[from]);
   m.tok = reinterpret_cast<const int*>(ws + w.tok[from]);
   m.valid = a.valid;
+  m.joins = a.joins;
   m.bounds = reinterpret_cast<Bounds*>(ws + w.bounds);
   m.carry = reinterpret_cast<float*>(ws + w.carry);
   const dim3 grid(w.chunks, (H + kColumns - 1) / kColumns);
