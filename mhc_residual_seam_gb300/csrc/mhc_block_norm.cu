@@ -127,8 +127,9 @@ struct TeamMemory {
 // STAGES rows ahead (0: no shared memory for that, plain loads), so loads stay in
 // flight across the two barriers of a row.  Arithmetic is two columns per
 // instruction.  rsqrtf (2 ulp) replaces a square root and a division that every
-// thread would repeat.  FULL: every part but a token gate is given and each thread
-// has all of its columns, known when compiling (no tests per row).
+// thread would repeat.  FULL: every part but a gate is given and each thread has all of
+// its columns, known when compiling (no tests per row; T = 16384, H = 5120 bf16: 121 us
+// against 125, the gradient 174 against 199).  At that size 102 us, 97 % of the copy.
 template <typename T, int VPT, bool WARP, int STAGES, bool FULL>
 __global__ void __launch_bounds__(kBigThreads) block_norm_kernel(const BlockNormArgs a) {
   __shared__ float4 buf[2][2][8];
@@ -263,6 +264,7 @@ __global__ void __launch_bounds__(kBigThreads) block_norm_kernel(const BlockNorm
 // columns over all of its team's rows, so the column sums stay in registers until
 // the end; a second kernel adds the CTAs' sums in a fixed order.  Rows and
 // their scalars are fetched ahead as in the forward kernel; FULL as there.
+// T = 16384, H = 5120 bf16: 167 us with the fold, 89 % of the copy.
 template <typename T, int VPT, bool WARP, bool BIG, int STAGES, bool FULL>
 __global__ void __launch_bounds__(BIG ? kBigThreads : kTeamThreads) block_norm_grad_kernel(const BlockNormGradArgs a) {
   constexpr int QUADS = BIG ? 8 : kTeamThreads / 128;

@@ -10,7 +10,9 @@
 //      row's end writes it (zero where the row has no token);
 //   3. a row whose tokens lie in more than one chunk is joined: the chunks'
 //      partial sums in chunk order, then the last chunk's tokens.
-// No float atomics, so the result does not depend on timing.
+// No float atomics, so the result does not depend on timing.  Bound by HBM at size:
+// T = 16384, V = 131072, H = 5120, four streams, fp32: 558 us for 3.36 GB, 89 % of the
+// copy, 541 of them in step 2.
 
 #include "mhc_ops.cuh"
 
