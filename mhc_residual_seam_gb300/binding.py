@@ -290,8 +290,17 @@ def _dense(t, shape, dtype, name: str):
     """The address of ``t``, a dense tensor of this shape and type, or None."""
     if t is None:
         return None
-    if t.dtype != dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
         _refuse(t, name, f"dense, of shape {shape}", dtype)
+    return t.data_ptr()
+
+
+def _vec(t, n: int, dtype, name: str):
+    """The address of ``t``, a dense vector of n elements of this type, or None."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.dim() != 1 or t.numel() != n or not t.is_cuda or not t.is_contiguous():
+        _refuse(t, name, f"a dense vector of {n}", dtype)
     return t.data_ptr()
 
 
@@ -299,7 +308,7 @@ def _pitch(t, T: int, H: int, dtype, name: str) -> int:
     """The row stride of a [T, H] matrix with dense rows (H for None)."""
     if t is None:
         return H
-    if t.dtype != dtype or t.shape != (T, H) or not t.is_cuda:
+    if t.dtype is not dtype or t.shape != (T, H) or not t.is_cuda:
         _refuse(t, name, f"[{T}, {H}]", dtype)
     rows, cols = t.stride()
     if cols != 1 and H > 1:
@@ -363,7 +372,7 @@ def mhc_embed_grad(ids, dout, dtable, workspace, scale: float = 1.0, first_id: i
 def _gate(gate, gate_mode: int, T: int, H: int, dtype):
     if gate is None:
         return None
-    return _dense(gate, (T,), _F32, "gate") if gate_mode == MHC_GATE_TOKEN else _dense(gate, (H,), dtype, "gate")
+    return _vec(gate, T, _F32, "gate") if gate_mode == MHC_GATE_TOKEN else _vec(gate, H, dtype, "gate")
 
 
 def mhc_block_norm(y, r, gamma_post, gate, gamma_pre, r_out, norm, rstd_post, rstd_pre, gate_mode: int = MHC_GATE_NONE,
@@ -376,11 +385,11 @@ def mhc_block_norm(y, r, gamma_post, gate, gamma_pre, r_out, norm, rstd_post, rs
     rc = L.mhc_block_norm(
         None if y is None else y.data_ptr(), _pitch(y, T, H, dt, "y"),
         None if r is None else r.data_ptr(), _pitch(r, T, H, dt, "r"),
-        _dense(gamma_post, (H,), dt, "gamma_post"), _gate(gate, gate_mode, T, H, dt), gate_mode,
-        _dense(gamma_pre, (H,), dt, "gamma_pre"), res_scale, eps, T, H, _dtype(x, "r"),
+        _vec(gamma_post, H, dt, "gamma_post"), _gate(gate, gate_mode, T, H, dt), gate_mode,
+        _vec(gamma_pre, H, dt, "gamma_pre"), res_scale, eps, T, H, _dtype(x, "r"),
         None if r_out is None else r_out.data_ptr(), _pitch(r_out, T, H, dt, "r_out"),
         None if norm is None else norm.data_ptr(), _pitch(norm, T, H, dt, "norm"),
-        _dense(rstd_post, (T,), _F32, "rstd_post"), _dense(rstd_pre, (T,), _F32, "rstd_pre"), _where(stream))
+        _vec(rstd_post, T, _F32, "rstd_post"), _vec(rstd_pre, T, _F32, "rstd_pre"), _where(stream))
     if rc:
         _check(rc)
 
@@ -401,12 +410,12 @@ def mhc_block_norm_grad(dr_out, dnorm, y, r_out, gamma_post, gate, gamma_pre, rs
     ws, n = _space(workspace)
     rc = L.mhc_block_norm_grad(
         _dense(dr_out, shape, dt, "dr_out"), _dense(dnorm, shape, dt, "dnorm"), _dense(y, shape, dt, "y"),
-        _dense(r_out, shape, dt, "r_out"), _dense(gamma_post, (H,), dt, "gamma_post"), _gate(gate, gate_mode, T, H, dt),
-        gate_mode, _dense(gamma_pre, (H,), dt, "gamma_pre"), _dense(rstd_post, (T,), _F32, "rstd_post"),
-        _dense(rstd_pre, (T,), _F32, "rstd_pre"), res_scale, T, H, _dtype(x, "dr"), _dense(dy, shape, dt, "dy"),
-        _dense(dr, shape, dt, "dr"), _dense(dgamma_post, (H,), _F32, "dgamma_post"),
-        _dense(dgate, (T,) if gate_mode == MHC_GATE_TOKEN else (H,), _F32, "dgate"),
-        _dense(dgamma_pre, (H,), _F32, "dgamma_pre"), ws, n, _where(stream))
+        _dense(r_out, shape, dt, "r_out"), _vec(gamma_post, H, dt, "gamma_post"), _gate(gate, gate_mode, T, H, dt),
+        gate_mode, _vec(gamma_pre, H, dt, "gamma_pre"), _vec(rstd_post, T, _F32, "rstd_post"),
+        _vec(rstd_pre, T, _F32, "rstd_pre"), res_scale, T, H, _dtype(x, "dr"), _dense(dy, shape, dt, "dy"),
+        _dense(dr, shape, dt, "dr"), _vec(dgamma_post, H, _F32, "dgamma_post"),
+        _vec(dgate, T if gate_mode == MHC_GATE_TOKEN else H, _F32, "dgate"),
+        _vec(dgamma_pre, H, _F32, "dgamma_pre"), ws, n, _where(stream))
     if rc:
         _check(rc)
 
@@ -424,9 +433,9 @@ def mhc_route(logits, bias, indices, weights, counts=None, workspace=None, score
     k = indices.shape[-1]
     ws, n = _space(workspace)
     rc = L.mhc_route(logits.data_ptr(), _pitch(logits, T, E, logits.dtype, "logits"), _dtype(logits, "logits"),
-                     _dense(bias, (E,), _F32, "bias"), score, E, groups, top_groups, k, int(renorm), scale, T,
+                     _vec(bias, E, _F32, "bias"), score, E, groups, top_groups, k, int(renorm), scale, T,
                      _dense(indices, (T, k), _I32, "indices"), _dense(weights, (T, k), _F32, "weights"),
-                     _dense(counts, (E,), _I32, "counts"), ws, n, _where(stream))
+                     _vec(counts, E, _I32, "counts"), ws, n, _where(stream))
     if rc:
         _check(rc)
 
