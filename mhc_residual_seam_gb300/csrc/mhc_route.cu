@@ -9,7 +9,9 @@ constexpr int kRouteWarps = 4;
 constexpr int kMaxExperts = 1024;
 // CTAs per SM of the choice: eight are resident (64 registers a thread), and twice as
 // many let an SM that gets through faster take more of them (T = 131072, E = 256: ten
-// resident and ten in all took 87 us where these took 81).
+// resident and ten in all took 87 us where these took 81).  Sixteen and 32 experts a lane
+// are given the registers of seven and four (T = 65536, E = 512: 69 us against 84 with as
+// many as they ask for; T = 32768, E = 1024: 94 against 124).
 constexpr int kRouteResident = 8, kRouteCtas = 16;
 
 template <typename T>
@@ -122,15 +124,6 @@ __device__ __forceinline__ unsigned seg_ballot(bool p) {
   else return (all >> (threadIdx.x & 31 & ~(LANES - 1))) & ((1u << LANES) - 1);
 }
 
-template <int EPL>
-struct BitsOf {
-  static constexpr int value = EPL == 1 ? 0 : 1 + BitsOf<EPL / 2>::value;
-};
-template <>
-struct BitsOf<1> {
-  static constexpr int value = 0;
-};
-
 // --------------------------------------------------- the choice, estimated --
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;
@@ -199,7 +192,7 @@ __device__ __forceinline__ void sort8(float* v) {
 // Bound by instruction issue: T = 131072, E = 256, 8 of 4 of 8 groups 68 us, 416
 // instructions a token at 72 % of the issue slots (its floor in HBM is 21 us).
 template <typename T, int EPL, int LANES, bool K8>
-__global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? kRouteResident : 1) route_kernel(const RouteArgs a) {
+__global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? kRouteResident : EPL == 16 ? kRouteResident - 1 : kRouteResident / 2) route_kernel(const RouteArgs a) {
   constexpr uint32_t LOW = EPL - 1;
   const int k = K8 ? 8 : a.k, log_slots = K8 ? 3 : a.log_slots;
   constexpr int TOKENS = 32 / LANES;
