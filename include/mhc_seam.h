@@ -302,7 +302,7 @@ size_t mhc_embed_grad_workspace_bytes(int64_t T, int64_t V, int H);
  *              is written (zero where no token has it); with `accumulate` not 0 the
  *              sum is added to dtable and rows without tokens are left alone
  *   padding_id NULL, or (host) the id that has no gradient
- * Ids outside the table have no gradient.  T and V at most 2^30.  Errors as
+ * Ids outside the table have no gradient.  T and V at most 2^30, H at most 2^20.  Errors as
  * mhc_embed(), and MHC_ERR_WORKSPACE. */
 int mhc_embed_grad(const void* ids, int id_bytes, const void* dout, mhc_dtype dtype, float scale, int64_t T, int H,
                    int streams, int64_t V, int64_t first_id, const int64_t* padding_id, int accumulate, void* dtable,
@@ -374,7 +374,8 @@ size_t mhc_route_workspace_bytes(int E);
  *   indices [T,k] int32, weights [T,k] fp32
  *   counts  [E] int32: tokens sent to each expert by this call, or NULL (then
  *           workspace may be NULL)
- * 1 <= E <= 1024, k <= 32, groups <= 32, k <= top_groups * E / groups.  Errors:
+ * 1 <= E <= 1024, k <= 32, groups <= 32, k <= top_groups * E / groups; T and a row's
+ * bytes are below 2^31.  A bias of -inf keeps an expert out as a logit does.  Errors:
  * MHC_ERR_CONFIG, MHC_ERR_SHAPE, MHC_ERR_NULL, MHC_ERR_ALIGN, MHC_ERR_WORKSPACE,
  * MHC_ERR_ALIAS, MHC_ERR_CUDA. */
 int mhc_route(const void* logits, int64_t ld, mhc_dtype dtype, const float* bias, mhc_score score, int E, int groups,
