@@ -323,8 +323,8 @@ int mhc_embed_grad(const void* ids, int id_bytes, const void* dout, mhc_dtype dt
  *             required where their gamma is given
  * r NULL: no residual, r_out = gate * p (what the seam takes as its Y).
  * y NULL is the norm before the first block: norm = r / rms(r) * gamma_pre, and
- * r_out is not written (gamma_post and the gate must be absent, else
- * MHC_ERR_INCOMPLETE_POST).  H <= 16384, T < 2^31.  Errors: MHC_ERR_CONFIG,
+ * r_out is not written and res_scale has no effect (gamma_post and the gate must
+ * be absent, else MHC_ERR_INCOMPLETE_POST).  H <= 16384, T < 2^31.  Errors: MHC_ERR_CONFIG,
  * MHC_ERR_SHAPE, MHC_ERR_NULL, MHC_ERR_INCOMPLETE_POST, MHC_ERR_ALIGN,
  * MHC_ERR_ALIAS, MHC_ERR_CUDA. */
 int mhc_block_norm(const void* y, int64_t ld_y, const void* r, int64_t ld_r, const void* gamma_post, const void* gate,
@@ -339,9 +339,10 @@ size_t mhc_block_norm_grad_workspace_bytes(int64_t T, int H);
 /* The gradient of mhc_block_norm(): from dr_out and dnorm, those of r_out and
  * norm, to dy, dr and the weights' gradients.  y, r_out, the weights, the gate
  * and the rstd arrays are those of the forward call; all matrices are dense.
- *   dr_out     NULL: zero (then gamma_pre must be given)
+ *   dr_out     NULL: zero (then gamma_pre must be given); without y, the gradient
+ *              that r has elsewhere
  *   dnorm, r_out, rstd_pre, dgamma_pre  used where gamma_pre is given; without y,
- *              r_out is the forward call's r
+ *              r_out is the forward call's r, and res_scale has no effect
  *   dy         required where y is given;  dr NULL: not wanted (the forward call had
  *              no r; then y must be given)
  *   dgamma_post, dgamma_pre [H] fp32, dgate [H] (channel) or [T] (token) fp32:

@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(kBigThreads) block_norm_kernel(const BlockNorm
 }
 
 // With x = r', c = gamma_pre dnorm and M = sum c x over the row:
-//   G = dr_out + rho2 c - x (rho2^3 M / H),  dr = scale G,
+//   G = dr_out + rho2 c - x (rho2^3 M / H),  dr = scale G (without y: G),
 //   dgamma_pre += rho2 dnorm x
 // and with g = rho1 G, w = gamma_post * gate (channel), b = w g, N = sum b y:
 //   dy = gate(token) (b - y (rho1^2 N / H)),  dgate(token) = N
@@ -750,8 +750,9 @@ int mhc_block_norm_grad(const void* dr_out, const void* dnorm, const void* y, co
     for (int q = o + 1; q < 6; ++q)
       if (rows_overlap(out[o], out[q])) return ops_fail(MHC_ERR_ALIAS, "two outputs overlap");
   }
+  // (without y the forward call normed r itself, unscaled)
   BlockNormGradArgs a = {dr_out, dnorm, y, r_out, gamma_post, gate, gamma_pre, rstd_post, rstd_pre, gate_mode,
-                               res_scale, T, H, dy, dr, dgamma_post, dgate, dgamma_pre, static_cast<float*>(workspace), 1};
+                               y ? res_scale : 1.f, T, H, dy, dr, dgamma_post, dgate, dgamma_pre, static_cast<float*>(workspace), 1};
   const TeamPlan plan = grad_plan(H, b);
   const bool full = y && dr && dr_out && gamma_post && gamma_pre && even_columns(H, plan);
   a.run = grad_run(T, plan);
