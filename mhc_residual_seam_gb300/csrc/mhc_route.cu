@@ -227,10 +227,10 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? kRouteResident : 
   const bool estimate = a.estimate && __all_sync(0xffffffffu, finite);
   const bool need_sum = !a.sigmoid && (a.bias || !a.renorm);
   // Estimates nearer than near0 + near1 * estimate may be in the wrong order: twice the
-  // error of one.  With a bias (scores at most 1): the score's 5e-7, the sum's rounding and
-  // the place.  Without: relative, from exp2's argument (at most 88 away from 0 or from
-  // the maximum, where the exact score's argument is rounded as well) and the place;
-  // 1e-36: scores that exp2 flushes to zero.
+  // error of one.  With a bias (scores at most 1): the score's 5e-7 (sigmoid; softmax: 7e-7 of
+  // a score, of two that add up to 1 at most), the sum's rounding and the place.  Without: relative, from exp2's
+  // argument (at most 88 away from 0 or from the maximum, which both kinds of softmax scores
+  // take off with the same rounding) and the place; 1e-36: scores that exp2 flushes to zero.
   const float place = (LOW + 2) * 2.4e-7f;
   const float near0 = a.bias ? 2e-6f : 1e-36f;
   const float near1 = place + (a.bias ? 0.f : a.sigmoid ? 1.5e-5f : 2.5e-5f);
@@ -355,11 +355,19 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? kRouteResident : 
         const float2 ms = softmax(v);
         if (lane == 0) soft[it * TOKENS + sub] = ms;
         redo = !(fabsf(ms.x) < 3e38f);
-        const float c = ms.x * 1.44269504f, share = a.bias ? rcp_approx(ms.y) : 1.f;
+        // the maximum is taken off first, as the exact scores do: a rounding of max * log2 e would scale
+        // every score of the row, but not the bias
+        const float share = a.bias ? rcp_approx(ms.y) : 1.f;
+        if constexpr (EPL == 1) {
+          v[0] = fmaf(ex2_approx((v[0] - ms.x) * 1.44269504f), share, bias[0]);
+        } else {
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-          const float s = fmaf(ex2_approx(fmaf(v[i], 1.44269504f, -c)), share, bias[i]);
-          v[i] = __uint_as_float((__float_as_uint(s) & ~LOW) | i);
+          for (int i = 0; i < EPL; i += 2) {
+            float2 s = __fmul2_rn(__fadd2_rn(make_float2(v[i], v[i + 1]), splat(-ms.x)), splat(1.44269504f));
+            s = __ffma2_rn(make_float2(ex2_approx(s.x), ex2_approx(s.y)), splat(share), make_float2(bias[i], bias[i + 1]));
+            v[i] = __uint_as_float((__float_as_uint(s.x) & ~LOW) | i);
+            v[i + 1] = __uint_as_float((__float_as_uint(s.y) & ~LOW) | (i + 1));
+          }
         }
       }
       if (masks) {

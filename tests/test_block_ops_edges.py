@@ -1,11 +1,13 @@
 """Edges of the operators around the seam on the GPU: arguments that have no
 effect, choices that only rounding decides, and sums whose order shows."""
+import math
+
 import pytest
 import torch
 
 from mhc_residual_seam_gb300 import binding as B
 
-from test_block_ops import block_inputs, check_grad, run_block, run_grad
+from test_block_ops import block_inputs, check_grad, run_block, run_grad, run_route
 
 pytestmark = pytest.mark.gpu
 
@@ -54,3 +56,73 @@ def test_the_gradient_without_y_against_differences_and_autograd():
             x.reshape(-1)[at] -= 2 * h
             slope = float((up - loss(*v)) / (2 * h))
             assert abs(slope - float(flat[at])) < 2e-4 * (1 + abs(slope)), (got, at)
+
+
+# ----------------------------------------------------------------- routing --
+def clear_choice(l, bias, groups, top, k, gap):
+    """The choice of softmax + bias in 64 bits, and the rows where every comparison that decides is wider than `gap`."""
+    T, E = l.shape
+    sel = torch.softmax(l.double(), 1) + bias.double()
+    sel = torch.where(l > -math.inf, sel, -math.inf)
+    clear = torch.ones(T, dtype=torch.bool, device=l.device)
+    if groups > 1:
+        best = sel.view(T, groups, -1).sort(dim=2, descending=True).values
+        val, order = (best[:, :, 0] + best[:, :, 1]).sort(dim=1, descending=True)
+        clear &= (val[:, top - 1] - val[:, top] > gap)
+        keep = torch.zeros(T, groups, dtype=torch.bool, device=l.device).scatter_(1, order[:, :top], True)
+        sel = torch.where(keep.repeat_interleave(E // groups, 1), sel, -math.inf)
+    val, idx = sel.sort(dim=1, descending=True)
+    n = min(k, E - 1)
+    clear &= ((val[:, :n] - val[:, 1:n + 1]) > gap).all(1)
+    return idx[:, :k], clear
+
+
+# fp32 scores of softmax + bias: exp (2 ulp), a sum of E terms (32 in a lane, then 5 levels), a division and the
+# bias's addition leave each at most 45 * 2^-24 of itself off, and the scores of a row add up to one; sums of two
+# such choices, up to 3 in size, are rounded twice more
+GAP = 5e-6
+
+
+@pytest.mark.parametrize("E,groups,top,k", [(64, 1, 1, 6), (8, 1, 1, 2), (32, 8, 3, 4), (128, 4, 2, 8), (256, 8, 4, 8), (256, 1, 1, 8),
+                                            (160, 8, 3, 6), (512, 1, 1, 10), (1024, 1, 1, 4)])
+@pytest.mark.parametrize("offset", [0.0, 1e3, 1e5, 1e6])
+def test_softmax_with_a_bias_does_not_depend_on_a_common_offset(E, groups, top, k, offset):
+    g = torch.Generator(device="cuda").manual_seed(E + k)
+    T = 100000
+    l = 1.5 * torch.randn(T, E, device="cuda", generator=g) + offset
+    bias = 0.1 * torch.randn(E, device="cuda", generator=g)
+    want, clear = clear_choice(l, bias, groups, top, k, GAP)
+    assert float(clear.double().mean()) > 0.7
+    idx, w, c = run_route(l, bias, False, groups, top, k, True)
+    assert torch.equal(idx.long()[clear], want[clear]), int((idx[clear] != want[clear]).any(1).sum())
+    assert torch.equal(c.long(), torch.bincount(idx.long().reshape(-1), minlength=E))
+
+
+@pytest.mark.parametrize("E,groups", [(8, 1), (64, 1), (64, 8), (256, 1), (256, 8)])
+def test_softmax_with_a_bias_chooses_between_near_scores_of_large_logits(E, groups):
+    # two experts in play, 3 apart; the second one's bias makes up for it but for a little, for every maximum
+    T = 20000
+    m = torch.arange(T, device="cuda") * 0.25 + 16  # a multiple of 1/4: the difference is exact
+    a, b = 1, E - 1
+    p = 1 / (1 + math.exp(-3.0))
+    for little in (6e-6, 1e-5, 2e-5, 4e-5, -6e-6, -1e-5, -2e-5, -4e-5):
+        l = torch.full((T, E), -math.inf, device="cuda")
+        l[:, a], l[:, b] = m, m - 3
+        bias = torch.zeros(E, device="cuda")
+        bias[b] = 2 * p - 1 - little
+        want, clear = clear_choice(l, bias, 1, 1, 1, 5.5e-6)
+        assert bool(clear.all()) and bool((want == (a if little > 0 else b)).all())
+        idx, _, _ = run_route(l, bias, False, groups, 1, 1, False)
+        assert torch.equal(idx.long(), want), (little, int((idx != want).sum()))
+
+
+@pytest.mark.parametrize("top", [3e9, 1e12, 1e30, 3e38])
+def test_softmax_with_a_bias_of_very_large_logits(top):
+    # the best expert's share is 1 and the others' 0
+    l = torch.zeros(1000, 64, device="cuda")
+    at = torch.arange(1000, device="cuda") % 64
+    l[torch.arange(1000, device="cuda"), at] = top * (1 - torch.arange(1000, device="cuda") * 1e-4)
+    bias = 0.25 - torch.arange(64, device="cuda") / 512.0
+    idx, w, _ = run_route(l, bias, False, 1, 1, 2, False, scale=1.0)
+    assert torch.equal(idx[:, 0].long(), at) and torch.equal(idx[:, 1].long(), (at == 0).long())
+    assert bool((w[:, 0] == 1).all()) and bool((w[:, 1] == 0).all())
