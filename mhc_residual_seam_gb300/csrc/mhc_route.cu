@@ -412,8 +412,9 @@ __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? kRouteResident : 
         const float behind = seg_fmax<LANES>(open);
         const bool keep = open == -INFINITY;
         redo |= keep && mine == last && mine - behind <= near;
-        if constexpr (LANES == 32) redo |= __popc(__ballot_sync(0xffffffffu, keep)) > a.top_groups * group_lanes && last > -INFINITY;
-        else redo |= seg_add<LANES>(keep) > a.top_groups * group_lanes && last > -INFINITY;
+        const bool kept = keep && mine > -INFINITY;  // equal groups leave the list together: there may be too many
+        if constexpr (LANES == 32) redo |= __popc(__ballot_sync(0xffffffffu, kept)) > a.top_groups * group_lanes;
+        else redo |= seg_add<LANES>(kept) > a.top_groups * group_lanes;
         if (!keep) {
 #pragma unroll
           for (int i = 0; i < KEPT; ++i) b[i] = -INFINITY;

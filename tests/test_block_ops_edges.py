@@ -126,3 +126,21 @@ def test_softmax_with_a_bias_of_very_large_logits(top):
     idx, w, _ = run_route(l, bias, False, 1, 1, 2, False, scale=1.0)
     assert torch.equal(idx[:, 0].long(), at) and torch.equal(idx[:, 1].long(), (at == 0).long())
     assert bool((w[:, 0] == 1).all()) and bool((w[:, 1] == 0).all())
+
+
+@pytest.mark.parametrize("E,groups", [(32, 4), (64, 8), (256, 8)])
+@pytest.mark.parametrize("live,top", [(3, 2), (4, 2), (4, 3)])
+def test_equal_groups_of_different_experts_go_to_the_lowest(E, groups, live, top):
+    # saturated sigmoids (scores of 1): the groups' sums of two are equal to the bit, their members are not
+    per = E // groups
+    pairs = [(0.25, 0.5), (0.125, 0.625), (0.4375, 0.3125), (0.1875, 0.5625)][:live]
+    l, bias = torch.full((100, E), -math.inf), torch.zeros(E)
+    for n, (x, y) in enumerate(pairs):
+        e = (groups - live + n) * per
+        l[:, e:e + 2] = 40.0
+        bias[e], bias[e + 1] = x, y
+    idx, w, c = run_route(l, bias, True, groups, top, 2 * top, False, scale=1.0)
+    first = [(groups - live + n) * per + i for n in range(top) for i in range(2)]
+    want = sorted(first, key=lambda e: -float(bias[e]))
+    assert bool((idx.cpu() == torch.tensor(want, dtype=torch.int32)).all()), (idx[0].tolist(), want)
+    assert bool((w == 1).all()) and int(c.sum()) == 100 * 2 * top
