@@ -7,7 +7,8 @@ import torch
 
 from mhc_residual_seam_gb300 import binding as B
 
-from test_block_ops import block_inputs, check_grad, run_block, run_grad, run_route
+import block_case as R
+from test_block_ops import block_inputs, check_grad, dev, gen, normal, run_block, run_grad, run_route
 
 pytestmark = pytest.mark.gpu
 
@@ -144,3 +145,24 @@ def test_equal_groups_of_different_experts_go_to_the_lowest(E, groups, live, top
     want = sorted(first, key=lambda e: -float(bias[e]))
     assert bool((idx.cpu() == torch.tensor(want, dtype=torch.int32)).all()), (idx[0].tolist(), want)
     assert bool((w == 1).all()) and int(c.sum()) == 100 * 2 * top
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("above", [64.0, 96.0, 120.0, 1000.0])
+def test_renormalised_softmax_of_experts_far_below_one_that_is_kept_out(above, dtype):
+    # the weights are the chosen scores' ratio, which does not depend on the row's maximum
+    T, E, k = 200, 64, 4
+    l = normal(gen(17), T, E).to(dtype)
+    bias = torch.arange(E) / 64.0  # the scores of the others are 0 beside it
+    bias[5] = -math.inf
+    l[:, 5] = above + l.float().max().ceil()
+    idx, w, _ = run_route(l, bias, False, 1, 1, k, True, scale=2.5)
+    assert bool((idx.cpu() == torch.tensor([63, 62, 61, 60], dtype=torch.int32)).all())
+    want = 2.5 * torch.softmax(l.double()[:, [63, 62, 61, 60]], 1)
+    R.check(w, want, want, n=64, what="weights")
+    # and the gradient is that of these weights
+    dw = normal(gen(18), T, k)
+    out = torch.empty(T, E, dtype=dtype, device="cuda")
+    B.mhc_route_grad(dev(dw), dev(l), idx, out, score=B.MHC_SCORE_SOFTMAX, scale=2.5)
+    ref, terms = R.route_grad(dw, torch.where(torch.arange(E) == 5, -math.inf, l.float()), idx.cpu(), False, True, 2.5)
+    R.check(out, ref, terms, n=128, what="dlogits")
