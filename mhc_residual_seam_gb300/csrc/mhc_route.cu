@@ -48,6 +48,8 @@ __device__ __forceinline__ void load_logits(const T* p, float* l) {
 // exp(l - max) with equal infinities at distance zero.
 __device__ __forceinline__ float soft_exp(float l, float m) { return l == -INFINITY ? 0.f : expf(l == m ? 0.f : l - m); }
 __device__ __forceinline__ float logistic(float l) { return __frcp_rn(1.0f + expf(-l)); }  // rounded as 1 / (1 + e)
+// 1 - logistic(l) = exp(-l) logistic(l): the difference itself has lost half its bits at l = 9 and all at 17
+__device__ __forceinline__ float logistic_rest(float l, float v) { return l > 0.f ? expf(-l) * v : 1.0f - v; }
 
 // A key whose unsigned order is the values' order; 0 for what cannot be chosen.
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -702,7 +704,7 @@ __device__ __forceinline__ void store_row(T* d, const float* src, int E, bool ve
 
 // Gradients that only the chosen experts have (sigmoid scores, or softmax
 // renormalised over the k): with q = v / sum v and v the score,
-//   renorm:  dl = scale q (dw - sum q dw) (1 - v for a sigmoid),   else dl = scale dw v (1 - v).
+//   renorm:  dl = scale q (dw - sum q dw) (1 - v for a sigmoid),   else (sigmoid) dl = scale dw v (1 - v).
 // One slot per lane, as many tokens per warp as have room; their rows are put
 // together in shared memory, written in 16-byte stores, and the slots' places set
 // back to zero.  Bound by the rows written (T = 131072, E = 256, fp32: 134 MB) and
@@ -737,16 +739,16 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_grad_kernel(const Rout
       v = soft_exp(l, m);
     }
     float d;
+    const float rest = a.sigmoid ? logistic_rest(l, v) : 1.f;
     if (a.renorm) {
       float total = v;
       for (int s = slots >> 1; s; s >>= 1) total += __shfl_xor_sync(0xffffffffu, total, s);
       const float q = total > 0.f ? v / total : 0.f;
       float mean = q * dw;
       for (int s = slots >> 1; s; s >>= 1) mean += __shfl_xor_sync(0xffffffffu, mean, s);
-      d = a.scale * q * (dw - mean);
-      if (a.sigmoid) d *= 1.f - v;
+      d = a.scale * q * (dw - mean) * rest;
     } else {
-      d = a.scale * dw * v * (1.f - v);
+      d = a.scale * dw * v * rest;
     }
     if (e >= 0) atomicAdd(&rows[tok * a.pad + e], d);  // (a token names an expert once; twice adds up)
     __syncwarp();

@@ -166,3 +166,25 @@ def test_renormalised_softmax_of_experts_far_below_one_that_is_kept_out(above, d
     B.mhc_route_grad(dev(dw), dev(l), idx, out, score=B.MHC_SCORE_SOFTMAX, scale=2.5)
     ref, terms = R.route_grad(dw, torch.where(torch.arange(E) == 5, -math.inf, l.float()), idx.cpu(), False, True, 2.5)
     R.check(out, ref, terms, n=128, what="dlogits")
+
+
+@pytest.mark.parametrize("renorm", [False, True])
+def test_the_gradient_of_saturated_sigmoids(renorm):
+    # s' = s (1 - s), with 1 - s = 1 / (1 + exp(l)) for large logits, where 1 - s from s would be 0
+    T, E, k = 400, 32, 4
+    g = gen(23)
+    l = 8 + 72 * torch.rand(T, E, generator=g)
+    idx, _, _ = run_route(l, None, True, 1, 1, k, renorm)
+    dw = normal(g, T, k)
+    out = torch.empty(T, E, device="cuda")
+    B.mhc_route_grad(dev(dw), dev(l), idx, out, renorm=renorm, scale=2.5)
+    x = l.double().gather(1, idx.cpu().long())
+    s, rest = 1 / (1 + torch.exp(-x)), 1 / (1 + torch.exp(x))
+    if renorm:
+        q = s / s.sum(1, keepdim=True)
+        mean = (q * dw.double()).sum(1, keepdim=True)
+        d, terms = q * (dw.double() - mean) * rest, q * (dw.double().abs() + (q * dw.double().abs()).sum(1, keepdim=True)) * rest
+    else:
+        d = terms = dw.double() * s * rest
+    # exp twice 2 ulp, the products, sums of four
+    R.check(out.cpu().gather(1, idx.cpu().long()), 2.5 * d, 2.5 * terms.abs(), n=32, what="dlogits")
