@@ -386,7 +386,8 @@ int mhc_route(const void* logits, int64_t ld, mhc_dtype dtype, const float* bias
 /* The gradient of mhc_route()'s weights by the logits (the choice itself has
  * none): dlogits [T,E] of `dtype`, rows ld_d apart, every element written, from
  * dweights [T,k] fp32 and the forward call's logits and indices.  Slots whose index is
- * not in [0, E) are skipped.  Errors as mhc_route(). */
+ * not in [0, E) are skipped; slots of a token that name the same expert add up, in slot
+ * order.  Errors as mhc_route(). */
 int mhc_route_grad(const float* dweights, const void* logits, int64_t ld, mhc_dtype dtype, const int32_t* indices,
                    mhc_score score, int E, int k, int renorm, float scale, int64_t T, void* dlogits, int64_t ld_d,
                    void* stream);

@@ -702,6 +702,26 @@ __device__ __forceinline__ void store_row(T* d, const float* src, int E, bool ve
   }
 }
 
+// A token of mhc_route names an expert once, but a caller's may not: the lanes whose
+// slots name the same place (-1: none) ...
+__device__ __forceinline__ unsigned same_place(int place) { return __match_any_sync(0xffffffffu, place); }
+// ... and their values summed into the lowest of them, in slot order, which alone then stores
+// (returns true there): one addend per place and no float atomics, so that the sum's order is fixed.
+__device__ __forceinline__ bool join_slots(unsigned same, bool named, float& x) {
+  const int id = threadIdx.x & 31;
+  const bool first = named && __ffs(same) - 1 == id;
+  if (__any_sync(0xffffffffu, named && !first)) {
+    float sum = x;
+#pragma unroll 1
+    for (int j = 1; j < 32; ++j) {
+      const float y = __shfl_sync(0xffffffffu, x, j);
+      if (first && j > id && (same >> j) & 1) sum += y;
+    }
+    x = sum;
+  }
+  return first;
+}
+
 // Gradients that only the chosen experts have (sigmoid scores, or softmax
 // renormalised over the k): with q = v / sum v and v the score,
 //   renorm:  dl = scale q (dw - sum q dw) (1 - v for a sigmoid),   else (sigmoid) dl = scale dw v (1 - v).
@@ -731,6 +751,8 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_grad_kernel(const Rout
         l = logit_of(static_cast<const T*>(a.logits) + t * a.ld + e);
       }
     }
+    const int place = e >= 0 ? tok * a.pad + e : -1;
+    const unsigned same = same_place(place);  // (while the loads are in flight)
     if (a.sigmoid) {
       if (e >= 0) v = logistic(l);
     } else {
@@ -750,13 +772,13 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_grad_kernel(const Rout
     } else {
       d = a.scale * dw * v * rest;
     }
-    if (e >= 0) atomicAdd(&rows[tok * a.pad + e], d);  // (a token names an expert once; twice adds up)
+    if (join_slots(same, e >= 0, d)) rows[place] = d;
     __syncwarp();
     const int n = (int)(a.T - base < a.rows ? a.T - base : a.rows);
     T* out = static_cast<T*>(a.dlogits) + base * a.ld_d;
     for (int i = 0; i < n; ++i, out += a.ld_d) store_row(out, rows + i * a.pad, a.E, a.vector);
     __syncwarp();
-    if (e >= 0) rows[tok * a.pad + e] = 0.f;
+    if (e >= 0) rows[place] = 0.f;
     __syncwarp();
   }
 }
@@ -777,6 +799,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_grad_dense_kernel(cons
     int e = id < a.k ? a.indices[t * a.k + id] : -1;
     if (e >= a.E) e = -1;
     const float dw = e >= 0 ? a.dweights[t * a.k + id] : 0.f;
+    const unsigned same = same_place(e >= 0 ? e : -1);
     float p[EPL], m = -INFINITY, total = 0.f;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
@@ -792,7 +815,8 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_grad_dense_kernel(cons
     total = warp_sum(total);
     const float share = total > 0.f ? 1.f / total : 0.f;
     const float mean = warp_sum(e >= 0 ? soft_exp(logit_of(row + e), m) * share * dw : 0.f);
-    if (e >= 0) atomicAdd(&up[e], dw);
+    float sum = dw;
+    if (join_slots(same, e >= 0, sum)) up[e] = sum;
     __syncwarp();
     T* d = static_cast<T*>(a.dlogits) + t * a.ld_d;
 #pragma unroll

@@ -188,3 +188,33 @@ def test_the_gradient_of_saturated_sigmoids(renorm):
         d = terms = dw.double() * s * rest
     # exp twice 2 ulp, the products, sums of four
     R.check(out.cpu().gather(1, idx.cpu().long()), 2.5 * d, 2.5 * terms.abs(), n=32, what="dlogits")
+
+
+@pytest.mark.parametrize("E,sigmoid,renorm", [(8, True, False), (256, True, False), (64, False, False)])
+def test_an_expert_named_often_adds_up_in_slot_order(E, sigmoid, renorm):
+    T, k = 500, 8
+    g = gen(29)
+    idx = torch.randint(0, 3, (T, k), generator=g).int()  # each several times
+    idx[::7, 2] = -1
+    idx[::5] = E - 1
+    dw = (2.0 ** torch.randint(0, 30, (T, k), generator=g)) * torch.randint(-1, 2, (T, k), generator=g)
+    l = torch.zeros(T, E)
+    outs = []
+    for _ in range(3):
+        out = torch.empty(T, E, device="cuda")
+        B.mhc_route_grad(dev(dw), dev(l), dev(idx), out, score=int(sigmoid), renorm=renorm, scale=1.0)
+        outs.append(out.cpu())
+    assert all(torch.equal(outs[0], o) for o in outs)
+    up = torch.zeros(T, E)
+    for j in range(k):  # one rounding per addition
+        t = torch.nonzero(idx[:, j] >= 0)[:, 0]
+        up[t, idx[t, j].long()] += dw[t, j]
+    if sigmoid:
+        want = 0.25 * up
+    else:  # every score is 1 / E, a power of two; the mean is a sum over 32 lanes, halves first
+        mean = torch.zeros(T, 32)
+        mean[:, :k] = torch.where(idx >= 0, dw / E, 0.0)
+        while mean.shape[1] > 1:
+            mean = mean[:, :mean.shape[1] // 2] + mean[:, mean.shape[1] // 2:]
+        want = (up - mean) / E
+    assert torch.equal(outs[0], want), int((outs[0] != want).any(1).sum())
