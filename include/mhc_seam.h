@@ -292,7 +292,8 @@ int mhc_embed(const void* ids, int id_bytes, const void* table, int64_t table_ld
               float scale, int64_t T, int H, int streams, mhc_dtype dtype, void* out, void* stream);
 
 /* Bytes of the workspace of mhc_embed_grad().  It needs no initialisation and
- * holds nothing between calls. */
+ * holds nothing between calls.  The size does not fall as T grows: a workspace for
+ * the most tokens serves any fewer. */
 size_t mhc_embed_grad_workspace_bytes(int64_t T, int64_t V, int H);
 
 /* The gradient of mhc_embed() by its table, from tokens sorted by row:
@@ -333,7 +334,8 @@ int mhc_block_norm(const void* y, int64_t ld_y, const void* r, int64_t ld_r, con
                    void* stream);
 
 /* Bytes of the workspace of mhc_block_norm_grad().  It needs no initialisation
- * and holds nothing between calls. */
+ * and holds nothing between calls.  The size does not fall as T grows: a workspace for
+ * the most tokens serves any fewer. */
 size_t mhc_block_norm_grad_workspace_bytes(int64_t T, int H);
 
 /* The gradient of mhc_block_norm(): from dr_out and dnorm, those of r_out and

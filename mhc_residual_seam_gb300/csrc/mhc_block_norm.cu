@@ -585,6 +585,13 @@ static int grad_run(int64_t T, const TeamPlan& p) {
   return T <= few ? few : resident_run(T, p);
 }
 static int64_t grad_ctas(int64_t T, const TeamPlan& p) { return (T + grad_run(T, p) - 1) / grad_run(T, p); }
+// The most CTAs that T rows or fewer take: one a team's rows, until all are resident.  (A longer
+// run halves their number, so grad_ctas itself falls where T grows past a full GPU.)
+static int64_t grad_ctas_most(int64_t T, const TeamPlan& p) {
+  if (T <= kFewRows * p.teams) return 1;
+  const int64_t each = (T + p.teams - 1) / p.teams, slots = (int64_t)kSMs * p.ctas;
+  return each < slots ? each : slots;
+}
 
 #define MHC_BY_TEAM(plan, full, ...)                                                                  \
   if (plan.stages == 0) { constexpr int K = 0; constexpr bool F = false; MHC_BY_TEAM_(plan, __VA_ARGS__) } \
@@ -690,7 +697,7 @@ size_t mhc_block_norm_grad_workspace_bytes(int64_t T, int H) {
   size_t most = 0;  // the plan differs by the type's size
   for (size_t b = 2; b <= 4; b += 2) {
     const mhc::TeamPlan p = mhc::grad_plan(H, b);
-    const size_t n = (size_t)mhc::grad_ctas(T, p) * 2 * H * sizeof(float);
+    const size_t n = (size_t)mhc::grad_ctas_most(T, p) * 2 * H * sizeof(float);
     if (n > most) most = n;
   }
   return most;

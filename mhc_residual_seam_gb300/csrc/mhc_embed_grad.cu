@@ -586,9 +586,11 @@ static EmbedGradWs embed_grad_plan(int64_t T, int64_t V, int H) {
     return o;
   };
   for (int i = 0; i < 2; ++i) w.key[i] = take((size_t)T * 4), w.tok[i] = take((size_t)T * 4);
-  w.hist = take((size_t)w.passes * w.tiles * kDigits * 4);
+  // (the larger tiles of many tokens are fewer at first: the size does not fall there)
+  const int room = T > kFewTokens && w.tiles < kFewTokens / kSortThreads ? kFewTokens / kSortThreads : w.tiles;
+  w.hist = take((size_t)w.passes * room * kDigits * 4);
   w.places = take(T <= kFewTokens ? 0 : (size_t)(w.tiles + 1) * kDigits * 4);
-  w.valid = take((size_t)w.tiles * 4);
+  w.valid = take((size_t)room * 4);
   w.joins = take((size_t)(w.chunks + 1) * 4);
   w.bounds = take((size_t)w.chunks * sizeof(Bounds));
   w.carry = take((size_t)w.chunks * 2 * H * 4);
