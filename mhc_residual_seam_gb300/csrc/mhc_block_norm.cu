@@ -124,7 +124,7 @@ struct TeamMemory {
 // Bound by HBM: y and r are read once, r' and the norm written once; the row
 // stays in registers between the two sums of squares.  The norm is formed from
 // the fp32 r', so it carries one rounding only.  Each thread fetches its columns
-// STAGES rows ahead (0: no shared memory for that, plain loads), so loads stay in
+// STAGES rows ahead (one or more: the widest fp32 row fits once), so loads stay in
 // flight across the two barriers of a row.  Arithmetic is two columns per
 // instruction.  rsqrtf (2 ulp) replaces a square root and a division that every
 // thread would repeat.  FULL: every part but a gate is given and each thread has all of
@@ -182,31 +182,25 @@ __global__ void __launch_bounds__(kBigThreads) block_norm_kernel(const BlockNorm
   uint32_t slot = m.ring, scalar = m.scalars;
   for (; t < end; t += step, flip ^= 1) {
     Vec8 p[VPT], x[VPT];
-    if constexpr (STAGES > 0) cp_async_wait<(STAGES > 0 ? STAGES - 1 : 0)>();
+    cp_async_wait<STAGES - 1>();
     float gt = 1.f;
     if (gates) {
       __syncwarp();
-      gt = STAGES ? lds4(scalar) : gates[t];
+      gt = lds4(scalar);
       __syncwarp();
     }
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       if (!FULL) p[i] = x[i] = zero8();
       if (on(i)) {
-        const char* pr = r + t * (a.ld_r * (int)sizeof(T)) + m.col[i];
-        const char* py = y + t * (a.ld_y * (int)sizeof(T)) + m.col[i];
-        if (has_r)
-          x[i] = unpack(STAGES ? fetched8<T>(slot + m.smem[i], m.plane) : ld8_stream(reinterpret_cast<const T*>(pr)));
-        if (has_y)
-          p[i] = unpack(STAGES ? fetched8<T>(slot + m.matrix + m.smem[i], m.plane) : ld8_stream(reinterpret_cast<const T*>(py)));
+        if (has_r) x[i] = unpack(fetched8<T>(slot + m.smem[i], m.plane));
+        if (has_y) p[i] = unpack(fetched8<T>(slot + m.matrix + m.smem[i], m.plane));
       }
     }
-    if constexpr (STAGES > 0) {
-      fetch(t + STAGES * step, slot, scalar);
-      slot += m.stage_bytes;
-      scalar += 16;
-      if (slot == m.ring + STAGES * m.stage_bytes) slot = m.ring, scalar = m.scalars;
-    }
+    fetch(t + STAGES * step, slot, scalar);
+    slot += m.stage_bytes;
+    scalar += 16;
+    if (slot == m.ring + STAGES * m.stage_bytes) slot = m.ring, scalar = m.scalars;
     if (has_y) {
       float k = gt;
       if (has_post) {
@@ -250,7 +244,7 @@ __global__ void __launch_bounds__(kBigThreads) block_norm_kernel(const BlockNorm
         }
     }
   }
-  if constexpr (STAGES > 0) cp_async_wait<0>();
+  cp_async_wait<0>();
 }
 
 // With x = r', c = gamma_pre dnorm and M = sum c x over the row:
@@ -263,7 +257,9 @@ __global__ void __launch_bounds__(kBigThreads) block_norm_kernel(const BlockNorm
 // term.)  Bound by HBM: four rows read, two written.  A thread keeps the same
 // columns over all of its team's rows, so the column sums stay in registers until
 // the end; a second kernel adds the CTAs' sums in a fixed order.  Rows and
-// their scalars are fetched ahead as in the forward kernel; FULL as there.
+// their scalars are fetched ahead as in the forward kernel (STAGES 0: fp32 rows
+// above 11520 columns, plain loads); FULL as there.  Above 10240 columns 64 registers a
+// thread are too few: 250 to 350 bytes of spills.
 // T = 16384, H = 5120 bf16: 167 us with the fold, 89 % of the copy.
 template <typename T, int VPT, bool WARP, bool BIG, int STAGES, bool FULL>
 __global__ void __launch_bounds__(BIG ? kBigThreads : kTeamThreads) block_norm_grad_kernel(const BlockNormGradArgs a) {
@@ -536,9 +532,9 @@ constexpr size_t kSmem = 227 * 1024;         // shared memory of an SM
 constexpr size_t kCtaSmem = 1024 + 512 + 128;  // what a CTA takes of it beside the dynamic part
 
 // `sm_threads`: threads of an SM that the kernel's registers allow for.
-static TeamPlan team_plan(int H, size_t type_bytes, int matrices, int sm_threads) {
+static constexpr TeamPlan team_plan(int H, size_t type_bytes, int matrices, int sm_threads) {
   const int segs = H / 8;
-  TeamPlan p;
+  TeamPlan p = {};
   // (the gradient keeps 64 registers of sums a thread: one warp per CTA instead of four
   // teams with two groups a thread, T = 65536, H = 512 bf16: 77 us against 114)
   p.warp = segs <= (matrices == 4 ? 32 : 64);
@@ -562,8 +558,8 @@ static TeamPlan team_plan(int H, size_t type_bytes, int matrices, int sm_threads
   return p;
 }
 
-static TeamPlan norm_plan(int H, size_t b) { return team_plan(H, b, 2, 1024); }
-static TeamPlan grad_plan(int H, size_t b) { return team_plan(H, b, 4, 640); }
+static constexpr TeamPlan norm_plan(int H, size_t b) { return team_plan(H, b, 2, 1024); }
+static constexpr TeamPlan grad_plan(int H, size_t b) { return team_plan(H, b, 4, 640); }
 
 // Rows of a CTA.  Forward: runs of four, so that CTAs start as others end and an
 // SM that gets through faster takes more of them (T = 16384, H = 5120 bf16: 102 us;
@@ -593,22 +589,40 @@ static int64_t grad_ctas_most(int64_t T, const TeamPlan& p) {
   return each < slots ? each : slots;
 }
 
-#define MHC_BY_TEAM(plan, full, ...)                                                                  \
-  if (plan.stages == 0) { constexpr int K = 0; constexpr bool F = false; MHC_BY_TEAM_(plan, __VA_ARGS__) } \
-  else if (full) { constexpr bool F = true; MHC_BY_STAGES(plan, __VA_ARGS__) }                        \
-  else { constexpr bool F = false; MHC_BY_STAGES(plan, __VA_ARGS__) }
-#define MHC_BY_STAGES(plan, ...)                                                                      \
-  if (plan.stages == 4) { constexpr int K = 4; MHC_BY_TEAM_(plan, __VA_ARGS__) }                      \
-  else if (plan.stages == 2) { constexpr int K = 2; MHC_BY_TEAM_(plan, __VA_ARGS__) }                 \
-  else { constexpr int K = 1; MHC_BY_TEAM_(plan, __VA_ARGS__) }
-#define MHC_BY_TEAM_(plan, ...)                                                                       \
-  if (plan.vpt == 1) { constexpr bool W = true, L = false; constexpr int N = 1; __VA_ARGS__; }        \
-  else if (plan.warp) { constexpr bool W = true, L = false; constexpr int N = 2; __VA_ARGS__; }       \
-  else if (!plan.big) { constexpr bool W = false, L = false; constexpr int N = 2; __VA_ARGS__; }      \
-  else { constexpr bool W = false, L = true; constexpr int N = 2; __VA_ARGS__; }
-
 // Whether every thread has all of its columns.
-static bool even_columns(int H, const TeamPlan& p) { return H / 8 == p.vpt * (p.warp ? 32 : p.threads); }
+static constexpr bool even_columns(int H, const TeamPlan& p) { return H / 8 == p.vpt * (p.warp ? 32 : p.threads); }
+
+constexpr int kMaxWidth = 16384;
+
+// Whether the plan of some width takes a variant; the others are not compiled.
+template <int BYTES, int MATRICES>
+static constexpr bool taken(int vpt, bool warp, bool big, int stages, bool full) {
+  for (int H = 8; H <= kMaxWidth; H += 8) {
+    const TeamPlan p = MATRICES == 2 ? norm_plan(H, BYTES) : grad_plan(H, BYTES);
+    if (p.vpt == vpt && p.warp == warp && p.big == big && p.stages == stages && (!full || even_columns(H, p))) return true;
+  }
+  return false;
+}
+
+// Runs its last argument with the plan's variant: groups per thread N, a warp per row W, more
+// than kTeamThreads L, rows ahead K, no tests F.
+#define MHC_BY_TEAM(plan, full, M, ...)                                                               \
+  if (plan.stages == 0) { constexpr int K = 0; constexpr bool F = false; MHC_BY_TEAM_(plan, M, __VA_ARGS__) } \
+  else if (full) { constexpr bool F = true; MHC_BY_STAGES(plan, M, __VA_ARGS__) }                     \
+  else { constexpr bool F = false; MHC_BY_STAGES(plan, M, __VA_ARGS__) }
+#define MHC_BY_STAGES(plan, M, ...)                                                                   \
+  if (plan.stages == 4) { constexpr int K = 4; MHC_BY_TEAM_(plan, M, __VA_ARGS__) }                   \
+  else if (plan.stages == 2) { constexpr int K = 2; MHC_BY_TEAM_(plan, M, __VA_ARGS__) }              \
+  else { constexpr int K = 1; MHC_BY_TEAM_(plan, M, __VA_ARGS__) }
+#define MHC_BY_TEAM_(plan, M, ...)                                                                    \
+  if (plan.vpt == 1) { MHC_TEAM(1, true, false, M, __VA_ARGS__) }                                     \
+  else if (plan.warp) { MHC_TEAM(2, true, false, M, __VA_ARGS__) }                                    \
+  else if (!plan.big) { MHC_TEAM(2, false, false, M, __VA_ARGS__) }                                   \
+  else { MHC_TEAM(2, false, true, M, __VA_ARGS__) }
+#define MHC_TEAM(n, w, l, M, ...)                                                                     \
+  constexpr int N = n;                                                                                \
+  constexpr bool W = w, L = l;                                                                        \
+  if constexpr (taken<(int)sizeof(E), M>(N, W, L, K, F)) { __VA_ARGS__; }
 
 template <typename T, int N, bool W, int K, bool F>
 static cudaError_t norm_launch(const BlockNormArgs& a, const TeamPlan& p, cudaStream_t s) {
@@ -628,8 +642,6 @@ static cudaError_t grad_launch(const BlockNormGradArgs& a, const TeamPlan& p, in
   block_norm_grad_kernel<T, N, W, L, K, F><<<(unsigned)grid, p.threads, p.smem, s>>>(a);
   return cudaGetLastError();
 }
-
-constexpr int kMaxWidth = 16384;
 
 static int shape_checks(int64_t T, int H, int dtype, int gate_mode) {
   if (!dtype_ok(dtype)) return ops_fail(MHC_ERR_CONFIG, "unknown dtype");
@@ -687,8 +699,8 @@ int mhc_block_norm(const void* y, int64_t ld_y, const void* r, int64_t ld_r, con
   const bool full = y && r && gamma_post && gamma_pre && even_columns(H, plan);
   a.run = norm_run(T, plan);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = cudaSuccess;
-  MHC_BY_DTYPE(dtype, E, { MHC_BY_TEAM(plan, full, { (void)L; e = norm_launch<E, N, W, K, F>(a, plan, s); }) });
+  cudaError_t e = cudaErrorInvalidConfiguration;  // a plan without a kernel: none
+  MHC_BY_DTYPE(dtype, E, { MHC_BY_TEAM(plan, full, 2, { e = norm_launch<E, N, W, K, F>(a, plan, s); }) });
   return ops_cuda(e, "block_norm launch");
 }
 
@@ -764,8 +776,8 @@ int mhc_block_norm_grad(const void* dr_out, const void* dnorm, const void* y, co
   const bool full = y && dr && dr_out && gamma_post && gamma_pre && even_columns(H, plan);
   a.run = grad_run(T, plan);
   const int64_t grid = grad_ctas(T, plan);
-  cudaError_t e = cudaSuccess;
-  MHC_BY_DTYPE(dtype, E, { MHC_BY_TEAM(plan, full, { e = grad_launch<E, N, W, L, K, F>(a, plan, grid, s); }) });
+  cudaError_t e = cudaErrorInvalidConfiguration;  // a plan without a kernel: none
+  MHC_BY_DTYPE(dtype, E, { MHC_BY_TEAM(plan, full, 4, { e = grad_launch<E, N, W, L, K, F>(a, plan, grid, s); }) });
   if (e == cudaSuccess && grid > 1 && (dgamma_post || dgamma_pre || channel))
     MHC_BY_DTYPE(dtype, E, {
       e = H >= 4096 ? launch_pdl(block_norm_fold_kernel<E, 4>, dim3((H + 127) / 128, 2), dim3(1024), 0, s, a, (int)grid)
