@@ -381,6 +381,8 @@ def mhc_block_norm(y, r, gamma_post, gate, gamma_pre, r_out, norm, rstd_post, rs
     y, r, r_out and norm are [T, H] (rows may be strided)."""
     L = _ops()
     x = y if r is None else r
+    if x is None:
+        raise MhcError(-1, "y or r is required")
     (T, H), dt = x.shape, x.dtype
     rc = L.mhc_block_norm(
         None if y is None else y.data_ptr(), _pitch(y, T, H, dt, "y"),
@@ -405,6 +407,8 @@ def mhc_block_norm_grad(dr_out, dnorm, y, r_out, gamma_post, gate, gamma_pre, rs
     weights' gradients fp32."""
     L = _ops()
     x = dy if dr is None else dr
+    if x is None:
+        raise MhcError(-1, "dy or dr is required")
     shape, dt = x.shape, x.dtype
     T, H = shape
     ws, n = _space(workspace)

@@ -1,5 +1,6 @@
 """Edges of the operators around the seam that need no GPU."""
 import pytest
+import torch
 
 from mhc_residual_seam_gb300 import binding as B
 
@@ -20,3 +21,14 @@ def test_embed_grad_workspace_does_not_fall_with_more_tokens(V, H):
              131073, 262144, 262145, 10 ** 6, 2 ** 24, 2 ** 30]
     sizes = [B.mhc_embed_grad_workspace_bytes(T, V, H) for T in steps]
     assert all(a <= b for a, b in zip(sizes, sizes[1:])), list(zip(steps, sizes))
+
+
+def test_the_binding_refuses_calls_without_a_matrix():
+    # nothing to take the sizes from: the library's error, not an attribute of None
+    w = torch.zeros(64)
+    with pytest.raises(B.MhcError) as e:
+        B.mhc_block_norm(None, None, None, None, w, None, w, None, w, stream=0)
+    assert e.value.code == -1
+    with pytest.raises(B.MhcError) as e:
+        B.mhc_block_norm_grad(w, w, None, w, None, None, w, None, w, None, None, None, None, w, None, stream=0)
+    assert e.value.code == -1
