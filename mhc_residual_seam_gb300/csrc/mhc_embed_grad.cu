@@ -571,7 +571,8 @@ static EmbedGradWs embed_grad_plan(int64_t T, int64_t V, int H) {
   const int cols = (H + kColumns - 1) / kColumns;
   // Chunks: rounds of CTAs, so that an SM that gets through faster takes more (T = 16384,
   // V = 131072, H = 5120: 681 us with 243 chunks, 605 with 487, 568 with 1024, 558 with
-  // 1433); at least 16 rows or tokens each; and 7 Mi columns of partial sums (56 MiB) at most.
+  // 1433); at least 16 rows or tokens each; and 7 Mi columns of partial sums (56 MiB) at most,
+  // but one chunk an SM (above 48000 columns that is more: 1.2 GB at the widest, 2^20).
   int64_t most = (kSumRounds * 152 * 8 + cols - 1) / cols;
   if (most * H > (int64_t)7 << 20) most = ((int64_t)7 << 20) / H;
   if (most < 152) most = 152;

@@ -10,8 +10,8 @@ constexpr int kMaxExperts = 1024;
 // CTAs per SM of the choice: eight are resident (64 registers a thread), and twice as
 // many let an SM that gets through faster take more of them (T = 131072, E = 256: ten
 // resident and ten in all took 87 us where these took 81).  Sixteen and 32 experts a lane
-// are given the registers of seven and four (T = 65536, E = 512: 69 us against 84 with as
-// many as they ask for; T = 32768, E = 1024: 94 against 124).
+// are given the registers of seven and four (sigmoid, bias, k = 8; T = 65536, E = 512: 69 us
+// against 84 with as many as they ask for, for 16 bytes of spills; T = 32768, E = 1024: 94 against 124).
 constexpr int kRouteResident = 8, kRouteCtas = 16;
 
 template <typename T>
@@ -191,8 +191,9 @@ __device__ __forceinline__ void sort8(float* v) {
 // A warp takes as many tokens in turn as it has lanes for their k slots; checks,
 // weights and stores are then one slot per lane.
 //
-// Bound by instruction issue: T = 131072, E = 256, 8 of 4 of 8 groups 68 us, 416
-// instructions a token at 72 % of the issue slots (its floor in HBM is 21 us).
+// Bound by instructions: T = 131072, E = 256, 8 of 4 of 8 groups 68 us, 418 a token at
+// 72 % of the issue slots; the busiest pipe (ALU: comparisons, maxima, moves) is 57 %
+// busy (its floor in HBM is 21 us).
 template <typename T, int EPL, int LANES, bool K8>
 __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? kRouteResident : EPL == 16 ? kRouteResident - 1 : kRouteResident / 2) route_kernel(const RouteArgs a) {
   constexpr uint32_t LOW = EPL - 1;
