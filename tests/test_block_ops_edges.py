@@ -218,3 +218,27 @@ def test_an_expert_named_often_adds_up_in_slot_order(E, sigmoid, renorm):
             mean = mean[:, :mean.shape[1] // 2] + mean[:, mean.shape[1] // 2:]
         want = (up - mean) / E
     assert torch.equal(outs[0], want), int((outs[0] != want).any(1).sum())
+
+
+@pytest.mark.parametrize("E,groups,top,k", [(8, 1, 1, 2), (33, 1, 1, 5), (64, 8, 3, 6), (64, 1, 1, 9), (128, 4, 2, 8), (256, 8, 4, 8),
+                                            (256, 1, 1, 12), (384, 1, 1, 4), (512, 8, 3, 2), (1024, 16, 14, 2)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_a_bias_that_is_not_finite_changes_nothing_but_its_expert(E, groups, top, k, dtype):
+    # an expert without a finite bias makes the router choose every token from the exact scores; on an expert that
+    # is never chosen the results are the same bits as from the estimates, whatever the sizes of logits and biases
+    g = torch.Generator(device="cuda").manual_seed(E + k)
+    for n, (std, offset, size) in enumerate([(1.0, 0.0, 0.1), (1.5, 1e6, 0.1), (0.01, 300.0, 1e-4), (40.0, -60.0, 1.0), (3.0, 5e3, 30.0),
+                                             (1e-3, 1e9, 1e-6), (0.5, 80.0, 1e3)]):
+        l = (std * torch.randn(20000, E, device="cuda", generator=g) + offset).to(dtype)
+        if n % 2:
+            l[torch.rand(l.shape, device="cuda", generator=g) < 0.3] = -math.inf
+        if n % 3 == 2:
+            l[torch.rand(l.shape, device="cuda", generator=g) < 0.01] = math.inf
+        dead = (7 * n + 3) % E
+        l[:, dead] = -math.inf
+        bias = size * torch.randn(E, device="cuda", generator=g)
+        other = bias.clone()
+        other[dead] = -math.inf
+        for sigmoid in (True, False):
+            a, b = (run_route(l, x, sigmoid, groups, top, k, n % 2 == 0) for x in (bias, other))
+            assert all(torch.equal(x, y) for x, y in zip(a, b)), (n, sigmoid, int((a[0] != b[0]).any(1).sum()))
