@@ -394,6 +394,24 @@ int mhc_route_grad(const float* dweights, const void* logits, int64_t ld, mhc_dt
                    mhc_score score, int E, int k, int renorm, float scale, int64_t T, void* dlogits, int64_t ld_d,
                    void* stream);
 
+/* Dropout before a residual add, with a mask that is never stored:
+ *   out[t,h] = r[t,h] + (keep(t,h) ? y[t,h] / (1 - p) : 0)
+ *   keep(t,h)  word i % 4 >= p 2^32 (rounded), i = t H + h, of Philox 4x32 with ten rounds
+ *              at the counter (i / 4, seed[1]) under the key seed[0], 64 bits each, low
+ *              words first
+ * so the same seed gives the same mask whatever the strides, and the gradient by y is
+ * this call on the gradient of out, without r.
+ *   y, r, out  [T,H] of `dtype`; r NULL: no residual; out may be y or r (same stride, in
+ *              place).  What is dropped is not looked at: a NaN there leaves no trace
+ *   seed       (device) the generator's key and the call's number.  It is read when the
+ *              kernel runs: a program that replays a captured call advances seed[1] on the
+ *              device between replays
+ *   p          in [0, 1]; 1 keeps nothing
+ * T < 2^31.  Errors: MHC_ERR_CONFIG, MHC_ERR_SHAPE, MHC_ERR_NULL, MHC_ERR_ALIGN,
+ * MHC_ERR_ALIAS, MHC_ERR_CUDA. */
+int mhc_dropout(const void* y, int64_t ld_y, const void* r, int64_t ld_r, double p, const uint64_t* seed, int64_t T,
+                int H, mhc_dtype dtype, void* out, int64_t ld_out, void* stream);
+
 /* Number of kernel launches the last successful mhc_seam() on this host
  * thread issued (1 for every non-empty call). */
 int mhc_last_launch_count(void);

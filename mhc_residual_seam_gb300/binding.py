@@ -95,6 +95,8 @@ def lib():
         L.mhc_route.argtypes = [P, I64, I, P, I, I, I, I, I, I, F, I64, P, P, P, P, SZ, P]
         L.mhc_route_grad.restype = I
         L.mhc_route_grad.argtypes = [P, P, I64, I, P, I, I, I, I, F, I64, P, I64, P]
+        L.mhc_dropout.restype = I
+        L.mhc_dropout.argtypes = [P, I64, P, I64, C.c_double, P, I64, I, I, P, I64, P]
         L.mhc_last_launch_count.restype = I
         L.mhc_last_launch_count.argtypes = []
         L.mhc_last_wave_parts.restype = I
@@ -249,18 +251,19 @@ def mhc_last_error_string() -> str:
 # a few microseconds of Python per call: messages are put together only for a
 # refusal.
 _DTYPES: dict = {}
-_F32 = _I32 = _raw_stream = _device = None
+_F32 = _I32 = _I64 = _U64 = _raw_stream = _device = None
 
 
 def _ops():
     """The library, with this section's constants and the stream lookup set up."""
-    global _F32, _I32, _raw_stream, _device
+    global _F32, _I32, _I64, _U64, _raw_stream, _device
     if _F32 is None:
         import torch
         _DTYPES.update({torch.bfloat16: MHC_DT_BF16, torch.float16: MHC_DT_F16, torch.float32: MHC_DT_F32})
         # the current stream's handle without a Stream object around it
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         _device = getattr(torch._C, "_cuda_getDevice", None)
+        _I64, _U64 = torch.int64, torch.uint64
         _F32, _I32 = torch.float32, torch.int32
     return lib()
 
@@ -453,6 +456,21 @@ def mhc_route_grad(dweights, logits, indices, dlogits, score: int = MHC_SCORE_SI
     rc = L.mhc_route_grad(_dense(dweights, (T, k), _F32, "dweights"), logits.data_ptr(), _pitch(logits, T, E, dt, "logits"),
                           _dtype(logits, "logits"), _dense(indices, (T, k), _I32, "indices"), score, E, k, int(renorm), scale,
                           T, dlogits.data_ptr(), _pitch(dlogits, T, E, dt, "dlogits"), _where(stream))
+    if rc:
+        _check(rc)
+
+
+def mhc_dropout(y, out, seed, r=None, p: float = 0.1, stream=None) -> None:
+    """Dropout of ``y`` [T, H] and the residual add of ``r``, into ``out`` (rows may be
+    strided).  ``seed`` is an int64 (or uint64) tensor of two on the GPU: the key and the
+    call's number.  The gradient by y is this call on the gradient of out, without r."""
+    L = _ops()
+    (T, H), dt = y.shape, y.dtype
+    if seed.dtype is not _I64 and seed.dtype is not _U64:
+        _refuse(seed, "seed", "a dense vector of 2", _I64)
+    rc = L.mhc_dropout(y.data_ptr(), _pitch(y, T, H, dt, "y"), None if r is None else r.data_ptr(), _pitch(r, T, H, dt, "r"),
+                       p, _vec(seed, 2, seed.dtype, "seed"), T, H, _dtype(y, "y"), out.data_ptr(),
+                       _pitch(out, T, H, dt, "out"), _where(stream))
     if rc:
         _check(rc)
 

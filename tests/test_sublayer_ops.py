@@ -1,0 +1,137 @@
+"""The operators inside a block on the GPU (dropout, the gated projections with
+their gradient, adapters of many requests) against plain 64-bit implementations."""
+import pytest
+import torch
+
+from mhc_residual_seam_gb300 import binding as B
+
+import block_case
+import sublayer_case as R
+
+pytestmark = pytest.mark.gpu
+
+BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    B.lib()
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def normal(g, *shape, std=1.0, dtype=F32):
+    return (std * torch.randn(*shape, generator=g)).to(dtype)
+
+
+def dev(t):
+    return None if t is None else t.cuda()
+
+
+def key_of(key, call):
+    wrap = lambda v: v - 2 ** 64 if v >= 2 ** 63 else v  # noqa: E731
+    return torch.tensor([wrap(key), wrap(call)], device="cuda")
+
+
+# ----------------------------------------------------------------- dropout --
+@pytest.mark.parametrize("T,H,dtype,res,p", [
+    (1, 8, BF16, True, 0.5), (3, 40, F16, False, 0.1), (33, 136, F32, True, 0.25), (7, 1032, BF16, False, 0.05),
+    (5, 64, F32, False, 0.0), (4, 64, BF16, True, 1.0), (2, 5120, BF16, True, 0.1), (257, 8, F16, True, 0.9)])
+def test_dropout(T, H, dtype, res, p):
+    g = gen(T + H)
+    y, r = normal(g, T, H, dtype=dtype), normal(g, T, H, std=2.0, dtype=dtype) if res else None
+    key, call = 0xFEDCBA9876543210, 0x89ABCDEF01234567
+    out = torch.full((T, H), 7.0, dtype=dtype, device="cuda")
+    B.mhc_dropout(dev(y), out, key_of(key, call), r=dev(r), p=p)
+    ref, terms = R.dropout(y, r, p, key, call)
+    # the scale's rounding, the product's and the sum's
+    block_case.check(out, ref, terms, n=3, what="dropout")
+    if not res:
+        assert torch.equal(out.cpu() == 0, ref == 0)  # the same mask
+
+
+def test_dropout_mask_does_not_depend_on_layout():
+    T, H = 50, 72
+    seed = key_of(11, 3)
+    big = normal(gen(1), T, 3 * H, dtype=BF16).cuda()
+    y, r = big[:, :H], big[:, 2 * H:]
+    want = torch.empty(T, H, dtype=BF16, device="cuda")
+    B.mhc_dropout(y.contiguous(), want, seed, r=r.contiguous(), p=0.3)
+    holder = torch.full((T, 2 * H), 9.0, dtype=BF16, device="cuda")
+    B.mhc_dropout(y, holder[:, H:], seed, r=r, p=0.3)
+    assert torch.equal(holder[:, H:], want) and bool((holder[:, :H] == 9).all())
+    # in place, on the residual and on y
+    a = r.contiguous()
+    B.mhc_dropout(y, a, seed, r=a, p=0.3)
+    assert torch.equal(a, want)
+    b = y.contiguous()
+    B.mhc_dropout(b, b, seed, r=r, p=0.3)
+    assert torch.equal(b, want)
+    # another call's number, another key: other masks
+    one = torch.ones(T, H, device="cuda")
+    masks = []
+    for k in (key_of(11, 3), key_of(11, 4), key_of(12, 3)):
+        m = torch.empty_like(one)
+        B.mhc_dropout(one, m, k, p=0.5)
+        masks.append(m)
+    assert not torch.equal(masks[0], masks[1]) and not torch.equal(masks[0], masks[2])
+
+
+def test_dropout_gradient_is_the_same_call():
+    T, H, p = 9, 64, 0.4
+    g = gen(3)
+    y, d = normal(g, T, H), normal(g, T, H)
+    out, dy = torch.empty(T, H, device="cuda"), torch.empty(T, H, device="cuda")
+    seed = key_of(5, 6)
+    B.mhc_dropout(y.cuda(), out, seed, p=p)
+    B.mhc_dropout(d.cuda(), dy, seed, p=p)
+    # by differences: out is linear in y
+    eps = 0.5
+    moved = torch.empty_like(out)
+    B.mhc_dropout((y + eps * d).cuda(), moved, seed, p=p)
+    # a difference of two rounded values, over eps
+    assert torch.allclose((moved - out).double() / eps, dy.double(), rtol=0, atol=float(4 * 2.0 ** -24 * moved.abs().max() / eps))
+
+
+def test_dropout_leaves_no_trace_of_what_is_dropped():
+    T, H = 20, 64
+    y = torch.full((T, H), float("nan"), device="cuda")
+    r = torch.ones(T, H, device="cuda")
+    out = torch.empty(T, H, device="cuda")
+    B.mhc_dropout(y, out, key_of(1, 2), r=r, p=0.5)
+    keep = (R.words(T, H, 1, 2) >= 2 ** 31).cuda()
+    assert torch.equal(torch.isnan(out), keep) and bool((out[~keep] == 1).all())
+    B.mhc_dropout(y, out, key_of(1, 2), r=r, p=1.0)
+    assert bool((out == 1).all())
+
+
+def test_dropout_replays_take_the_seed_of_the_moment():
+    T, H = 16, 128
+    y, out, seed = torch.ones(T, H, device="cuda"), torch.empty(T, H, device="cuda"), key_of(21, 0)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            B.mhc_dropout(y, out, seed, p=0.5)
+            seed[1] += 1
+    torch.cuda.current_stream().wait_stream(s)
+    for call in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out.cpu() != 0, R.words(T, H, 21, call) >= 2 ** 31), call
+
+
+def test_dropout_many_rows():
+    # the counter's upper word: element 2^34 is past 32 bits of counters of four
+    T, H = 2 ** 21 + 1, 8192
+    if torch.cuda.mem_get_info()[0] < 80 << 30:
+        pytest.skip("needs 70 GB")
+    y = torch.ones(T, H, dtype=BF16, device="cuda")
+    B.mhc_dropout(y, y, key_of(3, 4), p=0.5)
+    last = [R.philox((i & R.LOW, i >> 32, 4, 0), (3, 0)) for i in range((T - 1) * H // 4, (T - 1) * H // 4 + 16)]
+    assert torch.equal(y[-1, :64].cpu() != 0, torch.tensor(last).view(64) >= 2 ** 31)

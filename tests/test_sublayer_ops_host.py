@@ -1,0 +1,68 @@
+"""Refusals of the operators inside a block, and checks of their 64-bit test
+implementations, without a GPU.  The addresses below are fake; every call
+fails its checks before anything touches them."""
+import math
+
+import pytest
+import torch
+
+from mhc_residual_seam_gb300 import binding as B
+
+import sublayer_case as R
+
+A = 0x10000000  # 256-byte aligned, never dereferenced
+STEP = 0x1000000
+
+
+@pytest.fixture(scope="module")
+def L():
+    return B.lib()
+
+
+def _call(fn, base, over):
+    a = dict(base)
+    assert set(over) <= set(a), over
+    a.update(over)
+    return fn(*a.values())
+
+
+DROP = dict(y=A, ld_y=64, r=A + STEP, ld_r=64, p=0.1, seed=A + 2 * STEP, T=4, H=64, dtype=0, out=A + 3 * STEP, ld_out=64,
+            stream=None)
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(dtype=3), -10), (dict(p=-0.1), -10), (dict(p=1.5), -10), (dict(p=math.nan), -10), (dict(T=-1), -2),
+    (dict(T=2 ** 31), -2), (dict(H=0), -2), (dict(H=60), -2), (dict(ld_y=56), -2), (dict(ld_y=68), -2), (dict(ld_r=32), -2),
+    (dict(ld_out=65), -2), (dict(y=None), -1), (dict(out=None), -1), (dict(seed=None), -1), (dict(y=A + 8), -3),
+    (dict(r=A + STEP + 4), -3), (dict(seed=A + 4), -3), (dict(out=A, ld_out=72), -9), (dict(out=A + STEP + 16), -9),
+    (dict(out=A + 2 * STEP - 16), -9), (dict(T=0, y=None, out=None), 0)])
+def test_dropout_refusals(L, over, code):
+    assert _call(L.mhc_dropout, DROP, over) == code
+
+
+def test_binding_refuses_host_tensors_and_types():
+    f = torch.zeros
+    with pytest.raises(B.MhcError) as e:
+        B.mhc_dropout(f(4, 64), f(4, 64), f(2), stream=0)
+    assert e.value.code in (-2, -10)
+    with pytest.raises(B.MhcError) as e:
+        B.mhc_dropout(f(4, 64), f(4, 64), f(2, dtype=torch.int64), stream=0)
+    assert e.value.code == -10 and "GPU" in str(e.value)
+
+
+# ---------------------------------------- the test implementations themselves --
+def test_philox_known_answers():
+    # the generator's published test vectors (zeros, ones, digits of pi)
+    assert R.philox((0, 0, 0, 0), (0, 0)) == (0x6627E8D5, 0xE169C58D, 0xBC57AC4C, 0x9B00DBD8)
+    f = 0xFFFFFFFF
+    assert R.philox((f, f, f, f), (f, f)) == (0x408F276D, 0x41C83B0E, 0xA20BC7C6, 0x6D5451FD)
+    assert R.philox((0x243F6A88, 0x85A308D3, 0x13198A2E, 0x03707344), (0xA4093822, 0x299F31D0)) == \
+        (0xD16CFE09, 0x94FDCCEB, 0x5001E420, 0x24126EA1)
+
+
+def test_dropout_reference_by_hand():
+    y, r = torch.ones(2, 8), torch.full((2, 8), 3.0)
+    assert torch.equal(R.dropout(y, r, 0.0, 1, 2)[0], torch.full((2, 8), 4.0).double())
+    assert torch.equal(R.dropout(y, None, 1.0, 1, 2)[0], torch.zeros(2, 8).double())
+    out = R.dropout(torch.ones(100, 40), None, 0.25, 7, 9)[0]
+    assert set(out.unique().tolist()) == {0.0, 4 / 3} and abs(float((out == 0).double().mean()) - 0.25) < 5 * (0.1875 / 4000) ** 0.5
