@@ -279,6 +279,7 @@ int mhc_noalloc_check_status(void* stream);
 typedef enum { MHC_DT_BF16 = 0, MHC_DT_F16 = 1, MHC_DT_F32 = 2 } mhc_dtype;
 typedef enum { MHC_GATE_NONE = 0, MHC_GATE_CHANNEL = 1, MHC_GATE_TOKEN = 2 } mhc_gate_mode;
 typedef enum { MHC_SCORE_SOFTMAX = 0, MHC_SCORE_SIGMOID = 1 } mhc_score;
+typedef enum { MHC_ACT_SILU = 0, MHC_ACT_GELU = 1, MHC_ACT_GELU_TANH = 2, MHC_ACT_RELU = 3 } mhc_act;
 
 /* out[t,s,:] = scale * table[ids[t] - first_id, :] for s < streams.
  *   ids     [T] int32 or int64 (id_bytes 4 or 8)
@@ -393,6 +394,28 @@ int mhc_route(const void* logits, int64_t ld, mhc_dtype dtype, const float* bias
 int mhc_route_grad(const float* dweights, const void* logits, int64_t ld, mhc_dtype dtype, const int32_t* indices,
                    mhc_score score, int E, int k, int renorm, float scale, int64_t T, void* dlogits, int64_t ld_d,
                    void* stream);
+
+/* Bytes of the workspace of mhc_glu() and mhc_glu_grad().  It needs
+ * mhc_workspace_init() once; its counters reset themselves.  The size does not fall as T
+ * grows: a workspace for the most tokens serves any fewer. */
+size_t mhc_glu_workspace_bytes(int64_t T, int H, int F);
+
+/* The gated projections of a feed-forward block, their activation and product, in one
+ * launch:
+ *   g = x Wg^T + add_g,  u = x Wu^T + add_u,  h = act(g) * u
+ *   act: MHC_ACT_SILU g / (1 + exp(-g)); MHC_ACT_GELU g (1 + erf(g / sqrt 2)) / 2;
+ *        MHC_ACT_GELU_TANH its tanh form; MHC_ACT_RELU max(g, 0)
+ *   x     [T,H], rows ld_x apart (the seam's norm)
+ *   w     [2F,H], dense: the F rows of Wg, then those of Wu
+ *   add   [T,2F], rows ld_add apart (0: one row for all tokens, a bias), or NULL
+ *   gu    [T,2F], dense: g and u, rounded, for the gradient; NULL: not kept
+ *   h     [T,F], rows ld_h apart (formed from g and u before their rounding)
+ * bf16 or fp16 (sums fp32).  T <= 2^30; H and F multiples of 8, at most 2^20.  A bounded
+ * device wait that runs out is reported by mhc_check_status() on the workspace.  Errors:
+ * MHC_ERR_CONFIG, MHC_ERR_SHAPE, MHC_ERR_NULL, MHC_ERR_ALIGN, MHC_ERR_WORKSPACE,
+ * MHC_ERR_ALIAS, MHC_ERR_CUDA. */
+int mhc_glu(const void* x, int64_t ld_x, const void* w, const void* add, int64_t ld_add, int act, int64_t T, int H, int F,
+            mhc_dtype dtype, void* gu, void* h, int64_t ld_h, void* workspace, size_t ws_bytes, void* stream);
 
 /* Dropout before a residual add, with a mask that is never stored:
  *   out[t,h] = r[t,h] + (keep(t,h) ? y[t,h] / (1 - p) : 0)

@@ -20,6 +20,7 @@ MHC_OUT_FP8_GRID = 2
 MHC_DT_BF16, MHC_DT_F16, MHC_DT_F32 = 0, 1, 2
 MHC_GATE_NONE, MHC_GATE_CHANNEL, MHC_GATE_TOKEN = 0, 1, 2
 MHC_SCORE_SOFTMAX, MHC_SCORE_SIGMOID = 0, 1
+MHC_ACT_SILU, MHC_ACT_GELU, MHC_ACT_GELU_TANH, MHC_ACT_RELU = 0, 1, 2, 3
 STATUS_NAMES = {
     0: "MHC_OK", -1: "MHC_ERR_NULL", -2: "MHC_ERR_SHAPE", -3: "MHC_ERR_ALIGN", -4: "MHC_ERR_INCOMPLETE_POST",
     -5: "MHC_ERR_WORKSPACE", -6: "MHC_ERR_CAPTURE", -7: "MHC_ERR_TIMEOUT", -8: "MHC_ERR_CUDA", -9: "MHC_ERR_ALIAS",
@@ -95,6 +96,10 @@ def lib():
         L.mhc_route.argtypes = [P, I64, I, P, I, I, I, I, I, I, F, I64, P, P, P, P, SZ, P]
         L.mhc_route_grad.restype = I
         L.mhc_route_grad.argtypes = [P, P, I64, I, P, I, I, I, I, F, I64, P, I64, P]
+        L.mhc_glu_workspace_bytes.restype = SZ
+        L.mhc_glu_workspace_bytes.argtypes = [I64, I, I]
+        L.mhc_glu.restype = I
+        L.mhc_glu.argtypes = [P, I64, P, P, I64, I, I64, I, I, I, P, P, I64, P, SZ, P]
         L.mhc_dropout.restype = I
         L.mhc_dropout.argtypes = [P, I64, P, I64, C.c_double, P, I64, I, I, P, I64, P]
         L.mhc_last_launch_count.restype = I
@@ -456,6 +461,34 @@ def mhc_route_grad(dweights, logits, indices, dlogits, score: int = MHC_SCORE_SI
     rc = L.mhc_route_grad(_dense(dweights, (T, k), _F32, "dweights"), logits.data_ptr(), _pitch(logits, T, E, dt, "logits"),
                           _dtype(logits, "logits"), _dense(indices, (T, k), _I32, "indices"), score, E, k, int(renorm), scale,
                           T, dlogits.data_ptr(), _pitch(dlogits, T, E, dt, "dlogits"), _where(stream))
+    if rc:
+        _check(rc)
+
+
+def mhc_glu_workspace_bytes(T: int, H: int, F: int) -> int:
+    return int(lib().mhc_glu_workspace_bytes(int(T), int(H), int(F)))
+
+
+def _addend(add, T: int, N: int, dtype) -> int:
+    """The row stride of what is added to [T, N]: 0 where one row serves every token."""
+    if add is None:
+        return 0
+    if add.dim() == 2 and T > 1 and add.shape[0] == T and add.stride(0) == 0:
+        _pitch(add[:1], 1, N, dtype, "add")
+        return 0
+    return _pitch(add, T, N, dtype, "add")
+
+
+def mhc_glu(x, w, h, workspace, add=None, gu=None, act: int = MHC_ACT_SILU, stream=None) -> None:
+    """act(x Wg^T + add_g) * (x Wu^T + add_u) into ``h`` [T, F], of ``x`` [T, H] and ``w``
+    [2F, H] (the gate's rows first); ``add`` [T, 2F] may be one row expanded to all tokens."""
+    L = _ops()
+    (T, H), dt = x.shape, x.dtype
+    F = w.shape[0] // 2
+    ws, n = _space(workspace)
+    rc = L.mhc_glu(x.data_ptr(), _pitch(x, T, H, dt, "x"), _dense(w, (2 * F, H), dt, "w"), None if add is None else add.data_ptr(),
+                   _addend(add, T, 2 * F, dt), act, T, H, F, _dtype(x, "x"), _dense(gu, (T, 2 * F), dt, "gu"), h.data_ptr(),
+                   _pitch(h, T, F, dt, "h"), ws, n, _where(stream))
     if rc:
         _check(rc)
 

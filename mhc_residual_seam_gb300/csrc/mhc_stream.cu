@@ -82,7 +82,7 @@ static EncodeTiled get_encode() {
   return fn;
 }
 
-static bool encode(CUtensorMap* m, CUtensorMapDataType dt, int rank, const void* base, const cuuint64_t* dims,
+bool encode(CUtensorMap* m, CUtensorMapDataType dt, int rank, const void* base, const cuuint64_t* dims,
                    const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle sw) {
   EncodeTiled enc = get_encode();
   if (!enc) return false;

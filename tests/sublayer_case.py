@@ -37,3 +37,42 @@ def dropout(y, r, p, key, call):
     keep = words(*y.shape, key, call) >= math.floor(p * 2 ** 32 + 0.5)
     x = torch.where(keep, y.double() / (1 - p) if p < 1 else 0.0, 0.0)
     return (x, x.abs()) if r is None else (x + r.double(), x.abs() + r.double().abs())
+
+
+# ------------------------------------------------------- gated projections --
+ACTS = ("silu", "gelu", "gelu_tanh", "relu")  # in the order of the MHC_ACT numbers
+
+
+def act(g, name):
+    """(activation, derivative, the argument of its exponential) in 64 bits."""
+    g = g.double()
+    if name == "relu":
+        return torch.where(g > 0, g, 0.0), (g > 0).double(), torch.zeros_like(g)
+    if name == "gelu":
+        p = 0.5 * torch.erfc(-g / math.sqrt(2))
+        return g * p, p + g * torch.exp(-g * g / 2) / math.sqrt(2 * math.pi), g * g / 2
+    q = g if name == "silu" else math.sqrt(8 / math.pi) * (g + 0.044715 * g ** 3)
+    dq = 1.0 if name == "silu" else math.sqrt(8 / math.pi) * (1 + 3 * 0.044715 * g ** 2)
+    s = torch.sigmoid(q)
+    return g * s, s + g * s * (1 - s) * dq, q
+
+
+def glu(x, w, add, name):
+    """{h, gu} and the sums of their terms' absolute values, in units of 2^-24 roundings.
+
+    A sum of H products (exact in fp32) is off by at most 2 H 2^-24 of the products' absolute sum (H
+    additions, each off by at most a whole unit: the tensor cores' rounding is not documented); the
+    activation has a slope below 1.2, and its own error is some units and one per unit of the
+    exponential's argument."""
+    F = w.shape[0] // 2
+    H = x.shape[1]
+    gu, size = x.double() @ w.double().t(), x.double().abs() @ w.double().abs().t()
+    if add is not None:
+        gu, size = gu + add.double(), size + add.double().abs()
+    g, u = gu[:, :F], gu[:, F:]
+    a, _, q = act(g, name)
+    off = 2 * (H + 1) * size
+    terms = 1.2 * off[:, :F] * u.abs() + a.abs() * off[:, F:] + (64 + 4 * q.abs()) * (a * u).abs()
+    # the product of both errors
+    terms = terms + off[:, :F] * off[:, F:] * 2.0 ** -24
+    return {"h": a * u, "gu": gu}, {"h": terms, "gu": off}

@@ -135,3 +135,71 @@ def test_dropout_many_rows():
     B.mhc_dropout(y, y, key_of(3, 4), p=0.5)
     last = [R.philox((i & R.LOW, i >> 32, 4, 0), (3, 0)) for i in range((T - 1) * H // 4, (T - 1) * H // 4 + 16)]
     assert torch.equal(y[-1, :64].cpu() != 0, torch.tensor(last).view(64) >= 2 ** 31)
+
+
+# ------------------------------------------------------- gated projections --
+def workspace(n):
+    ws = torch.full((max(n, 16),), 0xA5, dtype=torch.uint8, device="cuda")
+    B.mhc_workspace_init(ws)
+    return ws
+
+
+def glu_inputs(T, H, F, dtype, add, seed=0):
+    g = gen(seed + T + H + F)
+    x, w = normal(g, T, H, dtype=dtype), normal(g, 2 * F, H, std=H ** -0.5, dtype=dtype)
+    a = {"none": None, "rows": normal(g, T, 2 * F, std=0.5, dtype=dtype), "bias": normal(g, 1, 2 * F, dtype=dtype)}[add]
+    return x, w, a
+
+
+@pytest.mark.parametrize("T,H,F,dtype,act,add,keep", [
+    (1, 8, 8, BF16, "silu", "none", True), (3, 64, 64, F16, "gelu", "rows", True), (16, 72, 40, BF16, "gelu_tanh", "bias", False),
+    (17, 136, 136, BF16, "silu", "rows", False), (64, 512, 128, F16, "relu", "none", True), (65, 1032, 72, BF16, "silu", "none", False),
+    (127, 200, 256, BF16, "gelu", "bias", True), (128, 320, 264, F16, "silu", "none", True), (129, 64, 1000, BF16, "relu", "rows", True),
+    (257, 520, 392, BF16, "gelu_tanh", "none", True), (300, 2056, 136, F16, "silu", "rows", False), (1000, 256, 1368, BF16, "silu", "none", True),
+    (1, 5120, 2048, BF16, "silu", "none", False), (4, 2048, 5000, F16, "gelu_tanh", "none", False),
+    (33, 1024, 3000, BF16, "silu", "rows", True), (2500, 64, 2048, BF16, "relu", "none", True)])
+def test_glu(T, H, F, dtype, act, add, keep):
+    x, w, a = glu_inputs(T, H, F, dtype, add)
+    ref, terms = R.glu(x, w, a, act)
+    ws = workspace(B.mhc_glu_workspace_bytes(T, H, F))
+    h = torch.full((T, F), 7.0, dtype=dtype, device="cuda")
+    gu = torch.full((T, 2 * F), 7.0, dtype=dtype, device="cuda") if keep else None
+    for again in range(2):  # the workspace is as good after a call as before
+        B.mhc_glu(dev(x), dev(w), h, ws, add=None if a is None else dev(a).expand(T, 2 * F), gu=gu, act=R.ACTS.index(act))
+        B.mhc_check_status(ws)
+        block_case.check(h, ref["h"], terms["h"], n=1, what="h")
+        if keep:
+            block_case.check(gu, ref["gu"], terms["gu"], n=1, what="gu")
+
+
+def test_glu_strides_and_neighbours():
+    T, H, F = 70, 136, 72
+    x, w, a = glu_inputs(T, H, F, BF16, "rows")
+    want = torch.empty(T, F, dtype=BF16, device="cuda")
+    ws = workspace(B.mhc_glu_workspace_bytes(T, H, F))
+    B.mhc_glu(dev(x), dev(w), want, ws, add=dev(a))
+    wide = torch.full((T, 4, H), float("nan"), dtype=BF16, device="cuda")
+    wide[:, 2] = dev(x)
+    wide_add = torch.full((T, 2 * F + 8), float("nan"), dtype=BF16, device="cuda")
+    wide_add[:, 8:] = dev(a)
+    out = torch.full((T + 2, F + 16), 5.0, dtype=BF16, device="cuda")
+    B.mhc_glu(wide[:, 2], dev(w), out[1:T + 1, 8:F + 8], ws, add=wide_add[:, 8:])
+    assert torch.equal(out[1:T + 1, 8:F + 8], want)
+    out[1:T + 1, 8:F + 8] = 5.0
+    assert bool((out == 5).all())
+    B.mhc_glu(dev(x)[:0], dev(w), want[:0], ws)
+
+
+@pytest.mark.parametrize("T", [5, 200])
+def test_glu_keeps_rows_and_features_apart(T):
+    # a NaN in one token's row and an infinity in one feature's weights stay there
+    H, F = 72, 200
+    x, w, _ = glu_inputs(T, H, F, BF16, "none")
+    x[T - 2, 3] = float("nan")
+    w[F - 1, 0], w[F + 7, 1] = float("inf"), float("nan")
+    h = torch.empty(T, F, dtype=BF16, device="cuda")
+    B.mhc_glu(dev(x), dev(w), h, workspace(B.mhc_glu_workspace_bytes(T, H, F)))
+    bad = ~torch.isfinite(h).cpu()
+    want = torch.zeros(T, F, dtype=torch.bool)
+    want[T - 2], want[:, 7] = True, True
+    assert torch.equal(bad[:, :F - 1], want[:, :F - 1])

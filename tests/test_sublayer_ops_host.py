@@ -66,3 +66,29 @@ def test_dropout_reference_by_hand():
     assert torch.equal(R.dropout(y, None, 1.0, 1, 2)[0], torch.zeros(2, 8).double())
     out = R.dropout(torch.ones(100, 40), None, 0.25, 7, 9)[0]
     assert set(out.unique().tolist()) == {0.0, 4 / 3} and abs(float((out == 0).double().mean()) - 0.25) < 5 * (0.1875 / 4000) ** 0.5
+
+
+GLU = dict(x=A, ld_x=64, w=A + STEP, add=A + 2 * STEP, ld_add=256, act=0, T=4, H=64, F=128, dtype=0, gu=A + 3 * STEP,
+           h=A + 4 * STEP, ld_h=128, ws=A + 5 * STEP, ws_bytes=1 << 27, stream=None)
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(dtype=2), -10), (dict(dtype=5), -10), (dict(act=4), -10), (dict(act=-1), -10), (dict(T=-1), -2), (dict(T=2 ** 31), -2),
+    (dict(H=60), -2), (dict(H=0), -2), (dict(F=132, ld_h=136), -2), (dict(F=0), -2), (dict(F=2 ** 21, ld_h=2 ** 21, ld_add=2 ** 22), -2),
+    (dict(ld_x=56), -2), (dict(ld_x=68), -2), (dict(ld_add=128), -2), (dict(ld_add=260), -2), (dict(ld_h=120), -2),
+    (dict(x=None), -1), (dict(w=None), -1), (dict(h=None), -1), (dict(x=A + 8), -3), (dict(w=A + STEP + 2), -3),
+    (dict(add=A + 2 * STEP + 4), -3), (dict(gu=A + 3 * STEP + 8), -3), (dict(h=A + 4 * STEP + 8), -3), (dict(ws=A + 5 * STEP + 4), -3),
+    (dict(ws=None), -5), (dict(ws_bytes=100), -5), (dict(h=A), -9), (dict(h=A + STEP), -9), (dict(gu=A + 2 * STEP), -9),
+    (dict(gu=A + 4 * STEP), -9), (dict(ws=A + 4 * STEP), -9), (dict(ws=A), -9), (dict(T=0, x=None, h=None, ws=None), 0)])
+def test_glu_refusals(L, over, code):
+    assert _call(L.mhc_glu, GLU, over) == code
+
+
+def test_glu_reference_is_torch():
+    g = torch.Generator().manual_seed(4)
+    x, w = torch.randn(3, 8, generator=g).double(), torch.randn(10, 8, generator=g).double()
+    f = torch.nn.functional
+    for name, fn in (("silu", f.silu), ("gelu", f.gelu), ("gelu_tanh", lambda v: f.gelu(v, approximate="tanh")), ("relu", f.relu)):
+        a, b = (x @ w.t())[:, :5].requires_grad_(), (x @ w.t())[:, 5:]
+        assert torch.allclose(R.glu(x, w, None, name)[0]["h"], (fn(a) * b).detach(), rtol=1e-9, atol=1e-12)
+        assert torch.allclose(R.act(a.detach(), name)[1], torch.autograd.grad(fn(a).sum(), a)[0], rtol=1e-9, atol=1e-12)
