@@ -417,6 +417,20 @@ size_t mhc_glu_workspace_bytes(int64_t T, int H, int F);
 int mhc_glu(const void* x, int64_t ld_x, const void* w, const void* add, int64_t ld_add, int act, int64_t T, int H, int F,
             mhc_dtype dtype, void* gu, void* h, int64_t ld_h, void* workspace, size_t ws_bytes, void* stream);
 
+/* The gradient of mhc_glu(), from dh and the kept gu:
+ *   dgu = [dh u act'(g) | dh act(g)]  (the gradient by `add`, and by what an adapter added)
+ *   dx  = dgu w,  dw = dgu^T x
+ *   dgu   [T,2F] of `dtype`, required; dx and dw are the products of its rounded values, which
+ *         the tensor cores take: their own error is that of dgu's rounding
+ *   dx    [T,H] of `dtype`, or NULL: not wanted (then w may be NULL)
+ *   dw    [2F,H] of `dtype` or fp32 (dw_dtype), or NULL: not wanted (then x may be NULL); with
+ *         `accumulate` not 0 added to, else written (zero for T = 0)
+ * x as in mhc_glu(); all other matrices are dense.  Workspace: mhc_glu_workspace_bytes().
+ * Errors as mhc_glu(). */
+int mhc_glu_grad(const void* dh, const void* gu, const void* x, int64_t ld_x, const void* w, int act, int64_t T, int H, int F,
+                 mhc_dtype dtype, void* dgu, void* dx, void* dw, mhc_dtype dw_dtype, int accumulate, void* workspace,
+                 size_t ws_bytes, void* stream);
+
 /* Dropout before a residual add, with a mask that is never stored:
  *   out[t,h] = r[t,h] + (keep(t,h) ? y[t,h] / (1 - p) : 0)
  *   keep(t,h)  word i % 4 >= p 2^32 (rounded), i = t H + h, of Philox 4x32 with ten rounds

@@ -100,6 +100,8 @@ def lib():
         L.mhc_glu_workspace_bytes.argtypes = [I64, I, I]
         L.mhc_glu.restype = I
         L.mhc_glu.argtypes = [P, I64, P, P, I64, I, I64, I, I, I, P, P, I64, P, SZ, P]
+        L.mhc_glu_grad.restype = I
+        L.mhc_glu_grad.argtypes = [P, P, P, I64, P, I, I64, I, I, I, P, P, P, I, I, P, SZ, P]
         L.mhc_dropout.restype = I
         L.mhc_dropout.argtypes = [P, I64, P, I64, C.c_double, P, I64, I, I, P, I64, P]
         L.mhc_last_launch_count.restype = I
@@ -489,6 +491,22 @@ def mhc_glu(x, w, h, workspace, add=None, gu=None, act: int = MHC_ACT_SILU, stre
     rc = L.mhc_glu(x.data_ptr(), _pitch(x, T, H, dt, "x"), _dense(w, (2 * F, H), dt, "w"), None if add is None else add.data_ptr(),
                    _addend(add, T, 2 * F, dt), act, T, H, F, _dtype(x, "x"), _dense(gu, (T, 2 * F), dt, "gu"), h.data_ptr(),
                    _pitch(h, T, F, dt, "h"), ws, n, _where(stream))
+    if rc:
+        _check(rc)
+
+
+def mhc_glu_grad(dh, gu, x, w, dgu, dx, dw, workspace, act: int = MHC_ACT_SILU, accumulate: bool = False, stream=None) -> None:
+    """The gradient of mhc_glu: ``dgu`` [T, 2F], ``dx`` [T, H] and ``dw`` [2F, H] (fp32 or x's
+    type) from ``dh`` [T, F] and the kept ``gu``; dx and dw may be None."""
+    L = _ops()
+    (T, F), dt = dh.shape, dh.dtype
+    H = x.shape[1] if x is not None else w.shape[1] if w is not None else 8
+    ws, n = _space(workspace)
+    rc = L.mhc_glu_grad(_dense(dh, (T, F), dt, "dh"), _dense(gu, (T, 2 * F), dt, "gu"), None if x is None else x.data_ptr(),
+                        _pitch(x, T, H, dt, "x"), _dense(w, (2 * F, H), dt, "w"), act, T, H, F, _dtype(dh, "dh"),
+                        _dense(dgu, (T, 2 * F), dt, "dgu"), _dense(dx, (T, H), dt, "dx"),
+                        None if dw is None else _dense(dw, (2 * F, H), dw.dtype, "dw"), MHC_DT_F32 if dw is None else _dtype(dw, "dw"),
+                        int(accumulate), ws, n, _where(stream))
     if rc:
         _check(rc)
 

@@ -19,7 +19,7 @@ struct GluEpilogue {
     constexpr int half = BN / 2;
     return n * half + (j < half ? j : (int)F + j - half);
   }
-  __device__ __forceinline__ void store(uint32_t tmem, int64_t row, int n) const {
+  __device__ __forceinline__ void store(uint32_t tmem, int64_t row, int n, int) const {
     constexpr int half = BN / 2;
 #pragma unroll 1
     for (int c = 0; c < half; c += 16) {
@@ -64,12 +64,13 @@ struct GluEpilogue {
 template <typename E>
 static cudaError_t glu_launch(const void* x, int64_t ld_x, const void* w, const void* add, int64_t ld_add, int act, int64_t T,
                               int H, int F, void* gu, void* h, int64_t ld_h, void* ws, cudaStream_t s) {
-  using S = Tile<1, 256, false, false>;
-  CUtensorMap a, b;
-  if (!encode_2d<E>(&a, x, T, H, ld_x, S::kBoxA) || !encode_2d<E>(&b, w, 2 * (int64_t)F, H, H, S::kBoxB))
+  using S = Tile<2, 256, false>;
+  Work<1> p;
+  p.status = static_cast<unsigned*>(ws);
+  if (!problem<E, S>(&p.p[0], T, (F + S::BN / 2 - 1) / (S::BN / 2), H, x, false, ld_x, w, 2 * (int64_t)F, H))
     return cudaErrorInvalidValue;
   const GluEpilogue<E, S::BN> epi = {static_cast<const E*>(add), static_cast<E*>(gu), static_cast<E*>(h), T, F, ld_add, ld_h, act};
-  return product_launch<E, S>(a, b, T, (F + S::BN / 2 - 1) / (S::BN / 2), H, static_cast<unsigned*>(ws), epi, s);
+  return product_launch<E, S, 1>(p, epi, s);
 }
 
 }  // namespace mhc

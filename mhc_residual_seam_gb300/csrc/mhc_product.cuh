@@ -11,7 +11,8 @@
 //
 // Either operand may lie with its reduction index k adjacent ("K-major", a row per
 // m or n) or with m or n adjacent (a row per k): then a tile is fetched as blocks of
-// 64 columns and the MMA reads it transposed.
+// 64 columns and the MMA reads it transposed.  One launch may do two products, so
+// that the second's tiles fill the SMs that the first leaves.
 //
 // What lies outside the matrices is fetched as zeros, so no size needs padding.
 // Every wait is bounded; one that runs out sets bit 1 of the workspace's status
@@ -111,11 +112,10 @@ __device__ __forceinline__ void take16(uint32_t* r) {
 // Shared-memory descriptor of a tile in the 128-byte swizzle layout.  K-major: rows of
 // 128 bytes (64 k), 8-row groups 1024 bytes apart.  Otherwise blocks of 64 columns (128
 // bytes) by 64 k: 8-k groups 1024 bytes apart, blocks 8192.
-template <bool MN>
-__device__ __forceinline__ uint64_t tile_desc(uint32_t saddr) {
+__device__ __forceinline__ uint64_t tile_desc(uint32_t saddr, bool mn) {
   uint64_t d = 0;
   d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)(MN ? 8192 >> 4 : 1) << 16;
+  d |= (uint64_t)(mn ? 8192 >> 4 : 1) << 16;
   d |= (uint64_t)(1024 >> 4) << 32;
   d |= (uint64_t)1 << 46;
   d |= (uint64_t)2 << 61;
@@ -129,40 +129,49 @@ __host__ __device__ constexpr uint32_t product_idesc(int M, int N, bool amn, boo
 }
 
 // ----------------------------------------------------------------- kernel --
+// One product: D in tiles of (128 CG) x BN, `kblocks` stages each; `amn`: A lies with m
+// adjacent.
+struct Problem {
+  CUtensorMap a, b;
+  int num_m, num_n, kblocks;
+  bool amn;
+};
+// The products of one launch.  Tiles are handed out in order, so the ones with more
+// stages come first.
+template <int N>
 struct Work {
-  int num_m, num_n, kblocks;  // tiles and stages per tile
+  Problem p[N];
+  int tiles[N];  // of this and the products before it
   unsigned* status;
 };
 
-template <int CG_, int BN_, bool AMN_, bool BMN_>
+template <int CG_, int BN_, bool BMN_>
 struct Tile {
-  static constexpr int CG = CG_, BN = BN_;      // CTAs of a group, columns of its tile
-  static constexpr bool AMN = AMN_, BMN = BMN_;
-  static constexpr int kRowsB = BN / CG;        // rows of B per CTA
+  static constexpr int CG = CG_, BN = BN_;  // CTAs of a group, columns of its tile
+  static constexpr bool BMN = BMN_;         // B lies with n adjacent
+  static constexpr int kRowsB = BN / CG;    // rows of B per CTA
   static constexpr int kA = kBM * 128, kB = kRowsB * 128, kStage = kA + kB;
   static constexpr int kStages = (200 * 1024) / kStage < 8 ? (200 * 1024) / kStage : 8;
-  static constexpr int kCols = 2 * BN;          // two accumulators
+  static constexpr int kCols = 2 * BN <= 256 ? 256 : 512;  // two accumulators
   static constexpr size_t kSmem = (size_t)kStages * kStage + 1024 + 256;
-  // rows of a TMA box: 64 columns are one swizzle row
-  static constexpr int kBoxA = AMN ? 64 : kBM, kBoxB = BMN ? 64 : (kRowsB > 128 ? 128 : kRowsB);
+  static constexpr int kBoxB = BMN ? 64 : (kRowsB > 128 ? kRowsB / 2 : kRowsB);  // rows of a TMA box of B
 };
 
 // Tile number -> (m, n): eight rows of tiles at a time, so that the tiles in flight
 // share rows of A and of B in L2.
-__device__ __forceinline__ void tile_place(int t, const Work& w, int& m, int& n) {
+__device__ __forceinline__ void tile_place(int t, int num_m, int num_n, int& m, int& n) {
   constexpr int kGroup = 8;
-  const int per = kGroup * w.num_n, g = t / per, r = t - g * per;
-  const int rows = min(kGroup, w.num_m - g * kGroup);
+  const int per = kGroup * num_n, g = t / per, r = t - g * per;
+  const int rows = min(kGroup, num_m - g * kGroup);
   n = r / rows;
   m = g * kGroup + r - n * rows;
 }
 
 // Epi: `row_b(n_tile, j)` is the row of B for column j of the tile; `store(tmem, row,
-// n_tile)` makes a lane's row of outputs.
-template <typename E, typename S, typename Epi>
+// n_tile, product)` makes a lane's row of outputs.
+template <typename E, typename S, int NP, typename Epi>
 __global__ void __launch_bounds__(256, 1)
-    product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const Work w,
-                   const Epi epi) {
+    product_kernel(const __grid_constant__ Work<NP> w, const __grid_constant__ Epi epi) {
   constexpr int CG = S::CG, kStages = S::kStages;
   extern __shared__ char raw[];
   const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
@@ -191,7 +200,8 @@ __global__ void __launch_bounds__(256, 1)
   const uint32_t tmem = *tmem_slot;
 
   const int groups = gridDim.x / CG, group = blockIdx.x / CG;
-  const int tiles = w.num_m * w.num_n;
+  const int tiles = w.tiles[NP - 1];
+  auto product_of = [&](int t) { return NP == 2 && t >= w.tiles[0] ? NP - 1 : 0; };
   bool ok = true;
 
   if (warp == 0) {  // ------------------------------------------- producer
@@ -199,25 +209,28 @@ __global__ void __launch_bounds__(256, 1)
       int st = 0, used = 0;
       uint32_t ph = 1;
       for (int t = group; t < tiles && ok; t += groups) {
+        const int which = product_of(t);
+        const Problem& p = w.p[which];
         int m, n;
-        tile_place(t, w, m, n);
+        tile_place(which ? t - w.tiles[0] : t, p.num_m, p.num_n, m, n);
         const int row = (m * CG + (int)rank) * kBM;
-        for (int k = 0; k < w.kblocks; ++k) {
+        for (int k = 0; k < p.kblocks; ++k) {
           ok = mbar_wait_cluster(empty + st, ph, kProductLimitNs);
           if (!ok) break;
           if (rank == 0) mbar_arrive_expect_tx(full + st, CG * S::kStage);
           const uint32_t bar = CG == 2 ? mapa_shared(smem_u32(full + st), 0) : smem_u32(full + st);
           const uint32_t a = base + st * S::kStage, b = a + S::kA;
-#pragma unroll
-          for (int j = 0; j < kBM; j += S::kBoxA) {
-            if (S::AMN) pair_load<CG>(a + j * 128, &map_a, bar, row + j, k * kBK);
-            else pair_load<CG>(a + j * 128, &map_a, bar, k * kBK, row + j);
+          if (p.amn) {
+            pair_load<CG>(a, &p.a, bar, row, k * kBK);
+            pair_load<CG>(a + 8192, &p.a, bar, row + 64, k * kBK);
+          } else {
+            pair_load<CG>(a, &p.a, bar, k * kBK, row);
           }
 #pragma unroll
           for (int j = 0; j < S::kRowsB; j += S::kBoxB) {
             const int rb = epi.row_b(n, (int)rank * S::kRowsB + j);
-            if (S::BMN) pair_load<CG>(b + j * 128, &map_b, bar, rb, k * kBK);
-            else pair_load<CG>(b + j * 128, &map_b, bar, k * kBK, rb);
+            if (S::BMN) pair_load<CG>(b + j * 128, &p.b, bar, rb, k * kBK);
+            else pair_load<CG>(b + j * 128, &p.b, bar, k * kBK, rb);
           }
           if (used < kStages) ++used;
           if (++st == kStages) st = 0, ph ^= 1;
@@ -231,7 +244,6 @@ __global__ void __launch_bounds__(256, 1)
     }
   } else if (warp == 1) {  // ------------------------------------------ MMA
     if (lane == 0 && rank == 0) {
-      constexpr uint32_t idesc = product_idesc<E>(kBM * CG, S::BN, S::AMN, S::BMN);
       int st = 0, b = 0;
       uint32_t ph = 0, pb = 1;
       for (int t = group; t < tiles && ok; t += groups) {
@@ -239,14 +251,19 @@ __global__ void __launch_bounds__(256, 1)
         if (!ok) break;
         tc_fence_after();
         const uint32_t d = tmem + b * S::BN;
-        for (int k = 0; k < w.kblocks; ++k) {
+        const Problem& p = w.p[product_of(t)];
+        const bool amn = p.amn;
+        const int kblocks = p.kblocks;
+        const uint32_t idesc = product_idesc<E>(kBM * CG, S::BN, amn, S::BMN);
+        // 16 of a stage's 64 k: 32 bytes along a K-major row, else two 8-k groups
+        const uint32_t step_a = (amn ? 2048 : 32) >> 4, step_b = (S::BMN ? 2048 : 32) >> 4;
+        for (int k = 0; k < kblocks; ++k) {
           ok = mbar_wait_cluster(full + st, ph, kProductLimitNs);
           if (!ok) break;
           tc_fence_after();
-          const uint64_t da = tile_desc<S::AMN>(base + st * S::kStage), db = tile_desc<S::BMN>(base + st * S::kStage + S::kA);
+          const uint64_t da = tile_desc(base + st * S::kStage, amn), db = tile_desc(base + st * S::kStage + S::kA, S::BMN);
 #pragma unroll
-          for (int q = 0; q < 4; ++q)  // 16 of the stage's 64 k: 32 bytes along a K-major row, else two 8-k groups
-            pair_mma<CG>(d, da + q * ((S::AMN ? 2048 : 32) >> 4), db + q * ((S::BMN ? 2048 : 32) >> 4), idesc, k | q);
+          for (int q = 0; q < 4; ++q) pair_mma<CG>(d, da + q * step_a, db + q * step_b, idesc, k | q);
           pair_commit<CG>(empty + st);
           if (++st == kStages) st = 0, ph ^= 1;
         }
@@ -261,9 +278,11 @@ __global__ void __launch_bounds__(256, 1)
       ok = __all_sync(0xffffffffu, mbar_wait_cluster(tfull + b, pb, kProductLimitNs));
       if (!ok) break;
       tc_fence_after();
+      const int which = product_of(t);
       int m, n;
-      tile_place(t, w, m, n);
-      epi.store(tmem + b * S::BN + ((uint32_t)(warp & 3) << 21), ((int64_t)m * CG + rank) * kBM + (warp & 3) * 32 + lane, n);
+      tile_place(which ? t - w.tiles[0] : t, w.p[which].num_m, w.p[which].num_n, m, n);
+      epi.store(tmem + b * S::BN + ((uint32_t)(warp & 3) << 21), ((int64_t)m * CG + rank) * kBM + (warp & 3) * 32 + lane, n,
+                which);
       tc_wait_ld();
       tc_fence_before();
       __syncwarp();
@@ -296,23 +315,34 @@ inline bool encode_2d(CUtensorMap* m, const void* p, int64_t rows, int64_t cols,
                 dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// M x N outputs of reduction length K in tiles of S; `num_n` column tiles.
-template <typename E, typename S, typename Epi>
-inline cudaError_t product_launch(const CUtensorMap& a, const CUtensorMap& b, int64_t M, int64_t num_n, int64_t K,
-                                  unsigned* status, const Epi& epi, cudaStream_t s) {
+// D [M, num_n tiles] of reduction length K.  A K-major operand is [rows, K], the other
+// kind [K, rows]; their row strides are ld_*.
+template <typename E, typename S>
+inline bool problem(Problem* p, int64_t M, int64_t num_n, int64_t K, const void* a, bool amn, int64_t ld_a, const void* b,
+                    int64_t rows_b, int64_t ld_b) {
+  p->num_m = (int)((M + kBM * S::CG - 1) / (kBM * S::CG));
+  p->num_n = (int)num_n;
+  p->kblocks = (int)((K + kBK - 1) / kBK);
+  p->amn = amn;
+  return encode_2d<E>(&p->a, a, amn ? K : M, amn ? M : K, ld_a, amn ? 64 : kBM) &&
+         encode_2d<E>(&p->b, b, S::BMN ? K : rows_b, S::BMN ? rows_b : K, ld_b, S::kBoxB);
+}
+
+template <typename E, typename S, int NP, typename Epi>
+inline cudaError_t product_launch(Work<NP>& w, const Epi& epi, cudaStream_t s) {
   static SmemGrant grant;
-  auto k = product_kernel<E, S, Epi>;
+  auto k = product_kernel<E, S, NP, Epi>;
   cudaError_t e = allow_smem(grant, (const void*)k, S::kSmem);
   if (e != cudaSuccess) return e;
   int sms = 0;
   e = sm_count(&sms);
   if (e != cudaSuccess) return e;
-  Work w;
-  w.num_m = (int)((M + kBM * S::CG - 1) / (kBM * S::CG));
-  w.num_n = (int)num_n;
-  w.kblocks = (int)((K + kBK - 1) / kBK);
-  w.status = status;
-  const int64_t tiles = (int64_t)w.num_m * num_n;
+  int64_t tiles = 0;
+  for (int i = 0; i < NP; ++i) {
+    tiles += (int64_t)w.p[i].num_m * w.p[i].num_n;
+    if (tiles > 0x7fffffff) return cudaErrorInvalidValue;
+    w.tiles[i] = (int)tiles;
+  }
   const int64_t groups = tiles < sms / S::CG ? tiles : sms / S::CG;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(groups * S::CG));
@@ -325,7 +355,7 @@ inline cudaError_t product_launch(const CUtensorMap& a, const CUtensorMap& b, in
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, k, a, b, w, epi);
+  e = cudaLaunchKernelEx(&cfg, k, w, epi);
   if (e != cudaSuccess) cudaGetLastError();  // it is this call's, not the next one's
   return e;
 }

@@ -76,3 +76,23 @@ def glu(x, w, add, name):
     # the product of both errors
     terms = terms + off[:, :F] * off[:, F:] * 2.0 ** -24
     return {"h": a * u, "gu": gu}, {"h": terms, "gu": off}
+
+
+def glu_grad(dh, gu, x, w, name, dtype):
+    """{dgu, dx, dw} and their terms in units of 2^-24: dgu's rounding to its type enters the products
+    with at most half a unit of each factor, and their sums as in glu()."""
+    from block_case import TINY, UNIT
+    F = dh.shape[1]
+    g, u, d = gu[:, :F].double(), gu[:, F:].double(), dh.double()
+    a, da, q = act(g, name)
+    dgu = torch.cat([d * u * da, d * a], 1)
+    # the derivative is a sum of terms of up to |g| (1 + |q'|): some units of each, and one per unit of the exponential's argument
+    slope = 1.0 if name in ("silu", "relu") else math.sqrt(8 / math.pi) * (1 + 3 * 0.044715 * g ** 2) if name == "gelu_tanh" else 1.0
+    size = 1.2 + (g.abs() * slope * torch.exp(-q.abs()) if name != "gelu" else g.abs() * torch.exp(-q) * 0.4)
+    n = 64 + 4 * q.abs()
+    off = torch.cat([n * (d * u).abs() * size, n * (d * a).abs()], 1)
+    step = (UNIT[dtype] * dgu.abs() * (1 + 2.0 ** -7) + TINY[dtype]) * 2.0 ** 24 + off
+    out = {"dgu": dgu, "dx": dgu @ w.double(), "dw": dgu.t() @ x.double()}
+    big = dgu.abs() + step * 2.0 ** -24
+    return out, {"dgu": off, "dx": (step + 2 * (2 * F + 1) * big) @ w.double().abs(),
+                 "dw": (step + 2 * (len(x) + 1) * big).t() @ x.double().abs()}

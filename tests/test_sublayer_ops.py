@@ -203,3 +203,67 @@ def test_glu_keeps_rows_and_features_apart(T):
     want = torch.zeros(T, F, dtype=torch.bool)
     want[T - 2], want[:, 7] = True, True
     assert torch.equal(bad[:, :F - 1], want[:, :F - 1])
+
+
+# ----------------------------------------------------- gated gradient --
+@pytest.mark.parametrize("T,H,F,dtype,act", [
+    (1, 8, 8, BF16, "silu"), (3, 72, 40, F16, "gelu"), (64, 64, 64, BF16, "relu"), (65, 136, 200, BF16, "gelu_tanh"),
+    (129, 520, 72, F16, "silu"), (200, 264, 128, BF16, "gelu"), (256, 256, 136, BF16, "silu"), (257, 1032, 264, F16, "relu"),
+    (1003, 512, 344, BF16, "gelu"), (700, 64, 1000, BF16, "silu"), (30, 2056, 520, BF16, "gelu_tanh")])
+def test_glu_grad(T, H, F, dtype, act):
+    x, w, _ = glu_inputs(T, H, F, dtype, "none")
+    g = gen(T)
+    gu, dh = normal(g, T, 2 * F, std=1.5, dtype=dtype), normal(g, T, F, dtype=dtype)
+    ref, terms = R.glu_grad(dh, gu, x, w, act, dtype)
+    ws = workspace(B.mhc_glu_workspace_bytes(T, H, F))
+    e = lambda *s, t=dtype: torch.full(s, 7.0, dtype=t, device="cuda")  # noqa: E731
+    dgu, dx, dw = e(T, 2 * F), e(T, H), e(2 * F, H)
+    B.mhc_glu_grad(dev(dh), dev(gu), dev(x), dev(w), dgu, dx, dw, ws, act=R.ACTS.index(act))
+    B.mhc_check_status(ws)
+    for got, k in ((dgu, "dgu"), (dx, "dx"), (dw, "dw")):
+        block_case.check(got, ref[k], terms[k], n=1, what=k)
+    # one product alone; 32-bit weights' gradients, added to what is there
+    again, dx2 = e(T, 2 * F), e(T, H)
+    B.mhc_glu_grad(dev(dh), dev(gu), None, dev(w), again, dx2, None, ws, act=R.ACTS.index(act))
+    assert torch.equal(again, dgu) and torch.equal(dx2, dx)
+    old = normal(g, 2 * F, H)
+    acc = dev(old)
+    B.mhc_glu_grad(dev(dh), dev(gu), dev(x), None, again, None, acc, ws, act=R.ACTS.index(act), accumulate=True)
+    block_case.check(acc, ref["dw"] + old.double(), terms["dw"] + old.double().abs(), n=1, what="dw added")
+    B.mhc_glu_grad(dev(dh), dev(gu), None, None, again, None, None, ws, act=R.ACTS.index(act))
+    assert torch.equal(again, dgu)
+
+
+def test_glu_grad_of_no_tokens():
+    H, F = 64, 72
+    ws = workspace(B.mhc_glu_workspace_bytes(1, H, F))
+    dw = torch.full((2 * F, H), 3.0, device="cuda")
+    z = lambda n: torch.empty(0, n, dtype=BF16, device="cuda")  # noqa: E731
+    w = torch.zeros(2 * F, H, dtype=BF16, device="cuda")
+    B.mhc_glu_grad(z(F), z(2 * F), z(H), w, z(2 * F), z(H), dw, ws, accumulate=True)
+    assert bool((dw == 3).all())
+    B.mhc_glu_grad(z(F), z(2 * F), z(H), w, z(2 * F), z(H), dw, ws)
+    assert not bool(dw.any())
+
+
+def test_glu_grad_against_differences():
+    # the directional derivative of sum(h * up), from two runs of the forward pass with weights apart by exact steps
+    T, H, F = 40, 64, 48
+    x, w, _ = glu_inputs(T, H, F, F16, "none")
+    ws = workspace(B.mhc_glu_workspace_bytes(T, H, F))
+    e = lambda *s: torch.empty(*s, dtype=F16, device="cuda")  # noqa: E731
+    h, gu, dgu, dx, dw = e(T, F), e(T, 2 * F), e(T, 2 * F), e(T, H), e(2 * F, H)
+    up = normal(gen(8), T, F, dtype=F16)
+    B.mhc_glu(dev(x), dev(w), h, ws, gu=gu)
+    B.mhc_glu_grad(dev(up), gu, dev(x), dev(w), dgu, dx, dw, ws)
+    way = torch.sign(dw.cpu().double())
+    step = 2.0 ** -9
+    f = []
+    for s in (step, -step):
+        moved = (w.double() + s * way).to(F16)
+        B.mhc_glu(dev(x), dev(moved), h, ws)
+        f.append((float((h.cpu().double() * up.double()).sum()), moved.double()))
+    want = float((dw.cpu().double() * (f[0][1] - f[1][1])).sum())
+    # h's rounding (2^-11 of each term, random signs: five deviations), the gradient's own, and the third derivative
+    noise = 5 * 2.0 ** -11 * float((h.cpu().double() * up.double()).square().sum().sqrt()) * 2
+    assert abs(f[0][0] - f[1][0] - want) <= noise + 0.01 * abs(want), (f[0][0] - f[1][0], want, noise)

@@ -92,3 +92,31 @@ def test_glu_reference_is_torch():
         a, b = (x @ w.t())[:, :5].requires_grad_(), (x @ w.t())[:, 5:]
         assert torch.allclose(R.glu(x, w, None, name)[0]["h"], (fn(a) * b).detach(), rtol=1e-9, atol=1e-12)
         assert torch.allclose(R.act(a.detach(), name)[1], torch.autograd.grad(fn(a).sum(), a)[0], rtol=1e-9, atol=1e-12)
+
+
+GGRAD = dict(dh=A, gu=A + STEP, x=A + 2 * STEP, ld_x=64, w=A + 3 * STEP, act=0, T=4, H=64, F=128, dtype=0, dgu=A + 4 * STEP,
+             dx=A + 5 * STEP, dw=A + 6 * STEP, dw_dtype=2, acc=0, ws=A + 7 * STEP, ws_bytes=1 << 24, stream=None)
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(dtype=2), -10), (dict(dw_dtype=1), -10), (dict(act=9), -10), (dict(T=-1), -2), (dict(H=12), -2), (dict(F=4), -2),
+    (dict(ld_x=60), -2), (dict(ld_x=32), -2), (dict(dh=None), -1), (dict(gu=None), -1), (dict(dgu=None), -1), (dict(x=None), -1),
+    (dict(w=None), -1), (dict(dh=A + 8), -3), (dict(dw=A + 6 * STEP + 4), -3), (dict(ws=A + 7 * STEP + 2), -3), (dict(ws=None), -5),
+    (dict(ws_bytes=10), -5), (dict(dgu=A + STEP), -9), (dict(dx=A + 2 * STEP), -9), (dict(dw=A + 3 * STEP), -9), (dict(dx=A + 4 * STEP), -9),
+    (dict(dw=A + 5 * STEP), -9), (dict(ws=A), -9), (dict(ws=A + 4 * STEP), -9), (dict(T=0, acc=1, dh=None, dgu=None, ws=None), 0),
+    (dict(T=0, dw=None, dh=None, dgu=None, ws=None), 0)])
+def test_glu_grad_refusals(L, over, code):
+    assert _call(L.mhc_glu_grad, GGRAD, over) == code
+
+
+def test_glu_reference_gradient_is_the_derivative():
+    g = torch.Generator().manual_seed(5)
+    n = lambda *s: torch.randn(*s, generator=g, dtype=torch.float64)  # noqa: E731
+    x, w, dh = n(4, 6).requires_grad_(), n(10, 6).requires_grad_(), n(4, 5)
+    for name in R.ACTS:
+        gu = x @ w.t()
+        h = R.act(gu[:, :5], name)[0] * gu[:, 5:]
+        want = torch.autograd.grad((h * dh).sum(), (gu, x, w))
+        got = R.glu_grad(dh, gu.detach(), x.detach(), w.detach(), name, torch.bfloat16)[0]
+        for k, v in zip(("dgu", "dx", "dw"), want):
+            assert torch.allclose(got[k], v, rtol=1e-9, atol=1e-11), (name, k)
