@@ -431,6 +431,28 @@ int mhc_glu_grad(const void* dh, const void* gu, const void* x, int64_t ld_x, co
                  mhc_dtype dtype, void* dgu, void* dx, void* dw, mhc_dtype dw_dtype, int accumulate, void* workspace,
                  size_t ws_bytes, void* stream);
 
+/* Bytes of the workspace of mhc_lora().  It needs no initialisation and holds nothing
+ * between calls.  The size does not fall as T grows. */
+size_t mhc_lora_workspace_bytes(int64_t T, int R);
+
+/* Low-rank adapters of many requests beside a shared projection:
+ *   out[t,:] = base[t,:] + scale[i] B_i (A_i x[t]),  i = index[t]
+ *   x       [T,H], rows ld_x apart
+ *   a, b    [n,R,H] and [n,N,R], dense: the adapters' two factors (a smaller rank is
+ *           filled up with zeros)
+ *   index   [T] int32: the token's adapter; outside [0, n) it has none: out = base
+ *   scale   [n] fp32, or NULL: 1
+ *   base    [T,N], rows ld_base apart: the shared projection's result, or NULL: 0 (out is
+ *           then what the adapters add, as mhc_glu() takes it in `add`)
+ *   out     [T,N], rows ld_out apart; may be base (same stride, in place)
+ * bf16 or fp16; A_i x is kept in fp32 and enters the second product as two 16-bit values.
+ * The tokens may come in any order; runs of one request cost least.  T <= 2^30, H and N
+ * multiples of 8, at most 2^20, R a multiple of 8, at most 256.  Errors: MHC_ERR_CONFIG,
+ * MHC_ERR_SHAPE, MHC_ERR_NULL, MHC_ERR_ALIGN, MHC_ERR_WORKSPACE, MHC_ERR_ALIAS, MHC_ERR_CUDA. */
+int mhc_lora(const void* x, int64_t ld_x, const void* a, const void* b, const int32_t* index, const float* scale,
+             int64_t T, int H, int N, int R, int n, mhc_dtype dtype, const void* base, int64_t ld_base, void* out,
+             int64_t ld_out, void* workspace, size_t ws_bytes, void* stream);
+
 /* Dropout before a residual add, with a mask that is never stored:
  *   out[t,h] = r[t,h] + (keep(t,h) ? y[t,h] / (1 - p) : 0)
  *   keep(t,h)  word i % 4 >= p 2^32 (rounded), i = t H + h, of Philox 4x32 with ten rounds

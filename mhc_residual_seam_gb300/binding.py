@@ -102,6 +102,10 @@ def lib():
         L.mhc_glu.argtypes = [P, I64, P, P, I64, I, I64, I, I, I, P, P, I64, P, SZ, P]
         L.mhc_glu_grad.restype = I
         L.mhc_glu_grad.argtypes = [P, P, P, I64, P, I, I64, I, I, I, P, P, P, I, I, P, SZ, P]
+        L.mhc_lora_workspace_bytes.restype = SZ
+        L.mhc_lora_workspace_bytes.argtypes = [I64, I]
+        L.mhc_lora.restype = I
+        L.mhc_lora.argtypes = [P, I64, P, P, P, P, I64, I, I, I, I, I, P, I64, P, I64, P, SZ, P]
         L.mhc_dropout.restype = I
         L.mhc_dropout.argtypes = [P, I64, P, I64, C.c_double, P, I64, I, I, P, I64, P]
         L.mhc_last_launch_count.restype = I
@@ -507,6 +511,25 @@ def mhc_glu_grad(dh, gu, x, w, dgu, dx, dw, workspace, act: int = MHC_ACT_SILU, 
                         _dense(dgu, (T, 2 * F), dt, "dgu"), _dense(dx, (T, H), dt, "dx"),
                         None if dw is None else _dense(dw, (2 * F, H), dw.dtype, "dw"), MHC_DT_F32 if dw is None else _dtype(dw, "dw"),
                         int(accumulate), ws, n, _where(stream))
+    if rc:
+        _check(rc)
+
+
+def mhc_lora_workspace_bytes(T: int, R: int) -> int:
+    return int(lib().mhc_lora_workspace_bytes(int(T), int(R)))
+
+
+def mhc_lora(x, a, b, index, out, workspace, scale=None, base=None, stream=None) -> None:
+    """base + scale[i] * b[i] @ (a[i] @ x[t]), i = index[t], into ``out`` [T, N]: of ``x``
+    [T, H], ``a`` [n, R, H] and ``b`` [n, N, R]; out may be base."""
+    L = _ops()
+    (T, H), dt = x.shape, x.dtype
+    n, N, R = b.shape
+    ws, size = _space(workspace)
+    rc = L.mhc_lora(x.data_ptr(), _pitch(x, T, H, dt, "x"), _dense(a, (n, R, H), dt, "a"), _dense(b, (n, N, R), dt, "b"),
+                    _vec(index, T, _I32, "index"), _vec(scale, n, _F32, "scale"), T, H, N, R, n, _dtype(x, "x"),
+                    None if base is None else base.data_ptr(), _pitch(base, T, N, dt, "base"), out.data_ptr(),
+                    _pitch(out, T, N, dt, "out"), ws, size, _where(stream))
     if rc:
         _check(rc)
 

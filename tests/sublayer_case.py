@@ -96,3 +96,26 @@ def glu_grad(dh, gu, x, w, name, dtype):
     big = dgu.abs() + step * 2.0 ** -24
     return out, {"dgu": off, "dx": (step + 2 * (2 * F + 1) * big) @ w.double().abs(),
                  "dw": (step + 2 * (len(x) + 1) * big).t() @ x.double().abs()}
+
+
+# --------------------------------------------------------------- adapters --
+def lora(x, a, b, index, scale, base):
+    """(out, its terms in units of 2^-24): v = A x is off by 2 H units of its products' absolute sum and, as two
+    16-bit values of a row brought to at most 2, by 2^-16 of itself (bf16; both halves round to nearest) or
+    2^-24 of the row's largest (fp16's subnormal step); B v by 2 R units of each of its two sums."""
+    T, H = x.shape
+    n, N, R = b.shape
+    out, terms = torch.zeros(T, N, dtype=torch.float64), torch.zeros(T, N, dtype=torch.float64)
+    if base is not None:
+        out, terms = base.double().clone(), base.double().abs()
+    for t in range(T):
+        i = int(index[t])
+        if not 0 <= i < n:
+            continue
+        s = 1.0 if scale is None else float(scale[i])
+        A, Bm, X = a[i].double(), b[i].double(), x[t].double()
+        v, size = A @ X, A.abs() @ X.abs()
+        off = 2 * (H + 32) * size + 2.0 ** 8 * v.abs() + 4 * v.abs().max() + 2 * (2 * R + 4) * (v.abs() + size * (H + 32) * 2.0 ** -23)
+        out[t] += s * (Bm @ v)
+        terms[t] += abs(s) * (Bm.abs() @ off) + 4 * abs(s) * (Bm @ v).abs()
+    return out, terms

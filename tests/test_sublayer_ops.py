@@ -267,3 +267,90 @@ def test_glu_grad_against_differences():
     # h's rounding (2^-11 of each term, random signs: five deviations), the gradient's own, and the third derivative
     noise = 5 * 2.0 ** -11 * float((h.cpu().double() * up.double()).square().sum().sqrt()) * 2
     assert abs(f[0][0] - f[1][0] - want) <= noise + 0.01 * abs(want), (f[0][0] - f[1][0], want, noise)
+
+
+# ---------------------------------------------------------------- adapters --
+def lora_inputs(T, H, N, R, n, dtype, order, seed=0):
+    g = gen(seed + T + H + N + R)
+    x, a, b = normal(g, T, H, dtype=dtype), normal(g, n, R, H, std=H ** -0.5, dtype=dtype), normal(g, n, N, R, std=R ** -0.5, dtype=dtype)
+    index = torch.randint(-1, n + 1, (T,), generator=g)
+    if order == "runs":
+        index = index.sort().values
+    if order == "one":
+        index[:] = n - 1
+    return x, a, b, index.int(), 0.5 + torch.rand(n, generator=g), normal(g, T, N, dtype=dtype)
+
+
+@pytest.mark.parametrize("T,H,N,rank,n,dtype,order,scaled,based", [
+    (1, 8, 8, 8, 1, BF16, "one", False, False), (2, 40, 72, 8, 3, F16, "any", True, True), (17, 136, 64, 16, 4, BF16, "any", True, True),
+    (16, 1032, 200, 24, 2, BF16, "one", True, False), (33, 264, 136, 32, 40, F16, "any", False, True), (64, 520, 256, 16, 32, BF16, "any", True, True),
+    (64, 512, 320, 64, 5, BF16, "runs", True, True), (65, 72, 1000, 40, 3, F16, "one", True, False), (130, 2056, 72, 64, 7, F16, "runs", True, True),
+    (200, 320, 264, 128, 3, BF16, "any", False, False), (100, 64, 520, 256, 2, F16, "any", True, True), (300, 5120, 64, 16, 9, BF16, "runs", True, True),
+    (63, 96, 8, 72, 70, BF16, "any", True, True)])
+def test_lora(T, H, N, rank, n, dtype, order, scaled, based):
+    x, a, b, index, scale, base = lora_inputs(T, H, N, rank, n, dtype, order)
+    scale, base = scale if scaled else None, base if based else None
+    ref, terms = R.lora(x, a, b, index, scale, base)
+    ws = torch.full((B.mhc_lora_workspace_bytes(T, rank),), 0xFF, dtype=torch.uint8, device="cuda")
+    out = torch.full((T, N), 7.0, dtype=dtype, device="cuda")
+    args = (dev(x), dev(a), dev(b), dev(index))
+    B.mhc_lora(*args, out, ws, scale=dev(scale), base=dev(base))
+    block_case.check(out, ref, terms, n=1, what="lora")
+    none = ((index < 0) | (index >= n)).cuda()
+    assert torch.equal(out[none], dev(base)[none] if based else torch.zeros_like(out[none]))
+    if based:  # in place
+        again = dev(base).clone()
+        B.mhc_lora(*args, again, ws, scale=dev(scale), base=again)
+        assert torch.equal(again, out)
+
+
+def test_lora_strides_and_neighbours():
+    T, H, N, r, n = 70, 136, 72, 16, 4
+    x, a, b, index, scale, base = (dev(t) for t in lora_inputs(T, H, N, r, n, BF16, "any"))
+    ws = torch.empty(B.mhc_lora_workspace_bytes(T, r), dtype=torch.uint8, device="cuda")
+    want = torch.empty(T, N, dtype=BF16, device="cuda")
+    B.mhc_lora(x, a, b, index, want, ws, scale=scale, base=base)
+    wide = torch.full((T, 4, H), float("nan"), dtype=BF16, device="cuda")
+    wide[:, 1] = x
+    holder = torch.full((T + 2, N + 16), 5.0, dtype=BF16, device="cuda")
+    inner = holder[1:T + 1, 8:N + 8]
+    inner.copy_(base)
+    B.mhc_lora(wide[:, 1], a, b, index, inner, ws, scale=scale, base=inner)
+    assert torch.equal(inner, want)
+    inner.fill_(5.0)
+    assert bool((holder == 5).all())
+    B.mhc_lora(x[:0], a, b, index[:0], want[:0], ws, scale=scale)
+
+
+def test_lora_keeps_tokens_and_adapters_apart():
+    # values of every size: fp16 sums past 65504, tiny rows, a NaN row, an infinite one, a broken adapter
+    T, H, N, r, n = 40, 256, 64, 16, 3
+    x, a, b, index, _, _ = lora_inputs(T, H, N, r, n, F16, "any")
+    index = index.clamp(0, n - 1)
+    x[3], x[4] = 60000.0, 2.0 ** -20
+    a[:] = a.abs()
+    b *= 2.0 ** -8
+    ref, terms = R.lora(x, a, b, index, None, None)
+    x[5, 7], x[6, 8] = float("nan"), float("inf")
+    index[7] = 2
+    a[2, 3, 4] = float("nan")
+    out = torch.empty(T, N, dtype=F16, device="cuda")
+    ws = torch.empty(B.mhc_lora_workspace_bytes(T, r), dtype=torch.uint8, device="cuda")
+    B.mhc_lora(dev(x), dev(a), dev(b), dev(index), out, ws)
+    fine = index != 2
+    fine[5] = fine[6] = fine[7] = False
+    block_case.check(out[fine.cuda()], ref[fine], terms[fine], n=1)
+    assert not bool(torch.isfinite(out[5]).any()) and not bool(torch.isfinite(out[6]).any())
+    assert bool(torch.isnan(out[(index == 2).cuda()]).all())
+
+
+def test_lora_results_do_not_depend_on_neighbours_order():
+    # tokens of the same adapter in another order in the batch give the same rows
+    T, H, N, r, n = 64, 512, 128, 32, 8
+    x, a, b, index, scale, base = (dev(t) for t in lora_inputs(T, H, N, r, n, BF16, "any"))
+    ws = torch.empty(B.mhc_lora_workspace_bytes(T, r), dtype=torch.uint8, device="cuda")
+    out, moved = torch.empty(T, N, dtype=BF16, device="cuda"), torch.empty(T, N, dtype=BF16, device="cuda")
+    B.mhc_lora(x, a, b, index, out, ws, scale=scale, base=base)
+    p = torch.randperm(T, generator=gen(2)).cuda()
+    B.mhc_lora(x[p], a, b, index[p], moved, ws, scale=scale, base=base[p])
+    assert torch.equal(moved, out[p])
