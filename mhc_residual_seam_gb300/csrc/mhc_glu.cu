@@ -1,6 +1,7 @@
 // mhc_glu: the gated projections of a feed-forward block in one kernel.
 
 #include "mhc_glu.cuh"
+#include "mhc_glu_few.cuh"
 #include "mhc_product.cuh"
 
 namespace mhc {
@@ -30,33 +31,38 @@ struct GluEpilogue {
       take16(g);
       take16(u);
       if (row >= T) continue;
+      float *a = reinterpret_cast<float*>(g), *b = reinterpret_cast<float*>(u);
+      const int64_t f = (int64_t)n * half + c;
+      const int pieces = (int)min((int64_t)2, (F - f) / 8);  // eight features each: F is a multiple of eight
+      if (pieces <= 0) continue;
+      if (add) {
 #pragma unroll
-      for (int p = 0; p < 16; p += 8) {  // eight features: F is a multiple of eight
-        const int64_t f = (int64_t)n * half + c + p;
-        if (f >= F) break;
-        Vec8 a, b;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          a.p[e] = make_float2(__uint_as_float(g[p + 2 * e]), __uint_as_float(g[p + 2 * e + 1]));
-          b.p[e] = make_float2(__uint_as_float(u[p + 2 * e]), __uint_as_float(u[p + 2 * e + 1]));
-        }
-        if (add) {
-          const Vec8 x = unpack(ld8(add + row * ld_add + f)), y = unpack(ld8(add + row * ld_add + F + f));
+        for (int p = 0; p < 2; ++p) {
+          if (p >= pieces) break;
+          const Vec8 x = unpack(ld8(add + row * ld_add + f + 8 * p)), y = unpack(ld8(add + row * ld_add + F + f + 8 * p));
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            a.p[e] = make_float2(a.p[e].x + x.p[e].x, a.p[e].y + x.p[e].y);
-            b.p[e] = make_float2(b.p[e].x + y.p[e].x, b.p[e].y + y.p[e].y);
+            a[8 * p + 2 * e] += x.p[e].x, a[8 * p + 2 * e + 1] += x.p[e].y;
+            b[8 * p + 2 * e] += y.p[e].x, b[8 * p + 2 * e + 1] += y.p[e].y;
           }
         }
-        if (gu) {
-          st8(gu + row * 2 * F + f, pack<E>(a));
-          st8(gu + row * 2 * F + F + f, pack<E>(b));
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          a.p[e] = make_float2(activate(a.p[e].x, act) * b.p[e].x, activate(a.p[e].y, act) * b.p[e].y);
-        st8(h + row * ld_h + f, pack<E>(a));
       }
+      if (gu) {
+        put16(gu + row * 2 * F + f, a, pieces);
+        put16(gu + row * 2 * F + F + f, b, pieces);
+      }
+      activate_product<16>(a, b, act);
+      put16(h + row * ld_h + f, a, pieces);
+    }
+  }
+  __device__ __forceinline__ static void put16(E* out, const float* v, int pieces) {
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      if (p >= pieces) break;
+      Vec8 o;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o.p[e] = make_float2(v[8 * p + 2 * e], v[8 * p + 2 * e + 1]);
+      st8(out + 8 * p, pack<E>(o));
     }
   }
 };
@@ -64,6 +70,10 @@ struct GluEpilogue {
 template <typename E>
 static cudaError_t glu_launch(const void* x, int64_t ld_x, const void* w, const void* add, int64_t ld_add, int act, int64_t T,
                               int H, int F, void* gu, void* h, int64_t ld_h, void* ws, cudaStream_t s) {
+#ifndef FEWT
+#define FEWT 128
+#endif
+  if (T <= FEWT) return glu_few_launch<E>(x, ld_x, w, add, ld_add, act, T, H, F, gu, h, ld_h, ws, s);
   using S = Tile<2, 256, false>;
   Work<1> p;
   p.status = static_cast<unsigned*>(ws);
@@ -75,7 +85,10 @@ static cudaError_t glu_launch(const void* x, int64_t ld_x, const void* w, const 
 
 }  // namespace mhc
 
-extern "C" size_t mhc_glu_workspace_bytes(int64_t T, int H, int F) { return T > 0 && H > 0 && F > 0 ? 256 : 0; }
+extern "C" size_t mhc_glu_workspace_bytes(int64_t T, int H, int F) {
+  using namespace mhc;
+  return T > 0 && H > 0 && F > 0 ? few_bytes(few_plan(T, H, F)) : 0;
+}
 
 extern "C" int mhc_glu(const void* x, int64_t ld_x, const void* w, const void* add, int64_t ld_add, int act, int64_t T, int H,
                        int F, mhc_dtype dtype, void* gu, void* h, int64_t ld_h, void* workspace, size_t ws_bytes, void* stream) {

@@ -10,31 +10,52 @@ __device__ __forceinline__ float logistic(float q) { return __fdividef(1.f, 1.f 
 
 constexpr float kGeluA = 1.5957691216057308f, kGeluB = 0.044715f;  // 2 sqrt(2 / pi); gelu(g) ~ g logistic(A (g + B g^3))
 
-__device__ __forceinline__ float activate(float g, int act) {
-  switch (act) {
-    case MHC_ACT_SILU: return g * logistic(g);
-    case MHC_ACT_GELU: return g * (0.5f * erfcf(g * -0.70710678f));
-    case MHC_ACT_GELU_TANH: return g * logistic(kGeluA * (g + kGeluB * g * g * g));
-    default: return g > 0.f || g != g ? g : 0.f;
-  }
+template <int ACT>
+__device__ __forceinline__ float activate(float g) {
+  if constexpr (ACT == MHC_ACT_SILU) return g * logistic(g);
+  if constexpr (ACT == MHC_ACT_GELU) return g * (0.5f * erfcf(g * -0.70710678f));
+  if constexpr (ACT == MHC_ACT_GELU_TANH) return g * logistic(kGeluA * (g + kGeluB * g * g * g));
+  return g > 0.f || g != g ? g : 0.f;
 }
 
 // The activation and its derivative.
-__device__ __forceinline__ float2 activate_grad(float g, int act) {
+template <int ACT>
+__device__ __forceinline__ float2 activate_grad(float g) {
+  if constexpr (ACT == MHC_ACT_SILU) {
+    const float s = logistic(g);
+    return make_float2(g * s, s + g * s * (1.f - s));
+  }
+  if constexpr (ACT == MHC_ACT_GELU) {
+    const float p = 0.5f * erfcf(g * -0.70710678f);
+    return make_float2(g * p, p + g * 0.3989422804f * __expf(-0.5f * g * g));
+  }
+  if constexpr (ACT == MHC_ACT_GELU_TANH) {
+    const float s = logistic(kGeluA * (g + kGeluB * g * g * g));
+    return make_float2(g * s, s + g * s * (1.f - s) * kGeluA * (1.f + 3.f * kGeluB * g * g));
+  }
+  return g > 0.f || g != g ? make_float2(g, 1.f) : make_float2(0.f, 0.f);
+}
+
+// g[i] = act(g[i]) * u[i].  The choice stands outside the loop, so the elements' chains of
+// exponential and reciprocal overlap.
+template <int N>
+__device__ __forceinline__ void activate_product(float* g, const float* u, int act) {
   switch (act) {
-    case MHC_ACT_SILU: {
-      const float s = logistic(g);
-      return make_float2(g * s, s + g * s * (1.f - s));
-    }
-    case MHC_ACT_GELU: {
-      const float p = 0.5f * erfcf(g * -0.70710678f);
-      return make_float2(g * p, p + g * 0.3989422804f * __expf(-0.5f * g * g));
-    }
-    case MHC_ACT_GELU_TANH: {
-      const float s = logistic(kGeluA * (g + kGeluB * g * g * g));
-      return make_float2(g * s, s + g * s * (1.f - s) * kGeluA * (1.f + 3.f * kGeluB * g * g));
-    }
-    default: return g > 0.f || g != g ? make_float2(g, 1.f) : make_float2(0.f, 0.f);
+    case MHC_ACT_SILU:
+#pragma unroll
+      for (int i = 0; i < N; ++i) g[i] = activate<MHC_ACT_SILU>(g[i]) * u[i];
+      break;
+    case MHC_ACT_GELU:
+#pragma unroll
+      for (int i = 0; i < N; ++i) g[i] = activate<MHC_ACT_GELU>(g[i]) * u[i];
+      break;
+    case MHC_ACT_GELU_TANH:
+#pragma unroll
+      for (int i = 0; i < N; ++i) g[i] = activate<MHC_ACT_GELU_TANH>(g[i]) * u[i];
+      break;
+    default:
+#pragma unroll
+      for (int i = 0; i < N; ++i) g[i] = activate<MHC_ACT_RELU>(g[i]) * u[i];
   }
 }
 

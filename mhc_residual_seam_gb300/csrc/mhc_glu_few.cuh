@@ -1,0 +1,308 @@
+// The gated projections of a few tokens: bound by reading the weights once.
+//
+// The weights are the product's rows (128 features of the gate and the same 128 of the
+// other projection: two accumulators) and the tokens its columns, so a token costs 16
+// bytes of shared memory a step, not a row of a 128-row tile.  The steps (128 features x
+// 64 columns of H, 32 KB of weights) of all tiles are cut into one equal run per SM: a
+// run that ends inside a tile leaves fp32 sums in the workspace, and the CTA that comes
+// last to a tile adds them up in the runs' order and finishes it.  No CTA waits for
+// another one, and the sums do not depend on who comes last.
+#pragma once
+
+#include "mhc_glu.cuh"
+#include "mhc_product.cuh"
+
+namespace mhc {
+
+constexpr int kFewTokens = 128;  // most tokens of this form
+constexpr int kFewRuns = 152;    // most runs
+
+struct FewPlan {
+  int tiles, kblocks, runs, cols;  // feature tiles, steps per tile, runs, columns of an accumulator (tokens, rounded up)
+};
+inline FewPlan few_plan(int64_t T, int H, int F) {
+  FewPlan p;
+  p.tiles = (F + kBM - 1) / kBM;
+  p.kblocks = (H + kBK - 1) / kBK;
+  const int64_t total = (int64_t)p.tiles * p.kblocks;
+  // at least four steps a run: shorter ones cost more in sums than they save
+  int64_t runs = (total + 3) / 4;
+  p.runs = (int)(runs < kFewRuns ? runs : kFewRuns);
+  const int64_t t = T < kFewTokens ? T : kFewTokens;
+  p.cols = (int)((t + 15) / 16 * 16);
+  return p;
+}
+// Workspace: status word, a counter per tile (the same place whatever the sizes, so that
+// calls of different sizes may share it), two parts per run.
+constexpr size_t kFewCounters = 256, kFewParts = kFewCounters + (size_t)((1 << 20) / kBM) * 4;
+inline size_t few_part_floats(const FewPlan& p) { return (size_t)2 * p.cols * kBM; }
+inline size_t few_bytes(const FewPlan& p) { return kFewParts + (size_t)p.runs * 2 * few_part_floats(p) * 4; }
+
+template <typename E>
+struct FewArgs {
+  CUtensorMap w, x;
+  const E* add;
+  E *gu, *h;
+  int64_t F, ld_add, ld_h;
+  unsigned* status;
+  unsigned* counters;
+  float* parts;
+  int T, act, tiles, kblocks, cols, stages;
+};
+
+// Barrier 1 over the four epilogue warps; whether `x` holds in all of them.
+__device__ __forceinline__ bool all_of_128(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred q, 1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)x)
+      : "memory");
+  return r != 0;
+}
+
+template <typename E>
+__global__ void __launch_bounds__(256, 1) glu_few_kernel(const __grid_constant__ FewArgs<E> p) {
+  extern __shared__ char raw[];
+  const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+  char* aligned = raw + (base - smem_u32(raw));
+  const int stage_bytes = 2 * kBM * 128 + p.cols * 128, stages = p.stages;
+  uint64_t* full = reinterpret_cast<uint64_t*>(aligned + (size_t)stages * stage_bytes);
+  uint64_t *empty = full + stages, *tfull = empty + stages, *tempty = tfull + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
+  volatile uint32_t* last = tmem_slot + 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int stride = (p.cols + 31) / 32 * 32;  // accumulators start at multiples of 32 columns
+  const uint32_t tcols = stride <= 32 ? 128 : stride <= 64 ? 256 : 512;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(full + s, 1);
+      mbar_init(empty + s, 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(tfull + b, 1);
+      mbar_init(tempty + b, 4);
+    }
+    mbar_fence_init();
+  }
+  if (warp == 2) pair_tmem_alloc<1>(tmem_slot, tcols);
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_launch();
+
+  const int64_t total = (int64_t)p.tiles * p.kblocks, runs = gridDim.x;
+  const int64_t begin = blockIdx.x * total / runs, end = (blockIdx.x + 1) * total / runs;
+  bool ok = true;
+
+  if (warp == 0) {  // ------------------------------------------- producer
+    if (lane == 0) {
+      pdl_wait();
+      int st = 0, used = 0, tile = (int)(begin / p.kblocks), k = (int)(begin - (int64_t)tile * p.kblocks);
+      uint32_t ph = 1;
+      for (int64_t i = begin; i < end; ++i) {
+        ok = mbar_wait(empty + st, ph, kProductLimitNs);
+        if (!ok) break;
+        mbar_arrive_expect_tx(full + st, stage_bytes);
+        const uint32_t at = base + st * stage_bytes, bar = smem_u32(full + st);
+        pair_load<1>(at, &p.w, bar, k * kBK, tile * kBM);
+        pair_load<1>(at + kBM * 128, &p.w, bar, k * kBK, (int)p.F + tile * kBM);
+        pair_load<1>(at + 2 * kBM * 128, &p.x, bar, k * kBK, 0);
+        if (used < stages) ++used;
+        if (++st == stages) st = 0, ph ^= 1;
+        if (++k == p.kblocks) k = 0, ++tile;
+      }
+      for (; used > 0 && ok; --used) {  // the MMAs' last arrivals come before the CTA ends
+        st = st == 0 ? (ph ^= 1, stages - 1) : st - 1;
+        ok = mbar_wait(empty + st, ph ^ 1, kProductLimitNs);
+      }
+    }
+  } else if (warp == 1) {  // ------------------------------------------ MMA
+    if (lane == 0) {
+      const uint32_t idesc = product_idesc<E>(kBM, p.cols, false, false);
+      int st = 0, b = 0, k = (int)(begin % p.kblocks);
+      uint32_t ph = 0, pb = 1;
+      for (int64_t i = begin; i < end && ok;) {
+        const int n = (int)min((int64_t)(p.kblocks - k), end - i);  // steps of this run in the tile
+        ok = mbar_wait(tempty + b, pb, kProductLimitNs);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t dg = tmem + b * 2 * stride, du = dg + stride;
+        for (int j = 0; j < n; ++j) {
+          ok = mbar_wait(full + st, ph, kProductLimitNs);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t at = base + st * stage_bytes;
+          const uint64_t g = tile_desc(at, false), u = tile_desc(at + kBM * 128, false), x = tile_desc(at + 2 * kBM * 128, false);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            pair_mma<1>(dg, g + 2 * q, x + 2 * q, idesc, j | q);
+            pair_mma<1>(du, u + 2 * q, x + 2 * q, idesc, j | q);
+          }
+          pair_commit<1>(empty + st);
+          if (++st == stages) st = 0, ph ^= 1;
+        }
+        if (ok) pair_commit<1>(tfull + b);
+        if ((b ^= 1) == 0) pb ^= 1;
+        i += n;
+        k = 0;
+      }
+    }
+  } else if (warp >= 4) {  // ------------------------------------ epilogue
+    pdl_wait();
+    const int feature = (warp & 3) * 32 + lane;
+    const size_t part = (size_t)2 * p.cols * kBM;
+    int b = 0, tile = (int)(begin / p.kblocks), k = (int)(begin - (int64_t)tile * p.kblocks);
+    uint32_t pb = 0;
+    // 16 tokens of this lane's feature (what is added is fetched for all of them before it is used)
+    auto finish = [&](float* g, float* u, int c) {
+      const int64_t f = (int64_t)tile * kBM + feature;
+      if (f >= p.F) return;
+      if (p.add) {
+        E a[16], v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int64_t t = min(c + i, p.T - 1);
+          a[i] = p.add[t * p.ld_add + f];
+          v[i] = p.add[t * p.ld_add + p.F + f];
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) g[i] += (float)a[i], u[i] += (float)v[i];
+      }
+      const int n = min(16, p.T - c);
+      if (p.gu) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          E* o = p.gu + (int64_t)(c + i) * 2 * p.F + f;
+          if (i < n) o[0] = (E)g[i], o[p.F] = (E)u[i];
+        }
+      }
+      activate_product<16>(g, u, p.act);
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (i < n) p.h[(c + i) * p.ld_h + f] = (E)g[i];
+    };
+    // a part lies as four columns of a feature together, features adjacent: 16 bytes a lane
+    auto read16 = [&](float4* v, const float* part_, int c) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = __ldcg(reinterpret_cast<const float4*>(part_ + (size_t)(c + 4 * e) * kBM));
+    };
+    auto add16 = [&](float* o, const float4* v) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[4 * e] += v[e].x, o[4 * e + 1] += v[e].y, o[4 * e + 2] += v[e].z, o[4 * e + 3] += v[e].w;
+    };
+    for (int64_t i = begin; i < end && ok; ++tile) {
+      const int n = (int)min((int64_t)(p.kblocks - k), end - i);
+      const bool whole = n == p.kblocks;
+      ok = all_of_128(mbar_wait(tfull + b, pb, kProductLimitNs));  // the four warps go on, or give up, together
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t d = tmem + b * 2 * stride + ((uint32_t)(warp & 3) << 21);
+      float* mine = p.parts + ((size_t)blockIdx.x * 2 + (i != begin)) * part + feature * 4;
+      for (int c = 0; c < p.cols; c += 16) {
+        uint32_t g[16], u[16];
+        __syncwarp();
+        issue16(d + c, g);
+        issue16(d + stride + c, u);
+        take16(g);
+        take16(u);
+        if (whole) {
+          finish(reinterpret_cast<float*>(g), reinterpret_cast<float*>(u), c);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) {
+            __stcg(reinterpret_cast<uint4*>(mine + (size_t)(c + e) * kBM), make_uint4(g[e], g[e + 1], g[e + 2], g[e + 3]));
+            __stcg(reinterpret_cast<uint4*>(mine + (size_t)(p.cols + c + e) * kBM), make_uint4(u[e], u[e + 1], u[e + 2], u[e + 3]));
+          }
+        }
+      }
+      tc_wait_ld();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(tempty + b);
+      if ((b ^= 1) == 0) pb ^= 1;
+      if (!whole) {
+        // the runs that share this tile: those of its first and of its last step, and all between
+        const int64_t u0 = (int64_t)tile * p.kblocks, u1 = u0 + p.kblocks - 1;
+        const int r0 = (int)(((u0 + 1) * runs - 1) / total), r1 = (int)(((u1 + 1) * runs - 1) / total);
+        __threadfence();
+        named_bar_sync(1, 128);
+        if (threadIdx.x == 128) *last = atomicAdd(p.counters + tile, 1u) == (unsigned)(r1 - r0);
+        named_bar_sync(1, 128);
+        if (*last) {
+          __threadfence();
+          auto part_of = [&](int r) {
+            const bool first = r * total / runs / p.kblocks == tile;  // the tile is the first of run r
+            return p.parts + ((size_t)r * 2 + !first) * part + feature * 4;
+          };
+          const float *p0 = part_of(r0), *p1 = part_of(r0 + 1);  // (a tile that is not whole has two runs at least)
+          for (int c = 0; c < p.cols; c += 16) {
+            float4 g0[4], u0[4], g1[4], u1[4];
+            read16(g0, p0, c);
+            read16(u0, p0, p.cols + c);
+            read16(g1, p1, c);
+            read16(u1, p1, p.cols + c);
+            float g[16], u[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) g[e] = u[e] = 0.f;
+            add16(g, g0);
+            add16(u, u0);
+            add16(g, g1);
+            add16(u, u1);
+            for (int r = r0 + 2; r <= r1; ++r) {
+              const float* pr = part_of(r);
+              read16(g0, pr, c);
+              read16(u0, pr, p.cols + c);
+              add16(g, g0);
+              add16(u, u0);
+            }
+            finish(g, u, c);
+          }
+          if (threadIdx.x == 128) p.counters[tile] = 0;
+        }
+        named_bar_sync(1, 128);  // (*last is read before the next tile's is written)
+      }
+      i += n;
+      k = 0;
+    }
+  }
+  if (!ok) {  // gave up: report, and let copies and MMAs in flight end before anything is freed
+    atomicOr(p.status, 2u);
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 20000000ull) __nanosleep(1000);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 2) pair_tmem_dealloc<1>(tmem, tcols);
+}
+
+template <typename E>
+inline cudaError_t glu_few_launch(const void* x, int64_t ld_x, const void* w, const void* add, int64_t ld_add, int act, int64_t T,
+                                  int H, int F, void* gu, void* h, int64_t ld_h, void* ws, cudaStream_t s) {
+  const FewPlan plan = few_plan(T, H, F);
+  FewArgs<E> p;
+  if (!encode_2d<E>(&p.w, w, 2 * (int64_t)F, H, H, kBM) || !encode_2d<E>(&p.x, x, T, H, ld_x, plan.cols)) return cudaErrorInvalidValue;
+  p.add = static_cast<const E*>(add);
+  p.gu = static_cast<E*>(gu);
+  p.h = static_cast<E*>(h);
+  p.F = F, p.ld_add = ld_add, p.ld_h = ld_h, p.T = (int)T, p.act = act;
+  p.tiles = plan.tiles, p.kblocks = plan.kblocks, p.cols = plan.cols;
+  p.status = static_cast<unsigned*>(ws);
+  p.counters = reinterpret_cast<unsigned*>(static_cast<char*>(ws) + kFewCounters);
+  p.parts = reinterpret_cast<float*>(static_cast<char*>(ws) + kFewParts);
+  const int stage = 2 * kBM * 128 + plan.cols * 128;
+  p.stages = 200 * 1024 / stage;
+  const size_t smem = (size_t)p.stages * stage + 1024 + 256;
+  static SmemGrant grant;
+  const cudaError_t e = allow_smem(grant, (const void*)glu_few_kernel<E>, 208 * 1024);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(glu_few_kernel<E>, dim3((unsigned)plan.runs), dim3(256), smem, s, p);
+}
+
+}  // namespace mhc

@@ -7,9 +7,9 @@ namespace mhc {
 
 // dg = dh u act'(g), du = dh act(g), from the kept pre-activations, into [T, 2F].  Bound
 // by HBM: three rows of F read, two written.  Work item = (token, 8 features).
-template <typename E>
-__global__ void __launch_bounds__(256) glu_act_grad_kernel(const E* __restrict__ dh, const E* __restrict__ gu, int act,
-                                                           int64_t n, int segs, E* __restrict__ dgu) {
+template <typename E, int ACT>
+__global__ void __launch_bounds__(256) glu_act_grad_kernel(const E* __restrict__ dh, const E* __restrict__ gu, int64_t n,
+                                                           int segs, E* __restrict__ dgu) {
   const int64_t stride = (int64_t)gridDim.x * blockDim.x;
   const int64_t F = (int64_t)segs * 8;
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += stride) {
@@ -19,7 +19,7 @@ __global__ void __launch_bounds__(256) glu_act_grad_kernel(const E* __restrict__
     Vec8 a, b;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float2 x = activate_grad(g.p[e].x, act), y = activate_grad(g.p[e].y, act);
+      const float2 x = activate_grad<ACT>(g.p[e].x), y = activate_grad<ACT>(g.p[e].y);
       a.p[e] = make_float2(d.p[e].x * u.p[e].x * x.y, d.p[e].y * u.p[e].y * y.y);
       b.p[e] = make_float2(d.p[e].x * x.x, d.p[e].y * y.x);
     }
@@ -80,8 +80,11 @@ static cudaError_t glu_grad_launch(const void* dh, const void* gu, const void* x
   const int64_t n = T * segs;
   int64_t blocks = (n + 255) / 256;
   if (blocks > 0x7fffffff) blocks = 0x7fffffff;
-  glu_act_grad_kernel<E><<<(unsigned)blocks, 256, 0, s>>>(static_cast<const E*>(dh), static_cast<const E*>(gu), act, n, segs,
-                                                          static_cast<E*>(dgu));
+  auto k = act == MHC_ACT_SILU   ? glu_act_grad_kernel<E, MHC_ACT_SILU>
+           : act == MHC_ACT_GELU ? glu_act_grad_kernel<E, MHC_ACT_GELU>
+           : act == MHC_ACT_RELU ? glu_act_grad_kernel<E, MHC_ACT_RELU>
+                                 : glu_act_grad_kernel<E, MHC_ACT_GELU_TANH>;
+  k<<<(unsigned)blocks, 256, 0, s>>>(static_cast<const E*>(dh), static_cast<const E*>(gu), n, segs, static_cast<E*>(dgu));
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || (!dx && !dw)) return e;
   using S = Tile<2, 256, true>;

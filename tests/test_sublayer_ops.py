@@ -354,3 +354,29 @@ def test_lora_results_do_not_depend_on_neighbours_order():
     p = torch.randperm(T, generator=gen(2)).cuda()
     B.mhc_lora(x[p], a, b, index[p], moved, ws, scale=scale, base=base[p])
     assert torch.equal(moved, out[p])
+
+
+def test_glu_calls_of_other_sizes_share_a_workspace():
+    sizes = [(5, 512, 1000), (128, 1024, 200), (1, 72, 3000), (64, 4096, 136), (200, 64, 72), (3, 2048, 640)]
+    ws = workspace(max(B.mhc_glu_workspace_bytes(*s) for s in sizes))
+    for again in range(2):
+        for T, H, F in sizes:
+            x, w, _ = glu_inputs(T, H, F, BF16, "none")
+            ref, terms = R.glu(x, w, None, "silu")
+            h = torch.empty(T, F, dtype=BF16, device="cuda")
+            B.mhc_glu(dev(x), dev(w), h, ws)
+            block_case.check(h, ref["h"], terms["h"], n=1)
+    B.mhc_check_status(ws)
+
+
+def test_glu_of_a_few_tokens_repeats_bit_for_bit():
+    # the sums of runs that share a tile do not depend on which of them ends last
+    T, H, F = 9, 5120, 2000
+    x, w, _ = (dev(t) if t is not None else None for t in glu_inputs(T, H, F, BF16, "none"))
+    ws = workspace(B.mhc_glu_workspace_bytes(T, H, F))
+    want = torch.empty(T, F, dtype=BF16, device="cuda")
+    B.mhc_glu(x, w, want, ws)
+    for _ in range(50):
+        h = torch.empty_like(want)
+        B.mhc_glu(x, w, h, ws)
+        assert torch.equal(h, want)
