@@ -50,22 +50,28 @@ struct FewArgs {
   int T, act, tiles, kblocks, cols, stages;
 };
 
-// Barrier 1 over the four epilogue warps; whether `x` holds in all of them.
-__device__ __forceinline__ bool all_of_128(bool x) {
+constexpr int kFewEpilogue = 256;  // epilogue threads: two warps per 32 features
+constexpr int kFewAhead = 8;       // steps whose weights are fetched into L2 ahead of the kernel before
+__device__ __forceinline__ void prefetch_tile(const CUtensorMap* map, int c0, int c1) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1)
+               : "memory");
+}
+// Barrier 1 over the epilogue warps; whether `x` holds in all of them.
+__device__ __forceinline__ bool all_of_epilogue(bool x) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.and.pred q, 1, 128, p;\n\t"
+      "barrier.cta.red.and.pred q, 1, %2, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"((uint32_t)x)
+      : "r"((uint32_t)x), "n"(kFewEpilogue)
       : "memory");
   return r != 0;
 }
 
 template <typename E>
-__global__ void __launch_bounds__(256, 1) glu_few_kernel(const __grid_constant__ FewArgs<E> p) {
+__global__ void __launch_bounds__(128 + kFewEpilogue, 1) glu_few_kernel(const __grid_constant__ FewArgs<E> p) {
   extern __shared__ char raw[];
   const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
   char* aligned = raw + (base - smem_u32(raw));
@@ -85,7 +91,7 @@ __global__ void __launch_bounds__(256, 1) glu_few_kernel(const __grid_constant__
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(tfull + b, 1);
-      mbar_init(tempty + b, 4);
+      mbar_init(tempty + b, kFewEpilogue / 32);
     }
     mbar_fence_init();
   }
@@ -93,7 +99,7 @@ __global__ void __launch_bounds__(256, 1) glu_few_kernel(const __grid_constant__
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  pdl_launch();
+  pdl_launch();  // the next kernel's CTAs may take the place of those that end early
 
   const int64_t total = (int64_t)p.tiles * p.kblocks, runs = gridDim.x;
   const int64_t begin = blockIdx.x * total / runs, end = (blockIdx.x + 1) * total / runs;
@@ -101,9 +107,18 @@ __global__ void __launch_bounds__(256, 1) glu_few_kernel(const __grid_constant__
 
   if (warp == 0) {  // ------------------------------------------- producer
     if (lane == 0) {
-      pdl_wait();
       int st = 0, used = 0, tile = (int)(begin / p.kblocks), k = (int)(begin - (int64_t)tile * p.kblocks);
       uint32_t ph = 1;
+      prefetch_tmap(&p.w);
+      prefetch_tmap(&p.x);
+      // While the kernel before this one ends, the first weights come as far as L2 (which also sees
+      // what that kernel may still write there).
+      for (int i = 0, t = tile, kk = k; i < kFewAhead && begin + i < end; ++i) {
+        prefetch_tile(&p.w, kk * kBK, t * kBM);
+        prefetch_tile(&p.w, kk * kBK, (int)p.F + t * kBM);
+        if (++kk == p.kblocks) kk = 0, ++t;
+      }
+      pdl_wait();
       for (int64_t i = begin; i < end; ++i) {
         ok = mbar_wait(empty + st, ph, kProductLimitNs);
         if (!ok) break;
@@ -155,6 +170,7 @@ __global__ void __launch_bounds__(256, 1) glu_few_kernel(const __grid_constant__
   } else if (warp >= 4) {  // ------------------------------------ epilogue
     pdl_wait();
     const int feature = (warp & 3) * 32 + lane;
+    const int group = (warp - 4) >> 2;  // takes every other 16 tokens
     const size_t part = (size_t)2 * p.cols * kBM;
     int b = 0, tile = (int)(begin / p.kblocks), k = (int)(begin - (int64_t)tile * p.kblocks);
     uint32_t pb = 0;
@@ -198,12 +214,12 @@ __global__ void __launch_bounds__(256, 1) glu_few_kernel(const __grid_constant__
     for (int64_t i = begin; i < end && ok; ++tile) {
       const int n = (int)min((int64_t)(p.kblocks - k), end - i);
       const bool whole = n == p.kblocks;
-      ok = all_of_128(mbar_wait(tfull + b, pb, kProductLimitNs));  // the four warps go on, or give up, together
+      ok = all_of_epilogue(mbar_wait(tfull + b, pb, kProductLimitNs));  // the warps go on, or give up, together
       if (!ok) break;
       tc_fence_after();
       const uint32_t d = tmem + b * 2 * stride + ((uint32_t)(warp & 3) << 21);
       float* mine = p.parts + ((size_t)blockIdx.x * 2 + (i != begin)) * part + feature * 4;
-      for (int c = 0; c < p.cols; c += 16) {
+      for (int c = group * 16; c < p.cols; c += kFewEpilogue / 8) {
         uint32_t g[16], u[16];
         __syncwarp();
         issue16(d + c, g);
@@ -230,9 +246,9 @@ __global__ void __launch_bounds__(256, 1) glu_few_kernel(const __grid_constant__
         const int64_t u0 = (int64_t)tile * p.kblocks, u1 = u0 + p.kblocks - 1;
         const int r0 = (int)(((u0 + 1) * runs - 1) / total), r1 = (int)(((u1 + 1) * runs - 1) / total);
         __threadfence();
-        named_bar_sync(1, 128);
+        named_bar_sync(1, kFewEpilogue);
         if (threadIdx.x == 128) *last = atomicAdd(p.counters + tile, 1u) == (unsigned)(r1 - r0);
-        named_bar_sync(1, 128);
+        named_bar_sync(1, kFewEpilogue);
         if (*last) {
           __threadfence();
           auto part_of = [&](int r) {
@@ -240,31 +256,31 @@ __global__ void __launch_bounds__(256, 1) glu_few_kernel(const __grid_constant__
             return p.parts + ((size_t)r * 2 + !first) * part + feature * 4;
           };
           const float *p0 = part_of(r0), *p1 = part_of(r0 + 1);  // (a tile that is not whole has two runs at least)
-          for (int c = 0; c < p.cols; c += 16) {
-            float4 g0[4], u0[4], g1[4], u1[4];
-            read16(g0, p0, c);
-            read16(u0, p0, p.cols + c);
-            read16(g1, p1, c);
-            read16(u1, p1, p.cols + c);
+          for (int c = group * 16; c < p.cols; c += kFewEpilogue / 8) {
+            float4 v[16];
+            read16(v, p0, c);
+            read16(v + 4, p0, p.cols + c);
+            read16(v + 8, p1, c);
+            read16(v + 12, p1, p.cols + c);
             float g[16], u[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) g[e] = u[e] = 0.f;
-            add16(g, g0);
-            add16(u, u0);
-            add16(g, g1);
-            add16(u, u1);
+            add16(g, v);
+            add16(u, v + 4);
+            add16(g, v + 8);
+            add16(u, v + 12);
             for (int r = r0 + 2; r <= r1; ++r) {
               const float* pr = part_of(r);
-              read16(g0, pr, c);
-              read16(u0, pr, p.cols + c);
-              add16(g, g0);
-              add16(u, u0);
+              read16(v, pr, c);
+              read16(v + 4, pr, p.cols + c);
+              add16(g, v);
+              add16(u, v + 4);
             }
             finish(g, u, c);
           }
           if (threadIdx.x == 128) p.counters[tile] = 0;
         }
-        named_bar_sync(1, 128);  // (*last is read before the next tile's is written)
+        named_bar_sync(1, kFewEpilogue);  // (*last is read before the next tile's is written)
       }
       i += n;
       k = 0;
@@ -302,7 +318,7 @@ inline cudaError_t glu_few_launch(const void* x, int64_t ld_x, const void* w, co
   static SmemGrant grant;
   const cudaError_t e = allow_smem(grant, (const void*)glu_few_kernel<E>, 208 * 1024);
   if (e != cudaSuccess) return e;
-  return launch_pdl(glu_few_kernel<E>, dim3((unsigned)plan.runs), dim3(256), smem, s, p);
+  return launch_pdl(glu_few_kernel<E>, dim3((unsigned)plan.runs), dim3(128 + kFewEpilogue), smem, s, p);
 }
 
 }  // namespace mhc

@@ -50,10 +50,10 @@ struct GradEpilogue {
     }
     st8(out, pack<O>(a));
   }
-  __device__ __forceinline__ void store(uint32_t tmem, int64_t row, int n, int which) const {
+  __device__ __forceinline__ void store(uint32_t tmem, int64_t row, int n, int which, int part) const {
     const bool is_w = (which != 0) != swapped;
 #pragma unroll 1
-    for (int c = 0; c < BN; c += 16) {
+    for (int c = part * 16; c < BN; c += 32) {
       uint32_t v[16];
       __syncwarp();
       issue16(tmem + c, v);
@@ -87,7 +87,11 @@ static cudaError_t glu_grad_launch(const void* dh, const void* gu, const void* x
   k<<<(unsigned)blocks, 256, 0, s>>>(static_cast<const E*>(dh), static_cast<const E*>(gu), n, segs, static_cast<E*>(dgu));
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || (!dx && !dw)) return e;
-  using S = Tile<2, 256, true>;
+#ifndef FCG
+#define FCG 2
+#define FBN 256
+#endif
+  using S = Tile<FCG, FBN, true>;
   const int64_t cols = (H + S::BN - 1) / S::BN, F2 = 2 * (int64_t)F;
   GradEpilogue<E, S::BN> epi = {static_cast<E*>(dx), dw, T, F2, H, dw32, accumulate, false};
   // dx = dgu w: the reduction runs over w's rows.  dw = dgu^T x: over the tokens

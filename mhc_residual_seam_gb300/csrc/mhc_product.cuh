@@ -4,7 +4,7 @@
 //
 // One persistent CTA (or pair of CTAs) per SM: a producer thread fetches 64-deep
 // tiles of A and B by TMA into a ring of stages, a second thread issues
-// tcgen05.mma on them, four warps turn finished accumulators into outputs while
+// tcgen05.mma on them, eight warps turn finished accumulators into outputs while
 // the next tile's products run (two accumulators).  A pair works on one tile of
 // 256 rows: each CTA holds its 128 rows of A and half of B, so that an SM fetches
 // 32 KB a step where a CTA by itself fetches 48.
@@ -31,6 +31,7 @@ bool encode(CUtensorMap* m, CUtensorMapDataType dt, int rank, const void* base, 
             const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle sw);
 
 constexpr int kBM = 128, kBK = 64;  // rows of A per CTA, depth of a stage
+constexpr int kProductThreads = 384;  // producer, MMA, allocation, an idle warp; eight epilogue warps
 constexpr uint64_t kProductLimitNs = 2000000000ull;
 
 // ------------------------------------------------------------ PTX, pairs --
@@ -154,7 +155,7 @@ struct Tile {
   static constexpr int kStages = (200 * 1024) / kStage < 8 ? (200 * 1024) / kStage : 8;
   static constexpr int kCols = 2 * BN <= 256 ? 256 : 512;  // two accumulators
   static constexpr size_t kSmem = (size_t)kStages * kStage + 1024 + 256;
-  static constexpr int kBoxB = BMN ? 64 : (kRowsB > 128 ? kRowsB / 2 : kRowsB);  // rows of a TMA box of B
+  static constexpr int kBoxB = BMN ? 64 : BN / 2;  // rows of a TMA box of B: a half of the columns may lie elsewhere than the other
 };
 
 // Tile number -> (m, n): eight rows of tiles at a time, so that the tiles in flight
@@ -168,9 +169,9 @@ __device__ __forceinline__ void tile_place(int t, int num_m, int num_n, int& m, 
 }
 
 // Epi: `row_b(n_tile, j)` is the row of B for column j of the tile; `store(tmem, row,
-// n_tile, product)` makes a lane's row of outputs.
+// n_tile, product, part)` makes a lane's row of outputs, every other 16 columns (part 0 or 1).
 template <typename E, typename S, int NP, typename Epi>
-__global__ void __launch_bounds__(256, 1)
+__global__ void __launch_bounds__(kProductThreads, 1)
     product_kernel(const __grid_constant__ Work<NP> w, const __grid_constant__ Epi epi) {
   constexpr int CG = S::CG, kStages = S::kStages;
   extern __shared__ char raw[];
@@ -189,7 +190,7 @@ __global__ void __launch_bounds__(256, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(tfull + b, 1);
-      mbar_init(tempty + b, 4 * CG);
+      mbar_init(tempty + b, 8 * CG);
     }
     mbar_fence_init();
   }
@@ -282,7 +283,7 @@ __global__ void __launch_bounds__(256, 1)
       int m, n;
       tile_place(which ? t - w.tiles[0] : t, w.p[which].num_m, w.p[which].num_n, m, n);
       epi.store(tmem + b * S::BN + ((uint32_t)(warp & 3) << 21), ((int64_t)m * CG + rank) * kBM + (warp & 3) * 32 + lane, n,
-                which);
+                which, (warp - 4) >> 2);
       tc_wait_ld();
       tc_fence_before();
       __syncwarp();
@@ -346,7 +347,7 @@ inline cudaError_t product_launch(Work<NP>& w, const Epi& epi, cudaStream_t s) {
   const int64_t groups = tiles < sms / S::CG ? tiles : sms / S::CG;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(groups * S::CG));
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(kProductThreads);
   cfg.dynamicSmemBytes = S::kSmem;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
