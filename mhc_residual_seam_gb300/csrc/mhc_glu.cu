@@ -20,18 +20,14 @@ struct GluEpilogue {
     constexpr int half = BN / 2;
     return n * half + (j < half ? j : (int)F + j - half);
   }
-  __device__ __forceinline__ void store(uint32_t tmem, int64_t row, int n, int, int part) const {
+  template <typename Source>
+  __device__ __forceinline__ void store(const Source& from, int64_t row, int n, int, int part) const {
     constexpr int half = BN / 2;
 #pragma unroll 1
     for (int c = part * 16; c < half; c += 32) {
-      uint32_t g[16], u[16];
-      __syncwarp();
-      issue16(tmem + c, g);
-      issue16(tmem + half + c, u);
-      take16(g);
-      take16(u);
+      float a[16], b[16];
+      from.get2(c, a, half + c, b);
       if (row >= T) continue;
-      float *a = reinterpret_cast<float*>(g), *b = reinterpret_cast<float*>(u);
       const int64_t f = (int64_t)n * half + c;
       const int pieces = (int)min((int64_t)2, (F - f) / 8);  // eight features each: F is a multiple of eight
       if (pieces <= 0) continue;
@@ -71,38 +67,33 @@ template <typename E, typename S>
 static cudaError_t glu_tiles(const void* x, int64_t ld_x, const void* w, const void* add, int64_t ld_add, int act, int64_t T,
                              int H, int F, void* gu, void* h, int64_t ld_h, void* ws, cudaStream_t s) {
   Work<1> p;
-  p.status = static_cast<unsigned*>(ws);
   if (!problem<E, S>(&p.p[0], T, (F + S::BN / 2 - 1) / (S::BN / 2), H, x, false, ld_x, w, 2 * (int64_t)F, H))
     return cudaErrorInvalidValue;
   const GluEpilogue<E, S::BN> epi = {static_cast<const E*>(add), static_cast<E*>(gu), static_cast<E*>(h), T, F, ld_add, ld_h, act};
-  return product_launch<E, S, 1>(p, epi, s);
+  return product_launch<E, S, 1>(p, ws, epi, s);
 }
 
 template <typename E>
 static cudaError_t glu_launch(const void* x, int64_t ld_x, const void* w, const void* add, int64_t ld_add, int act, int64_t T,
                               int H, int F, void* gu, void* h, int64_t ld_h, void* ws, cudaStream_t s) {
   if (T <= kFewTokens) return glu_few_launch<E>(x, ld_x, w, add, ld_add, act, T, H, F, gu, h, ld_h, ws, s);
-  // Rounds of tiles over the SMs times a tile's cost: T = 8192, H = 5120, F = 10240 takes 868 us in
-  // tiles of 256 x 256 (pairs of CTAs), 966 in 256 x 192, 1278 in 128 x 128 (a CTA each); T = 256 63, 54
-  // and 64; T = 300, H = 512, F = 1368 12.5, 10.7 and 8.0.
-  auto cost = [&](int rows, int columns, int groups, int each) {
-    const int64_t tiles = ((T + rows - 1) / rows) * ((F + columns / 2 - 1) / (columns / 2));
-    return (tiles + groups - 1) / groups * each;
-  };
-  const int64_t wide = cost(256, 256, 76, 100), middle = cost(256, 192, 76, 82), small = cost(128, 128, 152, 74);
-#ifdef FCG
-  return glu_tiles<E, Tile<FCG, FBN, false>>(x, ld_x, w, add, ld_add, act, T, H, F, gu, h, ld_h, ws, s);
-#endif
-  if (wide <= middle && wide <= small) return glu_tiles<E, Tile<2, 256, false>>(x, ld_x, w, add, ld_add, act, T, H, F, gu, h, ld_h, ws, s);
-  if (middle <= small) return glu_tiles<E, Tile<2, 192, false>>(x, ld_x, w, add, ld_add, act, T, H, F, gu, h, ld_h, ws, s);
-  return glu_tiles<E, Tile<1, 128, false>>(x, ld_x, w, add, ld_add, act, T, H, F, gu, h, ld_h, ws, s);
+  const int64_t kb = (H + kBK - 1) / kBK;
+  if (product_small(
+          [&](int, int rows, int columns, int64_t* n, int64_t* k) {
+            *n = ((T + rows - 1) / rows) * ((F + columns / 2 - 1) / (columns / 2)), *k = kb;
+          },
+          1))
+    return glu_tiles<E, Tile<1, 128, false>>(x, ld_x, w, add, ld_add, act, T, H, F, gu, h, ld_h, ws, s);
+  return glu_tiles<E, Tile<2, 256, false>>(x, ld_x, w, add, ld_add, act, T, H, F, gu, h, ld_h, ws, s);
 }
 
 }  // namespace mhc
 
 extern "C" size_t mhc_glu_workspace_bytes(int64_t T, int H, int F) {
   using namespace mhc;
-  return T > 0 && H > 0 && F > 0 ? few_bytes(few_plan(T, H, F)) : 0;
+  if (T <= 0 || H <= 0 || F <= 0) return 0;
+  const size_t few = few_bytes(few_plan(T, H, F));
+  return few > kProductBytes ? few : kProductBytes;
 }
 
 extern "C" int mhc_glu(const void* x, int64_t ld_x, const void* w, const void* add, int64_t ld_add, int act, int64_t T, int H,

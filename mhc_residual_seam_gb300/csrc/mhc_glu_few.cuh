@@ -34,7 +34,8 @@ inline FewPlan few_plan(int64_t T, int H, int F) {
 }
 // Workspace: status word, a counter per tile (the same place whatever the sizes, so that
 // calls of different sizes may share it), two parts per run.
-constexpr size_t kFewCounters = 256, kFewParts = kFewCounters + (size_t)((1 << 20) / kBM) * 4;
+constexpr size_t kFewCounters = kProductCounters, kFewParts = kProductParts;
+static_assert(kFewParts - kFewCounters >= (size_t)((1 << 20) / kBM) * 4, "a counter per tile of the largest F");
 inline size_t few_part_floats(const FewPlan& p) { return (size_t)2 * p.cols * kBM; }
 inline size_t few_bytes(const FewPlan& p) { return kFewParts + (size_t)p.runs * 2 * few_part_floats(p) * 4; }
 
@@ -56,20 +57,6 @@ __device__ __forceinline__ void prefetch_tile(const CUtensorMap* map, int c0, in
   asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1)
                : "memory");
 }
-// Barrier 1 over the epilogue warps; whether `x` holds in all of them.
-__device__ __forceinline__ bool all_of_epilogue(bool x) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.and.pred q, 1, %2, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"((uint32_t)x), "n"(kFewEpilogue)
-      : "memory");
-  return r != 0;
-}
-
 template <typename E>
 __global__ void __launch_bounds__(128 + kFewEpilogue, 1) glu_few_kernel(const __grid_constant__ FewArgs<E> p) {
   extern __shared__ char raw[];
@@ -214,7 +201,7 @@ __global__ void __launch_bounds__(128 + kFewEpilogue, 1) glu_few_kernel(const __
     for (int64_t i = begin; i < end && ok; ++tile) {
       const int n = (int)min((int64_t)(p.kblocks - k), end - i);
       const bool whole = n == p.kblocks;
-      ok = all_of_epilogue(mbar_wait(tfull + b, pb, kProductLimitNs));  // the warps go on, or give up, together
+      ok = all_of<kFewEpilogue>(mbar_wait(tfull + b, pb, kProductLimitNs));  // the warps go on, or give up, together
       if (!ok) break;
       tc_fence_after();
       const uint32_t d = tmem + b * 2 * stride + ((uint32_t)(warp & 3) << 21);

@@ -12,6 +12,7 @@ __global__ void __launch_bounds__(256) glu_act_grad_kernel(const E* __restrict__
                                                            int segs, E* __restrict__ dgu) {
   const int64_t stride = (int64_t)gridDim.x * blockDim.x;
   const int64_t F = (int64_t)segs * 8;
+  pdl_launch();
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += stride) {
     const int64_t t = i / segs;
     const int64_t at = i * 8 + t * F;  // 2 F t + f
@@ -39,10 +40,10 @@ struct GradEpilogue {
 
   __device__ __forceinline__ int row_b(int n, int j) const { return n * BN + j; }
   template <typename O>
-  __device__ __forceinline__ void put(O* out, const uint32_t* v, bool add) const {
+  __device__ __forceinline__ void put(O* out, const float* v, bool add) const {
     Vec8 a;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) a.p[e] = make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
+    for (int e = 0; e < 4; ++e) a.p[e] = make_float2(v[2 * e], v[2 * e + 1]);
     if (add) {
       const Vec8 o = unpack(ld8(out));
 #pragma unroll
@@ -50,14 +51,13 @@ struct GradEpilogue {
     }
     st8(out, pack<O>(a));
   }
-  __device__ __forceinline__ void store(uint32_t tmem, int64_t row, int n, int which, int part) const {
+  template <typename Source>
+  __device__ __forceinline__ void store(const Source& from, int64_t row, int n, int which, int part) const {
     const bool is_w = (which != 0) != swapped;
 #pragma unroll 1
     for (int c = part * 16; c < BN; c += 32) {
-      uint32_t v[16];
-      __syncwarp();
-      issue16(tmem + c, v);
-      take16(v);
+      float v[16];
+      from.get(c, v);
       if (row >= (is_w ? F2 : T)) continue;
 #pragma unroll
       for (int p = 0; p < 16; p += 8) {  // eight columns: H is a multiple of eight
@@ -71,6 +71,25 @@ struct GradEpilogue {
     }
   }
 };
+
+// dx = dgu w: the reduction runs over w's rows.  dw = dgu^T x: over the tokens.
+template <typename E, typename S>
+static cudaError_t grad_products(const void* x, int64_t ld_x, const void* w, int64_t T, int H, int64_t F2, const void* dgu, void* dx,
+                                 void* dw, bool dw32, bool accumulate, bool w_first, void* ws, cudaStream_t s) {
+  const int64_t cols = (H + S::BN - 1) / S::BN;
+  const GradEpilogue<E, S::BN> epi = {static_cast<E*>(dx), dw, T, F2, H, dw32, accumulate, w_first};
+  auto make = [&](Problem* p, bool is_w) {
+    return is_w ? problem<E, S>(p, F2, cols, T, dgu, true, F2, x, H, ld_x) : problem<E, S>(p, T, cols, F2, dgu, false, F2, w, H, H);
+  };
+  if (dx && dw) {
+    Work<2> p;
+    if (!make(&p.p[0], w_first) || !make(&p.p[1], !w_first)) return cudaErrorInvalidValue;
+    return product_launch<E, S, 2>(p, ws, epi, s);
+  }
+  Work<1> p;
+  if (!make(&p.p[0], w_first)) return cudaErrorInvalidValue;
+  return product_launch<E, S, 1>(p, ws, epi, s);
+}
 
 template <typename E>
 static cudaError_t glu_grad_launch(const void* dh, const void* gu, const void* x, int64_t ld_x, const void* w, int act, int64_t T,
@@ -87,28 +106,17 @@ static cudaError_t glu_grad_launch(const void* dh, const void* gu, const void* x
   k<<<(unsigned)blocks, 256, 0, s>>>(static_cast<const E*>(dh), static_cast<const E*>(gu), n, segs, static_cast<E*>(dgu));
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || (!dx && !dw)) return e;
-#ifndef FCG
-#define FCG 2
-#define FBN 256
-#endif
-  using S = Tile<FCG, FBN, true>;
-  const int64_t cols = (H + S::BN - 1) / S::BN, F2 = 2 * (int64_t)F;
-  GradEpilogue<E, S::BN> epi = {static_cast<E*>(dx), dw, T, F2, H, dw32, accumulate, false};
-  // dx = dgu w: the reduction runs over w's rows.  dw = dgu^T x: over the tokens
-  auto dx_problem = [&](Problem* p) { return problem<E, S>(p, T, cols, F2, dgu, false, F2, w, H, H); };
-  auto dw_problem = [&](Problem* p) { return problem<E, S>(p, F2, cols, T, dgu, true, F2, x, H, ld_x); };
-  if (dx && dw) {
-    Work<2> p;
-    p.status = static_cast<unsigned*>(ws);
-    epi.swapped = T > F2;
-    if (!dx_problem(&p.p[epi.swapped]) || !dw_problem(&p.p[!epi.swapped])) return cudaErrorInvalidValue;
-    return product_launch<E, S, 2>(p, epi, s);
-  }
-  Work<1> p;
-  p.status = static_cast<unsigned*>(ws);
-  epi.swapped = dx == nullptr;
-  if (dx ? !dx_problem(&p.p[0]) : !dw_problem(&p.p[0])) return cudaErrorInvalidValue;
-  return product_launch<E, S, 1>(p, epi, s);
+  const int64_t F2 = 2 * (int64_t)F;
+  const bool both = dx && dw, w_first = both ? T > F2 : dx == nullptr;  // the product of more stages comes first
+  if (product_small(
+          [&](int i, int rows, int columns, int64_t* n, int64_t* k) {
+            const bool is_w = (i == 0) == w_first;
+            *n = (((is_w ? F2 : T) + rows - 1) / rows) * ((H + columns - 1) / columns);
+            *k = ((is_w ? T : F2) + kBK - 1) / kBK;
+          },
+          both ? 2 : 1))
+    return grad_products<E, Tile<1, 128, true>>(x, ld_x, w, T, H, F2, dgu, dx, dw, dw32, accumulate, w_first, ws, s);
+  return grad_products<E, Tile<2, 256, true>>(x, ld_x, w, T, H, F2, dgu, dx, dw, dw32, accumulate, w_first, ws, s);
 }
 
 }  // namespace mhc

@@ -14,6 +14,12 @@
 // 64 columns and the MMA reads it transposed.  One launch may do two products, so
 // that the second's tiles fill the SMs that the first leaves.
 //
+// The tiles that do not fill a last round over the SMs are cut along k into equal runs
+// of stages instead, one per group, done first: a run that ends inside a tile leaves fp32
+// sums in the workspace, and the group that comes last to a tile adds them up in the
+// runs' order and finishes it, while its next tile's products run.  Nothing waits for
+// another group, and the sums do not depend on which comes last.
+//
 // What lies outside the matrices is fetched as zeros, so no size needs padding.
 // Every wait is bounded; one that runs out sets bit 1 of the workspace's status
 // word and the kernel gives up (mhc_check_status).
@@ -31,7 +37,7 @@ bool encode(CUtensorMap* m, CUtensorMapDataType dt, int rank, const void* base, 
             const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle sw);
 
 constexpr int kBM = 128, kBK = 64;  // rows of A per CTA, depth of a stage
-constexpr int kProductThreads = 384;  // producer, MMA, allocation, an idle warp; eight epilogue warps
+constexpr int kEpilogueThreads = 256, kProductThreads = 128 + kEpilogueThreads;  // producer, MMA, allocation, an idle warp; eight epilogue warps
 constexpr uint64_t kProductLimitNs = 2000000000ull;
 
 // ------------------------------------------------------------ PTX, pairs --
@@ -137,13 +143,22 @@ struct Problem {
   int num_m, num_n, kblocks;
   bool amn;
 };
-// The products of one launch.  Tiles are handed out in order, so the ones with more
-// stages come first.
+// The products of one launch: `whole` tiles of each are done as they are, the `rest` in
+// `runs` runs.
 template <int N>
 struct Work {
   Problem p[N];
-  int tiles[N];  // of this and the products before it
-  unsigned* status;
+  int whole[N], rest[N];
+  int runs, units;  // units: stages of all the rest
+  unsigned *status, *counters;
+  float* parts;
+};
+
+// A stretch of stages k0 .. k0 + nk of one tile.
+struct Stretch {
+  int which, m, n, k0, nk;
+  int tile, begin;  // of the rest: its number, and its first unit
+  bool all;         // the whole tile
 };
 
 template <int CG_, int BN_, bool BMN_>
@@ -168,8 +183,142 @@ __device__ __forceinline__ void tile_place(int t, int num_m, int num_n, int& m, 
   m = g * kGroup + r - n * rows;
 }
 
-// Epi: `row_b(n_tile, j)` is the row of B for column j of the tile; `store(tmem, row,
-// n_tile, product, part)` makes a lane's row of outputs, every other 16 columns (part 0 or 1).
+// The stretches of one group, in order; each role of the kernel goes through them.
+template <int N>
+struct Walk {
+  const Work<N>& w;
+  int at, end;  // units of this group's run that are left
+  int t, step;  // next whole tile
+  __device__ __forceinline__ Walk(const Work<N>& work, int group, int groups) : w(work), at(0), end(0), t(group), step(groups) {
+    if (group < w.runs) {
+      at = (int)((int64_t)group * w.units / w.runs);
+      end = (int)((int64_t)(group + 1) * w.units / w.runs);
+    }
+  }
+  __device__ __forceinline__ bool next(Stretch& s) {
+    int index;
+    if (at < end) {
+      const int units0 = w.rest[0] * w.p[0].kblocks;
+      s.which = N == 2 && at >= units0 ? N - 1 : 0;
+      const int before = s.which ? units0 : 0, kb = w.p[s.which].kblocks, i = (at - before) / kb;
+      s.begin = before + i * kb;
+      s.k0 = at - s.begin;
+      s.nk = min(kb - s.k0, end - at);
+      s.tile = (s.which ? w.rest[0] : 0) + i;
+      index = w.whole[s.which] + i;
+      at += s.nk;
+    } else {
+      index = t;
+      s.which = 0;
+      if (N == 2 && t >= w.whole[0]) s.which = N - 1, index -= w.whole[0];
+      if (index >= w.whole[s.which]) return false;
+      s.k0 = 0;
+      s.nk = w.p[s.which].kblocks;
+      t += step;
+    }
+    s.all = s.nk == w.p[s.which].kblocks;
+    tile_place(index, w.p[s.which].num_m, w.p[s.which].num_n, s.m, s.n);
+    return true;
+  }
+  // The run that has unit u.
+  __device__ __forceinline__ int run_of(int u) const { return (int)(((int64_t)(u + 1) * w.runs - 1) / w.units); }
+};
+
+// Where an epilogue finds 16 columns of its lane's row: in tensor memory, or as the sum of
+// a cut tile's parts.  A part lies as four columns of a row together, rows adjacent.
+struct FromTmem {
+  uint32_t at;
+  __device__ __forceinline__ void get(int c, float* v) const {
+    uint32_t* r = reinterpret_cast<uint32_t*>(v);
+    __syncwarp();
+    issue16(at + c, r);
+    take16(r);
+  }
+  __device__ __forceinline__ void get2(int c, float* v, int d, float* u) const {
+    uint32_t *r = reinterpret_cast<uint32_t*>(v), *q = reinterpret_cast<uint32_t*>(u);
+    __syncwarp();
+    issue16(at + c, r);
+    issue16(at + d, q);
+    take16(r);
+    take16(q);
+  }
+};
+struct FromParts {
+  const float* first;  // run r0's part, this lane's row
+  const float* next;   // run r0 + 1's: the tile is its first, as for the runs after it
+  size_t stride;       // from a run to the one after the next
+  int more;            // runs after r0 + 1
+  __device__ __forceinline__ static void read(float4* x, const float* p, int c) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = __ldcg(reinterpret_cast<const float4*>(p + (size_t)(c + 4 * e) * kBM));
+  }
+  __device__ __forceinline__ static void add(float* v, const float4* x) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[4 * e] += x[e].x, v[4 * e + 1] += x[e].y, v[4 * e + 2] += x[e].z, v[4 * e + 3] += x[e].w;
+  }
+  // (all that is fetched here is fetched before any of it is added: the time is the loads' latency)
+  __device__ __forceinline__ void get(int c, float* v) const {
+    float4 x[4], y[4], z[4];
+    read(x, first, c);
+    read(y, next, c);
+    if (more > 0) read(z, next + stride, c);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] = 0.f;
+    add(v, x);
+    add(v, y);
+    if (more > 0) add(v, z);
+    for (int i = 2; i <= more; ++i) {
+      read(x, next + i * stride, c);
+      add(v, x);
+    }
+  }
+  __device__ __forceinline__ void get2(int c, float* v, int d, float* u) const {
+    float4 x[4], y[4], p[4], q[4];
+    read(x, first, c);
+    read(p, first, d);
+    read(y, next, c);
+    read(q, next, d);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] = u[e] = 0.f;
+    add(v, x);
+    add(u, p);
+    add(v, y);
+    add(u, q);
+    for (int i = 1; i <= more; i += 2) {
+      const float *a = next + i * stride, *b = a + stride;
+      read(x, a, c);
+      read(p, a, d);
+      if (i < more) {
+        read(y, b, c);
+        read(q, b, d);
+      }
+      add(v, x);
+      add(u, p);
+      if (i < more) {
+        add(v, y);
+        add(u, q);
+      }
+    }
+  }
+};
+
+// Barrier 1 over THREADS threads; whether `x` holds in all of them.
+template <int THREADS>
+__device__ __forceinline__ bool all_of(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred q, 1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)x), "n"(THREADS)
+      : "memory");
+  return r != 0;
+}
+
+// Epi: `row_b(n_tile, j)` is the row of B for column j of the tile; `store(source,
+// row, n_tile, product, half)` makes a lane's row of outputs, every other 16 columns.
 template <typename E, typename S, int NP, typename Epi>
 __global__ void __launch_bounds__(kProductThreads, 1)
     product_kernel(const __grid_constant__ Work<NP> w, const __grid_constant__ Epi epi) {
@@ -180,6 +329,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(aligned + (size_t)kStages * S::kStage);
   uint64_t *empty = full + kStages, *tfull = empty + kStages, *tempty = tfull + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
+  volatile uint32_t* last = tmem_slot + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CG == 2 ? cluster_ctarank() : 0;
 
@@ -199,23 +349,22 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   if constexpr (CG == 2) cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  pdl_launch();  // the next kernel's CTAs may take the place of those that end early
 
   const int groups = gridDim.x / CG, group = blockIdx.x / CG;
-  const int tiles = w.tiles[NP - 1];
-  auto product_of = [&](int t) { return NP == 2 && t >= w.tiles[0] ? NP - 1 : 0; };
+  Walk<NP> walk(w, group, groups);
+  Stretch s;
   bool ok = true;
 
   if (warp == 0) {  // ------------------------------------------- producer
     if (lane == 0) {
+      pdl_wait();
       int st = 0, used = 0;
       uint32_t ph = 1;
-      for (int t = group; t < tiles && ok; t += groups) {
-        const int which = product_of(t);
-        const Problem& p = w.p[which];
-        int m, n;
-        tile_place(which ? t - w.tiles[0] : t, p.num_m, p.num_n, m, n);
-        const int row = (m * CG + (int)rank) * kBM;
-        for (int k = 0; k < p.kblocks; ++k) {
+      while (ok && walk.next(s)) {
+        const Problem& p = w.p[s.which];
+        const int row = (s.m * CG + (int)rank) * kBM;
+        for (int k = s.k0; k < s.k0 + s.nk; ++k) {
           ok = mbar_wait_cluster(empty + st, ph, kProductLimitNs);
           if (!ok) break;
           if (rank == 0) mbar_arrive_expect_tx(full + st, CG * S::kStage);
@@ -229,7 +378,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           }
 #pragma unroll
           for (int j = 0; j < S::kRowsB; j += S::kBoxB) {
-            const int rb = epi.row_b(n, (int)rank * S::kRowsB + j);
+            const int rb = epi.row_b(s.n, (int)rank * S::kRowsB + j);
             if (S::BMN) pair_load<CG>(b + j * 128, &p.b, bar, rb, k * kBK);
             else pair_load<CG>(b + j * 128, &p.b, bar, k * kBK, rb);
           }
@@ -247,18 +396,16 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     if (lane == 0 && rank == 0) {
       int st = 0, b = 0;
       uint32_t ph = 0, pb = 1;
-      for (int t = group; t < tiles && ok; t += groups) {
+      while (ok && walk.next(s)) {
         ok = mbar_wait_cluster(tempty + b, pb, kProductLimitNs);
         if (!ok) break;
         tc_fence_after();
         const uint32_t d = tmem + b * S::BN;
-        const Problem& p = w.p[product_of(t)];
-        const bool amn = p.amn;
-        const int kblocks = p.kblocks;
+        const bool amn = w.p[s.which].amn;
         const uint32_t idesc = product_idesc<E>(kBM * CG, S::BN, amn, S::BMN);
         // 16 of a stage's 64 k: 32 bytes along a K-major row, else two 8-k groups
         const uint32_t step_a = (amn ? 2048 : 32) >> 4, step_b = (S::BMN ? 2048 : 32) >> 4;
-        for (int k = 0; k < kblocks; ++k) {
+        for (int k = 0; k < s.nk; ++k) {
           ok = mbar_wait_cluster(full + st, ph, kProductLimitNs);
           if (!ok) break;
           tc_fence_after();
@@ -275,15 +422,28 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   } else if (warp >= 4) {  // ------------------------------------ epilogue
     int b = 0;
     uint32_t pb = 0;
-    for (int t = group; t < tiles && ok; t += groups) {
-      ok = __all_sync(0xffffffffu, mbar_wait_cluster(tfull + b, pb, kProductLimitNs));
+    pdl_wait();
+    const int half = (warp - 4) >> 2, in_tile = (warp & 3) * 32 + lane;
+    constexpr size_t kPart = (size_t)kBM * S::BN;
+    while (walk.next(s)) {
+      ok = all_of<kEpilogueThreads>(mbar_wait_cluster(tfull + b, pb, kProductLimitNs));  // the warps go on, or give up, together
       if (!ok) break;
       tc_fence_after();
-      const int which = product_of(t);
-      int m, n;
-      tile_place(which ? t - w.tiles[0] : t, w.p[which].num_m, w.p[which].num_n, m, n);
-      epi.store(tmem + b * S::BN + ((uint32_t)(warp & 3) << 21), ((int64_t)m * CG + rank) * kBM + (warp & 3) * 32 + lane, n,
-                which, (warp - 4) >> 2);
+      const FromTmem tile = {tmem + b * S::BN + ((uint32_t)(warp & 3) << 21)};
+      const int64_t row = ((int64_t)s.m * CG + rank) * kBM + in_tile;
+      if (s.all) {
+        epi.store(tile, row, s.n, s.which, half);
+      } else {
+        const bool is_first = s.begin <= (int)((int64_t)group * w.units / w.runs);
+        float* mine = w.parts + ((size_t)(group * 2 + !is_first) * CG + rank) * kPart + in_tile * 4;
+        for (int c = half * 16; c < S::BN; c += 32) {
+          float v[16];
+          tile.get(c, v);
+#pragma unroll
+          for (int e = 0; e < 16; e += 4)
+            __stcg(reinterpret_cast<float4*>(mine + (size_t)(c + e) * kBM), make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]));
+        }
+      }
       tc_wait_ld();
       tc_fence_before();
       __syncwarp();
@@ -292,6 +452,24 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         else mbar_arrive(tempty + b);
       }
       if ((b ^= 1) == 0) pb ^= 1;
+      if (!s.all) {
+        const int r0 = walk.run_of(s.begin), r1 = walk.run_of(s.begin + w.p[s.which].kblocks - 1);
+        unsigned* counter = w.counters + s.tile * CG + rank;
+        __threadfence();
+        named_bar_sync(1, kEpilogueThreads);
+        if (threadIdx.x == 128) *last = atomicAdd(counter, 1u) == (unsigned)(r1 - r0);
+        named_bar_sync(1, kEpilogueThreads);
+        if (*last) {
+          __threadfence();
+          const bool whole_run = s.begin <= (int)((int64_t)r0 * w.units / w.runs);  // run r0 begins in the tile
+          const float* at = w.parts + rank * kPart + in_tile * 4;
+          const FromParts sum = {at + (size_t)(r0 * 2 + !whole_run) * CG * kPart, at + (size_t)(r0 + 1) * 2 * CG * kPart,
+                                 2 * CG * kPart, r1 - r0 - 1};
+          epi.store(sum, row, s.n, s.which, half);
+          if (threadIdx.x == 128) *counter = 0;
+        }
+        named_bar_sync(1, kEpilogueThreads);  // (*last is read before the next tile's is written)
+      }
     }
   }
   if (!ok) {  // gave up: report, and let copies and MMAs in flight end before anything is freed
@@ -329,8 +507,66 @@ inline bool problem(Problem* p, int64_t M, int64_t num_n, int64_t K, const void*
          encode_2d<E>(&p->b, b, S::BMN ? K : rows_b, S::BMN ? rows_b : K, ld_b, S::kBoxB);
 }
 
+// Workspace of the products: the status word, counters of cut tiles, two parts per group.
+constexpr size_t kProductCounters = 256, kProductParts = kProductCounters + 32768;
+constexpr int kMostSms = 152;
+constexpr size_t kProductBytes = kProductParts + (size_t)kMostSms * 2 * kBM * 256 * 4;
+
+// How the tiles of one or two products (n[i] tiles of kb[i] stages) are done by `groups`
+// groups: whole rounds, and the rest of each cut into runs where that takes fewer stages.
+// A cut costs its sums' way through L2 and, where no whole tile comes after, the last
+// group's reading of them: about 10 stages and 5 for each part of a tile; so a tile is cut
+// into four at most.
+struct ProductPlan {
+  int64_t whole[2], rest[2], units, runs;
+  int64_t stages;  // of the group that has the most
+};
+inline ProductPlan product_plan(int products, const int64_t* n, const int64_t* kb, int groups) {
+  constexpr int kParts = 4, kLeast = 4;
+  ProductPlan p = {};
+  int64_t tiles = 0, uncut = 0, rounds = 0;
+  for (int i = 0; i < products; ++i) {
+    p.whole[i] = n[i] / groups * groups;
+    p.rest[i] = n[i] - p.whole[i];
+    rounds += n[i] / groups * kb[i];
+    p.units += p.rest[i] * kb[i];
+    tiles += p.rest[i];
+    if (p.rest[i] && kb[i] > uncut) uncut = kb[i];
+  }
+  if (tiles > groups) uncut += kb[products - 1];  // the longest come first
+  p.runs = (p.units + kLeast - 1) / kLeast;
+  if (p.runs > tiles * kParts) p.runs = tiles * kParts;
+  if (p.runs > groups) p.runs = groups;
+  int64_t cut = uncut + 1;
+  if (p.runs > 0) {
+    const int64_t each = (p.units + p.runs - 1) / p.runs;
+    cut = each + (rounds ? 6 : 20 + 15 * ((p.runs + tiles - 1) / tiles));
+  }
+  if (cut >= uncut) {
+    for (int i = 0; i < products; ++i) p.whole[i] += p.rest[i], p.rest[i] = 0;
+    p.units = p.runs = 0;
+    cut = uncut;
+  }
+  p.stages = rounds + cut;
+  return p;
+}
+
+// Whether tiles of 128 x 128 (a CTA each) take less time than tiles of 256 x 256 (a pair):
+// stages times a stage's time, in hundredths of the large tile's 0.3 us, and what the start and
+// the last tile's end cost beside them.  T = 8192, H = 5120, F = 10240 takes the gated projections
+// 855 us in large tiles and 1273 in small ones; T = 300, H = 512, F = 1368 9.4 and 7.2.
+template <typename Tiles>
+inline bool product_small(const Tiles& tiles, int products) {
+  int64_t n[2], kb[2], large, small;
+  for (int i = 0; i < products; ++i) tiles(i, 256, 256, n + i, kb + i);
+  large = product_plan(products, n, kb, kMostSms / 2).stages * 100 + 1300;
+  for (int i = 0; i < products; ++i) tiles(i, 128, 128, n + i, kb + i);
+  small = product_plan(products, n, kb, kMostSms).stages * 74 + 600;
+  return small < large;
+}
+
 template <typename E, typename S, int NP, typename Epi>
-inline cudaError_t product_launch(Work<NP>& w, const Epi& epi, cudaStream_t s) {
+inline cudaError_t product_launch(Work<NP>& w, void* ws, const Epi& epi, cudaStream_t s) {
   static SmemGrant grant;
   auto k = product_kernel<E, S, NP, Epi>;
   cudaError_t e = allow_smem(grant, (const void*)k, S::kSmem);
@@ -338,24 +574,33 @@ inline cudaError_t product_launch(Work<NP>& w, const Epi& epi, cudaStream_t s) {
   int sms = 0;
   e = sm_count(&sms);
   if (e != cudaSuccess) return e;
-  int64_t tiles = 0;
+  const int most = (sms < kMostSms ? sms : kMostSms) / S::CG;
+  int64_t n[2], kb[2], tiles = 0;
   for (int i = 0; i < NP; ++i) {
-    tiles += (int64_t)w.p[i].num_m * w.p[i].num_n;
-    if (tiles > 0x7fffffff) return cudaErrorInvalidValue;
-    w.tiles[i] = (int)tiles;
+    n[i] = (int64_t)w.p[i].num_m * w.p[i].num_n, kb[i] = w.p[i].kblocks;
+    tiles += n[i];
+    if (n[i] > 0x3fffffff) return cudaErrorInvalidValue;
   }
-  const int64_t groups = tiles < sms / S::CG ? tiles : sms / S::CG;
+  const ProductPlan plan = product_plan(NP, n, kb, most);
+  for (int i = 0; i < NP; ++i) w.whole[i] = (int)plan.whole[i], w.rest[i] = (int)plan.rest[i];
+  w.units = (int)plan.units, w.runs = (int)plan.runs;
+  const int64_t groups = plan.runs == 0 ? (tiles < most ? tiles : most) : (plan.whole[0] + plan.whole[NP - 1] == 0 ? plan.runs : most);
+  w.status = static_cast<unsigned*>(ws);
+  w.counters = reinterpret_cast<unsigned*>(static_cast<char*>(ws) + kProductCounters);
+  w.parts = reinterpret_cast<float*>(static_cast<char*>(ws) + kProductParts);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(groups * S::CG));
   cfg.blockDim = dim3(kProductThreads);
   cfg.dynamicSmemBytes = S::kSmem;
   cfg.stream = s;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = S::CG;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   e = cudaLaunchKernelEx(&cfg, k, w, epi);
   if (e != cudaSuccess) cudaGetLastError();  // it is this call's, not the next one's
   return e;

@@ -225,7 +225,8 @@ def test_glu_grad(T, H, F, dtype, act):
     # one product alone; 32-bit weights' gradients, added to what is there
     again, dx2 = e(T, 2 * F), e(T, H)
     B.mhc_glu_grad(dev(dh), dev(gu), None, dev(w), again, dx2, None, ws, act=R.ACTS.index(act))
-    assert torch.equal(again, dgu) and torch.equal(dx2, dx)
+    assert torch.equal(again, dgu)
+    block_case.check(dx2, ref["dx"], terms["dx"], n=1, what="dx alone")  # (its sums may be cut at other places)
     old = normal(g, 2 * F, H)
     acc = dev(old)
     B.mhc_glu_grad(dev(dh), dev(gu), dev(x), None, again, None, acc, ws, act=R.ACTS.index(act), accumulate=True)

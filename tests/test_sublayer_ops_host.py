@@ -95,7 +95,7 @@ def test_glu_reference_is_torch():
 
 
 GGRAD = dict(dh=A, gu=A + STEP, x=A + 2 * STEP, ld_x=64, w=A + 3 * STEP, act=0, T=4, H=64, F=128, dtype=0, dgu=A + 4 * STEP,
-             dx=A + 5 * STEP, dw=A + 6 * STEP, dw_dtype=2, acc=0, ws=A + 7 * STEP, ws_bytes=1 << 24, stream=None)
+             dx=A + 5 * STEP, dw=A + 6 * STEP, dw_dtype=2, acc=0, ws=A + 7 * STEP, ws_bytes=1 << 27, stream=None)
 
 
 @pytest.mark.parametrize("over,code", [
