@@ -446,8 +446,8 @@ size_t mhc_lora_workspace_bytes(int64_t T, int R);
  *           then what the adapters add, as mhc_glu() takes it in `add`)
  *   out     [T,N], rows ld_out apart; may be base (same stride, in place)
  * bf16 or fp16; A_i x is kept in fp32 and enters the second product as two 16-bit values.
- * The tokens may come in any order; runs of one request cost least.  T <= 2^30, H and N
- * multiples of 8, at most 2^20, R a multiple of 8, at most 256.  Errors: MHC_ERR_CONFIG,
+ * The tokens may come in any order (more than 64 are sorted by adapter, 1024 together).
+ * T <= 2^30, n <= 2^20, H and N multiples of 8, at most 2^20, R a multiple of 8, at most 256.  Errors: MHC_ERR_CONFIG,
  * MHC_ERR_SHAPE, MHC_ERR_NULL, MHC_ERR_ALIGN, MHC_ERR_WORKSPACE, MHC_ERR_ALIAS, MHC_ERR_CUDA. */
 int mhc_lora(const void* x, int64_t ld_x, const void* a, const void* b, const int32_t* index, const float* scale,
              int64_t T, int H, int N, int R, int n, mhc_dtype dtype, const void* base, int64_t ld_base, void* out,

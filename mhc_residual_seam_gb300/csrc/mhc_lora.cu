@@ -2,36 +2,116 @@
 //
 //   v[t,:] = A_a x[t],  out[t,:] = base[t,:] + s_a B_a v[t],  a = index[t]
 //
-// Two launches: the first makes v (split over H, so that a few tokens fill the GPU),
-// the second sums the parts and applies B.  Both work on tiles of 64 tokens: a CTA
-// finds the different adapters of its tile and takes the tokens of one adapter after
-// another as the rows of tensor-core products (mma.sync m16n8k16: the work is bound by
-// memory, x and out are read and written once, and an adapter's weights once per tile
-// that names it).  Operands go from memory to registers in 16-byte pieces: the order of
-// a product's reduction index and of its columns is free, so each thread's fragment is
-// taken from adjacent elements.
+// The work is bound by memory (x and base read once, out written once, an adapter's
+// weights once per unit), so its products run on mma.sync from registers.  A unit is up
+// to 64 tokens of one adapter: the rows of the products.
+//   plan    (more than 64 tokens) sorts runs of 1024 tokens by adapter and cuts them into
+//           units, so that tokens in any order share their adapter's weights
+//   shrink  v of a unit: a cluster of CTAs shares H, its sums meet in shared memory
+//   expand  B v, the scale and base: 64 columns a warp at a time
+// With up to 64 tokens each CTA finds its unit by itself.
+//
+// Operands go from memory to registers in 16-byte pieces: the order of a product's
+// reduction index and of its columns is free, so each thread's fragment is taken from
+// adjacent elements.
 
 #include <type_traits>
 
 #include "mhc_ops.cuh"
+#include "mhc_sm100.cuh"
 
 namespace mhc {
 
-constexpr int kTok = 64;  // tokens of a tile
+constexpr int kTok = 64;     // most tokens of a unit
+constexpr int kRun = 1024;   // tokens sorted together
+constexpr int kMostParts = 8;
 
-// The different adapters of a tile in order of appearance (-1: tokens without one), and
-// the tokens of one of them.  Made by warp 0.
-struct TileTokens {
-  int firsts[kTok], rows[kTok];
-  int distinct, count;
+struct Unit {
+  int adapter;  // -1: tokens without one
+  int first;    // in the sorted order
+  int count;
+  int pad;
+};
+struct LoraPlan {
+  const int* order;   // sorted order -> token; NULL: units are found in the kernel
+  const Unit* units;  // kRun per run of tokens
+  const int* made;    // units of a run
+  int most;           // CTAs per run
 };
 
-// Warp 0 holds the tile's adapters in two registers a lane (-2: past the last token).
 __device__ __forceinline__ int adapter_of(const int* index, int64_t t, int64_t T, int n) {
   if (t >= T) return -2;
   const int i = index[t];
   return i >= 0 && i < n ? i : -1;
 }
+
+// ---------------------------------------------------------------- the plan --
+// A thread per token: bitonic sort of (adapter, place) words, stable because the place is
+// part of them; then the first token of each 64 of an adapter starts a unit.
+__global__ void __launch_bounds__(kRun) lora_plan_kernel(const int* __restrict__ index, int64_t T, int n, int* __restrict__ order,
+                                                         Unit* __restrict__ units, int* __restrict__ made) {
+  __shared__ uint32_t word[kRun];
+  __shared__ int starts[kRun + 1], warp_sum[32];
+  pdl_wait();
+  pdl_launch();
+  const int i = threadIdx.x, lane = i & 31, warp = i >> 5;
+  const int64_t t0 = (int64_t)blockIdx.x * kRun;
+  const int m = (int)min((int64_t)kRun, T - t0);
+  const int id = adapter_of(index, t0 + i, T, n);
+  uint32_t key = id == -2 ? 0xffffffffu : ((uint32_t)(id < 0 ? n : id) << 10) | i;
+  for (int k = 2; k <= kRun; k <<= 1)
+    for (int j = k >> 1; j > 0; j >>= 1) {
+      uint32_t other;
+      if (j >= 32) {
+        word[i] = key;
+        __syncthreads();
+        other = word[i ^ j];
+        __syncthreads();
+      } else {
+        other = __shfl_xor_sync(0xffffffffu, key, j);
+      }
+      const bool low = (i & j) == 0, up = (i & k) == 0;
+      key = low == up ? min(key, other) : max(key, other);
+    }
+  word[i] = key;
+  __syncthreads();
+  const bool live = i < m;
+  const int a = (int)(key >> 10);
+  // where this adapter's tokens begin: the last start at or before this place
+  int begin = live && (i == 0 || (int)(word[i - 1] >> 10) != a) ? i : 0;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, begin, d);
+    if (lane >= d) begin = max(begin, o);
+  }
+  if (lane == 31) warp_sum[warp] = begin;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) begin = max(begin, warp_sum[w]);
+  const bool starts_unit = live && (i - begin) % kTok == 0;
+  const unsigned b = __ballot_sync(0xffffffffu, starts_unit);
+  __syncthreads();
+  if (lane == 0) warp_sum[warp] = __popc(b);
+  __syncthreads();
+  int u = __popc(b & ((1u << lane) - 1)), total = 0;
+  for (int w = 0; w < 32; ++w) {
+    if (w < warp) u += warp_sum[w];
+    total += warp_sum[w];
+  }
+  if (starts_unit) starts[u] = i;
+  if (i == 0) starts[total] = m, made[blockIdx.x] = total;
+  __syncthreads();
+  if (live) order[t0 + i] = (int)t0 + (int)(key & (kRun - 1));
+  if (starts_unit) units[t0 + u] = {a == n ? -1 : a, (int)t0 + i, starts[u + 1] - i, 0};
+}
+
+// ------------------------------------------------------------ finding units --
+// With up to 64 tokens: their different adapters in order of appearance, and the tokens of
+// one of them.  Made by warp 0, which holds the adapters in two registers a lane (-2: past
+// the last token).
+struct TileTokens {
+  int firsts[kTok], rows[kTok];
+  int distinct, count;
+};
 __device__ __forceinline__ void find_adapters(TileTokens& tile, int id0, int id1, int lane) {
   const unsigned all = 0xffffffffu, below = (1u << lane) - 1;
   // (every lane takes part in every exchange: none of them stands behind a condition)
@@ -56,6 +136,51 @@ __device__ __forceinline__ void find_tokens(TileTokens& tile, int id, int id0, i
   if (id1 == id) tile.rows[__popc(b0) + __popc(b1 & below)] = lane + 32;
   if (lane == 0) tile.count = __popc(b0) + __popc(b1);
 }
+// The units of this CTA one after another: `next` is called by all threads and leaves the
+// tokens in tile.rows (a barrier before the rows are used, and one before the next call,
+// are part of it).
+struct Units {
+  TileTokens& tile;
+  const LoraPlan& plan;
+  int id0, id1, j, step;
+  bool left;
+  __device__ __forceinline__ Units(TileTokens& t, const LoraPlan& p, const int* index, int64_t T, int n) : tile(t), plan(p), left(true) {
+    const int lane = threadIdx.x & 31;
+    if (!plan.order) {
+      id0 = adapter_of(index, lane, T, n), id1 = adapter_of(index, lane + 32, T, n);
+      if (threadIdx.x < 32) find_adapters(tile, id0, id1, lane);
+      __syncthreads();
+      j = blockIdx.x, step = gridDim.x;
+    }
+  }
+  __device__ __forceinline__ bool next(int& adapter, int& count) {
+    __syncthreads();
+    if (plan.order) {
+      const int64_t run = blockIdx.x / plan.most;
+      const int u = blockIdx.x - (int)run * plan.most;
+      if (!left || u >= plan.made[run]) return false;
+      left = false;
+      const Unit unit = plan.units[run * kRun + u];
+      if (threadIdx.x < unit.count) tile.rows[threadIdx.x] = plan.order[unit.first + threadIdx.x];
+      adapter = unit.adapter, count = unit.count;
+      __syncthreads();
+      return true;
+    }
+    if (j >= tile.distinct) return false;
+    adapter = tile.firsts[j];
+    if (threadIdx.x < 32) find_tokens(tile, adapter, id0, id1, threadIdx.x);
+    __syncthreads();
+    count = tile.count;
+    j += step;
+    return true;
+  }
+};
+
+// ---------------------------------------------------------------- products --
+// 16 bytes from `src`, or zeros (then `any` stands in for the address).
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t smem, const void* src, const void* any, bool take) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(take ? src : any), "r"(take ? 16 : 0) : "memory");
+}
 
 template <typename E>
 __device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -71,248 +196,385 @@ __device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uin
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// v[part, t, r] = sum over the part's columns of x[t, h] A[r, h], eight NT of the rank at
-// a time.  The four warps share a group of up to 64 tokens by 16 tokens and, where there
-// are fewer groups of 16, by columns; their sums are joined in a fixed order.
-template <typename E, int NT>
-__global__ void __launch_bounds__(128) lora_shrink_kernel(const E* __restrict__ x, int64_t ld_x, const E* __restrict__ a,
-                                                          const int* __restrict__ index, int64_t T, int H, int R, int n,
-                                                          int slice, float* __restrict__ v) {
-  __shared__ TileTokens tile;
-  __shared__ float sums[4][16][NT * 8 + 2];
+// Shared memory of a shrink CTA: a ring of three steps of 64 tokens, and the sums [64, R
+// rounded up to 16, plus 4], which take the ring's place where one pass makes the whole rank.
+template <int NT>
+__host__ __device__ constexpr int ring_bytes() {
+  return 3 * (8 + NT) * 2048;
+}
+__host__ __device__ constexpr int sums_stride(int R) { return (R + 15) / 16 * 16 + 4; }
+template <int NT>
+__host__ __device__ constexpr size_t shrink_smem(int R) {
+  return R <= NT * 8 ? ((size_t)ring_bytes<NT>() > (size_t)kTok * sums_stride(R) * 4 ? ring_bytes<NT>() : (size_t)kTok * sums_stride(R) * 4)
+                     : ring_bytes<NT>() + (size_t)kTok * sums_stride(R) * 4;
+}
+
+// The sums of 16 MG tokens over columns [k0, k1), for a warp that takes every fourth 32
+// of them.  A thread's fragments pass through a ring in shared memory that only the thread
+// itself writes (cp.async) and reads, some steps ahead: its own wait_group is all the
+// synchronisation, and a warp's 16-byte pieces are adjacent.
+template <typename E, int NT, int MG>
+__device__ __forceinline__ void shrink_sums(float (&acc)[MG][NT][4], const E* x, int64_t ld_x, const int* rows, int count, const E* a,
+                                            int left, int H, int k0, int k1, uint32_t ring) {
+  constexpr int kPieces = 2 * MG + NT, kAll = ring_bytes<NT>() / (kPieces * 2048), kSteps = kAll > 8 ? 8 : kAll;
+  static_assert(kSteps >= 3, "");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane & 3, g = lane >> 2;
-  const int64_t t0 = (int64_t)blockIdx.x * kTok;
-  const int id0 = adapter_of(index, t0 + lane, T, n), id1 = adapter_of(index, t0 + lane + 32, T, n);
-  if (warp == 0) find_adapters(tile, id0, id1, lane);
-  __syncthreads();
-  pdl_launch();
-  const int distinct = tile.distinct;
-  const int k0 = blockIdx.z * slice, k1 = min(H, k0 + slice);
-  v += (int64_t)blockIdx.z * T * R;
-  for (int j = blockIdx.y; j < distinct; j += gridDim.y) {
-    const int id = tile.firsts[j];
-    if (id < 0) continue;
-    if (warp == 0) find_tokens(tile, id, id0, id1, lane);
-    __syncthreads();
-    const int count = tile.count;
-    const int groups = count <= 16 ? 1 : count <= 32 ? 2 : 4, parts = 4 / groups;
-    const int m = warp % groups, part = warp / groups;
-    const int ra = m * 16 + g, rb = ra + 8;
-    const E* xa = ra < count ? x + (t0 + tile.rows[ra]) * ld_x + q * 8 : nullptr;
-    const E* xb = rb < count ? x + (t0 + tile.rows[rb]) * ld_x + q * 8 : nullptr;
-    for (int r0 = 0; r0 < R; r0 += NT * 8) {
-      float acc[NT][4];
+  const E* px[2 * MG];
 #pragma unroll
-      for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-      const E* ar = a + ((int64_t)id * R + r0 + g) * H + q * 8;
-      if (m * 16 < count) {
-        const uint4 none = make_uint4(0, 0, 0, 0);
-#pragma unroll 2
-        for (int k = k0 + part * 32; k < k1; k += parts * 32) {
-          const bool in = k + q * 8 < k1;
-          const uint4 u = in && xa ? *reinterpret_cast<const uint4*>(xa + k) : none;
-          const uint4 w = in && xb ? *reinterpret_cast<const uint4*>(xb + k) : none;
-          uint4 b[NT];
+  for (int i = 0; i < 2 * MG; ++i) {
+    const int r = i * 8 + g;
+    px[i] = r < count ? x + rows[r] * ld_x + q * 8 : nullptr;
+  }
+  const E* pa = a + (int64_t)g * H + q * 8;
+  auto fetch = [&](int step, int k) {
+    const uint32_t at = ring + step * kPieces * 2048 + threadIdx.x * 16;
+    const bool in = k + q * 8 < k1;
 #pragma unroll
-          for (int i = 0; i < NT; ++i)
-            b[i] = in && r0 + i * 8 + g < R ? *reinterpret_cast<const uint4*>(ar + (int64_t)i * 8 * H + k) : none;
+    for (int i = 0; i < 2 * MG; ++i) cp_async16_or_zero(at + i * 2048, px[i] + k, x, in && px[i]);
 #pragma unroll
-          for (int i = 0; i < NT; ++i) {
-            mma16816<E>(acc[i], u.x, w.x, u.y, w.y, b[i].x, b[i].y);
-            mma16816<E>(acc[i], u.z, w.z, u.w, w.w, b[i].z, b[i].w);
-          }
-        }
-      }
+    for (int i = 0; i < NT; ++i) cp_async16_or_zero(at + (2 * MG + i) * 2048, pa + (int64_t)i * 8 * H + k, x, in && i * 8 + g < left);
+  };
+  const int first = k0 + warp * 32;
+  int ahead = first, step = 0, filled = 0;
+#pragma unroll
+  for (int i = 0; i < kSteps - 1; ++i, ahead += 128) {
+    if (ahead < k1) fetch(i, ahead);
+    cp_async_commit();
+  }
+  filled = kSteps - 1;
+  for (int k = first; k < k1; k += 128) {
+    cp_async_wait<kSteps - 2>();
+    const uint32_t at = ring + step * kPieces * 2048 + threadIdx.x * 16;
+    uint4 b[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) b[i] = lds16(at + (2 * MG + i) * 2048);
+#pragma unroll
+    for (int m = 0; m < MG; ++m) {
+      const uint4 u = lds16(at + 2 * m * 2048), w = lds16(at + (2 * m + 1) * 2048);
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
-        *reinterpret_cast<float2*>(&sums[warp][g][i * 8 + 2 * q]) = make_float2(acc[i][0], acc[i][1]);
-        *reinterpret_cast<float2*>(&sums[warp][g + 8][i * 8 + 2 * q]) = make_float2(acc[i][2], acc[i][3]);
+        mma16816<E>(acc[m][i], u.x, w.x, u.y, w.y, b[i].x, b[i].y);
+        mma16816<E>(acc[m][i], u.z, w.z, u.w, w.w, b[i].z, b[i].w);
       }
-      __syncthreads();
-      for (int i = threadIdx.x; i < count * NT * 8; i += 128) {
-        const int row = i / (NT * 8), c = i % (NT * 8);
-        if (r0 + c >= R) continue;
-        float s = sums[row >> 4][row & 15][c];
-        for (int p = 1; p < parts; ++p) s += sums[(row >> 4) + p * groups][row & 15][c];
-        v[(t0 + tile.rows[row]) * R + r0 + c] = s;
-      }
-      __syncthreads();
     }
+    if (ahead < k1) fetch(filled, ahead);
+    cp_async_commit();
+    ahead += 128;
+    if (++filled == kSteps) filled = 0;
+    if (++step == kSteps) step = 0;
+  }
+  cp_async_wait<0>();
+}
+
+__device__ __forceinline__ float4 lds_cluster(uint32_t at) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+  return v;
+}
+
+// v of the units, as the second product takes it.  The CTAs of a cluster (blockIdx.z) share
+// the columns of H, and in a CTA the warps; eight NT of the rank at a time.  The sums are
+// joined warp after warp and CTA after CTA: their order is fixed.
+//
+// v is fp32 and B has 16 bits: each v is kept as two 16-bit values (its rounding and the
+// rounding of the rest, 16 or 22 bits together), and both are multiplied.  A row is first
+// brought to about 1 by a power of two, so that fp16 neither overflows nor loses the rest to
+// subnormals; `factor` takes it back, with the adapter's scale.  Layout [token][16 of the
+// rank][4 adjacent of them: four roundings, four rests].
+template <typename E, int NT>
+__global__ void __launch_bounds__(128) lora_shrink_kernel(const E* __restrict__ x, int64_t ld_x, const E* __restrict__ a,
+                                                          const int* __restrict__ index, const float* __restrict__ scale,
+                                                          const LoraPlan plan, int64_t T, int H, int R, int n, int slice,
+                                                          uint4* __restrict__ vq, float* __restrict__ factor) {
+  extern __shared__ __align__(16) char smem[];
+  __shared__ TileTokens tile;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane & 3, g = lane >> 2;
+  const int stride = sums_stride(R), chunks = (R + 15) / 16;
+  float* sums = reinterpret_cast<float*>(R <= NT * 8 ? smem : smem + ring_bytes<NT>());
+  const int parts = gridDim.z, part = blockIdx.z;
+  const int k0 = part * slice, k1 = min(H, k0 + slice);
+  pdl_wait();
+  pdl_launch();
+  Units units(tile, plan, index, T, n);
+  int id, count;
+  while (units.next(id, count)) {
+    if (id < 0) continue;
+    for (int r0 = 0; r0 < R; r0 += NT * 8) {
+      const E* ar = a + ((int64_t)id * R + r0) * H;
+      auto go = [&](auto groups) {
+        constexpr int MG = decltype(groups)::value;
+        float acc[MG][NT][4];
+#pragma unroll
+        for (int m = 0; m < MG; ++m)
+#pragma unroll
+          for (int i = 0; i < NT; ++i) acc[m][i][0] = acc[m][i][1] = acc[m][i][2] = acc[m][i][3] = 0.f;
+        shrink_sums<E, NT, MG>(acc, x, ld_x, tile.rows, count, ar, R - r0, H, k0, k1, smem_of(smem));
+        __syncthreads();  // (the sums may take the ring's place)
+        for (int p = 0; p < 4; ++p) {  // warp after warp
+          if (warp == p) {
+#pragma unroll
+            for (int m = 0; m < MG; ++m)
+#pragma unroll
+              for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  const int c = r0 + i * 8 + 2 * q;
+                  if (c >= R) continue;
+                  float2* s = reinterpret_cast<float2*>(sums + (m * 16 + g + 8 * h) * stride + c);
+                  const float2 o = p ? *s : make_float2(0.f, 0.f);
+                  *s = make_float2(o.x + acc[m][i][2 * h], o.y + acc[m][i][2 * h + 1]);
+                }
+          }
+          __syncthreads();
+        }
+      };
+      if (count <= 16) go(std::integral_constant<int, 1>());
+      else if (count <= 32) go(std::integral_constant<int, 2>());
+      else go(std::integral_constant<int, 4>());
+    }
+    __syncwarp();
+    cluster_sync_all();
+    // this CTA's share of the rows, eight lanes a row, four of the rank a lane and step
+    const uint32_t at = smem_of(sums);
+    const float s = scale ? scale[id] : 1.f;
+    for (int r0 = part * 16; r0 < count; r0 += parts * 16) {
+      const int row = r0 + warp * 4 + (lane >> 3), l = lane & 7;
+      float4 z[8];
+      float most = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = i * 32 + l * 4;
+        z[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (row < count && r < R)
+          for (int p = 0; p < parts; ++p) {
+            const float4 y = lds_cluster(mapa_shared(at + (row * stride + r) * 4, p));
+            z[i] = make_float4(z[i].x + y.x, z[i].y + y.y, z[i].z + y.z, z[i].w + y.w);
+          }
+        for (float y : {z[i].x, z[i].y, z[i].z, z[i].w})
+          if (fabsf(y) <= 3e38f) most = fmaxf(most, fabsf(y));
+      }
+#pragma unroll
+      for (int d = 4; d; d >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+      // 2^e of the largest, from its exponent bits; rows of zeros and of subnormals stay as they are
+      const uint32_t e = __float_as_uint(most) >> 23;
+      const bool plain = e < 16 || e > 238;
+      const float down = plain ? 1.f : __uint_as_float((254 - e) << 23), up = plain ? 1.f : __uint_as_float(e << 23);
+      if (row < count) {
+        const int64_t t = tile.rows[row];
+        if (l == 0) factor[t] = s * up;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = i * 32 + l * 4;
+          if (r >= chunks * 16) break;
+          const float2 w[2] = {{z[i].x * down, z[i].y * down}, {z[i].z * down, z[i].w * down}};
+          uint32_t big[2], rest[2];
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            big[p] = word_of(w[p].x, w[p].y, E());
+            const float2 f = pair_of(big[p], E());
+            // (an infinite value has no rest)
+            rest[p] = word_of(fabsf(f.x) <= 3e38f ? w[p].x - f.x : 0.f, fabsf(f.y) <= 3e38f ? w[p].y - f.y : 0.f, E());
+          }
+          vq[t * chunks * 4 + r / 4] = make_uint4(big[0], big[1], rest[0], rest[1]);
+        }
+      }
+    }
+    __syncwarp();
+    cluster_sync_all();  // (the sums are read before the next unit's, or the CTA's end)
   }
 }
 
-// out = base + s B v for the tokens of a tile, 64 columns a warp at a time.
-//
-// v is fp32 and B has 16 bits: each v is cut into two 16-bit values (its rounding and
-// the rounding of the rest, 16 or 22 bits together), and both are multiplied.  A row is
-// first brought to about 1 by a power of two, so that fp16 neither overflows nor loses
-// the rest to subnormals.
-template <typename E>
-__global__ void __launch_bounds__(128) lora_expand_kernel(const float* __restrict__ v, int parts, const E* __restrict__ b,
-                                                          const int* __restrict__ index, const float* __restrict__ scale,
-                                                          int64_t T, int N, int R, int n, const E* base, int64_t ld_b, E* out,
-                                                          int64_t ld_o) {
-  extern __shared__ char raw[];
+// out = base + B v for the units, 64 columns a warp at a time.  A warp keeps the weights of
+// its columns (up to 16 CH of the rank) in registers for all the tokens.
+template <typename E, int CH>
+__global__ void __launch_bounds__(128, 3) lora_expand_kernel(const uint4* vq, const float* factor, const E* __restrict__ b,
+                                                             const int* __restrict__ index, const LoraPlan plan, int64_t T, int N,
+                                                             int R, int n, const E* base, int64_t ld_b, E* out, int64_t ld_o) {
   __shared__ TileTokens tile;
-  __shared__ float factor[kTok];
-  const int chunks = (R + 15) / 16, width = chunks * 16 + 4;
-  // fragments of v, [16 tokens][chunk of 16][lane]: four registers of the rounding, four of the rest
-  uint4* frag = reinterpret_cast<uint4*>(raw);
-  float* vs = reinterpret_cast<float*>(raw + (size_t)(kTok / 16) * chunks * 1024);
+  const int chunks = (R + 15) / 16;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane & 3, g = lane >> 2;
-  const int64_t t0 = (int64_t)blockIdx.x * kTok;
-  const int id0 = adapter_of(index, t0 + lane, T, n), id1 = adapter_of(index, t0 + lane + 32, T, n);
-  if (warp == 0) find_adapters(tile, id0, id1, lane);
-  __syncthreads();
   pdl_wait();
-  const int distinct = tile.distinct;
-  for (int j = blockIdx.y; j < distinct; j += gridDim.y) {
-    const int id = tile.firsts[j];
+  Units units(tile, plan, index, T, n);
+  int id, count;
+  while (units.next(id, count)) {
     if (id < 0 && base == out) continue;
-    if (warp == 0) find_tokens(tile, id, id0, id1, lane);
-    __syncthreads();
-    const int count = tile.count, groups = (count + 15) / 16;
-    if (id >= 0) {
-      const float s = scale ? scale[id] : 1.f;
-      for (int row = warp; row < groups * 16; row += 4) {  // a warp per row: the parts' sum, and the row's exponent
-        float most = 0.f;
-        for (int r = lane; r < chunks * 16; r += 32) {
-          float z = 0.f;
-          if (row < count && r < R) {
-            const float* p = v + (t0 + tile.rows[row]) * R + r;
-            for (int i = 0; i < parts; ++i) z += p[(int64_t)i * T * R];
-          }
-          vs[row * width + r] = z;
-          if (fabsf(z) <= 3e38f) most = fmaxf(most, fabsf(z));
-        }
-#pragma unroll
-        for (int d = 16; d; d >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
-        // 2^e of the largest, from its exponent bits; rows of zeros and of subnormals as they are
-        const uint32_t e = __float_as_uint(most) >> 23;
-        const bool plain = e < 16 || e > 238;
-        const float down = plain ? 1.f : __uint_as_float((254 - e) << 23), up = plain ? 1.f : __uint_as_float(e << 23);
-        for (int r = lane; r < chunks * 16; r += 32) vs[row * width + r] *= down;
-        if (lane == 0) factor[row] = s * up;
-      }
-      __syncthreads();
-      for (int i = threadIdx.x; i < groups * chunks * 32; i += 128) {
-        const int ln = i & 31, c = (i >> 5) % chunks, m = (i >> 5) / chunks;
-        const float4 lo = *reinterpret_cast<const float4*>(vs + (m * 16 + (ln >> 2)) * width + c * 16 + (ln & 3) * 4);
-        const float4 hi = *reinterpret_cast<const float4*>(vs + (m * 16 + 8 + (ln >> 2)) * width + c * 16 + (ln & 3) * 4);
-        const float2 w[4] = {{lo.x, lo.y}, {hi.x, hi.y}, {lo.z, lo.w}, {hi.z, hi.w}};
-        uint32_t big[4], rest[4];
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          big[p] = word_of(w[p].x, w[p].y, E());
-          const float2 f = pair_of(big[p], E());
-          // (an infinite row has no rest)
-          rest[p] = word_of(fabsf(f.x) <= 3e38f ? w[p].x - f.x : 0.f, fabsf(f.y) <= 3e38f ? w[p].y - f.y : 0.f, E());
-        }
-        frag[i * 2] = make_uint4(big[0], big[1], big[2], big[3]);
-        frag[i * 2 + 1] = make_uint4(rest[0], rest[1], rest[2], rest[3]);
-      }
-      __syncthreads();
-    }
+    const int groups = (count + 15) / 16;
     // column of fragment column 2 p + e of product i: 16 p + 2 i + e, so a thread's 16 results of a row are adjacent
     const E* bw = b + (int64_t)max(id, 0) * N * R;
     for (int c0 = (blockIdx.z * 4 + warp) * 64; c0 < N; c0 += gridDim.z * 256) {
+      uint2 w[CH][8];
+      auto weights = [&](int first) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          const int r = (first + c) * 16 + q * 4;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int col = c0 + (g >> 1) * 16 + 2 * i + (g & 1);
+            w[c][i] = make_uint2(0, 0);
+            if (col < N && r < R) w[c][i] = *reinterpret_cast<const uint2*>(bw + (int64_t)col * R + r);
+          }
+        }
+      };
+      const bool once = chunks <= CH;
+      if (id >= 0 && once) weights(0);
       for (int m = 0; m < groups; ++m) {
+        Raw8<E> old[2][2];
+        int64_t at[2];
+        float f[2] = {0.f, 0.f};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int row = m * 16 + g + 8 * h;
+          at[h] = row < count ? tile.rows[row] : -1;
+          if (at[h] >= 0 && id >= 0) f[h] = factor[at[h]];
+#pragma unroll
+          for (int p = 0; p < 2; ++p)
+            if (base && at[h] >= 0 && c0 + q * 16 + p * 8 < N) old[h][p] = ld8_stream(base + at[h] * ld_b + c0 + q * 16 + p * 8);
+        }
         float acc[8][4];
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
         if (id >= 0) {
-          for (int c = 0; c < chunks; ++c) {
-            const uint4 big = frag[((m * chunks + c) * 32 + lane) * 2], rest = frag[((m * chunks + c) * 32 + lane) * 2 + 1];
-            const int r = c * 16 + q * 4;
+          for (int first = 0; first < chunks; first += CH) {
+            uint4 v[CH][2];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int col = c0 + (g >> 1) * 16 + 2 * i + (g & 1);
-              uint2 w = make_uint2(0, 0);
-              if (col < N && r < R) w = *reinterpret_cast<const uint2*>(bw + (int64_t)col * R + r);
-              mma16816<E>(acc[i], big.x, big.y, big.z, big.w, w.x, w.y);
-              mma16816<E>(acc[i], rest.x, rest.y, rest.z, rest.w, w.x, w.y);
+            for (int c = 0; c < CH; ++c)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                v[c][h] = make_uint4(0, 0, 0, 0);
+                if (at[h] >= 0 && first + c < chunks) v[c][h] = vq[(at[h] * chunks + first + c) * 4 + q];
+              }
+            if (!once) weights(first);
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+              if (first + c >= chunks) break;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                mma16816<E>(acc[i], v[c][0].x, v[c][1].x, v[c][0].y, v[c][1].y, w[c][i].x, w[c][i].y);
+                mma16816<E>(acc[i], v[c][0].z, v[c][1].z, v[c][0].w, v[c][1].w, w[c][i].x, w[c][i].y);
+              }
             }
           }
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int row = m * 16 + g + 8 * h;
-          if (row >= count) continue;
-          const int64_t t = t0 + tile.rows[row];
-          const float f = id >= 0 ? factor[row] : 0.f;
+          if (at[h] < 0) continue;
 #pragma unroll
           for (int p = 0; p < 2; ++p) {
             const int col = c0 + q * 16 + p * 8;
             if (col >= N) break;
             Vec8 o = zero8();
-            if (base) o = unpack(ld8_stream(base + t * ld_b + col));
+            if (base) o = unpack(old[h][p]);
             if (id >= 0) {
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                o.p[e].x = fmaf(f, acc[p * 4 + e][2 * h], o.p[e].x);
-                o.p[e].y = fmaf(f, acc[p * 4 + e][2 * h + 1], o.p[e].y);
+                o.p[e].x = fmaf(f[h], acc[p * 4 + e][2 * h], o.p[e].x);
+                o.p[e].y = fmaf(f[h], acc[p * 4 + e][2 * h + 1], o.p[e].y);
               }
             }
-            st8_stream(out + t * ld_o + col, pack<E>(o));
+            st8_stream(out + at[h] * ld_o + col, pack<E>(o));
           }
         }
       }
     }
-    __syncthreads();
   }
 }
 
-// Parts of H for the first launch: enough CTAs for a few tokens, at least 128 columns each.
-constexpr int kMostParts = 16, kWantCtas = 4 * 152;
-static int lora_parts(int64_t T, int H) {
-  const int64_t tiles = (T + kTok - 1) / kTok, want = (kWantCtas + tiles - 1) / tiles;
-  int most = (H + 127) / 128;
-  if (most > kMostParts) most = kMostParts;
-  return (int)(want < most ? want : most);
+// ------------------------------------------------------------------- host --
+// Workspace: v, factors, and the plan (order, units, units made per run), each from a
+// multiple of 256 bytes.
+struct LoraSpace {
+  size_t factor, order, units, made, bytes;
+};
+static LoraSpace lora_space(int64_t T, int R) {
+  const auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+  const size_t chunks = (R + 15) / 16, t = (size_t)T;
+  LoraSpace s;
+  s.factor = up(t * chunks * 64);
+  s.order = s.factor + up(t * 4);
+  s.units = s.order + up(t * 4);
+  s.made = s.units + up(t * sizeof(Unit));
+  s.bytes = s.made + up((t + kRun - 1) / kRun * 4);
+  return s;
 }
-// CTAs that share a tile's adapters: many where there are few tiles.
-static int lora_sharers(int64_t T, int n) {
-  const int64_t tiles = (T + kTok - 1) / kTok;
-  int64_t most = n + 1 < kTok ? n + 1 : kTok;
-  if (T < most) most = T;
-  const int64_t want = (152 + tiles - 1) / tiles;
-  return (int)(want < most ? want : most);
+
+template <typename... Params, typename... Args>
+static cudaError_t launch_cluster_z(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = grid.z;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+  if (e != cudaSuccess) cudaGetLastError();  // it is this call's, not the next one's
+  return e;
+}
+
+template <typename E, int NT>
+static cudaError_t shrink_launch(dim3 grid, const void* x, int64_t ld_x, const void* a, const int* index, const float* scale,
+                                 const LoraPlan& plan, int64_t T, int H, int R, int n, int slice, void* vq, float* factor,
+                                 cudaStream_t s) {
+  static SmemGrant grant;
+  const size_t smem = shrink_smem<NT>(R);
+  cudaError_t e = allow_smem(grant, (const void*)lora_shrink_kernel<E, NT>, smem);
+  if (e != cudaSuccess) return e;
+  return launch_cluster_z(lora_shrink_kernel<E, NT>, grid, dim3(128), smem, s, static_cast<const E*>(x), ld_x, static_cast<const E*>(a),
+                          index, scale, plan, T, H, R, n, slice, static_cast<uint4*>(vq), factor);
 }
 
 template <typename E>
 static cudaError_t lora_launch(const void* x, int64_t ld_x, const void* a, const void* b, const int* index, const float* scale,
                                int64_t T, int H, int N, int R, int n, const void* base, int64_t ld_b, void* out, int64_t ld_o,
                                void* ws, cudaStream_t s) {
-  const unsigned tiles = (unsigned)((T + kTok - 1) / kTok), share = (unsigned)lora_sharers(T, n);
-  int parts = lora_parts(T, H);
+  const LoraSpace space = lora_space(T, R);
+  char* w = static_cast<char*>(ws);
+  float* factor = reinterpret_cast<float*>(w + space.factor);
+  LoraPlan plan = {};
+  int64_t units, busy;  // CTAs along x, and how many of them have work
+  cudaError_t e;
+  if (T <= kTok) {
+    units = busy = T < n + 1 ? T : n + 1;
+  } else {
+    int* order = reinterpret_cast<int*>(w + space.order);
+    Unit* table = reinterpret_cast<Unit*>(w + space.units);
+    int* made = reinterpret_cast<int*>(w + space.made);
+    const int64_t runs = (T + kRun - 1) / kRun, tokens = T < kRun ? T : kRun;
+    // a run's units: its tokens by 64, and one more for each adapter
+    const int64_t most = tokens / kTok + (n + 1 < tokens ? n + 1 : tokens);
+    plan = {order, table, made, (int)(most < tokens ? most : tokens)};
+    units = runs * plan.most;
+    busy = T / kTok + runs * (n < 4 ? n : 4);
+    e = launch_pdl(lora_plan_kernel, dim3((unsigned)runs), dim3(kRun), 0, s, index, T, n, order, table, made);
+    if (e != cudaSuccess) return e;
+  }
+  // parts of H: enough CTAs for a few tokens, at least 128 columns each
+  int parts = 1;
+  while (parts < kMostParts && busy * parts < 304 && H / (2 * parts) >= 128) parts *= 2;
   const int slice = ((H + parts - 1) / parts + 31) / 32 * 32;
-  parts = (H + slice - 1) / slice;
-  auto k = R <= 8 ? lora_shrink_kernel<E, 1> : R <= 16 ? lora_shrink_kernel<E, 2> : R <= 32 ? lora_shrink_kernel<E, 4> : lora_shrink_kernel<E, 8>;
-  float* v = static_cast<float*>(ws);
-  k<<<dim3(tiles, share, parts), 128, 0, s>>>(static_cast<const E*>(x), ld_x, static_cast<const E*>(a), index, T, H, R, n, slice, v);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  const int chunks = (R + 15) / 16;
-  const size_t smem = (size_t)(kTok / 16) * chunks * 1024 + (size_t)kTok * (chunks * 16 + 4) * 4;
-  static SmemGrant grant;
-  e = allow_smem(grant, (const void*)lora_expand_kernel<E>, smem);
+  const dim3 grid((unsigned)units, 1, parts);
+  e = R <= 8    ? shrink_launch<E, 1>(grid, x, ld_x, a, index, scale, plan, T, H, R, n, slice, w, factor, s)
+      : R <= 16 ? shrink_launch<E, 2>(grid, x, ld_x, a, index, scale, plan, T, H, R, n, slice, w, factor, s)
+      : R <= 32 ? shrink_launch<E, 4>(grid, x, ld_x, a, index, scale, plan, T, H, R, n, slice, w, factor, s)
+                : shrink_launch<E, 8>(grid, x, ld_x, a, index, scale, plan, T, H, R, n, slice, w, factor, s);
   if (e != cudaSuccess) return e;
   const int64_t blocks = (N + 255) / 256;
-  int64_t wide = (8 * 152 + (int64_t)tiles * share - 1) / ((int64_t)tiles * share);
+  int64_t wide = (6 * 152 + busy - 1) / busy;
   if (wide > blocks) wide = blocks;
-  return launch_pdl(lora_expand_kernel<E>, dim3(tiles, share, (unsigned)wide), dim3(128), smem, s, v, parts, static_cast<const E*>(b), index,
-                    scale, T, N, R, n, static_cast<const E*>(base), ld_b, static_cast<E*>(out), ld_o);
+  auto expand = R <= 16 ? lora_expand_kernel<E, 1> : R <= 32 ? lora_expand_kernel<E, 2> : lora_expand_kernel<E, 4>;
+  return launch_pdl(expand, dim3((unsigned)units, 1, (unsigned)wide), dim3(128), 0, s, static_cast<const uint4*>(ws), factor,
+                    static_cast<const E*>(b), index, plan, T, N, R, n, static_cast<const E*>(base), ld_b, static_cast<E*>(out), ld_o);
 }
 
 }  // namespace mhc
 
-extern "C" size_t mhc_lora_workspace_bytes(int64_t T, int R) {
-  using namespace mhc;
-  if (T <= 0 || R <= 0) return 0;
-  // parts * T at most: parts is at most kMostParts, and below kWantCtas / tiles + 1
-  const int64_t few = kMostParts * T, many = (int64_t)kWantCtas * kTok + T;
-  return (size_t)(few < many ? few : many) * R * 4;
-}
+extern "C" size_t mhc_lora_workspace_bytes(int64_t T, int R) { return T > 0 && R > 0 ? mhc::lora_space(T, R).bytes : 0; }
 
 extern "C" int mhc_lora(const void* x, int64_t ld_x, const void* a, const void* b, const int32_t* index, const float* scale,
                         int64_t T, int H, int N, int R, int n, mhc_dtype dtype, const void* base, int64_t ld_base, void* out,
@@ -320,8 +582,8 @@ extern "C" int mhc_lora(const void* x, int64_t ld_x, const void* a, const void* 
   using namespace mhc;
   if (dtype != MHC_DT_BF16 && dtype != MHC_DT_F16) return ops_fail(MHC_ERR_CONFIG, "dtype must be bf16 or fp16");
   if (T < 0 || T > (1 << 30) || H <= 0 || H % 8 != 0 || H > (1 << 20) || N <= 0 || N % 8 != 0 || N > (1 << 20) || R <= 0 ||
-      R % 8 != 0 || R > 256 || n < 0)
-    return ops_fail(MHC_ERR_SHAPE, "need 0 <= T <= 2^30, H and N (at most 2^20) and R (at most 256) positive multiples of 8, n >= 0");
+      R % 8 != 0 || R > 256 || n < 0 || n > (1 << 20))
+    return ops_fail(MHC_ERR_SHAPE, "need 0 <= T <= 2^30, H and N (at most 2^20) and R (at most 256) positive multiples of 8, 0 <= n <= 2^20");
   if (ld_x < H || ld_x % 8 != 0 || ld_out < N || ld_out % 8 != 0 || (base && (ld_base < N || ld_base % 8 != 0)))
     return ops_fail(MHC_ERR_SHAPE, "row strides must be multiples of 8, at least the row");
   if (T == 0) return MHC_OK;

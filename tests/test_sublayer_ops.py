@@ -381,3 +381,20 @@ def test_glu_of_a_few_tokens_repeats_bit_for_bit():
         h = torch.empty_like(want)
         B.mhc_glu(x, w, h, ws)
         assert torch.equal(h, want)
+
+
+@pytest.mark.parametrize("T,H,N,rank,n,order", [(65, 64, 72, 8, 100, "any"), (1024, 72, 8, 16, 3, "any"), (1025, 40, 64, 8, 2, "one"),
+                                                (2100, 64, 136, 24, 600, "any"), (3000, 136, 64, 40, 5, "runs"), (2048, 8, 8, 8, 1, "any")])
+def test_lora_of_many_tokens(T, H, N, rank, n, order):
+    x, a, b, index, scale, base = lora_inputs(T, H, N, rank, n, BF16, order)
+    out = torch.full((T, N), 7.0, dtype=BF16, device="cuda")
+    ws = torch.full((B.mhc_lora_workspace_bytes(T, rank),), 0xFF, dtype=torch.uint8, device="cuda")
+    B.mhc_lora(dev(x), dev(a), dev(b), dev(index), out, ws, scale=dev(scale), base=dev(base))
+    some = torch.cat([torch.arange(min(T, 70)), torch.randint(0, T, (150,), generator=gen(1)), torch.arange(T - 40, T)]).unique()
+    ref, terms = R.lora(x[some], a, b, index[some], scale, base[some])
+    block_case.check(out[some.cuda()], ref, terms, n=1, what="lora")
+    # every token, against the same call token by token in other company
+    p = torch.randperm(T, generator=gen(2)).cuda()
+    moved = torch.empty_like(out)
+    B.mhc_lora(dev(x)[p], dev(a), dev(b), dev(index)[p], moved, ws, scale=dev(scale), base=dev(base)[p])
+    assert bool(((moved.double() - out[p].double()).abs() <= 2.0 ** -7 * out[p].double().abs() + 1e-4).all())

@@ -130,7 +130,7 @@ LORA = dict(x=A, ld_x=64, a=A + STEP, b=A + 2 * STEP, index=A + 3 * STEP, scale=
     (dict(dtype=2), -10), (dict(T=-1), -2), (dict(H=4), -2), (dict(N=12), -2), (dict(R=0), -2), (dict(R=12), -2), (dict(R=264), -2),
     (dict(n=-1), -2), (dict(ld_x=60), -2), (dict(ld_base=120), -2), (dict(ld_out=129), -2), (dict(x=None), -1), (dict(a=None), -1),
     (dict(b=None), -1), (dict(index=None), -1), (dict(out=None), -1), (dict(x=A + 8), -3), (dict(b=A + 2 * STEP + 4), -3),
-    (dict(index=A + 3 * STEP + 2), -3), (dict(scale=A + 4 * STEP + 1), -3), (dict(ws=None), -5), (dict(ws_bytes=4095), -5),
+    (dict(index=A + 3 * STEP + 2), -3), (dict(scale=A + 4 * STEP + 1), -3), (dict(ws=None), -5), (dict(ws_bytes=100), -5), (dict(n=2 ** 21), -2),
     (dict(out=A), -9), (dict(out=A + 2 * STEP), -9), (dict(out=A + 5 * STEP + 16), -9), (dict(out=A + 5 * STEP, ld_out=136), -9),
     (dict(ws=A + 5 * STEP), -9), (dict(ws=A + 6 * STEP), -9), (dict(ws=A + 3 * STEP), -9), (dict(T=0, x=None, out=None, ws=None), 0)])
 def test_lora_refusals(L, over, code):
@@ -139,7 +139,7 @@ def test_lora_refusals(L, over, code):
 
 def test_lora_workspace_grows(L):
     sizes = [L.mhc_lora_workspace_bytes(t, 16) for t in (0, 1, 64, 2432, 2500, 40000, 10 ** 6)]
-    assert sizes == sorted(sizes) and sizes[1] == 16 * 16 * 4 and sizes[0] == 0
+    assert sizes == sorted(sizes) and sizes[0] == 0 and sizes[-1] >= 10 ** 6 * 64
 
 
 def test_lora_reference_by_hand():
