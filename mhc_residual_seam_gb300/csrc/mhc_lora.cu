@@ -197,7 +197,8 @@ __device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uin
 }
 
 // Shared memory of a shrink CTA: a ring of three steps of 64 tokens, and the sums [64, R
-// rounded up to 16, plus 4], which take the ring's place where one pass makes the whole rank.
+// rounded up to 16, plus 4], which take the ring's place (a copy of each warp) where one pass
+// makes the whole rank.
 template <int NT>
 __host__ __device__ constexpr int ring_bytes() {
   return 3 * (8 + NT) * 2048;
@@ -205,8 +206,8 @@ __host__ __device__ constexpr int ring_bytes() {
 __host__ __device__ constexpr int sums_stride(int R) { return (R + 15) / 16 * 16 + 4; }
 template <int NT>
 __host__ __device__ constexpr size_t shrink_smem(int R) {
-  return R <= NT * 8 ? ((size_t)ring_bytes<NT>() > (size_t)kTok * sums_stride(R) * 4 ? ring_bytes<NT>() : (size_t)kTok * sums_stride(R) * 4)
-                     : ring_bytes<NT>() + (size_t)kTok * sums_stride(R) * 4;
+  const size_t sums = (size_t)kTok * sums_stride(R) * 4, ring = ring_bytes<NT>();
+  return R > NT * 8 ? ring + sums : ring > 4 * sums ? ring : 4 * sums;
 }
 
 // The sums of 16 MG tokens over columns [k0, k1), for a warp that takes every fourth 32
@@ -223,16 +224,26 @@ __device__ __forceinline__ void shrink_sums(float (&acc)[MG][NT][4], const E* x,
 #pragma unroll
   for (int i = 0; i < 2 * MG; ++i) {
     const int r = i * 8 + g;
-    px[i] = r < count ? x + rows[r] * ld_x + q * 8 : nullptr;
+    px[i] = x + rows[r < count ? r : 0] * ld_x + q * 8;  // (what rows past the last give is not used)
   }
-  const E* pa = a + (int64_t)g * H + q * 8;
+  const E* pa = a + (int64_t)min(g, left - 1) * H + q * 8;
+  const int64_t row8 = (int64_t)8 * H;
   auto fetch = [&](int step, int k) {
     const uint32_t at = ring + step * kPieces * 2048 + threadIdx.x * 16;
-    const bool in = k + q * 8 < k1;
+    if (k + 32 <= k1) {
 #pragma unroll
-    for (int i = 0; i < 2 * MG; ++i) cp_async16_or_zero(at + i * 2048, px[i] + k, x, in && px[i]);
+      for (int i = 0; i < 2 * MG; ++i) cp_async16(at + i * 2048, px[i] + k);
 #pragma unroll
-    for (int i = 0; i < NT; ++i) cp_async16_or_zero(at + (2 * MG + i) * 2048, pa + (int64_t)i * 8 * H + k, x, in && i * 8 + g < left);
+      for (int i = 0; i < NT; ++i)
+        if (i * 8 < left) cp_async16(at + (2 * MG + i) * 2048, pa + i * row8 + k);
+    } else {  // the last columns: zeros past the end
+      const bool in = k + q * 8 < k1;
+#pragma unroll
+      for (int i = 0; i < 2 * MG; ++i) cp_async16_or_zero(at + i * 2048, px[i] + k, x, in);
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+        if (i * 8 < left) cp_async16_or_zero(at + (2 * MG + i) * 2048, pa + i * row8 + k, x, in);
+    }
   };
   const int first = k0 + warp * 32;
   int ahead = first, step = 0, filled = 0;
@@ -310,8 +321,11 @@ __global__ void __launch_bounds__(128) lora_shrink_kernel(const E* __restrict__ 
           for (int i = 0; i < NT; ++i) acc[m][i][0] = acc[m][i][1] = acc[m][i][2] = acc[m][i][3] = 0.f;
         shrink_sums<E, NT, MG>(acc, x, ld_x, tile.rows, count, ar, R - r0, H, k0, k1, smem_of(smem));
         __syncthreads();  // (the sums may take the ring's place)
-        for (int p = 0; p < 4; ++p) {  // warp after warp
-          if (warp == p) {
+        const bool apart = R <= NT * 8;  // room for a copy of each warp
+#pragma unroll 1
+        for (int p = 0; p < (apart ? 1 : 4); ++p) {  // otherwise warp after warp
+          if (apart || warp == p) {
+            float* mine = sums + (apart ? warp * kTok * stride : 0);
 #pragma unroll
             for (int m = 0; m < MG; ++m)
 #pragma unroll
@@ -320,12 +334,23 @@ __global__ void __launch_bounds__(128) lora_shrink_kernel(const E* __restrict__ 
                 for (int h = 0; h < 2; ++h) {
                   const int c = r0 + i * 8 + 2 * q;
                   if (c >= R) continue;
-                  float2* s = reinterpret_cast<float2*>(sums + (m * 16 + g + 8 * h) * stride + c);
-                  const float2 o = p ? *s : make_float2(0.f, 0.f);
-                  *s = make_float2(o.x + acc[m][i][2 * h], o.y + acc[m][i][2 * h + 1]);
+                  float2* o = reinterpret_cast<float2*>(mine + (m * 16 + g + 8 * h) * stride + c);
+                  float2 z = make_float2(acc[m][i][2 * h], acc[m][i][2 * h + 1]);
+                  if (!apart && p) z = make_float2(o->x + z.x, o->y + z.y);
+                  *o = z;
                 }
           }
           __syncthreads();
+        }
+        if (apart) {
+          for (int i = threadIdx.x; i < count * stride / 4; i += 128) {
+            float4* o = reinterpret_cast<float4*>(sums) + i;
+            float4 z[4];
+#pragma unroll
+            for (int p = 0; p < 4; ++p) z[p] = o[p * (kTok * stride / 4)];
+            *o = make_float4(z[0].x + z[1].x + z[2].x + z[3].x, z[0].y + z[1].y + z[2].y + z[3].y, z[0].z + z[1].z + z[2].z + z[3].z,
+                             z[0].w + z[1].w + z[2].w + z[3].w);
+          }
         }
       };
       if (count <= 16) go(std::integral_constant<int, 1>());
@@ -384,97 +409,147 @@ __global__ void __launch_bounds__(128) lora_shrink_kernel(const E* __restrict__ 
   }
 }
 
-// out = base + B v for the units, 64 columns a warp at a time.  A warp keeps the weights of
-// its columns (up to 16 CH of the rank) in registers for all the tokens.
+// 64 columns from c0 of a unit's rows, by one warp; lane_w points at the lane's first
+// weights, rows at the unit's tokens.  Column of fragment column 2 p + e of product i:
+// 16 p + 2 i + e, so a thread's 16 results of a row are adjacent.
+//
+// FULL: all 64 columns exist and the rank is 16 CH: nothing is tested but the stores, rows
+// past the unit's last stand in as its first.  The warp keeps the weights of its columns in
+// registers for all the tokens, and fetches a group's base and v while the one before it is
+// multiplied.
 template <typename E, int CH>
-__global__ void __launch_bounds__(128, 3) lora_expand_kernel(const uint4* vq, const float* factor, const E* __restrict__ b,
+struct ExpandGroup {
+  uint4 v[CH][2];
+  Raw8<E> old[2][2];
+  float f[2];
+};
+template <typename E, int CH, bool BASE>
+__device__ __forceinline__ void expand_fetch(ExpandGroup<E, CH>& x, const uint4* vq, const float* factor, const E* base, int64_t ld_b,
+                                             const int* rows, int count, int m, int col, int g, int q) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int row = m * 16 + g + 8 * h;
+    const int64_t t = rows[row < count ? row : 0];
+    x.f[h] = factor[t];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) x.v[c][h] = vq[(t * CH + c) * 4 + q];
+    if constexpr (BASE) {
+#pragma unroll
+      for (int p = 0; p < 2; ++p) x.old[h][p] = ld8_stream(base + t * ld_b + col + p * 8);
+    }
+  }
+}
+template <typename E, int CH, bool BASE>
+__device__ __forceinline__ void expand_full(const uint4* vq, const float* factor, const E* lane_w, int R, const E* base, int64_t ld_b,
+                                            E* out, int64_t ld_o, const int* rows, int count, int c0, int g, int q) {
+  uint2 w[CH][8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int c = 0; c < CH; ++c) w[c][i] = *reinterpret_cast<const uint2*>(lane_w + 2 * i * R + c * 16);
+  const int groups = (count + 15) / 16, col = c0 + q * 16;
+  ExpandGroup<E, CH> x, ahead;
+  expand_fetch<E, CH, BASE>(x, vq, factor, base, ld_b, rows, count, 0, col, g, q);
+  for (int m = 0; m < groups; ++m) {
+    if (m + 1 < groups) expand_fetch<E, CH, BASE>(ahead, vq, factor, base, ld_b, rows, count, m + 1, col, g, q);
+    float acc[8][4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) mma16816<E>(acc[i], x.v[c][0].x, x.v[c][1].x, x.v[c][0].y, x.v[c][1].y, w[c][i].x, w[c][i].y);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) mma16816<E>(acc[i], x.v[c][0].z, x.v[c][1].z, x.v[c][0].w, x.v[c][1].w, w[c][i].x, w[c][i].y);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int row = m * 16 + g + 8 * h;
+      E* o = out + (int64_t)rows[row < count ? row : 0] * ld_o + col;
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        Vec8 y = zero8();
+        if constexpr (BASE) y = unpack(x.old[h][p]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          y.p[e] = __ffma2_rn(splat(x.f[h]), make_float2(acc[p * 4 + e][2 * h], acc[p * 4 + e][2 * h + 1]), y.p[e]);
+        if (row < count) st8_stream(o + p * 8, pack<E>(y));
+      }
+    }
+    x = ahead;
+  }
+}
+// The same with every test, for what is left.
+template <typename E>
+__device__ __forceinline__ void expand_any(const uint4* vq, const float* factor, const E* lane_w, int id, int N, int R, const E* base,
+                                           int64_t ld_b, E* out, int64_t ld_o, const int* rows, int count, int c0, int g, int q) {
+  const int chunks = (R + 15) / 16;
+  for (int m = 0; m * 16 < count; ++m) {
+    int64_t at[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) at[h] = m * 16 + g + 8 * h < count ? rows[m * 16 + g + 8 * h] : -1;
+    float acc[8][4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+    for (int c = 0; id >= 0 && c < chunks; ++c) {
+      uint4 v[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) v[h] = at[h] >= 0 ? vq[(at[h] * chunks + c) * 4 + q] : make_uint4(0, 0, 0, 0);
+      uint2 w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int col = c0 + (g >> 1) * 16 + 2 * i + (g & 1);
+        w[i] = make_uint2(0, 0);
+        if (col < N && c * 16 + q * 4 < R) w[i] = *reinterpret_cast<const uint2*>(lane_w + 2 * i * R + c * 16);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        mma16816<E>(acc[i], v[0].x, v[1].x, v[0].y, v[1].y, w[i].x, w[i].y);
+        mma16816<E>(acc[i], v[0].z, v[1].z, v[0].w, v[1].w, w[i].x, w[i].y);
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (at[h] < 0) continue;
+      const float f = id >= 0 ? factor[at[h]] : 0.f;
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const int col = c0 + q * 16 + p * 8;
+        if (col >= N) break;
+        Vec8 o = zero8();
+        if (base) o = unpack(ld8_stream(base + at[h] * ld_b + col));
+        if (id >= 0) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            o.p[e].x = fmaf(f, acc[p * 4 + e][2 * h], o.p[e].x);
+            o.p[e].y = fmaf(f, acc[p * 4 + e][2 * h + 1], o.p[e].y);
+          }
+        }
+        st8_stream(out + at[h] * ld_o + col, pack<E>(o));
+      }
+    }
+  }
+}
+
+// out = base + B v for the units, 64 columns a warp at a time.
+template <typename E, int CH, bool BASE>
+__global__ void __launch_bounds__(128, CH == 4 ? 3 : 4) lora_expand_kernel(const uint4* vq, const float* factor, const E* __restrict__ b,
                                                              const int* __restrict__ index, const LoraPlan plan, int64_t T, int N,
                                                              int R, int n, const E* base, int64_t ld_b, E* out, int64_t ld_o) {
   __shared__ TileTokens tile;
-  const int chunks = (R + 15) / 16;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane & 3, g = lane >> 2;
   pdl_wait();
   Units units(tile, plan, index, T, n);
   int id, count;
   while (units.next(id, count)) {
     if (id < 0 && base == out) continue;
-    const int groups = (count + 15) / 16;
-    // column of fragment column 2 p + e of product i: 16 p + 2 i + e, so a thread's 16 results of a row are adjacent
     const E* bw = b + (int64_t)max(id, 0) * N * R;
     for (int c0 = (blockIdx.z * 4 + warp) * 64; c0 < N; c0 += gridDim.z * 256) {
-      uint2 w[CH][8];
-      auto weights = [&](int first) {
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          const int r = (first + c) * 16 + q * 4;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int col = c0 + (g >> 1) * 16 + 2 * i + (g & 1);
-            w[c][i] = make_uint2(0, 0);
-            if (col < N && r < R) w[c][i] = *reinterpret_cast<const uint2*>(bw + (int64_t)col * R + r);
-          }
-        }
-      };
-      const bool once = chunks <= CH;
-      if (id >= 0 && once) weights(0);
-      for (int m = 0; m < groups; ++m) {
-        Raw8<E> old[2][2];
-        int64_t at[2];
-        float f[2] = {0.f, 0.f};
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int row = m * 16 + g + 8 * h;
-          at[h] = row < count ? tile.rows[row] : -1;
-          if (at[h] >= 0 && id >= 0) f[h] = factor[at[h]];
-#pragma unroll
-          for (int p = 0; p < 2; ++p)
-            if (base && at[h] >= 0 && c0 + q * 16 + p * 8 < N) old[h][p] = ld8_stream(base + at[h] * ld_b + c0 + q * 16 + p * 8);
-        }
-        float acc[8][4];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-        if (id >= 0) {
-          for (int first = 0; first < chunks; first += CH) {
-            uint4 v[CH][2];
-#pragma unroll
-            for (int c = 0; c < CH; ++c)
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                v[c][h] = make_uint4(0, 0, 0, 0);
-                if (at[h] >= 0 && first + c < chunks) v[c][h] = vq[(at[h] * chunks + first + c) * 4 + q];
-              }
-            if (!once) weights(first);
-#pragma unroll
-            for (int c = 0; c < CH; ++c) {
-              if (first + c >= chunks) break;
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                mma16816<E>(acc[i], v[c][0].x, v[c][1].x, v[c][0].y, v[c][1].y, w[c][i].x, w[c][i].y);
-                mma16816<E>(acc[i], v[c][0].z, v[c][1].z, v[c][0].w, v[c][1].w, w[c][i].x, w[c][i].y);
-              }
-            }
-          }
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (at[h] < 0) continue;
-#pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            const int col = c0 + q * 16 + p * 8;
-            if (col >= N) break;
-            Vec8 o = zero8();
-            if (base) o = unpack(old[h][p]);
-            if (id >= 0) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                o.p[e].x = fmaf(f[h], acc[p * 4 + e][2 * h], o.p[e].x);
-                o.p[e].y = fmaf(f[h], acc[p * 4 + e][2 * h + 1], o.p[e].y);
-              }
-            }
-            st8_stream(out + at[h] * ld_o + col, pack<E>(o));
-          }
-        }
-      }
+      const E* lane_w = bw + ((int64_t)c0 + (g >> 1) * 16 + (g & 1)) * R + q * 4;
+      if (id >= 0 && c0 + 64 <= N && R == CH * 16)
+        expand_full<E, CH, BASE>(vq, factor, lane_w, R, base, ld_b, out, ld_o, tile.rows, count, c0, g, q);
+      else
+        expand_any<E>(vq, factor, lane_w, id, N, R, base, ld_b, out, ld_o, tile.rows, count, c0, g, q);
     }
   }
 }
@@ -567,7 +642,9 @@ static cudaError_t lora_launch(const void* x, int64_t ld_x, const void* a, const
   const int64_t blocks = (N + 255) / 256;
   int64_t wide = (6 * 152 + busy - 1) / busy;
   if (wide > blocks) wide = blocks;
-  auto expand = R <= 16 ? lora_expand_kernel<E, 1> : R <= 32 ? lora_expand_kernel<E, 2> : lora_expand_kernel<E, 4>;
+  auto expand = R <= 16   ? base ? lora_expand_kernel<E, 1, true> : lora_expand_kernel<E, 1, false>
+                : R <= 32 ? base ? lora_expand_kernel<E, 2, true> : lora_expand_kernel<E, 2, false>
+                          : base ? lora_expand_kernel<E, 4, true> : lora_expand_kernel<E, 4, false>;
   return launch_pdl(expand, dim3((unsigned)units, 1, (unsigned)wide), dim3(128), 0, s, static_cast<const uint4*>(ws), factor,
                     static_cast<const E*>(b), index, plan, T, N, R, n, static_cast<const E*>(base), ld_b, static_cast<E*>(out), ld_o);
 }
