@@ -25,6 +25,10 @@ namespace mhc {
 constexpr int kTok = 64;     // most tokens of a unit
 constexpr int kRun = 1024;   // tokens sorted together
 constexpr int kMostParts = 8;
+#ifndef KEXP
+#define KEXP 10
+#endif
+constexpr int kExpandCtas = KEXP;
 
 struct Unit {
   int adapter;  // -1: tokens without one
@@ -409,147 +413,145 @@ __global__ void __launch_bounds__(128) lora_shrink_kernel(const E* __restrict__ 
   }
 }
 
-// 64 columns from c0 of a unit's rows, by one warp; lane_w points at the lane's first
-// weights, rows at the unit's tokens.  Column of fragment column 2 p + e of product i:
-// 16 p + 2 i + e, so a thread's 16 results of a row are adjacent.
+// 32 columns from c0 of a unit's rows, by one warp.  `frag` holds v as the products take
+// it, [16 tokens][16 of the rank][lane]: four registers of roundings, four of rests.
+// lane_w points at the lane's first weights; column of fragment column 2 p + e of product
+// i: 8 p + 2 i + e, so a thread's eight results of a row are adjacent.
 //
-// FULL: all 64 columns exist and the rank is 16 CH: nothing is tested but the stores, rows
-// past the unit's last stand in as its first.  The warp keeps the weights of its columns in
-// registers for all the tokens, and fetches a group's base and v while the one before it is
+// With all 32 columns and a rank of 16 CH nothing is tested but the stores, and rows past
+// the unit's last stand in as its first.  The warp keeps the weights of its columns in
+// registers for all the tokens and fetches a group's base while the one before it is
 // multiplied.
-template <typename E, int CH>
-struct ExpandGroup {
-  uint4 v[CH][2];
-  Raw8<E> old[2][2];
-  float f[2];
-};
 template <typename E, int CH, bool BASE>
-__device__ __forceinline__ void expand_fetch(ExpandGroup<E, CH>& x, const uint4* vq, const float* factor, const E* base, int64_t ld_b,
-                                             const int* rows, int count, int m, int col, int g, int q) {
+__device__ __forceinline__ void expand_full(const uint4* frag, const float* factor, const E* lane_w, int R, const E* base, int64_t ld_b,
+                                            E* out, int64_t ld_o, const int* rows, int count, int col, int lane) {
+  const int g = lane >> 2;
+  uint2 w[CH][4];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int row = m * 16 + g + 8 * h;
-    const int64_t t = rows[row < count ? row : 0];
-    x.f[h] = factor[t];
-#pragma unroll
-    for (int c = 0; c < CH; ++c) x.v[c][h] = vq[(t * CH + c) * 4 + q];
-    if constexpr (BASE) {
-#pragma unroll
-      for (int p = 0; p < 2; ++p) x.old[h][p] = ld8_stream(base + t * ld_b + col + p * 8);
-    }
-  }
-}
-template <typename E, int CH, bool BASE>
-__device__ __forceinline__ void expand_full(const uint4* vq, const float* factor, const E* lane_w, int R, const E* base, int64_t ld_b,
-                                            E* out, int64_t ld_o, const int* rows, int count, int c0, int g, int q) {
-  uint2 w[CH][8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
+  for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int c = 0; c < CH; ++c) w[c][i] = *reinterpret_cast<const uint2*>(lane_w + 2 * i * R + c * 16);
-  const int groups = (count + 15) / 16, col = c0 + q * 16;
-  ExpandGroup<E, CH> x, ahead;
-  expand_fetch<E, CH, BASE>(x, vq, factor, base, ld_b, rows, count, 0, col, g, q);
-  for (int m = 0; m < groups; ++m) {
-    if (m + 1 < groups) expand_fetch<E, CH, BASE>(ahead, vq, factor, base, ld_b, rows, count, m + 1, col, g, q);
-    float acc[8][4];
+  const int groups = (count + 15) / 16;
+  base += col;
+  out += col;
+  Raw8<E> old[2][2];
+  auto fetch = [&](Raw8<E>* o, int m) {
+    if constexpr (BASE) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+      for (int h = 0; h < 2; ++h) {
+        const int row = m * 16 + g + 8 * h;
+        o[h] = ld8_stream(base + rows[row < count ? row : 0] * ld_b);
+      }
+    }
+  };
+  auto group = [&](const Raw8<E>* o, int m) {
+    float acc[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+    const uint4* f = frag + (m * CH * 32 + lane) * 2;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
+      const uint4 big = f[c * 64], rest = f[c * 64 + 1];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) mma16816<E>(acc[i], x.v[c][0].x, x.v[c][1].x, x.v[c][0].y, x.v[c][1].y, w[c][i].x, w[c][i].y);
+      for (int i = 0; i < 4; ++i) mma16816<E>(acc[i], big.x, big.y, big.z, big.w, w[c][i].x, w[c][i].y);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) mma16816<E>(acc[i], x.v[c][0].z, x.v[c][1].z, x.v[c][0].w, x.v[c][1].w, w[c][i].x, w[c][i].y);
+      for (int i = 0; i < 4; ++i) mma16816<E>(acc[i], rest.x, rest.y, rest.z, rest.w, w[c][i].x, w[c][i].y);
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int row = m * 16 + g + 8 * h;
-      E* o = out + (int64_t)rows[row < count ? row : 0] * ld_o + col;
+      const float2 k = splat(factor[row]);
+      Vec8 y = zero8();
+      if constexpr (BASE) y = unpack(o[h]);
 #pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        Vec8 y = zero8();
-        if constexpr (BASE) y = unpack(x.old[h][p]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          y.p[e] = __ffma2_rn(splat(x.f[h]), make_float2(acc[p * 4 + e][2 * h], acc[p * 4 + e][2 * h + 1]), y.p[e]);
-        if (row < count) st8_stream(o + p * 8, pack<E>(y));
-      }
+      for (int e = 0; e < 4; ++e) y.p[e] = __ffma2_rn(k, make_float2(acc[e][2 * h], acc[e][2 * h + 1]), y.p[e]);
+      if (row < count) st8_stream(out + rows[row] * ld_o, pack<E>(y));
     }
-    x = ahead;
+  };
+  fetch(old[0], 0);
+  for (int m = 0; m < groups; m += 2) {
+    if (m + 1 < groups) fetch(old[1], m + 1);
+    group(old[0], m);
+    if (m + 1 < groups) {
+      if (m + 2 < groups) fetch(old[0], m + 2);
+      group(old[1], m + 1);
+    }
   }
 }
 // The same with every test, for what is left.
 template <typename E>
-__device__ __forceinline__ void expand_any(const uint4* vq, const float* factor, const E* lane_w, int id, int N, int R, const E* base,
-                                           int64_t ld_b, E* out, int64_t ld_o, const int* rows, int count, int c0, int g, int q) {
-  const int chunks = (R + 15) / 16;
+__device__ __forceinline__ void expand_any(const uint4* frag, const float* factor, const E* lane_w, int id, int N, int R, const E* base,
+                                           int64_t ld_b, E* out, int64_t ld_o, const int* rows, int count, int c0, int lane) {
+  const int chunks = (R + 15) / 16, g = lane >> 2, q = lane & 3, col = c0 + q * 8;
   for (int m = 0; m * 16 < count; ++m) {
-    int64_t at[2];
+    float acc[4][4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) at[h] = m * 16 + g + 8 * h < count ? rows[m * 16 + g + 8 * h] : -1;
-    float acc[8][4];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+    for (int i = 0; i < 4; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
     for (int c = 0; id >= 0 && c < chunks; ++c) {
-      uint4 v[2];
+      const uint4* f = frag + ((m * chunks + c) * 32 + lane) * 2;
+      const uint4 big = f[0], rest = f[1];
+      uint2 w[4];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) v[h] = at[h] >= 0 ? vq[(at[h] * chunks + c) * 4 + q] : make_uint4(0, 0, 0, 0);
-      uint2 w[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int col = c0 + (g >> 1) * 16 + 2 * i + (g & 1);
+      for (int i = 0; i < 4; ++i) {
         w[i] = make_uint2(0, 0);
-        if (col < N && c * 16 + q * 4 < R) w[i] = *reinterpret_cast<const uint2*>(lane_w + 2 * i * R + c * 16);
+        if (c0 + (g >> 1) * 8 + 2 * i + (g & 1) < N && c * 16 + q * 4 < R)
+          w[i] = *reinterpret_cast<const uint2*>(lane_w + 2 * i * R + c * 16);
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        mma16816<E>(acc[i], v[0].x, v[1].x, v[0].y, v[1].y, w[i].x, w[i].y);
-        mma16816<E>(acc[i], v[0].z, v[1].z, v[0].w, v[1].w, w[i].x, w[i].y);
+      for (int i = 0; i < 4; ++i) {
+        mma16816<E>(acc[i], big.x, big.y, big.z, big.w, w[i].x, w[i].y);
+        mma16816<E>(acc[i], rest.x, rest.y, rest.z, rest.w, w[i].x, w[i].y);
       }
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      if (at[h] < 0) continue;
-      const float f = id >= 0 ? factor[at[h]] : 0.f;
+      const int row = m * 16 + g + 8 * h;
+      if (row >= count || col >= N) continue;
+      const int64_t t = rows[row];
+      Vec8 o = zero8();
+      if (base) o = unpack(ld8_stream(base + t * ld_b + col));
+      if (id >= 0) {
 #pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        const int col = c0 + q * 16 + p * 8;
-        if (col >= N) break;
-        Vec8 o = zero8();
-        if (base) o = unpack(ld8_stream(base + at[h] * ld_b + col));
-        if (id >= 0) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            o.p[e].x = fmaf(f, acc[p * 4 + e][2 * h], o.p[e].x);
-            o.p[e].y = fmaf(f, acc[p * 4 + e][2 * h + 1], o.p[e].y);
-          }
-        }
-        st8_stream(out + at[h] * ld_o + col, pack<E>(o));
+        for (int e = 0; e < 4; ++e)
+          o.p[e] = __ffma2_rn(splat(factor[row]), make_float2(acc[e][2 * h], acc[e][2 * h + 1]), o.p[e]);
       }
+      st8_stream(out + t * ld_o + col, pack<E>(o));
     }
   }
 }
 
-// out = base + B v for the units, 64 columns a warp at a time.
+// out = base + B v for the units, 32 columns a warp at a time.
 template <typename E, int CH, bool BASE>
-__global__ void __launch_bounds__(128, CH == 4 ? 3 : 4) lora_expand_kernel(const uint4* vq, const float* factor, const E* __restrict__ b,
+__global__ void __launch_bounds__(128, 5) lora_expand_kernel(const uint4* vq, const float* factor, const E* __restrict__ b,
                                                              const int* __restrict__ index, const LoraPlan plan, int64_t T, int N,
                                                              int R, int n, const E* base, int64_t ld_b, E* out, int64_t ld_o) {
+  extern __shared__ uint4 frag[];
   __shared__ TileTokens tile;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane & 3, g = lane >> 2;
+  __shared__ float factors[kTok];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane & 3, g = lane >> 2, chunks = (R + 15) / 16;
   pdl_wait();
   Units units(tile, plan, index, T, n);
   int id, count;
   while (units.next(id, count)) {
     if (id < 0 && base == out) continue;
+    if (id >= 0) {
+      for (int i = threadIdx.x; i < (count + 15) / 16 * chunks * 32; i += 128) {
+        const int c = (i >> 5) % chunks, ra = (i >> 5) / chunks * 16 + g, rb = ra + 8;
+        const uint4 u = vq[((int64_t)tile.rows[ra < count ? ra : 0] * chunks + c) * 4 + q];
+        const uint4 v = vq[((int64_t)tile.rows[rb < count ? rb : 0] * chunks + c) * 4 + q];
+        frag[i * 2] = make_uint4(u.x, v.x, u.y, v.y);
+        frag[i * 2 + 1] = make_uint4(u.z, v.z, u.w, v.w);
+      }
+      if (threadIdx.x < kTok) factors[threadIdx.x] = factor[tile.rows[threadIdx.x < count ? threadIdx.x : 0]];
+      __syncthreads();
+    }
     const E* bw = b + (int64_t)max(id, 0) * N * R;
-    for (int c0 = (blockIdx.z * 4 + warp) * 64; c0 < N; c0 += gridDim.z * 256) {
-      const E* lane_w = bw + ((int64_t)c0 + (g >> 1) * 16 + (g & 1)) * R + q * 4;
-      if (id >= 0 && c0 + 64 <= N && R == CH * 16)
-        expand_full<E, CH, BASE>(vq, factor, lane_w, R, base, ld_b, out, ld_o, tile.rows, count, c0, g, q);
+    for (int c0 = (blockIdx.z * 4 + warp) * 32; c0 < N; c0 += gridDim.z * 128) {
+      const E* lane_w = bw + ((int64_t)c0 + (g >> 1) * 8 + (g & 1)) * R + q * 4;
+      if (id >= 0 && c0 + 32 <= N && R == CH * 16)
+        expand_full<E, CH, BASE>(frag, factors, lane_w, R, base, ld_b, out, ld_o, tile.rows, count, c0 + q * 8, lane);
       else
-        expand_any<E>(vq, factor, lane_w, id, N, R, base, ld_b, out, ld_o, tile.rows, count, c0, g, q);
+        expand_any<E>(frag, factors, lane_w, id, N, R, base, ld_b, out, ld_o, tile.rows, count, c0, lane);
     }
   }
 }
@@ -639,13 +641,20 @@ static cudaError_t lora_launch(const void* x, int64_t ld_x, const void* a, const
       : R <= 32 ? shrink_launch<E, 4>(grid, x, ld_x, a, index, scale, plan, T, H, R, n, slice, w, factor, s)
                 : shrink_launch<E, 8>(grid, x, ld_x, a, index, scale, plan, T, H, R, n, slice, w, factor, s);
   if (e != cudaSuccess) return e;
-  const int64_t blocks = (N + 255) / 256;
-  int64_t wide = (6 * 152 + busy - 1) / busy;
+  const int64_t blocks = (N + 127) / 128;
+  int64_t wide = (kExpandCtas * 152 + busy - 1) / busy;
   if (wide > blocks) wide = blocks;
-  auto expand = R <= 16   ? base ? lora_expand_kernel<E, 1, true> : lora_expand_kernel<E, 1, false>
-                : R <= 32 ? base ? lora_expand_kernel<E, 2, true> : lora_expand_kernel<E, 2, false>
-                          : base ? lora_expand_kernel<E, 4, true> : lora_expand_kernel<E, 4, false>;
-  return launch_pdl(expand, dim3((unsigned)units, 1, (unsigned)wide), dim3(128), 0, s, static_cast<const uint4*>(ws), factor,
+  const int64_t each = (blocks + wide - 1) / wide;  // column blocks of a CTA: as even as they can be
+  wide = (blocks + each - 1) / each;
+  const int which = (R <= 16 ? 0 : R <= 32 ? 1 : 2) + (base ? 3 : 0);
+  const decltype(&lora_expand_kernel<E, 1, true>) kernels[] = {lora_expand_kernel<E, 1, false>, lora_expand_kernel<E, 2, false>,
+                                                               lora_expand_kernel<E, 4, false>, lora_expand_kernel<E, 1, true>,
+                                                               lora_expand_kernel<E, 2, true>,  lora_expand_kernel<E, 4, true>};
+  static SmemGrant grants[6];
+  const size_t smem = (size_t)(kTok / 16) * ((R + 15) / 16) * 1024;
+  e = allow_smem(grants[which], (const void*)kernels[which], smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kernels[which], dim3((unsigned)units, 1, (unsigned)wide), dim3(128), smem, s, static_cast<const uint4*>(ws), factor,
                     static_cast<const E*>(b), index, plan, T, N, R, n, static_cast<const E*>(base), ld_b, static_cast<E*>(out), ld_o);
 }
 
