@@ -25,10 +25,7 @@ namespace mhc {
 constexpr int kTok = 64;     // most tokens of a unit
 constexpr int kRun = 1024;   // tokens sorted together
 constexpr int kMostParts = 8;
-#ifndef KEXP
-#define KEXP 10
-#endif
-constexpr int kExpandCtas = KEXP;
+constexpr int kExpandCtas = 5;
 
 struct Unit {
   int adapter;  // -1: tokens without one
@@ -40,7 +37,7 @@ struct LoraPlan {
   const int* order;   // sorted order -> token; NULL: units are found in the kernel
   const Unit* units;  // kRun per run of tokens
   const int* made;    // units of a run
-  int most;           // CTAs per run
+  int runs;
 };
 
 __device__ __forceinline__ int adapter_of(const int* index, int64_t t, int64_t T, int n) {
@@ -140,42 +137,45 @@ __device__ __forceinline__ void find_tokens(TileTokens& tile, int id, int id0, i
   if (id1 == id) tile.rows[__popc(b0) + __popc(b1 & below)] = lane + 32;
   if (lane == 0) tile.count = __popc(b0) + __popc(b1);
 }
-// The units of this CTA one after another: `next` is called by all threads and leaves the
-// tokens in tile.rows (a barrier before the rows are used, and one before the next call,
-// are part of it).
+// The units of this CTA, every gridDim.x-th, one after another: `next` is called by all
+// threads and leaves the tokens in tile.rows (a barrier before the rows are used, and one
+// before the next call, are part of it).
 struct Units {
   TileTokens& tile;
   const LoraPlan& plan;
-  int id0, id1, j, step;
-  bool left;
-  __device__ __forceinline__ Units(TileTokens& t, const LoraPlan& p, const int* index, int64_t T, int n) : tile(t), plan(p), left(true) {
+  int id0, id1;
+  int64_t at, before;  // the next unit; units of the runs before `run`
+  int run, made;
+  __device__ __forceinline__ Units(TileTokens& t, const LoraPlan& p, const int* index, int64_t T, int n)
+      : tile(t), plan(p), id0(0), id1(0), at(blockIdx.x), before(0), run(0), made(0) {
     const int lane = threadIdx.x & 31;
-    if (!plan.order) {
+    if (plan.order) {
+      made = plan.made[0];
+    } else {
       id0 = adapter_of(index, lane, T, n), id1 = adapter_of(index, lane + 32, T, n);
       if (threadIdx.x < 32) find_adapters(tile, id0, id1, lane);
-      __syncthreads();
-      j = blockIdx.x, step = gridDim.x;
     }
   }
   __device__ __forceinline__ bool next(int& adapter, int& count) {
     __syncthreads();
     if (plan.order) {
-      const int64_t run = blockIdx.x / plan.most;
-      const int u = blockIdx.x - (int)run * plan.most;
-      if (!left || u >= plan.made[run]) return false;
-      left = false;
-      const Unit unit = plan.units[run * kRun + u];
+      while (at >= before + made) {
+        if (++run >= plan.runs) return false;
+        before += made;
+        made = plan.made[run];
+      }
+      const Unit unit = plan.units[(int64_t)run * kRun + (at - before)];
       if (threadIdx.x < unit.count) tile.rows[threadIdx.x] = plan.order[unit.first + threadIdx.x];
       adapter = unit.adapter, count = unit.count;
       __syncthreads();
-      return true;
+    } else {
+      if (at >= tile.distinct) return false;
+      adapter = tile.firsts[at];
+      if (threadIdx.x < 32) find_tokens(tile, adapter, id0, id1, threadIdx.x);
+      __syncthreads();
+      count = tile.count;
     }
-    if (j >= tile.distinct) return false;
-    adapter = tile.firsts[j];
-    if (threadIdx.x < 32) find_tokens(tile, adapter, id0, id1, threadIdx.x);
-    __syncthreads();
-    count = tile.count;
-    j += step;
+    at += gridDim.x;
     return true;
   }
 };
@@ -185,7 +185,6 @@ struct Units {
 __device__ __forceinline__ void cp_async16_or_zero(uint32_t smem, const void* src, const void* any, bool take) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(take ? src : any), "r"(take ? 16 : 0) : "memory");
 }
-
 template <typename E>
 __device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   if constexpr (std::is_same<E, __half>::value)
@@ -200,85 +199,80 @@ __device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uin
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Shared memory of a shrink CTA: a ring of three steps of 64 tokens, and the sums [64, R
-// rounded up to 16, plus 4], which take the ring's place (a copy of each warp) where one pass
-// makes the whole rank.
+// Shared memory of a shrink CTA: a ring of stages (64 columns of 64 tokens and of 8 NT of the
+// rank), and the sums [64, R rounded up to 16, plus 4], twice: in the ring's place where one
+// pass makes the whole rank.
+constexpr int kShrinkStages = 4;
 template <int NT>
-__host__ __device__ constexpr int ring_bytes() {
-  return 3 * (8 + NT) * 2048;
+__host__ __device__ constexpr int stage_bytes() {
+  return (kTok + NT * 8) * 128;
 }
 __host__ __device__ constexpr int sums_stride(int R) { return (R + 15) / 16 * 16 + 4; }
 template <int NT>
 __host__ __device__ constexpr size_t shrink_smem(int R) {
-  const size_t sums = (size_t)kTok * sums_stride(R) * 4, ring = ring_bytes<NT>();
-  return R > NT * 8 ? ring + sums : ring > 4 * sums ? ring : 4 * sums;
+  const size_t sums = (size_t)kTok * sums_stride(R) * 4, ring = kShrinkStages * stage_bytes<NT>();
+  return R > NT * 8 ? ring + sums : ring > 2 * sums ? ring : 2 * sums;
 }
 
-// The sums of 16 MG tokens over columns [k0, k1), for a warp that takes every fourth 32
-// of them.  A thread's fragments pass through a ring in shared memory that only the thread
-// itself writes (cp.async) and reads, some steps ahead: its own wait_group is all the
-// synchronisation, and a warp's 16-byte pieces are adjacent.
+// acc = the sums of a warp's 16 MG tokens over columns [k0, k1).  All warps fetch a stage (cp.async,
+// whole lines of 128 bytes), some stages ahead; a warp takes one half of a stage's columns.
+// 16-byte pieces of odd rows lie four further, so
+// that the eight lanes that read together meet no bank twice.
 template <typename E, int NT, int MG>
 __device__ __forceinline__ void shrink_sums(float (&acc)[MG][NT][4], const E* x, int64_t ld_x, const int* rows, int count, const E* a,
-                                            int left, int H, int k0, int k1, uint32_t ring) {
-  constexpr int kPieces = 2 * MG + NT, kAll = ring_bytes<NT>() / (kPieces * 2048), kSteps = kAll > 8 ? 8 : kAll;
-  static_assert(kSteps >= 3, "");
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane & 3, g = lane >> 2;
-  const E* px[2 * MG];
+                                            int left, int H, int k0, int k1, uint32_t ring, int m, int half, bool busy) {
+  const int lane = threadIdx.x & 31, q = lane & 3, g = lane >> 2;
+  // the pieces that this thread fetches: rows tid / 8 + 16 j, columns 8 (tid % 8)
+  const int row = threadIdx.x >> 3, c = threadIdx.x & 7;
+  const uint32_t put = (row * 8 + (c ^ ((row & 1) << 2))) * 16;
+  const E* px[4];
 #pragma unroll
-  for (int i = 0; i < 2 * MG; ++i) {
-    const int r = i * 8 + g;
-    px[i] = x + rows[r < count ? r : 0] * ld_x + q * 8;  // (what rows past the last give is not used)
-  }
-  const E* pa = a + (int64_t)min(g, left - 1) * H + q * 8;
-  const int64_t row8 = (int64_t)8 * H;
-  auto fetch = [&](int step, int k) {
-    const uint32_t at = ring + step * kPieces * 2048 + threadIdx.x * 16;
-    if (k + 32 <= k1) {
+  for (int j = 0; j < 4; ++j) px[j] = x + (int64_t)rows[row + 16 * j < count ? row + 16 * j : 0] * ld_x + c * 8;
+  const E* pa = a + (int64_t)row * H + c * 8;
+  const int64_t row16 = (int64_t)16 * H;
+  auto fetch = [&](int slot, int k) {
+    const uint32_t at = ring + slot * stage_bytes<NT>() + put;
+    const bool in = k + c * 8 < k1;
 #pragma unroll
-      for (int i = 0; i < 2 * MG; ++i) cp_async16(at + i * 2048, px[i] + k);
+    for (int j = 0; j < 4; ++j)
+      if (16 * j < count) cp_async16_or_zero(at + j * 2048, px[j] + k, x, in);
 #pragma unroll
-      for (int i = 0; i < NT; ++i)
-        if (i * 8 < left) cp_async16(at + (2 * MG + i) * 2048, pa + i * row8 + k);
-    } else {  // the last columns: zeros past the end
-      const bool in = k + q * 8 < k1;
-#pragma unroll
-      for (int i = 0; i < 2 * MG; ++i) cp_async16_or_zero(at + i * 2048, px[i] + k, x, in);
-#pragma unroll
-      for (int i = 0; i < NT; ++i)
-        if (i * 8 < left) cp_async16_or_zero(at + (2 * MG + i) * 2048, pa + i * row8 + k, x, in);
-    }
+    for (int j = 0; j < (NT + 1) / 2; ++j)
+      if (row + 16 * j < NT * 8 && row + 16 * j < left) cp_async16_or_zero(at + kTok * 128 + j * 2048, pa + j * row16 + k, x, in);
   };
-  const int first = k0 + warp * 32;
-  int ahead = first, step = 0, filled = 0;
+  int ahead = k0, filled = 0, slot = 0;
 #pragma unroll
-  for (int i = 0; i < kSteps - 1; ++i, ahead += 128) {
+  for (int i = 0; i < kShrinkStages - 1; ++i, ahead += 64) {
     if (ahead < k1) fetch(i, ahead);
     cp_async_commit();
   }
-  filled = kSteps - 1;
-  for (int k = first; k < k1; k += 128) {
-    cp_async_wait<kSteps - 2>();
-    const uint32_t at = ring + step * kPieces * 2048 + threadIdx.x * 16;
-    uint4 b[NT];
-#pragma unroll
-    for (int i = 0; i < NT; ++i) b[i] = lds16(at + (2 * MG + i) * 2048);
-#pragma unroll
-    for (int m = 0; m < MG; ++m) {
-      const uint4 u = lds16(at + 2 * m * 2048), w = lds16(at + (2 * m + 1) * 2048);
-#pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        mma16816<E>(acc[m][i], u.x, w.x, u.y, w.y, b[i].x, b[i].y);
-        mma16816<E>(acc[m][i], u.z, w.z, u.w, w.w, b[i].z, b[i].w);
-      }
-    }
+  filled = kShrinkStages - 1;
+  const uint32_t lane_at = g * 128 + (((half & 1) * 4 + q) ^ ((g & 1) << 2)) * 16;
+  for (int k = k0; k < k1; k += 64) {
+    cp_async_wait<kShrinkStages - 2>();
+    __syncthreads();  // the stage is here, and the one before it has been read by all
     if (ahead < k1) fetch(filled, ahead);
     cp_async_commit();
-    ahead += 128;
-    if (++filled == kSteps) filled = 0;
-    if (++step == kSteps) step = 0;
+    ahead += 64;
+    if (++filled == kShrinkStages) filled = 0;
+    if (busy) {
+      const uint32_t at = ring + slot * stage_bytes<NT>() + lane_at;
+      uint4 b[NT];
+#pragma unroll
+      for (int i = 0; i < NT; ++i) b[i] = lds16(at + kTok * 128 + i * 1024);
+#pragma unroll
+      for (int j = 0; j < MG; ++j) {
+        const uint4 u = lds16(at + (m * MG + j) * 2048), w = lds16(at + (m * MG + j) * 2048 + 1024);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) mma16816<E>(acc[j][i], u.x, w.x, u.y, w.y, b[i].x, b[i].y);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) mma16816<E>(acc[j][i], u.z, w.z, u.w, w.w, b[i].z, b[i].w);
+      }
+    }
+    if (++slot == kShrinkStages) slot = 0;
   }
   cp_async_wait<0>();
+  __syncthreads();  // (the sums may take the ring's place)
 }
 
 __device__ __forceinline__ float4 lds_cluster(uint32_t at) {
@@ -288,8 +282,7 @@ __device__ __forceinline__ float4 lds_cluster(uint32_t at) {
 }
 
 // v of the units, as the second product takes it.  The CTAs of a cluster (blockIdx.z) share
-// the columns of H, and in a CTA the warps; eight NT of the rank at a time.  The sums are
-// joined warp after warp and CTA after CTA: their order is fixed.
+// the columns of H; eight NT of the rank at a time.  The sums are joined in a fixed order.
 //
 // v is fp32 and B has 16 bits: each v is kept as two 16-bit values (its rounding and the
 // rounding of the rest, 16 or 22 bits together), and both are multiplied.  A row is first
@@ -297,7 +290,7 @@ __device__ __forceinline__ float4 lds_cluster(uint32_t at) {
 // subnormals; `factor` takes it back, with the adapter's scale.  Layout [token][16 of the
 // rank][4 adjacent of them: four roundings, four rests].
 template <typename E, int NT>
-__global__ void __launch_bounds__(128) lora_shrink_kernel(const E* __restrict__ x, int64_t ld_x, const E* __restrict__ a,
+__global__ void __launch_bounds__(128, NT == 8 ? 3 : 4) lora_shrink_kernel(const E* __restrict__ x, int64_t ld_x, const E* __restrict__ a,
                                                           const int* __restrict__ index, const float* __restrict__ scale,
                                                           const LoraPlan plan, int64_t T, int H, int R, int n, int slice,
                                                           uint4* __restrict__ vq, float* __restrict__ factor) {
@@ -305,7 +298,7 @@ __global__ void __launch_bounds__(128) lora_shrink_kernel(const E* __restrict__ 
   __shared__ TileTokens tile;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane & 3, g = lane >> 2;
   const int stride = sums_stride(R), chunks = (R + 15) / 16;
-  float* sums = reinterpret_cast<float*>(R <= NT * 8 ? smem : smem + ring_bytes<NT>());
+  float* sums = reinterpret_cast<float*>(R <= NT * 8 ? smem : smem + kShrinkStages * stage_bytes<NT>());
   const int parts = gridDim.z, part = blockIdx.z;
   const int k0 = part * slice, k1 = min(H, k0 + slice);
   pdl_wait();
@@ -314,52 +307,44 @@ __global__ void __launch_bounds__(128) lora_shrink_kernel(const E* __restrict__ 
   int id, count;
   while (units.next(id, count)) {
     if (id < 0) continue;
+    // two warps take the tokens (16 or 32 each, one warp where there are 16 at most), twice for
+    // the halves of a stage's columns
+    const int groups = count <= 16 ? 1 : 2, m = warp % groups, half = warp / groups;
+    const bool apart = R <= NT * 8;  // room for the sums of both halves
     for (int r0 = 0; r0 < R; r0 += NT * 8) {
-      const E* ar = a + ((int64_t)id * R + r0) * H;
-      auto go = [&](auto groups) {
-        constexpr int MG = decltype(groups)::value;
+      auto go = [&](auto tokens) {
+        constexpr int MG = decltype(tokens)::value;
+        const bool busy = half < 2 && m * 16 * MG < count;
         float acc[MG][NT][4];
 #pragma unroll
-        for (int m = 0; m < MG; ++m)
+        for (int j = 0; j < MG; ++j)
 #pragma unroll
-          for (int i = 0; i < NT; ++i) acc[m][i][0] = acc[m][i][1] = acc[m][i][2] = acc[m][i][3] = 0.f;
-        shrink_sums<E, NT, MG>(acc, x, ld_x, tile.rows, count, ar, R - r0, H, k0, k1, smem_of(smem));
-        __syncthreads();  // (the sums may take the ring's place)
-        const bool apart = R <= NT * 8;  // room for a copy of each warp
-#pragma unroll 1
-        for (int p = 0; p < (apart ? 1 : 4); ++p) {  // otherwise warp after warp
-          if (apart || warp == p) {
-            float* mine = sums + (apart ? warp * kTok * stride : 0);
+          for (int i = 0; i < NT; ++i) acc[j][i][0] = acc[j][i][1] = acc[j][i][2] = acc[j][i][3] = 0.f;
+        shrink_sums<E, NT, MG>(acc, x, ld_x, tile.rows, count, a + ((int64_t)id * R + r0) * H, R - r0, H, k0, k1, smem_of(smem), m, half,
+                               busy);
+        for (int p = 0; p < 2; ++p) {  // the first half's sums, then the second's
+          if (busy && half == p) {
 #pragma unroll
-            for (int m = 0; m < MG; ++m)
+            for (int j = 0; j < MG; ++j) {
+              float* mine = sums + (apart ? p * kTok * stride : 0) + ((m * MG + j) * 16 + g) * stride + r0 + 2 * q;
 #pragma unroll
-              for (int i = 0; i < NT; ++i)
+              for (int i = 0; i < NT; ++i) {
+                if (r0 + i * 8 + 2 * q >= R) break;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                  const int c = r0 + i * 8 + 2 * q;
-                  if (c >= R) continue;
-                  float2* o = reinterpret_cast<float2*>(mine + (m * 16 + g + 8 * h) * stride + c);
-                  float2 z = make_float2(acc[m][i][2 * h], acc[m][i][2 * h + 1]);
+                  float2* o = reinterpret_cast<float2*>(mine + 8 * h * stride + i * 8);
+                  float2 z = make_float2(acc[j][i][2 * h], acc[j][i][2 * h + 1]);
                   if (!apart && p) z = make_float2(o->x + z.x, o->y + z.y);
                   *o = z;
                 }
+              }
+            }
           }
-          __syncthreads();
-        }
-        if (apart) {
-          for (int i = threadIdx.x; i < count * stride / 4; i += 128) {
-            float4* o = reinterpret_cast<float4*>(sums) + i;
-            float4 z[4];
-#pragma unroll
-            for (int p = 0; p < 4; ++p) z[p] = o[p * (kTok * stride / 4)];
-            *o = make_float4(z[0].x + z[1].x + z[2].x + z[3].x, z[0].y + z[1].y + z[2].y + z[3].y, z[0].z + z[1].z + z[2].z + z[3].z,
-                             z[0].w + z[1].w + z[2].w + z[3].w);
-          }
+          if (!apart) __syncthreads();
         }
       };
-      if (count <= 16) go(std::integral_constant<int, 1>());
-      else if (count <= 32) go(std::integral_constant<int, 2>());
-      else go(std::integral_constant<int, 4>());
+      if (count <= 32) go(std::integral_constant<int, 1>());
+      else go(std::integral_constant<int, 2>());
     }
     __syncwarp();
     cluster_sync_all();
@@ -376,8 +361,13 @@ __global__ void __launch_bounds__(128) lora_shrink_kernel(const E* __restrict__ 
         z[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (row < count && r < R)
           for (int p = 0; p < parts; ++p) {
-            const float4 y = lds_cluster(mapa_shared(at + (row * stride + r) * 4, p));
+            const uint32_t from = mapa_shared(at + (row * stride + r) * 4, p);
+            const float4 y = lds_cluster(from);
             z[i] = make_float4(z[i].x + y.x, z[i].y + y.y, z[i].z + y.z, z[i].w + y.w);
+            if (apart) {
+              const float4 w = lds_cluster(from + kTok * stride * 4);
+              z[i] = make_float4(z[i].x + w.x, z[i].y + w.y, z[i].z + w.z, z[i].w + w.w);
+            }
           }
         for (float y : {z[i].x, z[i].y, z[i].z, z[i].w})
           if (fabsf(y) <= 3e38f) most = fmaxf(most, fabsf(y));
@@ -614,28 +604,30 @@ static cudaError_t lora_launch(const void* x, int64_t ld_x, const void* a, const
   char* w = static_cast<char*>(ws);
   float* factor = reinterpret_cast<float*>(w + space.factor);
   LoraPlan plan = {};
-  int64_t units, busy;  // CTAs along x, and how many of them have work
+  int64_t most, busy;  // units at most, and about how many there are
   cudaError_t e;
   if (T <= kTok) {
-    units = busy = T < n + 1 ? T : n + 1;
+    most = busy = T < n + 1 ? T : n + 1;
   } else {
     int* order = reinterpret_cast<int*>(w + space.order);
     Unit* table = reinterpret_cast<Unit*>(w + space.units);
     int* made = reinterpret_cast<int*>(w + space.made);
     const int64_t runs = (T + kRun - 1) / kRun, tokens = T < kRun ? T : kRun;
-    // a run's units: its tokens by 64, and one more for each adapter
-    const int64_t most = tokens / kTok + (n + 1 < tokens ? n + 1 : tokens);
-    plan = {order, table, made, (int)(most < tokens ? most : tokens)};
-    units = runs * plan.most;
+    most = tokens / kTok + (n + 1 < tokens ? n + 1 : tokens);  // of a run: its tokens by 64, and one more for each adapter
+    most = runs * (most < tokens ? most : tokens);
     busy = T / kTok + runs * (n < 4 ? n : 4);
+    plan = {order, table, made, (int)runs};
     e = launch_pdl(lora_plan_kernel, dim3((unsigned)runs), dim3(kRun), 0, s, index, T, n, order, table, made);
     if (e != cudaSuccess) return e;
   }
   // parts of H: enough CTAs for a few tokens, at least 128 columns each
+  // (more than these gain nothing: two, or five for small ranks, an SM)
+  const int resident = R <= 32 ? 5 * 152 : 334;
   int parts = 1;
-  while (parts < kMostParts && busy * parts < 304 && H / (2 * parts) >= 128) parts *= 2;
-  const int slice = ((H + parts - 1) / parts + 31) / 32 * 32;
-  const dim3 grid((unsigned)units, 1, parts);
+  while (parts < kMostParts && busy * parts * 2 <= resident && H / (2 * parts) >= 128) parts *= 2;
+  const int slice = ((H + parts - 1) / parts + 63) / 64 * 64;
+  const int64_t across = most < (1 << 20) ? most : 1 << 20;  // (those past the last unit end at once)
+  const dim3 grid((unsigned)across, 1, parts);
   e = R <= 8    ? shrink_launch<E, 1>(grid, x, ld_x, a, index, scale, plan, T, H, R, n, slice, w, factor, s)
       : R <= 16 ? shrink_launch<E, 2>(grid, x, ld_x, a, index, scale, plan, T, H, R, n, slice, w, factor, s)
       : R <= 32 ? shrink_launch<E, 4>(grid, x, ld_x, a, index, scale, plan, T, H, R, n, slice, w, factor, s)
@@ -654,7 +646,7 @@ static cudaError_t lora_launch(const void* x, int64_t ld_x, const void* a, const
   const size_t smem = (size_t)(kTok / 16) * ((R + 15) / 16) * 1024;
   e = allow_smem(grants[which], (const void*)kernels[which], smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kernels[which], dim3((unsigned)units, 1, (unsigned)wide), dim3(128), smem, s, static_cast<const uint4*>(ws), factor,
+  return launch_pdl(kernels[which], dim3((unsigned)across, 1, (unsigned)wide), dim3(128), smem, s, static_cast<const uint4*>(ws), factor,
                     static_cast<const E*>(b), index, plan, T, N, R, n, static_cast<const E*>(base), ld_b, static_cast<E*>(out), ld_o);
 }
 
