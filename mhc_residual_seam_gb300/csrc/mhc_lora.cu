@@ -290,7 +290,7 @@ __device__ __forceinline__ float4 lds_cluster(uint32_t at) {
 // subnormals; `factor` takes it back, with the adapter's scale.  Layout [token][16 of the
 // rank][4 adjacent of them: four roundings, four rests].
 template <typename E, int NT>
-__global__ void __launch_bounds__(128, NT == 8 ? 3 : 4) lora_shrink_kernel(const E* __restrict__ x, int64_t ld_x, const E* __restrict__ a,
+__global__ void __launch_bounds__(128, NT == 16 ? 2 : NT == 8 ? 3 : 4) lora_shrink_kernel(const E* __restrict__ x, int64_t ld_x, const E* __restrict__ a,
                                                           const int* __restrict__ index, const float* __restrict__ scale,
                                                           const LoraPlan plan, int64_t T, int H, int R, int n, int slice,
                                                           uint4* __restrict__ vq, float* __restrict__ factor) {
@@ -408,19 +408,20 @@ __global__ void __launch_bounds__(128, NT == 8 ? 3 : 4) lora_shrink_kernel(const
 // lane_w points at the lane's first weights; column of fragment column 2 p + e of product
 // i: 8 p + 2 i + e, so a thread's eight results of a row are adjacent.
 //
-// With all 32 columns and a rank of 16 CH nothing is tested but the stores, and rows past
+// With all 32 columns and a rank of at most 16 CH little is tested but the stores, and rows past
 // the unit's last stand in as its first.  The warp keeps the weights of its columns in
 // registers for all the tokens and fetches a group's base while the one before it is
 // multiplied.
 template <typename E, int CH, bool BASE>
 __device__ __forceinline__ void expand_full(const uint4* frag, const float* factor, const E* lane_w, int R, const E* base, int64_t ld_b,
                                             E* out, int64_t ld_o, const int* rows, int count, int col, int lane) {
-  const int g = lane >> 2;
+  const int g = lane >> 2, chunks = (R + 15) / 16, left = R - (lane & 3) * 4;
   uint2 w[CH][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int c = 0; c < CH; ++c) w[c][i] = *reinterpret_cast<const uint2*>(lane_w + 2 * i * R + c * 16);
+    for (int c = 0; c < CH; ++c)
+      w[c][i] = c * 16 < left ? *reinterpret_cast<const uint2*>(lane_w + 2 * i * R + c * 16) : make_uint2(0, 0);
   const int groups = (count + 15) / 16;
   base += col;
   out += col;
@@ -438,9 +439,10 @@ __device__ __forceinline__ void expand_full(const uint4* frag, const float* fact
     float acc[4][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-    const uint4* f = frag + (m * CH * 32 + lane) * 2;
+    const uint4* f = frag + (m * chunks * 32 + lane) * 2;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
+      if (c >= chunks) break;
       const uint4 big = f[c * 64], rest = f[c * 64 + 1];
 #pragma unroll
       for (int i = 0; i < 4; ++i) mma16816<E>(acc[i], big.x, big.y, big.z, big.w, w[c][i].x, w[c][i].y);
@@ -512,7 +514,7 @@ __device__ __forceinline__ void expand_any(const uint4* frag, const float* facto
 
 // out = base + B v for the units, 32 columns a warp at a time.
 template <typename E, int CH, bool BASE>
-__global__ void __launch_bounds__(128, 5) lora_expand_kernel(const uint4* vq, const float* factor, const E* __restrict__ b,
+__global__ void __launch_bounds__(128, CH == 8 ? 4 : 5) lora_expand_kernel(const uint4* vq, const float* factor, const E* __restrict__ b,
                                                              const int* __restrict__ index, const LoraPlan plan, int64_t T, int N,
                                                              int R, int n, const E* base, int64_t ld_b, E* out, int64_t ld_o) {
   extern __shared__ uint4 frag[];
@@ -538,7 +540,7 @@ __global__ void __launch_bounds__(128, 5) lora_expand_kernel(const uint4* vq, co
     const E* bw = b + (int64_t)max(id, 0) * N * R;
     for (int c0 = (blockIdx.z * 4 + warp) * 32; c0 < N; c0 += gridDim.z * 128) {
       const E* lane_w = bw + ((int64_t)c0 + (g >> 1) * 8 + (g & 1)) * R + q * 4;
-      if (id >= 0 && c0 + 32 <= N && R == CH * 16)
+      if (id >= 0 && c0 + 32 <= N && R <= CH * 16)
         expand_full<E, CH, BASE>(frag, factors, lane_w, R, base, ld_b, out, ld_o, tile.rows, count, c0 + q * 8, lane);
       else
         expand_any<E>(frag, factors, lane_w, id, N, R, base, ld_b, out, ld_o, tile.rows, count, c0, lane);
@@ -631,18 +633,19 @@ static cudaError_t lora_launch(const void* x, int64_t ld_x, const void* a, const
   e = R <= 8    ? shrink_launch<E, 1>(grid, x, ld_x, a, index, scale, plan, T, H, R, n, slice, w, factor, s)
       : R <= 16 ? shrink_launch<E, 2>(grid, x, ld_x, a, index, scale, plan, T, H, R, n, slice, w, factor, s)
       : R <= 32 ? shrink_launch<E, 4>(grid, x, ld_x, a, index, scale, plan, T, H, R, n, slice, w, factor, s)
-                : shrink_launch<E, 8>(grid, x, ld_x, a, index, scale, plan, T, H, R, n, slice, w, factor, s);
+      : R <= 64 ? shrink_launch<E, 8>(grid, x, ld_x, a, index, scale, plan, T, H, R, n, slice, w, factor, s)
+                : shrink_launch<E, 16>(grid, x, ld_x, a, index, scale, plan, T, H, R, n, slice, w, factor, s);
   if (e != cudaSuccess) return e;
   const int64_t blocks = (N + 127) / 128;
   int64_t wide = (kExpandCtas * 152 + busy - 1) / busy;
   if (wide > blocks) wide = blocks;
   const int64_t each = (blocks + wide - 1) / wide;  // column blocks of a CTA: as even as they can be
   wide = (blocks + each - 1) / each;
-  const int which = (R <= 16 ? 0 : R <= 32 ? 1 : 2) + (base ? 3 : 0);
-  const decltype(&lora_expand_kernel<E, 1, true>) kernels[] = {lora_expand_kernel<E, 1, false>, lora_expand_kernel<E, 2, false>,
-                                                               lora_expand_kernel<E, 4, false>, lora_expand_kernel<E, 1, true>,
-                                                               lora_expand_kernel<E, 2, true>,  lora_expand_kernel<E, 4, true>};
-  static SmemGrant grants[6];
+  const int which = (R <= 16 ? 0 : R <= 32 ? 1 : R <= 64 ? 2 : 3) + (base ? 4 : 0);
+  const decltype(&lora_expand_kernel<E, 1, true>) kernels[] = {
+      lora_expand_kernel<E, 1, false>, lora_expand_kernel<E, 2, false>, lora_expand_kernel<E, 4, false>, lora_expand_kernel<E, 8, false>,
+      lora_expand_kernel<E, 1, true>,  lora_expand_kernel<E, 2, true>,  lora_expand_kernel<E, 4, true>,  lora_expand_kernel<E, 8, true>};
+  static SmemGrant grants[8];
   const size_t smem = (size_t)(kTok / 16) * ((R + 15) / 16) * 1024;
   e = allow_smem(grants[which], (const void*)kernels[which], smem);
   if (e != cudaSuccess) return e;
