@@ -51,8 +51,8 @@ __device__ __forceinline__ int adapter_of(const int* index, int64_t t, int64_t T
 // part of them; then the first token of each 64 of an adapter starts a unit.
 __global__ void __launch_bounds__(kRun) lora_plan_kernel(const int* __restrict__ index, int64_t T, int n, int* __restrict__ order,
                                                          Unit* __restrict__ units, int* __restrict__ made) {
-  __shared__ uint32_t word[kRun];
-  __shared__ int starts[kRun + 1], warp_sum[32];
+  __shared__ uint32_t word[2][kRun];
+  __shared__ int starts[kRun + 1], last[32], found[32];
   pdl_wait();
   pdl_launch();
   const int i = threadIdx.x, lane = i & 31, warp = i >> 5;
@@ -60,44 +60,52 @@ __global__ void __launch_bounds__(kRun) lora_plan_kernel(const int* __restrict__
   const int m = (int)min((int64_t)kRun, T - t0);
   const int id = adapter_of(index, t0 + i, T, n);
   uint32_t key = id == -2 ? 0xffffffffu : ((uint32_t)(id < 0 ? n : id) << 10) | i;
+  int side = 0;  // two copies in turn: one barrier an exchange
+#pragma unroll
   for (int k = 2; k <= kRun; k <<= 1)
+#pragma unroll
     for (int j = k >> 1; j > 0; j >>= 1) {
       uint32_t other;
       if (j >= 32) {
-        word[i] = key;
+        word[side][i] = key;
         __syncthreads();
-        other = word[i ^ j];
-        __syncthreads();
+        other = word[side][i ^ j];
+        side ^= 1;
       } else {
         other = __shfl_xor_sync(0xffffffffu, key, j);
       }
       const bool low = (i & j) == 0, up = (i & k) == 0;
       key = low == up ? min(key, other) : max(key, other);
     }
-  word[i] = key;
+  word[side][i] = key;
   __syncthreads();
   const bool live = i < m;
   const int a = (int)(key >> 10);
   // where this adapter's tokens begin: the last start at or before this place
-  int begin = live && (i == 0 || (int)(word[i - 1] >> 10) != a) ? i : 0;
+  int begin = live && (i == 0 || (int)(word[side][max(i - 1, 0)] >> 10) != a) ? i : 0;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const int o = __shfl_up_sync(0xffffffffu, begin, d);
     if (lane >= d) begin = max(begin, o);
   }
-  if (lane == 31) warp_sum[warp] = begin;
+  if (lane == 31) last[warp] = begin;
   __syncthreads();
-  for (int w = 0; w < warp; ++w) begin = max(begin, warp_sum[w]);
+  int earlier = lane < warp ? last[lane] : 0;
+#pragma unroll
+  for (int d = 16; d; d >>= 1) earlier = max(earlier, __shfl_xor_sync(0xffffffffu, earlier, d));
+  begin = max(begin, earlier);
   const bool starts_unit = live && (i - begin) % kTok == 0;
   const unsigned b = __ballot_sync(0xffffffffu, starts_unit);
+  if (lane == 0) found[warp] = __popc(b);
   __syncthreads();
-  if (lane == 0) warp_sum[warp] = __popc(b);
-  __syncthreads();
-  int u = __popc(b & ((1u << lane) - 1)), total = 0;
-  for (int w = 0; w < 32; ++w) {
-    if (w < warp) u += warp_sum[w];
-    total += warp_sum[w];
+  const int theirs = found[lane];
+  int before = lane < warp ? theirs : 0, total = theirs;
+#pragma unroll
+  for (int d = 16; d; d >>= 1) {
+    before += __shfl_xor_sync(0xffffffffu, before, d);
+    total += __shfl_xor_sync(0xffffffffu, total, d);
   }
+  const int u = before + __popc(b & ((1u << lane) - 1));
   if (starts_unit) starts[u] = i;
   if (i == 0) starts[total] = m, made[blockIdx.x] = total;
   __syncthreads();
