@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(128 + kFewEpilogue, 1) glu_few_kernel(const __
         prefetch_tile(&p.w, kk * kBK, (int)p.F + t * kBM);
         if (++kk == p.kblocks) kk = 0, ++t;
       }
-      pdl_wait();
+      wait_for_inputs();
       for (int64_t i = begin; i < end; ++i) {
         ok = mbar_wait(empty + st, ph, kProductLimitNs);
         if (!ok) break;
@@ -125,6 +125,7 @@ __global__ void __launch_bounds__(128 + kFewEpilogue, 1) glu_few_kernel(const __
     }
   } else if (warp == 1) {  // ------------------------------------------ MMA
     if (lane == 0) {
+      pdl_wait();  // (no wait with a limit begins before the kernel before this one has ended)
       const uint32_t idesc = product_idesc<E>(kBM, p.cols, false, false);
       int st = 0, b = 0, k = (int)(begin % p.kblocks);
       uint32_t ph = 0, pb = 1;

@@ -41,6 +41,11 @@ constexpr int kEpilogueThreads = 256, kProductThreads = 128 + kEpilogueThreads; 
 constexpr uint64_t kProductLimitNs = 2000000000ull;
 
 // ------------------------------------------------------------ PTX, pairs --
+// Before the first TMA read of what the kernel before this one wrote.
+__device__ __forceinline__ void wait_for_inputs() {
+  pdl_wait();
+  asm volatile("fence.proxy.async;" ::: "memory");
+}
 template <int CG>
 __device__ __forceinline__ void pair_tmem_alloc(uint32_t* dst, uint32_t ncols) {
   if constexpr (CG == 1) {
@@ -358,7 +363,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
 
   if (warp == 0) {  // ------------------------------------------- producer
     if (lane == 0) {
-      pdl_wait();
+      wait_for_inputs();
       int st = 0, used = 0;
       uint32_t ph = 1;
       while (ok && walk.next(s)) {
@@ -394,6 +399,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     }
   } else if (warp == 1) {  // ------------------------------------------ MMA
     if (lane == 0 && rank == 0) {
+      pdl_wait();  // (no wait with a limit begins before the kernel before this one has ended)
       int st = 0, b = 0;
       uint32_t ph = 0, pb = 1;
       while (ok && walk.next(s)) {
@@ -534,7 +540,7 @@ inline ProductPlan product_plan(int products, const int64_t* n, const int64_t* k
     if (p.rest[i] && kb[i] > uncut) uncut = kb[i];
   }
   if (tiles > groups) uncut += kb[products - 1];  // the longest come first
-  p.runs = (p.units + kLeast - 1) / kLeast;
+  p.runs = p.units > 0x3fffffff ? 0 : (p.units + kLeast - 1) / kLeast;
   if (p.runs > tiles * kParts) p.runs = tiles * kParts;
   if (p.runs > groups) p.runs = groups;
   int64_t cut = uncut + 1;

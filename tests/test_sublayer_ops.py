@@ -398,3 +398,121 @@ def test_lora_of_many_tokens(T, H, N, rank, n, order):
     moved = torch.empty_like(out)
     B.mhc_lora(dev(x)[p], dev(a), dev(b), dev(index)[p], moved, ws, scale=dev(scale), base=dev(base)[p])
     assert bool(((moved.double() - out[p].double()).abs() <= 2.0 ** -7 * out[p].double().abs() + 1e-4).all())
+
+
+# ------------------------------------------------- sizes that cut tiles along k --
+# (whole rounds and a rest; a few tiles with long sums; both products of the gradient at once)
+@pytest.mark.parametrize("T,H,F,dtype", [(1100, 2048, 5000, BF16), (256, 4096, 10000, F16), (130, 8192, 264, BF16), (2304, 1536, 4224, BF16),
+                                         (16384, 64, 72, F16), (129, 16384, 8, BF16), (128, 16384, 24, F16), (2, 72, 40000, BF16)])
+def test_glu_of_larger_sizes(T, H, F, dtype):
+    x, w, a = (dev(t) for t in glu_inputs(T, H, F, dtype, "rows"))
+    ref, terms = R.glu(x, w, a, "silu")
+    ws = workspace(B.mhc_glu_workspace_bytes(T, H, F))
+    want = None
+    for _ in range(3):
+        h, gu = torch.full((T, F), 7.0, dtype=dtype, device="cuda"), torch.full((T, 2 * F), 7.0, dtype=dtype, device="cuda")
+        B.mhc_glu(x, w, h, ws, add=a, gu=gu)
+        if want is None:
+            want = (h, gu)
+            block_case.check(h, ref["h"].cpu(), terms["h"].cpu(), n=1, what="h")
+            block_case.check(gu, ref["gu"].cpu(), terms["gu"].cpu(), n=1, what="gu")
+        assert torch.equal(h, want[0]) and torch.equal(gu, want[1])  # the same bits whatever the timing
+    B.mhc_check_status(ws)
+
+
+@pytest.mark.parametrize("T,H,F,dtype", [(3000, 520, 2000, BF16), (128, 512, 20000, F16), (20000, 72, 64, BF16), (1024, 1024, 4096, BF16),
+                                         (700, 2920, 1000, F16), (5, 40, 16384, BF16)])
+def test_glu_grad_of_larger_sizes(T, H, F, dtype):
+    x, w, _ = (None if t is None else dev(t) for t in glu_inputs(T, H, F, dtype, "none"))
+    g = gen(T)
+    gu, dh = dev(normal(g, T, 2 * F, dtype=dtype)), dev(normal(g, T, F, std=0.1, dtype=dtype))
+    ref, terms = R.glu_grad(dh, gu, x, w, "silu", dtype)
+    ws = workspace(B.mhc_glu_workspace_bytes(T, H, F))
+    want = None
+    for _ in range(3):
+        e = lambda *s: torch.full(s, 7.0, dtype=dtype, device="cuda")  # noqa: E731
+        out = {"dgu": e(T, 2 * F), "dx": e(T, H), "dw": e(2 * F, H)}
+        B.mhc_glu_grad(dh, gu, x, w, out["dgu"], out["dx"], out["dw"], ws)
+        if want is None:
+            want = out
+            for k in out:
+                block_case.check(out[k], ref[k].cpu(), terms[k].cpu(), n=1, what=k)
+        assert all(torch.equal(out[k], want[k]) for k in out)
+    acc = torch.ones(2 * F, H, device="cuda")
+    B.mhc_glu_grad(dh, gu, x, w, out["dgu"], out["dx"], acc, ws, accumulate=True)
+    block_case.check(acc, ref["dw"].cpu() + 1, terms["dw"].cpu() + 1, n=1, what="dw added")
+    B.mhc_check_status(ws)
+
+
+# --------------------------------------------------------- streams and graphs --
+def test_two_streams_with_workspaces_of_their_own():
+    sizes = [(64, 1024, 2000), (300, 512, 1368)]
+    jobs = []
+    for T, H, F in sizes:
+        x, w, _ = glu_inputs(T, H, F, BF16, "none")
+        lx, la, lb, li, ls, lbase = (dev(t) for t in lora_inputs(T, H, 264, 16, 5, BF16, "any"))
+        jobs.append({"x": dev(x), "w": dev(w), "ws": workspace(B.mhc_glu_workspace_bytes(T, H, F)), "stream": torch.cuda.Stream(),
+                     "h": torch.empty(T, F, dtype=BF16, device="cuda"), "lora": (lx, la, lb, li), "scale": ls, "base": lbase,
+                     "out": torch.empty_like(lbase), "lws": workspace(B.mhc_lora_workspace_bytes(T, 16))})
+    for j in jobs:
+        B.mhc_glu(j["x"], j["w"], j["h"], j["ws"])
+        B.mhc_lora(*j["lora"], j["out"], j["lws"], scale=j["scale"], base=j["base"])
+        j["want"] = (j["h"].clone(), j["out"].clone())
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for j in jobs:
+            B.mhc_glu(j["x"], j["w"], j["h"], j["ws"], stream=j["stream"])
+            B.mhc_lora(*j["lora"], j["out"], j["lws"], scale=j["scale"], base=j["base"], stream=j["stream"])
+    torch.cuda.synchronize()
+    for j in jobs:
+        assert torch.equal(j["h"], j["want"][0]) and torch.equal(j["out"], j["want"][1])
+
+
+FIRST = """
+import torch
+from mhc_residual_seam_gb300 import binding as B
+T, H, F = %d, 512, 1000
+n = lambda *s: torch.randn(*s, device="cuda").bfloat16()
+x, w, dh, a, b = n(T, H), n(2 * F, H), n(T, F), n(3, 16, H), n(3, 2 * F, 16)
+e = lambda *s: torch.zeros(*s, device="cuda", dtype=torch.bfloat16)
+add, h, gu, dgu, dx, dw, out = e(T, 2 * F), e(T, F), e(T, 2 * F), e(T, 2 * F), e(T, H), e(2 * F, H), e(T, H)
+index, seed = torch.arange(T, device="cuda").int() %% 4 - 1, torch.tensor([1, 2], device="cuda")
+ws = torch.zeros(B.mhc_glu_workspace_bytes(T, H, F), device="cuda", dtype=torch.uint8)
+lws = torch.zeros(B.mhc_lora_workspace_bytes(T, 16), device="cuda", dtype=torch.uint8)
+def calls():
+    B.mhc_lora(x, a, b, index, add, lws)
+    B.mhc_glu(x, w, h, ws, add=add, gu=gu)
+    B.mhc_glu_grad(dh, gu, x, w, dgu, dx, dw, ws)
+    B.mhc_dropout(dx, out, seed, r=x, p=0.5)
+s = torch.cuda.Stream()
+s.wait_stream(torch.cuda.current_stream())
+with torch.cuda.stream(s):
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        calls()  # the first calls of the process are captured
+torch.cuda.current_stream().wait_stream(s)
+for t in (add, h, gu, dgu, dx, dw, out):
+    t.zero_()
+g.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in (add, h, gu, dgu, dx, dw, out)]
+g.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(p, q) for p, q in zip(got, (add, h, gu, dgu, dx, dw, out)))
+calls()
+torch.cuda.synchronize()
+assert all(torch.equal(p, q) for p, q in zip(got, (add, h, gu, dgu, dx, dw, out)))
+assert all(bool(torch.isfinite(t).all()) and bool(t.any()) for t in got)
+B.mhc_check_status(ws)
+print("fine")
+"""
+
+
+@pytest.mark.parametrize("T", [7, 300])
+def test_first_calls_under_capture(T):
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST % T], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "fine" in r.stdout, r.stderr[-2000:]
