@@ -431,8 +431,8 @@ int mhc_glu_grad(const void* dh, const void* gu, const void* x, int64_t ld_x, co
                  mhc_dtype dtype, void* dgu, void* dx, void* dw, mhc_dtype dw_dtype, int accumulate, void* workspace,
                  size_t ws_bytes, void* stream);
 
-/* Bytes of the workspace of mhc_lora().  It needs no initialisation and holds nothing
- * between calls.  The size does not fall as T grows. */
+/* Bytes of the workspace of mhc_lora().  It needs mhc_workspace_init() once (for the status
+ * word; it holds nothing else between calls).  The size does not fall as T grows. */
 size_t mhc_lora_workspace_bytes(int64_t T, int R);
 
 /* Low-rank adapters of many requests beside a shared projection:
@@ -447,7 +447,8 @@ size_t mhc_lora_workspace_bytes(int64_t T, int R);
  *   out     [T,N], rows ld_out apart; may be base (same stride, in place)
  * bf16 or fp16; A_i x is kept in fp32 and enters the second product as two 16-bit values.
  * The tokens may come in any order (more than 64 are sorted by adapter, 1024 together).
- * T <= 2^30, n <= 2^20, H and N multiples of 8, at most 2^20, R a multiple of 8, at most 256.  Errors: MHC_ERR_CONFIG,
+ * T <= 2^30, n <= 2^20, H and N multiples of 8, at most 2^20, R a multiple of 8, at most 256.
+ * A bounded device wait that runs out is reported by mhc_check_status() on the workspace.  Errors: MHC_ERR_CONFIG,
  * MHC_ERR_SHAPE, MHC_ERR_NULL, MHC_ERR_ALIGN, MHC_ERR_WORKSPACE, MHC_ERR_ALIAS, MHC_ERR_CUDA. */
 int mhc_lora(const void* x, int64_t ld_x, const void* a, const void* b, const int32_t* index, const float* scale,
              int64_t T, int H, int N, int R, int n, mhc_dtype dtype, const void* base, int64_t ld_base, void* out,

@@ -17,8 +17,7 @@
 
 #include <type_traits>
 
-#include "mhc_ops.cuh"
-#include "mhc_sm100.cuh"
+#include "mhc_product.cuh"
 
 namespace mhc {
 
@@ -289,6 +288,62 @@ __device__ __forceinline__ float4 lds_cluster(uint32_t at) {
   return v;
 }
 
+// A unit's sums, [token][rank] fp32 at `at` in each CTA of the cluster (and, with `apart`, the
+// other half's behind them), into v and the factors.
+template <typename E>
+__device__ __forceinline__ void join_rows(uint32_t at, bool apart, int stride, float s, const int* rows, int count, int R, int warp,
+                                          uint4* vq, float* factor) {
+  const int lane = threadIdx.x & 31, chunks = (R + 15) / 16, parts = gridDim.z, part = blockIdx.z;
+  // this CTA's share of the rows, eight lanes a row, four of the rank a lane and step
+  for (int r0 = part * 16; r0 < count; r0 += parts * 16) {
+    const int row = r0 + warp * 4 + (lane >> 3), l = lane & 7;
+    float4 z[8];
+    float most = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = i * 32 + l * 4;
+      z[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (row < count && r < R)
+        for (int p = 0; p < parts; ++p) {
+          const uint32_t from = mapa_shared(at + (row * stride + r) * 4, p);
+          const float4 y = lds_cluster(from);
+          z[i] = make_float4(z[i].x + y.x, z[i].y + y.y, z[i].z + y.z, z[i].w + y.w);
+          if (apart) {
+            const float4 w = lds_cluster(from + kTok * stride * 4);
+            z[i] = make_float4(z[i].x + w.x, z[i].y + w.y, z[i].z + w.z, z[i].w + w.w);
+          }
+        }
+      for (float y : {z[i].x, z[i].y, z[i].z, z[i].w})
+        if (fabsf(y) <= 3e38f) most = fmaxf(most, fabsf(y));
+    }
+#pragma unroll
+    for (int d = 4; d; d >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+    // 2^e of the largest, from its exponent bits; rows of zeros and of subnormals stay as they are
+    const uint32_t e = __float_as_uint(most) >> 23;
+    const bool plain = e < 16 || e > 238;
+    const float down = plain ? 1.f : __uint_as_float((254 - e) << 23), up = plain ? 1.f : __uint_as_float(e << 23);
+    if (row < count) {
+      const int64_t t = rows[row];
+      if (l == 0) factor[t] = s * up;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = i * 32 + l * 4;
+        if (r >= chunks * 16) break;
+        const float2 w[2] = {{z[i].x * down, z[i].y * down}, {z[i].z * down, z[i].w * down}};
+        uint32_t big[2], rest[2];
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          big[p] = word_of(w[p].x, w[p].y, E());
+          const float2 f = pair_of(big[p], E());
+          // (an infinite value has no rest)
+          rest[p] = word_of(fabsf(f.x) <= 3e38f ? w[p].x - f.x : 0.f, fabsf(f.y) <= 3e38f ? w[p].y - f.y : 0.f, E());
+        }
+        vq[t * chunks * 4 + r / 4] = make_uint4(big[0], big[1], rest[0], rest[1]);
+      }
+    }
+  }
+}
+
 // v of the units, as the second product takes it.  The CTAs of a cluster (blockIdx.z) share
 // the columns of H; eight NT of the rank at a time.  The sums are joined in a fixed order.
 //
@@ -305,10 +360,9 @@ __global__ void __launch_bounds__(128, NT == 16 ? 2 : NT == 8 ? 3 : 4) lora_shri
   extern __shared__ __align__(16) char smem[];
   __shared__ TileTokens tile;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane & 3, g = lane >> 2;
-  const int stride = sums_stride(R), chunks = (R + 15) / 16;
+  const int stride = sums_stride(R);
   float* sums = reinterpret_cast<float*>(R <= NT * 8 ? smem : smem + kShrinkStages * stage_bytes<NT>());
-  const int parts = gridDim.z, part = blockIdx.z;
-  const int k0 = part * slice, k1 = min(H, k0 + slice);
+  const int k0 = blockIdx.z * slice, k1 = min(H, k0 + slice);
   pdl_wait();
   pdl_launch();
   Units units(tile, plan, index, T, n);
@@ -356,56 +410,7 @@ __global__ void __launch_bounds__(128, NT == 16 ? 2 : NT == 8 ? 3 : 4) lora_shri
     }
     __syncwarp();
     cluster_sync_all();
-    // this CTA's share of the rows, eight lanes a row, four of the rank a lane and step
-    const uint32_t at = smem_of(sums);
-    const float s = scale ? scale[id] : 1.f;
-    for (int r0 = part * 16; r0 < count; r0 += parts * 16) {
-      const int row = r0 + warp * 4 + (lane >> 3), l = lane & 7;
-      float4 z[8];
-      float most = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = i * 32 + l * 4;
-        z[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (row < count && r < R)
-          for (int p = 0; p < parts; ++p) {
-            const uint32_t from = mapa_shared(at + (row * stride + r) * 4, p);
-            const float4 y = lds_cluster(from);
-            z[i] = make_float4(z[i].x + y.x, z[i].y + y.y, z[i].z + y.z, z[i].w + y.w);
-            if (apart) {
-              const float4 w = lds_cluster(from + kTok * stride * 4);
-              z[i] = make_float4(z[i].x + w.x, z[i].y + w.y, z[i].z + w.z, z[i].w + w.w);
-            }
-          }
-        for (float y : {z[i].x, z[i].y, z[i].z, z[i].w})
-          if (fabsf(y) <= 3e38f) most = fmaxf(most, fabsf(y));
-      }
-#pragma unroll
-      for (int d = 4; d; d >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
-      // 2^e of the largest, from its exponent bits; rows of zeros and of subnormals stay as they are
-      const uint32_t e = __float_as_uint(most) >> 23;
-      const bool plain = e < 16 || e > 238;
-      const float down = plain ? 1.f : __uint_as_float((254 - e) << 23), up = plain ? 1.f : __uint_as_float(e << 23);
-      if (row < count) {
-        const int64_t t = tile.rows[row];
-        if (l == 0) factor[t] = s * up;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = i * 32 + l * 4;
-          if (r >= chunks * 16) break;
-          const float2 w[2] = {{z[i].x * down, z[i].y * down}, {z[i].z * down, z[i].w * down}};
-          uint32_t big[2], rest[2];
-#pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            big[p] = word_of(w[p].x, w[p].y, E());
-            const float2 f = pair_of(big[p], E());
-            // (an infinite value has no rest)
-            rest[p] = word_of(fabsf(f.x) <= 3e38f ? w[p].x - f.x : 0.f, fabsf(f.y) <= 3e38f ? w[p].y - f.y : 0.f, E());
-          }
-          vq[t * chunks * 4 + r / 4] = make_uint4(big[0], big[1], rest[0], rest[1]);
-        }
-      }
-    }
+    join_rows<E>(smem_of(sums), apart, stride, scale ? scale[id] : 1.f, tile.rows, count, R, warp, vq, factor);
     __syncwarp();
     cluster_sync_all();  // (the sums are read before the next unit's, or the CTA's end)
   }
@@ -556,17 +561,198 @@ __global__ void __launch_bounds__(128, CH == 8 ? 4 : 5) lora_expand_kernel(const
   }
 }
 
+// The same for many tokens and larger ranks, where the form above is bound by shared memory
+// and L1 (the weights and v pass through them for every product): tcgen05.mma with the output
+// columns as its rows (128, an adapter's weights by TMA) and the unit's tokens as its
+// columns, D in tensor memory.  A ninth warp's first thread fetches weights and issues the
+// products of a tile while the eight others bring the last one from tensor memory through
+// shared memory into rows, where base and out are read and written 256 bytes at a time; the
+// next tile's base is fetched before this one's is used.
+constexpr int kWideStages = 2, kWideEpilogue = 256, kWideThreads = kWideEpilogue + 32, kWidePitch = 132;
+struct WideShape {
+  int blocks;     // of 64 of the rank
+  size_t v, weights, rows, bars, bytes;  // offsets from an aligned start
+};
+__host__ __device__ inline WideShape wide_shape(int R) {
+  WideShape w;
+  w.blocks = (R + 63) / 64;
+  w.v = 0;  // [blocks][roundings, rests][64 tokens][128 bytes]
+  w.weights = (size_t)w.blocks * 2 * kTok * 128;
+  w.rows = w.weights + (size_t)kWideStages * w.blocks * 128 * 128;
+  w.bars = w.rows + (size_t)kTok * kWidePitch * 4;
+  w.bytes = w.bars + 128 + 1024;
+  return w;
+}
+
+template <typename E, bool BASE>
+__global__ void __launch_bounds__(kWideThreads, 2) lora_wide_kernel(const __grid_constant__ CUtensorMap map, const uint4* vq,
+                                                                const float* factor, const int* __restrict__ index,
+                                                                const LoraPlan plan, int64_t T, int N, int R, int n, const E* base,
+                                                                int64_t ld_b, E* out, int64_t ld_o, unsigned* status) {
+  extern __shared__ char raw[];
+  __shared__ TileTokens tile;
+  __shared__ float factors[kTok];
+  const WideShape shape = wide_shape(R);
+  const uint32_t start = (smem_u32(raw) + 1023u) & ~1023u;
+  char* aligned = raw + (start - smem_u32(raw));
+  float* staged = reinterpret_cast<float*>(aligned + shape.rows);
+  uint64_t* full = reinterpret_cast<uint64_t*>(aligned + shape.bars);
+  uint64_t *empty = full + kWideStages, *tfull = empty + kWideStages, *tempty = tfull + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, chunks = (R + 15) / 16;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kWideStages; ++i) mbar_init(full + i, 1), mbar_init(empty + i, 1);
+    for (int i = 0; i < 2; ++i) mbar_init(tfull + i, 1), mbar_init(tempty + i, kWideEpilogue / 32);
+    mbar_fence_init();
+  }
+  if (warp == kWideEpilogue / 32) pair_tmem_alloc<1>(tmem_slot, 2 * kTok);
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  wait_for_inputs();
+  Units units(tile, plan, index, T, n);
+  int id, count, st = 0, buf = 0;  // (stages and accumulators go on across units)
+  uint32_t ph = 0, pb = 0;
+  bool ok = true;
+  while (units.next(id, count)) {
+    if (id < 0) {  // no adapter: out = base
+      if (base != out)
+        for (int64_t i = threadIdx.x; i < (int64_t)count * (N / 8); i += kWideThreads) {
+          const int64_t t = tile.rows[i / (N / 8)];
+          const int c = (int)(i % (N / 8)) * 8;
+          Raw8<E> z = pack<E>(zero8());
+          if (BASE) z = ld8_stream(base + t * ld_b + c);
+          st8_stream(out + t * ld_o + c, z);
+        }
+      continue;
+    }
+    // v into shared memory as rows of 64 of the rank, 16-byte pieces swizzled by the row
+    for (int i = threadIdx.x; i < count * chunks * 4; i += kWideThreads) {
+      const int row = i / (chunks * 4), p = i - row * chunks * 4;  // p: four of the rank
+      const uint4 x = vq[(int64_t)tile.rows[row] * chunks * 4 + p];
+      const int block = p >> 4, piece = (p & 15) >> 1;
+      char* at = aligned + (size_t)block * 2 * kTok * 128 + row * 128 + ((piece ^ (row & 7)) << 4) + (p & 1) * 8;
+      *reinterpret_cast<uint2*>(at) = make_uint2(x.x, x.y);
+      *reinterpret_cast<uint2*>(at + kTok * 128) = make_uint2(x.z, x.w);
+    }
+    if (threadIdx.x < kTok) factors[threadIdx.x] = factor[tile.rows[threadIdx.x < count ? threadIdx.x : 0]];
+    fence_proxy_async_smem();
+    __syncthreads();
+    const int first = blockIdx.z, step = gridDim.z, tiles = (N + 127) / 128;
+    if (warp == kWideEpilogue / 32) {
+      if (lane == 0) {
+        const uint32_t bytes = shape.blocks * 128 * 128;
+        constexpr uint32_t idesc = product_idesc<E>(128, kTok, false, false);
+        int fs = st;  // the stage to fill next, and the parity with which its last use has ended
+        uint32_t fp = ph;
+        auto fetch = [&](int t) {
+          ok = mbar_wait(empty + fs, fp ^ 1, kProductLimitNs);
+          if (!ok) return;
+          mbar_arrive_expect_tx(full + fs, bytes);
+          for (int k = 0; k < shape.blocks; ++k)
+            pair_load<1>(start + (uint32_t)shape.weights + fs * bytes + k * 128 * 128, &map, smem_u32(full + fs), k * 64, id * N + t * 128);
+          if (++fs == kWideStages) fs = 0, fp ^= 1;
+        };
+        int ahead = first;
+        for (int i = 0; i < kWideStages && ahead < tiles && ok; ++i, ahead += step) fetch(ahead);
+        for (int t = first; t < tiles && ok; t += step) {
+          ok = mbar_wait(tempty + buf, pb ^ 1, kProductLimitNs) && mbar_wait(full + st, ph, kProductLimitNs);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t a = start + (uint32_t)shape.weights + st * bytes, v = start;
+          for (int c = 0; c < chunks; ++c) {
+            const uint32_t k = (c & 3) * 32, block = c >> 2;
+            const uint64_t da = tile_desc(a + block * 128 * 128 + k, false);
+            pair_mma<1>(tmem + buf * kTok, da, tile_desc(v + block * 2 * kTok * 128 + k, false), idesc, c);
+            pair_mma<1>(tmem + buf * kTok, da, tile_desc(v + block * 2 * kTok * 128 + kTok * 128 + k, false), idesc, 1);
+          }
+          pair_commit<1>(empty + st);
+          pair_commit<1>(tfull + buf);
+          if (++st == kWideStages) st = 0, ph ^= 1;
+          if ((buf ^= 1) == 0) pb ^= 1;
+          if (ahead < tiles) fetch(ahead), ahead += step;
+        }
+        // the MMAs that read this unit's v have ended before the next one's takes its place
+        for (int i = 0; i < kWideStages && ok; ++i) {
+          fs = fs == 0 ? (fp ^= 1, kWideStages - 1) : fs - 1;
+          ok = mbar_wait(empty + fs, fp, kProductLimitNs);
+        }
+      }
+    } else {
+      constexpr int kRows = kTok / (kWideEpilogue / 32);  // rows a warp reads and writes
+      const int r0 = warp * kRows;
+      uint2 old[kRows], next[kRows];
+      auto fetch = [&](uint2* o, int t) {
+        if constexpr (BASE) {
+          const int col = t * 128 + lane * 4;
+#pragma unroll
+          for (int i = 0; i < kRows; ++i)
+            if (col < N && r0 + i < count) o[i] = __ldcs(reinterpret_cast<const uint2*>(base + (int64_t)tile.rows[r0 + i] * ld_b + col));
+        }
+      };
+      if (first < tiles) fetch(old, first);
+      for (int t = first; t < tiles; t += step) {
+        if (t + step < tiles) fetch(next, t + step);
+        ok = all_of<kWideEpilogue>(mbar_wait(tfull + buf, pb, kProductLimitNs));  // (also: all have read the last tile's rows)
+        if (!ok) break;
+        tc_fence_after();
+        for (int c = (warp >> 2) * 16; c < count; c += kWideEpilogue / 8) {  // (a warp reads the lanes of its quarter)
+          uint32_t d[16];
+          __syncwarp();
+          issue16(tmem + buf * kTok + c + ((uint32_t)(warp & 3) << 21), d);
+          take16(d);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) staged[(c + e) * kWidePitch + (warp & 3) * 32 + lane] = __uint_as_float(d[e]);
+        }
+        tc_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(tempty + buf);
+        if ((buf ^= 1) == 0) pb ^= 1;
+        named_bar_sync(1, kWideEpilogue);
+        const int col = t * 128 + lane * 4;
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+          const int row = r0 + i;
+          if (row >= count || col >= N) continue;
+          const float4 d = *reinterpret_cast<const float4*>(staged + row * kWidePitch + lane * 4);
+          const float f = factors[row];
+          float2 lo = make_float2(0.f, 0.f), hi = lo;
+          if constexpr (BASE) lo = pair_of(old[i].x, E()), hi = pair_of(old[i].y, E());
+          const uint2 o = make_uint2(word_of(fmaf(f, d.x, lo.x), fmaf(f, d.y, lo.y), E()), word_of(fmaf(f, d.z, hi.x), fmaf(f, d.w, hi.y), E()));
+          __stcs(reinterpret_cast<uint2*>(out + (int64_t)tile.rows[row] * ld_o + col), o);
+        }
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) old[i] = next[i];
+      }
+    }
+    // all give up together
+    if (!__syncthreads_and(ok)) {
+      if (threadIdx.x == 0) atomicOr(status, 2u);
+      const uint64_t t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 20000000ull) __nanosleep(1000);
+      break;
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kWideEpilogue / 32) pair_tmem_dealloc<1>(tmem, 2 * kTok);
+}
+
 // ------------------------------------------------------------------- host --
-// Workspace: v, factors, and the plan (order, units, units made per run), each from a
+// Workspace: the status word, v, factors, and the plan (order, units, units made per run), each from a
 // multiple of 256 bytes.
 struct LoraSpace {
-  size_t factor, order, units, made, bytes;
+  size_t v, factor, order, units, made, bytes;
 };
 static LoraSpace lora_space(int64_t T, int R) {
   const auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   const size_t chunks = (R + 15) / 16, t = (size_t)T;
   LoraSpace s;
-  s.factor = up(t * chunks * 64);
+  s.v = 256;
+  s.factor = s.v + up(t * chunks * 64);
   s.order = s.factor + up(t * 4);
   s.units = s.order + up(t * 4);
   s.made = s.units + up(t * sizeof(Unit));
@@ -631,19 +817,34 @@ static cudaError_t lora_launch(const void* x, int64_t ld_x, const void* a, const
     if (e != cudaSuccess) return e;
   }
   // parts of H: enough CTAs for a few tokens, at least 128 columns each
-  // (more than these gain nothing: two, or five for small ranks, an SM)
+  // (more than these gain nothing: two an SM, five for small ranks)
   const int resident = R <= 32 ? 5 * 152 : 334;
   int parts = 1;
   while (parts < kMostParts && busy * parts * 2 <= resident && H / (2 * parts) >= 128) parts *= 2;
   const int slice = ((H + parts - 1) / parts + 63) / 64 * 64;
   const int64_t across = most < (1 << 20) ? most : 1 << 20;  // (those past the last unit end at once)
   const dim3 grid((unsigned)across, 1, parts);
-  e = R <= 8    ? shrink_launch<E, 1>(grid, x, ld_x, a, index, scale, plan, T, H, R, n, slice, w, factor, s)
-      : R <= 16 ? shrink_launch<E, 2>(grid, x, ld_x, a, index, scale, plan, T, H, R, n, slice, w, factor, s)
-      : R <= 32 ? shrink_launch<E, 4>(grid, x, ld_x, a, index, scale, plan, T, H, R, n, slice, w, factor, s)
-      : R <= 64 ? shrink_launch<E, 8>(grid, x, ld_x, a, index, scale, plan, T, H, R, n, slice, w, factor, s)
-                : shrink_launch<E, 16>(grid, x, ld_x, a, index, scale, plan, T, H, R, n, slice, w, factor, s);
+  e = R <= 8    ? shrink_launch<E, 1>(grid, x, ld_x, a, index, scale, plan, T, H, R, n, slice, w + space.v, factor, s)
+      : R <= 16 ? shrink_launch<E, 2>(grid, x, ld_x, a, index, scale, plan, T, H, R, n, slice, w + space.v, factor, s)
+      : R <= 32 ? shrink_launch<E, 4>(grid, x, ld_x, a, index, scale, plan, T, H, R, n, slice, w + space.v, factor, s)
+      : R <= 64 ? shrink_launch<E, 8>(grid, x, ld_x, a, index, scale, plan, T, H, R, n, slice, w + space.v, factor, s)
+                : shrink_launch<E, 16>(grid, x, ld_x, a, index, scale, plan, T, H, R, n, slice, w + space.v, factor, s);
   if (e != cudaSuccess) return e;
+  // (T = 8192, H = N = 5120: rank 64 47 against 61 us, rank 128 about 70 against 130, rank 24 the other way)
+  if (plan.order && R >= 48 && (int64_t)n * N < 0x7fffffff) {
+    CUtensorMap map;
+    if (!encode_2d<E>(&map, b, (int64_t)n * N, R, R, 128)) return cudaErrorInvalidValue;
+    const size_t smem = wide_shape(R).bytes;
+    auto kernel = base ? lora_wide_kernel<E, true> : lora_wide_kernel<E, false>;
+    static SmemGrant grants[2];
+    e = allow_smem(grants[base != nullptr], (const void*)kernel, smem);
+    if (e != cudaSuccess) return e;
+    int64_t wide = (2 * 152 + busy - 1) / busy;
+    if (wide > (N + 127) / 128) wide = (N + 127) / 128;
+    return launch_pdl(kernel, dim3((unsigned)across, 1, (unsigned)wide), dim3(kWideThreads), smem, s, map,
+                      reinterpret_cast<const uint4*>(w + space.v), factor, index, plan, T, N, R, n, static_cast<const E*>(base), ld_b,
+                      static_cast<E*>(out), ld_o, static_cast<unsigned*>(ws));
+  }
   const int64_t blocks = (N + 127) / 128;
   int64_t wide = (kExpandCtas * 152 + busy - 1) / busy;
   if (wide > blocks) wide = blocks;
@@ -657,7 +858,7 @@ static cudaError_t lora_launch(const void* x, int64_t ld_x, const void* a, const
   const size_t smem = (size_t)(kTok / 16) * ((R + 15) / 16) * 1024;
   e = allow_smem(grants[which], (const void*)kernels[which], smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kernels[which], dim3((unsigned)across, 1, (unsigned)wide), dim3(128), smem, s, static_cast<const uint4*>(ws), factor,
+  return launch_pdl(kernels[which], dim3((unsigned)across, 1, (unsigned)wide), dim3(128), smem, s, reinterpret_cast<const uint4*>(w + space.v), factor,
                     static_cast<const E*>(b), index, plan, T, N, R, n, static_cast<const E*>(base), ld_b, static_cast<E*>(out), ld_o);
 }
 

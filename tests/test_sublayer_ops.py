@@ -292,7 +292,7 @@ def test_lora(T, H, N, rank, n, dtype, order, scaled, based):
     x, a, b, index, scale, base = lora_inputs(T, H, N, rank, n, dtype, order)
     scale, base = scale if scaled else None, base if based else None
     ref, terms = R.lora(x, a, b, index, scale, base)
-    ws = torch.full((B.mhc_lora_workspace_bytes(T, rank),), 0xFF, dtype=torch.uint8, device="cuda")
+    ws = workspace(B.mhc_lora_workspace_bytes(T, rank))
     out = torch.full((T, N), 7.0, dtype=dtype, device="cuda")
     args = (dev(x), dev(a), dev(b), dev(index))
     B.mhc_lora(*args, out, ws, scale=dev(scale), base=dev(base))
@@ -308,7 +308,7 @@ def test_lora(T, H, N, rank, n, dtype, order, scaled, based):
 def test_lora_strides_and_neighbours():
     T, H, N, r, n = 70, 136, 72, 16, 4
     x, a, b, index, scale, base = (dev(t) for t in lora_inputs(T, H, N, r, n, BF16, "any"))
-    ws = torch.empty(B.mhc_lora_workspace_bytes(T, r), dtype=torch.uint8, device="cuda")
+    ws = workspace(B.mhc_lora_workspace_bytes(T, r))
     want = torch.empty(T, N, dtype=BF16, device="cuda")
     B.mhc_lora(x, a, b, index, want, ws, scale=scale, base=base)
     wide = torch.full((T, 4, H), float("nan"), dtype=BF16, device="cuda")
@@ -336,7 +336,7 @@ def test_lora_keeps_tokens_and_adapters_apart():
     index[7] = 2
     a[2, 3, 4] = float("nan")
     out = torch.empty(T, N, dtype=F16, device="cuda")
-    ws = torch.empty(B.mhc_lora_workspace_bytes(T, r), dtype=torch.uint8, device="cuda")
+    ws = workspace(B.mhc_lora_workspace_bytes(T, r))
     B.mhc_lora(dev(x), dev(a), dev(b), dev(index), out, ws)
     fine = index != 2
     fine[5] = fine[6] = fine[7] = False
@@ -349,7 +349,7 @@ def test_lora_results_do_not_depend_on_neighbours_order():
     # tokens of the same adapter in another order in the batch give the same rows
     T, H, N, r, n = 64, 512, 128, 32, 8
     x, a, b, index, scale, base = (dev(t) for t in lora_inputs(T, H, N, r, n, BF16, "any"))
-    ws = torch.empty(B.mhc_lora_workspace_bytes(T, r), dtype=torch.uint8, device="cuda")
+    ws = workspace(B.mhc_lora_workspace_bytes(T, r))
     out, moved = torch.empty(T, N, dtype=BF16, device="cuda"), torch.empty(T, N, dtype=BF16, device="cuda")
     B.mhc_lora(x, a, b, index, out, ws, scale=scale, base=base)
     p = torch.randperm(T, generator=gen(2)).cuda()
@@ -384,11 +384,11 @@ def test_glu_of_a_few_tokens_repeats_bit_for_bit():
 
 
 @pytest.mark.parametrize("T,H,N,rank,n,order", [(65, 64, 72, 8, 100, "any"), (1024, 72, 8, 16, 3, "any"), (1025, 40, 64, 8, 2, "one"),
-                                                (2100, 64, 136, 24, 600, "any"), (3000, 136, 64, 40, 5, "runs"), (2048, 8, 8, 8, 1, "any")])
+                                                (2100, 64, 136, 24, 600, "any"), (3000, 136, 64, 40, 5, "runs"), (2048, 8, 8, 8, 1, "any"), (500, 72, 1000, 64, 7, "runs"), (1500, 64, 264, 96, 40, "any"), (130, 40, 128, 200, 3, "runs")])
 def test_lora_of_many_tokens(T, H, N, rank, n, order):
     x, a, b, index, scale, base = lora_inputs(T, H, N, rank, n, BF16, order)
     out = torch.full((T, N), 7.0, dtype=BF16, device="cuda")
-    ws = torch.full((B.mhc_lora_workspace_bytes(T, rank),), 0xFF, dtype=torch.uint8, device="cuda")
+    ws = workspace(B.mhc_lora_workspace_bytes(T, rank))
     B.mhc_lora(dev(x), dev(a), dev(b), dev(index), out, ws, scale=dev(scale), base=dev(base))
     some = torch.cat([torch.arange(min(T, 70)), torch.randint(0, T, (150,), generator=gen(1)), torch.arange(T - 40, T)]).unique()
     ref, terms = R.lora(x[some], a, b, index[some], scale, base[some])
