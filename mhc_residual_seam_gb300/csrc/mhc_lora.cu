@@ -617,7 +617,7 @@ __global__ void __launch_bounds__(kWideThreads, 2) lora_wide_kernel(const __grid
   while (units.next(id, count)) {
     if (id < 0) {  // no adapter: out = base
       if (base != out)
-        for (int64_t i = threadIdx.x; i < (int64_t)count * (N / 8); i += kWideThreads) {
+        for (int64_t i = (int64_t)blockIdx.z * kWideThreads + threadIdx.x; i < (int64_t)count * (N / 8); i += (int64_t)gridDim.z * kWideThreads) {
           const int64_t t = tile.rows[i / (N / 8)];
           const int c = (int)(i % (N / 8)) * 8;
           Raw8<E> z = pack<E>(zero8());
