@@ -516,3 +516,39 @@ def test_first_calls_under_capture(T):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", FIRST % T], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "fine" in r.stdout, r.stderr[-2000:]
+
+
+def test_weights_written_just_before_the_call():
+    # the call starts beside the end of the kernel that writes its weights (here a gradient), and reads what that one wrote
+    T, H, F = 600, 1024, 2048
+    x, w, _ = (None if t is None else dev(t) for t in glu_inputs(T, H, F, BF16, "none"))
+    few = dev(normal(gen(6), 5, H, dtype=BF16))
+    ws, ws2 = workspace(B.mhc_glu_workspace_bytes(T, H, F)), workspace(B.mhc_glu_workspace_bytes(T, H, F))
+    e = lambda *s: torch.empty(*s, dtype=BF16, device="cuda")  # noqa: E731
+    gu, dgu, dw, h, big = dev(normal(gen(7), T, 2 * F, dtype=BF16)), e(T, 2 * F), e(2 * F, H), e(5, F), e(T, F)
+    for i in range(6):
+        dh = dev(normal(gen(20 + i), T, F, std=0.02, dtype=BF16))
+        dw.fill_(float("nan"))
+        B.mhc_glu_grad(dh, gu, x, None, dgu, None, dw, ws)
+        B.mhc_glu(few, dw, h, ws2)
+        B.mhc_glu(x, dw, big, ws2)
+        got = (h.clone(), big.clone())
+        torch.cuda.synchronize()
+        B.mhc_glu(few, dw, h, ws2)
+        torch.cuda.synchronize()
+        B.mhc_glu(x, dw, big, ws2)
+        assert bool(torch.isfinite(got[0]).all()) and torch.equal(got[0], h) and torch.equal(got[1], big)
+    # and an adapter's result is the projections' addend, the projections' output the adapter's input
+    a, b, index = dev(normal(gen(8), 3, 16, H, dtype=BF16)), dev(normal(gen(9), 3, 2 * F, 16, dtype=BF16)), (torch.arange(T) % 4 - 1).int().cuda()
+    add, lws = e(T, 2 * F), workspace(B.mhc_lora_workspace_bytes(T, 16))
+    for rows in (5, 64, 65, T):
+        want = None
+        for _ in range(4):
+            add.fill_(float("nan"))
+            B.mhc_lora(x[:rows], a, b, index[:rows], add[:rows], lws)
+            B.mhc_glu(x[:rows], w, big[:rows], ws, add=add[:rows])
+            if want is None:
+                torch.cuda.synchronize()
+                B.mhc_glu(x[:rows], w, big[:rows], ws, add=add[:rows])
+                want = big[:rows].clone()
+            assert torch.equal(big[:rows], want) and bool(torch.isfinite(want).all())
