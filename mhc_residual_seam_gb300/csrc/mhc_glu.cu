@@ -92,7 +92,7 @@ static cudaError_t glu_launch(const void* x, int64_t ld_x, const void* w, const 
 extern "C" size_t mhc_glu_workspace_bytes(int64_t T, int H, int F) {
   using namespace mhc;
   if (T <= 0 || H <= 0 || F <= 0) return 0;
-  const size_t few = few_bytes(few_plan(T, H, F));
+  const size_t few = few_bytes(few_plan(H, F));
   return few > kProductBytes ? few : kProductBytes;
 }
 

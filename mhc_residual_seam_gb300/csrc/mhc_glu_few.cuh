@@ -1,12 +1,17 @@
 // The gated projections of a few tokens: bound by reading the weights once.
 //
 // The weights are the product's rows (128 features of the gate and the same 128 of the
-// other projection: two accumulators) and the tokens its columns, so a token costs 16
-// bytes of shared memory a step, not a row of a 128-row tile.  The steps (128 features x
-// 64 columns of H, 32 KB of weights) of all tiles are cut into one equal run per SM: a
-// run that ends inside a tile leaves fp32 sums in the workspace, and the CTA that comes
-// last to a tile adds them up in the runs' order and finishes it.  No CTA waits for
-// another one, and the sums do not depend on who comes last.
+// other projection: two accumulators) and the tokens its 16 columns, so they cost 2 KB of
+// shared memory a step, not a tile of 128 rows.  The steps (128 features x 64 columns of
+// H, 32 KB of weights) of all tiles are cut into one equal run per SM: a run that ends inside
+// a tile leaves fp32 sums in the workspace, and the CTA that comes last to a tile adds them
+// up in the runs' order and finishes it.  No CTA waits for another one, and the sums do not
+// depend on who comes last.
+//
+// H = 5120, F = 10240: T = 4 38.4 us against 57.4 in tiles of tokens, T = 16 38.6 against
+// 41.0 (210 MB of weights are 30.9 at the copy's rate; the steps run at 7 TB/s, the rest is
+// the start, 2.3 us to the first step, and the SMs' uneven ends, 3.6).  With more columns
+// this form lost from 32 tokens on (T = 64 45.3 against 41.2): the parts grow with them.
 #pragma once
 
 #include "mhc_glu.cuh"
@@ -14,13 +19,13 @@
 
 namespace mhc {
 
-constexpr int kFewTokens = 128;  // most tokens of this form
+constexpr int kFewTokens = 16;   // most tokens of this form, columns of an accumulator
 constexpr int kFewRuns = 152;    // most runs
 
 struct FewPlan {
-  int tiles, kblocks, runs, cols;  // feature tiles, steps per tile, runs, columns of an accumulator (tokens, rounded up)
+  int tiles, kblocks, runs;  // feature tiles, steps per tile, runs
 };
-inline FewPlan few_plan(int64_t T, int H, int F) {
+inline FewPlan few_plan(int H, int F) {
   FewPlan p;
   p.tiles = (F + kBM - 1) / kBM;
   p.kblocks = (H + kBK - 1) / kBK;
@@ -28,16 +33,16 @@ inline FewPlan few_plan(int64_t T, int H, int F) {
   // at least four steps a run: shorter ones cost more in sums than they save
   int64_t runs = (total + 3) / 4;
   p.runs = (int)(runs < kFewRuns ? runs : kFewRuns);
-  const int64_t t = T < kFewTokens ? T : kFewTokens;
-  p.cols = (int)((t + 15) / 16 * 16);
   return p;
 }
 // Workspace: status word, a counter per tile (the same place whatever the sizes, so that
 // calls of different sizes may share it), two parts per run.
 constexpr size_t kFewCounters = kProductCounters, kFewParts = kProductParts;
 static_assert(kFewParts - kFewCounters >= (size_t)((1 << 20) / kBM) * 4, "a counter per tile of the largest F");
-inline size_t few_part_floats(const FewPlan& p) { return (size_t)2 * p.cols * kBM; }
-inline size_t few_bytes(const FewPlan& p) { return kFewParts + (size_t)p.runs * 2 * few_part_floats(p) * 4; }
+constexpr size_t kFewPart = (size_t)2 * kFewTokens * kBM;  // floats of a part
+constexpr int kFewStage = 2 * kBM * 128 + kFewTokens * 128, kFewStages = 5;
+constexpr size_t kFewSmem = (size_t)kFewStages * kFewStage + 1024 + 256;
+inline size_t few_bytes(const FewPlan& p) { return kFewParts + (size_t)p.runs * 2 * kFewPart * 4; }
 
 template <typename E>
 struct FewArgs {
@@ -48,10 +53,10 @@ struct FewArgs {
   unsigned* status;
   unsigned* counters;
   float* parts;
-  int T, act, tiles, kblocks, cols, stages;
+  int T, act, tiles, kblocks;
 };
 
-constexpr int kFewEpilogue = 256;  // epilogue threads: two warps per 32 features
+constexpr int kFewEpilogue = 256;  // epilogue threads: two warps per 32 features, eight tokens each
 constexpr int kFewAhead = 8;       // steps whose weights are fetched into L2 ahead of the kernel before
 __device__ __forceinline__ void prefetch_tile(const CUtensorMap* map, int c0, int c1) {
   asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1)
@@ -62,14 +67,13 @@ __global__ void __launch_bounds__(128 + kFewEpilogue, 1) glu_few_kernel(const __
   extern __shared__ char raw[];
   const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
   char* aligned = raw + (base - smem_u32(raw));
-  const int stage_bytes = 2 * kBM * 128 + p.cols * 128, stages = p.stages;
+  constexpr int stage_bytes = kFewStage, stages = kFewStages;
   uint64_t* full = reinterpret_cast<uint64_t*>(aligned + (size_t)stages * stage_bytes);
   uint64_t *empty = full + stages, *tfull = empty + stages, *tempty = tfull + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
   volatile uint32_t* last = tmem_slot + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int stride = (p.cols + 31) / 32 * 32;  // accumulators start at multiples of 32 columns
-  const uint32_t tcols = stride <= 32 ? 128 : stride <= 64 ? 256 : 512;
+  constexpr uint32_t stride = 32, tcols = 4 * stride;  // two accumulators, twice, at multiples of 32 columns
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
@@ -126,7 +130,7 @@ __global__ void __launch_bounds__(128 + kFewEpilogue, 1) glu_few_kernel(const __
   } else if (warp == 1) {  // ------------------------------------------ MMA
     if (lane == 0) {
       pdl_wait();  // (no wait with a limit begins before the kernel before this one has ended)
-      const uint32_t idesc = product_idesc<E>(kBM, p.cols, false, false);
+      const uint32_t idesc = product_idesc<E>(kBM, kFewTokens, false, false);
       int st = 0, b = 0, k = (int)(begin % p.kblocks);
       uint32_t ph = 0, pb = 1;
       for (int64_t i = begin; i < end && ok;) {
@@ -158,46 +162,52 @@ __global__ void __launch_bounds__(128 + kFewEpilogue, 1) glu_few_kernel(const __
   } else if (warp >= 4) {  // ------------------------------------ epilogue
     pdl_wait();
     const int feature = (warp & 3) * 32 + lane;
-    const int group = (warp - 4) >> 2;  // takes every other 16 tokens
-    const size_t part = (size_t)2 * p.cols * kBM;
+    const int c = (warp - 4) >> 2 << 3;  // this warp's first token
     int b = 0, tile = (int)(begin / p.kblocks), k = (int)(begin - (int64_t)tile * p.kblocks);
     uint32_t pb = 0;
-    // 16 tokens of this lane's feature (what is added is fetched for all of them before it is used)
-    auto finish = [&](float* g, float* u, int c) {
+    // eight tokens of this lane's feature (what is added is fetched for all of them before it is used)
+    auto finish = [&](float* g, float* u) {
       const int64_t f = (int64_t)tile * kBM + feature;
-      if (f >= p.F) return;
+      const int n = min(8, p.T - c);
+      if (f >= p.F || n <= 0) return;
       if (p.add) {
-        E a[16], v[16];
+        E a[8], v[8];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < 8; ++i) {
           const int64_t t = min(c + i, p.T - 1);
           a[i] = p.add[t * p.ld_add + f];
           v[i] = p.add[t * p.ld_add + p.F + f];
         }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) g[i] += (float)a[i], u[i] += (float)v[i];
+        for (int i = 0; i < 8; ++i) g[i] += (float)a[i], u[i] += (float)v[i];
       }
-      const int n = min(16, p.T - c);
       if (p.gu) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < 8; ++i) {
           E* o = p.gu + (int64_t)(c + i) * 2 * p.F + f;
           if (i < n) o[0] = (E)g[i], o[p.F] = (E)u[i];
         }
       }
-      activate_product<16>(g, u, p.act);
+      activate_product<8>(g, u, p.act);
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
+      for (int i = 0; i < 8; ++i)
         if (i < n) p.h[(c + i) * p.ld_h + f] = (E)g[i];
     };
     // a part lies as four columns of a feature together, features adjacent: 16 bytes a lane
-    auto read16 = [&](float4* v, const float* part_, int c) {
+    const size_t at_g = (size_t)c * kBM + feature * 4, at_u = at_g + (size_t)kFewTokens * kBM;
+    auto read8 = [&](float4* v, const float* part) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = __ldcg(reinterpret_cast<const float4*>(part_ + (size_t)(c + 4 * e) * kBM));
+      for (int e = 0; e < 2; ++e) {
+        v[e] = __ldcg(reinterpret_cast<const float4*>(part + at_g + (size_t)4 * e * kBM));
+        v[2 + e] = __ldcg(reinterpret_cast<const float4*>(part + at_u + (size_t)4 * e * kBM));
+      }
     };
-    auto add16 = [&](float* o, const float4* v) {
+    auto add8 = [&](float* g, float* u, const float4* v) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[4 * e] += v[e].x, o[4 * e + 1] += v[e].y, o[4 * e + 2] += v[e].z, o[4 * e + 3] += v[e].w;
+      for (int e = 0; e < 2; ++e) {
+        g[4 * e] += v[e].x, g[4 * e + 1] += v[e].y, g[4 * e + 2] += v[e].z, g[4 * e + 3] += v[e].w;
+        u[4 * e] += v[2 + e].x, u[4 * e + 1] += v[2 + e].y, u[4 * e + 2] += v[2 + e].z, u[4 * e + 3] += v[2 + e].w;
+      }
     };
     for (int64_t i = begin; i < end && ok; ++tile) {
       const int n = (int)min((int64_t)(p.kblocks - k), end - i);
@@ -206,22 +216,20 @@ __global__ void __launch_bounds__(128 + kFewEpilogue, 1) glu_few_kernel(const __
       if (!ok) break;
       tc_fence_after();
       const uint32_t d = tmem + b * 2 * stride + ((uint32_t)(warp & 3) << 21);
-      float* mine = p.parts + ((size_t)blockIdx.x * 2 + (i != begin)) * part + feature * 4;
-      for (int c = group * 16; c < p.cols; c += kFewEpilogue / 8) {
-        uint32_t g[16], u[16];
-        __syncwarp();
-        issue16(d + c, g);
-        issue16(d + stride + c, u);
-        take16(g);
-        take16(u);
-        if (whole) {
-          finish(reinterpret_cast<float*>(g), reinterpret_cast<float*>(u), c);
-        } else {
+      uint32_t gr[8], ur[8];
+      __syncwarp();
+      tc_ld_x8_issue(d + c, gr);
+      tc_ld_x8_issue(d + stride + c, ur);
+      tc_wait_ld_x8(gr);
+      tc_wait_ld_x8(ur);
+      if (whole) {
+        finish(reinterpret_cast<float*>(gr), reinterpret_cast<float*>(ur));
+      } else {
+        float* mine = p.parts + ((size_t)blockIdx.x * 2 + (i != begin)) * kFewPart;
 #pragma unroll
-          for (int e = 0; e < 16; e += 4) {
-            __stcg(reinterpret_cast<uint4*>(mine + (size_t)(c + e) * kBM), make_uint4(g[e], g[e + 1], g[e + 2], g[e + 3]));
-            __stcg(reinterpret_cast<uint4*>(mine + (size_t)(p.cols + c + e) * kBM), make_uint4(u[e], u[e + 1], u[e + 2], u[e + 3]));
-          }
+        for (int e = 0; e < 8; e += 4) {
+          __stcg(reinterpret_cast<uint4*>(mine + at_g + (size_t)e * kBM), make_uint4(gr[e], gr[e + 1], gr[e + 2], gr[e + 3]));
+          __stcg(reinterpret_cast<uint4*>(mine + at_u + (size_t)e * kBM), make_uint4(ur[e], ur[e + 1], ur[e + 2], ur[e + 3]));
         }
       }
       tc_wait_ld();
@@ -241,31 +249,24 @@ __global__ void __launch_bounds__(128 + kFewEpilogue, 1) glu_few_kernel(const __
           __threadfence();
           auto part_of = [&](int r) {
             const bool first = r * total / runs / p.kblocks == tile;  // the tile is the first of run r
-            return p.parts + ((size_t)r * 2 + !first) * part + feature * 4;
+            return p.parts + ((size_t)r * 2 + !first) * kFewPart;
           };
-          const float *p0 = part_of(r0), *p1 = part_of(r0 + 1);  // (a tile that is not whole has two runs at least)
-          for (int c = group * 16; c < p.cols; c += kFewEpilogue / 8) {
-            float4 v[16];
-            read16(v, p0, c);
-            read16(v + 4, p0, p.cols + c);
-            read16(v + 8, p1, c);
-            read16(v + 12, p1, p.cols + c);
-            float g[16], u[16];
+          // (a tile that is not whole has two runs at least, and seldom more than three: fetched together)
+          float4 x[4], y[4], z[4];
+          read8(x, part_of(r0));
+          read8(y, part_of(r0 + 1));
+          if (r1 > r0 + 1) read8(z, part_of(r0 + 2));
+          float g[8], u[8];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) g[e] = u[e] = 0.f;
-            add16(g, v);
-            add16(u, v + 4);
-            add16(g, v + 8);
-            add16(u, v + 12);
-            for (int r = r0 + 2; r <= r1; ++r) {
-              const float* pr = part_of(r);
-              read16(v, pr, c);
-              read16(v + 4, pr, p.cols + c);
-              add16(g, v);
-              add16(u, v + 4);
-            }
-            finish(g, u, c);
+          for (int e = 0; e < 8; ++e) g[e] = u[e] = 0.f;
+          add8(g, u, x);
+          add8(g, u, y);
+          if (r1 > r0 + 1) add8(g, u, z);
+          for (int r = r0 + 3; r <= r1; ++r) {
+            read8(x, part_of(r));
+            add8(g, u, x);
           }
+          finish(g, u);
           if (threadIdx.x == 128) p.counters[tile] = 0;
         }
         named_bar_sync(1, kFewEpilogue);  // (*last is read before the next tile's is written)
@@ -289,24 +290,21 @@ __global__ void __launch_bounds__(128 + kFewEpilogue, 1) glu_few_kernel(const __
 template <typename E>
 inline cudaError_t glu_few_launch(const void* x, int64_t ld_x, const void* w, const void* add, int64_t ld_add, int act, int64_t T,
                                   int H, int F, void* gu, void* h, int64_t ld_h, void* ws, cudaStream_t s) {
-  const FewPlan plan = few_plan(T, H, F);
+  const FewPlan plan = few_plan(H, F);
   FewArgs<E> p;
-  if (!encode_2d<E>(&p.w, w, 2 * (int64_t)F, H, H, kBM) || !encode_2d<E>(&p.x, x, T, H, ld_x, plan.cols)) return cudaErrorInvalidValue;
+  if (!encode_2d<E>(&p.w, w, 2 * (int64_t)F, H, H, kBM) || !encode_2d<E>(&p.x, x, T, H, ld_x, kFewTokens)) return cudaErrorInvalidValue;
   p.add = static_cast<const E*>(add);
   p.gu = static_cast<E*>(gu);
   p.h = static_cast<E*>(h);
   p.F = F, p.ld_add = ld_add, p.ld_h = ld_h, p.T = (int)T, p.act = act;
-  p.tiles = plan.tiles, p.kblocks = plan.kblocks, p.cols = plan.cols;
+  p.tiles = plan.tiles, p.kblocks = plan.kblocks;
   p.status = static_cast<unsigned*>(ws);
   p.counters = reinterpret_cast<unsigned*>(static_cast<char*>(ws) + kFewCounters);
   p.parts = reinterpret_cast<float*>(static_cast<char*>(ws) + kFewParts);
-  const int stage = 2 * kBM * 128 + plan.cols * 128;
-  p.stages = 200 * 1024 / stage;
-  const size_t smem = (size_t)p.stages * stage + 1024 + 256;
   static SmemGrant grant;
-  const cudaError_t e = allow_smem(grant, (const void*)glu_few_kernel<E>, 208 * 1024);
+  const cudaError_t e = allow_smem(grant, (const void*)glu_few_kernel<E>, kFewSmem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(glu_few_kernel<E>, dim3((unsigned)plan.runs), dim3(128 + kFewEpilogue), smem, s, p);
+  return launch_pdl(glu_few_kernel<E>, dim3((unsigned)plan.runs), dim3(128 + kFewEpilogue), kFewSmem, s, p);
 }
 
 }  // namespace mhc
