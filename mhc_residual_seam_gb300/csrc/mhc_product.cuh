@@ -514,39 +514,62 @@ inline bool problem(Problem* p, int64_t M, int64_t num_n, int64_t K, const void*
 }
 
 // Workspace of the products: the status word, counters of cut tiles, two parts per group.
-constexpr size_t kProductCounters = 256, kProductParts = kProductCounters + 32768;
 constexpr int kMostSms = 152;
+constexpr size_t kProductCounters = 256, kProductParts = kProductCounters + 32768;
 constexpr size_t kProductBytes = kProductParts + (size_t)kMostSms * 2 * kBM * 256 * 4;
 
 // How the tiles of one or two products (n[i] tiles of kb[i] stages) are done by `groups`
-// groups: whole rounds, and the rest of each cut into runs where that takes fewer stages.
-// A cut costs its sums' way through L2 and, where no whole tile comes after, the last
-// group's reading of them: about 10 stages and 5 for each part of a tile; so a tile is cut
-// into four at most.
+// groups: whole rounds, and the rest of each cut into runs where that takes fewer stages (a
+// tile of fewer than kShort is mostly its end, and is not cut).  A tile has eight parts at
+// most, four where large tiles come after it: its last group reads them one after another.
+// What a cut costs, in stages: a few (its sums' way through L2); and, as far as no whole tiles
+// after it hide that, five and three for each part where each run is a part of one tile,
+// thirty where runs end anywhere, both twice for the large tiles.
 struct ProductPlan {
   int64_t whole[2], rest[2], units, runs;
   int64_t stages;  // of the group that has the most
 };
 inline ProductPlan product_plan(int products, const int64_t* n, const int64_t* kb, int groups) {
-  constexpr int kParts = 4, kLeast = 4;
+  constexpr int kLeast = 4, kShort = 16, kEnd = 8;
+  const int large = groups <= kMostSms / 2 ? 2 : 1;
   ProductPlan p = {};
-  int64_t tiles = 0, uncut = 0, rounds = 0;
+  int64_t tiles = 0, longest = 0, last = 0, rounds = 0, all = 0;
   for (int i = 0; i < products; ++i) {
+    all += n[i];
+    if (kb[i] < kShort) {
+      p.whole[i] = n[i];
+      rounds += (n[i] + groups - 1) / groups * (kb[i] > kEnd ? kb[i] : kEnd);
+      continue;
+    }
     p.whole[i] = n[i] / groups * groups;
     p.rest[i] = n[i] - p.whole[i];
     rounds += n[i] / groups * kb[i];
     p.units += p.rest[i] * kb[i];
     tiles += p.rest[i];
-    if (p.rest[i] && kb[i] > uncut) uncut = kb[i];
+    if (p.rest[i] && kb[i] > longest) longest = kb[i];
+    last = kb[i];
   }
-  if (tiles > groups) uncut += kb[products - 1];  // the longest come first
-  p.runs = p.units > 0x3fffffff ? 0 : (p.units + kLeast - 1) / kLeast;
-  if (p.runs > tiles * kParts) p.runs = tiles * kParts;
-  if (p.runs > groups) p.runs = groups;
+  p.stages = rounds;
+  if (p.units == 0) return p;
+  const int kParts = rounds && large == 2 ? 4 : 8;
+  // as whole tiles: the longest come first, a second round where there are more than groups
+  const int64_t uncut = all <= groups ? longest - rounds : tiles > groups ? longest + last : longest;
+  auto cost = [&](int64_t each, int64_t join) { return each + 6 + (join > rounds ? join - rounds : 0); };
   int64_t cut = uncut + 1;
-  if (p.runs > 0) {
-    const int64_t each = (p.units + p.runs - 1) / p.runs;
-    cut = each + (rounds ? 6 : 20 + 15 * ((p.runs + tiles - 1) / tiles));
+  if (p.units <= 0x3fffffff) {
+    const bool alone = p.units == tiles * longest;  // tiles of one length
+    int64_t parts = groups / tiles < kParts ? groups / tiles : kParts;
+    if (parts > longest / kLeast) parts = longest / kLeast;
+    if (alone && parts >= 2) {
+      p.runs = tiles * parts;
+      cut = cost((longest + parts - 1) / parts, (5 + 3 * parts) * large);
+    } else {
+      p.runs = (p.units + kLeast - 1) / kLeast;
+      if (p.runs > kParts * p.units / longest) p.runs = kParts * p.units / longest;
+      if (p.runs > groups) p.runs = groups;
+      if (p.runs < 1) p.runs = 1;
+      cut = cost((p.units + p.runs - 1) / p.runs, 30 * large);
+    }
   }
   if (cut >= uncut) {
     for (int i = 0; i < products; ++i) p.whole[i] += p.rest[i], p.rest[i] = 0;
