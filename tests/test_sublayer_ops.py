@@ -552,3 +552,44 @@ def test_weights_written_just_before_the_call():
                 B.mhc_glu(x[:rows], w, big[:rows], ws, add=add[:rows])
                 want = big[:rows].clone()
             assert torch.equal(big[:rows], want) and bool(torch.isfinite(want).all())
+
+
+# --------------------------------------------------------- offsets past 32 bits --
+def test_offsets_past_32_bits():
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 50 GB")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rand = lambda *s, std=1.0: torch.empty(*s, device="cuda", dtype=BF16).normal_(0, std, generator=g)  # noqa: E731
+    T, H, F = 135001, 64, 8192  # T * 2F is past 2^31
+    x, w, add = rand(T, H), rand(2 * F, H, std=0.125), rand(T, 2 * F)
+    h, gu = torch.empty(T, F, dtype=BF16, device="cuda"), torch.empty(T, 2 * F, dtype=BF16, device="cuda")
+    ws = workspace(B.mhc_glu_workspace_bytes(T, H, F))
+    B.mhc_glu(x, w, h, ws, add=add, gu=gu)
+    rows = torch.tensor([0, 65535, 131071, 131072, T - 129, T - 1], device="cuda")
+    ref, terms = R.glu(x[rows], w, add[rows], "silu")
+    block_case.check(h[rows], ref["h"].cpu(), terms["h"].cpu(), n=1, what="h")
+    block_case.check(gu[rows], ref["gu"].cpu(), terms["gu"].cpu(), n=1, what="gu")
+    dh, dgu, dx = h, add, torch.empty(T, H, dtype=BF16, device="cuda")
+    B.mhc_glu_grad(dh, gu, None, w, dgu, dx, None, ws)
+    ref, terms = R.glu_grad(dh[rows], gu[rows], x[rows], w, "silu", BF16)
+    block_case.check(dgu[rows], ref["dgu"].cpu(), terms["dgu"].cpu(), n=1, what="dgu")
+    block_case.check(dx[rows], ref["dx"].cpu(), terms["dx"].cpu(), n=1, what="dx")
+    del h, gu, dh, dgu, add
+    N = 2 * F
+    for rank in (16, 64):
+        a, b = rand(3, rank, H, std=0.125), rand(3, N, rank, std=0.25)
+        base, out = rand(T, N), torch.empty(T, N, dtype=BF16, device="cuda")
+        index = (torch.arange(T, device="cuda") % 4 - 1).int()
+        B.mhc_lora(x, a, b, index, out, workspace(B.mhc_lora_workspace_bytes(T, rank)), base=base)
+        ref, terms = R.lora(x[rows].cpu(), a.cpu(), b.cpu(), index[rows].cpu(), None, base[rows].cpu())
+        block_case.check(out[rows], ref, terms, n=1, what="lora")
+        del base, out
+
+
+def test_a_reported_wait_is_an_error_once():
+    ws = workspace(B.mhc_glu_workspace_bytes(4, 64, 64))
+    ws[:4].view(torch.int32).fill_(2)  # as a wait that ran out leaves it
+    with pytest.raises(B.MhcError) as e:
+        B.mhc_check_status(ws)
+    assert e.value.code == -7
+    B.mhc_check_status(ws)
