@@ -68,7 +68,7 @@ struct Philox {
 // same ones.  Work item = 8 adjacent columns = two counters.
 // A thread loads the items of its next step before it draws the present one's numbers,
 // so memory and the generator overlap.  T = 16384, H = 5120, bf16: with a residual
-// 78.7 us (94 % of the copy; 92 with one item a thread and no loop), without one 69.6
+// 76.5 us (97 % of the copy; 92 with one item a thread and no loop), without one 66.5
 // (86), bound by the multiplier: 36 wide products an item at 4 cycles a warp are 41 us.
 // Two items a step for many rows (with one 86 and 76 us), one where that would leave
 // CTAs without work, and for fp32, whose items are twice as large.
@@ -81,8 +81,10 @@ struct Items {
 
 template <typename T, bool RES, bool DENSE, int PER>
 __global__ void __launch_bounds__(256, kCtas) dropout_kernel(const T* y, int64_t ld_y, const T* r, int64_t ld_r,
-                                                      const uint64_t* __restrict__ seed, uint32_t threshold, bool any,
+                                                      const uint64_t* seed, uint32_t threshold, bool any,
                                                       float scale, int64_t n, int segs, T* out, int64_t ld_o) {
+  pdl_wait_for(y, r, seed);
+  pdl_launch();
   const uint64_t key = seed[0], call = seed[1];
   auto place = [&](int64_t i, int64_t ld) -> int64_t {
     if constexpr (DENSE) return i * 8;
@@ -152,9 +154,8 @@ static cudaError_t dropout_launch(const void* y, int64_t ld_y, const void* r, in
   if (blocks > (int64_t)sms * kCtas * kSteps) blocks = (int64_t)sms * kCtas * kSteps;
   auto k = many ? dense ? dropout_kernel<T, RES, true, kPer> : dropout_kernel<T, RES, false, kPer>
                 : dense ? dropout_kernel<T, RES, true, 1> : dropout_kernel<T, RES, false, 1>;
-  k<<<(unsigned)blocks, 256, 0, s>>>(static_cast<const T*>(y), ld_y, static_cast<const T*>(r), ld_r,
-                                     static_cast<const uint64_t*>(seed), threshold, any, scale, n, segs, static_cast<T*>(out), ld_o);
-  return cudaGetLastError();
+  return launch_pdl(k, dim3((unsigned)blocks), dim3(256), 0, s, static_cast<const T*>(y), ld_y, static_cast<const T*>(r), ld_r,
+                    static_cast<const uint64_t*>(seed), threshold, any, scale, n, segs, static_cast<T*>(out), ld_o);
 }
 
 }  // namespace mhc

@@ -8,10 +8,11 @@ namespace mhc {
 // dg = dh u act'(g), du = dh act(g), from the kept pre-activations, into [T, 2F].  Bound
 // by HBM: three rows of F read, two written.  Work item = (token, 8 features).
 template <typename E, int ACT>
-__global__ void __launch_bounds__(256) glu_act_grad_kernel(const E* __restrict__ dh, const E* __restrict__ gu, int64_t n,
+__global__ void __launch_bounds__(256) glu_act_grad_kernel(const E* dh, const E* gu, int64_t n,
                                                            int segs, E* __restrict__ dgu) {
   const int64_t stride = (int64_t)gridDim.x * blockDim.x;
   const int64_t F = (int64_t)segs * 8;
+  pdl_wait_for(dh, gu);
   pdl_launch();
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += stride) {
     const int64_t t = i / segs;
@@ -103,8 +104,8 @@ static cudaError_t glu_grad_launch(const void* dh, const void* gu, const void* x
            : act == MHC_ACT_GELU ? glu_act_grad_kernel<E, MHC_ACT_GELU>
            : act == MHC_ACT_RELU ? glu_act_grad_kernel<E, MHC_ACT_RELU>
                                  : glu_act_grad_kernel<E, MHC_ACT_GELU_TANH>;
-  k<<<(unsigned)blocks, 256, 0, s>>>(static_cast<const E*>(dh), static_cast<const E*>(gu), n, segs, static_cast<E*>(dgu));
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_pdl(k, dim3((unsigned)blocks), dim3(256), 0, s, static_cast<const E*>(dh), static_cast<const E*>(gu), n,
+                                   segs, static_cast<E*>(dgu));
   if (e != cudaSuccess || (!dx && !dw)) return e;
   const int64_t F2 = 2 * (int64_t)F;
   const bool both = dx && dw, w_first = both ? T > F2 : dx == nullptr;  // the product of more stages comes first

@@ -48,11 +48,11 @@ __device__ __forceinline__ int adapter_of(const int* index, int64_t t, int64_t T
 // ---------------------------------------------------------------- the plan --
 // A thread per token: bitonic sort of (adapter, place) words, stable because the place is
 // part of them; then the first token of each 64 of an adapter starts a unit.
-__global__ void __launch_bounds__(kRun) lora_plan_kernel(const int* __restrict__ index, int64_t T, int n, int* __restrict__ order,
+__global__ void __launch_bounds__(kRun) lora_plan_kernel(const int* index, int64_t T, int n, int* __restrict__ order,
                                                          Unit* __restrict__ units, int* __restrict__ made) {
   __shared__ uint32_t word[2][kRun];
   __shared__ int starts[kRun + 1], last[32], found[32];
-  pdl_wait();
+  pdl_wait_for(index);
   pdl_launch();
   const int i = threadIdx.x, lane = i & 31, warp = i >> 5;
   const int64_t t0 = (int64_t)blockIdx.x * kRun;
@@ -353,8 +353,8 @@ __device__ __forceinline__ void join_rows(uint32_t at, bool apart, int stride, f
 // subnormals; `factor` takes it back, with the adapter's scale.  Layout [token][16 of the
 // rank][4 adjacent of them: four roundings, four rests].
 template <typename E, int NT>
-__global__ void __launch_bounds__(128, NT == 16 ? 2 : NT == 8 ? 3 : 4) lora_shrink_kernel(const E* __restrict__ x, int64_t ld_x, const E* __restrict__ a,
-                                                          const int* __restrict__ index, const float* __restrict__ scale,
+__global__ void __launch_bounds__(128, NT == 16 ? 2 : NT == 8 ? 3 : 4) lora_shrink_kernel(const E* x, int64_t ld_x, const E* a,
+                                                          const int* index, const float* scale,
                                                           const LoraPlan plan, int64_t T, int H, int R, int n, int slice,
                                                           uint4* __restrict__ vq, float* __restrict__ factor) {
   extern __shared__ __align__(16) char smem[];
@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(128, NT == 16 ? 2 : NT == 8 ? 3 : 4) lora_shri
   const int stride = sums_stride(R);
   float* sums = reinterpret_cast<float*>(R <= NT * 8 ? smem : smem + kShrinkStages * stage_bytes<NT>());
   const int k0 = blockIdx.z * slice, k1 = min(H, k0 + slice);
-  pdl_wait();
+  pdl_wait_for(x, a, index, scale);
   pdl_launch();
   Units units(tile, plan, index, T, n);
   int id, count;
@@ -527,14 +527,14 @@ __device__ __forceinline__ void expand_any(const uint4* frag, const float* facto
 
 // out = base + B v for the units, 32 columns a warp at a time.
 template <typename E, int CH, bool BASE>
-__global__ void __launch_bounds__(128, CH == 8 ? 4 : 5) lora_expand_kernel(const uint4* vq, const float* factor, const E* __restrict__ b,
-                                                             const int* __restrict__ index, const LoraPlan plan, int64_t T, int N,
+__global__ void __launch_bounds__(128, CH == 8 ? 4 : 5) lora_expand_kernel(const uint4* vq, const float* factor, const E* b,
+                                                             const int* index, const LoraPlan plan, int64_t T, int N,
                                                              int R, int n, const E* base, int64_t ld_b, E* out, int64_t ld_o) {
   extern __shared__ uint4 frag[];
   __shared__ TileTokens tile;
   __shared__ float factors[kTok];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane & 3, g = lane >> 2, chunks = (R + 15) / 16;
-  pdl_wait();
+  pdl_wait_for(vq, factor, b, index, base);
   Units units(tile, plan, index, T, n);
   int id, count;
   while (units.next(id, count)) {
@@ -586,7 +586,7 @@ __host__ __device__ inline WideShape wide_shape(int R) {
 
 template <typename E, bool BASE>
 __global__ void __launch_bounds__(kWideThreads, 2) lora_wide_kernel(const __grid_constant__ CUtensorMap map, const uint4* vq,
-                                                                const float* factor, const int* __restrict__ index,
+                                                                const float* factor, const int* index,
                                                                 const LoraPlan plan, int64_t T, int N, int R, int n, const E* base,
                                                                 int64_t ld_b, E* out, int64_t ld_o, unsigned* status) {
   extern __shared__ char raw[];
@@ -610,6 +610,7 @@ __global__ void __launch_bounds__(kWideThreads, 2) lora_wide_kernel(const __grid
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   wait_for_inputs();
+  pdl_wait_for(vq, factor, index, base);
   Units units(tile, plan, index, T, n);
   int id, count, st = 0, buf = 0;  // (stages and accumulators go on across units)
   uint32_t ph = 0, pb = 0;

@@ -162,6 +162,13 @@ __device__ __forceinline__ float warp_sum(float x) {
 
 // ------------------------------------------- programmatic dependent launch --
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// pdl_wait() for a kernel that then reads through these pointers: the reads cannot be moved
+// above it, whatever the compiler takes them for.
+template <typename... P>
+__device__ __forceinline__ void pdl_wait_for(P*&... p) {
+  pdl_wait();
+  (..., [](P*& q) { asm volatile("" : "+l"(q)::"memory"); }(p));
+}
 __device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // ------------------------------------------------------------------ host --

@@ -593,3 +593,33 @@ def test_a_reported_wait_is_an_error_once():
         B.mhc_check_status(ws)
     assert e.value.code == -7
     B.mhc_check_status(ws)
+
+
+def test_chains_of_calls_read_what_the_last_one_wrote():
+    # each call starts beside the end of the one before it; every output is the next one's input
+    T, H, F = 700, 512, 1024
+    x, w, _ = (None if t is None else dev(t) for t in glu_inputs(T, H, F, BF16, "none"))
+    w2, seed = dev(normal(gen(3), 2 * F, F, std=F ** -0.5, dtype=BF16)), key_of(1, 2)
+    a, b, index = dev(normal(gen(4), 2, 64, F, std=0.05, dtype=BF16)), dev(normal(gen(5), 2, F, 64, std=0.1, dtype=BF16)), (torch.arange(T) % 3 - 1).int().cuda()
+    ws, lws = workspace(B.mhc_glu_workspace_bytes(T, F, F)), workspace(B.mhc_lora_workspace_bytes(T, 64))
+    e = lambda *s: torch.empty(*s, dtype=BF16, device="cuda")  # noqa: E731
+    gu, h, drop, more, h2, dgu, dx, last = e(T, 2 * F), e(T, F), e(T, F), e(T, F), e(T, F), e(T, 2 * F), e(T, H), e(T, H)
+    outs = (gu, h, drop, more, h2, dgu, dx, last)
+
+    def chain(sync):
+        wait = torch.cuda.synchronize if sync else (lambda: None)
+        for t in outs:
+            t.fill_(float("nan"))
+        B.mhc_glu(x, w, h, ws, gu=gu); wait()  # noqa: E702
+        B.mhc_dropout(h, drop, seed, p=0.25); wait()  # noqa: E702
+        B.mhc_lora(drop, a, b, index, more, lws, base=drop); wait()  # noqa: E702
+        B.mhc_glu(more, w2, h2, ws); wait()  # noqa: E702
+        B.mhc_glu_grad(h2, gu, x, w, dgu, dx, None, ws); wait()  # noqa: E702
+        B.mhc_dropout(dx, last, seed, r=x, p=0.5); wait()  # noqa: E702
+        torch.cuda.synchronize()
+        return [t.clone() for t in outs]
+
+    want = chain(True)
+    assert all(bool(torch.isfinite(t).all()) for t in want)
+    for _ in range(20):
+        assert all(torch.equal(p, q) for p, q in zip(chain(False), want))
