@@ -566,9 +566,9 @@ __global__ void __launch_bounds__(128, CH == 8 ? 4 : 5) lora_expand_kernel(const
 // columns as its rows (128, an adapter's weights by TMA) and the unit's tokens as its
 // columns, D in tensor memory.  A ninth warp's first thread fetches weights and issues the
 // products of a tile while the eight others bring the last one from tensor memory through
-// shared memory into rows, where base and out are read and written 256 bytes at a time; the
-// next tile's base is fetched before this one's is used.
-constexpr int kWideStages = 2, kWideEpilogue = 256, kWideThreads = kWideEpilogue + 32, kWidePitch = 132;
+// shared memory into rows, where base and out are read and written 256 bytes at a time; a
+// tile's base is fetched before its products are waited for.
+constexpr int kWideStages = 1, kWideEpilogue = 256, kWideThreads = kWideEpilogue + 32, kWidePitch = 132;
 struct WideShape {
   int blocks;     // of 64 of the rank
   size_t v, weights, rows, bars, bytes;  // offsets from an aligned start
@@ -585,7 +585,7 @@ __host__ __device__ inline WideShape wide_shape(int R) {
 }
 
 template <typename E, bool BASE>
-__global__ void __launch_bounds__(kWideThreads, 2) lora_wide_kernel(const __grid_constant__ CUtensorMap map, const uint4* vq,
+__global__ void __launch_bounds__(kWideThreads, 3) lora_wide_kernel(const __grid_constant__ CUtensorMap map, const uint4* vq,
                                                                 const float* factor, const int* index,
                                                                 const LoraPlan plan, int64_t T, int N, int R, int n, const E* base,
                                                                 int64_t ld_b, E* out, int64_t ld_o, unsigned* status) {
@@ -682,7 +682,7 @@ __global__ void __launch_bounds__(kWideThreads, 2) lora_wide_kernel(const __grid
     } else {
       constexpr int kRows = kTok / (kWideEpilogue / 32);  // rows a warp reads and writes
       const int r0 = warp * kRows;
-      uint2 old[kRows], next[kRows];
+      uint2 old[kRows];
       auto fetch = [&](uint2* o, int t) {
         if constexpr (BASE) {
           const int col = t * 128 + lane * 4;
@@ -691,9 +691,8 @@ __global__ void __launch_bounds__(kWideThreads, 2) lora_wide_kernel(const __grid
             if (col < N && r0 + i < count) o[i] = __ldcs(reinterpret_cast<const uint2*>(base + (int64_t)tile.rows[r0 + i] * ld_b + col));
         }
       };
-      if (first < tiles) fetch(old, first);
       for (int t = first; t < tiles; t += step) {
-        if (t + step < tiles) fetch(next, t + step);
+        fetch(old, t);
         ok = all_of<kWideEpilogue>(mbar_wait(tfull + buf, pb, kProductLimitNs));  // (also: all have read the last tile's rows)
         if (!ok) break;
         tc_fence_after();
@@ -723,8 +722,6 @@ __global__ void __launch_bounds__(kWideThreads, 2) lora_wide_kernel(const __grid
           const uint2 o = make_uint2(word_of(fmaf(f, d.x, lo.x), fmaf(f, d.y, lo.y), E()), word_of(fmaf(f, d.z, hi.x), fmaf(f, d.w, hi.y), E()));
           __stcs(reinterpret_cast<uint2*>(out + (int64_t)tile.rows[row] * ld_o + col), o);
         }
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) old[i] = next[i];
       }
     }
     // all give up together
@@ -840,7 +837,7 @@ static cudaError_t lora_launch(const void* x, int64_t ld_x, const void* a, const
     static SmemGrant grants[2];
     e = allow_smem(grants[base != nullptr], (const void*)kernel, smem);
     if (e != cudaSuccess) return e;
-    int64_t wide = (2 * 152 + busy - 1) / busy;
+    int64_t wide = ((R <= 64 ? 3 : 2) * 152 + busy - 1) / busy;  // (as many CTAs as an SM has room for)
     if (wide > (N + 127) / 128) wide = (N + 127) / 128;
     return launch_pdl(kernel, dim3((unsigned)across, 1, (unsigned)wide), dim3(kWideThreads), smem, s, map,
                       reinterpret_cast<const uint4*>(w + space.v), factor, index, plan, T, N, R, n, static_cast<const E*>(base), ld_b,
