@@ -396,8 +396,10 @@ int mhc_route_grad(const float* dweights, const void* logits, int64_t ld, mhc_dt
                    void* stream);
 
 /* Bytes of the workspace of mhc_glu() and mhc_glu_grad().  It needs
- * mhc_workspace_init() once; its counters reset themselves.  The size does not fall as T
- * grows: a workspace for the most tokens serves any fewer. */
+ * mhc_workspace_init() once; its counters reset themselves (after a call that
+ * mhc_check_status() reports, run mhc_workspace_init() again).  Calls of any sizes may share
+ * it, one after another; the size does not fall as T grows, so one for the most tokens serves
+ * any fewer. */
 size_t mhc_glu_workspace_bytes(int64_t T, int H, int F);
 
 /* The gated projections of a feed-forward block, their activation and product, in one

@@ -3,17 +3,16 @@
 //   v[t,:] = A_a x[t],  out[t,:] = base[t,:] + s_a B_a v[t],  a = index[t]
 //
 // The work is bound by memory (x and base read once, out written once, an adapter's
-// weights once per unit), so its products run on mma.sync from registers.  A unit is up
-// to 64 tokens of one adapter: the rows of the products.
+// weights once per unit).  A unit is up to 64 tokens of one adapter.
 //   plan    (more than 64 tokens) sorts runs of 1024 tokens by adapter and cuts them into
 //           units, so that tokens in any order share their adapter's weights
 //   shrink  v of a unit: a cluster of CTAs shares H, its sums meet in shared memory
-//   expand  B v, the scale and base: 64 columns a warp at a time
+//   expand  B v, the scale and base: 32 columns a warp at a time on mma.sync, or, for
+//           larger ranks of many tokens, 128 columns a CTA on tcgen05 (lora_wide_kernel)
 // With up to 64 tokens each CTA finds its unit by itself.
 //
-// Operands go from memory to registers in 16-byte pieces: the order of a product's
-// reduction index and of its columns is free, so each thread's fragment is taken from
-// adjacent elements.
+// On mma.sync the order of a product's reduction index and of its columns is free, so
+// each thread's fragment is taken from adjacent elements, in pieces of 8 and 16 bytes.
 
 #include <type_traits>
 
@@ -24,7 +23,7 @@ namespace mhc {
 constexpr int kTok = 64;     // most tokens of a unit
 constexpr int kRun = 1024;   // tokens sorted together
 constexpr int kMostParts = 8;
-constexpr int kExpandCtas = 5;
+constexpr int kExpandCtas = 5;  // per SM, about
 
 struct Unit {
   int adapter;  // -1: tokens without one
@@ -221,10 +220,11 @@ __host__ __device__ constexpr size_t shrink_smem(int R) {
   return R > NT * 8 ? ring + sums : ring > 2 * sums ? ring : 2 * sums;
 }
 
-// acc = the sums of a warp's 16 MG tokens over columns [k0, k1).  All warps fetch a stage (cp.async,
-// whole lines of 128 bytes), some stages ahead; a warp takes one half of a stage's columns.
-// 16-byte pieces of odd rows lie four further, so
-// that the eight lanes that read together meet no bank twice.
+// acc = the sums of a warp's 16 MG tokens over columns [k0, k1).  All warps fetch a stage
+// (cp.async, whole lines of 128 bytes), some stages ahead; a warp takes one half of a stage's
+// columns.  16-byte pieces of odd rows lie four further, so that the eight lanes that read
+// together meet no bank twice.  T = 8192, H = 5120: rank 16 23 us, rank 64 40, bound by the
+// time that a stage takes to come (1.7 to 2.3 us) and the few that fit an SM.
 template <typename E, int NT, int MG>
 __device__ __forceinline__ void shrink_sums(float (&acc)[MG][NT][4], const E* x, int64_t ld_x, const int* rows, int count, const E* a,
                                             int left, int H, int k0, int k1, uint32_t ring, int m, int half, bool busy) {
