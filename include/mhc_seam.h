@@ -441,7 +441,7 @@ size_t mhc_lora_workspace_bytes(int64_t T, int R);
  *   out[t,:] = base[t,:] + scale[i] B_i (A_i x[t]),  i = index[t]
  *   x       [T,H], rows ld_x apart
  *   a, b    [n,R,H] and [n,N,R], dense: the adapters' two factors (a smaller rank is
- *           filled up with zeros)
+ *           filled up with zeros); n may be 0, and a and b are then not looked at
  *   index   [T] int32: the token's adapter; outside [0, n) it has none: out = base
  *   scale   [n] fp32, or NULL: 1
  *   base    [T,N], rows ld_base apart: the shared projection's result, or NULL: 0 (out is

@@ -829,7 +829,8 @@ static cudaError_t lora_launch(const void* x, int64_t ld_x, const void* a, const
                 : shrink_launch<E, 16>(grid, x, ld_x, a, index, scale, plan, T, H, R, n, slice, w + space.v, factor, s);
   if (e != cudaSuccess) return e;
   // (T = 8192, H = N = 5120, both launches: rank 64 91 against 105 us, rank 128 109 against 182, rank 24 103 against 81)
-  if (plan.order && R >= 48 && (int64_t)n * N < 0x7fffffff) {
+  // (without adapters there are no weights to lay a tensor map over)
+  if (plan.order && R >= 48 && n > 0 && (int64_t)n * N < 0x7fffffff) {
     CUtensorMap map;
     if (!encode_2d<E>(&map, b, (int64_t)n * N, R, R, 128)) return cudaErrorInvalidValue;
     const size_t smem = wide_shape(R).bytes;
