@@ -43,6 +43,11 @@
  *  - T == 0 is valid and launches nothing.  Offsets are 64-bit.
  *  - Thread safety: calls may come from several host threads; a workspace
  *    must not be shared by calls that can overlap on the GPU.
+ *  - A workspace that mhc_workspace_init() prepares keeps counters from call to call, which
+ *    an operator with another workspace layout (also one that needs no initialisation)
+ *    would overwrite: it serves the calls that its size function names.  mhc_glu(),
+ *    mhc_glu_grad() and mhc_lora() may share one, of the largest size that any of them
+ *    asks for.
  */
 #ifndef MHC_SEAM_H
 #define MHC_SEAM_H
@@ -398,8 +403,8 @@ int mhc_route_grad(const float* dweights, const void* logits, int64_t ld, mhc_dt
 /* Bytes of the workspace of mhc_glu() and mhc_glu_grad().  It needs
  * mhc_workspace_init() once; its counters reset themselves (after a call that
  * mhc_check_status() reports, run mhc_workspace_init() again).  Calls of any sizes may share
- * it, one after another; the size does not fall as T grows, so one for the most tokens serves
- * any fewer. */
+ * it, one after another, and calls of mhc_lora() between them; the size does not fall as T
+ * grows, so one for the most tokens serves any fewer. */
 size_t mhc_glu_workspace_bytes(int64_t T, int H, int F);
 
 /* The gated projections of a feed-forward block, their activation and product, in one
@@ -433,15 +438,16 @@ int mhc_glu_grad(const void* dh, const void* gu, const void* x, int64_t ld_x, co
                  mhc_dtype dtype, void* dgu, void* dx, void* dw, mhc_dtype dw_dtype, int accumulate, void* workspace,
                  size_t ws_bytes, void* stream);
 
-/* Bytes of the workspace of mhc_lora().  It needs mhc_workspace_init() once (for the status
- * word; it holds nothing else between calls).  The size does not fall as T grows. */
+/* Bytes of the workspace of mhc_lora().  It needs mhc_workspace_init() once.  It may be the
+ * workspace of mhc_glu() and mhc_glu_grad(), whose counters mhc_lora() leaves alone.  The size
+ * does not fall as T grows. */
 size_t mhc_lora_workspace_bytes(int64_t T, int R);
 
 /* Low-rank adapters of many requests beside a shared projection:
  *   out[t,:] = base[t,:] + scale[i] B_i (A_i x[t]),  i = index[t]
  *   x       [T,H], rows ld_x apart
  *   a, b    [n,R,H] and [n,N,R], dense: the adapters' two factors (a smaller rank is
- *           filled up with zeros); n may be 0, and a and b are then not looked at
+ *           filled up with zeros); n may be 0, and a and b NULL then
  *   index   [T] int32: the token's adapter; outside [0, n) it has none: out = base
  *   scale   [n] fp32, or NULL: 1
  *   base    [T,N], rows ld_base apart: the shared projection's result, or NULL: 0 (out is

@@ -740,8 +740,10 @@ __global__ void __launch_bounds__(kWideThreads, 3) lora_wide_kernel(const __grid
 }
 
 // ------------------------------------------------------------------- host --
-// Workspace: the status word, v, factors, and the plan (order, units, units made per run), each from a
-// multiple of 256 bytes.
+// Workspace: the status word, the place of the products' counters (which outlive this call where both
+// work in one buffer), v, factors, and the plan (order, units, units made per run), each from a multiple
+// of 256 bytes.
+static_assert(kProductParts % 256 == 0, "");
 struct LoraSpace {
   size_t v, factor, order, units, made, bytes;
 };
@@ -749,7 +751,7 @@ static LoraSpace lora_space(int64_t T, int R) {
   const auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   const size_t chunks = (R + 15) / 16, t = (size_t)T;
   LoraSpace s;
-  s.v = 256;
+  s.v = kProductParts;
   s.factor = s.v + up(t * chunks * 64);
   s.order = s.factor + up(t * 4);
   s.units = s.order + up(t * 4);

@@ -1,8 +1,11 @@
-"""The operators inside a block where they can go wrong: no adapters at all."""
+"""The operators inside a block where they can go wrong: no adapters at all, one buffer as the workspace of all of
+them."""
 import pytest
 import torch
 
 from mhc_residual_seam_gb300 import binding as B
+
+import sublayer_exact_case as X
 
 pytestmark = pytest.mark.gpu
 
@@ -44,4 +47,33 @@ def test_lora_without_adapters(T, rank):
     again = base.clone()
     B.mhc_lora(x, a, b, index, again, ws, scale=torch.empty(0, device="cuda"), base=again)
     assert torch.equal(again, base)
+    B.mhc_check_status(ws)
+
+
+# ------------------------------------------------- one buffer for all of them --
+def test_one_buffer_for_projections_and_adapters():
+    # the projections' counters outlive an adapter's call in the same buffer
+    sizes = [(130, 8192, 264), (9, 5120, 2000), (1100, 2048, 5000)]  # tiles cut along H, in both forms
+    lora = [(70, 16), (8192, 64), (20, 256), (3000, 8)]
+    ws = workspace(max([B.mhc_glu_workspace_bytes(*s) for s in sizes] + [B.mhc_lora_workspace_bytes(*s) for s in lora]))
+    g = torch.Generator(device="cuda").manual_seed(1)
+    normal = lambda *s: torch.empty(*s, dtype=BF16, device="cuda").normal_(generator=g)  # noqa: E731
+    jobs = []
+    for T, H, F in sizes:
+        x, w, add = X.glu_inputs(T, H, F, BF16, "cuda")
+        jobs.append((x, w, add, X.glu(x, w, add, BF16)[0]))
+    dh, gu, gx, gw = X.grad_inputs(700, 2920, 1000, BF16, "cuda")
+    want = [t.to(BF16) for t in X.grad(dh, gu, gx, gw)]
+    for T, rank in lora:
+        lx, la, lb = normal(T, 264), normal(3, rank, 264), normal(3, 136, rank)
+        index, out = (torch.arange(T, device="cuda") % 4 - 1).int(), full(T, 136)
+        for x, w, add, h in jobs:
+            B.mhc_lora(lx, la, lb, index, out, ws)
+            got = full(*h.shape)
+            B.mhc_glu(x, w, got, ws, add=add, act=B.MHC_ACT_RELU)
+            assert torch.equal(got, h)
+        B.mhc_lora(lx, la, lb, index, out, ws)
+        got = [full(*t.shape) for t in want]
+        B.mhc_glu_grad(dh, gu, gx, gw, *got, ws, act=B.MHC_ACT_RELU)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
     B.mhc_check_status(ws)
