@@ -31,7 +31,8 @@ __device__ __forceinline__ float2 activate_grad(float g) {
   }
   if constexpr (ACT == MHC_ACT_GELU_TANH) {
     const float s = logistic(kGeluA * (g + kGeluB * g * g * g));
-    return make_float2(g * s, s + g * s * (1.f - s) * kGeluA * (1.f + 3.f * kGeluB * g * g));
+    // (the square stays finite: s (1 - s) is 0 there, and 0 times infinity would be a NaN)
+    return make_float2(g * s, s + g * s * (1.f - s) * kGeluA * (1.f + 3.f * kGeluB * fminf(g * g, 1e30f)));
   }
   return g > 0.f || g != g ? make_float2(g, 1.f) : make_float2(0.f, 0.f);
 }

@@ -1,10 +1,11 @@
 """The operators inside a block where they can go wrong: no adapters at all, one buffer as the workspace of all of
-them."""
+them, pre-activations whose squares leave fp32."""
 import pytest
 import torch
 
 from mhc_residual_seam_gb300 import binding as B
 
+import sublayer_case as R
 import sublayer_exact_case as X
 
 pytestmark = pytest.mark.gpu
@@ -77,3 +78,25 @@ def test_one_buffer_for_projections_and_adapters():
         B.mhc_glu_grad(dh, gu, gx, gw, *got, ws, act=B.MHC_ACT_RELU)
         assert all(torch.equal(a, b) for a, b in zip(got, want))
     B.mhc_check_status(ws)
+
+
+# ----------------------------------- pre-activations whose squares leave fp32 --
+@pytest.mark.parametrize("act", range(4))
+def test_gradient_of_huge_preactivations(act):
+    g = torch.tensor([1e15, 1e19, 2e19, 1e25, 3e38, 1e5, 40.0, 1.0], dtype=BF16)
+    g = torch.stack([g, -g])
+    gu = torch.cat([g, torch.ones(2, 8, dtype=BF16)], 1)
+    dh, x, w = torch.ones(2, 8, dtype=BF16), torch.ones(2, 8, dtype=BF16), torch.ones(16, 8, dtype=BF16)
+    dgu = full(2, 16)
+    B.mhc_glu_grad(dh.cuda(), gu.cuda(), None, None, dgu, None, None, workspace(B.mhc_glu_workspace_bytes(2, 8, 8)), act=act)
+    name = R.ACTS[act]
+    dgu = dgu.cpu().double()
+    a, da, _ = R.act(g, name)  # (far out the activation is g or 0 and its derivative 1 or 0)
+    for got, want in ((dgu[:, :8], da), (dgu[:, 8:], a)):
+        # one rounding to bf16, and for g = 1 and -1 some fp32 ones of terms of about 1
+        assert torch.allclose(got, want, rtol=2.0 ** -8, atol=2.0 ** -18)
+    gu[:, 0] = float("nan")  # a NaN stays one
+    B.mhc_glu_grad(dh.cuda(), gu.cuda(), None, None, out := full(2, 16), None, None,
+                   workspace(B.mhc_glu_workspace_bytes(2, 8, 8)), act=act)
+    assert bool(torch.isnan(out[:, 8]).all()) and (name == "relu" or bool(torch.isnan(out[:, 0]).all()))
+    assert torch.equal(out.cpu().double()[:, 1:8], dgu[:, 1:8])
