@@ -1,5 +1,6 @@
 """The operators inside a block where they can go wrong: no adapters at all, one buffer as the workspace of all of
-them, pre-activations whose squares leave fp32."""
+them, pre-activations whose squares leave fp32, and sums of whole numbers, which have one value in whatever order they
+are added."""
 import pytest
 import torch
 
@@ -100,3 +101,54 @@ def test_gradient_of_huge_preactivations(act):
                    workspace(B.mhc_glu_workspace_bytes(2, 8, 8)), act=act)
     assert bool(torch.isnan(out[:, 8]).all()) and (name == "relu" or bool(torch.isnan(out[:, 0]).all()))
     assert torch.equal(out.cpu().double()[:, 1:8], dgu[:, 1:8])
+
+
+# ---------------------------------------------------- sums of whole numbers --
+@pytest.mark.parametrize("T,H,F", X.GLU)
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_glu_of_whole_numbers(T, H, F, dtype):
+    x, w, add = X.glu_inputs(T, H, F, dtype, "cuda")
+    h, gu = X.glu(x, w, add, dtype)
+    ws = workspace(B.mhc_glu_workspace_bytes(T, H, F))
+    for keep in (True, False):
+        got, kept = full(T, F, dtype=dtype), full(T, 2 * F, dtype=dtype) if keep else None
+        B.mhc_glu(x, w, got, ws, add=add, gu=kept, act=B.MHC_ACT_RELU)
+        assert torch.equal(got, h) and (not keep or torch.equal(kept, gu))
+    B.mhc_check_status(ws)
+
+
+@pytest.mark.parametrize("T,H,F", X.GRAD)
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_glu_grad_of_whole_numbers(T, H, F, dtype):
+    dh, gu, x, w = X.grad_inputs(T, H, F, dtype, "cuda")
+    dgu, dx, dw = X.grad(dh, gu, x, w)
+    ws = workspace(B.mhc_glu_workspace_bytes(T, H, F))
+    old = X.whole(torch.Generator().manual_seed(1), 2 * F, H, most=100).cuda()
+    for wdt in (dtype, F32):
+        for add in (False, True):
+            to = old.to(wdt, copy=True)
+            want = (dw + old.double() if add else dw).to(wdt)
+            got = [full(T, 2 * F, dtype=dtype), full(T, H, dtype=dtype)]
+            B.mhc_glu_grad(dh, gu, x, w, *got, to, ws, act=B.MHC_ACT_RELU, accumulate=add)
+            assert torch.equal(got[0], dgu.to(dtype)) and torch.equal(got[1], dx.to(dtype)) and torch.equal(to, want)
+            # each product by itself: its tiles are cut at other places
+            to = old.to(wdt, copy=True)
+            B.mhc_glu_grad(dh, gu, x, None, got[0], None, to, ws, act=B.MHC_ACT_RELU, accumulate=add)
+            assert torch.equal(to, want)
+    alone = full(T, H, dtype=dtype)
+    B.mhc_glu_grad(dh, gu, None, w, got[0], alone, None, ws, act=B.MHC_ACT_RELU)
+    assert torch.equal(alone, dx.to(dtype))
+    B.mhc_check_status(ws)
+
+
+@pytest.mark.parametrize("T,H,N,rank,n", X.LORA)
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_lora_of_whole_numbers(T, H, N, rank, n, dtype):
+    x, a, b, index, scale, base = X.lora_inputs(T, H, N, rank, n, dtype, "cuda")
+    ws = workspace(B.mhc_lora_workspace_bytes(T, rank))
+    out = full(T, N, dtype=dtype)
+    B.mhc_lora(x, a, b, index, out, ws, scale=scale, base=base)
+    assert torch.equal(out, X.lora(x, a, b, index, scale, base).to(dtype))
+    B.mhc_lora(x, a, b, index, out, ws)
+    assert torch.equal(out, X.lora(x, a, b, index, torch.ones_like(scale), torch.zeros_like(base)).to(dtype))
+    B.mhc_check_status(ws)
