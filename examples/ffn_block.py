@@ -61,6 +61,11 @@ class Block:
                    o["workspace"])
         return o
 
+    def outputs(self):
+        """What a step writes, one after another."""
+        seam = ("norm", "residual_out", "pre_out", "post_out", "comb_out")
+        return {"add": self.add, "h": self.h, "y": self.y, "Y": self.Y, **{k: self.seam[k] for k in seam}}
+
 
 def serve(T=8, H=1024, F=2048, n=4, seed=0):
     """A step of T requests, once as calls and once as a replayed graph."""
@@ -71,8 +76,9 @@ def serve(T=8, H=1024, F=2048, n=4, seed=0):
     index = torch.randint(-1, n, (T,), device="cuda", generator=g).int()  # -1: a request without an adapter
     gates = {"pre": torch.full((T, 4), 0.25, device="cuda"), "post": torch.ones(T, 4, device="cuda"),
              "comb": torch.full((T, 4, 4), 0.25, device="cuda")}
-    eager = {k: v.clone() for k, v in b.step(R, norm, gates, index).items() if k in ("residual_out", "norm")}
-    eager |= {"add": b.add.clone(), "h": b.h.clone(), "y": b.y.clone()}
+    b.step(R, norm, gates, index)
+    outputs = b.outputs()
+    eager = {k: v.clone() for k, v in outputs.items()}
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):
@@ -81,11 +87,13 @@ def serve(T=8, H=1024, F=2048, n=4, seed=0):
         with torch.cuda.graph(graph, stream=side):
             b.step(R, norm, gates, index)
     torch.cuda.current_stream().wait_stream(side)
-    b.seam["norm"].zero_()
+    for v in outputs.values():
+        v.fill_(float("nan"))  # what a replay does not write is seen
     graph.replay()
     torch.cuda.synchronize()
-    B.mhc_check_status(b.ws)
-    return {"block": b, "x": norm, "index": index, "eager": eager, "replayed": b.seam}
+    for ws in (b.ws, b.lora_ws, b.seam["workspace"]):
+        B.mhc_check_status(ws)
+    return {"block": b, "x": norm, "index": index, "eager": eager, "replayed": outputs}
 
 
 # ------------------------------------------------------------------- train --
@@ -206,7 +214,7 @@ if __name__ == "__main__":
     if what == "serve":
         out = serve()
         print("adapters of the requests:", out["index"].tolist())
-        print("the replay gives the same:", torch.equal(out["eager"]["norm"], out["replayed"]["norm"]))
+        print("the replay gives the same:", all(torch.equal(v, out["replayed"][k]) for k, v in out["eager"].items()))
     elif what == "train":
         losses = train()
         print("loss", " ".join("%.3f" % x for x in losses[::10] + losses[-1:]))
