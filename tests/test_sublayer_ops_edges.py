@@ -1,6 +1,9 @@
 """The operators inside a block where they can go wrong: no adapters at all, one buffer as the workspace of all of
 them, pre-activations whose squares leave fp32, and sums of whole numbers, which have one value in whatever order they
 are added."""
+import os
+import sys
+
 import pytest
 import torch
 
@@ -152,3 +155,18 @@ def test_lora_of_whole_numbers(T, H, N, rank, n, dtype):
     B.mhc_lora(x, a, b, index, out, ws)
     assert torch.equal(out, X.lora(x, a, b, index, torch.ones_like(scale), torch.zeros_like(base)).to(dtype))
     B.mhc_check_status(ws)
+
+
+# ---------------------------------------------------------- the smoke test --
+def test_smoke_initialises_every_workspace(monkeypatch):
+    sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    import __graft_entry__ as entry
+    ready = set()
+    init = B.mhc_workspace_init
+    monkeypatch.setattr(B, "mhc_workspace_init", lambda ws, *a: (init(ws, *a), ready.add((ws.data_ptr(), ws.numel()))))
+    for name, at in (("mhc_lora", 5), ("mhc_glu", 3), ("mhc_glu_grad", 7)):
+        def call(*a, f=getattr(B, name), at=at, **k):
+            assert (a[at].data_ptr(), a[at].numel()) in ready, f
+            f(*a, **k)
+        monkeypatch.setattr(B, name, call)
+    entry._smoke_sublayer(torch, B)
