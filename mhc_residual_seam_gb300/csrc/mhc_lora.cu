@@ -840,7 +840,11 @@ static cudaError_t lora_launch(const void* x, int64_t ld_x, const void* a, const
     static SmemGrant grants[2];
     e = allow_smem(grants[base != nullptr], (const void*)kernel, smem);
     if (e != cudaSuccess) return e;
-    int64_t wide = ((R <= 64 ? 3 : 2) * 152 + busy - 1) / busy;  // (as many CTAs as an SM has room for)
+    // As many CTAs as an SM's 228 KB have room for: three up to rank 64, two up to 128, then one.  (Both
+    // launches with one and with two for rank 256: T = 8192, H = N = 5120, 24 prompts 253 and 260 us; T = 1003,
+    // H = 2048, N = 10000 73 and 80; 64 adapters in any order, whose units are many as it is, 895 and 870.)
+    const int64_t room = (228 << 10) / (smem + 2048);
+    int64_t wide = (room * 152 + busy - 1) / busy;
     if (wide > (N + 127) / 128) wide = (N + 127) / 128;
     return launch_pdl(kernel, dim3((unsigned)across, 1, (unsigned)wide), dim3(kWideThreads), smem, s, map,
                       reinterpret_cast<const uint4*>(w + space.v), factor, index, plan, T, N, R, n, static_cast<const E*>(base), ld_b,
