@@ -567,8 +567,10 @@ __global__ void __launch_bounds__(128, CH == 8 ? 4 : 5) lora_expand_kernel(const
 // columns, D in tensor memory.  A ninth warp's first thread fetches weights and issues the
 // products of a tile while the eight others bring the last one from tensor memory through
 // shared memory into rows, where base and out are read and written 256 bytes at a time; a
-// tile's base is fetched before its products are waited for.
-constexpr int kWideStages = 1, kWideEpilogue = 256, kWideThreads = kWideEpilogue + 32, kWidePitch = 132;
+// tile's base is fetched before its products are waited for.  The weights have one place, filled
+// again when the products that read it have ended: a second one would cost an SM its third CTA
+// (T = 8192, H = N = 5120, both launches: rank 64 91 us with one place, 97 with two).
+constexpr int kWideEpilogue = 256, kWideThreads = kWideEpilogue + 32, kWidePitch = 132;
 struct WideShape {
   int blocks;     // of 64 of the rank
   size_t v, weights, rows, bars, bytes;  // offsets from an aligned start
@@ -578,7 +580,7 @@ __host__ __device__ inline WideShape wide_shape(int R) {
   w.blocks = (R + 63) / 64;
   w.v = 0;  // [blocks][roundings, rests][64 tokens][128 bytes]
   w.weights = (size_t)w.blocks * 2 * kTok * 128;
-  w.rows = w.weights + (size_t)kWideStages * w.blocks * 128 * 128;
+  w.rows = w.weights + (size_t)w.blocks * 128 * 128;
   w.bars = w.rows + (size_t)kTok * kWidePitch * 4;
   w.bytes = w.bars + 128 + 1024;
   return w;
@@ -597,11 +599,11 @@ __global__ void __launch_bounds__(kWideThreads, 3) lora_wide_kernel(const __grid
   char* aligned = raw + (start - smem_u32(raw));
   float* staged = reinterpret_cast<float*>(aligned + shape.rows);
   uint64_t* full = reinterpret_cast<uint64_t*>(aligned + shape.bars);
-  uint64_t *empty = full + kWideStages, *tfull = empty + kWideStages, *tempty = tfull + 2;
+  uint64_t *empty = full + 1, *tfull = empty + 1, *tempty = tfull + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, chunks = (R + 15) / 16;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kWideStages; ++i) mbar_init(full + i, 1), mbar_init(empty + i, 1);
+    mbar_init(full, 1), mbar_init(empty, 1);
     for (int i = 0; i < 2; ++i) mbar_init(tfull + i, 1), mbar_init(tempty + i, kWideEpilogue / 32);
     mbar_fence_init();
   }
@@ -612,7 +614,7 @@ __global__ void __launch_bounds__(kWideThreads, 3) lora_wide_kernel(const __grid
   wait_for_inputs();
   pdl_wait_for(vq, factor, index, base);
   Units units(tile, plan, index, T, n);
-  int id, count, st = 0, buf = 0;  // (stages and accumulators go on across units)
+  int id, count, buf = 0;  // (accumulators and the parities go on across units)
   uint32_t ph = 0, pb = 0;
   bool ok = true;
   while (units.next(id, count)) {
@@ -644,40 +646,33 @@ __global__ void __launch_bounds__(kWideThreads, 3) lora_wide_kernel(const __grid
       if (lane == 0) {
         const uint32_t bytes = shape.blocks * 128 * 128;
         constexpr uint32_t idesc = product_idesc<E>(128, kTok, false, false);
-        int fs = st;  // the stage to fill next, and the parity with which its last use has ended
-        uint32_t fp = ph;
         auto fetch = [&](int t) {
-          ok = mbar_wait(empty + fs, fp ^ 1, kProductLimitNs);
+          ok = mbar_wait(empty, ph ^ 1, kProductLimitNs);
           if (!ok) return;
-          mbar_arrive_expect_tx(full + fs, bytes);
+          mbar_arrive_expect_tx(full, bytes);
           for (int k = 0; k < shape.blocks; ++k)
-            pair_load<1>(start + (uint32_t)shape.weights + fs * bytes + k * 128 * 128, &map, smem_u32(full + fs), k * 64, id * N + t * 128);
-          if (++fs == kWideStages) fs = 0, fp ^= 1;
+            pair_load<1>(start + (uint32_t)shape.weights + k * 128 * 128, &map, smem_u32(full), k * 64, id * N + t * 128);
         };
-        int ahead = first;
-        for (int i = 0; i < kWideStages && ahead < tiles && ok; ++i, ahead += step) fetch(ahead);
+        fetch(first);
         for (int t = first; t < tiles && ok; t += step) {
-          ok = mbar_wait(tempty + buf, pb ^ 1, kProductLimitNs) && mbar_wait(full + st, ph, kProductLimitNs);
+          ok = mbar_wait(tempty + buf, pb ^ 1, kProductLimitNs) && mbar_wait(full, ph, kProductLimitNs);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t a = start + (uint32_t)shape.weights + st * bytes, v = start;
+          const uint32_t a = start + (uint32_t)shape.weights, v = start;
           for (int c = 0; c < chunks; ++c) {
             const uint32_t k = (c & 3) * 32, block = c >> 2;
             const uint64_t da = tile_desc(a + block * 128 * 128 + k, false);
             pair_mma<1>(tmem + buf * kTok, da, tile_desc(v + block * 2 * kTok * 128 + k, false), idesc, c);
             pair_mma<1>(tmem + buf * kTok, da, tile_desc(v + block * 2 * kTok * 128 + kTok * 128 + k, false), idesc, 1);
           }
-          pair_commit<1>(empty + st);
+          pair_commit<1>(empty);
           pair_commit<1>(tfull + buf);
-          if (++st == kWideStages) st = 0, ph ^= 1;
+          ph ^= 1;
           if ((buf ^= 1) == 0) pb ^= 1;
-          if (ahead < tiles) fetch(ahead), ahead += step;
+          if (t + step < tiles) fetch(t + step);
         }
         // the MMAs that read this unit's v have ended before the next one's takes its place
-        for (int i = 0; i < kWideStages && ok; ++i) {
-          fs = fs == 0 ? (fp ^= 1, kWideStages - 1) : fs - 1;
-          ok = mbar_wait(empty + fs, fp, kProductLimitNs);
-        }
+        if (ok) ok = mbar_wait(empty, ph ^ 1, kProductLimitNs);
       }
     } else {
       constexpr int kRows = kTok / (kWideEpilogue / 32);  // rows a warp reads and writes
