@@ -69,7 +69,8 @@ struct Philox {
 // A thread loads the items of its next step before it draws the present one's numbers,
 // so memory and the generator overlap.  T = 16384, H = 5120, bf16: with a residual
 // 76.5 us (97 % of the copy; 92 with one item a thread and no loop), without one 66.5
-// (86), bound by the multiplier: 36 wide products an item at 4 cycles a warp are 41 us.
+// (86), bound by the multiplier's pipe (72 % busy: 36 wide products an item at 4 cycles a
+// warp are 41 us) and by dispatch beside it; its warps wait for loads 6 % of their time.
 // Two items a step for many rows (with one 86 and 76 us), one where that would leave
 // CTAs without work, and for fp32, whose items are twice as large.
 constexpr int kCtas = 4, kSteps = 4;
